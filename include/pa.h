@@ -8,7 +8,10 @@
  *
  * pa_decode_step issues all three; pa_decode_splitk_multi (several query tokens per
  * request) and pa_decode_splitk_window / pa_decode_step_window (sliding-window layers)
- * are the producer's other forms.  Every entry point takes plain device pointers
+ * are the producer's other forms.  Around the step: pa_rope_append writes a layer's new
+ * keys and values into the pools, pa_tree_attention / pa_decode_step_tree verify drafted
+ * trees, pa_accumulate_weights, pa_evict and pa_compact_cache shrink a cache.
+ * Every entry point takes plain device pointers
  * and sizes, enqueues work on `stream` (a cudaStream_t passed as void*, NULL = the
  * legacy default stream) and returns without synchronising.  The step's own inputs
  * and outputs -- q, req_pool_indices, seq_lens, out, lse -- may instead point into
@@ -80,11 +83,20 @@ typedef enum {
 #define PA_DEVERR_SLOT_OUT_OF_RANGE 0x4u     /* token slot outside full_to_swa_mapping */
 #define PA_DEVERR_WAIT_TIMEOUT 0x8u          /* a shared-memory copy wait gave up (~2 s) */
 #define PA_DEVERR_SEQLEN_OUT_OF_RANGE 0x10u  /* cache_seqlens < 0 or > max_seq_pages*page_size */
+#define PA_DEVERR_KEPT_OUT_OF_RANGE 0x20u    /* pa_compact_cache: a kept position or its target */
+#define PA_DEVERR_TREE_PARENT 0x40u          /* pa_build_tree_mask: parent not an earlier node */
 
 /* cu_seqlens_q modes of pa_build_metadata_full. */
 #define PA_Q_MODE_NONE 0    /* leave cu_seqlens_q untouched (decode, target-verify) */
 #define PA_Q_MODE_CUMSUM 1  /* cu_seqlens_q[0] = 0, [i+1] = sum_{j<=i} int32(qlens[j]) */
 #define PA_Q_MODE_STRIDED 2 /* cu_seqlens_q[0] = 0, [i+1] = (i+1) * q_stride */
+
+/* Frequency scalings of pa_rope_frequencies. */
+#define PA_ROPE_PLAIN 0      /* none */
+#define PA_ROPE_LINEAR 1     /* every frequency divided by the factor */
+#define PA_ROPE_BASE 2       /* a larger base: the slowest pair is slowed by the factor */
+#define PA_ROPE_BY_PARTS 3   /* fast pairs kept, slow ones divided, a ramp over the pairs between */
+#define PA_ROPE_WAVELENGTH 4 /* the same split by wavelength, blended in the wavelength */
 
 /*
  * pa_build_metadata -- the fused per-step metadata update.
@@ -468,6 +480,209 @@ PA_API pa_status pa_decode_step_static_scratch(
     int32_t kv_dtype, int32_t bs, int32_t num_q_heads, int32_t num_kv_heads,
     int32_t head_dim, int32_t page_size, int64_t num_pages, int32_t num_splits,
     float sm_scale, void* out, float* lse, void* stream, int32_t use_pdl);
+
+/*
+ * pa_rope_frequencies -- radians per position of each rotated pair, computed on the host in
+ * 64 bits: inv_freq[i], 0 <= i < rotary_dim / 2 (host memory; upload it once).  With
+ * f_i = base^(-2 i / rotary_dim), L = original_length (positions the model was trained on):
+ *   PA_ROPE_PLAIN       f_i
+ *   PA_ROPE_LINEAR      f_i / factor
+ *   PA_ROPE_BASE        (base * factor^(rotary_dim / (rotary_dim - 2)))^(-2 i / rotary_dim)
+ *   PA_ROPE_BY_PARTS    pair(t) = rotary_dim ln(L / (2 pi t)) / (2 ln base) is the pair that
+ *                       turns t times over L; lo = max(0, floor(pair(high))), hi =
+ *                       min(rotary_dim - 1, ceil(pair(low))), r_i = clamp((i - lo) /
+ *                       max(hi - lo, 0.001), 0, 1); f_i (1 - r_i) + f_i / factor r_i
+ *   PA_ROPE_WAVELENGTH  turns t_i = L f_i / (2 pi): f_i where t_i > high, f_i / factor where
+ *                       t_i < low, else s = (t_i - low) / (high - low), (1 - s) f_i / factor + s f_i
+ * low and high are turns over L (customary: 1 and 32 by parts, 1 and 4 by wavelength).
+ * Arguments that a scaling does not name are ignored.  Errors: PA_ERR_INVALID for a NULL
+ * table, a rotary_dim that is not even and positive (2 for PA_ROPE_BASE), base <= 1, or a
+ * factor, L, low or high that the scaling needs and that is not finite and positive
+ * (high > low); an unknown scaling.
+ */
+PA_API pa_status pa_rope_frequencies(double* inv_freq, int32_t rotary_dim, double base,
+                                     int32_t scaling, double factor, int64_t original_length,
+                                     double low, double high);
+
+/*
+ * pa_rope_append -- rotary positions on the new queries and keys, and the new keys and
+ * values written to the cache: what a layer runs before its attention.  One launch.
+ * For token t, pair i of every query and key head is turned by the angle
+ * positions[t] * inv_freq[i] and scaled by `amplitude` (1, or the attention factor of a
+ * long-context scaling): (a, b) -> amplitude (a cos - b sin, b cos + a sin).  A pair is
+ * channels (i, i + rotary_dim / 2), or (2 i, 2 i + 1) when `interleaved` is non-zero;
+ * channels >= rotary_dim pass through unscaled.  The angle is reduced to a fraction of a
+ * turn exactly (64-bit fixed point), so positions up to 2^31 lose nothing; the rotation
+ * is fp32, rounded once.
+ *   q, k, v    bf16, head h of token t at x[t * x_stride + h * 128]; strides in elements,
+ *              multiples of 8 (views of one projection's output are fine)
+ *   positions  [num_tokens] int64;  slots [num_tokens] int64: the token's slot, page *
+ *              page_size + row; negative: the token is not written to the cache (padding)
+ *   inv_freq   [rotary_dim / 2] double, device memory
+ *   q_out      bf16, token stride q_out_stride; may be q itself with q's stride (in place)
+ *   k_cache, v_cache, k_scale, v_scale   the pools of pa_decode_splitk.  int8: scale = the
+ *              row's largest magnitude / 127, codes = round-to-even(x / scale) (an all-zero
+ *              row: scale 0); rows must be finite.
+ * Two tokens with the same slot leave that row unspecified.  A slot at or past num_pages *
+ * page_size is not written and sets PA_DEVERR_SLOT_OUT_OF_RANGE.  The kernel reads nothing
+ * before it has waited on the previous grid and never triggers its dependents early, so
+ * its outputs may be the inputs that a step reads before its own wait.
+ * Supported: head_dim 128; rotary_dim 16, 32, ..., 128; page_size 16, 32, 64, 128; any
+ * num_q_heads, num_kv_heads >= 1.  All device memory, 16-byte aligned (positions, slots
+ * and inv_freq: 8).
+ */
+PA_API pa_status pa_rope_append(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                                const void* v, int64_t v_stride, const int64_t* positions,
+                                const int64_t* slots, const double* inv_freq, int32_t rotary_dim,
+                                int32_t interleaved, float amplitude, int32_t num_tokens,
+                                int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                                void* q_out, int64_t q_out_stride, void* k_cache, void* v_cache,
+                                float* k_scale, float* v_scale, int32_t kv_dtype,
+                                int32_t page_size, int64_t num_pages, void* stream,
+                                int32_t use_pdl);
+
+/*
+ * pa_build_tree_mask -- ancestor masks of drafted trees, from parent indices.
+ *   parents    [total_q] int32: of node i of request b (row cu_seqlens_q[b] + i) the node
+ *              index of its parent within the request (< i), or -1 for a root
+ *   tree_mask  [total_q, mask_words] int64 (out): bit t % 64 of word t / 64 is set for
+ *              t = i and every ancestor t of node i
+ * mask_words >= ceil(max_q_len / 64), 1 <= max_q_len <= 256.  Rows at or past
+ * cu_seqlens_q[bs] are not touched.  A parent that is not in [-1, i) sets
+ * PA_DEVERR_TREE_PARENT and counts as -1.
+ */
+PA_API pa_status pa_build_tree_mask(const int32_t* parents, const int32_t* cu_seqlens_q,
+                                    int32_t bs, int32_t total_q, int32_t max_q_len,
+                                    int64_t* tree_mask, int32_t mask_words, void* stream,
+                                    int32_t use_pdl);
+
+/*
+ * pa_tree_attention -- attention of drafted trees over the cache (speculative verify).
+ * Query rows of request b are q[cu_seqlens_q[b] .. cu_seqlens_q[b+1]) ([total_q,
+ * num_q_heads, 128] bf16), q_len <= max_q_len of them; they are the request's newest
+ * tokens, already in its cache in the same order.  With n = cache_seqlens[b], query i
+ * attends to every position j < n - q_len and to position n - q_len + t where bit t of
+ * tree_mask row i is set (bits t >= q_len are ignored; the caller sets bit i for the
+ * query's own token).  A query that attends to nothing gives out = 0, lse = -inf.
+ *   out [total_q, num_q_heads, 128] bf16;  lse [total_q, num_q_heads] fp32 or NULL; rows at
+ *   or past cu_seqlens_q[bs] (padding of a captured batch) are not touched.
+ *   tree_mask [total_q, mask_words] int64, mask_words >= ceil(max_q_len / 64)
+ * K/V pools, scales, page_table and cache_seqlens as for pa_decode_splitk (page_table as the
+ * metadata stage writes it).  K of positions that a query does not attend to may hold
+ * anything; so may V at or past n, but a non-finite V row below n reaches every query of
+ * its request (a weight of 0 times it is NaN).
+ * num_splits: context splits, or 0 for pa_choose_tree_splits(...).  With one split the
+ * output is written directly and `workspace` may be NULL; otherwise the partials go to
+ * `workspace` (16-byte aligned, workspace_bytes >= pa_workspace_bytes(total_q, num_q_heads,
+ * 128, splits)) and a second launch combines them.  Calls that overlap on the GPU need
+ * workspaces of their own.
+ * Supported: head_dim 128; page_size 16, 32, 64, 128; num_q_heads / num_kv_heads in {1, 2,
+ * 4, 8, 16}; 1 <= max_q_len <= 256; max_seq_pages * page_size <= 2^29.  All device memory.  Request lengths and row offsets
+ * that only the device sees are bounds-checked like those of pa_decode_splitk_multi.
+ */
+PA_API pa_status pa_tree_attention(
+    const void* q, const void* k_cache, const void* v_cache, const float* k_scale,
+    const float* v_scale, int32_t kv_dtype, const int32_t* page_table, int64_t page_table_stride,
+    const int32_t* cache_seqlens, const int32_t* cu_seqlens_q, const int64_t* tree_mask,
+    int32_t mask_words, int32_t bs, int32_t total_q, int32_t max_q_len, int32_t num_q_heads,
+    int32_t num_kv_heads, int32_t head_dim, int32_t page_size, int64_t num_pages,
+    int32_t max_seq_pages, int32_t num_splits, float sm_scale, void* workspace,
+    size_t workspace_bytes, void* out, float* lse, void* stream, int32_t use_pdl);
+
+/*
+ * pa_decode_step_tree -- the verify step of a drafted tree: pa_build_metadata_full with the
+ * query side (q_mode, qlens, q_stride as for pa_decode_step_multi), then pa_tree_attention
+ * over the page table it wrote.  The arguments are those of the two calls; everything is
+ * checked before anything is enqueued.  total_q == 0 runs the metadata stage only.
+ */
+PA_API pa_status pa_decode_step_tree(
+    const int64_t* req_pool_indices, const int64_t* seq_lens, const int32_t* req_to_token,
+    int64_t req_to_token_rows, int64_t req_to_token_stride,
+    const int64_t* full_to_swa_mapping, int64_t full_to_swa_mapping_len,
+    int32_t seqlen_offset, int32_t max_seq_pages, int32_t* cache_seqlens,
+    int32_t* cu_seqlens_k, int32_t* page_table, int64_t page_table_stride,
+    int32_t* swa_page_table, int64_t swa_page_table_stride, const int64_t* qlens,
+    int32_t q_mode, int32_t q_stride, int32_t* cu_seqlens_q, const int64_t* tree_mask,
+    int32_t mask_words, const void* q, int32_t total_q, int32_t max_q_len, const void* k_cache,
+    const void* v_cache, const float* k_scale, const float* v_scale, int32_t kv_dtype,
+    int32_t bs, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim, int32_t page_size,
+    int64_t num_pages, int32_t num_splits, float sm_scale, void* workspace,
+    size_t workspace_bytes, void* out, float* lse, void* stream, int32_t use_pdl);
+
+/*
+ * The split count that pa_tree_attention picks for num_splits == 0 (sm_count <= 0: the
+ * current device), and the workspace bytes it then needs (0 with one split).
+ */
+PA_API int32_t pa_choose_tree_splits(int32_t bs, int32_t max_q_len, int32_t num_q_heads,
+                                     int32_t num_kv_heads, int32_t page_size,
+                                     int32_t max_seq_pages, int32_t sm_count);
+PA_API size_t pa_tree_workspace_bytes(int32_t bs, int32_t total_q, int32_t max_q_len,
+                                      int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                                      int32_t page_size, int32_t max_seq_pages);
+
+/*
+ * pa_accumulate_weights -- the attention weights of a decode step added up per cached row:
+ * for request b, kv head h and position j < cache_seqlens[b] (row r of page p),
+ *   weights[p, h, r] += sum over the query heads of h of exp(sm_scale q . K_j - lse)
+ * with the step's q [bs, num_q_heads, 128] bf16 and lse [bs, num_q_heads] fp32 (a head with
+ * lse = -inf adds nothing).  weights [num_pages, num_kv_heads, page_size] fp32, kept with
+ * the pools; pools, tables and limits as for pa_decode_splitk (k_scale: int8 only).  Rows of
+ * other positions are not touched.  A page that several requests share gets all of their
+ * weights, in an order that is not fixed; otherwise the result is the same every time.
+ */
+PA_API pa_status pa_accumulate_weights(
+    const void* q, const float* lse, const void* k_cache, const float* k_scale, int32_t kv_dtype,
+    const int32_t* page_table, int64_t page_table_stride, const int32_t* cache_seqlens,
+    float* weights, int32_t bs, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+    int32_t page_size, int64_t num_pages, int32_t max_seq_pages, float sm_scale, void* stream,
+    int32_t use_pdl);
+
+/*
+ * pa_compact_cache -- rows of the cache moved to the front, in order: of every request b
+ * and kv head h, position kept[b, h, i] (0 <= i < counts[b]) moves to position begin[b] + i
+ * (begin NULL: 0) of the pages in dst_page_table: K and V rows, their scales and, where
+ * `weights` is given, their accumulated weights.  new_seqlens[b] = begin[b] + counts[b]
+ * (may be NULL; not cache_seqlens or counts).
+ *   kept   [bs, kept_heads, kept_stride] int32, strictly ascending in i; kept_heads is
+ *          num_kv_heads, or 1 for one list that all heads share (the accepted path of a tree)
+ *   dst_page_table   page_table itself, the same pointer and stride: in place, which needs
+ *          kept[b, h, i] >= begin[b] + i; or another table whose pages of the moved
+ *          positions hold no position that this call reads (fresh pages: needed where
+ *          requests share pages).  [bs, dst_page_table_stride], dst_max_pages columns used.
+ * Rows of the destination that no kept position moves to are left as they are.  A kept
+ * position outside [0, cache_seqlens[b]), a target past dst_max_pages * page_size or, in
+ * place, a kept position before its target is not moved and sets
+ * PA_DEVERR_KEPT_OUT_OF_RANGE.  max_kept: the largest count; larger counts are cut to it.
+ * Supported: head_dim 128; page_size 16, 32, 64, 128.
+ */
+PA_API pa_status pa_compact_cache(
+    const int32_t* page_table, int64_t page_table_stride, const int32_t* cache_seqlens,
+    int32_t max_seq_pages, const int32_t* kept, int32_t kept_heads, int64_t kept_stride,
+    const int32_t* counts, const int32_t* begin, int32_t max_kept, void* k_cache, void* v_cache,
+    float* k_scale, float* v_scale, int32_t kv_dtype, float* weights,
+    const int32_t* dst_page_table, int64_t dst_page_table_stride, int32_t dst_max_pages,
+    int32_t* new_seqlens, int32_t bs, int32_t num_kv_heads, int32_t head_dim, int32_t page_size,
+    int64_t num_pages, void* stream, int32_t use_pdl);
+
+/*
+ * pa_evict -- each request's cache shrunk to `budget` rows per kv head by accumulated
+ * weight.  With n = cache_seqlens[b]: if n <= budget every position is kept; otherwise the
+ * first num_first, the last num_recent, and of the others the budget - num_first -
+ * num_recent with the largest weights (equal weights: the lowest position; NaN counts as
+ * the largest, -0 as 0).  kept [bs, num_kv_heads, budget] int32 (out): the kept positions in
+ * ascending order, then -1; new_seqlens [bs] int32 (out): min(n, budget) (not
+ * cache_seqlens).  The rows then move as by pa_compact_cache with begin 0 (weights always
+ * move too); every head keeps its own positions, so position i of the shrunk cache is a
+ * different token from head to head.  1 <= budget, num_first + num_recent <= budget.
+ */
+PA_API pa_status pa_evict(const int32_t* page_table, int64_t page_table_stride,
+                          const int32_t* cache_seqlens, int32_t max_seq_pages, float* weights,
+                          void* k_cache, void* v_cache, float* k_scale, float* v_scale,
+                          int32_t kv_dtype, int32_t budget, int32_t num_first, int32_t num_recent,
+                          const int32_t* dst_page_table, int64_t dst_page_table_stride,
+                          int32_t dst_max_pages, int32_t* kept, int32_t* new_seqlens, int32_t bs,
+                          int32_t num_kv_heads, int32_t head_dim, int32_t page_size,
+                          int64_t num_pages, void* stream, int32_t use_pdl);
 
 /* Bytes of workspace pa_decode_step needs: m, l and acc partials, each 256-byte aligned. */
 PA_API size_t pa_workspace_bytes(int32_t bs, int32_t num_q_heads, int32_t head_dim,

@@ -27,6 +27,9 @@ DEVERR_POOL_ROW_OUT_OF_RANGE = 0x2
 DEVERR_SLOT_OUT_OF_RANGE = 0x4
 DEVERR_WAIT_TIMEOUT = 0x8
 DEVERR_SEQLEN_OUT_OF_RANGE = 0x10
+DEVERR_KEPT_OUT_OF_RANGE = 0x20
+DEVERR_TREE_PARENT = 0x40
+PA_ROPE_PLAIN, PA_ROPE_LINEAR, PA_ROPE_BASE, PA_ROPE_BY_PARTS, PA_ROPE_WAVELENGTH = range(5)
 
 _lock = threading.Lock()
 _lib: Optional[ctypes.CDLL] = None
@@ -126,6 +129,28 @@ def _declare(lib):
                                                   i32, i32, i32, i32, i32, i64, i32, f32, vp, vp,
                                                   vp, i32]
     lib.pa_decode_step_static_scratch.restype = ctypes.c_int
+    f64 = ctypes.c_double
+    lib.pa_rope_frequencies.argtypes = [vp, i32, f64, i32, f64, i64, f64, f64]
+    lib.pa_rope_append.argtypes = [vp, i64, vp, i64, vp, i64, vp, vp, vp, i32, i32, f32, i32, i32,
+                                   i32, i32, vp, i64, vp, vp, vp, vp, i32, i32, i64, vp, i32]
+    lib.pa_build_tree_mask.argtypes = [vp, vp, i32, i32, i32, vp, i32, vp, i32]
+    lib.pa_tree_attention.argtypes = [vp, vp, vp, vp, vp, i32, vp, i64, vp, vp, vp, i32, i32, i32,
+                                      i32, i32, i32, i32, i32, i64, i32, i32, f32, vp, sz, vp, vp,
+                                      vp, i32]
+    lib.pa_decode_step_tree.argtypes = [vp, vp, vp, i64, i64, vp, i64, i32, i32, vp, vp, vp, i64,
+                                        vp, i64, vp, i32, i32, vp, vp, i32, vp, i32, i32, vp, vp,
+                                        vp, vp, i32, i32, i32, i32, i32, i32, i64, i32, f32, vp,
+                                        sz, vp, vp, vp, i32]
+    lib.pa_choose_tree_splits.argtypes = [i32] * 7
+    lib.pa_choose_tree_splits.restype = i32
+    lib.pa_tree_workspace_bytes.argtypes = [i32] * 8
+    lib.pa_tree_workspace_bytes.restype = sz
+    lib.pa_accumulate_weights.argtypes = [vp, vp, vp, vp, i32, vp, i64, vp, vp, i32, i32, i32, i32,
+                                          i32, i64, i32, f32, vp, i32]
+    lib.pa_compact_cache.argtypes = [vp, i64, vp, i32, vp, i32, i64, vp, vp, i32, vp, vp, vp, vp,
+                                     i32, vp, vp, i64, i32, vp, i32, i32, i32, i32, i64, vp, i32]
+    lib.pa_evict.argtypes = [vp, i64, vp, i32, vp, vp, vp, vp, vp, i32, i32, i32, i32, vp, i64, i32,
+                             vp, vp, i32, i32, i32, i32, i64, vp, i32]
     lib.pa_workspace_bytes.argtypes = [i32, i32, i32, i32]
     lib.pa_workspace_bytes.restype = sz
     lib.pa_choose_splits.argtypes = [i32, i32, i32, i32, i32, i32]
@@ -141,7 +166,9 @@ def _declare(lib):
                  "pa_decode_splitk_multi", "pa_decode_splitk_window", "pa_reduce",
                  "pa_decode_step", "pa_decode_step_host", "pa_decode_step_host_packed",
                  "pa_decode_step_multi",
-                 "pa_decode_step_window",
+                 "pa_decode_step_window", "pa_rope_frequencies", "pa_rope_append",
+                 "pa_build_tree_mask", "pa_tree_attention", "pa_decode_step_tree",
+                 "pa_accumulate_weights", "pa_compact_cache", "pa_evict",
                  "pa_read_error_flags"):
         getattr(lib, name).restype = ctypes.c_int
     return lib
@@ -620,3 +647,356 @@ def pa_read_error_flags(reset: bool = True, lib=None) -> int:
     lib = lib or load()
     _check("pa_read_error_flags", lib.pa_read_error_flags(ctypes.byref(v), int(bool(reset))), lib)
     return int(v.value)
+
+
+# ---- the cache operators: rotary append, tree attention, weights, eviction ------------------
+
+
+def _on_device(**tensors):
+    """The named tensors are CUDA tensors of the current device (whose context the launch
+    uses); None entries pass."""
+    current = torch.cuda.current_device() if torch.cuda.is_available() else None
+    for name, t in tensors.items():
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+        if t.device.index != current:
+            raise ValueError(f"{name} is on cuda:{t.device.index}, the current device is "
+                             f"cuda:{current}")
+
+
+def _shape(t: torch.Tensor, shape: tuple, name: str):
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+
+
+def _table(t: torch.Tensor, bs: int, columns: int, name: str):
+    """Pointer and row stride of a [bs, >= columns] int32 page table."""
+    stride = _row_stride(t, name)
+    if t.shape[0] != bs or t.shape[1] < columns:
+        raise ValueError(f"{name} must be [{bs}, >= {columns}], got {tuple(t.shape)}")
+    return _ptr2d(t, torch.int32, name), stride if bs > 1 else max(stride, t.shape[1])
+
+
+def _pools(k_cache, v_cache, k_scale, v_scale):
+    """(kv_dtype, scale pointers, pool shape) of pools of equal type and shape."""
+    if k_cache.dim() != 4:
+        raise ValueError("k_cache must be [num_pages, num_kv_heads, page_size, head_dim]")
+    if v_cache.dtype != k_cache.dtype:
+        raise ValueError(f"v_cache must be {k_cache.dtype}, got {v_cache.dtype}")
+    _shape(v_cache, tuple(k_cache.shape), "v_cache")
+    kv_dtype, ks, vs = _kv_args(k_cache, v_cache, k_scale, v_scale)
+    if kv_dtype == PA_KV_INT8:
+        _shape(k_scale, tuple(k_cache.shape[:3]), "k_scale")
+        _shape(v_scale, tuple(k_cache.shape[:3]), "v_scale")
+    return kv_dtype, ks, vs, tuple(k_cache.shape)
+
+
+def pa_rope_frequencies(rotary_dim: int, base: float = 10000.0, scaling: int = PA_ROPE_PLAIN, *,
+                        factor: float = 1.0, original_length: int = 0, low: float = 0.0,
+                        high: float = 0.0) -> torch.Tensor:
+    """Radians per position of each rotated pair, a CPU tensor [rotary_dim / 2] float64;
+    see include/pa.h."""
+    out = torch.empty(max(int(rotary_dim) // 2, 1), dtype=torch.float64)
+    _check("pa_rope_frequencies", load().pa_rope_frequencies(
+        out.data_ptr(), int(rotary_dim), float(base), int(scaling), float(factor),
+        int(original_length), float(low), float(high)))
+    return out
+
+
+def _token_rows(t: torch.Tensor, tokens: int, name: str):
+    """(pointer, token stride, heads) of [tokens, heads, 128] bf16 rows whose heads are
+    contiguous (a view of a wider projection row is fine)."""
+    if t.dim() != 3 or t.shape[0] != tokens or t.dtype != torch.bfloat16:
+        raise ValueError(f"{name} must be [{tokens}, heads, head_dim] bf16")
+    heads, d = t.shape[1], t.shape[2]
+    if (d > 1 and t.stride(2) != 1) or (heads > 1 and t.stride(1) != d):
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    return t.data_ptr(), t.stride(0) if tokens > 1 else heads * d, heads
+
+
+def _rope_append_args(*, q, k, v, positions, slots, inv_freq, q_out, k_cache, v_cache,
+                      k_scale=None, v_scale=None, interleaved: bool = False,
+                      amplitude: float = 1.0, stream=None, use_pdl: bool = True):
+    _on_device(q=q, k=k, v=v, positions=positions, slots=slots, inv_freq=inv_freq, q_out=q_out,
+               k_cache=k_cache, v_cache=v_cache, k_scale=k_scale, v_scale=v_scale)
+    kv_dtype, ks, vs, (num_pages, hkv, page_size, d) = _pools(k_cache, v_cache, k_scale, v_scale)
+    tokens = q.shape[0]
+    qp, q_stride, hq = _token_rows(q, tokens, "q")
+    kp, k_stride, k_heads = _token_rows(k, tokens, "k")
+    vp, v_stride, v_heads = _token_rows(v, tokens, "v")
+    op, o_stride, _ = _token_rows(q_out, tokens, "q_out")
+    _shape(q_out, tuple(q.shape), "q_out")
+    if k_heads != hkv or v_heads != hkv or not q.shape[2] == k.shape[2] == v.shape[2] == d:
+        raise ValueError("k and v must have the pools' heads, and all rows their head_dim")
+    _shape(positions, (tokens,), "positions")
+    _shape(slots, (tokens,), "slots")
+    if inv_freq.dim() != 1:
+        raise ValueError("inv_freq must be [rotary_dim / 2]")
+    return (qp, q_stride, kp, k_stride, vp, v_stride, _ptr(positions, torch.int64, "positions"),
+            _ptr(slots, torch.int64, "slots"), _ptr(inv_freq, torch.float64, "inv_freq"),
+            2 * inv_freq.numel(), int(bool(interleaved)), float(amplitude), tokens, hq, hkv, d, op,
+            o_stride, _ptr(k_cache, None, "k_cache"), _ptr(v_cache, None, "v_cache"), ks, vs,
+            kv_dtype, page_size, num_pages, _stream(stream), int(bool(use_pdl)))
+
+
+def pa_rope_append(**kw):
+    """Rotary positions on q (into q_out) and k, and the new k and v rows written to their
+    slots of the pools; see include/pa.h.  Keyword arguments: those of
+    ``_rope_append_args``."""
+    _check("pa_rope_append", load().pa_rope_append(*_rope_append_args(**kw)))
+
+
+def prepare_rope_append(*, lib=None, **kw) -> PreparedCall:
+    """``pa_rope_append`` with the given keyword arguments, marshalled once."""
+    return PreparedCall("pa_rope_append", _rope_append_args(**kw), lib, keep=tuple(kw.values()))
+
+
+def pa_build_tree_mask(parents, cu_seqlens_q, tree_mask, *, max_q_len: int, stream=None,
+                       use_pdl: bool = True):
+    """Ancestor masks of drafted trees from parent indices; see include/pa.h."""
+    _on_device(parents=parents, cu_seqlens_q=cu_seqlens_q, tree_mask=tree_mask)
+    _shape(parents, (tree_mask.shape[0],), "parents")
+    if tree_mask.dim() != 2:
+        raise ValueError("tree_mask must be [total_q, mask_words]")
+    _check("pa_build_tree_mask", load().pa_build_tree_mask(
+        _ptr(parents, torch.int32, "parents"), _ptr(cu_seqlens_q, torch.int32, "cu_seqlens_q"),
+        cu_seqlens_q.numel() - 1, tree_mask.shape[0], int(max_q_len),
+        _ptr(tree_mask, torch.int64, "tree_mask"), tree_mask.shape[1], _stream(stream),
+        int(bool(use_pdl))))
+
+
+def pa_choose_tree_splits(bs: int, max_q_len: int, num_q_heads: int, num_kv_heads: int,
+                          page_size: int, max_seq_pages: int, sm_count: int = 0) -> int:
+    """Split count of a tree attention; see include/pa.h."""
+    return int(load().pa_choose_tree_splits(bs, max_q_len, num_q_heads, num_kv_heads, page_size,
+                                            max_seq_pages, sm_count))
+
+
+def pa_tree_workspace_bytes(bs: int, total_q: int, max_q_len: int, num_q_heads: int,
+                            num_kv_heads: int, head_dim: int, page_size: int,
+                            max_seq_pages: int) -> int:
+    """Workspace of a tree attention with the library's split count; see include/pa.h."""
+    return int(load().pa_tree_workspace_bytes(bs, total_q, max_q_len, num_q_heads, num_kv_heads,
+                                              head_dim, page_size, max_seq_pages))
+
+
+def _workspace(workspace):
+    if workspace is None:
+        return None, 0
+    return _ptr(workspace, None, "workspace"), workspace.numel() * workspace.element_size()
+
+
+def _tree_rows(q, tree_mask, cu_seqlens_q, cache_seqlens, out, lse, d: int):
+    """Shapes shared by the tree calls; returns (total_q, num_q_heads, bs, mask_words)."""
+    if q.dim() != 3 or q.shape[2] != d:
+        raise ValueError(f"q must be [total_q, num_q_heads, {d}]")
+    total_q, hq, _ = q.shape
+    bs = cache_seqlens.shape[0]
+    _shape(cu_seqlens_q, (bs + 1,), "cu_seqlens_q")
+    if tree_mask.dim() != 2 or tree_mask.shape[0] != total_q:
+        raise ValueError("tree_mask must be [total_q, mask_words]")
+    _shape(out, tuple(q.shape), "out")
+    if lse is not None:
+        _shape(lse, (total_q, hq), "lse")
+    return total_q, hq, bs, tree_mask.shape[1]
+
+
+def _tree_attention_args(*, q, k_cache, v_cache, page_table, cache_seqlens, cu_seqlens_q,
+                         tree_mask, max_q_len: int, max_seq_pages: int, sm_scale: float, out,
+                         lse=None, num_splits: int = 0, workspace=None, k_scale=None,
+                         v_scale=None, stream=None, use_pdl: bool = True):
+    _on_device(q=q, k_cache=k_cache, v_cache=v_cache, page_table=page_table,
+               cache_seqlens=cache_seqlens, cu_seqlens_q=cu_seqlens_q, tree_mask=tree_mask,
+               out=out, lse=lse, workspace=workspace, k_scale=k_scale, v_scale=v_scale)
+    kv_dtype, ks, vs, (num_pages, hkv, page_size, d) = _pools(k_cache, v_cache, k_scale, v_scale)
+    total_q, hq, bs, words = _tree_rows(q, tree_mask, cu_seqlens_q, cache_seqlens, out, lse, d)
+    pt, pt_stride = _table(page_table, bs, int(max_seq_pages), "page_table")
+    ws, ws_bytes = _workspace(workspace)
+    return (_ptr(q, torch.bfloat16, "q"), _ptr(k_cache, None, "k_cache"),
+            _ptr(v_cache, None, "v_cache"), ks, vs, kv_dtype, pt, pt_stride,
+            _ptr(cache_seqlens, torch.int32, "cache_seqlens"),
+            _ptr(cu_seqlens_q, torch.int32, "cu_seqlens_q"),
+            _ptr(tree_mask, torch.int64, "tree_mask"), words, bs, total_q, int(max_q_len), hq, hkv,
+            d, page_size, num_pages, int(max_seq_pages), int(num_splits), float(sm_scale), ws,
+            ws_bytes, _ptr(out, torch.bfloat16, "out"), _ptr(lse, torch.float32, "lse"),
+            _stream(stream), int(bool(use_pdl)))
+
+
+def pa_tree_attention(**kw):
+    """Attention of drafted trees over the cache; see include/pa.h.  Keyword arguments:
+    those of ``_tree_attention_args``."""
+    _check("pa_tree_attention", load().pa_tree_attention(*_tree_attention_args(**kw)))
+
+
+def prepare_tree_attention(*, lib=None, **kw) -> PreparedCall:
+    """``pa_tree_attention`` with the given keyword arguments, marshalled once."""
+    return PreparedCall("pa_tree_attention", _tree_attention_args(**kw), lib,
+                        keep=tuple(kw.values()))
+
+
+def _decode_step_tree_args(*, req_pool_indices, seq_lens, req_to_token, seqlen_offset: int,
+                           max_seq_pages: int, cache_seqlens, cu_seqlens_k, page_table,
+                           cu_seqlens_q, tree_mask, q, max_q_len: int, k_cache, v_cache,
+                           sm_scale: float, out, lse=None, num_splits: int = 0, workspace=None,
+                           qlens=None, q_mode: int = PA_Q_MODE_CUMSUM, q_stride: int = 0,
+                           k_scale=None, v_scale=None, full_to_swa_mapping=None,
+                           swa_page_table=None, stream=None, use_pdl: bool = True):
+    _on_device(req_pool_indices=req_pool_indices, seq_lens=seq_lens, req_to_token=req_to_token,
+               cache_seqlens=cache_seqlens, cu_seqlens_k=cu_seqlens_k, page_table=page_table,
+               cu_seqlens_q=cu_seqlens_q, tree_mask=tree_mask, q=q, k_cache=k_cache,
+               v_cache=v_cache, out=out, lse=lse, workspace=workspace, qlens=qlens,
+               k_scale=k_scale, v_scale=v_scale, full_to_swa_mapping=full_to_swa_mapping,
+               swa_page_table=swa_page_table)
+    kv_dtype, ks, vs, (num_pages, hkv, page_size, d) = _pools(k_cache, v_cache, k_scale, v_scale)
+    total_q, hq, bs, words = _tree_rows(q, tree_mask, cu_seqlens_q, cache_seqlens, out, lse, d)
+    _shape(req_pool_indices, (bs,), "req_pool_indices")
+    _shape(seq_lens, (bs,), "seq_lens")
+    _shape(cu_seqlens_k, (bs + 1,), "cu_seqlens_k")
+    if qlens is not None:
+        _shape(qlens, (bs,), "qlens")
+    pt, pt_stride = _table(page_table, bs, int(max_seq_pages), "page_table")
+    swa, swa_stride = (None, 0) if swa_page_table is None else \
+        _table(swa_page_table, bs, int(max_seq_pages), "swa_page_table")
+    ws, ws_bytes = _workspace(workspace)
+    return (_ptr(req_pool_indices, torch.int64, "req_pool_indices"),
+            _ptr(seq_lens, torch.int64, "seq_lens"),
+            _ptr2d(req_to_token, torch.int32, "req_to_token"), req_to_token.shape[0],
+            req_to_token.stride(0), _ptr(full_to_swa_mapping, torch.int64, "full_to_swa_mapping"),
+            full_to_swa_mapping.numel() if full_to_swa_mapping is not None else 0,
+            int(seqlen_offset), int(max_seq_pages),
+            _ptr(cache_seqlens, torch.int32, "cache_seqlens"),
+            _ptr(cu_seqlens_k, torch.int32, "cu_seqlens_k"), pt, pt_stride, swa, swa_stride,
+            _ptr(qlens, torch.int64, "qlens"), int(q_mode), int(q_stride),
+            _ptr(cu_seqlens_q, torch.int32, "cu_seqlens_q"),
+            _ptr(tree_mask, torch.int64, "tree_mask"), words, _ptr(q, torch.bfloat16, "q"),
+            total_q, int(max_q_len), _ptr(k_cache, None, "k_cache"),
+            _ptr(v_cache, None, "v_cache"), ks, vs, kv_dtype, bs, hq, hkv, d, page_size, num_pages,
+            int(num_splits), float(sm_scale), ws, ws_bytes, _ptr(out, torch.bfloat16, "out"),
+            _ptr(lse, torch.float32, "lse"), _stream(stream), int(bool(use_pdl)))
+
+
+def pa_decode_step_tree(*, lib=None, **kw):
+    """Metadata (with cu_seqlens_q) + tree attention in one call; see include/pa.h.
+    Keyword arguments: those of ``_decode_step_tree_args``."""
+    lib = lib or load()
+    _check("pa_decode_step_tree", lib.pa_decode_step_tree(*_decode_step_tree_args(**kw)), lib)
+
+
+def prepare_decode_step_tree(*, lib=None, **kw) -> PreparedCall:
+    """``pa_decode_step_tree`` with the given keyword arguments, marshalled once."""
+    return PreparedCall("pa_decode_step_tree", _decode_step_tree_args(**kw), lib,
+                        keep=tuple(kw.values()))
+
+
+def _accumulate_weights_args(*, q, lse, k_cache, page_table, cache_seqlens, weights,
+                             max_seq_pages: int, sm_scale: float, k_scale=None, stream=None,
+                             use_pdl: bool = True):
+    _on_device(q=q, lse=lse, k_cache=k_cache, page_table=page_table, cache_seqlens=cache_seqlens,
+               weights=weights, k_scale=k_scale)
+    kv_dtype, ks, _, (num_pages, hkv, page_size, d) = _pools(k_cache, k_cache, k_scale, k_scale)
+    bs = cache_seqlens.shape[0]
+    if q.dim() != 3 or q.shape[0] != bs or q.shape[2] != d:
+        raise ValueError(f"q must be [{bs}, num_q_heads, {d}]")
+    hq = q.shape[1]
+    _shape(lse, (bs, hq), "lse")
+    _shape(weights, (num_pages, hkv, page_size), "weights")
+    pt, pt_stride = _table(page_table, bs, int(max_seq_pages), "page_table")
+    return (_ptr(q, torch.bfloat16, "q"), _ptr(lse, torch.float32, "lse"),
+            _ptr(k_cache, None, "k_cache"), ks, kv_dtype, pt, pt_stride,
+            _ptr(cache_seqlens, torch.int32, "cache_seqlens"),
+            _ptr(weights, torch.float32, "weights"), bs, hq, hkv, d, page_size, num_pages,
+            int(max_seq_pages), float(sm_scale), _stream(stream), int(bool(use_pdl)))
+
+
+def pa_accumulate_weights(**kw):
+    """Attention weights of a decode step added to the cached rows' totals; see
+    include/pa.h.  Keyword arguments: those of ``_accumulate_weights_args``."""
+    _check("pa_accumulate_weights",
+           load().pa_accumulate_weights(*_accumulate_weights_args(**kw)))
+
+
+def prepare_accumulate_weights(*, lib=None, **kw) -> PreparedCall:
+    """``pa_accumulate_weights`` with the given keyword arguments, marshalled once."""
+    return PreparedCall("pa_accumulate_weights", _accumulate_weights_args(**kw), lib,
+                        keep=tuple(kw.values()))
+
+
+def _destination(page_table, dst_page_table, bs: int):
+    """(pointer, stride, columns) of the destination table; None means in place."""
+    dst = page_table if dst_page_table is None else dst_page_table
+    return (*_table(dst, bs, 1, "dst_page_table"), dst.shape[1])
+
+
+def _compact_cache_args(*, page_table, cache_seqlens, kept, counts, k_cache, v_cache,
+                        max_seq_pages: int, dst_page_table=None, begin=None, new_seqlens=None,
+                        weights=None, k_scale=None, v_scale=None, stream=None,
+                        use_pdl: bool = True):
+    _on_device(page_table=page_table, cache_seqlens=cache_seqlens, kept=kept, counts=counts,
+               k_cache=k_cache, v_cache=v_cache, dst_page_table=dst_page_table, begin=begin,
+               new_seqlens=new_seqlens, weights=weights, k_scale=k_scale, v_scale=v_scale)
+    kv_dtype, ks, vs, (num_pages, hkv, page_size, d) = _pools(k_cache, v_cache, k_scale, v_scale)
+    bs = cache_seqlens.shape[0]
+    if kept.dim() != 3 or kept.shape[0] != bs or kept.shape[1] not in (1, hkv):
+        raise ValueError(f"kept must be [{bs}, 1 or {hkv}, max_kept]")
+    for name, t in (("counts", counts), ("begin", begin), ("new_seqlens", new_seqlens)):
+        if t is not None:
+            _shape(t, (bs,), name)
+    if weights is not None:
+        _shape(weights, (num_pages, hkv, page_size), "weights")
+    pt, pt_stride = _table(page_table, bs, int(max_seq_pages), "page_table")
+    dst, dst_stride, dst_pages = _destination(page_table, dst_page_table, bs)
+    return (pt, pt_stride, _ptr(cache_seqlens, torch.int32, "cache_seqlens"), int(max_seq_pages),
+            _ptr(kept, torch.int32, "kept"), kept.shape[1], kept.shape[2],
+            _ptr(counts, torch.int32, "counts"), _ptr(begin, torch.int32, "begin"), kept.shape[2],
+            _ptr(k_cache, None, "k_cache"), _ptr(v_cache, None, "v_cache"), ks, vs, kv_dtype,
+            _ptr(weights, torch.float32, "weights"), dst, dst_stride, dst_pages,
+            _ptr(new_seqlens, torch.int32, "new_seqlens"), bs, hkv, d, page_size, num_pages,
+            _stream(stream), int(bool(use_pdl)))
+
+
+def pa_compact_cache(**kw):
+    """Kept rows of the cache moved to the front, in order, in place or to the pages of
+    ``dst_page_table``; see include/pa.h.  Keyword arguments: those of
+    ``_compact_cache_args``."""
+    _check("pa_compact_cache", load().pa_compact_cache(*_compact_cache_args(**kw)))
+
+
+def prepare_compact_cache(*, lib=None, **kw) -> PreparedCall:
+    """``pa_compact_cache`` with the given keyword arguments, marshalled once."""
+    return PreparedCall("pa_compact_cache", _compact_cache_args(**kw), lib,
+                        keep=tuple(kw.values()))
+
+
+def _evict_args(*, page_table, cache_seqlens, weights, k_cache, v_cache, max_seq_pages: int,
+                budget: int, kept, new_seqlens, num_first: int = 0, num_recent: int = 0,
+                dst_page_table=None, k_scale=None, v_scale=None, stream=None,
+                use_pdl: bool = True):
+    _on_device(page_table=page_table, cache_seqlens=cache_seqlens, weights=weights,
+               k_cache=k_cache, v_cache=v_cache, dst_page_table=dst_page_table, kept=kept,
+               new_seqlens=new_seqlens, k_scale=k_scale, v_scale=v_scale)
+    kv_dtype, ks, vs, (num_pages, hkv, page_size, d) = _pools(k_cache, v_cache, k_scale, v_scale)
+    bs = cache_seqlens.shape[0]
+    _shape(weights, (num_pages, hkv, page_size), "weights")
+    _shape(kept, (bs, hkv, int(budget)), "kept")
+    _shape(new_seqlens, (bs,), "new_seqlens")
+    pt, pt_stride = _table(page_table, bs, int(max_seq_pages), "page_table")
+    dst, dst_stride, dst_pages = _destination(page_table, dst_page_table, bs)
+    return (pt, pt_stride, _ptr(cache_seqlens, torch.int32, "cache_seqlens"), int(max_seq_pages),
+            _ptr(weights, torch.float32, "weights"), _ptr(k_cache, None, "k_cache"),
+            _ptr(v_cache, None, "v_cache"), ks, vs, kv_dtype, int(budget), int(num_first),
+            int(num_recent), dst, dst_stride, dst_pages, _ptr(kept, torch.int32, "kept"),
+            _ptr(new_seqlens, torch.int32, "new_seqlens"), bs, hkv, d, page_size, num_pages,
+            _stream(stream), int(bool(use_pdl)))
+
+
+def pa_evict(**kw):
+    """Each request's cache shrunk to ``budget`` rows per kv head by accumulated weight;
+    see include/pa.h.  Keyword arguments: those of ``_evict_args``."""
+    _check("pa_evict", load().pa_evict(*_evict_args(**kw)))
+
+
+def prepare_evict(*, lib=None, **kw) -> PreparedCall:
+    """``pa_evict`` with the given keyword arguments, marshalled once."""
+    return PreparedCall("pa_evict", _evict_args(**kw), lib, keep=tuple(kw.values()))

@@ -45,6 +45,18 @@ std::atomic<int32_t> g_hold_loads{0};
 std::atomic<int32_t> g_no_persist{0};
 std::atomic<int> g_sm_count[kMaxDevices];
 
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+using pa::from_cuda;
+
+size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
+
+int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+}  // namespace
+
+namespace pa {
+
 cudaError_t error_word(unsigned int** out) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -72,14 +84,6 @@ int sm_count_of_current_device() {
   }
   return n;
 }
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-using pa::from_cuda;
-
-size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
-
-int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 pa_status check_metadata(const void* req_pool_indices, const void* seq_lens,
                          const int32_t* req_to_token, int64_t req_to_token_rows,
@@ -135,6 +139,15 @@ pa_status check_attention(const void* q, const void* k_cache, const void* v_cach
   if (static_cast<int64_t>(max_seq_pages) * page_size > INT32_MAX) return PA_ERR_INVALID;
   return PA_OK;
 }
+
+}  // namespace pa
+
+namespace {
+
+using pa::check_attention;
+using pa::check_metadata;
+using pa::error_word;
+using pa::sm_count_of_current_device;
 
 // Limits of the producer that will run (the selected implementation, the query tile,
 // the window bounds), checked before any launch.  The decode-step entry points call it

@@ -86,7 +86,112 @@ struct ReduceParams {
   int32_t num_splits;
   void* out;   // bf16 [num_rows, 128]
   float* lse;  // [num_rows] or nullptr
+  // nullptr, or a device count of query rows: only the first *live_q * heads rows are
+  // combined and written
+  const int32_t* live_q;
+  int32_t heads;
   unsigned long long* ts;  // stage timestamps (instrumented builds only), else nullptr
+};
+
+struct RopeParams {
+  const void *q, *k, *v;  // bf16 rows, head h of token t at x + t * stride + h * 128
+  int64_t q_stride, k_stride, v_stride;
+  const int64_t* positions;
+  const int64_t* slots;
+  const double* inv_freq;
+  int32_t rotary_dim;
+  float amplitude;
+  int32_t num_tokens, num_q_heads, num_kv_heads;
+  void* q_out;
+  int64_t q_out_stride;
+  void *k_cache, *v_cache;
+  float *k_scale, *v_scale;  // int8 pools only
+  int32_t page_size;
+  int64_t num_pages;
+  unsigned int* err;
+};
+
+struct TreeMaskParams {
+  const int32_t* parents;
+  const int32_t* cu_seqlens_q;
+  int32_t bs, total_q, max_q_len;
+  int64_t* tree_mask;
+  int32_t mask_words;
+  unsigned int* err;
+};
+
+struct TreeParams {
+  const void* q;  // bf16 [total_q, Hq, 128]
+  const void *k_cache, *v_cache;
+  const float *k_scale, *v_scale;
+  const int32_t* page_table;
+  int64_t page_table_stride;
+  const int32_t* cache_seqlens;
+  const int32_t* cu_seqlens_q;
+  const uint32_t* tree_mask;  // 2 * mask_words 32-bit words a row
+  int32_t mask_words;
+  int32_t bs, total_q, max_q_len;
+  int32_t num_q_heads, num_kv_heads;
+  int64_t num_pages;
+  int32_t max_seq_pages, pages_per_split, num_splits;
+  float q_scale;  // sm_scale * log2(e)
+  // partials of several splits, or (one split) the output itself
+  float *m_out, *l_out, *acc_out;
+  void* out;
+  float* lse;
+  unsigned int* err;
+};
+
+struct WeightsParams {
+  const void* q;
+  const float* lse;
+  const void* k_cache;
+  const float* k_scale;
+  const int32_t* page_table;
+  int64_t page_table_stride;
+  const int32_t* cache_seqlens;
+  float* weights;
+  int32_t bs, num_q_heads, num_kv_heads;
+  int64_t num_pages;
+  int32_t max_seq_pages;
+  float q_scale;  // sm_scale * log2(e)
+  unsigned int* err;
+};
+
+struct SelectParams {
+  const int32_t* page_table;
+  int64_t page_table_stride;
+  const int32_t* cache_seqlens;
+  int32_t max_seq_pages;
+  const float* weights;
+  int32_t budget, num_first, num_recent;
+  int32_t* kept;
+  int32_t* new_seqlens;
+  int32_t bs, num_kv_heads, page_size;
+  int64_t num_pages;
+  unsigned int* err;
+};
+
+struct CompactParams {
+  const int32_t* page_table;
+  int64_t page_table_stride;
+  const int32_t* cache_seqlens;
+  int32_t max_seq_pages;
+  const int32_t* kept;
+  int32_t kept_heads;
+  int64_t kept_stride;
+  const int32_t* counts;
+  const int32_t* begin;  // nullptr: 0
+  int32_t max_kept;
+  void *k_cache, *v_cache;
+  float *k_scale, *v_scale, *weights;  // nullptr where absent
+  const int32_t* dst_page_table;
+  int64_t dst_page_table_stride;
+  int32_t dst_max_pages;
+  int32_t* new_seqlens;  // nullptr: not written
+  int32_t bs, num_kv_heads, page_size;
+  int64_t num_pages;
+  unsigned int* err;
 };
 
 // Step of the last failed launch on this host thread (for pa_last_error_string).
@@ -99,6 +204,26 @@ inline cudaError_t fail_at(cudaError_t e, const char* site) {
 // PA_OK for cudaSuccess; otherwise records `where`, the failed step and the CUDA error
 // for pa_last_error_string on this host thread and returns PA_ERR_CUDA.
 pa_status from_cuda(cudaError_t e, const char* where);
+
+// Device address of the current device's error word (looked up once per device).
+cudaError_t error_word(unsigned int** out);
+int sm_count_of_current_device();
+
+// Argument checks shared by the entry points: the metadata stage's, and those of every
+// attention over the pools (bs == 0 passes).
+pa_status check_metadata(const void* req_pool_indices, const void* seq_lens,
+                         const int32_t* req_to_token, int64_t req_to_token_rows,
+                         int64_t req_to_token_stride, const int64_t* mapping, int64_t mapping_len,
+                         int32_t* cache_seqlens, int32_t* cu_seqlens_k, int32_t* page_table,
+                         int64_t page_table_stride, int32_t* swa_page_table,
+                         int64_t swa_page_table_stride, int32_t bs, int32_t max_seq_pages,
+                         int32_t page_size);
+pa_status check_attention(const void* q, const void* k_cache, const void* v_cache,
+                          const float* k_scale, const float* v_scale, int32_t kv_dtype,
+                          const int32_t* page_table, int64_t page_table_stride,
+                          const int32_t* cache_seqlens, int32_t bs, int32_t num_q_heads,
+                          int32_t num_kv_heads, int32_t head_dim, int32_t page_size,
+                          int64_t num_pages, int32_t max_seq_pages, int32_t num_splits);
 
 cudaError_t launch_metadata(const MetadataParams& p, cudaStream_t stream, bool use_pdl);
 
@@ -119,5 +244,17 @@ cudaError_t launch_splitk_mma_window_int8(const SplitKParams& p, int bs, int gro
                                           int page_size, cudaStream_t stream, bool use_pdl);
 
 cudaError_t launch_reduce(const ReduceParams& p, cudaStream_t stream, bool use_pdl);
+
+cudaError_t launch_rope(const RopeParams& p, bool int8, bool interleaved, cudaStream_t stream,
+                        bool use_pdl);
+cudaError_t launch_tree_mask(const TreeMaskParams& p, cudaStream_t stream, bool use_pdl);
+cudaError_t launch_tree(const TreeParams& p, bool int8, int group, int page_size,
+                        cudaStream_t stream, bool use_pdl);
+cudaError_t launch_weights(const WeightsParams& p, bool int8, int group, int page_size,
+                           cudaStream_t stream, bool use_pdl);
+cudaError_t launch_select(const SelectParams& p, cudaStream_t stream, bool use_pdl);
+// in_place: the destination pages are the source pages.
+cudaError_t launch_compact(const CompactParams& p, bool int8, bool in_place, cudaStream_t stream,
+                           bool use_pdl);
 
 }  // namespace pa
