@@ -576,6 +576,7 @@ PA_API pa_status pa_build_tree_mask(const int32_t* parents, const int32_t* cu_se
  * `workspace` (16-byte aligned, workspace_bytes >= pa_workspace_bytes(total_q, num_q_heads,
  * 128, splits)) and a second launch combines them.  Calls that overlap on the GPU need
  * workspaces of their own.
+ * sm_scale is finite and positive.
  * Supported: head_dim 128; page_size 16, 32, 64, 128; num_q_heads / num_kv_heads in {1, 2,
  * 4, 8, 16}; 1 <= max_q_len <= 256; max_seq_pages * page_size <= 2^29.  All device memory.  Request lengths and row offsets
  * that only the device sees are bounds-checked like those of pa_decode_splitk_multi.

@@ -164,9 +164,14 @@ int32_t pa_choose_tree_splits(int32_t bs, int32_t max_q_len, int32_t num_q_heads
     return 1;
   if (sm_count <= 0) sm_count = pa::sm_count_of_current_device();
   if (sm_count <= 0) sm_count = 152;
-  const int64_t units = static_cast<int64_t>(bs) * max_q_len * num_q_heads;
-  int64_t want = cdiv(static_cast<int64_t>(sm_count) * 8, units);
+  const int64_t group = num_q_heads / num_kv_heads > 0 ? num_q_heads / num_kv_heads : 1;
+  const int64_t units = static_cast<int64_t>(bs) * num_kv_heads * cdiv(group * max_q_len, 256);
+  int64_t want = cdiv(static_cast<int64_t>(sm_count) * 3, units);
+  // at least two 128-token chunks per split
+  const int64_t most = cdiv(static_cast<int64_t>(max_seq_pages) * page_size, 256);
+  if (want > most) want = most;
   if (want > max_seq_pages) want = max_seq_pages;
+  if (want > 4096) want = 4096;
   const int64_t pages_per_split = cdiv(max_seq_pages, want);
   return static_cast<int32_t>(cdiv(max_seq_pages, pages_per_split));
 }
@@ -190,8 +195,9 @@ pa_status check_tree(const void* q, const void* k_cache, const void* v_cache, co
                      const int32_t* cu_seqlens_q, const int64_t* tree_mask, int32_t mask_words,
                      int32_t bs, int32_t total_q, int32_t max_q_len, int32_t num_q_heads,
                      int32_t num_kv_heads, int32_t head_dim, int32_t page_size, int64_t num_pages,
-                     int32_t max_seq_pages, int32_t num_splits, const void* workspace,
-                     size_t workspace_bytes, const void* out, int32_t* splits) {
+                     int32_t max_seq_pages, int32_t num_splits, float sm_scale,
+                     const void* workspace, size_t workspace_bytes, const void* out,
+                     int32_t* splits) {
   if (num_splits < 0 || max_q_len < 1 || mask_words < cdiv(max_q_len, 64)) return PA_ERR_INVALID;
   *splits = num_splits > 0 ? num_splits
                            : pa_choose_tree_splits(bs, max_q_len, num_q_heads, num_kv_heads,
@@ -203,12 +209,15 @@ pa_status check_tree(const void* q, const void* k_cache, const void* v_cache, co
   if (st != PA_OK) return st;
   if (!cu_seqlens_q || !tree_mask || !aligned(tree_mask, 8)) return PA_ERR_INVALID;
   if (!out || !aligned(out, 16)) return PA_ERR_INVALID;
+  if (!std::isfinite(sm_scale) || !(sm_scale > 0.f)) return PA_ERR_INVALID;
   if (*splits > 1 &&
       (!workspace || !aligned(workspace, 16) ||
        workspace_bytes < pa_workspace_bytes(total_q, num_q_heads, head_dim, *splits)))
     return PA_ERR_INVALID;
-  // (the second keeps every position the kernel forms within int32)
-  if (max_q_len > kMaxTreeNodes || static_cast<int64_t>(max_seq_pages) * page_size > (int64_t{1} << 29))
+  if (max_q_len > kMaxTreeNodes) return PA_ERR_UNSUPPORTED;
+  // keeps every position the kernel forms within int32
+  if (static_cast<int64_t>(max_seq_pages) * page_size > (int64_t{1} << 29)) return PA_ERR_UNSUPPORTED;
+  if (num_kv_heads * cdiv(static_cast<int64_t>(num_q_heads / num_kv_heads) * max_q_len, 256) > 65535)
     return PA_ERR_UNSUPPORTED;
   return PA_OK;
 }
@@ -233,8 +242,8 @@ pa_status pa_tree_attention(const void* q, const void* k_cache, const void* v_ca
   pa_status st = check_tree(q, k_cache, v_cache, k_scale, v_scale, kv_dtype, page_table,
                             page_table_stride, cache_seqlens, cu_seqlens_q, tree_mask, mask_words,
                             bs, total_q, max_q_len, num_q_heads, num_kv_heads, head_dim, page_size,
-                            num_pages, max_seq_pages, num_splits, workspace, workspace_bytes, out,
-                            &splits);
+                            num_pages, max_seq_pages, num_splits, sm_scale, workspace,
+                            workspace_bytes, out, &splits);
   if (st != PA_OK) return st;
   const size_t rows = static_cast<size_t>(total_q) * num_q_heads * splits;
   char* ws = static_cast<char*>(workspace);
@@ -306,8 +315,8 @@ pa_status pa_decode_step_tree(
     pa_status st = check_tree(q, k_cache, v_cache, k_scale, v_scale, kv_dtype, page_table,
                               page_table_stride, cache_seqlens, cu_seqlens_q, tree_mask,
                               mask_words, bs, total_q, max_q_len, num_q_heads, num_kv_heads,
-                              head_dim, page_size, num_pages, max_seq_pages, num_splits, workspace,
-                              workspace_bytes, out, &splits);
+                              head_dim, page_size, num_pages, max_seq_pages, num_splits, sm_scale,
+                              workspace, workspace_bytes, out, &splits);
     if (st != PA_OK) return st;
   }
   pa_status st = pa_build_metadata_full(

@@ -250,6 +250,8 @@ cudaError_t launch_rope(const RopeParams& p, bool int8, bool interleaved, cudaSt
 cudaError_t launch_tree_mask(const TreeMaskParams& p, cudaStream_t stream, bool use_pdl);
 cudaError_t launch_tree(const TreeParams& p, bool int8, int group, int page_size,
                         cudaStream_t stream, bool use_pdl);
+cudaError_t launch_tree_mma_bf16(const TreeParams& p, int group, int page_size,
+                                 cudaStream_t stream, bool use_pdl);
 cudaError_t launch_weights(const WeightsParams& p, bool int8, int group, int page_size,
                            cudaStream_t stream, bool use_pdl);
 cudaError_t launch_select(const SelectParams& p, cudaStream_t stream, bool use_pdl);

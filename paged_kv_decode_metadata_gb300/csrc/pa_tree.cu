@@ -171,7 +171,7 @@ cudaError_t launch_tree_mask(const TreeMaskParams& p, cudaStream_t stream, bool 
 
 cudaError_t launch_tree(const TreeParams& p, bool int8, int group, int page_size,
                         cudaStream_t stream, bool use_pdl) {
-  (void)group;
+  if (!int8) return launch_tree_mma_bf16(p, group, page_size, stream, use_pdl);
   const dim3 grid(static_cast<unsigned>(p.num_splits * p.max_q_len),
                   static_cast<unsigned>(p.num_q_heads), static_cast<unsigned>(p.bs));
   return fail_at(launch_kernel(int8 ? tree_kernel<true> : tree_kernel<false>, grid, dim3(kWarps * 32),

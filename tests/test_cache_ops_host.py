@@ -74,6 +74,8 @@ TREE = dict(q=FAKE, k=FAKE, v=FAKE, ks=None, vs=None, kv=0, pt=FAKE, pts=16, cl=
     (dict(ws=None), B.PA_ERR_INVALID),
     (dict(wsb=100), B.PA_ERR_INVALID),
     (dict(S=-1), B.PA_ERR_INVALID),
+    (dict(scale=0.0), B.PA_ERR_INVALID), (dict(scale=-1.0), B.PA_ERR_INVALID),
+    (dict(scale=math.nan), B.PA_ERR_INVALID), (dict(scale=math.inf), B.PA_ERR_INVALID),
     (dict(S=5000), B.PA_ERR_INVALID),
     (dict(hq=30), B.PA_ERR_INVALID),
     (dict(hq=256), B.PA_ERR_UNSUPPORTED),          # group 32
