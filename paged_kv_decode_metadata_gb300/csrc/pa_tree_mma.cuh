@@ -39,6 +39,9 @@ constexpr int kTile = 128;            // rows of a tile, tokens of a chunk
 constexpr int kSoftmaxThreads = 256;  // two groups of four warps
 constexpr int kTmaWarp = 8, kMmaWarp = 9, kFixWarp = 10;
 constexpr int kThreads = 384;
+// registers per thread after the split: 256 x 224 + 128 x 56 = 384 x 168 at launch
+constexpr int kSoftmaxRegs = 224, kOtherRegs = 56;
+static_assert(256 * kSoftmaxRegs + 128 * kOtherRegs <= kThreads * 168, "register split");
 constexpr int kSlots = 5;             // ring tiles
 constexpr int kHalfBytes = kTile * 128;       // 64 channels of 128 rows
 constexpr int kTileBytes = 2 * kHalfBytes;
@@ -50,7 +53,7 @@ struct Shared {
   static constexpr int kEnd = kRing + kSlots * kTileBytes;
   struct Control {
     uint64_t full[kSlots], empty[kSlots];
-    uint64_t q_full, s_full[2], p_ready[2], o_full[2], v_last, v_fixed, drained;
+    uint64_t q_full, s_full[2], p_half[2], p_ready[2], o_full[2], v_last, v_fixed, drained;
     uint32_t tmem;
     int abort, issued;
   };
@@ -103,6 +106,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&ctl.q_full, 1);
     for (int s = 0; s < 2; ++s) {
       mbar_init(&ctl.s_full[s], 1);
+      mbar_init(&ctl.p_half[s], 4);
       mbar_init(&ctl.p_ready[s], 4);
       mbar_init(&ctl.o_full[s], 1);
     }
@@ -181,10 +185,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     *abort_flag = 1;
   };
 
-  float m_ref = -CUDART_INF_F, l = 0.f;  // softmax threads: their row's reference and sum
-
   if (warp < kTmaWarp) {
     // ======================= softmax ===================================================
+    umma::registers_up<kSoftmaxRegs>();
     const int s = warp >> 2, r = tid & (kTile - 1);
     const int tile = two ? s : 0;
     const uint32_t lane_base = static_cast<uint32_t>(warp & 3) << 21;  // lane 32 (warp % 4)
@@ -196,6 +199,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int words = 2 * prm.mask_words;
     const float scale = prm.q_scale;
     const int mine = stream_chunks(s);
+    float m_ref = -CUDART_INF_F, l = 0.f;  // the row's reference and sum of weights
     for (int k = 0; k < mine; ++k) {
       const int c = two ? k : 2 * k + s;
       const int p0 = begin + c * kTile;
@@ -223,9 +227,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
       }
-      float mx[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
+      float mx[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
-      for (int j = 0; j < kTile; ++j) mx[j & 3] = fmaxf(mx[j & 3], x[j]);
+      for (int j = 4; j < kTile - 4; j += 8)
+#pragma unroll
+        for (int u = 0; u < 4; ++u) mx[u] = umma::max3(mx[u], x[j + u], x[j + 4 + u]);
+#pragma unroll
+      for (int u = 0; u < 4; ++u) mx[u] = fmaxf(mx[u], x[kTile - 4 + u]);
       // (sm_scale > 0: the largest score is the largest product)
       const float m_new = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale;
       float alpha = 1.f;
@@ -248,26 +256,118 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       const float ref = m_ref == -CUDART_INF_F ? 0.f : m_ref;
-      float sum[4] = {0.f, 0.f, 0.f, 0.f};
+      const uint64_t scale2 = umma::pair(scale, scale), ref2 = umma::pair(-ref, -ref);
+      uint64_t sum[4] = {0, 0, 0, 0};  // pairs of +0
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         uint32_t w[16];
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
-          const float a = mma::fast_exp2(fmaf(x[32 * i + 2 * j], scale, -ref));
-          const float d = mma::fast_exp2(fmaf(x[32 * i + 2 * j + 1], scale, -ref));
-          sum[j & 3] += a + d;
-          w[j] = mma::pack_bf16(a, d);
+          float lo, hi;
+          umma::unpair(umma::fma2(umma::pair(x[32 * i + 2 * j], x[32 * i + 2 * j + 1]), scale2, ref2),
+                       lo, hi);
+          lo = mma::fast_exp2(lo);
+          hi = mma::fast_exp2(hi);
+          sum[j & 3] = umma::add2(sum[j & 3], umma::pair(lo, hi));
+          w[j] = mma::pack_bf16(lo, hi);
         }
         umma::st16(sc + 16 * i, w);
+        if (i == 1) {  // half of the weights: their products may start
+          umma::wait_st();
+          umma::fence_before();
+          __syncwarp();
+          if (lane == 0) mma::mbar_arrive(&ctl.p_half[s]);
+        }
       }
-      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+      float lo, hi;
+      umma::unpair(umma::add2(umma::add2(sum[0], sum[1]), umma::add2(sum[2], sum[3])), lo, hi);
+      l += lo + hi;
       umma::wait_st();
       umma::fence_before();
       __syncwarp();
       if (lane == 0) mma::mbar_arrive(&ctl.p_ready[s]);
     }
-  } else if (warp == kTmaWarp) {
+
+    // ----- the rows' results -----------------------------------------------------------
+    const bool has = mine > 0;
+    if (has && !*abort_flag && !mbar_wait_bounded(&ctl.o_full[s], 0) && lane == 0) give_up();
+    umma::fence_after();
+    trigger_dependents();
+    float factor = 1.f;  // of this stream's accumulator
+    float* joined = reinterpret_cast<float*>(smem + Shared::kRing);
+    float2* ml = reinterpret_cast<float2*>(joined + kTile * kMergeStride);
+    // (both streams' products are over before either writes into the ring)
+    asm volatile("bar.sync 1, 256;" ::: "memory");
+    if (!two) {  // one tile: join the streams, stream 1 hands its rows over
+      ml[s * kTile + r] = make_float2(m_ref, l);
+      asm volatile("bar.sync 1, 256;" ::: "memory");
+      const float2 other = ml[(1 - s) * kTile + r];
+      const float m_all = fmaxf(m_ref, other.x);
+      if (m_all != -CUDART_INF_F) {
+        factor = m_ref == -CUDART_INF_F ? 0.f : mma::fast_exp2(m_ref - m_all);
+        l = l * factor + (other.x == -CUDART_INF_F ? 0.f : other.y * mma::fast_exp2(other.x - m_all));
+        m_ref = m_all;
+      }
+      if (s == 1 && has) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint32_t o[32];
+          umma::ld32(oc + 32 * i, o);
+          umma::wait_ld(o);
+#pragma unroll
+          for (int j = 0; j < 32; ++j)
+            joined[r * kMergeStride + 32 * i + j] = __uint_as_float(o[j]) * factor;
+        }
+      }
+      asm volatile("bar.sync 1, 256;" ::: "memory");
+    }
+    const bool add = !two && stream_chunks(1) > 0;
+    const bool write = live && !*abort_flag;
+    if (two || s == 0) {
+      const int64_t slot = write ? slot_of(tile, r) : 0;
+      const float inv = S == 1 ? (l > 0.f || l != l ? 1.f / l : 0.f) : 1.f;
+      factor *= inv;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        uint32_t o[32];
+        umma::ld32(oc + 32 * i, o);
+        umma::wait_ld(o);
+        float y[32];
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+          y[j] = __uint_as_float(o[j]) * factor;
+          if (add) y[j] += joined[r * kMergeStride + 32 * i + j] * inv;
+        }
+        if (write && S == 1) {
+          uint4* out = static_cast<uint4*>(prm.out) + slot * 16 + 4 * i;
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            out[j] = make_uint4(mma::pack_bf16(y[8 * j], y[8 * j + 1]),
+                                mma::pack_bf16(y[8 * j + 2], y[8 * j + 3]),
+                                mma::pack_bf16(y[8 * j + 4], y[8 * j + 5]),
+                                mma::pack_bf16(y[8 * j + 6], y[8 * j + 7]));
+        } else if (write) {
+          float4* acc = reinterpret_cast<float4*>(prm.acc_out) + (slot * S + split) * 32 + 8 * i;
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            acc[j] = make_float4(y[4 * j], y[4 * j + 1], y[4 * j + 2], y[4 * j + 3]);
+        }
+        __syncwarp();
+      }
+      if (write) {
+        const float m_nat = m_ref * 0.69314718055994530942f;  // -inf stays -inf
+        if (S > 1) {
+          prm.m_out[slot * S + split] = m_nat;
+          prm.l_out[slot * S + split] = l;
+        } else if (prm.lse != nullptr) {
+          prm.lse[slot] = m_ref == -CUDART_INF_F ? m_ref : m_nat + logf(l);
+        }
+      }
+    }
+    umma::fence_before();
+  } else {
+    umma::registers_down<kOtherRegs>();
+    if (warp == kTmaWarp) {
     // ======================= TMA ========================================================
     constexpr int kBoxRows = P < 64 ? P : 64;
     constexpr int kBoxes = kTile / kBoxRows;
@@ -363,7 +463,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int c = 0; c < chunks && ok; ++c) {
         const int s_begin = two ? 0 : c & 1, s_end = two ? 2 : s_begin + 1;
         for (int s = s_begin; s < s_end && ok; ++s) {
-          ok = mbar_wait_bounded(&ctl.p_ready[s], used[s] & 1u);
+          ok = mbar_wait_bounded(&ctl.p_half[s], used[s] & 1u);
           if (ok && s == s_begin) {
             ok = c == chunks - 1 && clean_last ? mbar_wait_bounded(&ctl.v_fixed, 0)
                                                : wait_tile(2 * c + 1);
@@ -371,10 +471,18 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!ok) break;
           umma::fence_after();
           const uint32_t v = tile_addr(2 * c + 1);
+          // 16 tokens a step: 8 columns of P, 16 rows of V
 #pragma unroll
-          for (int j = 0; j < 8; ++j)  // 16 tokens each: 8 columns of P, 16 rows of V
+          for (int j = 0; j < 4; ++j)
             umma::mma_ts(o_col(s), s_col(s) + 8 * j, umma::operand(v + j * 16 * 128, kHalfBytes),
                          kOutput, used[s] > 0 || j > 0);
+          ok = mbar_wait_bounded(&ctl.p_ready[s], used[s] & 1u);
+          if (!ok) break;
+          umma::fence_after();
+#pragma unroll
+          for (int j = 4; j < 8; ++j)
+            umma::mma_ts(o_col(s), s_col(s) + 8 * j, umma::operand(v + j * 16 * 128, kHalfBytes),
+                         kOutput, true);
           ++used[s];
           if (s == s_end - 1) umma::commit(&ctl.empty[(2 * c + 1) % kSlots]);
           const int next = two ? c + 1 : c + 2;
@@ -411,90 +519,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (lane == 0) {
       give_up();
     }
+    }
   }
 
-  // ======================= the rows' results ==============================================
-  if (warp < kTmaWarp) {
-    const int s = warp >> 2, r = tid & (kTile - 1);
-    const int tile = two ? s : 0;
-    const uint32_t oc = o_col(s) + (static_cast<uint32_t>(warp & 3) << 21);
-    const bool has = stream_chunks(s) > 0;
-    if (has && !*abort_flag && !mbar_wait_bounded(&ctl.o_full[s], 0) && lane == 0) give_up();
-    umma::fence_after();
-    trigger_dependents();
-    float factor = 1.f;  // of this stream's accumulator
-    float* joined = reinterpret_cast<float*>(smem + Shared::kRing);
-    float2* ml = reinterpret_cast<float2*>(joined + kTile * kMergeStride);
-    // (both streams' products are over before either writes into the ring)
-    asm volatile("bar.sync 1, 256;" ::: "memory");
-    if (!two) {  // one tile: join the streams, stream 1 hands its rows over
-      ml[s * kTile + r] = make_float2(m_ref, l);
-      asm volatile("bar.sync 1, 256;" ::: "memory");
-      const float2 other = ml[(1 - s) * kTile + r];
-      const float m_all = fmaxf(m_ref, other.x);
-      if (m_all != -CUDART_INF_F) {
-        factor = m_ref == -CUDART_INF_F ? 0.f : mma::fast_exp2(m_ref - m_all);
-        l = l * factor + (other.x == -CUDART_INF_F ? 0.f : other.y * mma::fast_exp2(other.x - m_all));
-        m_ref = m_all;
-      }
-      if (s == 1 && has) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          uint32_t o[32];
-          umma::ld32(oc + 32 * i, o);
-          umma::wait_ld(o);
-#pragma unroll
-          for (int j = 0; j < 32; ++j)
-            joined[r * kMergeStride + 32 * i + j] = __uint_as_float(o[j]) * factor;
-        }
-      }
-      asm volatile("bar.sync 1, 256;" ::: "memory");
-    }
-    const bool add = !two && stream_chunks(1) > 0;
-    const bool live = r < rows - tile * kTile && (two || s == 0) && !*abort_flag;
-    if (two || s == 0) {
-      const int64_t slot = live ? slot_of(tile, r) : 0;
-      const float inv = S == 1 ? (l > 0.f || l != l ? 1.f / l : 0.f) : 1.f;
-      factor *= inv;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        uint32_t o[32];
-        umma::ld32(oc + 32 * i, o);
-        umma::wait_ld(o);
-        float y[32];
-#pragma unroll
-        for (int j = 0; j < 32; ++j) {
-          y[j] = __uint_as_float(o[j]) * factor;
-          if (add) y[j] += joined[r * kMergeStride + 32 * i + j] * inv;
-        }
-        if (live && S == 1) {
-          uint4* out = static_cast<uint4*>(prm.out) + slot * 16 + 4 * i;
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            out[j] = make_uint4(mma::pack_bf16(y[8 * j], y[8 * j + 1]),
-                                mma::pack_bf16(y[8 * j + 2], y[8 * j + 3]),
-                                mma::pack_bf16(y[8 * j + 4], y[8 * j + 5]),
-                                mma::pack_bf16(y[8 * j + 6], y[8 * j + 7]));
-        } else if (live) {
-          float4* acc = reinterpret_cast<float4*>(prm.acc_out) + (slot * S + split) * 32 + 8 * i;
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-            acc[j] = make_float4(y[4 * j], y[4 * j + 1], y[4 * j + 2], y[4 * j + 3]);
-        }
-        __syncwarp();
-      }
-      if (live) {
-        const float m_nat = m_ref * 0.69314718055994530942f;  // -inf stays -inf
-        if (S > 1) {
-          prm.m_out[slot * S + split] = m_nat;
-          prm.l_out[slot * S + split] = l;
-        } else if (prm.lse != nullptr) {
-          prm.lse[slot] = m_ref == -CUDART_INF_F ? m_ref : m_nat + logf(l);
-        }
-      }
-    }
-    umma::fence_before();
-  }
   __syncthreads();  // every load from tensor memory is over
   if (*abort_flag && tid == 0) {
     // copies in flight must land before the block's memory is given up
