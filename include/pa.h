@@ -571,14 +571,18 @@ PA_API pa_status pa_build_tree_mask(const int32_t* parents, const int32_t* cu_se
  * metadata stage writes it).  K of positions that a query does not attend to may hold
  * anything; so may V at or past n, but a non-finite V row below n reaches every query of
  * its request (a weight of 0 times it is NaN).
- * num_splits: context splits, or 0 for pa_choose_tree_splits(...).  With one split the
- * output is written directly and `workspace` may be NULL; otherwise the partials go to
- * `workspace` (16-byte aligned, workspace_bytes >= pa_workspace_bytes(total_q, num_q_heads,
- * 128, splits)) and a second launch combines them.  Calls that overlap on the GPU need
+ * num_splits: the most pieces that a row's context may be cut into, or 0 for
+ * pa_choose_tree_splits(...).  With 1 the output is written directly and `workspace` may be
+ * NULL; otherwise the partials of rows that are cut go to `workspace` (16-byte aligned,
+ * workspace_bytes >= pa_workspace_bytes(total_q, num_q_heads, 128, that number)) and a
+ * second launch combines them.  The cuts follow from the lengths on the device, so equal
+ * inputs give equal bits.  Calls that overlap on the GPU need
  * workspaces of their own.
  * sm_scale is finite and positive.
  * Supported: head_dim 128; page_size 16, 32, 64, 128; num_q_heads / num_kv_heads in {1, 2,
- * 4, 8, 16}; 1 <= max_q_len <= 256; max_seq_pages * page_size <= 2^29.  All device memory.  Request lengths and row offsets
+ * 4, 8, 16}; 1 <= max_q_len <= 256; max_seq_pages * page_size <= 2^29 and bs *
+ * num_kv_heads * ceil(num_q_heads / num_kv_heads * max_q_len / 256) * ceil(max_seq_pages *
+ * page_size / 128) < 2^30.  All device memory.  Request lengths and row offsets
  * that only the device sees are bounds-checked like those of pa_decode_splitk_multi.
  */
 PA_API pa_status pa_tree_attention(
@@ -611,8 +615,8 @@ PA_API pa_status pa_decode_step_tree(
     size_t workspace_bytes, void* out, float* lse, void* stream, int32_t use_pdl);
 
 /*
- * The split count that pa_tree_attention picks for num_splits == 0 (sm_count <= 0: the
- * current device), and the workspace bytes it then needs (0 with one split).
+ * The number of pieces that pa_tree_attention allows for num_splits == 0 (sm_count <= 0:
+ * the current device), and the workspace bytes it then needs (0 where it is 1).
  */
 PA_API int32_t pa_choose_tree_splits(int32_t bs, int32_t max_q_len, int32_t num_q_heads,
                                      int32_t num_kv_heads, int32_t page_size,

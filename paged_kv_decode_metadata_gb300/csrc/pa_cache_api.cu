@@ -164,16 +164,18 @@ int32_t pa_choose_tree_splits(int32_t bs, int32_t max_q_len, int32_t num_q_heads
     return 1;
   if (sm_count <= 0) sm_count = pa::sm_count_of_current_device();
   if (sm_count <= 0) sm_count = 152;
+  // The batch's chunks of 128 tokens are shared out equally, so a unit (up to 256 rows of a
+  // kv head) longer than a share is cut.  Shares of a batch of equal lengths, and room for
+  // one of half the length on average (a ragged one) before shares have to grow.
   const int64_t group = num_q_heads / num_kv_heads > 0 ? num_q_heads / num_kv_heads : 1;
   const int64_t units = static_cast<int64_t>(bs) * num_kv_heads * cdiv(group * max_q_len, 256);
-  int64_t want = cdiv(static_cast<int64_t>(sm_count) * 3, units);
-  // at least two 128-token chunks per split
-  const int64_t most = cdiv(static_cast<int64_t>(max_seq_pages) * page_size, 256);
-  if (want > most) want = most;
-  if (want > max_seq_pages) want = max_seq_pages;
+  const int64_t chunks = cdiv(static_cast<int64_t>(max_seq_pages) * page_size, 128);
+  int64_t share = units * chunks / sm_count;
+  if (share < 1) share = 1;
+  int64_t want = cdiv(2 * chunks, share) + 1;
+  if (want > chunks) want = chunks;  // a piece holds a chunk at least
   if (want > 4096) want = 4096;
-  const int64_t pages_per_split = cdiv(max_seq_pages, want);
-  return static_cast<int32_t>(cdiv(max_seq_pages, pages_per_split));
+  return static_cast<int32_t>(want);
 }
 
 size_t pa_tree_workspace_bytes(int32_t bs, int32_t total_q, int32_t max_q_len, int32_t num_q_heads,
@@ -217,8 +219,10 @@ pa_status check_tree(const void* q, const void* k_cache, const void* v_cache, co
   if (max_q_len > kMaxTreeNodes) return PA_ERR_UNSUPPORTED;
   // keeps every position the kernel forms within int32
   if (static_cast<int64_t>(max_seq_pages) * page_size > (int64_t{1} << 29)) return PA_ERR_UNSUPPORTED;
-  if (num_kv_heads * cdiv(static_cast<int64_t>(num_q_heads / num_kv_heads) * max_q_len, 256) > 65535)
-    return PA_ERR_UNSUPPORTED;
+  // keeps the batch's chunks (128 tokens of up to 256 rows of a kv head) within 31 bits
+  const int64_t tiles = cdiv(static_cast<int64_t>(num_q_heads / num_kv_heads) * max_q_len, 256);
+  const int64_t chunks = cdiv(static_cast<int64_t>(max_seq_pages) * page_size, 128);
+  if (static_cast<int64_t>(bs) * num_kv_heads > INT32_MAX / 2 / (tiles * chunks)) return PA_ERR_UNSUPPORTED;
   return PA_OK;
 }
 
@@ -266,8 +270,17 @@ pa_status pa_tree_attention(const void* q, const void* k_cache, const void* v_ca
   p.num_kv_heads = num_kv_heads;
   p.num_pages = num_pages;
   p.max_seq_pages = max_seq_pages;
-  p.pages_per_split = static_cast<int32_t>(cdiv(max_seq_pages, splits));
   p.num_splits = splits;
+  const int64_t chunks = cdiv(static_cast<int64_t>(max_seq_pages) * page_size, 128);
+  // a unit of c chunks meets at most floor((c - 1) / share) + 2 shares (c of them if share = 1)
+  p.min_share = splits == 1 || splits >= chunks
+                    ? 1
+                    : static_cast<int32_t>(cdiv(chunks, splits - 1));
+  const int64_t most = static_cast<int64_t>(bs) * num_kv_heads *
+                       cdiv(static_cast<int64_t>(num_q_heads / num_kv_heads) * max_q_len, 256) * chunks;
+  int64_t sms = pa::sm_count_of_current_device();
+  if (sms < 1) sms = 1;
+  p.blocks = static_cast<int32_t>(most < sms ? most : sms);
   p.q_scale = sm_scale * 1.4426950408889634f;  // log2(e): the kernel works in base 2
   if (splits > 1) {
     p.m_out = reinterpret_cast<float*>(ws);
@@ -283,17 +296,7 @@ pa_status pa_tree_attention(const void* q, const void* k_cache, const void* v_ca
                               use_pdl != 0),
               "tree attention launch");
   if (st != PA_OK || splits == 1) return st;
-  pa::ReduceParams r = {};
-  r.m = p.m_out;
-  r.l = p.l_out;
-  r.acc = p.acc_out;
-  r.num_rows = static_cast<int64_t>(total_q) * num_q_heads;
-  r.num_splits = splits;
-  r.out = out;
-  r.lse = lse;
-  r.live_q = cu_seqlens_q + bs;
-  r.heads = num_q_heads;
-  return finish(pa::launch_reduce(r, s, use_pdl != 0), "reducer launch");
+  return finish(pa::launch_tree_join(p, s, use_pdl != 0), "tree join launch");
 }
 
 pa_status pa_decode_step_tree(

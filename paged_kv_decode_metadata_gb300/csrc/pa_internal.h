@@ -86,10 +86,6 @@ struct ReduceParams {
   int32_t num_splits;
   void* out;   // bf16 [num_rows, 128]
   float* lse;  // [num_rows] or nullptr
-  // nullptr, or a device count of query rows: only the first *live_q * heads rows are
-  // combined and written
-  const int32_t* live_q;
-  int32_t heads;
   unsigned long long* ts;  // stage timestamps (instrumented builds only), else nullptr
 };
 
@@ -133,7 +129,10 @@ struct TreeParams {
   int32_t bs, total_q, max_q_len;
   int32_t num_q_heads, num_kv_heads;
   int64_t num_pages;
-  int32_t max_seq_pages, pages_per_split, num_splits;
+  int32_t max_seq_pages;
+  int32_t num_splits;  // most pieces of a row's context (partial slots per row)
+  int32_t min_share;   // fewest chunks in a block's share (keeps the pieces within num_splits)
+  int32_t blocks;
   float q_scale;  // sm_scale * log2(e)
   // partials of several splits, or (one split) the output itself
   float *m_out, *l_out, *acc_out;
@@ -247,6 +246,8 @@ cudaError_t launch_reduce(const ReduceParams& p, cudaStream_t stream, bool use_p
 
 cudaError_t launch_rope(const RopeParams& p, bool int8, bool interleaved, cudaStream_t stream,
                         bool use_pdl);
+// Combines the partials that the tree attention left in `m_out`, `l_out` and `acc_out`.
+cudaError_t launch_tree_join(const TreeParams& p, cudaStream_t stream, bool use_pdl);
 cudaError_t launch_tree_mask(const TreeMaskParams& p, cudaStream_t stream, bool use_pdl);
 cudaError_t launch_tree(const TreeParams& p, bool int8, int group, int page_size,
                         cudaStream_t stream, bool use_pdl);

@@ -38,13 +38,11 @@ __global__ void __launch_bounds__(kThreads) reduce_kernel(const ReduceParams p) 
   const int s_begin = min(sub * spw, S), s_end = min(s_begin + spw, S);
   float* w = smem + warp * S;
   float4* part = reinterpret_cast<float4*>(smem + kWarps * S);
-  bool active = row < p.num_rows;
+  const bool active = row < p.num_rows;
 
   PA_TS_FIRST(p.ts, 2, kTsEntry);
   grid_dependency_wait();  // the producer's partials are complete and visible
   PA_TS_FIRST(p.ts, 2, kTsReady);
-  // rows past the batch's last query have no partials (their loads below read row 0)
-  if (p.live_q != nullptr) active = active && row < static_cast<int64_t>(*p.live_q) * p.heads;
 
   const int64_t r = active ? row : 0;
   const float4* acc = reinterpret_cast<const float4*>(p.acc + r * S * 128) + lane;

@@ -1,10 +1,5 @@
-// Attention of drafted trees over the paged cache, and the trees' ancestor masks.
-//
-// Mathematics.  Query i of a request sees every committed position (j < n - q_len) and the
-// drafted positions of its ancestor mask; over the positions of a split,
-//   m = max x_j, l = sum e^(x_j - m), acc = sum e^(x_j - m) V_j,   x_j = sm_scale q . K_j,
-// in one pass with the running maximum; splits are joined by the reducer, and a single
-// split writes acc / l and m + ln l itself.
+// Ancestor masks of drafted trees, and the join of the partial results that the tree
+// attention (pa_tree_mma.cuh) leaves of rows whose context was cut into pieces.
 #include <math_constants.h>
 
 #include "pa_common.cuh"
@@ -65,7 +60,7 @@ __global__ void __launch_bounds__(kWarps * 32) tree_kernel(const TreeParams p, i
   __shared__ float m_s[kWarps], l_s[kWarps];
   __shared__ float4 o_s[kWarps][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int split = blockIdx.x % p.num_splits, qi = blockIdx.x / p.num_splits;
+  const int qi = blockIdx.x;
   const int head = blockIdx.y, b = blockIdx.z;
   const int kvh = head / (p.num_q_heads / p.num_kv_heads);
   grid_dependency_wait();
@@ -88,8 +83,7 @@ __global__ void __launch_bounds__(kWarps * 32) tree_kernel(const TreeParams p, i
                                                   (row * p.num_q_heads + head) * 128)[lane];
   const float q0 = bf16_lo(qw.x), q1 = bf16_hi(qw.x), q2 = bf16_lo(qw.y), q3 = bf16_hi(qw.y);
   const int base = n - q_len;
-  const int begin = split * p.pages_per_split * page_size;
-  const int end = min(n, begin + p.pages_per_split * page_size);
+  const int begin = 0, end = n;
   float m = -CUDART_INF_F, l = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int j = begin + warp; j < end; j += kWarps) {
@@ -144,14 +138,8 @@ __global__ void __launch_bounds__(kWarps * 32) tree_kernel(const TreeParams p, i
     o.x += ow.x * a; o.y += ow.y * a; o.z += ow.z * a; o.w += ow.w * a;
   }
   const int64_t slot = row * p.num_q_heads + head;
-  if (p.num_splits > 1) {
-    const int64_t s = slot * p.num_splits + split;
-    if (lane == 0) {
-      p.m_out[s] = mm * 0.69314718055994530942f;
-      p.l_out[s] = total;
-    }
-    reinterpret_cast<float4*>(p.acc_out)[s * 32 + lane] = o;
-  } else {
+  {
+    if (p.num_splits > 1 && lane == 0) p.l_out[slot * p.num_splits] = -1.f;
     const float inv = total > 0.f ? 1.f / total : 0.f;
     const __nv_bfloat162 lo = __floats2bfloat162_rn(o.x * inv, o.y * inv);
     const __nv_bfloat162 hi = __floats2bfloat162_rn(o.z * inv, o.w * inv);
@@ -162,6 +150,72 @@ __global__ void __launch_bounds__(kWarps * 32) tree_kernel(const TreeParams p, i
   }
 }
 
+// ---- the join of a row's pieces ---------------------------------------------------------------
+
+constexpr int kJoinWarps = 8;
+
+// The list of a row's pieces is its l values up to the first negative one (or num_splits of
+// them); a row whose first l is negative has its output already.  A warp looks at `per`
+// rows at once and combines those that were cut, a lane owning 4 channels:
+//   M = max m_s, out = sum acc_s e^(m_s - M) / sum l_s e^(m_s - M), lse = M + ln of that sum.
+__global__ void __launch_bounds__(kJoinWarps * 32) tree_join_kernel(const TreeParams p, int per) {
+  const int lane = threadIdx.x & 31;
+  const int64_t row0 =
+      (static_cast<int64_t>(blockIdx.x) * kJoinWarps + (threadIdx.x >> 5)) * per;
+  const int S = p.num_splits;
+  grid_dependency_wait();
+  const int64_t rows =
+      static_cast<int64_t>(max(0, min(p.cu_seqlens_q[p.bs], p.total_q))) * p.num_q_heads;
+  const bool cut = lane < per && row0 + lane < rows && !(p.l_out[(row0 + lane) * S] < 0.f);
+  uint32_t todo = __ballot_sync(0xffffffffu, cut);
+  while (todo != 0) {
+    const int64_t row = row0 + __ffs(todo) - 1;
+    todo &= todo - 1;
+    const float* m = p.m_out + row * S;
+    const float* l = p.l_out + row * S;
+    const float4* acc = reinterpret_cast<const float4*>(p.acc_out) + row * S * 32 + lane;
+    float top = -CUDART_INF_F, total = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int s0 = 0; s0 < S; s0 += 32) {
+      const float ls = s0 + lane < S ? l[s0 + lane] : -1.f;
+      const uint32_t ends = __ballot_sync(0xffffffffu, ls < 0.f);
+      const int count = ends != 0 ? __ffs(ends) - 1 : 32;
+      const float ms = lane < count ? m[s0 + lane] : -CUDART_INF_F;
+      const float new_top = fmaxf(top, warp_max(ms));
+      if (new_top != -CUDART_INF_F) {
+        const float keep = top == -CUDART_INF_F ? 0.f : expf(top - new_top);
+        const float w = ms == -CUDART_INF_F ? 0.f : expf(ms - new_top);
+        total = total * keep + warp_sum(lane < count ? w * ls : 0.f);
+        o.x *= keep; o.y *= keep; o.z *= keep; o.w *= keep;
+        for (int s = 0; s < count; s += 4) {
+          float4 a[4];
+#pragma unroll
+          for (int u = 0; u < 4; ++u) a[u] = acc[(s0 + min(s + u, count - 1)) * 32];
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const float ws = __shfl_sync(0xffffffffu, w, min(s + u, count - 1));
+            if (s + u < count && ws != 0.f) {
+              o.x = fmaf(ws, a[u].x, o.x);
+              o.y = fmaf(ws, a[u].y, o.y);
+              o.z = fmaf(ws, a[u].z, o.z);
+              o.w = fmaf(ws, a[u].w, o.w);
+            }
+          }
+        }
+        top = new_top;
+      }
+      if (count < 32) break;
+    }
+    const float inv = top == -CUDART_INF_F ? 0.f : 1.f / total;
+    const __nv_bfloat162 lo = __floats2bfloat162_rn(o.x * inv, o.y * inv);
+    const __nv_bfloat162 hi = __floats2bfloat162_rn(o.z * inv, o.w * inv);
+    static_cast<uint2*>(p.out)[row * 32 + lane] = make_uint2(
+        *reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+    if (p.lse != nullptr && lane == 0)
+      p.lse[row] = top == -CUDART_INF_F ? top : top + logf(total);
+  }
+}
+
 }  // namespace
 
 cudaError_t launch_tree_mask(const TreeMaskParams& p, cudaStream_t stream, bool use_pdl) {
@@ -169,10 +223,21 @@ cudaError_t launch_tree_mask(const TreeMaskParams& p, cudaStream_t stream, bool 
                  "cudaLaunchKernelEx");
 }
 
+cudaError_t launch_tree_join(const TreeParams& p, cudaStream_t stream, bool use_pdl) {
+  const int64_t rows = static_cast<int64_t>(p.total_q) * p.num_q_heads;
+  // rows per warp: few while there are not two rows a warp slot of the device
+  int per = 1;
+  while (per < 32 && rows / per > 152 * 64) per *= 2;
+  const int64_t warps = (rows + per - 1) / per;
+  return fail_at(launch_kernel(tree_join_kernel, dim3(static_cast<unsigned>((warps + kJoinWarps - 1) / kJoinWarps)),
+                               dim3(kJoinWarps * 32), 0, stream, use_pdl, p, per),
+                 "cudaLaunchKernelEx (join)");
+}
+
 cudaError_t launch_tree(const TreeParams& p, bool int8, int group, int page_size,
                         cudaStream_t stream, bool use_pdl) {
   if (!int8) return launch_tree_mma_bf16(p, group, page_size, stream, use_pdl);
-  const dim3 grid(static_cast<unsigned>(p.num_splits * p.max_q_len),
+  const dim3 grid(static_cast<unsigned>(p.max_q_len),
                   static_cast<unsigned>(p.num_q_heads), static_cast<unsigned>(p.bs));
   return fail_at(launch_kernel(int8 ? tree_kernel<true> : tree_kernel<false>, grid, dim3(kWarps * 32),
                                0, stream, use_pdl, p, page_size),

@@ -7,21 +7,24 @@
 // than 2^8, so the accumulator is rescaled a few times per split, not per chunk.  Weights
 // enter P V rounded to bf16 (2^-8 of each weight's share); their sum l stays unrounded fp32.
 //
-// Shape of a block.  One CTA per SM takes up to 256 rows (two tiles of 128) of one (request,
-// kv head) over one split, so a K/V chunk of 128 tokens is fetched once for both.  Two
-// streams, each with a score buffer and an accumulator in tensor memory (4 x 128 columns =
-// all 512): with two tiles a stream is a tile; with one, the streams take alternate chunks
+// Shape.  A unit of work is up to 256 rows (two tiles of 128) of one (request, kv head), so a
+// K/V chunk of 128 tokens is fetched once for both tiles.  The batch's units are laid end to
+// end and cut into equal shares of chunks, one persistent block per SM: ragged batches and
+// unit counts that are no multiple of the SMs leave no block idle, and only the units that a
+// cut falls into need partials (the rest write their output directly).
+// Two streams, each with a score buffer and an accumulator in tensor memory (4 x 128 columns
+// = all 512): with two tiles a stream is a tile; with one, the streams take alternate chunks
 // and are joined at the end.  So the tensor cores work on one stream while the other's
 // softmax runs.
 //   warps 0-3, 4-7   softmax of stream 0, 1: a thread owns a row, so maxima and sums need no
 //                    exchange; scores come from and weights go back to tensor memory (P
 //                    takes the place of S, as the A operand of P V)
-//   warp 8           TMA: a ring of five 32 KiB tiles, K and V in turn; a lane issues one
-//                    box (up to 64 tokens of one page, 64 channels), so small pages cost no
-//                    more time than large ones
-//   warp 9           one thread issues every MMA: P V of chunk c, then Q K^T of the stream's
-//                    next chunk, whose scores are ready when the other stream's are used up
-//   warps 10, 11     zero the V rows past the request's last token (0 * NaN is NaN)
+//   warp 8           TMA: a ring of five 32 KiB tiles, K and V in turn, running ahead into the
+//                    next unit; a lane issues one box (up to 64 tokens of one page, 64
+//                    channels), so small pages cost no more time than large ones
+//   warp 9           issues every MMA: P V of chunk c, then Q K^T of the stream's next chunk,
+//                    whose scores are ready when the other stream's are used up
+//   warp 10          zeroes V rows past a request's last token (0 * NaN is NaN)
 // Masks cost nothing before the last chunks: only chunks that reach the drafted positions
 // look at the ancestor bits.
 //
@@ -37,30 +40,14 @@ namespace tree {
 
 constexpr int kTile = 128;            // rows of a tile, tokens of a chunk
 constexpr int kSoftmaxThreads = 256;  // two groups of four warps
-constexpr int kTmaWarp = 8, kMmaWarp = 9, kFixWarp = 10;
+constexpr int kTmaWarp = 8, kMmaWarp = 9, kCleanWarp = 10;
 constexpr int kThreads = 384;
-// registers per thread after the split: 256 x 224 + 128 x 56 = 384 x 168 at launch
-constexpr int kSoftmaxRegs = 224, kOtherRegs = 56;
+// registers per thread after the split: 256 x 216 + 128 x 72 = 384 x 168 at launch
+constexpr int kSoftmaxRegs = 216, kOtherRegs = 72;
 static_assert(256 * kSoftmaxRegs + 128 * kOtherRegs <= kThreads * 168, "register split");
 constexpr int kSlots = 5;             // ring tiles
 constexpr int kHalfBytes = kTile * 128;       // 64 channels of 128 rows
 constexpr int kTileBytes = 2 * kHalfBytes;
-constexpr int kMergeStride = 132;     // floats; the pad spreads a column over the banks
-
-struct Shared {
-  static constexpr int kQ = 0;
-  static constexpr int kRing = 2 * kTileBytes;
-  static constexpr int kEnd = kRing + kSlots * kTileBytes;
-  struct Control {
-    uint64_t full[kSlots], empty[kSlots];
-    uint64_t q_full, s_full[2], p_half[2], p_ready[2], o_full[2], v_last, v_fixed, drained;
-    uint32_t tmem;
-    int abort, issued;
-  };
-  static constexpr int kBytes = kEnd + static_cast<int>(sizeof(Control)) + 1024;  // + alignment
-};
-static_assert(Shared::kBytes <= 227 * 1024, "one block's shared memory");
-static_assert(kTile * kMergeStride * 4 + 2 * kTile * 8 <= kSlots * kTileBytes, "join buffer");
 
 // Bits of the 32 positions from p0 that a row sees: every committed one (< base), of the
 // drafted ones those of its mask (bit t: position base + t), none at or past `end`.
@@ -81,11 +68,169 @@ __device__ __forceinline__ uint32_t visible(int p0, int base, int end, const uin
   return left >= 32 ? bits : bits & ((1u << left) - 1u);
 }
 
+// One piece of work: chunks [c0, c1) of one unit.  A unit is up to 256 rows (two tiles) of a
+// (request, kv head); the units of a request follow one another kv head by kv head.
+struct Piece {
+  int b, q_begin, q_len, n;  // the request, its query rows, its cached tokens
+  int kvh, pair;
+  int c0, c1;
+  int slot, pieces;  // which of the unit's pieces this is, and how many it has
+};
+
+// The batch as one line of chunks, unit after unit, cut into equal shares: block i takes
+// [i share, (i + 1) share).  Every warp walks its block's share by itself.  (The host keeps
+// the line's length within 31 bits.)
+struct Walk {
+  int b, q_begin, q_len, n, pairs, chunks;  // the request at hand
+  int base, pos, end, share;                // its start on the line; where the walk is
+
+  // Lengths of request r, checked; `report` records what is wrong with them.
+  __device__ __forceinline__ void load(const TreeParams& prm, int page_size, int r, bool report) {
+    b = r;
+    q_begin = prm.cu_seqlens_q[r];
+    q_len = prm.cu_seqlens_q[r + 1] - q_begin;
+    n = prm.cache_seqlens[r];
+    if (q_begin < 0 || q_len < 0 || q_len > prm.max_q_len || q_begin > prm.total_q - q_len) {
+      if (report) record_error(prm.err, kErrSeqLenOutOfRange);
+      q_len = 0;
+    }
+    const int cap = prm.max_seq_pages * page_size;
+    if (n < 0 || n > cap) {
+      if (report) record_error(prm.err, kErrSeqLenOutOfRange);
+      n = n < 0 ? 0 : cap;
+    }
+    const int G = prm.num_q_heads / prm.num_kv_heads;
+    pairs = (q_len * G + 2 * kTile - 1) / (2 * kTile);
+    chunks = (n + kTile - 1) / kTile;
+  }
+  __device__ __forceinline__ int length(const TreeParams& prm) const {
+    return pairs * prm.num_kv_heads * chunks;
+  }
+
+  // Whole-warp: finds the block's share.  Returns whether some request has queries but
+  // nothing cached (its rows are no work, but have a result).
+  __device__ __forceinline__ bool start(const TreeParams& prm, int page_size, int lane, bool report) {
+    int total = 0, first_sum = 0, first_w = 0;  // the first 32 requests' lengths are kept
+    bool empties = false;
+    for (int r0 = 0; r0 < prm.bs; r0 += 32) {
+      int w = 0;
+      if (r0 + lane < prm.bs) {
+        load(prm, page_size, r0 + lane, report);
+        w = length(prm);
+        empties = empties || (q_len > 0 && n == 0);
+      }
+      int incl = w;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int up = __shfl_up_sync(0xffffffffu, incl, d);
+        if (lane >= d) incl += up;
+      }
+      if (r0 == 0) {
+        first_sum = incl;
+        first_w = w;
+      }
+      total += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    empties = __any_sync(0xffffffffu, empties);
+    const int grid = static_cast<int>(gridDim.x);
+    share = max((total + grid - 1) / grid, prm.min_share);
+    const long long at_ll = static_cast<long long>(blockIdx.x) * share;
+    pos = static_cast<int>(min(at_ll, static_cast<long long>(total)));
+    end = static_cast<int>(min(at_ll + share, static_cast<long long>(total)));
+    const bool whole = prm.num_splits == 1;
+    if (pos >= end) return empties;
+    // the request that holds pos and, where units are not cut, the unit starts at or after
+    // pos and end
+    int at = 0, new_end = end < total ? end : total, found = -1, found_base = 0;
+    bool end_found = !whole || end == total;
+    for (int r0 = 0; r0 < prm.bs && !(found >= 0 && end_found); r0 += 32) {
+      int w = first_w, incl = first_sum;
+      if (r0 > 0) {
+        w = 0;
+        if (r0 + lane < prm.bs) {
+          load(prm, page_size, r0 + lane, false);
+          w = length(prm);
+        }
+        incl = w;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+          const int up = __shfl_up_sync(0xffffffffu, incl, d);
+          if (lane >= d) incl += up;
+        }
+      }
+      const int first = at + incl - w;
+      const uint32_t has = __ballot_sync(0xffffffffu, first <= pos && pos < first + w);
+      if (has != 0) {
+        found = r0 + __ffs(has) - 1;
+        found_base = __shfl_sync(0xffffffffu, first, __ffs(has) - 1);
+      }
+      const uint32_t last = __ballot_sync(0xffffffffu, first <= end && end < first + w);
+      if (whole && last != 0) {
+        load(prm, page_size, r0 + __ffs(last) - 1, false);
+        const int f = __shfl_sync(0xffffffffu, first, __ffs(last) - 1);
+        new_end = f + (end - f + chunks - 1) / chunks * chunks;
+        end_found = true;
+      }
+      at += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    load(prm, page_size, found, false);  // (found >= 0: pos lies on the line)
+    base = found_base;
+    if (whole) {
+      pos = base + (pos - base + chunks - 1) / chunks * chunks;
+      end = new_end;
+    }
+    return empties;
+  }
+
+  __device__ __forceinline__ bool next(const TreeParams& prm, int page_size, Piece& p) {
+    if (pos >= end) return false;
+    while (pos - base >= length(prm)) {  // into the next request that has work
+      base += length(prm);
+      load(prm, page_size, b + 1, false);
+    }
+    const int unit = (pos - base) / chunks, from = base + unit * chunks;
+    p.b = b;
+    p.q_begin = q_begin;
+    p.q_len = q_len;
+    p.n = n;
+    p.kvh = unit / pairs;
+    p.pair = unit - p.kvh * pairs;
+    p.c0 = pos - from;
+    p.c1 = min(chunks, end - from);
+    p.slot = 0;
+    p.pieces = 1;
+    if (prm.num_splits > 1) {
+      const int first = from / share;
+      p.slot = static_cast<int>(blockIdx.x) - first;
+      p.pieces = (from + chunks - 1) / share - first + 1;
+    }
+    pos = from + p.c1;
+    return true;
+  }
+};
+
+struct Shared {
+  static constexpr int kQ = 0;
+  static constexpr int kRing = 2 * kTileBytes;
+  static constexpr int kEnd = kRing + kSlots * kTileBytes;
+  struct Control {
+    uint64_t full[kSlots], empty[kSlots];
+    uint64_t q_full, q_empty, s_full[2], p_half[2], p_ready[2], o_full[2], v_last, drained;
+    Walk walk[kSoftmaxThreads / 32];  // of the softmax warps
+    Piece piece[kSoftmaxThreads / 32];
+    float join[2][kTile];  // one number a row, from stream to stream
+    uint32_t tmem;
+    int abort, issued, issued_v, issued_q;
+  };
+  static constexpr int kBytes = kEnd + static_cast<int>(sizeof(Control)) + 1024;  // + alignment
+};
+static_assert(Shared::kBytes <= 227 * 1024, "one block's shared memory");
+
 template <int P>
 __global__ void __launch_bounds__(kThreads, 1)
     tree_mma_kernel(const __grid_constant__ CUtensorMap map_q,
                     const __grid_constant__ CUtensorMap map_k,
-                    const __grid_constant__ CUtensorMap map_v, const TreeParams prm, int pairs) {
+                    const __grid_constant__ CUtensorMap map_v, const TreeParams prm) {
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -93,10 +238,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   Shared::Control& ctl = *reinterpret_cast<Shared::Control*>(smem + Shared::kEnd);
   volatile int* abort_flag = &ctl.abort;
 
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // (uniform for the compiler too)
   const int G = prm.num_q_heads / prm.num_kv_heads;
-  const int split = blockIdx.x, b = blockIdx.z;
-  const int kvh = blockIdx.y / pairs, pair = blockIdx.y - kvh * pairs;
+  const int S = prm.num_splits;
 
   if (tid == 0) {
     for (int i = 0; i < kSlots; ++i) {
@@ -104,6 +249,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&ctl.empty[i], 1);
     }
     mbar_init(&ctl.q_full, 1);
+    mbar_init(&ctl.q_empty, 1);
     for (int s = 0; s < 2; ++s) {
       mbar_init(&ctl.s_full[s], 1);
       mbar_init(&ctl.p_half[s], 4);
@@ -111,61 +257,34 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&ctl.o_full[s], 1);
     }
     mbar_init(&ctl.v_last, 1);
-    mbar_init(&ctl.v_fixed, 2);
     mbar_init(&ctl.drained, 1);
     ctl.abort = 0;
     ctl.issued = 0;
+    ctl.issued_v = 0;
+    ctl.issued_q = 0;
     fence_barrier_init();
   }
+  if (warp == kMmaWarp) umma::alloc_all(&ctl.tmem);
   grid_dependency_wait();
 
-  // ---- the block's rows and tokens (every thread computes them alike) --------------------
-  const int q_begin = prm.cu_seqlens_q[b];
-  int q_len = prm.cu_seqlens_q[b + 1] - q_begin;
-  if (q_begin < 0 || q_len < 0 || q_len > prm.max_q_len || q_begin > prm.total_q - q_len) {
-    if (tid == 0 && blockIdx.x == 0 && blockIdx.y == 0) record_error(prm.err, kErrSeqLenOutOfRange);
-    q_len = 0;
-  }
-  const int cap = prm.max_seq_pages * P;
-  int n = prm.cache_seqlens[b];
-  if (n < 0 || n > cap) {
-    if (tid == 0 && blockIdx.x == 0 && blockIdx.y == 0) record_error(prm.err, kErrSeqLenOutOfRange);
-    n = n < 0 ? 0 : cap;
-  }
-  const int rows = min(q_len * G - pair * 2 * kTile, 2 * kTile);  // of this block
-  if (rows <= 0) return;
-  const bool two = rows > kTile;  // two tiles: a stream each
-  const int base = n - q_len;
-  const int begin = split * prm.pages_per_split * P;
-  const int end = min(n, begin + prm.pages_per_split * P);
-  const int n_tok = end - begin;
-  const int S = prm.num_splits;
-  // output slot of row r of tile t (the row's query and head)
-  auto slot_of = [&](int t, int r) -> int64_t {
-    const int row = (pair * 2 + t) * kTile + r;
-    const int qi = row / G;
-    return (static_cast<int64_t>(q_begin) + qi) * prm.num_q_heads + kvh * G + (row - qi * G);
-  };
-
-  if (n_tok <= 0) {  // nothing to attend to in this split
-    trigger_dependents();
-    for (int r = tid; r < rows; r += kThreads) {
-      const int64_t slot = slot_of(0, r);
-      if (S > 1) {
-        prm.m_out[slot * S + split] = -CUDART_INF_F;
-        prm.l_out[slot * S + split] = 0.f;
-      } else if (prm.lse != nullptr) {
-        prm.lse[slot] = -CUDART_INF_F;
+  Walk walk;
+  const bool empties = walk.start(prm, P, lane, blockIdx.x == 0 && warp == 0);
+  if (empties) {  // requests with queries and an empty cache
+    Walk w;
+    for (int r = blockIdx.x; r < prm.bs; r += gridDim.x) {
+      w.load(prm, P, r, false);
+      if (w.n > 0) continue;
+      const int64_t first = static_cast<int64_t>(w.q_begin) * prm.num_q_heads;
+      for (int i = tid; i < w.q_len * prm.num_q_heads; i += kThreads) {
+        if (prm.lse != nullptr) prm.lse[first + i] = -CUDART_INF_F;
+        if (S > 1) prm.l_out[(first + i) * S] = -1.f;
       }
+      for (int i = tid; i < w.q_len * prm.num_q_heads * 16; i += kThreads)
+        static_cast<uint4*>(prm.out)[first * 16 + i] = make_uint4(0u, 0u, 0u, 0u);
     }
-    if (S == 1) {
-      for (int i = tid; i < rows * 16; i += kThreads)
-        static_cast<uint4*>(prm.out)[slot_of(0, i >> 4) * 16 + (i & 15)] = make_uint4(0u, 0u, 0u, 0u);
-    }
-    return;
   }
 
-  if (warp == kMmaWarp) umma::alloc_all(&ctl.tmem);
+  if (warp < kTmaWarp && lane == 0) ctl.walk[warp] = walk;
   umma::fence_before();
   __syncthreads();  // barriers initialised, tensor memory allocated
   umma::fence_after();
@@ -173,173 +292,198 @@ __global__ void __launch_bounds__(kThreads, 1)
   // columns: scores (and weights) of stream s at 128 s, accumulator at 256 + 128 s
   auto s_col = [&](int s) { return tmem + static_cast<uint32_t>(s) * kTile; };
   auto o_col = [&](int s) { return tmem + 256u + static_cast<uint32_t>(s) * kTile; };
-
-  const int chunks = (n_tok + kTile - 1) / kTile;
-  const int last_valid = n_tok - (chunks - 1) * kTile;  // tokens of the last chunk
-  // a partial last chunk: its V tile completes v_last, is cleaned, and is handed on by v_fixed
-  const bool clean_last = last_valid < kTile;
-  // chunks of stream s: all of them (two tiles), or every second one from s
-  auto stream_chunks = [&](int s) { return two ? chunks : (chunks + 1 - s) / 2; };
   auto give_up = [&]() {
     record_error(prm.err, kErrWaitTimeout);
     *abort_flag = 1;
   };
+  // two tiles: each is a stream over every chunk; one: the streams take alternate chunks
+  auto two_tiles = [&](const Piece& p) { return p.q_len * G - p.pair * 2 * kTile > kTile; };
+  auto stream_chunks = [](bool two, int chunks, int s) { return two ? chunks : (chunks + 1 - s) / 2; };
 
   if (warp < kTmaWarp) {
     // ======================= softmax ===================================================
     umma::registers_up<kSoftmaxRegs>();
     const int s = warp >> 2, r = tid & (kTile - 1);
-    const int tile = two ? s : 0;
     const uint32_t lane_base = static_cast<uint32_t>(warp & 3) << 21;  // lane 32 (warp % 4)
     const uint32_t sc = s_col(s) + lane_base, oc = o_col(s) + lane_base;
-    const int row = (pair * 2 + tile) * kTile + r;
-    const bool live = row < q_len * G;
-    const uint32_t* mask = prm.tree_mask + (static_cast<int64_t>(q_begin) + (live ? row / G : 0)) *
-                                               (2 * prm.mask_words);
-    const int words = 2 * prm.mask_words;
     const float scale = prm.q_scale;
-    const int mine = stream_chunks(s);
-    float m_ref = -CUDART_INF_F, l = 0.f;  // the row's reference and sum of weights
-    for (int k = 0; k < mine; ++k) {
-      const int c = two ? k : 2 * k + s;
-      const int p0 = begin + c * kTile;
-      if (!mbar_wait_bounded(&ctl.s_full[s], static_cast<uint32_t>(k) & 1u)) {
-        if (lane == 0) give_up();
-        break;
+    const int words = 2 * prm.mask_words;
+    uint32_t step = 0, outputs = 0;  // of this stream, over all pieces
+    // (after a wait that gave up, the pieces that are left only meet the barriers of the
+    // softmax warps, so that none of them waits there for good)
+    bool ok = true;
+    // A thread's registers hold a row of scores, so the walk and the piece stay in shared
+    // memory: `volatile` has them read again where they are needed.
+    const volatile Piece& vp = ctl.piece[warp];
+    while (true) {
+      __syncwarp();
+      if (lane == 0) {
+        Walk w = ctl.walk[warp];
+        Piece next;
+        next.c1 = 0;
+        w.next(prm, P, next);
+        ctl.walk[warp] = w;
+        ctl.piece[warp] = next;
       }
-      umma::fence_after();
-      const bool tail = p0 + kTile > min(base, end);  // drafted or missing positions
-      float x[kTile];
+      __syncwarp();
+      if (vp.c1 == 0) break;
+      const bool two = vp.q_len * G - vp.pair * 2 * kTile > kTile;
+      // this stream's chunks: c0 + k (two tiles) or c0 + 2 k + s; from `plain` on they reach the
+      // drafted positions
+      const int mine = stream_chunks(two, vp.c1 - vp.c0, s);
+      const int committed = max(0, vp.n - vp.q_len) / kTile - vp.c0;  // chunks of those alone
+      const int plain = two ? committed : (committed - s + 1) >> 1;
+      float m_ref = -CUDART_INF_F, l = 0.f;  // the row's reference and sum of weights
+      for (int k = 0; k < mine && ok; ++k) {
+        ok = mbar_wait_bounded(&ctl.s_full[s], step & 1u);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        ++step;
+        umma::fence_after();
+        float x[kTile];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        uint32_t(&v)[32] = *reinterpret_cast<uint32_t(*)[32]>(&x[32 * i]);
-        umma::ld32(sc + 32 * i, v);
-      }
+        for (int i = 0; i < 4; ++i)
+          umma::ld32(sc + 32 * i, *reinterpret_cast<uint32_t(*)[32]>(&x[32 * i]));
 #pragma unroll
-      for (int i = 0; i < 4; ++i) umma::wait_ld(*reinterpret_cast<uint32_t(*)[32]>(&x[32 * i]));
-      if (tail) {
+        for (int i = 0; i < 4; ++i) umma::wait_ld(*reinterpret_cast<uint32_t(*)[32]>(&x[32 * i]));
+        if (k >= plain) {  // drafted or missing positions
+          const int row = (vp.pair * 2 + (two ? s : 0)) * kTile + r;
+          const int q_len = vp.q_len, n = vp.n;
+          const bool live = row < q_len * G;
+          const uint32_t* mask =
+              prm.tree_mask + (static_cast<int64_t>(vp.q_begin) + (live ? row / G : 0)) * words;
+          const int p0 = (vp.c0 + (two ? k : 2 * k + s)) * kTile;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint32_t bits = live ? visible(p0 + 32 * i, base, end, mask, words) : 0u;
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t bits = live ? visible(p0 + 32 * i, n - q_len, n, mask, words) : 0u;
 #pragma unroll
-          for (int j = 0; j < 32; ++j)
-            x[32 * i + j] = (bits >> j) & 1u ? x[32 * i + j] : -CUDART_INF_F;
+            for (int j = 0; j < 32; ++j)
+              x[32 * i + j] = (bits >> j) & 1u ? x[32 * i + j] : -CUDART_INF_F;
+          }
+          __syncwarp();
+        }
+        float mx[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+        for (int j = 4; j < kTile - 4; j += 8)
+#pragma unroll
+          for (int u = 0; u < 4; ++u) mx[u] = umma::max3(mx[u], x[j + u], x[j + 4 + u]);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) mx[u] = fmaxf(mx[u], x[kTile - 4 + u]);
+        // (sm_scale > 0: the largest score is the largest product)
+        const float m_new = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale;
+        float alpha = 1.f;
+        if (m_new > m_ref + mma::kMaxSlack) {
+          alpha = m_ref == -CUDART_INF_F ? 0.f : mma::fast_exp2(m_ref - m_new);
+          m_ref = m_new;
+          l *= alpha;
         }
         __syncwarp();
-      }
-      float mx[4] = {x[0], x[1], x[2], x[3]};
+        // the accumulator follows a moved reference (before the first product there is none;
+        // earlier products are over once the scores are)
+        if (k > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
 #pragma unroll
-      for (int j = 4; j < kTile - 4; j += 8)
+          for (int i = 0; i < 4; ++i) {
+            uint32_t o[32];
+            umma::ld32(oc + 32 * i, o);
+            umma::wait_ld(o);
 #pragma unroll
-        for (int u = 0; u < 4; ++u) mx[u] = umma::max3(mx[u], x[j + u], x[j + 4 + u]);
-#pragma unroll
-      for (int u = 0; u < 4; ++u) mx[u] = fmaxf(mx[u], x[kTile - 4 + u]);
-      // (sm_scale > 0: the largest score is the largest product)
-      const float m_new = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale;
-      float alpha = 1.f;
-      if (m_new > m_ref + mma::kMaxSlack) {
-        alpha = m_ref == -CUDART_INF_F ? 0.f : mma::fast_exp2(m_ref - m_new);
-        m_ref = m_new;
-        l *= alpha;
-      }
-      __syncwarp();
-      // the accumulator follows a moved reference (before the first product there is none)
-      if (k > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+            for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * alpha);
+            umma::st32(oc + 32 * i, o);
+          }
+        }
+        const float ref = m_ref == -CUDART_INF_F ? 0.f : m_ref;
+        const uint64_t scale2 = umma::pair(scale, scale), ref2 = umma::pair(-ref, -ref);
+        uint64_t sum[4] = {0, 0, 0, 0};  // pairs of +0
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          uint32_t o[32];
-          umma::ld32(oc + 32 * i, o);
-          umma::wait_ld(o);
+          uint32_t w[16];
 #pragma unroll
-          for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * alpha);
-          umma::st32(oc + 32 * i, o);
+          for (int j = 0; j < 16; ++j) {
+            float lo, hi;
+            umma::unpair(umma::fma2(umma::pair(x[32 * i + 2 * j], x[32 * i + 2 * j + 1]), scale2, ref2),
+                         lo, hi);
+            lo = mma::fast_exp2(lo);
+            hi = mma::fast_exp2(hi);
+            sum[j & 3] = umma::add2(sum[j & 3], umma::pair(lo, hi));
+            w[j] = mma::pack_bf16(lo, hi);
+          }
+          umma::st16(sc + 16 * i, w);
+          if (i & 1) {  // half of the weights: their products may start
+            umma::wait_st();
+            umma::fence_before();
+            __syncwarp();
+            if (lane == 0) mma::mbar_arrive(i == 1 ? &ctl.p_half[s] : &ctl.p_ready[s]);
+          }
         }
+        float lo, hi;
+        umma::unpair(umma::add2(umma::add2(sum[0], sum[1]), umma::add2(sum[2], sum[3])), lo, hi);
+        l += lo + hi;
       }
-      const float ref = m_ref == -CUDART_INF_F ? 0.f : m_ref;
-      const uint64_t scale2 = umma::pair(scale, scale), ref2 = umma::pair(-ref, -ref);
-      uint64_t sum[4] = {0, 0, 0, 0};  // pairs of +0
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        uint32_t w[16];
-#pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          float lo, hi;
-          umma::unpair(umma::fma2(umma::pair(x[32 * i + 2 * j], x[32 * i + 2 * j + 1]), scale2, ref2),
-                       lo, hi);
-          lo = mma::fast_exp2(lo);
-          hi = mma::fast_exp2(hi);
-          sum[j & 3] = umma::add2(sum[j & 3], umma::pair(lo, hi));
-          w[j] = mma::pack_bf16(lo, hi);
-        }
-        umma::st16(sc + 16 * i, w);
-        if (i == 1) {  // half of the weights: their products may start
-          umma::wait_st();
-          umma::fence_before();
-          __syncwarp();
-          if (lane == 0) mma::mbar_arrive(&ctl.p_half[s]);
-        }
-      }
-      float lo, hi;
-      umma::unpair(umma::add2(umma::add2(sum[0], sum[1]), umma::add2(sum[2], sum[3])), lo, hi);
-      l += lo + hi;
-      umma::wait_st();
-      umma::fence_before();
-      __syncwarp();
-      if (lane == 0) mma::mbar_arrive(&ctl.p_ready[s]);
-    }
 
-    // ----- the rows' results -----------------------------------------------------------
-    const bool has = mine > 0;
-    if (has && !*abort_flag && !mbar_wait_bounded(&ctl.o_full[s], 0) && lane == 0) give_up();
-    umma::fence_after();
-    trigger_dependents();
-    float factor = 1.f;  // of this stream's accumulator
-    float* joined = reinterpret_cast<float*>(smem + Shared::kRing);
-    float2* ml = reinterpret_cast<float2*>(joined + kTile * kMergeStride);
-    // (both streams' products are over before either writes into the ring)
-    asm volatile("bar.sync 1, 256;" ::: "memory");
-    if (!two) {  // one tile: join the streams, stream 1 hands its rows over
-      ml[s * kTile + r] = make_float2(m_ref, l);
-      asm volatile("bar.sync 1, 256;" ::: "memory");
-      const float2 other = ml[(1 - s) * kTile + r];
-      const float m_all = fmaxf(m_ref, other.x);
-      if (m_all != -CUDART_INF_F) {
-        factor = m_ref == -CUDART_INF_F ? 0.f : mma::fast_exp2(m_ref - m_all);
-        l = l * factor + (other.x == -CUDART_INF_F ? 0.f : other.y * mma::fast_exp2(other.x - m_all));
+      // ----- the rows' results -------------------------------------------------------------
+      if (ok && mine > 0) {
+        ok = mbar_wait_bounded(&ctl.o_full[s], outputs & 1u);
+        ok = __all_sync(0xffffffffu, ok);
+        ++outputs;
+      }
+      if (!ok && lane == 0) give_up();
+      umma::fence_after();
+      const Piece p = {vp.b, vp.q_begin, vp.q_len, vp.n, vp.kvh, vp.pair, vp.c0, vp.c1, vp.slot, vp.pieces};
+      const int row = (p.pair * 2 + (two ? s : 0)) * kTile + r;
+      const bool live = row < p.q_len * G;
+      const int qi = live ? row / G : 0;
+      const int64_t slot = (static_cast<int64_t>(p.q_begin) + qi) * prm.num_q_heads + p.kvh * G +
+                           (live ? row - qi * G : 0);
+      float f_own = 1.f, f_other = 0.f;  // factors of this and the other stream's accumulator
+      int col0 = 0, col1 = kTile;        // channels this thread writes
+      if (!two && p.c1 - p.c0 > 1) {
+        // one tile: join the streams (both see each other's accumulator: the same lanes);
+        // each writes half of the channels
+        float* box = ctl.join[s];
+        box[r] = m_ref;
+        umma::fence_before();
+        asm volatile("bar.sync 1, 256;" ::: "memory");
+        umma::fence_after();
+        const float m_other = ctl.join[1 - s][r];
+        asm volatile("bar.sync 1, 256;" ::: "memory");
+        box[r] = l;
+        asm volatile("bar.sync 1, 256;" ::: "memory");
+        const float m_all = fmaxf(m_ref, m_other);
+        f_own = m_ref == -CUDART_INF_F ? 0.f : mma::fast_exp2(m_ref - m_all);
+        f_other = m_other == -CUDART_INF_F ? 0.f : mma::fast_exp2(m_other - m_all);
+        l = l * f_own + ctl.join[1 - s][r] * f_other;
         m_ref = m_all;
+        col0 = s * (kTile / 2);
+        col1 = col0 + kTile / 2;
+      } else if (!two && s == 1) {
+        col1 = 0;  // a single chunk: stream 0 has it all
       }
-      if (s == 1 && has) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          uint32_t o[32];
-          umma::ld32(oc + 32 * i, o);
-          umma::wait_ld(o);
-#pragma unroll
-          for (int j = 0; j < 32; ++j)
-            joined[r * kMergeStride + 32 * i + j] = __uint_as_float(o[j]) * factor;
-        }
-      }
-      asm volatile("bar.sync 1, 256;" ::: "memory");
-    }
-    const bool add = !two && stream_chunks(1) > 0;
-    const bool write = live && !*abort_flag;
-    if (two || s == 0) {
-      const int64_t slot = write ? slot_of(tile, r) : 0;
-      const float inv = S == 1 ? (l > 0.f || l != l ? 1.f / l : 0.f) : 1.f;
-      factor *= inv;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        uint32_t o[32];
-        umma::ld32(oc + 32 * i, o);
-        umma::wait_ld(o);
+      const bool direct = p.pieces == 1;
+      const float inv = direct ? (l > 0.f || l != l ? 1.f / l : 0.f) : 1.f;
+      const uint32_t other = o_col(1 - s) + lane_base;
+      const bool write = live && ok;
+      for (int c = col0; c < col1; c += 32) {
         float y[32];
+        uint32_t o[32];
+        __syncwarp();
+        umma::ld32(oc + c, o);
+        umma::wait_ld(o);
 #pragma unroll
-        for (int j = 0; j < 32; ++j) {
-          y[j] = __uint_as_float(o[j]) * factor;
-          if (add) y[j] += joined[r * kMergeStride + 32 * i + j] * inv;
+        for (int j = 0; j < 32; ++j) y[j] = __uint_as_float(o[j]) * f_own;
+        if (!two) {
+          umma::ld32(other + c, o);
+          umma::wait_ld(o);
+          // (without a second chunk the other accumulator holds nothing of this piece)
+          if (f_other != 0.f) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) y[j] = fmaf(__uint_as_float(o[j]), f_other, y[j]);
+          }
+          __syncwarp();
         }
-        if (write && S == 1) {
-          uint4* out = static_cast<uint4*>(prm.out) + slot * 16 + 4 * i;
+#pragma unroll
+        for (int j = 0; j < 32; ++j) y[j] *= inv;
+        if (write && direct) {
+          uint4* out = static_cast<uint4*>(prm.out) + slot * 16 + c / 8;
 #pragma unroll
           for (int j = 0; j < 4; ++j)
             out[j] = make_uint4(mma::pack_bf16(y[8 * j], y[8 * j + 1]),
@@ -347,193 +491,221 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 mma::pack_bf16(y[8 * j + 4], y[8 * j + 5]),
                                 mma::pack_bf16(y[8 * j + 6], y[8 * j + 7]));
         } else if (write) {
-          float4* acc = reinterpret_cast<float4*>(prm.acc_out) + (slot * S + split) * 32 + 8 * i;
+          float4* acc = reinterpret_cast<float4*>(prm.acc_out) + (slot * S + p.slot) * 32 + c / 4;
 #pragma unroll
           for (int j = 0; j < 8; ++j)
             acc[j] = make_float4(y[4 * j], y[4 * j + 1], y[4 * j + 2], y[4 * j + 3]);
         }
-        __syncwarp();
       }
-      if (write) {
+      if (write && (two || s == 0)) {
         const float m_nat = m_ref * 0.69314718055994530942f;  // -inf stays -inf
-        if (S > 1) {
-          prm.m_out[slot * S + split] = m_nat;
-          prm.l_out[slot * S + split] = l;
-        } else if (prm.lse != nullptr) {
-          prm.lse[slot] = m_ref == -CUDART_INF_F ? m_ref : m_nat + logf(l);
+        if (direct) {
+          if (prm.lse != nullptr) prm.lse[slot] = m_ref == -CUDART_INF_F ? m_ref : m_nat + logf(l);
+          if (S > 1) prm.l_out[slot * S] = -1.f;  // nothing to combine
+        } else {
+          prm.m_out[slot * S + p.slot] = m_nat;
+          prm.l_out[slot * S + p.slot] = l;
+          // the sum after the last piece's ends the row's list
+          if (p.slot == 0 && p.pieces < S) prm.l_out[slot * S + p.pieces] = -1.f;
         }
       }
+      umma::fence_before();
+      // neither stream's next product may overwrite an accumulator that the other reads, nor
+      // the next join this one's numbers
+      if (!two) asm volatile("bar.sync 1, 256;" ::: "memory");
     }
-    umma::fence_before();
   } else {
     umma::registers_down<kOtherRegs>();
+    Piece p;
     if (warp == kTmaWarp) {
-    // ======================= TMA ========================================================
-    constexpr int kBoxRows = P < 64 ? P : 64;
-    constexpr int kBoxes = kTile / kBoxRows;
-    const uint64_t policy = l2_evict_first_policy();
-    if (lane == 0) {
-      const int tiles = two ? 2 : 1;
-      mbar_arrive_expect_tx(&ctl.q_full, tiles * kTileBytes);
-      for (int t = 0; t < tiles; ++t)
-        for (int h = 0; h < 2; ++h)
-          asm volatile(
-              "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-              " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(base_addr + Shared::kQ + t * kTileBytes +
-                                                     h * kHalfBytes),
-              "l"(reinterpret_cast<uint64_t>(&map_q)), "r"(64 * h), "r"(kvh * G),
-              "r"(q_begin + (pair * 2 + t) * (kTile / G)), "r"(smem_addr(&ctl.q_full))
-              : "memory");
-    }
-    // lane -> (box of the chunk, channel half)
-    const int box = lane >> 1, half = lane & 1;
-    const int32_t* pt = prm.page_table + static_cast<int64_t>(b) * prm.page_table_stride;
-    auto page_of = [&](int c) -> int {  // this lane's page of chunk c, -1: nothing to load
-      const int tok = c * kTile + box * kBoxRows;
-      return box < kBoxes && tok < n_tok ? pt[(begin + tok) / P] : -1;
-    };
-    int next = page_of(0);
-    bool ok = true;
-    for (int c = 0; c < chunks && ok; ++c) {
-      const int tok = c * kTile + box * kBoxRows;
-      const bool mine = box < kBoxes && tok < n_tok;
-      int pg = next;
-      if (c + 1 < chunks) next = page_of(c + 1);
-      if (mine && (pg < 0 || pg >= prm.num_pages)) {
-        record_error(prm.err, kErrPageOutOfRange);
-        pg = 0;
+      // ======================= TMA ======================================================
+      constexpr int kBoxRows = P < 64 ? P : 64;
+      constexpr int kBoxes = kTile / kBoxRows;
+      const uint64_t policy = l2_evict_first_policy();
+      // lane -> (box of the chunk, channel half)
+      const int box = lane >> 1, half = lane & 1;
+      int it = 0;  // ring tiles issued
+      uint32_t piece = 0;
+      bool ok = true;
+      while (ok && walk.next(prm, P, p)) {
+        const int32_t* pt = prm.page_table + static_cast<int64_t>(p.b) * prm.page_table_stride;
+        auto token_of = [&](int c) { return c * kTile + box * kBoxRows; };
+        auto page_of = [&](int c) -> int {  // this lane's page of chunk c, -1: nothing to load
+          const int tok = token_of(c);
+          return c < p.c1 && box < kBoxes && tok < p.n ? pt[tok / P] : -1;
+        };
+        int next = page_of(p.c0);
+        for (int c = p.c0; c < p.c1 && ok; ++c) {
+          const int tok = token_of(c);
+          const bool mine = box < kBoxes && tok < p.n;
+          int pg = next;
+          next = page_of(c + 1);
+          if (mine && (pg < 0 || pg >= prm.num_pages)) {
+            record_error(prm.err, kErrPageOutOfRange);
+            pg = 0;
+          }
+          const int boxes = min(kBoxes, (p.n - c * kTile + kBoxRows - 1) / kBoxRows);
+          for (int kv = 0; kv < 2; ++kv, ++it) {
+            const int slot = it % kSlots;
+            ok = it < kSlots ||
+                 mbar_wait_bounded(&ctl.empty[slot], static_cast<uint32_t>(it / kSlots - 1) & 1u);
+            ok = __all_sync(0xffffffffu, ok && !*abort_flag);
+            if (!ok) break;
+            // (a last V tile that the request's end cuts goes to the cleaning warp first, which
+            // then completes the slot's barrier)
+            uint64_t* bar = kv && (c + 1) * kTile > p.n ? &ctl.v_last : &ctl.full[slot];
+            if (lane == 0) {
+              if (bar == &ctl.v_last) {
+                ctl.issued_v += 1;
+              } else {
+                ctl.issued = it + 1;
+              }
+              mbar_arrive_expect_tx(bar, boxes * kBoxRows * 256);
+            }
+            __syncwarp();
+            if (mine)
+              mma::tma_load_4d(base_addr + Shared::kRing + slot * kTileBytes + half * kHalfBytes +
+                                   box * kBoxRows * 128,
+                               kv ? &map_v : &map_k, 64 * half, tok % P, p.kvh, pg, bar, policy);
+            __syncwarp();
+          }
+          if (ok && c == p.c0) {  // the rows: once the previous piece's scores are over
+            ok = piece == 0 || mbar_wait_bounded(&ctl.q_empty, (piece - 1) & 1u);
+            ok = __all_sync(0xffffffffu, ok);
+            if (ok && lane == 0) {
+              const int tiles = two_tiles(p) ? 2 : 1;
+              ctl.issued_q = piece + 1;
+              mbar_arrive_expect_tx(&ctl.q_full, tiles * kTileBytes);
+              for (int t = 0; t < tiles; ++t)
+                for (int h = 0; h < 2; ++h)
+                  asm volatile(
+                      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+                      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(base_addr + Shared::kQ +
+                                                             t * kTileBytes + h * kHalfBytes),
+                      "l"(reinterpret_cast<uint64_t>(&map_q)), "r"(64 * h), "r"(p.kvh * G),
+                      "r"(p.q_begin + (p.pair * 2 + t) * (kTile / G)), "r"(smem_addr(&ctl.q_full))
+                      : "memory");
+            }
+            __syncwarp();
+            ++piece;
+          }
+        }
       }
-      const int boxes = min(kBoxes, (n_tok - c * kTile + kBoxRows - 1) / kBoxRows);
-      for (int kv = 0; kv < 2; ++kv) {
-        const int i = 2 * c + kv, slot = i % kSlots;
-        if (i >= kSlots &&
-            (!mbar_wait_bounded(&ctl.empty[slot], static_cast<uint32_t>(i / kSlots - 1) & 1u) ||
-             *abort_flag)) {
-          ok = false;
-        }
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) {
-          if (lane == 0) give_up();
-          break;
-        }
-        uint64_t* bar = kv && c == chunks - 1 && clean_last ? &ctl.v_last : &ctl.full[slot];
-        if (lane == 0) {
-          ctl.issued = i + 1;
-          mbar_arrive_expect_tx(bar, boxes * kBoxRows * 256);
-        }
-        __syncwarp();
-        if (mine)
-          mma::tma_load_4d(base_addr + Shared::kRing + slot * kTileBytes + half * kHalfBytes +
-                               box * kBoxRows * 128,
-                           kv ? &map_v : &map_k, 64 * half, (begin + tok) % P, kvh, pg, bar, policy);
-        __syncwarp();
-      }
-    }
-  } else if (warp == kMmaWarp) {
-    // ======================= MMA issue ==================================================
-    if (lane == 0) {
+      if (!ok && lane == 0) give_up();
+    } else if (warp == kMmaWarp) {
+      // ======================= MMA issue ==================================================
+      if (umma::elect()) {
       constexpr uint32_t kScores = umma::instruction(kTile, kTile, false);
       constexpr uint32_t kOutput = umma::instruction(kTile, kTile, true);
+      int it0 = 0;  // ring tiles of the pieces before
+      uint32_t piece = 0, used0 = 0, used1 = 0;  // products of each stream
+      auto wait = [&](uint64_t* bar, uint32_t parity) { return mbar_wait_bounded(bar, parity & 1u); };
       auto tile_addr = [&](int i) { return base_addr + Shared::kRing + (i % kSlots) * kTileBytes; };
-      auto wait_tile = [&](int i) {
-        return mbar_wait_bounded(&ctl.full[i % kSlots], static_cast<uint32_t>(i / kSlots) & 1u);
-      };
-      auto scores = [&](int s, int c) {  // S_s = Q_tile K_c^T
-        const uint32_t q = base_addr + Shared::kQ + (two ? s : 0) * kTileBytes;
-        const uint32_t k = tile_addr(2 * c);
+      auto wait_tile = [&](int i) { return wait(&ctl.full[i % kSlots], static_cast<uint32_t>(i / kSlots)); };
+      bool ok = true;
+      while (ok && walk.next(prm, P, p)) {
+        const bool two = two_tiles(p);
+        const int chunks = p.c1 - p.c0;
+        auto scores = [&](int s, int c) {  // S_s = Q_tile K_c^T; the tile and Q are done with
+          const uint32_t q = umma::operand(base_addr + Shared::kQ + (two ? s : 0) * kTileBytes, 16);
+          const uint32_t k = umma::operand(tile_addr(it0 + 2 * c), 16);
+          const uint32_t d = s_col(s);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const uint32_t off = (j >> 2) * kHalfBytes + (j & 3) * 32;
-          umma::mma_ss(s_col(s), umma::operand(q + off, 16), umma::operand(k + off, 16), kScores, j > 0);
-        }
-        umma::commit(&ctl.s_full[s]);
-      };
-      bool ok = mbar_wait_bounded(&ctl.q_full, 0);
-      // the first scores of both streams
-      for (int s = 0; s < 2 && ok; ++s) {
-        if (stream_chunks(s) == 0) break;
-        const int c = two ? 0 : s;
-        if (s == 0 || !two) ok = wait_tile(2 * c);
-        if (!ok) break;
-        umma::fence_after();
-        scores(s, c);
-        if (s == 1 || !two) umma::commit(&ctl.empty[(2 * c) % kSlots]);
-      }
-      uint32_t used[2] = {0, 0};  // chunks of each stream whose P V has been issued
-      for (int c = 0; c < chunks && ok; ++c) {
-        const int s_begin = two ? 0 : c & 1, s_end = two ? 2 : s_begin + 1;
-        for (int s = s_begin; s < s_end && ok; ++s) {
-          ok = mbar_wait_bounded(&ctl.p_half[s], used[s] & 1u);
-          if (ok && s == s_begin) {
-            ok = c == chunks - 1 && clean_last ? mbar_wait_bounded(&ctl.v_fixed, 0)
-                                               : wait_tile(2 * c + 1);
+          for (int j = 0; j < 8; ++j) {
+            const uint32_t off = ((j >> 2) * kHalfBytes + (j & 3) * 32) >> 4;
+            umma::mma_ss(d, q + off, k + off, kScores, j > 0);
           }
-          if (!ok) break;
-          umma::fence_after();
-          const uint32_t v = tile_addr(2 * c + 1);
-          // 16 tokens a step: 8 columns of P, 16 rows of V
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            umma::mma_ts(o_col(s), s_col(s) + 8 * j, umma::operand(v + j * 16 * 128, kHalfBytes),
-                         kOutput, used[s] > 0 || j > 0);
-          ok = mbar_wait_bounded(&ctl.p_ready[s], used[s] & 1u);
-          if (!ok) break;
-          umma::fence_after();
-#pragma unroll
-          for (int j = 4; j < 8; ++j)
-            umma::mma_ts(o_col(s), s_col(s) + 8 * j, umma::operand(v + j * 16 * 128, kHalfBytes),
-                         kOutput, true);
-          ++used[s];
-          if (s == s_end - 1) umma::commit(&ctl.empty[(2 * c + 1) % kSlots]);
+          umma::commit(&ctl.s_full[s]);
+          if (!two || s == 1) {
+            umma::commit(&ctl.empty[(it0 + 2 * c) % kSlots]);
+            if (c == chunks - 1) umma::commit(&ctl.q_empty);
+          }
+        };
+        ok = wait(&ctl.q_full, piece);
+        ++piece;
+        // the first scores of both streams
+        for (int s = 0; s < 2 && ok; ++s) {
+          const int c = two ? 0 : s;
+          if (c >= chunks) break;
+          if (s == 0 || !two) ok = wait_tile(it0 + 2 * c);
+          if (ok) scores(s, c);
+        }
+        for (int c = 0; c < chunks && ok; ++c) {
+          const int s_begin = two ? 0 : c & 1, s_end = two ? 2 : s_begin + 1;
+          const uint32_t v = umma::operand(tile_addr(it0 + 2 * c + 1), kHalfBytes);
+          const bool first = two ? c == 0 : c < 2;  // of the piece in this stream
           const int next = two ? c + 1 : c + 2;
-          if (next < chunks) {
-            if (s == s_begin) ok = wait_tile(2 * next);
+          for (int s = s_begin; s < s_end && ok; ++s) {
+            const uint32_t use = s == 0 ? used0++ : used1++;
+            ok = wait(&ctl.p_half[s], use);
+            if (ok && s == s_begin) ok = wait_tile(it0 + 2 * c + 1);
+            if (!ok) break;
+            const uint32_t d = o_col(s), a = s_col(s);
+            // 16 tokens a step: 8 columns of P, 16 rows (2 KiB) of V
+            umma::fence_after();
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              umma::mma_ts(d, a + 8 * j, v + j * (2048 >> 4), kOutput, !first || j > 0);
+            ok = wait(&ctl.p_ready[s], use);
             if (!ok) break;
             umma::fence_after();
-            scores(s, next);
-            if (s == s_end - 1) umma::commit(&ctl.empty[(2 * next) % kSlots]);
-          } else {
-            umma::commit(&ctl.o_full[s]);
+#pragma unroll
+            for (int j = 4; j < 8; ++j)
+              umma::mma_ts(d, a + 8 * j, v + j * (2048 >> 4), kOutput, true);
+            if (s == s_end - 1) umma::commit(&ctl.empty[(it0 + 2 * c + 1) % kSlots]);
+            if (next >= chunks) umma::commit(&ctl.o_full[s]);
+            if (next < chunks) {
+              if (s == s_begin) ok = wait_tile(it0 + 2 * next);
+              if (ok) scores(s, next);
+            }
           }
         }
+        it0 += 2 * chunks;
       }
       if (!ok) {
         give_up();
         umma::commit(&ctl.drained);  // what was issued must be over before the memory is freed
-        mbar_wait_bounded(&ctl.drained, 0);
+        wait(&ctl.drained, 0);
       }
-    }
-    __syncwarp();
-  } else if (clean_last) {
-    // ======================= V rows past the last token ===================================
-    const int slot = (2 * chunks - 1) % kSlots;
-    if (mbar_wait_bounded(&ctl.v_last, 0)) {
-      unsigned char* v = smem + Shared::kRing + slot * kTileBytes;
-      for (int u = last_valid * 8 + (warp - kFixWarp) * 32 + lane; u < kTile * 8; u += 64) {
-        *reinterpret_cast<uint4*>(v + u * 16) = make_uint4(0u, 0u, 0u, 0u);
-        *reinterpret_cast<uint4*>(v + kHalfBytes + u * 16) = make_uint4(0u, 0u, 0u, 0u);
       }
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
-      if (lane == 0) mma::mbar_arrive(&ctl.v_fixed);
-    } else if (lane == 0) {
-      give_up();
-    }
+    } else if (warp == kCleanWarp) {
+      // ======================= V rows past the last token ===================================
+      int it = 0;
+      uint32_t cleaned = 0;
+      while (walk.next(prm, P, p)) {
+        it += 2 * (p.c1 - p.c0);
+        const int valid = p.n - (p.c1 - 1) * kTile;  // tokens of the last chunk
+        if (valid >= kTile) continue;
+        if (!mbar_wait_bounded(&ctl.v_last, cleaned & 1u)) {
+          if (lane == 0) give_up();
+          break;
+        }
+        ++cleaned;
+        unsigned char* rows = smem + Shared::kRing + ((it - 1) % kSlots) * kTileBytes;
+        for (int u = valid * 8 + lane; u < kTile * 8; u += 32) {
+          *reinterpret_cast<uint4*>(rows + u * 16) = make_uint4(0u, 0u, 0u, 0u);
+          *reinterpret_cast<uint4*>(rows + kHalfBytes + u * 16) = make_uint4(0u, 0u, 0u, 0u);
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) mma::mbar_arrive(&ctl.full[(it - 1) % kSlots]);
+      }
+      __syncwarp();
     }
   }
-
+  trigger_dependents();
+  __syncwarp();
   __syncthreads();  // every load from tensor memory is over
   if (*abort_flag && tid == 0) {
     // copies in flight must land before the block's memory is given up
     const int issued = *static_cast<volatile int*>(&ctl.issued);
-    for (int i = max(0, issued - kSlots); i < issued; ++i) {
-      if (i == 2 * chunks - 1 && clean_last) {
-        mbar_wait_bounded(&ctl.v_last, 0);
-      } else {
-        mbar_wait_bounded(&ctl.full[i % kSlots], static_cast<uint32_t>(i / kSlots) & 1u);
-      }
-    }
-    mbar_wait_bounded(&ctl.q_full, 0);
+    for (int i = max(0, issued - kSlots); i < issued; ++i)
+      mbar_wait_bounded(&ctl.full[i % kSlots], static_cast<uint32_t>(i / kSlots) & 1u);
+    const int issued_v = *static_cast<volatile int*>(&ctl.issued_v);
+    if (issued_v > 0) mbar_wait_bounded(&ctl.v_last, static_cast<uint32_t>(issued_v - 1) & 1u);
+    const int issued_q = *static_cast<volatile int*>(&ctl.issued_q);
+    if (issued_q > 0) mbar_wait_bounded(&ctl.q_full, static_cast<uint32_t>(issued_q - 1) & 1u);
   }
   if (warp == kMmaWarp) {
     umma::fence_after();
@@ -580,12 +752,8 @@ cudaError_t launch_one(const TreeParams& p, int group, cudaStream_t stream, bool
     if (e != cudaSuccess) return fail_at(e, "shared-memory attribute");
     configured.fetch_or(bit);
   }
-  const int pairs = (group * p.max_q_len + 2 * kTile - 1) / (2 * kTile);
-  const dim3 grid(static_cast<unsigned>(p.num_splits), static_cast<unsigned>(p.num_kv_heads * pairs),
-                  static_cast<unsigned>(p.bs));
-  return fail_at(launch_kernel(tree_mma_kernel<P>, grid, dim3(kThreads),
-                               static_cast<size_t>(Shared::kBytes), stream, use_pdl, mq, mk, mv, p,
-                               pairs),
+  return fail_at(launch_kernel(tree_mma_kernel<P>, dim3(p.blocks), dim3(kThreads),
+                               static_cast<size_t>(Shared::kBytes), stream, use_pdl, mq, mk, mv, p),
                  "cudaLaunchKernelEx");
 }
 

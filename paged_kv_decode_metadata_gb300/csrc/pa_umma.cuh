@@ -11,16 +11,16 @@
 namespace pa {
 namespace umma {
 
-// Operand descriptor of a 128-byte-swizzled tile at shared address `addr`: address, leading
-// and stride byte offsets in 16-byte units, descriptor version 1, swizzle mode 2 (128 B).
+// Operand descriptor of a 128-byte-swizzled tile: address, leading and stride byte offsets in
+// 16-byte units, descriptor version 1, swizzle mode 2 (128 B).  Only the low word (address,
+// leading offset) differs from tile to tile; the high word is kOperandHigh.
 //   K-major: the stride offset steps 8 rows (1024 bytes); the leading offset is not used.
 //   MN-major: the leading offset steps 64 elements along the row (the next 128-byte-wide
 //   tile), the stride offset 8 rows.
-__device__ __forceinline__ uint64_t operand(uint32_t addr, uint32_t leading) {
-  return static_cast<uint64_t>((addr & 0x3ffffu) >> 4) |
-         (static_cast<uint64_t>((leading >> 4) & 0x3fffu) << 16) |
-         (static_cast<uint64_t>(1024u >> 4) << 32) | (1ull << 46) | (2ull << 61);
+__device__ __forceinline__ constexpr uint32_t operand(uint32_t addr, uint32_t leading) {
+  return ((addr & 0x3ffffu) >> 4) | ((leading >> 4) << 16);
 }
+constexpr uint32_t kOperandHigh = (1024u >> 4) | (1u << 14) | (2u << 29);
 
 // Instruction descriptor: fp32 accumulator, bf16 operands, A K-major, M x N.
 constexpr uint32_t instruction(int m, int n, bool b_mn_major) {
@@ -28,23 +28,36 @@ constexpr uint32_t instruction(int m, int n, bool b_mn_major) {
          (static_cast<uint32_t>(n / 8) << 17) | (static_cast<uint32_t>(m / 16) << 24);
 }
 
+// True in one thread of a converged warp.  MMAs are issued under it and nothing else: under
+// any other condition the compiler has to allow for several issuing threads, and each MMA
+// then costs about 100 cycles to issue, against 64 to run.
+__device__ __forceinline__ bool elect() {
+  uint32_t one;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(one));
+  return one != 0;
+}
+
 // D[tmem] (+)= A[smem] B[smem]; issued by one thread.
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc,
                                        bool accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(accumulate ? 1u : 0u)
+      "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\tsetp.ne.u32 p, %5, 0;\n\t"
+      "mov.b64 da, {%1, %4};\n\tmov.b64 db, {%2, %4};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "r"(kOperandHigh), "r"(accumulate ? 1u : 0u)
       : "memory");
 }
 
 // The same with A in tensor memory (two bf16 to a column).
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc,
                                        bool accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(accumulate ? 1u : 0u)
+      "{\n\t.reg .pred p;\n\t.reg .b64 db;\n\tsetp.ne.u32 p, %5, 0;\n\t"
+      "mov.b64 db, {%2, %4};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "r"(kOperandHigh), "r"(accumulate ? 1u : 0u)
       : "memory");
 }
 

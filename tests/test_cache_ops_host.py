@@ -85,6 +85,7 @@ TREE = dict(q=FAKE, k=FAKE, v=FAKE, ks=None, vs=None, kv=0, pt=FAKE, pts=16, cl=
     (dict(kv=1), B.PA_ERR_INVALID),
     (dict(pts=8), B.PA_ERR_INVALID),
     (dict(msp=1 << 24, pts=1 << 24), B.PA_ERR_UNSUPPORTED),  # positions past 2^29
+    (dict(msp=1 << 22, pts=1 << 22, bs=1000), B.PA_ERR_UNSUPPORTED),  # chunks past 2^30
 ])
 def test_tree_refusals(lib, over, status):
     assert _caller(lib.pa_tree_attention, TREE)(**over) == status
@@ -219,11 +220,11 @@ def test_rope_frequency_refusals(kw):
 
 
 def test_tree_splits_and_workspace():
-    for bs, mql, hq, hkv, P, msp in ((1, 8, 32, 8, 64, 16), (32, 32, 32, 8, 64, 128), (1, 1, 1, 1, 16, 1),
-                                     (16, 64, 64, 8, 128, 128), (64, 256, 64, 8, 16, 1024)):
-        s = B.pa_choose_tree_splits(bs, mql, hq, hkv, P, msp, 152)
-        assert 1 <= s <= msp
-        assert -(-msp // -(-msp // s)) == s       # the longest request has no empty split
+    for (bs, mql, hq, hkv, P, msp), most in (((1, 8, 32, 8, 64, 16), 8), ((32, 32, 32, 8, 64, 128), 3),
+                                             ((1, 1, 1, 1, 16, 1), 1), ((16, 64, 64, 8, 128, 128), 3),
+                                             ((64, 256, 64, 8, 16, 1024), 2)):
+        # no more pieces than chunks of 128 tokens; two or three once units outnumber the SMs
+        assert 1 <= B.pa_choose_tree_splits(bs, mql, hq, hkv, P, msp, 152) <= most
     assert B.pa_choose_tree_splits(0, 8, 32, 8, 64, 16, 152) == 1
     assert B.pa_tree_workspace_bytes(0, 0, 0, 0, 0, 128, 64, 0) == 0
 
