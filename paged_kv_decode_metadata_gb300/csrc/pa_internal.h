@@ -133,6 +133,7 @@ struct TreeParams {
   int32_t num_splits;  // most pieces of a row's context (partial slots per row)
   int32_t min_share;   // fewest chunks in a block's share (keeps the pieces within num_splits)
   int32_t blocks;
+  int32_t group_shift;  // log2 of the query heads per kv head
   float q_scale;  // sm_scale * log2(e)
   // partials of several splits, or (one split) the output itself
   float *m_out, *l_out, *acc_out;

@@ -19,7 +19,7 @@
 //   warps 0-3, 4-7   softmax of stream 0, 1: a thread owns a row, so maxima and sums need no
 //                    exchange; scores come from and weights go back to tensor memory (P
 //                    takes the place of S, as the A operand of P V)
-//   warp 8           TMA: a ring of five 32 KiB tiles, K and V in turn, running ahead into the
+//   warp 8           TMA: a ring of four or five 32 KiB tiles, K and V in turn, running ahead into the
 //                    next unit; a lane issues one box (up to 64 tokens of one page, 64
 //                    channels), so small pages cost no more time than large ones
 //   warp 9           issues every MMA: P V of chunk c, then Q K^T of the stream's next chunk,
@@ -45,7 +45,7 @@ constexpr int kThreads = 384;
 // registers per thread after the split: 256 x 216 + 128 x 72 = 384 x 168 at launch
 constexpr int kSoftmaxRegs = 216, kOtherRegs = 72;
 static_assert(256 * kSoftmaxRegs + 128 * kOtherRegs <= kThreads * 168, "register split");
-constexpr int kSlots = 5;             // ring tiles
+constexpr int kStageBytes = 4096;     // per softmax warp: 128 bytes of each of its 32 rows
 constexpr int kHalfBytes = kTile * 128;       // 64 channels of 128 rows
 constexpr int kTileBytes = 2 * kHalfBytes;
 
@@ -83,6 +83,7 @@ struct Piece {
 struct Walk {
   int b, q_begin, q_len, n, pairs, chunks;  // the request at hand
   int base, pos, end, share;                // its start on the line; where the walk is
+  bool whole;                               // units are not cut
 
   // Lengths of request r, checked; `report` records what is wrong with them.
   __device__ __forceinline__ void load(const TreeParams& prm, int page_size, int r, bool report) {
@@ -99,8 +100,7 @@ struct Walk {
       if (report) record_error(prm.err, kErrSeqLenOutOfRange);
       n = n < 0 ? 0 : cap;
     }
-    const int G = prm.num_q_heads / prm.num_kv_heads;
-    pairs = (q_len * G + 2 * kTile - 1) / (2 * kTile);
+    pairs = ((q_len << prm.group_shift) + 2 * kTile - 1) / (2 * kTile);
     chunks = (n + kTile - 1) / kTile;
   }
   __device__ __forceinline__ int length(const TreeParams& prm) const {
@@ -111,6 +111,7 @@ struct Walk {
   // nothing cached (its rows are no work, but have a result).
   __device__ __forceinline__ bool start(const TreeParams& prm, int page_size, int lane, bool report) {
     int total = 0, first_sum = 0, first_w = 0;  // the first 32 requests' lengths are kept
+    int longest = 0, shortest = INT_MAX;        // units, in chunks
     bool empties = false;
     for (int r0 = 0; r0 < prm.bs; r0 += 32) {
       int w = 0;
@@ -118,6 +119,10 @@ struct Walk {
         load(prm, page_size, r0 + lane, report);
         w = length(prm);
         empties = empties || (q_len > 0 && n == 0);
+        if (w > 0) {
+          longest = max(longest, chunks);
+          shortest = min(shortest, chunks);
+        }
       }
       int incl = w;
 #pragma unroll
@@ -133,11 +138,17 @@ struct Walk {
     }
     empties = __any_sync(0xffffffffu, empties);
     const int grid = static_cast<int>(gridDim.x);
+    longest = __reduce_max_sync(0xffffffffu, longest);
+    shortest = __reduce_min_sync(0xffffffffu, shortest);
     share = max((total + grid - 1) / grid, prm.min_share);
+    // Units of one length that fill the blocks well enough stay whole: partials and their
+    // join cost more than up to a quarter of a share left idle (256 units on 152 SMs: whole
+    // 169 / 382 us, cut 179 / 407 us for one and two tiles).
+    whole = prm.num_splits == 1 ||
+            (longest == shortest && (total / longest + grid - 1) / grid * longest <= share + share / 4);
     const long long at_ll = static_cast<long long>(blockIdx.x) * share;
     pos = static_cast<int>(min(at_ll, static_cast<long long>(total)));
     end = static_cast<int>(min(at_ll + share, static_cast<long long>(total)));
-    const bool whole = prm.num_splits == 1;
     if (pos >= end) return empties;
     // the request that holds pos and, where units are not cut, the unit starts at or after
     // pos and end
@@ -173,7 +184,16 @@ struct Walk {
       }
       at += __shfl_sync(0xffffffffu, incl, 31);
     }
-    load(prm, page_size, found, false);  // (found >= 0: pos lies on the line)
+    if (prm.bs <= 32 && !whole) {  // the lane that holds it has its lengths
+      b = found;
+      q_begin = __shfl_sync(0xffffffffu, q_begin, found);
+      q_len = __shfl_sync(0xffffffffu, q_len, found);
+      n = __shfl_sync(0xffffffffu, n, found);
+      pairs = __shfl_sync(0xffffffffu, pairs, found);
+      chunks = __shfl_sync(0xffffffffu, chunks, found);
+    } else {
+      load(prm, page_size, found, false);  // (found >= 0: pos lies on the line)
+    }
     base = found_base;
     if (whole) {
       pos = base + (pos - base + chunks - 1) / chunks * chunks;
@@ -199,7 +219,7 @@ struct Walk {
     p.c1 = min(chunks, end - from);
     p.slot = 0;
     p.pieces = 1;
-    if (prm.num_splits > 1) {
+    if (!whole) {
       const int first = from / share;
       p.slot = static_cast<int>(blockIdx.x) - first;
       p.pieces = (from + chunks - 1) / share - first + 1;
@@ -209,10 +229,16 @@ struct Walk {
   }
 };
 
+// Shared memory of a block: the Q tiles, the ring, the softmax warps' way out, the control
+// words.  kTiles: Q tiles of the batch's units; with one, the other's room is a ring tile
+// more (memory bound there: two V tiles are held by the streams, the rest is in flight).
+template <int kTiles>
 struct Shared {
+  static constexpr int kSlots = 6 - kTiles;
   static constexpr int kQ = 0;
-  static constexpr int kRing = 2 * kTileBytes;
-  static constexpr int kEnd = kRing + kSlots * kTileBytes;
+  static constexpr int kRing = kTiles * kTileBytes;
+  static constexpr int kStage = kRing + kSlots * kTileBytes;
+  static constexpr int kEnd = kStage + kSoftmaxThreads / 32 * kStageBytes;
   struct Control {
     uint64_t full[kSlots], empty[kSlots];
     uint64_t q_full, q_empty, s_full[2], p_half[2], p_ready[2], o_full[2], v_last, drained;
@@ -223,24 +249,26 @@ struct Shared {
     int abort, issued, issued_v, issued_q;
   };
   static constexpr int kBytes = kEnd + static_cast<int>(sizeof(Control)) + 1024;  // + alignment
+  static_assert(kBytes <= 227 * 1024, "one block's shared memory");
 };
-static_assert(Shared::kBytes <= 227 * 1024, "one block's shared memory");
 
-template <int P>
+template <int P, int kTiles>
 __global__ void __launch_bounds__(kThreads, 1)
     tree_mma_kernel(const __grid_constant__ CUtensorMap map_q,
                     const __grid_constant__ CUtensorMap map_k,
                     const __grid_constant__ CUtensorMap map_v, const TreeParams prm) {
+  using Sh = Shared<kTiles>;
+  constexpr int kSlots = Sh::kSlots;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const uint32_t base_addr = smem_addr(smem);
-  Shared::Control& ctl = *reinterpret_cast<Shared::Control*>(smem + Shared::kEnd);
+  typename Sh::Control& ctl = *reinterpret_cast<typename Sh::Control*>(smem + Sh::kEnd);
   volatile int* abort_flag = &ctl.abort;
 
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // (uniform for the compiler too)
-  const int G = prm.num_q_heads / prm.num_kv_heads;
+  const int gs = prm.group_shift, G = 1 << gs;  // heads of a kv head: a power of two
   const int S = prm.num_splits;
 
   if (tid == 0) {
@@ -297,7 +325,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     *abort_flag = 1;
   };
   // two tiles: each is a stream over every chunk; one: the streams take alternate chunks
-  auto two_tiles = [&](const Piece& p) { return p.q_len * G - p.pair * 2 * kTile > kTile; };
+  auto two_tiles = [&](const Piece& p) {
+    return kTiles == 2 && p.q_len * G - p.pair * 2 * kTile > kTile;
+  };
   auto stream_chunks = [](bool two, int chunks, int s) { return two ? chunks : (chunks + 1 - s) / 2; };
 
   if (warp < kTmaWarp) {
@@ -327,7 +357,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       __syncwarp();
       if (vp.c1 == 0) break;
-      const bool two = vp.q_len * G - vp.pair * 2 * kTile > kTile;
+      const bool two = kTiles == 2 && vp.q_len * G - vp.pair * 2 * kTile > kTile;
       // this stream's chunks: c0 + k (two tiles) or c0 + 2 k + s; from `plain` on they reach the
       // drafted positions
       const int mine = stream_chunks(two, vp.c1 - vp.c0, s);
@@ -351,7 +381,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int q_len = vp.q_len, n = vp.n;
           const bool live = row < q_len * G;
           const uint32_t* mask =
-              prm.tree_mask + (static_cast<int64_t>(vp.q_begin) + (live ? row / G : 0)) * words;
+              prm.tree_mask + (static_cast<int64_t>(vp.q_begin) + (live ? row >> gs : 0)) * words;
           const int p0 = (vp.c0 + (two ? k : 2 * k + s)) * kTile;
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
@@ -431,7 +461,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const Piece p = {vp.b, vp.q_begin, vp.q_len, vp.n, vp.kvh, vp.pair, vp.c0, vp.c1, vp.slot, vp.pieces};
       const int row = (p.pair * 2 + (two ? s : 0)) * kTile + r;
       const bool live = row < p.q_len * G;
-      const int qi = live ? row / G : 0;
+      const int qi = live ? row >> gs : 0;
       const int64_t slot = (static_cast<int64_t>(p.q_begin) + qi) * prm.num_q_heads + p.kvh * G +
                            (live ? row - qi * G : 0);
       float f_own = 1.f, f_other = 0.f;  // factors of this and the other stream's accumulator
@@ -462,6 +492,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float inv = direct ? (l > 0.f || l != l ? 1.f / l : 0.f) : 1.f;
       const uint32_t other = o_col(1 - s) + lane_base;
       const bool write = live && ok;
+      // Rows leave through shared memory, 128 bytes of each of the warp's 32 at a time, so
+      // that a store covers whole lines of four rows: storing a row per thread took 32 lines
+      // a store and held up every other warp's shared-memory work for 8K cycles.  (16-byte
+      // pieces are XORed with the row: no bank conflicts either way.)
+      uint4* stage = reinterpret_cast<uint4*>(smem + Sh::kStage + warp * kStageBytes);
+      const int row0 = (p.pair * 2 + (two ? s : 0)) * kTile + (warp & 3) * 32;
+      const int live_rows = ok ? p.q_len * G - row0 : 0;  // of the warp's 32
       for (int c = col0; c < col1; c += 32) {
         float y[32];
         uint32_t o[32];
@@ -480,22 +517,40 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           __syncwarp();
         }
-#pragma unroll
-        for (int j = 0; j < 32; ++j) y[j] *= inv;
-        if (write && direct) {
-          uint4* out = static_cast<uint4*>(prm.out) + slot * 16 + c / 8;
+        if (direct) {
+          const int first = (c & 32) / 8;  // bf16: two steps of 32 channels fill the 128 bytes
 #pragma unroll
           for (int j = 0; j < 4; ++j)
-            out[j] = make_uint4(mma::pack_bf16(y[8 * j], y[8 * j + 1]),
-                                mma::pack_bf16(y[8 * j + 2], y[8 * j + 3]),
-                                mma::pack_bf16(y[8 * j + 4], y[8 * j + 5]),
-                                mma::pack_bf16(y[8 * j + 6], y[8 * j + 7]));
-        } else if (write) {
-          float4* acc = reinterpret_cast<float4*>(prm.acc_out) + (slot * S + p.slot) * 32 + c / 4;
+            stage[lane * 8 + ((first + j) ^ (lane & 7))] =
+                make_uint4(mma::pack_bf16(y[8 * j] * inv, y[8 * j + 1] * inv),
+                           mma::pack_bf16(y[8 * j + 2] * inv, y[8 * j + 3] * inv),
+                           mma::pack_bf16(y[8 * j + 4] * inv, y[8 * j + 5] * inv),
+                           mma::pack_bf16(y[8 * j + 6] * inv, y[8 * j + 7] * inv));
+          if (first == 0) continue;
+        } else {
 #pragma unroll
           for (int j = 0; j < 8; ++j)
-            acc[j] = make_float4(y[4 * j], y[4 * j + 1], y[4 * j + 2], y[4 * j + 3]);
+            stage[lane * 8 + (j ^ (lane & 7))] =
+                make_uint4(__float_as_uint(y[4 * j]), __float_as_uint(y[4 * j + 1]),
+                           __float_as_uint(y[4 * j + 2]), __float_as_uint(y[4 * j + 3]));
         }
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int rr = 4 * i + (lane >> 3), piece = lane & 7;
+          if (rr < live_rows) {
+            const uint4 w = stage[rr * 8 + (piece ^ (rr & 7))];
+            const int q = (row0 + rr) >> gs;
+            const int64_t at = (static_cast<int64_t>(p.q_begin) + q) * prm.num_q_heads + p.kvh * G +
+                               (row0 + rr - q * G);
+            if (direct) {
+              static_cast<uint4*>(prm.out)[at * 16 + (c & 64) / 8 + piece] = w;
+            } else {
+              reinterpret_cast<uint4*>(prm.acc_out)[(at * S + p.slot) * 32 + c / 4 + piece] = w;
+            }
+          }
+        }
+        __syncwarp();
       }
       if (write && (two || s == 0)) {
         const float m_nat = m_ref * 0.69314718055994530942f;  // -inf stays -inf
@@ -526,8 +581,24 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int box = lane >> 1, half = lane & 1;
       int it = 0;  // ring tiles issued
       uint32_t piece = 0;
-      bool ok = true;
-      while (ok && walk.next(prm, P, p)) {
+      bool ok = true, more = walk.next(prm, P, p);
+      auto load_rows = [&]() {  // Q of piece p; lane 0
+        const int tiles = two_tiles(p) ? 2 : 1;
+        ctl.issued_q = piece + 1;
+        mbar_arrive_expect_tx(&ctl.q_full, tiles * kTileBytes);
+        for (int t = 0; t < tiles; ++t)
+          for (int h = 0; h < 2; ++h)
+            asm volatile(
+                "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+                " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(base_addr + Sh::kQ + t * kTileBytes +
+                                                       h * kHalfBytes),
+                "l"(reinterpret_cast<uint64_t>(&map_q)), "r"(64 * h), "r"(p.kvh * G),
+                "r"(p.q_begin + (p.pair * 2 + t) * (kTile >> gs)), "r"(smem_addr(&ctl.q_full))
+                : "memory");
+      };
+      if (more && lane == 0) load_rows();
+      __syncwarp();
+      while (ok && more) {
         const int32_t* pt = prm.page_table + static_cast<int64_t>(p.b) * prm.page_table_stride;
         auto token_of = [&](int c) { return c * kTile + box * kBoxRows; };
         auto page_of = [&](int c) -> int {  // this lane's page of chunk c, -1: nothing to load
@@ -564,32 +635,20 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             __syncwarp();
             if (mine)
-              mma::tma_load_4d(base_addr + Shared::kRing + slot * kTileBytes + half * kHalfBytes +
+              mma::tma_load_4d(base_addr + Sh::kRing + slot * kTileBytes + half * kHalfBytes +
                                    box * kBoxRows * 128,
                                kv ? &map_v : &map_k, 64 * half, tok % P, p.kvh, pg, bar, policy);
             __syncwarp();
           }
-          if (ok && c == p.c0) {  // the rows: once the previous piece's scores are over
-            ok = piece == 0 || mbar_wait_bounded(&ctl.q_empty, (piece - 1) & 1u);
+          if (ok && c == p.c0 && piece > 0) {  // Q, once the previous piece's scores are over
+            ok = mbar_wait_bounded(&ctl.q_empty, (piece - 1) & 1u);
             ok = __all_sync(0xffffffffu, ok);
-            if (ok && lane == 0) {
-              const int tiles = two_tiles(p) ? 2 : 1;
-              ctl.issued_q = piece + 1;
-              mbar_arrive_expect_tx(&ctl.q_full, tiles * kTileBytes);
-              for (int t = 0; t < tiles; ++t)
-                for (int h = 0; h < 2; ++h)
-                  asm volatile(
-                      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-                      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(base_addr + Shared::kQ +
-                                                             t * kTileBytes + h * kHalfBytes),
-                      "l"(reinterpret_cast<uint64_t>(&map_q)), "r"(64 * h), "r"(p.kvh * G),
-                      "r"(p.q_begin + (p.pair * 2 + t) * (kTile / G)), "r"(smem_addr(&ctl.q_full))
-                      : "memory");
-            }
+            if (ok && lane == 0) load_rows();
             __syncwarp();
-            ++piece;
           }
         }
+        ++piece;
+        more = walk.next(prm, P, p);
       }
       if (!ok && lane == 0) give_up();
     } else if (warp == kMmaWarp) {
@@ -600,14 +659,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       int it0 = 0;  // ring tiles of the pieces before
       uint32_t piece = 0, used0 = 0, used1 = 0;  // products of each stream
       auto wait = [&](uint64_t* bar, uint32_t parity) { return mbar_wait_bounded(bar, parity & 1u); };
-      auto tile_addr = [&](int i) { return base_addr + Shared::kRing + (i % kSlots) * kTileBytes; };
+      auto tile_addr = [&](int i) { return base_addr + Sh::kRing + (i % kSlots) * kTileBytes; };
       auto wait_tile = [&](int i) { return wait(&ctl.full[i % kSlots], static_cast<uint32_t>(i / kSlots)); };
-      bool ok = true;
-      while (ok && walk.next(prm, P, p)) {
+      bool ok = true, more = walk.next(prm, P, p);
+      while (ok && more) {
         const bool two = two_tiles(p);
         const int chunks = p.c1 - p.c0;
         auto scores = [&](int s, int c) {  // S_s = Q_tile K_c^T; the tile and Q are done with
-          const uint32_t q = umma::operand(base_addr + Shared::kQ + (two ? s : 0) * kTileBytes, 16);
+          const uint32_t q = umma::operand(base_addr + Sh::kQ + (two ? s : 0) * kTileBytes, 16);
           const uint32_t k = umma::operand(tile_addr(it0 + 2 * c), 16);
           const uint32_t d = s_col(s);
 #pragma unroll
@@ -630,6 +689,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (s == 0 || !two) ok = wait_tile(it0 + 2 * c);
           if (ok) scores(s, c);
         }
+        more = walk.next(prm, P, p);  // (ahead: its look-ups wait for memory)
         for (int c = 0; c < chunks && ok; ++c) {
           const int s_begin = two ? 0 : c & 1, s_end = two ? 2 : s_begin + 1;
           const uint32_t v = umma::operand(tile_addr(it0 + 2 * c + 1), kHalfBytes);
@@ -682,7 +742,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           break;
         }
         ++cleaned;
-        unsigned char* rows = smem + Shared::kRing + ((it - 1) % kSlots) * kTileBytes;
+        unsigned char* rows = smem + Sh::kRing + ((it - 1) % kSlots) * kTileBytes;
         for (int u = valid * 8 + lane; u < kTile * 8; u += 32) {
           *reinterpret_cast<uint4*>(rows + u * 16) = make_uint4(0u, 0u, 0u, 0u);
           *reinterpret_cast<uint4*>(rows + kHalfBytes + u * 16) = make_uint4(0u, 0u, 0u, 0u);
@@ -732,7 +792,7 @@ inline cudaError_t encode_q_map(CUtensorMap* map, const TreeParams& p, int group
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-template <int P>
+template <int P, int kTiles>
 cudaError_t launch_one(const TreeParams& p, int group, cudaStream_t stream, bool use_pdl) {
   CUtensorMap mq, mk, mv;
   cudaError_t e = encode_q_map(&mq, p, group);
@@ -747,13 +807,13 @@ cudaError_t launch_one(const TreeParams& p, int group, cudaStream_t stream, bool
   if (e != cudaSuccess) return e;
   const unsigned long long bit = 1ull << (dev & 63);
   if ((configured.load() & bit) == 0) {
-    e = cudaFuncSetAttribute(tree_mma_kernel<P>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             Shared::kBytes);
+    e = cudaFuncSetAttribute(tree_mma_kernel<P, kTiles>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             Shared<kTiles>::kBytes);
     if (e != cudaSuccess) return fail_at(e, "shared-memory attribute");
     configured.fetch_or(bit);
   }
-  return fail_at(launch_kernel(tree_mma_kernel<P>, dim3(p.blocks), dim3(kThreads),
-                               static_cast<size_t>(Shared::kBytes), stream, use_pdl, mq, mk, mv, p),
+  return fail_at(launch_kernel(tree_mma_kernel<P, kTiles>, dim3(p.blocks), dim3(kThreads),
+                               static_cast<size_t>(Shared<kTiles>::kBytes), stream, use_pdl, mq, mk, mv, p),
                  "cudaLaunchKernelEx");
 }
 
