@@ -293,8 +293,8 @@ pa_status pa_tree_attention(const void* q, const void* k_cache, const void* v_ca
   cudaError_t e = pa::error_word(&p.err);
   if (e != cudaSuccess) return pa::from_cuda(e, "error word lookup");
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  st = finish(pa::launch_tree(p, kv_dtype == PA_KV_INT8, num_q_heads / num_kv_heads, page_size, s,
-                              use_pdl != 0),
+  st = finish((kv_dtype == PA_KV_INT8 ? pa::launch_tree_mma_int8 : pa::launch_tree_mma_bf16)(
+                  p, num_q_heads / num_kv_heads, page_size, s, use_pdl != 0),
               "tree attention launch");
   if (st != PA_OK || splits == 1) return st;
   return finish(pa::launch_tree_join(p, s, use_pdl != 0), "tree join launch");

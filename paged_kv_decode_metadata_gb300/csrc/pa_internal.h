@@ -250,9 +250,9 @@ cudaError_t launch_rope(const RopeParams& p, bool int8, bool interleaved, cudaSt
 // Combines the partials that the tree attention left in `m_out`, `l_out` and `acc_out`.
 cudaError_t launch_tree_join(const TreeParams& p, cudaStream_t stream, bool use_pdl);
 cudaError_t launch_tree_mask(const TreeMaskParams& p, cudaStream_t stream, bool use_pdl);
-cudaError_t launch_tree(const TreeParams& p, bool int8, int group, int page_size,
-                        cudaStream_t stream, bool use_pdl);
 cudaError_t launch_tree_mma_bf16(const TreeParams& p, int group, int page_size,
+                                 cudaStream_t stream, bool use_pdl);
+cudaError_t launch_tree_mma_int8(const TreeParams& p, int group, int page_size,
                                  cudaStream_t stream, bool use_pdl);
 cudaError_t launch_weights(const WeightsParams& p, bool int8, int group, int page_size,
                            cudaStream_t stream, bool use_pdl);

@@ -49,107 +49,6 @@ __global__ void __launch_bounds__(kMaxNodes) tree_mask_kernel(const TreeMaskPara
   }
 }
 
-// ---- attention --------------------------------------------------------------------------------
-
-constexpr int kWarps = 4;
-
-// One block per (split, query head, query row of the request); a warp takes every fourth
-// position, a lane 4 channels.
-template <bool kInt8>
-__global__ void __launch_bounds__(kWarps * 32) tree_kernel(const TreeParams p, int page_size) {
-  __shared__ float m_s[kWarps], l_s[kWarps];
-  __shared__ float4 o_s[kWarps][32];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int qi = blockIdx.x;
-  const int head = blockIdx.y, b = blockIdx.z;
-  const int kvh = head / (p.num_q_heads / p.num_kv_heads);
-  grid_dependency_wait();
-  const int q_begin = p.cu_seqlens_q[b];
-  int q_len = p.cu_seqlens_q[b + 1] - q_begin;
-  if (q_begin < 0 || q_len < 0 || q_len > p.max_q_len || q_begin > p.total_q - q_len) {
-    if (threadIdx.x == 0 && head == 0 && blockIdx.x == 0) record_error(p.err, kErrSeqLenOutOfRange);
-    q_len = 0;
-  }
-  if (qi >= q_len) return;
-  const int cap = p.max_seq_pages * page_size;
-  int n = p.cache_seqlens[b];
-  if (n < 0 || n > cap) {
-    if (threadIdx.x == 0 && head == 0 && blockIdx.x == 0) record_error(p.err, kErrSeqLenOutOfRange);
-    n = n < 0 ? 0 : cap;
-  }
-  const int64_t row = static_cast<int64_t>(q_begin) + qi;
-  const uint32_t* mask = p.tree_mask + row * (2 * p.mask_words);
-  const uint2 qw = reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(p.q) +
-                                                  (row * p.num_q_heads + head) * 128)[lane];
-  const float q0 = bf16_lo(qw.x), q1 = bf16_hi(qw.x), q2 = bf16_lo(qw.y), q3 = bf16_hi(qw.y);
-  const int base = n - q_len;
-  const int begin = 0, end = n;
-  float m = -CUDART_INF_F, l = 0.f;
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int j = begin + warp; j < end; j += kWarps) {
-    const int t = j - base;
-    if (t >= 0 && !((mask[t >> 5] >> (t & 31)) & 1u)) continue;
-    const int pg = p.page_table[static_cast<int64_t>(b) * p.page_table_stride + j / page_size];
-    if (pg < 0 || pg >= p.num_pages) {
-      if (lane == 0) record_error(p.err, kErrPageOutOfRange);
-      continue;
-    }
-    const int64_t r = (static_cast<int64_t>(pg) * p.num_kv_heads + kvh) * page_size + j % page_size;
-    float4 k, v;
-    if constexpr (kInt8) {
-      const uint32_t kw = static_cast<const uint32_t*>(p.k_cache)[r * 32 + lane];
-      const uint32_t vw = static_cast<const uint32_t*>(p.v_cache)[r * 32 + lane];
-      const float ks = p.k_scale[r], vs = p.v_scale[r];
-      s8x4_to_float(kw, k.x, k.y, k.z, k.w);
-      s8x4_to_float(vw, v.x, v.y, v.z, v.w);
-      k.x *= ks; k.y *= ks; k.z *= ks; k.w *= ks;
-      v.x *= vs; v.y *= vs; v.z *= vs; v.w *= vs;
-    } else {
-      const uint2 kw = static_cast<const uint2*>(p.k_cache)[r * 32 + lane];
-      const uint2 vw = static_cast<const uint2*>(p.v_cache)[r * 32 + lane];
-      k = make_float4(bf16_lo(kw.x), bf16_hi(kw.x), bf16_lo(kw.y), bf16_hi(kw.y));
-      v = make_float4(bf16_lo(vw.x), bf16_hi(vw.x), bf16_lo(vw.y), bf16_hi(vw.y));
-    }
-    const float x = warp_sum(q0 * k.x + q1 * k.y + q2 * k.z + q3 * k.w) * p.q_scale;
-    const float m_new = fmaxf(m, x);
-    const float a = exp2f(m - m_new), w = exp2f(x - m_new);
-    m = m_new;
-    l = l * a + w;
-    o.x = o.x * a + w * v.x;
-    o.y = o.y * a + w * v.y;
-    o.z = o.z * a + w * v.z;
-    o.w = o.w * a + w * v.w;
-  }
-  if (lane == 0) {
-    m_s[warp] = m;
-    l_s[warp] = l;
-  }
-  o_s[warp][lane] = o;
-  __syncthreads();
-  if (warp != 0) return;
-  float mm = -CUDART_INF_F;
-  for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, m_s[w]);
-  float total = 0.f;
-  o = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int w = 0; w < kWarps; ++w) {
-    const float a = m_s[w] == -CUDART_INF_F ? 0.f : exp2f(m_s[w] - mm);
-    const float4 ow = o_s[w][lane];
-    total += l_s[w] * a;
-    o.x += ow.x * a; o.y += ow.y * a; o.z += ow.z * a; o.w += ow.w * a;
-  }
-  const int64_t slot = row * p.num_q_heads + head;
-  {
-    if (p.num_splits > 1 && lane == 0) p.l_out[slot * p.num_splits] = -1.f;
-    const float inv = total > 0.f ? 1.f / total : 0.f;
-    const __nv_bfloat162 lo = __floats2bfloat162_rn(o.x * inv, o.y * inv);
-    const __nv_bfloat162 hi = __floats2bfloat162_rn(o.z * inv, o.w * inv);
-    static_cast<uint2*>(p.out)[slot * 32 + lane] = make_uint2(
-        *reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
-    if (p.lse != nullptr && lane == 0)
-      p.lse[slot] = mm == -CUDART_INF_F ? mm : mm * 0.69314718055994530942f + logf(total);
-  }
-}
-
 // ---- the join of a row's pieces ---------------------------------------------------------------
 
 constexpr int kJoinWarps = 8;
@@ -232,16 +131,6 @@ cudaError_t launch_tree_join(const TreeParams& p, cudaStream_t stream, bool use_
   return fail_at(launch_kernel(tree_join_kernel, dim3(static_cast<unsigned>((warps + kJoinWarps - 1) / kJoinWarps)),
                                dim3(kJoinWarps * 32), 0, stream, use_pdl, p, per),
                  "cudaLaunchKernelEx (join)");
-}
-
-cudaError_t launch_tree(const TreeParams& p, bool int8, int group, int page_size,
-                        cudaStream_t stream, bool use_pdl) {
-  if (!int8) return launch_tree_mma_bf16(p, group, page_size, stream, use_pdl);
-  const dim3 grid(static_cast<unsigned>(p.max_q_len),
-                  static_cast<unsigned>(p.num_q_heads), static_cast<unsigned>(p.bs));
-  return fail_at(launch_kernel(int8 ? tree_kernel<true> : tree_kernel<false>, grid, dim3(kWarps * 32),
-                               0, stream, use_pdl, p, page_size),
-                 "cudaLaunchKernelEx");
 }
 
 }  // namespace pa

@@ -25,6 +25,9 @@
 //   warp 9           issues every MMA: P V of chunk c, then Q K^T of the stream's next chunk,
 //                    whose scores are ready when the other stream's are used up
 //   warp 10          zeroes V rows past a request's last token (0 * NaN is NaN)
+//   warps 12-15      int8 pools: codes to bf16 (exact), from a ring of raw tiles into the ring;
+//                    the K scale multiplies the fp32 score, the V scale the weight before
+//                    it is rounded
 // Masks cost nothing before the last chunks: only chunks that reach the drafted positions
 // look at the ancestor bits.
 //
@@ -40,14 +43,27 @@ namespace tree {
 
 constexpr int kTile = 128;            // rows of a tile, tokens of a chunk
 constexpr int kSoftmaxThreads = 256;  // two groups of four warps
-constexpr int kTmaWarp = 8, kMmaWarp = 9, kCleanWarp = 10;
-constexpr int kThreads = 384;
-// registers per thread after the split: 256 x 216 + 128 x 72 = 384 x 168 at launch
-constexpr int kSoftmaxRegs = 216, kOtherRegs = 72;
-static_assert(256 * kSoftmaxRegs + 128 * kOtherRegs <= kThreads * 168, "register split");
+constexpr int kTmaWarp = 8, kMmaWarp = 9, kCleanWarp = 10, kConvertWarp = 12;
+// Threads of a block, and registers per thread after the split between the softmax warps,
+// warps 8-11 and (int8) warps 12-15: together what the block was launched with.
+template <bool kQuant>
+struct Roles {
+  static constexpr int kThreads = kQuant ? 512 : 384;
+  static constexpr int kSoftmaxRegs = kQuant ? 192 : 216, kOtherRegs = kQuant ? 64 : 72;
+  static constexpr int kConvertRegs = 64;
+  static constexpr int kLaunchRegs = kQuant ? 128 : 168;
+  static_assert(256 * kSoftmaxRegs + 128 * kOtherRegs + (kQuant ? 128 * kConvertRegs : 0) <=
+                    kThreads * kLaunchRegs,
+                "register split");
+};
 constexpr int kStageBytes = 4096;     // per softmax warp: 128 bytes of each of its 32 rows
 constexpr int kHalfBytes = kTile * 128;       // 64 channels of 128 rows
 constexpr int kTileBytes = 2 * kHalfBytes;
+// int8: codes of a tile as they come, and behind a K tile's the chunk's K and V scales
+constexpr int kRawSlots = 3;
+constexpr int kRawCodes = kTile * 128;
+constexpr int kRawBytes = kRawCodes + 2 * kTile * 4;
+constexpr int kScaleSlots = 4;
 
 // Bits of the 32 positions from p0 that a row sees: every committed one (< base), of the
 // drafted ones those of its mask (bit t: position base + t), none at or past `end`.
@@ -232,15 +248,19 @@ struct Walk {
 // Shared memory of a block: the Q tiles, the ring, the softmax warps' way out, the control
 // words.  kTiles: Q tiles of the batch's units; with one, the other's room is a ring tile
 // more (memory bound there: two V tiles are held by the streams, the rest is in flight).
-template <int kTiles>
+// int8: the ring holds widened tiles (two or three: the codes behind them, not it, are what is
+// in flight).
+template <int kTiles, bool kQuant>
 struct Shared {
-  static constexpr int kSlots = 6 - kTiles;
+  static constexpr int kSlots = kQuant ? 4 - kTiles : 6 - kTiles;
   static constexpr int kQ = 0;
   static constexpr int kRing = kTiles * kTileBytes;
-  static constexpr int kStage = kRing + kSlots * kTileBytes;
+  static constexpr int kRaw = kRing + kSlots * kTileBytes;
+  static constexpr int kScales = kRaw + (kQuant ? kRawSlots * kRawBytes : 0);
+  static constexpr int kStage = kScales + (kQuant ? kScaleSlots * 2 * kTile * 4 : 0);
   static constexpr int kEnd = kStage + kSoftmaxThreads / 32 * kStageBytes;
   struct Control {
-    uint64_t full[kSlots], empty[kSlots];
+    uint64_t full[kSlots], empty[kSlots], raw_full[kRawSlots], raw_empty[kRawSlots];
     uint64_t q_full, q_empty, s_full[2], p_half[2], p_ready[2], o_full[2], v_last, drained;
     Walk walk[kSoftmaxThreads / 32];  // of the softmax warps
     Piece piece[kSoftmaxThreads / 32];
@@ -252,12 +272,25 @@ struct Shared {
   static_assert(kBytes <= 227 * 1024, "one block's shared memory");
 };
 
-template <int P, int kTiles>
-__global__ void __launch_bounds__(kThreads, 1)
+// Four int8 codes -> two words of two bf16 each, exactly.  A byte b = 128 s + m (s the sign
+// bit, m the low seven) behind 0x43 reads as 128 + m with the sign bit cleared and as 128 (1 +
+// s) with m cleared; the difference is m - 128 s, the code.
+__device__ __forceinline__ uint32_t codes_to_bf16x2(uint32_t word, uint32_t selector) {
+  const uint32_t t = __byte_perm(word, 0x43434343u, selector);
+  const uint32_t x = t & 0xff7fff7fu, y = t & 0xff80ff80u;
+  const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&x),
+                                   *reinterpret_cast<const __nv_bfloat162*>(&y));
+  return *reinterpret_cast<const uint32_t*>(&d);
+}
+
+template <int P, int kTiles, bool kQuant>
+__global__ void __launch_bounds__(Roles<kQuant>::kThreads, 1)
     tree_mma_kernel(const __grid_constant__ CUtensorMap map_q,
                     const __grid_constant__ CUtensorMap map_k,
                     const __grid_constant__ CUtensorMap map_v, const TreeParams prm) {
-  using Sh = Shared<kTiles>;
+  using Sh = Shared<kTiles, kQuant>;
+  using Ro = Roles<kQuant>;
+  constexpr int kThreads = Ro::kThreads;
   constexpr int kSlots = Sh::kSlots;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>(
@@ -273,8 +306,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (tid == 0) {
     for (int i = 0; i < kSlots; ++i) {
-      mbar_init(&ctl.full[i], 1);
+      mbar_init(&ctl.full[i], kQuant ? 4 : 1);  // int8: the widening warps
       mbar_init(&ctl.empty[i], 1);
+    }
+    for (int i = 0; i < kRawSlots; ++i) {
+      mbar_init(&ctl.raw_full[i], 1);
+      mbar_init(&ctl.raw_empty[i], 4);
     }
     mbar_init(&ctl.q_full, 1);
     mbar_init(&ctl.q_empty, 1);
@@ -332,13 +369,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp < kTmaWarp) {
     // ======================= softmax ===================================================
-    umma::registers_up<kSoftmaxRegs>();
+    umma::registers_up<Ro::kSoftmaxRegs>();
     const int s = warp >> 2, r = tid & (kTile - 1);
     const uint32_t lane_base = static_cast<uint32_t>(warp & 3) << 21;  // lane 32 (warp % 4)
     const uint32_t sc = s_col(s) + lane_base, oc = o_col(s) + lane_base;
     const float scale = prm.q_scale;
     const int words = 2 * prm.mask_words;
     uint32_t step = 0, outputs = 0;  // of this stream, over all pieces
+    uint32_t chunk0 = 0;             // chunks of the pieces before
     // (after a wait that gave up, the pieces that are left only meet the barriers of the
     // softmax warps, so that none of them waits there for good)
     bool ok = true;
@@ -364,92 +402,241 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int committed = max(0, vp.n - vp.q_len) / kTile - vp.c0;  // chunks of those alone
       const int plain = two ? committed : (committed - s + 1) >> 1;
       float m_ref = -CUDART_INF_F, l = 0.f;  // the row's reference and sum of weights
+      float mq[4], lq[4];                    // int8: those of the thread's four rows
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        mq[q] = -CUDART_INF_F;
+        lq[q] = 0.f;
+      }
       for (int k = 0; k < mine && ok; ++k) {
         ok = mbar_wait_bounded(&ctl.s_full[s], step & 1u);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         ++step;
         umma::fence_after();
-        float x[kTile];
+        if constexpr (kQuant) {
+          // A thread holds 32 columns of four rows here (16 i + t / 4 + 8 j), so that a scale read
+          // from shared memory serves four rows: with a row per thread every scale went to
+          // every warp by itself, 2048 shared-memory cycles a chunk.
+          const float2* scales = reinterpret_cast<const float2*>(smem + Sh::kScales) +
+                                 (chunk0 + (two ? k : 2 * k + s)) % kScaleSlots * kTile + (lane & 3);
+          // (the chunk's K scales, then its V scales; written before the scores' K tile was
+          // handed on, so before these scores)
+          uint32_t xr[2][64];
+          umma::ld_frag64(sc, xr[0]);
+          umma::ld_frag64(sc + (16u << 16), xr[1]);
+          umma::wait_ld(xr[0]);
+          umma::wait_ld(xr[1]);
+          auto value = [&](int h, int i) -> float { return __uint_as_float(xr[h][i]); };
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          umma::ld32(sc + 32 * i, *reinterpret_cast<uint32_t(*)[32]>(&x[32 * i]));
+          for (int c = 0; c < 16; ++c) {  // columns 8 c + 2 (t % 4), + 1
+            const float2 f = scales[4 * c];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) umma::wait_ld(*reinterpret_cast<uint32_t(*)[32]>(&x[32 * i]));
-        if (k >= plain) {  // drafted or missing positions
-          const int row = (vp.pair * 2 + (two ? s : 0)) * kTile + r;
-          const int q_len = vp.q_len, n = vp.n;
-          const bool live = row < q_len * G;
-          const uint32_t* mask =
-              prm.tree_mask + (static_cast<int64_t>(vp.q_begin) + (live ? row >> gs : 0)) * words;
-          const int p0 = (vp.c0 + (two ? k : 2 * k + s)) * kTile;
+            for (int h = 0; h < 2; ++h)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint32_t bits = live ? visible(p0 + 32 * i, n - q_len, n, mask, words) : 0u;
+              for (int j = 0; j < 2; ++j) {
+                float lo, hi;
+                umma::unpair(umma::mul2(umma::pair(value(h, 4 * c + 2 * j), value(h, 4 * c + 2 * j + 1)),
+                                        umma::pair(f.x, f.y)),
+                             lo, hi);
+                xr[h][4 * c + 2 * j] = __float_as_uint(lo);
+                xr[h][4 * c + 2 * j + 1] = __float_as_uint(hi);
+              }
+          }
+          if (k >= plain) {  // drafted or missing positions
+            const int q_len = vp.q_len, n = vp.n;
+            const int p0 = (vp.c0 + (two ? k : 2 * k + s)) * kTile;
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-              x[32 * i + j] = (bits >> j) & 1u ? x[32 * i + j] : -CUDART_INF_F;
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+              for (int j = 0; j < 2; ++j) {
+                const int row = (vp.pair * 2 + (two ? s : 0)) * kTile + (warp & 3) * 32 + 16 * h + 8 * j +
+                                (lane >> 2);
+                const bool live = row < q_len * G;
+                const uint32_t* mask =
+                    prm.tree_mask + (static_cast<int64_t>(vp.q_begin) + (live ? row >> gs : 0)) * words;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  const uint32_t bits =
+                      live ? visible(p0 + 32 * i, n - q_len, n, mask, words) >> (2 * (lane & 3)) : 0u;
+#pragma unroll
+                  for (int c = 0; c < 4; ++c) {
+                    uint32_t& lo = xr[h][16 * i + 4 * c + 2 * j];
+                    uint32_t& hi = xr[h][16 * i + 4 * c + 2 * j + 1];
+                    lo = (bits >> (8 * c)) & 1u ? lo : 0xff800000u;  // -inf
+                    hi = (bits >> (8 * c + 1)) & 1u ? hi : 0xff800000u;
+                  }
+                }
+              }
+            __syncwarp();
+          }
+          float alpha[4];
+          bool moved = false;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const int h = q >> 1, j = q & 1;
+            float top = fmaxf(value(h, 2 * j), value(h, 2 * j + 1));
+#pragma unroll
+            for (int c = 1; c < 16; ++c)
+              top = umma::max3(top, value(h, 4 * c + 2 * j), value(h, 4 * c + 2 * j + 1));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            const float m_new = top * scale;
+            alpha[q] = 1.f;
+            if (m_new > mq[q] + mma::kMaxSlack) {
+              alpha[q] = mq[q] == -CUDART_INF_F ? 0.f : mma::fast_exp2(mq[q] - m_new);
+              mq[q] = m_new;
+              lq[q] *= alpha[q];
+              moved = true;
+            }
           }
           __syncwarp();
-        }
-        float mx[4] = {x[0], x[1], x[2], x[3]};
+          if (k > 0 && __any_sync(0xffffffffu, moved)) {
 #pragma unroll
-        for (int j = 4; j < kTile - 4; j += 8)
+            for (int h = 0; h < 2; ++h)
 #pragma unroll
-          for (int u = 0; u < 4; ++u) mx[u] = umma::max3(mx[u], x[j + u], x[j + 4 + u]);
+              for (int i = 0; i < 4; ++i) {
+                uint32_t o[16];
+                umma::ld_frag16(oc + 32 * i + (h ? 16u << 16 : 0u), o);
+                umma::wait_ld(o);
 #pragma unroll
-        for (int u = 0; u < 4; ++u) mx[u] = fmaxf(mx[u], x[kTile - 4 + u]);
-        // (sm_scale > 0: the largest score is the largest product)
-        const float m_new = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale;
-        float alpha = 1.f;
-        if (m_new > m_ref + mma::kMaxSlack) {
-          alpha = m_ref == -CUDART_INF_F ? 0.f : mma::fast_exp2(m_ref - m_new);
-          m_ref = m_new;
-          l *= alpha;
-        }
-        __syncwarp();
-        // the accumulator follows a moved reference (before the first product there is none;
-        // earlier products are over once the scores are)
-        if (k > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            uint32_t o[32];
-            umma::ld32(oc + 32 * i, o);
-            umma::wait_ld(o);
-#pragma unroll
-            for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * alpha);
-            umma::st32(oc + 32 * i, o);
+                for (int u = 0; u < 16; ++u)
+                  o[u] = __float_as_uint(__uint_as_float(o[u]) * alpha[2 * h + ((u >> 1) & 1)]);
+                umma::st_frag16(oc + 32 * i + (h ? 16u << 16 : 0u), o);
+              }
           }
-        }
-        const float ref = m_ref == -CUDART_INF_F ? 0.f : m_ref;
-        const uint64_t scale2 = umma::pair(scale, scale), ref2 = umma::pair(-ref, -ref);
-        uint64_t sum[4] = {0, 0, 0, 0};  // pairs of +0
+          const uint64_t scale2 = umma::pair(scale, scale);
+          uint64_t sum[4] = {0, 0, 0, 0};  // pairs of +0
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          uint32_t w[16];
+          for (int half = 0; half < 2; ++half) {
+            uint32_t w[2][16];
 #pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            float lo, hi;
-            umma::unpair(umma::fma2(umma::pair(x[32 * i + 2 * j], x[32 * i + 2 * j + 1]), scale2, ref2),
-                         lo, hi);
-            lo = mma::fast_exp2(lo);
-            hi = mma::fast_exp2(hi);
-            sum[j & 3] = umma::add2(sum[j & 3], umma::pair(lo, hi));
-            w[j] = mma::pack_bf16(lo, hi);
-          }
-          umma::st16(sc + 16 * i, w);
-          if (i & 1) {  // half of the weights: their products may start
+            for (int c = 0; c < 8; ++c) {
+              const float2 f = scales[kTile / 2 + 4 * (8 * half + c)];
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                const int h = q >> 1, j = q & 1, i = 4 * (8 * half + c) + 2 * j;
+                const float ref = mq[q] == -CUDART_INF_F ? 0.f : mq[q];
+                float lo, hi;
+                umma::unpair(umma::fma2(umma::pair(value(h, i), value(h, i + 1)), scale2,
+                                        umma::pair(-ref, -ref)),
+                             lo, hi);
+                lo = mma::fast_exp2(lo);
+                hi = mma::fast_exp2(hi);
+                sum[q] = umma::add2(sum[q], umma::pair(lo, hi));
+                // the V scale goes with the weight
+                umma::unpair(umma::mul2(umma::pair(lo, hi), umma::pair(f.x, f.y)), lo, hi);
+                w[h][2 * c + j] = mma::pack_bf16(lo, hi);
+              }
+            }
+            umma::st_pairs16(sc + 32 * half, w[0]);
+            umma::st_pairs16(sc + 32 * half + (16u << 16), w[1]);
             umma::wait_st();
             umma::fence_before();
             __syncwarp();
-            if (lane == 0) mma::mbar_arrive(i == 1 ? &ctl.p_half[s] : &ctl.p_ready[s]);
+            if (lane == 0) mma::mbar_arrive(half == 0 ? &ctl.p_half[s] : &ctl.p_ready[s]);
           }
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            float lo, hi;
+            umma::unpair(sum[q], lo, hi);
+            lq[q] += lo + hi;
+          }
+        } else {
+          float x[kTile];
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            umma::ld32(sc + 32 * i, *reinterpret_cast<uint32_t(*)[32]>(&x[32 * i]));
+#pragma unroll
+          for (int i = 0; i < 4; ++i) umma::wait_ld(*reinterpret_cast<uint32_t(*)[32]>(&x[32 * i]));
+          if (k >= plain) {  // drafted or missing positions
+            const int row = (vp.pair * 2 + (two ? s : 0)) * kTile + r;
+            const int q_len = vp.q_len, n = vp.n;
+            const bool live = row < q_len * G;
+            const uint32_t* mask =
+                prm.tree_mask + (static_cast<int64_t>(vp.q_begin) + (live ? row >> gs : 0)) * words;
+            const int p0 = (vp.c0 + (two ? k : 2 * k + s)) * kTile;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const uint32_t bits = live ? visible(p0 + 32 * i, n - q_len, n, mask, words) : 0u;
+#pragma unroll
+              for (int j = 0; j < 32; ++j)
+                x[32 * i + j] = (bits >> j) & 1u ? x[32 * i + j] : -CUDART_INF_F;
+            }
+            __syncwarp();
+          }
+          float mx[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+          for (int j = 4; j < kTile - 4; j += 8)
+#pragma unroll
+            for (int u = 0; u < 4; ++u) mx[u] = umma::max3(mx[u], x[j + u], x[j + 4 + u]);
+#pragma unroll
+          for (int u = 0; u < 4; ++u) mx[u] = fmaxf(mx[u], x[kTile - 4 + u]);
+          // (sm_scale > 0: the largest score is the largest product)
+          const float m_new = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale;
+          float alpha = 1.f;
+          if (m_new > m_ref + mma::kMaxSlack) {
+            alpha = m_ref == -CUDART_INF_F ? 0.f : mma::fast_exp2(m_ref - m_new);
+            m_ref = m_new;
+            l *= alpha;
+          }
+          __syncwarp();
+          // the accumulator follows a moved reference (before the first product there is none;
+          // earlier products are over once the scores are)
+          if (k > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              uint32_t o[32];
+              umma::ld32(oc + 32 * i, o);
+              umma::wait_ld(o);
+#pragma unroll
+              for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * alpha);
+              umma::st32(oc + 32 * i, o);
+            }
+          }
+          const float ref = m_ref == -CUDART_INF_F ? 0.f : m_ref;
+          const uint64_t scale2 = umma::pair(scale, scale), ref2 = umma::pair(-ref, -ref);
+          uint64_t sum[4] = {0, 0, 0, 0};  // pairs of +0
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t w[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              float lo, hi;
+              umma::unpair(umma::fma2(umma::pair(x[32 * i + 2 * j], x[32 * i + 2 * j + 1]), scale2, ref2),
+                           lo, hi);
+              lo = mma::fast_exp2(lo);
+              hi = mma::fast_exp2(hi);
+              sum[j & 3] = umma::add2(sum[j & 3], umma::pair(lo, hi));
+              w[j] = mma::pack_bf16(lo, hi);
+            }
+            umma::st16(sc + 16 * i, w);
+            if (i & 1) {  // half of the weights: their products may start
+              umma::wait_st();
+              umma::fence_before();
+              __syncwarp();
+              if (lane == 0) mma::mbar_arrive(i == 1 ? &ctl.p_half[s] : &ctl.p_ready[s]);
+            }
+          }
+          float lo, hi;
+          umma::unpair(umma::add2(umma::add2(sum[0], sum[1]), umma::add2(sum[2], sum[3])), lo, hi);
+          l += lo + hi;
         }
-        float lo, hi;
-        umma::unpair(umma::add2(umma::add2(sum[0], sum[1]), umma::add2(sum[2], sum[3])), lo, hi);
-        l += lo + hi;
       }
-
+      if constexpr (kQuant) {  // the four rows' numbers to the threads that own the rows below
+        float2* box = reinterpret_cast<float2*>(smem + Sh::kStage + warp * kStageBytes);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          lq[q] += __shfl_xor_sync(0xffffffffu, lq[q], 1);
+          lq[q] += __shfl_xor_sync(0xffffffffu, lq[q], 2);
+          if ((lane & 3) == 0) box[16 * (q >> 1) + 8 * (q & 1) + (lane >> 2)] = make_float2(mq[q], lq[q]);
+        }
+        __syncwarp();
+        m_ref = box[lane].x;
+        l = box[lane].y;
+        __syncwarp();
+      }
+      chunk0 += vp.c1 - vp.c0;
       // ----- the rows' results -------------------------------------------------------------
       if (ok && mine > 0) {
         ok = mbar_wait_bounded(&ctl.o_full[s], outputs & 1u);
@@ -569,8 +756,70 @@ __global__ void __launch_bounds__(kThreads, 1)
       // the next join this one's numbers
       if (!two) asm volatile("bar.sync 1, 256;" ::: "memory");
     }
+  } else if (kQuant && warp >= kConvertWarp) {
+    // ======================= int8: codes to bf16 ============================================
+    umma::registers_down<Ro::kConvertRegs>();
+    Piece p;
+    const int t = tid - kConvertWarp * 32;  // 0..127
+    int it = 0;
+    uint32_t chunk = 0;
+    bool ok = true;
+    while (ok && walk.next(prm, P, p)) {
+      for (int c = p.c0; c < p.c1 && ok; ++c, ++chunk) {
+        for (int kv = 0; kv < 2; ++kv, ++it) {
+          const int raw = it % kRawSlots, slot = it % kSlots;
+          ok = mbar_wait_bounded(&ctl.raw_full[raw], static_cast<uint32_t>(it / kRawSlots) & 1u) &&
+               (it < kSlots ||
+                mbar_wait_bounded(&ctl.empty[slot], static_cast<uint32_t>(it / kSlots - 1) & 1u));
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          const unsigned char* src = smem + Sh::kRaw + raw * kRawBytes;
+          unsigned char* dst = smem + Sh::kRing + slot * kTileBytes;
+          if (kv == 0) {
+            // V scales of positions past the end may hold anything, and 0 * NaN is NaN
+            const float* in = reinterpret_cast<const float*>(src + kRawCodes);
+            float* out = reinterpret_cast<float*>(smem + Sh::kScales) + chunk % kScaleSlots * 2 * kTile;
+            out[t] = in[t];
+            out[kTile + t] = c * kTile + t < p.n ? in[kTile + t] : 0.f;
+          }
+          // a warp turns 8 rows x 4 pieces of 16 codes at a time: every row's swizzle puts its
+          // piece in another bank group, for the loads and for both stores
+#pragma unroll
+          for (int u0 = 0; u0 < 8; u0 += 4) {
+            // (four pieces are loaded before the first store: the compiler cannot know that the
+            // two tiles do not overlap)
+            uint4 w[4];
+            auto row_of = [&](int u) { return ((warp - kConvertWarp) * 4 + (u >> 1)) * 8 + (lane & 7); };
+            auto piece_of = [&](int u) { return (u & 1) * 4 + (lane >> 3); };
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+              w[u] = *reinterpret_cast<const uint4*>(src + mma::swz(row_of(u0 + u), piece_of(u)));
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              const int row = row_of(u0 + u), j = piece_of(u);
+              const uint4 lo =
+                  make_uint4(codes_to_bf16x2(w[u].x, 0x4140), codes_to_bf16x2(w[u].x, 0x4342),
+                             codes_to_bf16x2(w[u].y, 0x4140), codes_to_bf16x2(w[u].y, 0x4342));
+              const uint4 hi =
+                  make_uint4(codes_to_bf16x2(w[u].z, 0x4140), codes_to_bf16x2(w[u].z, 0x4342),
+                             codes_to_bf16x2(w[u].w, 0x4140), codes_to_bf16x2(w[u].w, 0x4342));
+              unsigned char* half = dst + (j >> 2) * kHalfBytes;
+              *reinterpret_cast<uint4*>(half + mma::swz(row, (2 * j) & 7)) = lo;
+              *reinterpret_cast<uint4*>(half + mma::swz(row, (2 * j + 1) & 7)) = hi;
+            }
+          }
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+          if (lane == 0) {
+            mma::mbar_arrive(&ctl.full[slot]);
+            mma::mbar_arrive(&ctl.raw_empty[raw]);
+          }
+        }
+      }
+    }
+    if (!ok && lane == 0) give_up();
   } else {
-    umma::registers_down<kOtherRegs>();
+    umma::registers_down<Ro::kOtherRegs>();
     Piece p;
     if (warp == kTmaWarp) {
       // ======================= TMA ======================================================
@@ -578,7 +827,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       constexpr int kBoxes = kTile / kBoxRows;
       const uint64_t policy = l2_evict_first_policy();
       // lane -> (box of the chunk, channel half)
-      const int box = lane >> 1, half = lane & 1;
+      // (int8: lane -> box and what of it: the codes, and with K its K and its V scales)
+      const int box = kQuant ? lane & 7 : lane >> 1, half = kQuant ? lane >> 3 : lane & 1;
       int it = 0;  // ring tiles issued
       uint32_t piece = 0;
       bool ok = true, more = walk.next(prm, P, p);
@@ -617,6 +867,32 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           const int boxes = min(kBoxes, (p.n - c * kTile + kBoxRows - 1) / kBoxRows);
           for (int kv = 0; kv < 2; ++kv, ++it) {
+            if constexpr (kQuant) {
+              const int slot = it % kRawSlots;
+              ok = it < kRawSlots || mbar_wait_bounded(&ctl.raw_empty[slot],
+                                                       static_cast<uint32_t>(it / kRawSlots - 1) & 1u);
+              ok = __all_sync(0xffffffffu, ok && !*abort_flag);
+              if (!ok) break;
+              if (lane == 0) {
+                ctl.issued = it + 1;
+                mbar_arrive_expect_tx(&ctl.raw_full[slot],
+                                      boxes * kBoxRows * (128 + (kv == 0 ? 2 * 4 : 0)));
+              }
+              __syncwarp();
+              const uint32_t at = base_addr + Sh::kRaw + slot * kRawBytes;
+              if (mine && half == 0) {
+                mma::tma_load_4d(at + box * kBoxRows * 128, kv ? &map_v : &map_k, 0, tok % P, p.kvh, pg,
+                                 &ctl.raw_full[slot], policy);
+              } else if (mine && half <= 2 && kv == 0) {
+                const int64_t row = (static_cast<int64_t>(pg) * prm.num_kv_heads + p.kvh) * P + tok % P;
+                bulk_copy_g2s(smem + Sh::kRaw + slot * kRawBytes + kRawCodes +
+                                  ((half - 1) * kTile + box * kBoxRows) * 4,
+                              (half == 1 ? prm.k_scale : prm.v_scale) + row, kBoxRows * 4,
+                              &ctl.raw_full[slot], policy);
+              }
+              __syncwarp();
+              continue;
+            }
             const int slot = it % kSlots;
             ok = it < kSlots ||
                  mbar_wait_bounded(&ctl.empty[slot], static_cast<uint32_t>(it / kSlots - 1) & 1u);
@@ -729,7 +1005,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       }
       __syncwarp();
-    } else if (warp == kCleanWarp) {
+    } else if (!kQuant && warp == kCleanWarp) {
       // ======================= V rows past the last token ===================================
       int it = 0;
       uint32_t cleaned = 0;
@@ -760,8 +1036,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (*abort_flag && tid == 0) {
     // copies in flight must land before the block's memory is given up
     const int issued = *static_cast<volatile int*>(&ctl.issued);
-    for (int i = max(0, issued - kSlots); i < issued; ++i)
-      mbar_wait_bounded(&ctl.full[i % kSlots], static_cast<uint32_t>(i / kSlots) & 1u);
+    constexpr int kInFlight = kQuant ? kRawSlots : kSlots;
+    uint64_t* landed = kQuant ? ctl.raw_full : ctl.full;
+    for (int i = max(0, issued - kInFlight); i < issued; ++i)
+      mbar_wait_bounded(&landed[i % kInFlight], static_cast<uint32_t>(i / kInFlight) & 1u);
     const int issued_v = *static_cast<volatile int*>(&ctl.issued_v);
     if (issued_v > 0) mbar_wait_bounded(&ctl.v_last, static_cast<uint32_t>(issued_v - 1) & 1u);
     const int issued_q = *static_cast<volatile int*>(&ctl.issued_q);
@@ -792,14 +1070,14 @@ inline cudaError_t encode_q_map(CUtensorMap* map, const TreeParams& p, int group
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-template <int P, int kTiles>
+template <int P, int kTiles, bool kQuant>
 cudaError_t launch_one(const TreeParams& p, int group, cudaStream_t stream, bool use_pdl) {
   CUtensorMap mq, mk, mv;
   cudaError_t e = encode_q_map(&mq, p, group);
   if (e != cudaSuccess) return fail_at(e, "tensor map encode (Q)");
-  e = mma::encode_pool_map(&mk, p.k_cache, false, p.num_pages, p.num_kv_heads, P);
+  e = mma::encode_pool_map(&mk, p.k_cache, kQuant, p.num_pages, p.num_kv_heads, P);
   if (e != cudaSuccess) return fail_at(e, "tensor map encode (K)");
-  e = mma::encode_pool_map(&mv, p.v_cache, false, p.num_pages, p.num_kv_heads, P);
+  e = mma::encode_pool_map(&mv, p.v_cache, kQuant, p.num_pages, p.num_kv_heads, P);
   if (e != cudaSuccess) return fail_at(e, "tensor map encode (V)");
   static std::atomic<unsigned long long> configured{0};
   int dev = 0;
@@ -807,14 +1085,31 @@ cudaError_t launch_one(const TreeParams& p, int group, cudaStream_t stream, bool
   if (e != cudaSuccess) return e;
   const unsigned long long bit = 1ull << (dev & 63);
   if ((configured.load() & bit) == 0) {
-    e = cudaFuncSetAttribute(tree_mma_kernel<P, kTiles>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             Shared<kTiles>::kBytes);
+    e = cudaFuncSetAttribute(tree_mma_kernel<P, kTiles, kQuant>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             Shared<kTiles, kQuant>::kBytes);
     if (e != cudaSuccess) return fail_at(e, "shared-memory attribute");
     configured.fetch_or(bit);
   }
-  return fail_at(launch_kernel(tree_mma_kernel<P, kTiles>, dim3(p.blocks), dim3(kThreads),
-                               static_cast<size_t>(Shared<kTiles>::kBytes), stream, use_pdl, mq, mk, mv, p),
+  return fail_at(launch_kernel(tree_mma_kernel<P, kTiles, kQuant>, dim3(p.blocks), dim3(Roles<kQuant>::kThreads),
+                               static_cast<size_t>(Shared<kTiles, kQuant>::kBytes), stream, use_pdl, mq, mk, mv, p),
                  "cudaLaunchKernelEx");
+}
+
+template <bool kQuant>
+cudaError_t launch(const TreeParams& p, int group, int page_size, cudaStream_t stream, bool use_pdl) {
+  const bool one = group * p.max_q_len <= kTile;
+#define PA_TREE_CASE(P)                                                       \
+  case P:                                                                     \
+    return one ? launch_one<P, 1, kQuant>(p, group, stream, use_pdl)          \
+               : launch_one<P, 2, kQuant>(p, group, stream, use_pdl);
+  switch (page_size) {
+    PA_TREE_CASE(16)
+    PA_TREE_CASE(32)
+    PA_TREE_CASE(64)
+    PA_TREE_CASE(128)
+  }
+#undef PA_TREE_CASE
+  return cudaErrorInvalidValue;
 }
 
 }  // namespace tree
