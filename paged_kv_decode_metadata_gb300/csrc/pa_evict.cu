@@ -10,8 +10,7 @@
 // the warps (larger keys, equal keys) give every kept position its place.  Bound by the
 // latency of a block's passes; the keys are read once and kept in shared memory.
 //
-// Move.  To other pages (compact_kernel): a thread moves 16-byte pieces of K and V rows,
-// every row independent.  In place (compact_in_place_kernel): kept[i] >= i, so moving in
+// Move.  To other pages (compact_kernel): every row is independent.  In place (compact_in_place_kernel): kept[i] >= i, so moving in
 // ascending batches never overwrites a row that is still to be read, as long as a batch is
 // read whole before it is stored; a block owns one (request, kv head) and a slice of the
 // channels of K or of V (slices do not touch one another's bytes, so they need no order).
@@ -29,8 +28,8 @@ namespace {
 constexpr int kSelectThreads = 1024;
 constexpr int kSelectWarps = kSelectThreads / 32;
 constexpr int kBins = 2048;
-// positions whose keys stay in shared memory; longer rows read them again (from L2)
-constexpr int kCachedKeys = 48 * 1024;
+// positions of a row whose keys stay in shared memory; longer rows read them again (from L2)
+constexpr int kCachedKeys = 40 * 1024;
 
 // Orders like the weight: larger weight, larger key; -0 equals 0; every NaN is the largest.
 __device__ __forceinline__ uint32_t weight_key(float w) {
@@ -39,43 +38,23 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-// Inclusive sum over the block, in thread order; *total gets the sum of all.
-__device__ __forceinline__ int block_scan(int v, int* warp_sums, int* total) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-#pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const int up = __shfl_up_sync(0xffffffffu, v, d);
-    if (lane >= d) v += up;
-  }
-  if (lane == 31) warp_sums[warp] = v;
-  __syncthreads();
-  if (warp == 0) {
-    int s = warp_sums[lane];
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const int up = __shfl_up_sync(0xffffffffu, s, d);
-      if (lane >= d) s += up;
-    }
-    warp_sums[lane] = s;
-  }
-  __syncthreads();
-  if (warp > 0) v += warp_sums[warp - 1];
-  *total = warp_sums[kSelectWarps - 1];
-  __syncthreads();  // warp_sums may be used again
-  return v;
-}
-
 __global__ void __launch_bounds__(kSelectThreads) select_kernel(const SelectParams p, int cached) {
-  extern __shared__ uint32_t keys_s[];  // the first `cached` keys
-  __shared__ int hist[kBins];
-  __shared__ int warp_sums[kSelectWarps];
-  __shared__ uint32_t found_s[2];  // digit, keys above it
+  extern __shared__ uint32_t keys_s[];  // the keys, of rows of up to `cached`
+  // the first digit has two histograms, for even and odd lanes: weights cluster in few
+  // exponents, and a warp's counts of one bin queue up
+  __shared__ int hist[4][kBins];
+  __shared__ int warp_sums[3][kSelectWarps];
+  __shared__ uint32_t found_s[3][2];  // digit, keys above it
+  __shared__ int2 placed_s[kSelectWarps];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int h = blockIdx.x, b = blockIdx.y;
-  const int P = p.page_size;
+  const int ps = 31 - __clz(p.page_size);  // page sizes are powers of two
+#pragma unroll
+  for (int d = 0; d < 4; ++d)
+    for (int i = tid; i < kBins; i += kSelectThreads) hist[d][i] = 0;
   grid_dependency_wait();
 
-  const int cap = p.max_seq_pages * P;
+  const int cap = p.max_seq_pages << ps;
   int n = p.cache_seqlens[b];
   if (n < 0 || n > cap) {
     if (tid == 0 && h == 0) record_error(p.err, kErrSeqLenOutOfRange);
@@ -91,88 +70,145 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const SelectPara
   }
 
   const int32_t* pt = p.page_table + static_cast<int64_t>(b) * p.page_table_stride;
-  auto load_key = [&](int j) -> uint32_t {
-    const int pg = pt[j / P];
+  auto key_of = [&](int pg, int j) -> uint32_t {
     if (pg < 0 || pg >= p.num_pages) {
       record_error(p.err, kErrPageOutOfRange);
       return 0u;
     }
-    return weight_key(p.weights[(static_cast<int64_t>(pg) * p.num_kv_heads + h) * P + j % P]);
+    return weight_key(
+        p.weights[((static_cast<int64_t>(pg) * p.num_kv_heads + h) << ps) + (j & (p.page_size - 1))]);
   };
-  auto key_at = [&](int j) -> uint32_t { return j < cached ? keys_s[j] : load_key(j); };
-  const int in_smem = min(n, cached);
-  for (int j = tid; j < in_smem; j += kSelectThreads) keys_s[j] = load_key(j);
+  // Keys of positions j, j + step, ..: from shared memory or, of rows too long for it, again
+  // from memory; all on their way before the first is used.
+  constexpr int kAhead = 8;
+  const bool in_smem = n <= cached;
+  auto keys_at = [&](uint32_t (&k)[kAhead], int j, int step, int limit) {
+    if (in_smem) {
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) k[u] = j + u * step < limit ? keys_s[j + u * step] : 0u;
+    } else {
+      int pg[kAhead];
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) pg[u] = j + u * step < limit ? pt[(j + u * step) >> ps] : -2;
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) k[u] = pg[u] == -2 ? 0u : key_of(pg[u], j + u * step);
+    }
+  };
 
   // candidates: neither among the first nor among the newest
   const int lo = p.num_first, hi = n - p.num_recent;
   int need = p.budget - p.num_first - p.num_recent;  // of the candidates; < hi - lo
+  const bool none = need == 0;                        // only the first and the newest stay
   uint32_t prefix = 0;                                // digits of the need-th largest key
-  int shift = 21;
-#pragma unroll 1
-  for (int digit = 0; digit < 3 && need > 0; ++digit) {
-    const int bits = digit < 2 ? 11 : 10;
-    for (int i = tid; i < kBins; i += kSelectThreads) hist[i] = 0;
-    __syncthreads();
-    // (digit 0: no key has been narrowed yet; a 32-bit shift would be undefined)
-    for (int j = lo + tid; j < hi; j += kSelectThreads) {
-      const uint32_t k = key_at(j);
-      if (digit == 0 || (k >> (shift + bits)) == prefix)
-        atomicAdd(&hist[(k >> shift) & ((1u << bits) - 1u)], 1);
+  __syncthreads();  // the histograms are clear
+#pragma unroll
+  for (int digit = 0; digit < 3; ++digit) {
+    const int bits = digit < 2 ? 11 : 10, shift = digit == 0 ? 21 : digit == 1 ? 10 : 0;
+    if (none) break;
+    int* bins = hist[digit == 0 ? lane & 1 : digit + 1];
+    for (int j0 = tid; j0 < n; j0 += kAhead * kSelectThreads) {
+      uint32_t k[kAhead];
+      if (digit == 0) {  // the keys come with the first digit's pass: a page and a weight each
+        int pg[kAhead];
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+          const int j = j0 + u * kSelectThreads;
+          pg[u] = j < n ? pt[j >> ps] : -2;
+        }
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) k[u] = pg[u] == -2 ? 0u : key_of(pg[u], j0 + u * kSelectThreads);
+        if (in_smem) {
+#pragma unroll
+          for (int u = 0; u < kAhead; ++u)
+            if (j0 + u * kSelectThreads < n) keys_s[j0 + u * kSelectThreads] = k[u];
+        }
+      } else {
+        keys_at(k, j0, kSelectThreads, n);
+      }
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        const int j = j0 + u * kSelectThreads;
+        if (j >= lo && j < hi && (digit == 0 || (k[u] >> (shift + bits)) == prefix))
+          atomicAdd(&bins[(k[u] >> shift) & ((1u << bits) - 1u)], 1);
+      }
     }
     __syncthreads();
-    // bins from the largest down, two a thread: the one in which the count reaches `need`
+    // bins from the largest down, 64 a warp, two a lane: the one in which the count from
+    // above reaches `need`
     const int top = kBins - 1 - 2 * tid;
-    const int c0 = hist[top], c1 = hist[top - 1];
-    int all;
-    const int incl = block_scan(c0 + c1, warp_sums, &all);
+    const int* sums = hist[digit == 0 ? 0 : digit + 1];
+    const int c0 = sums[top] + (digit == 0 ? hist[1][top] : 0);
+    const int c1 = sums[top - 1] + (digit == 0 ? hist[1][top - 1] : 0);
+    int incl = c0 + c1;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int up = __shfl_up_sync(0xffffffffu, incl, d);
+      if (lane >= d) incl += up;
+    }
+    if (lane == 31) warp_sums[digit][warp] = incl;
+    __syncthreads();
+    int before = lane < warp ? warp_sums[digit][lane] : 0;
+#pragma unroll
+    for (int d = 16; d >= 1; d >>= 1) before += __shfl_xor_sync(0xffffffffu, before, d);
+    incl += before;
     const int above = incl - c0 - c1;
     if (above < need && incl >= need) {
       const bool first = above + c0 >= need;
-      found_s[0] = first ? top : top - 1;
-      found_s[1] = first ? above : above + c0;
+      found_s[digit][0] = first ? top : top - 1;
+      found_s[digit][1] = first ? above : above + c0;
     }
     __syncthreads();
-    prefix = (prefix << bits) | found_s[0];
-    need -= static_cast<int>(found_s[1]);
-    shift -= digit == 0 ? 11 : 10;
-    __syncthreads();
+    prefix = (prefix << bits) | found_s[digit][0];
+    need -= static_cast<int>(found_s[digit][1]);
   }
   // `prefix` is the smallest kept key; `need` of the keys equal to it stay (the lowest
-  // positions).  Nothing beyond the first and the newest is wanted when need was 0.
-  const bool none = p.budget - p.num_first - p.num_recent == 0;
+  // positions)
 
   // each warp places the kept positions of its run
   const int run = ((n + kSelectWarps - 1) / kSelectWarps + 31) / 32 * 32;
-  const int r0 = warp * run, r1 = min(n, r0 + run);
+  const int r0 = min(warp * run, n), r1 = min(n, r0 + run);
   int sure = 0, equal = 0;  // this warp's, over the run
-  for (int j0 = r0; j0 < r1; j0 += 32) {
-    const int j = j0 + lane;
+  auto judge = [&](int j, uint32_t k, bool& keep, bool& tie) {
     const bool in = j < r1;
     const bool cand = in && j >= lo && j < hi && !none;
-    const uint32_t k = cand ? key_at(j) : 0u;
-    const bool keep = in && (j < lo || j >= hi || (cand && k > prefix));
-    sure += __popc(__ballot_sync(0xffffffffu, keep));
-    equal += __popc(__ballot_sync(0xffffffffu, cand && k == prefix));
+    keep = in && (j < lo || j >= hi || (cand && k > prefix));
+    tie = cand && k == prefix;
+  };
+  for (int j0 = r0; j0 < r1; j0 += 32 * kAhead) {
+    uint32_t k[kAhead];
+    if (!none) keys_at(k, j0 + lane, 32, r1);
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      bool keep, tie;
+      judge(j0 + 32 * u + lane, k[u], keep, tie);
+      sure += __popc(__ballot_sync(0xffffffffu, keep));
+      equal += __popc(__ballot_sync(0xffffffffu, tie));
+    }
   }
-  int total;
-  const int sure_end = block_scan(lane == 0 ? sure : 0, warp_sums, &total);
-  const int equal_end = block_scan(lane == 0 ? equal : 0, warp_sums, &total);
-  int sure_at = __shfl_sync(0xffffffffu, sure_end, 0) - sure;
-  int equal_at = __shfl_sync(0xffffffffu, equal_end, 0) - equal;
+  if (lane == 0) placed_s[warp] = make_int2(sure, equal);
+  __syncthreads();
+  const int2 other = placed_s[lane];
+  int sure_at = lane < warp ? other.x : 0, equal_at = lane < warp ? other.y : 0;
+#pragma unroll
+  for (int d = 16; d >= 1; d >>= 1) {
+    sure_at += __shfl_xor_sync(0xffffffffu, sure_at, d);
+    equal_at += __shfl_xor_sync(0xffffffffu, equal_at, d);
+  }
   const uint32_t below = (1u << lane) - 1u;
-  for (int j0 = r0; j0 < r1; j0 += 32) {
-    const int j = j0 + lane;
-    const bool in = j < r1;
-    const bool cand = in && j >= lo && j < hi && !none;
-    const uint32_t k = cand ? key_at(j) : 0u;
-    const bool keep = in && (j < lo || j >= hi || (cand && k > prefix));
-    const bool tie = cand && k == prefix;
-    const uint32_t keeps = __ballot_sync(0xffffffffu, keep), ties = __ballot_sync(0xffffffffu, tie);
-    const int ties_before = equal_at + __popc(ties & below);
-    const int place = sure_at + __popc(keeps & below) + min(ties_before, need);
-    if (keep || (tie && ties_before < need)) kept[place] = j;
-    sure_at += __popc(keeps);
-    equal_at += __popc(ties);
+  for (int j0 = r0; j0 < r1; j0 += 32 * kAhead) {
+    uint32_t k[kAhead];
+    if (!none) keys_at(k, j0 + lane, 32, r1);
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      bool keep, tie;
+      judge(j0 + 32 * u + lane, k[u], keep, tie);
+      const uint32_t keeps = __ballot_sync(0xffffffffu, keep), ties = __ballot_sync(0xffffffffu, tie);
+      const int ties_before = equal_at + __popc(ties & below);
+      const int place = sure_at + __popc(keeps & below) + min(ties_before, need);
+      if (keep || (tie && ties_before < need)) kept[place] = j0 + 32 * u + lane;
+      sure_at += __popc(keeps);
+      equal_at += __popc(ties);
+    }
   }
 }
 
@@ -184,13 +220,13 @@ constexpr int kUnroll = 4;
 // Pool row of position j of the request, -1 where its page is outside the pool.
 __device__ __forceinline__ int64_t pool_row(const CompactParams& p, const int32_t* table, int j,
                                             int h) {
-  const int page = j / p.page_size;
-  const int pg = table[page];
+  const int ps = 31 - __clz(p.page_size);  // page sizes are powers of two
+  const int pg = table[j >> ps];
   if (pg < 0 || pg >= p.num_pages) {
     record_error(p.err, kErrPageOutOfRange);
     return -1;
   }
-  return (static_cast<int64_t>(pg) * p.num_kv_heads + h) * p.page_size + (j - page * p.page_size);
+  return ((static_cast<int64_t>(pg) * p.num_kv_heads + h) << ps) + (j & (p.page_size - 1));
 }
 
 struct Move {
@@ -230,37 +266,61 @@ __device__ __forceinline__ Move move_of(const CompactParams& p, const Row& r, in
   return m;
 }
 
-// kPieces: 16-byte pieces of a row (16: bf16, 8: int8).
+// kPieces: 16-byte pieces of a row (16: bf16, 8: int8).  A warp moves 32 rows: each lane looks
+// one up (kept position, both pages) and moves its 4-byte values, then the warp moves the
+// rows themselves, 32 / kPieces at a time and four such steps in flight.
 template <int kPieces>
 __global__ void __launch_bounds__(kMoveThreads) compact_kernel(const CompactParams p) {
-  constexpr int kRows = kMoveThreads / kPieces;
-  const int piece = threadIdx.x % kPieces, lane_row = threadIdx.x / kPieces;
+  constexpr int kAtOnce = 32 / kPieces;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int h = blockIdx.y, b = blockIdx.z;
   grid_dependency_wait();
   const Row r = row_of(p, b, h);
   if (p.new_seqlens != nullptr && blockIdx.x == 0 && h == 0 && threadIdx.x == 0)
     p.new_seqlens[b] = r.first + r.count;
-  const int i0 = blockIdx.x * kRows * kUnroll + lane_row;
-  if (blockIdx.x * kRows * kUnroll >= r.count) return;
-  Move m[kUnroll];
-  uint4 k[kUnroll], v[kUnroll];
+  const int i0 = (blockIdx.x * (kMoveThreads / 32) + warp) * 32;
+  if (i0 >= r.count) return;
+  const Move m = move_of<false>(p, r, i0 + lane, h);
+  const int piece = lane % kPieces, sub = lane / kPieces;
+  const uint4* k_in = static_cast<const uint4*>(p.k_cache) + piece;
+  const uint4* v_in = static_cast<const uint4*>(p.v_cache) + piece;
+  uint4* k_out = static_cast<uint4*>(p.k_cache) + piece;
+  uint4* v_out = static_cast<uint4*>(p.v_cache) + piece;
+  float w = 0.f, ks = 0.f, vs = 0.f;
+  if (m.src >= 0) {
+    if (p.weights != nullptr) w = p.weights[m.src];
+    if (p.k_scale != nullptr) {
+      ks = p.k_scale[m.src];
+      vs = p.v_scale[m.src];
+    }
+  }
 #pragma unroll
-  for (int u = 0; u < kUnroll; ++u) m[u] = move_of<false>(p, r, i0 + u * kRows, h);
+  for (int j = 0; j < 32; j += kAtOnce * kUnroll) {
+    int64_t src[kUnroll], dst[kUnroll];
+    uint4 k[kUnroll], v[kUnroll];
 #pragma unroll
-  for (int u = 0; u < kUnroll; ++u)
-    if (m[u].src >= 0) {
-      k[u] = static_cast<const uint4*>(p.k_cache)[m[u].src * kPieces + piece];
-      v[u] = static_cast<const uint4*>(p.v_cache)[m[u].src * kPieces + piece];
+    for (int u = 0; u < kUnroll; ++u) {
+      src[u] = __shfl_sync(0xffffffffu, m.src, j + u * kAtOnce + sub);
+      dst[u] = __shfl_sync(0xffffffffu, m.dst, j + u * kAtOnce + sub);
+      if (src[u] >= 0) {
+        k[u] = k_in[src[u] * kPieces];
+        v[u] = v_in[src[u] * kPieces];
+      }
     }
 #pragma unroll
-  for (int u = 0; u < kUnroll; ++u)
-    if (m[u].src >= 0) {
-      static_cast<uint4*>(p.k_cache)[m[u].dst * kPieces + piece] = k[u];
-      static_cast<uint4*>(p.v_cache)[m[u].dst * kPieces + piece] = v[u];
-      if (piece == 0 && p.weights != nullptr) p.weights[m[u].dst] = p.weights[m[u].src];
-      if (piece == 1 && p.k_scale != nullptr) p.k_scale[m[u].dst] = p.k_scale[m[u].src];
-      if (piece == 2 && p.v_scale != nullptr) p.v_scale[m[u].dst] = p.v_scale[m[u].src];
+    for (int u = 0; u < kUnroll; ++u)
+      if (src[u] >= 0) {
+        k_out[dst[u] * kPieces] = k[u];
+        v_out[dst[u] * kPieces] = v[u];
+      }
+  }
+  if (m.src >= 0) {
+    if (p.weights != nullptr) p.weights[m.dst] = w;
+    if (p.k_scale != nullptr) {
+      p.k_scale[m.dst] = ks;
+      p.v_scale[m.dst] = vs;
     }
+  }
 }
 
 // In place.  blockIdx.x: slice s of kSlices * 2 (K slices, then V slices) of 4 pieces each.
@@ -312,9 +372,10 @@ __global__ void __launch_bounds__(kMoveThreads) compact_in_place_kernel(const Co
 
 cudaError_t launch_select(const SelectParams& p, cudaStream_t stream, bool use_pdl) {
   const int64_t tokens = static_cast<int64_t>(p.max_seq_pages) * p.page_size;
+  // (a table wider than that still holds short rows)
   const int cached = static_cast<int>(tokens < kCachedKeys ? tokens : kCachedKeys);
   const size_t smem = static_cast<size_t>(cached) * 4;
-  if (smem > 32 * 1024) {
+  if (smem > 14 * 1024) {  // 33 KiB of static shared memory are in the 48 that need no asking
     cudaError_t e = cudaFuncSetAttribute(select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          kCachedKeys * 4);
     if (e != cudaSuccess) return fail_at(e, "shared-memory attribute");
@@ -334,8 +395,7 @@ cudaError_t launch_compact(const CompactParams& p, bool int8, bool in_place, cud
                                  dim3(kMoveThreads), 0, stream, use_pdl, p),
                    "cudaLaunchKernelEx (move)");
   }
-  const int rows = kMoveThreads / pieces * kUnroll;
-  const int blocks = (p.max_kept + rows - 1) / rows;
+  const int blocks = (p.max_kept + kMoveThreads - 1) / kMoveThreads;  // 32 rows a warp
   const dim3 grid(static_cast<unsigned>(blocks > 0 ? blocks : 1), hkv, bs);
   return fail_at(launch_kernel(int8 ? compact_kernel<8> : compact_kernel<16>, grid, dim3(kMoveThreads),
                                0, stream, use_pdl, p),

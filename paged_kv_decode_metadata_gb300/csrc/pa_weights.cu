@@ -20,23 +20,46 @@ namespace pa {
 namespace {
 
 constexpr int kWarps = 4;
-constexpr int kBlockTokens = 256;
+
+// One warp's 16 tokens of K on their way to the MMA registers: rows gid and gid + 8.
+template <bool kInt8>
+struct Tile {
+  uint4 a[kInt8 ? 2 : 4], b[kInt8 ? 2 : 4];
+  float sa, sb;  // int8: their scales
+
+  // row0: the pool row of the first token
+  __device__ __forceinline__ void load(const WeightsParams& p, int64_t row0, int gid, int tig) {
+    constexpr int kStep = kInt8 ? 1 : 4;  // pieces of a lane: side by side, or every fourth
+    const uint4* k0 = static_cast<const uint4*>(p.k_cache) + (row0 + gid) * (kInt8 ? 8 : 16) +
+                      (kInt8 ? 2 : 1) * tig;
+#pragma unroll
+    for (int j = 0; j < (kInt8 ? 2 : 4); ++j) {
+      a[j] = k0[kStep * j];
+      b[j] = k0[kStep * j + 8 * (kInt8 ? 8 : 16)];
+    }
+    if constexpr (kInt8) {
+      sa = p.k_scale[row0 + gid];
+      sb = p.k_scale[row0 + gid + 8];
+    }
+  }
+};
 
 template <bool kInt8, int kNT>
-__global__ void __launch_bounds__(kWarps * 32) weights_kernel(const WeightsParams p, int page_size) {
+__global__ void __launch_bounds__(kWarps * 32)
+    weights_kernel(const WeightsParams p, int page_shift, int block_tokens) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int gid = lane >> 2, tig = lane & 3;
   const int b = blockIdx.z, kvh = blockIdx.y;
   const int G = p.num_q_heads / p.num_kv_heads;
   grid_dependency_wait();
 
-  const int cap = p.max_seq_pages * page_size;
+  const int page_size = 1 << page_shift, cap = p.max_seq_pages << page_shift;
   int n = p.cache_seqlens[b];
   if (n < 0 || n > cap) {
     if (threadIdx.x == 0 && blockIdx.x == 0 && kvh == 0) record_error(p.err, kErrSeqLenOutOfRange);
     n = n < 0 ? 0 : cap;
   }
-  const int begin = blockIdx.x * kBlockTokens, end = min(n, begin + kBlockTokens);
+  const int begin = blockIdx.x * block_tokens, end = min(n, begin + block_tokens);
   if (begin >= end) return;
 
   // Q fragments (B operand) in the channel order of the K pieces, and the scores' factors
@@ -80,13 +103,21 @@ __global__ void __launch_bounds__(kWarps * 32) weights_kernel(const WeightsParam
     }
 
   const int32_t* pt = p.page_table + static_cast<int64_t>(b) * p.page_table_stride;
-  for (int t0 = begin + warp * 16; t0 < end; t0 += kWarps * 16) {
-    const int pg = pt[t0 / page_size];
+  constexpr int kStep = kWarps * 16;
+  int at = begin + warp * 16;
+  int next = at < end ? pt[at >> page_shift] : 0;
+#pragma unroll 1
+  for (; at < end; at += kStep) {
+    const int pg = next;
+    if (at + kStep < end) next = pt[(at + kStep) >> page_shift];
     if (pg < 0 || pg >= p.num_pages) {
       if (lane == 0) record_error(p.err, kErrPageOutOfRange);
       continue;
     }
-    const int64_t row0 = (static_cast<int64_t>(pg) * p.num_kv_heads + kvh) * page_size + t0 % page_size;
+    const int64_t row0 = ((static_cast<int64_t>(pg) * p.num_kv_heads + kvh) << page_shift) +
+                         (at & (page_size - 1));
+    Tile<kInt8> k;
+    k.load(p, row0, gid, tig);
     float acc[kNT][4];
 #pragma unroll
     for (int nt = 0; nt < kNT; ++nt)
@@ -94,13 +125,10 @@ __global__ void __launch_bounds__(kWarps * 32) weights_kernel(const WeightsParam
       for (int i = 0; i < 4; ++i) acc[nt][i] = 0.f;
     float ks[2] = {1.f, 1.f};
     if constexpr (kInt8) {
-      const uint4* k0 = reinterpret_cast<const uint4*>(static_cast<const int8_t*>(p.k_cache) +
-                                                       (row0 + gid) * 128) + 2 * tig;
-      const uint4 r[4] = {k0[0], k0[1], k0[64], k0[65]};  // rows gid and gid + 8
-      ks[0] = p.k_scale[row0 + gid];
-      ks[1] = p.k_scale[row0 + gid + 8];
-      const uint32_t w0[8] = {r[0].x, r[0].y, r[0].z, r[0].w, r[1].x, r[1].y, r[1].z, r[1].w};
-      const uint32_t w1[8] = {r[2].x, r[2].y, r[2].z, r[2].w, r[3].x, r[3].y, r[3].z, r[3].w};
+      ks[0] = k.sa;
+      ks[1] = k.sb;
+      const uint32_t w0[8] = {k.a[0].x, k.a[0].y, k.a[0].z, k.a[0].w, k.a[1].x, k.a[1].y, k.a[1].z, k.a[1].w};
+      const uint32_t w1[8] = {k.b[0].x, k.b[0].y, k.b[0].z, k.b[0].w, k.b[1].x, k.b[1].y, k.b[1].z, k.b[1].w};
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const uint32_t x0 = w0[j] ^ 0x80808080u, x1 = w1[j] ^ 0x80808080u;
@@ -119,18 +147,10 @@ __global__ void __launch_bounds__(kWarps * 32) weights_kernel(const WeightsParam
         for (int nt = 0; nt < kNT; ++nt) mma::mma16816<true>(acc[nt], a, qb[nt][j][0], qb[nt][j][1]);
       }
     } else {
-      const uint4* k0 = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.k_cache) +
-                                                       (row0 + gid) * 128) + tig;
-      uint4 r0[4], r1[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        r0[j] = k0[4 * j];
-        r1[j] = k0[4 * j + 128];
-      }
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const uint32_t lo[4] = {r0[j].x, r1[j].x, r0[j].y, r1[j].y};
-        const uint32_t hi[4] = {r0[j].z, r1[j].z, r0[j].w, r1[j].w};
+        const uint32_t lo[4] = {k.a[j].x, k.b[j].x, k.a[j].y, k.b[j].y};
+        const uint32_t hi[4] = {k.a[j].z, k.b[j].z, k.a[j].w, k.b[j].w};
 #pragma unroll
         for (int nt = 0; nt < kNT; ++nt) {
           mma::mma16816<false>(acc[nt], lo, qb[nt][2 * j][0], qb[nt][2 * j][1]);
@@ -153,7 +173,7 @@ __global__ void __launch_bounds__(kWarps * 32) weights_kernel(const WeightsParam
     }
     // (an add without a return: rows of a page that requests share meet in the L2)
     if (tig < 2) {
-      const int j = t0 + gid + 8 * tig;
+      const int j = at + gid + 8 * tig;
       if (j < end) atomicAdd(p.weights + row0 + gid + 8 * tig, tig == 0 ? sum[0] : sum[1]);
     }
   }
@@ -163,13 +183,23 @@ __global__ void __launch_bounds__(kWarps * 32) weights_kernel(const WeightsParam
 
 cudaError_t launch_weights(const WeightsParams& p, bool int8, int group, int page_size,
                            cudaStream_t stream, bool use_pdl) {
+  // Tokens per block: the more the fewer loads of Q (a fifth of the time at 256), but only
+  // while the blocks fill every slot (8 per SM) a few times over.  bs64 ragged to 16K int8:
+  // 181 / 133 / 112 / 104 / 107 us with 64 / 128 / 256 / 512 / 1024; one request of 8K:
+  // 3.5 / 3.5 / 4.5 / 6.7 us with 64 / 128 / 256 / 512.
   const int64_t tokens = static_cast<int64_t>(p.max_seq_pages) * page_size;
-  const dim3 grid(static_cast<unsigned>((tokens + kBlockTokens - 1) / kBlockTokens),
+  const int64_t units = static_cast<int64_t>(p.num_kv_heads) * p.bs;
+  int block_tokens = 128;
+  while (block_tokens < 512 && tokens / (2 * block_tokens) * units >= 152 * 8 * 3) block_tokens *= 2;
+  const dim3 grid(static_cast<unsigned>((tokens + block_tokens - 1) / block_tokens),
                   static_cast<unsigned>(p.num_kv_heads), static_cast<unsigned>(p.bs));
-  void (*kernel)(const WeightsParams, int) =
+  void (*kernel)(const WeightsParams, int, int) =
       int8 ? (group > 8 ? weights_kernel<true, 2> : weights_kernel<true, 1>)
            : (group > 8 ? weights_kernel<false, 2> : weights_kernel<false, 1>);
-  return fail_at(launch_kernel(kernel, grid, dim3(kWarps * 32), 0, stream, use_pdl, p, page_size),
+  int shift = 0;
+  while ((1 << shift) < page_size) ++shift;
+  return fail_at(launch_kernel(kernel, grid, dim3(kWarps * 32), 0, stream, use_pdl, p, shift,
+                               block_tokens),
                  "cudaLaunchKernelEx");
 }
 
