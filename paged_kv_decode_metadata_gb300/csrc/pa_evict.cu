@@ -6,8 +6,8 @@
 // to a 32-bit key that orders like it; the need-th largest key is found digit by digit from
 // the top (11 + 11 + 10 bits: a histogram of the keys that share the digits found so far,
 // then the bin in which the count from above reaches `need`).  Keys above it stay, of the
-// equal ones the lowest positions.  Each warp owns a run of positions; two prefix sums over
-// the warps (larger keys, equal keys) give every kept position its place.  Bound by the
+// equal ones the lowest positions.  Each thread owns a run of positions; two prefix sums over
+// the threads (larger keys, equal keys) give every kept position its place.  Bound by the
 // latency of a block's passes; the keys are read once and kept in shared memory.
 //
 // Move.  To other pages (compact_kernel): every row is independent.  In place (compact_in_place_kernel): kept[i] >= i, so moving in
@@ -39,7 +39,7 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
 }
 
 __global__ void __launch_bounds__(kSelectThreads) select_kernel(const SelectParams p, int cached) {
-  extern __shared__ uint32_t keys_s[];  // the keys, of rows of up to `cached`
+  extern __shared__ __align__(16) uint32_t keys_s[];  // the keys, of rows of up to `cached`
   // the first digit has two histograms, for even and odd lanes: weights cluster in few
   // exponents, and a warp's counts of one bin queue up
   __shared__ int hist[4][kBins];
@@ -53,6 +53,7 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const SelectPara
   for (int d = 0; d < 4; ++d)
     for (int i = tid; i < kBins; i += kSelectThreads) hist[d][i] = 0;
   grid_dependency_wait();
+  trigger_dependents();  // (the move behind it waits for this grid's end)
 
   const int cap = p.max_seq_pages << ps;
   int n = p.cache_seqlens[b];
@@ -164,50 +165,69 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const SelectPara
   // `prefix` is the smallest kept key; `need` of the keys equal to it stay (the lowest
   // positions)
 
-  // each warp places the kept positions of its run
-  const int run = ((n + kSelectWarps - 1) / kSelectWarps + 31) / 32 * 32;
-  const int r0 = min(warp * run, n), r1 = min(n, r0 + run);
-  int sure = 0, equal = 0;  // this warp's, over the run
+  // Each thread places the kept positions of its run, eight at a time (a lane's eight keys
+  // are two 16-byte reads); prefix sums over the threads say where it starts.
+  const int run = ((n + kSelectThreads - 1) / kSelectThreads + kAhead - 1) / kAhead * kAhead;
+  const int r0 = min(tid * run, n), r1 = min(n, r0 + run);
+  auto load_run = [&](uint32_t (&k)[kAhead], int j) {
+    if (none) return;
+    if (in_smem) {  // (keys past n are there, unused: the room is a multiple of 16 positions)
+      const uint4 a = *reinterpret_cast<const uint4*>(keys_s + j);
+      const uint4 c = *reinterpret_cast<const uint4*>(keys_s + j + 4);
+      k[0] = a.x; k[1] = a.y; k[2] = a.z; k[3] = a.w;
+      k[4] = c.x; k[5] = c.y; k[6] = c.z; k[7] = c.w;
+    } else {
+      keys_at(k, j, 1, r1);
+    }
+  };
   auto judge = [&](int j, uint32_t k, bool& keep, bool& tie) {
     const bool in = j < r1;
-    const bool cand = in && j >= lo && j < hi && !none;
-    keep = in && (j < lo || j >= hi || (cand && k > prefix));
-    tie = cand && k == prefix;
+    const bool always = j < lo || j >= hi;
+    keep = in && (always || (!none && k > prefix));
+    tie = in && !always && !none && k == prefix;
   };
-  for (int j0 = r0; j0 < r1; j0 += 32 * kAhead) {
+  int sure = 0, equal = 0;  // this thread's
+  for (int j = r0; j < r1; j += kAhead) {
     uint32_t k[kAhead];
-    if (!none) keys_at(k, j0 + lane, 32, r1);
+    load_run(k, j);
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
       bool keep, tie;
-      judge(j0 + 32 * u + lane, k[u], keep, tie);
-      sure += __popc(__ballot_sync(0xffffffffu, keep));
-      equal += __popc(__ballot_sync(0xffffffffu, tie));
+      judge(j + u, k[u], keep, tie);
+      sure += keep;
+      equal += tie;
     }
   }
-  if (lane == 0) placed_s[warp] = make_int2(sure, equal);
+  int sure_at = sure, equal_at = equal;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int up = __shfl_up_sync(0xffffffffu, sure_at, d), eq = __shfl_up_sync(0xffffffffu, equal_at, d);
+    if (lane >= d) {
+      sure_at += up;
+      equal_at += eq;
+    }
+  }
+  if (lane == 31) placed_s[warp] = make_int2(sure_at, equal_at);
   __syncthreads();
-  const int2 other = placed_s[lane];
-  int sure_at = lane < warp ? other.x : 0, equal_at = lane < warp ? other.y : 0;
+  int2 other = placed_s[lane];
+  if (lane >= warp) other = make_int2(0, 0);
 #pragma unroll
   for (int d = 16; d >= 1; d >>= 1) {
-    sure_at += __shfl_xor_sync(0xffffffffu, sure_at, d);
-    equal_at += __shfl_xor_sync(0xffffffffu, equal_at, d);
+    other.x += __shfl_xor_sync(0xffffffffu, other.x, d);
+    other.y += __shfl_xor_sync(0xffffffffu, other.y, d);
   }
-  const uint32_t below = (1u << lane) - 1u;
-  for (int j0 = r0; j0 < r1; j0 += 32 * kAhead) {
+  sure_at += other.x - sure;
+  equal_at += other.y - equal;
+  for (int j = r0; j < r1; j += kAhead) {
     uint32_t k[kAhead];
-    if (!none) keys_at(k, j0 + lane, 32, r1);
+    load_run(k, j);
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
       bool keep, tie;
-      judge(j0 + 32 * u + lane, k[u], keep, tie);
-      const uint32_t keeps = __ballot_sync(0xffffffffu, keep), ties = __ballot_sync(0xffffffffu, tie);
-      const int ties_before = equal_at + __popc(ties & below);
-      const int place = sure_at + __popc(keeps & below) + min(ties_before, need);
-      if (keep || (tie && ties_before < need)) kept[place] = j0 + 32 * u + lane;
-      sure_at += __popc(keeps);
-      equal_at += __popc(ties);
+      judge(j + u, k[u], keep, tie);
+      if (keep || (tie && equal_at < need)) kept[sure_at + min(equal_at, need)] = j + u;
+      sure_at += keep;
+      equal_at += tie;
     }
   }
 }
