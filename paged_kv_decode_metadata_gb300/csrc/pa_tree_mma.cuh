@@ -16,12 +16,13 @@
 // = all 512): with two tiles a stream is a tile; with one, the streams take alternate chunks
 // and are joined at the end.  So the tensor cores work on one stream while the other's
 // softmax runs.
-//   warps 0-3, 4-7   softmax of stream 0, 1: a thread owns a row, so maxima and sums need no
-//                    exchange; scores come from and weights go back to tensor memory (P
-//                    takes the place of S, as the A operand of P V)
-//   warp 8           TMA: a ring of four or five 32 KiB tiles, K and V in turn, running ahead into the
-//                    next unit; a lane issues one box (up to 64 tokens of one page, 64
-//                    channels), so small pages cost no more time than large ones
+//   warps 0-3, 4-7   softmax of stream 0, 1: bf16: a thread owns a row, so maxima and sums need
+//                    no exchange; int8: columns of four rows, so that a scale serves four.
+//                    Scores come from and weights go back to tensor memory (P takes the place
+//                    of S, as the A operand of P V)
+//   warp 8           TMA: a ring of four or five 32 KiB tiles, K and V in turn, running ahead
+//                    into the next unit; a lane issues one box (up to 64 tokens of one page,
+//                    64 channels), so small pages cost no more time than large ones
 //   warp 9           issues every MMA: P V of chunk c, then Q K^T of the stream's next chunk,
 //                    whose scores are ready when the other stream's are used up
 //   warp 10          zeroes V rows past a request's last token (0 * NaN is NaN)
@@ -31,8 +32,12 @@
 // Masks cost nothing before the last chunks: only chunks that reach the drafted positions
 // look at the ancestor bits.
 //
-// Bound by: memory up to about 256 rows per kv head (64 KiB of K/V per 128 tokens against
-// 1024 tensor cycles per tile), the tensor cores above.
+// Bound by, bf16: memory up to about 256 rows per kv head (64 KiB of K/V per 128 tokens against
+// 1024 tensor cycles per tile), the tensor cores above.  int8: a chunk takes 2.5 us with one
+// tile and 2.7 with two, 1.6 and 2.3 without the widening (bf16: 1.5 and 1.7): the three
+// integer steps and the subtraction of each pair of codes share the schedulers with the
+// softmax.  Eight widening warps instead of four, four for K and four for V, a third raw tile,
+// and shares weighted by the tiles of a chunk were all measured and were no faster.
 #pragma once
 
 #include "pa_splitk_mma.cuh"
@@ -44,23 +49,17 @@ namespace tree {
 constexpr int kTile = 128;            // rows of a tile, tokens of a chunk
 constexpr int kSoftmaxThreads = 256;  // two groups of four warps
 constexpr int kTmaWarp = 8, kMmaWarp = 9, kCleanWarp = 10, kConvertWarp = 12;
-// Threads of a block, and registers per thread after the split between the softmax warps,
-// warps 8-11 and (int8) warps 12-15: together what the block was launched with.
+// Threads of a block.  bf16: the softmax warps (a row's 128 scores in registers) and the others
+// split the registers that the block was launched with; int8: everyone keeps 128.
 template <bool kQuant>
 struct Roles {
   static constexpr int kThreads = kQuant ? 512 : 384;
-  static constexpr int kSoftmaxRegs = kQuant ? 192 : 216, kOtherRegs = kQuant ? 64 : 72;
-  static constexpr int kConvertRegs = 64;
-  static constexpr int kLaunchRegs = kQuant ? 128 : 168;
-  static_assert(256 * kSoftmaxRegs + 128 * kOtherRegs + (kQuant ? 128 * kConvertRegs : 0) <=
-                    kThreads * kLaunchRegs,
-                "register split");
+  static constexpr int kSoftmaxRegs = 216, kOtherRegs = 72;
+  static_assert(256 * kSoftmaxRegs + 128 * kOtherRegs <= 384 * 168, "register split");
 };
-constexpr int kStageBytes = 4096;     // per softmax warp: 128 bytes of each of its 32 rows
 constexpr int kHalfBytes = kTile * 128;       // 64 channels of 128 rows
 constexpr int kTileBytes = 2 * kHalfBytes;
 // int8: codes of a tile as they come, and behind a K tile's the chunk's K and V scales
-constexpr int kRawSlots = 3;
 constexpr int kRawCodes = kTile * 128;
 constexpr int kRawBytes = kRawCodes + 2 * kTile * 4;
 constexpr int kScaleSlots = 4;
@@ -248,11 +247,14 @@ struct Walk {
 // Shared memory of a block: the Q tiles, the ring, the softmax warps' way out, the control
 // words.  kTiles: Q tiles of the batch's units; with one, the other's room is a ring tile
 // more (memory bound there: two V tiles are held by the streams, the rest is in flight).
-// int8: the ring holds widened tiles (two or three: the codes behind them, not it, are what is
-// in flight).
+// int8: the ring holds three widened tiles (so that widening V of a chunk does not wait for
+// the products of the chunk before); the raw tiles behind it are what is in flight.
 template <int kTiles, bool kQuant>
 struct Shared {
-  static constexpr int kSlots = kQuant ? 4 - kTiles : 6 - kTiles;
+  static constexpr int kSlots = kQuant ? 3 : 6 - kTiles;
+  static constexpr int kRawSlots = kTiles == 2 ? 2 : 4;
+  static constexpr int kLinePieces = kQuant ? 4 : 8;  // 16-byte pieces of a row on the way out
+  static constexpr int kStageBytes = 32 * 16 * kLinePieces;  // per softmax warp
   static constexpr int kQ = 0;
   static constexpr int kRing = kTiles * kTileBytes;
   static constexpr int kRaw = kRing + kSlots * kTileBytes;
@@ -261,7 +263,10 @@ struct Shared {
   static constexpr int kEnd = kStage + kSoftmaxThreads / 32 * kStageBytes;
   struct Control {
     uint64_t full[kSlots], empty[kSlots], raw_full[kRawSlots], raw_empty[kRawSlots];
-    uint64_t q_full, q_empty, s_full[2], p_half[2], p_ready[2], o_full[2], v_last, drained;
+    uint64_t q_full, q_empty, o_full[2], v_last, drained;
+    // bf16: a stream's scores, the first half of its weights, all of them; int8: [stream][half
+    // of the chunk], and each product's end
+    uint64_t s_full[4], p_half[2], p_ready[4], pv_done[2];
     Walk walk[kSoftmaxThreads / 32];  // of the softmax warps
     Piece piece[kSoftmaxThreads / 32];
     float join[2][kTile];  // one number a row, from stream to stream
@@ -291,10 +296,11 @@ __global__ void __launch_bounds__(Roles<kQuant>::kThreads, 1)
   using Sh = Shared<kTiles, kQuant>;
   using Ro = Roles<kQuant>;
   constexpr int kThreads = Ro::kThreads;
-  constexpr int kSlots = Sh::kSlots;
+  constexpr int kSlots = Sh::kSlots, kRawSlots = Sh::kRawSlots;
   extern __shared__ unsigned char smem_raw[];
-  unsigned char* smem = reinterpret_cast<unsigned char*>(
-      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  // (rounded up by an offset, not by way of an integer: the compiler then still knows that it
+  // is shared memory, and the generic accesses it would use otherwise took four times as long)
+  unsigned char* smem = smem_raw + (-smem_addr(smem_raw) & 1023u);
   const uint32_t base_addr = smem_addr(smem);
   typename Sh::Control& ctl = *reinterpret_cast<typename Sh::Control*>(smem + Sh::kEnd);
   volatile int* abort_flag = &ctl.abort;
@@ -315,11 +321,14 @@ __global__ void __launch_bounds__(Roles<kQuant>::kThreads, 1)
     }
     mbar_init(&ctl.q_full, 1);
     mbar_init(&ctl.q_empty, 1);
-    for (int s = 0; s < 2; ++s) {
+    for (int s = 0; s < 4; ++s) {
       mbar_init(&ctl.s_full[s], 1);
-      mbar_init(&ctl.p_half[s], 4);
       mbar_init(&ctl.p_ready[s], 4);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&ctl.p_half[s], 4);
       mbar_init(&ctl.o_full[s], 1);
+      mbar_init(&ctl.pv_done[s], 1);
     }
     mbar_init(&ctl.v_last, 1);
     mbar_init(&ctl.drained, 1);
@@ -369,7 +378,7 @@ __global__ void __launch_bounds__(Roles<kQuant>::kThreads, 1)
 
   if (warp < kTmaWarp) {
     // ======================= softmax ===================================================
-    umma::registers_up<Ro::kSoftmaxRegs>();
+    if constexpr (!kQuant) umma::registers_up<Ro::kSoftmaxRegs>();
     const int s = warp >> 2, r = tid & (kTile - 1);
     const uint32_t lane_base = static_cast<uint32_t>(warp & 3) << 21;  // lane 32 (warp % 4)
     const uint32_t sc = s_col(s) + lane_base, oc = o_col(s) + lane_base;
@@ -380,6 +389,20 @@ __global__ void __launch_bounds__(Roles<kQuant>::kThreads, 1)
     // (after a wait that gave up, the pieces that are left only meet the barriers of the
     // softmax warps, so that none of them waits there for good)
     bool ok = true;
+    // What the warp's rows see of a chunk that reaches the drafted positions: four words of 32
+    // positions a row, in shared memory (one loop, kept rolled).
+    uint32_t* seen_s = reinterpret_cast<uint32_t*>(smem + Sh::kStage + warp * Sh::kStageBytes);
+    auto look = [&](const volatile Piece& vp, bool two, int c) {
+      const int row = (vp.pair * 2 + (two ? s : 0)) * kTile + r;
+      const int q_len = vp.q_len, n = vp.n;
+      const bool live = row < q_len * G;
+      const uint32_t* mask =
+          prm.tree_mask + (static_cast<int64_t>(vp.q_begin) + (live ? row >> gs : 0)) * words;
+#pragma unroll 1
+      for (int i = 0; i < 4; ++i)
+        seen_s[4 * lane + i] = live ? visible(c * kTile + 32 * i, n - q_len, n, mask, words) : 0u;
+      __syncwarp();
+    };
     // A thread's registers hold a row of scores, so the walk and the piece stay in shared
     // memory: `volatile` has them read again where they are needed.
     const volatile Piece& vp = ctl.piece[warp];
@@ -409,140 +432,172 @@ __global__ void __launch_bounds__(Roles<kQuant>::kThreads, 1)
         lq[q] = 0.f;
       }
       for (int k = 0; k < mine && ok; ++k) {
-        ok = mbar_wait_bounded(&ctl.s_full[s], step & 1u);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        ++step;
-        umma::fence_after();
         if constexpr (kQuant) {
-          // A thread holds 32 columns of four rows here (16 i + t / 4 + 8 j), so that a scale read
-          // from shared memory serves four rows: with a row per thread every scale went to
-          // every warp by itself, 2048 shared-memory cycles a chunk.
+          // Half a chunk at a time, each half with its own scores in tensor memory: while one
+          // half's weights are made, the tensor cores work on the other's.  A thread holds
+          // columns of four rows (8 q + t / 4), so that a scale read from shared memory
+          // serves four rows: with a row per thread every scale went to every warp by itself,
+          // 2048 shared-memory cycles a chunk.
           const float2* scales = reinterpret_cast<const float2*>(smem + Sh::kScales) +
                                  (chunk0 + (two ? k : 2 * k + s)) % kScaleSlots * kTile + (lane & 3);
-          // (the chunk's K scales, then its V scales; written before the scores' K tile was
-          // handed on, so before these scores)
-          uint32_t xr[2][64];
-          umma::ld_frag64(sc, xr[0]);
-          umma::ld_frag64(sc + (16u << 16), xr[1]);
-          umma::wait_ld(xr[0]);
-          umma::wait_ld(xr[1]);
-          auto value = [&](int h, int i) -> float { return __uint_as_float(xr[h][i]); };
+          // (the chunk's K scales times the softmax scale, then its V scales; written before the
+          // scores' K tile was handed on, so before these scores)
+          constexpr uint32_t kLower = 16u << 16;  // the warp's lanes 16-31
+          const bool tail = k >= plain;           // drafted or missing positions
+#pragma unroll 1
+          for (int half = 0; half < 2; ++half) {
+            ok = mbar_wait_bounded(&ctl.s_full[2 * s + half], step & 1u);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            umma::fence_after();
+            const uint32_t at = sc + 64 * half;
+            const float2* f_of = scales + 32 * half;
+            uint32_t v[2][2][16];  // [32 columns][16 rows]
 #pragma unroll
-          for (int c = 0; c < 16; ++c) {  // columns 8 c + 2 (t % 4), + 1
-            const float2 f = scales[4 * c];
+            for (int i = 0; i < 2; ++i) {
+              umma::ld_frag16(at + 32 * i, v[i][0]);
+              umma::ld_frag16(at + 32 * i + kLower, v[i][1]);
+            }
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
+            for (int i = 0; i < 2; ++i) {
+              umma::wait_ld(v[i][0]);
+              umma::wait_ld(v[i][1]);
+            }
+            // columns 32 i + 8 c + 2 (t % 4), + 1 of row q
+            auto pair_of = [&](int i, int c, int q) -> uint64_t {
+              const uint32_t(&r)[16] = v[i][q >> 1];
+              const int e = 4 * c + 2 * (q & 1);
+              return umma::pair(__uint_as_float(r[e]), __uint_as_float(r[e + 1]));
+            };
+            auto set_pair = [&](int i, int c, int q, float lo, float hi) {
+              uint32_t(&r)[16] = v[i][q >> 1];
+              const int e = 4 * c + 2 * (q & 1);
+              r[e] = __float_as_uint(lo);
+              r[e + 1] = __float_as_uint(hi);
+            };
 #pragma unroll
-              for (int j = 0; j < 2; ++j) {
-                float lo, hi;
-                umma::unpair(umma::mul2(umma::pair(value(h, 4 * c + 2 * j), value(h, 4 * c + 2 * j + 1)),
-                                        umma::pair(f.x, f.y)),
-                             lo, hi);
-                xr[h][4 * c + 2 * j] = __float_as_uint(lo);
-                xr[h][4 * c + 2 * j + 1] = __float_as_uint(hi);
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+              for (int c = 0; c < 4; ++c) {
+                const float2 f = f_of[16 * i + 4 * c];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                  float lo, hi;
+                  umma::unpair(umma::mul2(pair_of(i, c, q), umma::pair(f.x, f.y)), lo, hi);
+                  set_pair(i, c, q, lo, hi);
+                }
               }
-          }
-          if (k >= plain) {  // drafted or missing positions
-            const int q_len = vp.q_len, n = vp.n;
-            const int p0 = (vp.c0 + (two ? k : 2 * k + s)) * kTile;
+            if (tail) {
+              if (half == 0) look(vp, two, vp.c0 + (two ? k : 2 * k + s));
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
+              for (int q = 0; q < 4; ++q) {
+                const uint2 seen = reinterpret_cast<const uint2*>(seen_s)[2 * (8 * q + (lane >> 2)) + half];
 #pragma unroll
-              for (int j = 0; j < 2; ++j) {
-                const int row = (vp.pair * 2 + (two ? s : 0)) * kTile + (warp & 3) * 32 + 16 * h + 8 * j +
-                                (lane >> 2);
-                const bool live = row < q_len * G;
-                const uint32_t* mask =
-                    prm.tree_mask + (static_cast<int64_t>(vp.q_begin) + (live ? row >> gs : 0)) * words;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                  const uint32_t bits =
-                      live ? visible(p0 + 32 * i, n - q_len, n, mask, words) >> (2 * (lane & 3)) : 0u;
+                for (int i = 0; i < 2; ++i) {
+                  const uint32_t bits = (i == 0 ? seen.x : seen.y) >> (2 * (lane & 3));
 #pragma unroll
                   for (int c = 0; c < 4; ++c) {
-                    uint32_t& lo = xr[h][16 * i + 4 * c + 2 * j];
-                    uint32_t& hi = xr[h][16 * i + 4 * c + 2 * j + 1];
-                    lo = (bits >> (8 * c)) & 1u ? lo : 0xff800000u;  // -inf
-                    hi = (bits >> (8 * c + 1)) & 1u ? hi : 0xff800000u;
+                    float lo, hi;
+                    umma::unpair(pair_of(i, c, q), lo, hi);
+                    set_pair(i, c, q, (bits >> (8 * c)) & 1u ? lo : -CUDART_INF_F,
+                             (bits >> (8 * c + 1)) & 1u ? hi : -CUDART_INF_F);
                   }
                 }
               }
-            __syncwarp();
-          }
-          float alpha[4];
-          bool moved = false;
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const int h = q >> 1, j = q & 1;
-            float top = fmaxf(value(h, 2 * j), value(h, 2 * j + 1));
-#pragma unroll
-            for (int c = 1; c < 16; ++c)
-              top = umma::max3(top, value(h, 4 * c + 2 * j), value(h, 4 * c + 2 * j + 1));
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-            const float m_new = top * scale;
-            alpha[q] = 1.f;
-            if (m_new > mq[q] + mma::kMaxSlack) {
-              alpha[q] = mq[q] == -CUDART_INF_F ? 0.f : mma::fast_exp2(mq[q] - m_new);
-              mq[q] = m_new;
-              lq[q] *= alpha[q];
-              moved = true;
+              __syncwarp();
             }
-          }
-          __syncwarp();
-          if (k > 0 && __any_sync(0xffffffffu, moved)) {
+            float alpha[4];
+            bool moved = false;
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
+            for (int q = 0; q < 4; ++q) {
+              float top[2] = {-CUDART_INF_F, -CUDART_INF_F};
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
+              for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                  float lo, hi;
+                  umma::unpair(pair_of(i, c, q), lo, hi);
+                  top[i] = umma::max3(top[i], lo, hi);
+                }
+              float m_new = fmaxf(top[0], top[1]);
+              m_new = fmaxf(m_new, __shfl_xor_sync(0xffffffffu, m_new, 1));
+              m_new = fmaxf(m_new, __shfl_xor_sync(0xffffffffu, m_new, 2));
+              alpha[q] = 1.f;
+              if (m_new > mq[q] + mma::kMaxSlack) {
+                alpha[q] = mq[q] == -CUDART_INF_F ? 0.f : mma::fast_exp2(mq[q] - m_new);
+                mq[q] = m_new;
+                lq[q] *= alpha[q];
+                moved = true;
+              }
+            }
+            __syncwarp();
+            // The accumulator follows a moved reference, once the last product is over (before
+            // the piece's first there is none).
+            if (k + half > 0 && __any_sync(0xffffffffu, moved)) {
+              ok = mbar_wait_bounded(&ctl.pv_done[s], (2 * step + half - 1) & 1u);
+              ok = __all_sync(0xffffffffu, ok);
+              if (!ok) break;
+              umma::fence_after();
+#pragma unroll 1
+              for (int i = 0; i < 8; ++i) {
                 uint32_t o[16];
-                umma::ld_frag16(oc + 32 * i + (h ? 16u << 16 : 0u), o);
+                const uint32_t col = oc + 32 * (i & 3) + (i >> 2 ? kLower : 0u);
+                umma::ld_frag16(col, o);
                 umma::wait_ld(o);
 #pragma unroll
                 for (int u = 0; u < 16; ++u)
-                  o[u] = __float_as_uint(__uint_as_float(o[u]) * alpha[2 * h + ((u >> 1) & 1)]);
-                umma::st_frag16(oc + 32 * i + (h ? 16u << 16 : 0u), o);
-              }
-          }
-          const uint64_t scale2 = umma::pair(scale, scale);
-          uint64_t sum[4] = {0, 0, 0, 0};  // pairs of +0
-#pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            uint32_t w[2][16];
-#pragma unroll
-            for (int c = 0; c < 8; ++c) {
-              const float2 f = scales[kTile / 2 + 4 * (8 * half + c)];
-#pragma unroll
-              for (int q = 0; q < 4; ++q) {
-                const int h = q >> 1, j = q & 1, i = 4 * (8 * half + c) + 2 * j;
-                const float ref = mq[q] == -CUDART_INF_F ? 0.f : mq[q];
-                float lo, hi;
-                umma::unpair(umma::fma2(umma::pair(value(h, i), value(h, i + 1)), scale2,
-                                        umma::pair(-ref, -ref)),
-                             lo, hi);
-                lo = mma::fast_exp2(lo);
-                hi = mma::fast_exp2(hi);
-                sum[q] = umma::add2(sum[q], umma::pair(lo, hi));
-                // the V scale goes with the weight
-                umma::unpair(umma::mul2(umma::pair(lo, hi), umma::pair(f.x, f.y)), lo, hi);
-                w[h][2 * c + j] = mma::pack_bf16(lo, hi);
+                  o[u] = __float_as_uint(__uint_as_float(o[u]) *
+                                         ((u >> 1) & 1 ? (i >> 2 ? alpha[3] : alpha[1])
+                                                       : (i >> 2 ? alpha[2] : alpha[0])));
+                umma::st_frag16(col, o);
               }
             }
-            umma::st_pairs16(sc + 32 * half, w[0]);
-            umma::st_pairs16(sc + 32 * half + (16u << 16), w[1]);
+            uint64_t ref2[4], sum[4] = {0, 0, 0, 0};  // pairs of +0
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const float ref = mq[q] == -CUDART_INF_F ? 0.f : mq[q];
+              ref2[q] = umma::pair(-ref, -ref);
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              uint32_t w[2][8];
+#pragma unroll
+              for (int c = 0; c < 4; ++c) {
+                const float2 g = f_of[kTile / 2 + 16 * i + 4 * c];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                  float lo, hi;
+                  umma::unpair(umma::add2(pair_of(i, c, q), ref2[q]), lo, hi);
+                  lo = mma::fast_exp2(lo);
+                  hi = mma::fast_exp2(hi);
+                  sum[q] = umma::add2(sum[q], umma::pair(lo, hi));
+                  // the V scale goes with the weight
+                  umma::unpair(umma::mul2(umma::pair(lo, hi), umma::pair(g.x, g.y)), lo, hi);
+                  w[q >> 1][2 * c + (q & 1)] = mma::pack_bf16(lo, hi);
+                }
+              }
+              umma::st_pairs8(at + 16 * i, w[0]);
+              umma::st_pairs8(at + 16 * i + kLower, w[1]);
+            }
             umma::wait_st();
             umma::fence_before();
             __syncwarp();
-            if (lane == 0) mma::mbar_arrive(half == 0 ? &ctl.p_half[s] : &ctl.p_ready[s]);
-          }
+            if (lane == 0) mma::mbar_arrive(&ctl.p_ready[2 * s + half]);
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            float lo, hi;
-            umma::unpair(sum[q], lo, hi);
-            lq[q] += lo + hi;
+            for (int q = 0; q < 4; ++q) {
+              float lo, hi;
+              umma::unpair(sum[q], lo, hi);
+              lq[q] += lo + hi;
+            }
           }
+          if (!ok) break;
+          ++step;
         } else {
+          ok = mbar_wait_bounded(&ctl.s_full[s], step & 1u);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          ++step;
+          umma::fence_after();
           float x[kTile];
 #pragma unroll
           for (int i = 0; i < 4; ++i)
@@ -624,12 +679,12 @@ __global__ void __launch_bounds__(Roles<kQuant>::kThreads, 1)
         }
       }
       if constexpr (kQuant) {  // the four rows' numbers to the threads that own the rows below
-        float2* box = reinterpret_cast<float2*>(smem + Sh::kStage + warp * kStageBytes);
+        float2* box = reinterpret_cast<float2*>(smem + Sh::kStage + warp * Sh::kStageBytes);
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           lq[q] += __shfl_xor_sync(0xffffffffu, lq[q], 1);
           lq[q] += __shfl_xor_sync(0xffffffffu, lq[q], 2);
-          if ((lane & 3) == 0) box[16 * (q >> 1) + 8 * (q & 1) + (lane >> 2)] = make_float2(mq[q], lq[q]);
+          if ((lane & 3) == 0) box[8 * q + (lane >> 2)] = make_float2(mq[q], lq[q]);
         }
         __syncwarp();
         m_ref = box[lane].x;
@@ -679,13 +734,35 @@ __global__ void __launch_bounds__(Roles<kQuant>::kThreads, 1)
       const float inv = direct ? (l > 0.f || l != l ? 1.f / l : 0.f) : 1.f;
       const uint32_t other = o_col(1 - s) + lane_base;
       const bool write = live && ok;
-      // Rows leave through shared memory, 128 bytes of each of the warp's 32 at a time, so
-      // that a store covers whole lines of four rows: storing a row per thread took 32 lines
-      // a store and held up every other warp's shared-memory work for 8K cycles.  (16-byte
-      // pieces are XORed with the row: no bank conflicts either way.)
-      uint4* stage = reinterpret_cast<uint4*>(smem + Sh::kStage + warp * kStageBytes);
+      // Rows leave through shared memory, a line (128 bytes, int8: 64) of each of the warp's 32
+      // at a time, so that a store covers lines of several rows: storing a row per thread took
+      // 32 lines a store and held up every other warp's shared-memory work for 8K cycles.
+      // (16-byte pieces are XORed with the row: few bank conflicts either way.)
+      constexpr int kLine = Sh::kLinePieces;
+      uint4* stage = reinterpret_cast<uint4*>(smem + Sh::kStage + warp * Sh::kStageBytes);
       const int row0 = (p.pair * 2 + (two ? s : 0)) * kTile + (warp & 3) * 32;
       const int live_rows = ok ? p.q_len * G - row0 : 0;  // of the warp's 32
+      auto put = [&](int piece, uint4 w) { stage[lane * kLine + (piece ^ (lane & (kLine - 1)))] = w; };
+      // the line at 16-byte piece `at` of every row
+      auto flush = [&](int at) {
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < kLine; ++i) {
+          const int rr = (32 / kLine) * i + lane / kLine, piece = lane & (kLine - 1);
+          if (rr < live_rows) {
+            const uint4 w = stage[rr * kLine + (piece ^ (rr & (kLine - 1)))];
+            const int q = (row0 + rr) >> gs;
+            const int64_t to = (static_cast<int64_t>(p.q_begin) + q) * prm.num_q_heads + p.kvh * G +
+                               (row0 + rr - q * G);
+            if (direct) {
+              static_cast<uint4*>(prm.out)[to * 16 + at + piece] = w;
+            } else {
+              reinterpret_cast<uint4*>(prm.acc_out)[(to * S + p.slot) * 32 + at + piece] = w;
+            }
+          }
+        }
+        __syncwarp();
+      };
       for (int c = col0; c < col1; c += 32) {
         float y[32];
         uint32_t o[32];
@@ -705,39 +782,22 @@ __global__ void __launch_bounds__(Roles<kQuant>::kThreads, 1)
           __syncwarp();
         }
         if (direct) {
-          const int first = (c & 32) / 8;  // bf16: two steps of 32 channels fill the 128 bytes
+          const int first = c / 8 & (kLine - 1);  // bf16: 32 channels are four pieces
 #pragma unroll
           for (int j = 0; j < 4; ++j)
-            stage[lane * 8 + ((first + j) ^ (lane & 7))] =
-                make_uint4(mma::pack_bf16(y[8 * j] * inv, y[8 * j + 1] * inv),
-                           mma::pack_bf16(y[8 * j + 2] * inv, y[8 * j + 3] * inv),
-                           mma::pack_bf16(y[8 * j + 4] * inv, y[8 * j + 5] * inv),
-                           mma::pack_bf16(y[8 * j + 6] * inv, y[8 * j + 7] * inv));
-          if (first == 0) continue;
-        } else {
+            put(first + j, make_uint4(mma::pack_bf16(y[8 * j] * inv, y[8 * j + 1] * inv),
+                                      mma::pack_bf16(y[8 * j + 2] * inv, y[8 * j + 3] * inv),
+                                      mma::pack_bf16(y[8 * j + 4] * inv, y[8 * j + 5] * inv),
+                                      mma::pack_bf16(y[8 * j + 6] * inv, y[8 * j + 7] * inv)));
+          if (first + 4 == kLine) flush(c / 8 + 4 - kLine);
+        } else {  // fp32: eight pieces
 #pragma unroll
-          for (int j = 0; j < 8; ++j)
-            stage[lane * 8 + (j ^ (lane & 7))] =
-                make_uint4(__float_as_uint(y[4 * j]), __float_as_uint(y[4 * j + 1]),
-                           __float_as_uint(y[4 * j + 2]), __float_as_uint(y[4 * j + 3]));
-        }
-        __syncwarp();
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int rr = 4 * i + (lane >> 3), piece = lane & 7;
-          if (rr < live_rows) {
-            const uint4 w = stage[rr * 8 + (piece ^ (rr & 7))];
-            const int q = (row0 + rr) >> gs;
-            const int64_t at = (static_cast<int64_t>(p.q_begin) + q) * prm.num_q_heads + p.kvh * G +
-                               (row0 + rr - q * G);
-            if (direct) {
-              static_cast<uint4*>(prm.out)[at * 16 + (c & 64) / 8 + piece] = w;
-            } else {
-              reinterpret_cast<uint4*>(prm.acc_out)[(at * S + p.slot) * 32 + c / 4 + piece] = w;
-            }
+          for (int j = 0; j < 8; ++j) {
+            put(j & (kLine - 1), make_uint4(__float_as_uint(y[4 * j]), __float_as_uint(y[4 * j + 1]),
+                                            __float_as_uint(y[4 * j + 2]), __float_as_uint(y[4 * j + 3])));
+            if ((j & (kLine - 1)) == kLine - 1) flush(c / 4 + j + 1 - kLine);
           }
         }
-        __syncwarp();
       }
       if (write && (two || s == 0)) {
         const float m_nat = m_ref * 0.69314718055994530942f;  // -inf stays -inf
@@ -758,7 +818,6 @@ __global__ void __launch_bounds__(Roles<kQuant>::kThreads, 1)
     }
   } else if (kQuant && warp >= kConvertWarp) {
     // ======================= int8: codes to bf16 ============================================
-    umma::registers_down<Ro::kConvertRegs>();
     Piece p;
     const int t = tid - kConvertWarp * 32;  // 0..127
     int it = 0;
@@ -779,12 +838,12 @@ __global__ void __launch_bounds__(Roles<kQuant>::kThreads, 1)
             // V scales of positions past the end may hold anything, and 0 * NaN is NaN
             const float* in = reinterpret_cast<const float*>(src + kRawCodes);
             float* out = reinterpret_cast<float*>(smem + Sh::kScales) + chunk % kScaleSlots * 2 * kTile;
-            out[t] = in[t];
+            out[t] = in[t] * prm.q_scale;
             out[kTile + t] = c * kTile + t < p.n ? in[kTile + t] : 0.f;
           }
           // a warp turns 8 rows x 4 pieces of 16 codes at a time: every row's swizzle puts its
           // piece in another bank group, for the loads and for both stores
-#pragma unroll
+#pragma unroll 1
           for (int u0 = 0; u0 < 8; u0 += 4) {
             // (four pieces are loaded before the first store: the compiler cannot know that the
             // two tiles do not overlap)
@@ -819,7 +878,7 @@ __global__ void __launch_bounds__(Roles<kQuant>::kThreads, 1)
     }
     if (!ok && lane == 0) give_up();
   } else {
-    umma::registers_down<Ro::kOtherRegs>();
+    if constexpr (!kQuant) umma::registers_down<Ro::kOtherRegs>();
     Piece p;
     if (warp == kTmaWarp) {
       // ======================= TMA ======================================================
@@ -930,7 +989,8 @@ __global__ void __launch_bounds__(Roles<kQuant>::kThreads, 1)
     } else if (warp == kMmaWarp) {
       // ======================= MMA issue ==================================================
       if (umma::elect()) {
-      constexpr uint32_t kScores = umma::instruction(kTile, kTile, false);
+      constexpr int kStep = kQuant ? kTile / 2 : kTile;  // tokens of one set of scores
+      constexpr uint32_t kScores = umma::instruction(kTile, kStep, false);
       constexpr uint32_t kOutput = umma::instruction(kTile, kTile, true);
       int it0 = 0;  // ring tiles of the pieces before
       uint32_t piece = 0, used0 = 0, used1 = 0;  // products of each stream
@@ -941,17 +1001,18 @@ __global__ void __launch_bounds__(Roles<kQuant>::kThreads, 1)
       while (ok && more) {
         const bool two = two_tiles(p);
         const int chunks = p.c1 - p.c0;
-        auto scores = [&](int s, int c) {  // S_s = Q_tile K_c^T; the tile and Q are done with
+        // S_s = Q_tile K_c^T (int8: tokens 64 half .. of it); then the tile and Q are done with
+        auto scores = [&](int s, int c, int half) {
           const uint32_t q = umma::operand(base_addr + Sh::kQ + (two ? s : 0) * kTileBytes, 16);
-          const uint32_t k = umma::operand(tile_addr(it0 + 2 * c), 16);
-          const uint32_t d = s_col(s);
+          const uint32_t k = umma::operand(tile_addr(it0 + 2 * c) + half * kStep * 128, 16);
+          const uint32_t d = s_col(s) + half * kStep;
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
             const uint32_t off = ((j >> 2) * kHalfBytes + (j & 3) * 32) >> 4;
             umma::mma_ss(d, q + off, k + off, kScores, j > 0);
           }
-          umma::commit(&ctl.s_full[s]);
-          if (!two || s == 1) {
+          umma::commit(&ctl.s_full[kQuant ? 2 * s + half : s]);
+          if ((!two || s == 1) && (!kQuant || half == 1)) {
             umma::commit(&ctl.empty[(it0 + 2 * c) % kSlots]);
             if (c == chunks - 1) umma::commit(&ctl.q_empty);
           }
@@ -963,7 +1024,7 @@ __global__ void __launch_bounds__(Roles<kQuant>::kThreads, 1)
           const int c = two ? 0 : s;
           if (c >= chunks) break;
           if (s == 0 || !two) ok = wait_tile(it0 + 2 * c);
-          if (ok) scores(s, c);
+          for (int half = 0; half < (kQuant ? 2 : 1) && ok; ++half) scores(s, c, half);
         }
         more = walk.next(prm, P, p);  // (ahead: its look-ups wait for memory)
         for (int c = 0; c < chunks && ok; ++c) {
@@ -971,7 +1032,36 @@ __global__ void __launch_bounds__(Roles<kQuant>::kThreads, 1)
           const uint32_t v = umma::operand(tile_addr(it0 + 2 * c + 1), kHalfBytes);
           const bool first = two ? c == 0 : c < 2;  // of the piece in this stream
           const int next = two ? c + 1 : c + 2;
-          for (int s = s_begin; s < s_end && ok; ++s) {
+          if constexpr (kQuant) {
+            for (int i = 0; i < 2 * (s_end - s_begin) && ok; ++i) {  // stream by stream, half by half
+              const int half = two ? i >> 1 : i, s = two ? i & 1 : s_begin;
+              const bool last = i == 2 * (s_end - s_begin) - 1;
+              ok = wait(&ctl.p_ready[2 * s + half], s == 0 ? used0 : used1);
+              if (ok && i == 0) ok = wait_tile(it0 + 2 * c + 1);
+              if (!ok) break;
+              if (half == 1) (s == 0 ? used0 : used1) += 1;
+              const uint32_t d = o_col(s), a = s_col(s) + half * kStep;
+              const uint32_t v0 = v + (half * kStep * 128 >> 4);
+              umma::fence_after();
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                umma::mma_ts(d, a + 8 * j, v0 + j * (2048 >> 4), kOutput, !first || half > 0 || j > 0);
+              umma::commit(&ctl.pv_done[s]);
+              if (last) umma::commit(&ctl.empty[(it0 + 2 * c + 1) % kSlots]);
+              if (next >= chunks) {
+                if (half == 1) umma::commit(&ctl.o_full[s]);
+              } else if (two) {
+                if (i == 0) ok = wait_tile(it0 + 2 * next);
+                if (ok) scores(s, next, half);
+              } else if (last) {
+                // (one tile: two chunks ahead, whose K takes the ring tile that V just left)
+                ok = wait_tile(it0 + 2 * next);
+                if (ok) scores(s, next, 0);
+                if (ok) scores(s, next, 1);
+              }
+            }
+          }
+          for (int s = s_begin; !kQuant && s < s_end && ok; ++s) {
             const uint32_t use = s == 0 ? used0++ : used1++;
             ok = wait(&ctl.p_half[s], use);
             if (ok && s == s_begin) ok = wait_tile(it0 + 2 * c + 1);
@@ -992,7 +1082,7 @@ __global__ void __launch_bounds__(Roles<kQuant>::kThreads, 1)
             if (next >= chunks) umma::commit(&ctl.o_full[s]);
             if (next < chunks) {
               if (s == s_begin) ok = wait_tile(it0 + 2 * next);
-              if (ok) scores(s, next);
+              if (ok) scores(s, next, 0);
             }
           }
         }
