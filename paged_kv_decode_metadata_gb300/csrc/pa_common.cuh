@@ -24,8 +24,6 @@ enum : unsigned int {
   kErrSlotOutOfRange = 1u << 2,     // token slot outside full_to_swa_mapping / a table row
   kErrWaitTimeout = 1u << 3,        // an mbarrier wait gave up
   kErrSeqLenOutOfRange = 1u << 4,   // cache_seqlens entry < 0 or beyond the page table
-  kErrKeptOutOfRange = 1u << 5,     // kept position, or the position it moves to
-  kErrTreeParent = 1u << 6,         // parent of a drafted node that is not an earlier node
 };
 
 // ~2 s: far longer than any copy this library issues takes on a healthy GPU.

@@ -8,6 +8,10 @@
 
 namespace pa {
 
+// Error-word bits of the cache operators, beside those of pa_common.cuh (include/pa.h).
+constexpr unsigned int kErrKeptOutOfRange = 1u << 5;  // kept position, or the position it moves to
+constexpr unsigned int kErrTreeParent = 1u << 6;      // parent of a drafted node, not an earlier node
+
 struct MetadataParams {
   const void* req_pool_indices;  // int64 or int32 (idx64)
   const void* seq_lens;          // int64 or int32 (idx64)
