@@ -148,6 +148,28 @@ def test_rope_append(tokens, hq, hkv, page, kv, rot, inter, amp, start, in_place
         assert same_bits(dev, qkv)                       # inputs are only read
 
 
+@pytest.mark.parametrize("power", [-125, -110, -61, 100])
+def test_rope_int8_codes_of_tiny_and_large_rows(power):
+    """1 / scale of the smallest rows does not fit fp32."""
+    c = Cache([3], 2, 16, "int8", 6)
+    g = torch.Generator().manual_seed(9)
+    x = (torch.randn((3, 2, 128), generator=g).double() * 2.0 ** power).to(torch.bfloat16)
+    slots = int(c.table[0, 0]) * 16 + torch.arange(3)
+    d = x.cuda()
+    B.pa_rope_append(q=d, k=d, v=d, positions=torch.zeros(3, dtype=torch.int64).cuda(), slots=slots.cuda(),
+                     inv_freq=B.pa_rope_frequencies(128).cuda(), q_out=torch.empty_like(d), k_cache=c.d_k,
+                     v_cache=c.d_v, k_scale=c.d_ks, v_scale=c.d_vs)
+    page = int(c.table[0, 0])
+    for pool, scales in ((c.d_k, c.d_ks), (c.d_v, c.d_vs)):   # (position 0 turns nothing)
+        code = pool.cpu()[page, :, :3].double().transpose(0, 1)
+        scale = scales.cpu()[page, :, :3].double().T[..., None]
+        top = x.double().abs().amax(-1, keepdim=True)
+        # one fp32 division, subnormal results within half of 2^-149
+        assert bool(((scale - top / 127).abs() <= 2.0 ** -23 * top / 127 + 2.0 ** -150).all())
+        # half a step, and 1 / scale and the product rounded (127 * 2^-22 steps)
+        assert bool(((code * scale - x.double()).abs() <= scale * (0.5 + 127 * 2.0 ** -22)).all())
+
+
 def test_rope_zero_row_and_slot_past_the_pool():
     c = Cache([20], 2, 16, "int8", 5)
     x = torch.zeros((2, 2, 128), dtype=torch.bfloat16, device="cuda")
