@@ -521,8 +521,8 @@ PA_API pa_status pa_rope_frequencies(double* inv_freq, int32_t rotary_dim, doubl
  *   inv_freq   [rotary_dim / 2] double, device memory
  *   q_out      bf16, token stride q_out_stride; may be q itself with q's stride (in place)
  *   k_cache, v_cache, k_scale, v_scale   the pools of pa_decode_splitk.  int8: scale = the
- *              row's largest magnitude / 127, codes = round-to-even(x / scale) (an all-zero
- *              row: scale 0); rows must be finite.
+ *              row's largest magnitude / 127, codes = round-to-even(x * (1 / scale)) in fp32 (an
+ *              all-zero row: scale 0); rows must be finite.
  * Two tokens with the same slot leave that row unspecified.  A slot at or past num_pages *
  * page_size is not written and sets PA_DEVERR_SLOT_OUT_OF_RANGE.  The kernel reads nothing
  * before it has waited on the previous grid and never triggers its dependents early, so
@@ -631,7 +631,8 @@ PA_API size_t pa_tree_workspace_bytes(int32_t bs, int32_t total_q, int32_t max_q
  *   weights[p, h, r] += sum over the query heads of h of exp(sm_scale q . K_j - lse)
  * with the step's q [bs, num_q_heads, 128] bf16 and lse [bs, num_q_heads] fp32 (a head with
  * lse = -inf adds nothing).  weights [num_pages, num_kv_heads, page_size] fp32, kept with
- * the pools; pools, tables and limits as for pa_decode_splitk (k_scale: int8 only).  Rows of
+ * the pools; pools, tables and limits as for pa_decode_splitk (k_scale: int8 only), and
+ * max_seq_pages * page_size <= 2^30.  Rows of
  * other positions are not touched.  A page that several requests share gets all of their
  * weights, in an order that is not fixed; otherwise the result is the same every time.
  */
@@ -647,7 +648,7 @@ PA_API pa_status pa_accumulate_weights(
  * and kv head h, position kept[b, h, i] (0 <= i < counts[b]) moves to position begin[b] + i
  * (begin NULL: 0) of the pages in dst_page_table: K and V rows, their scales and, where
  * `weights` is given, their accumulated weights.  new_seqlens[b] = begin[b] + counts[b]
- * (may be NULL; not cache_seqlens or counts).
+ * (may be NULL; not cache_seqlens, counts or begin).
  *   kept   [bs, kept_heads, kept_stride] int32, strictly ascending in i; kept_heads is
  *          num_kv_heads, or 1 for one list that all heads share (the accepted path of a tree)
  *   dst_page_table   page_table itself, the same pointer and stride: in place, which needs
@@ -658,7 +659,8 @@ PA_API pa_status pa_accumulate_weights(
  * position outside [0, cache_seqlens[b]), a target past dst_max_pages * page_size or, in
  * place, a kept position before its target is not moved and sets
  * PA_DEVERR_KEPT_OUT_OF_RANGE.  max_kept: the largest count; larger counts are cut to it.
- * Supported: head_dim 128; page_size 16, 32, 64, 128.
+ * Supported: head_dim 128; page_size 16, 32, 64, 128; max_seq_pages * page_size and max_kept
+ * <= 2^30.
  */
 PA_API pa_status pa_compact_cache(
     const int32_t* page_table, int64_t page_table_stride, const int32_t* cache_seqlens,
@@ -678,7 +680,8 @@ PA_API pa_status pa_compact_cache(
  * ascending order, then -1; new_seqlens [bs] int32 (out): min(n, budget) (not
  * cache_seqlens).  The rows then move as by pa_compact_cache with begin 0 (weights always
  * move too); every head keeps its own positions, so position i of the shrunk cache is a
- * different token from head to head.  1 <= budget, num_first + num_recent <= budget.
+ * different token from head to head.  1 <= budget, num_first + num_recent <= budget;
+ * max_seq_pages * page_size <= 2^30.
  */
 PA_API pa_status pa_evict(const int32_t* page_table, int64_t page_table_stride,
                           const int32_t* cache_seqlens, int32_t max_seq_pages, float* weights,

@@ -11,6 +11,7 @@
 namespace {
 
 constexpr int32_t kMaxTreeNodes = 256;
+constexpr int64_t kMaxPositions = int64_t{1} << 30;  // of a request: positions plus a block stay int32
 
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 bool page_size_ok(int32_t p) { return p == 16 || p == 32 || p == 64 || p == 128; }
@@ -349,6 +350,7 @@ pa_status pa_accumulate_weights(const void* q, const float* lse, const void* k_c
                                      num_kv_heads, head_dim, page_size, num_pages, max_seq_pages, 1);
   if (st != PA_OK || bs == 0) return st;
   if (!lse || !weights || !aligned(lse, 4) || !aligned(weights, 16)) return PA_ERR_INVALID;
+  if (static_cast<int64_t>(max_seq_pages) * page_size > kMaxPositions) return PA_ERR_UNSUPPORTED;
   pa::WeightsParams p = {};
   p.q = q;
   p.lse = lse;
@@ -393,6 +395,7 @@ pa_status compact_params(const int32_t* page_table, int64_t page_table_stride,
   if (static_cast<int64_t>(max_seq_pages) * page_size > INT32_MAX ||
       static_cast<int64_t>(dst_max_pages) * page_size > INT32_MAX)
     return PA_ERR_INVALID;
+  if (static_cast<int64_t>(max_seq_pages) * page_size > kMaxPositions) return PA_ERR_UNSUPPORTED;
   if (weights != nullptr && !aligned(weights, 4)) return PA_ERR_INVALID;
   *in_place = dst_page_table == page_table;
   if (*in_place && dst_page_table_stride != page_table_stride) return PA_ERR_INVALID;
@@ -441,6 +444,7 @@ pa_status pa_compact_cache(const int32_t* page_table, int64_t page_table_stride,
   if (st != PA_OK) return st;
   if (!counts || max_kept < 0 || kept_stride < max_kept) return PA_ERR_INVALID;
   if (kept_heads != 1 && kept_heads != num_kv_heads) return PA_ERR_INVALID;
+  if (max_kept > kMaxPositions) return PA_ERR_UNSUPPORTED;
   // the blocks read these while one of them writes new_seqlens
   if (new_seqlens != nullptr && (new_seqlens == cache_seqlens || new_seqlens == counts || new_seqlens == begin))
     return PA_ERR_INVALID;

@@ -128,6 +128,7 @@ WEIGHTS = dict(q=FAKE, lse=FAKE, k=FAKE, ks=None, kv=0, pt=FAKE, pts=16, cl=FAKE
     (dict(kv=1), B.PA_ERR_INVALID), (dict(hq=24), B.PA_ERR_UNSUPPORTED),
     (dict(d=64), B.PA_ERR_UNSUPPORTED), (dict(P=256), B.PA_ERR_UNSUPPORTED),
     (dict(msp=0), B.PA_ERR_INVALID),
+    (dict(msp=(1 << 24) + 1, pts=1 << 25), B.PA_ERR_UNSUPPORTED),   # positions past 2^30
 ])
 def test_weights_refusals(lib, over, status):
     assert _caller(lib.pa_accumulate_weights, WEIGHTS)(**over) == status
@@ -146,6 +147,9 @@ COMPACT = dict(pt=FAKE, pts=16, cl=FAKE, msp=16, kept=FAKE, heads=8, ks=100, cou
     (dict(dpts=17), B.PA_ERR_INVALID),                   # in place with another stride
     (dict(dpt=FAKE + 256, dmp=0), B.PA_ERR_INVALID), (dict(dpt=FAKE + 256, dmp=20), B.PA_ERR_INVALID),
     (dict(kv=1), B.PA_ERR_INVALID), (dict(P=20), B.PA_ERR_UNSUPPORTED), (dict(d=256), B.PA_ERR_UNSUPPORTED),
+    (dict(begin=FAKE + 128), B.PA_ERR_INVALID),          # new_seqlens
+    (dict(msp=(1 << 24) + 1, pts=1 << 25, dpts=1 << 25), B.PA_ERR_UNSUPPORTED),   # positions past 2^30
+    (dict(max_kept=(1 << 30) + 1, ks=1 << 31), B.PA_ERR_UNSUPPORTED),
 ])
 def test_compact_refusals(lib, over, status):
     assert _caller(lib.pa_compact_cache, COMPACT)(**over) == status
@@ -163,6 +167,7 @@ EVICT = dict(pt=FAKE, pts=16, cl=FAKE, msp=16, w=FAKE, k=FAKE, v=FAKE, ksc=None,
     (dict(first=2**31 - 1, recent=2**31 - 1, budget=2**31 - 1), B.PA_ERR_INVALID),
     (dict(dpt=FAKE + 256, dmp=1), B.PA_ERR_INVALID),     # 100 rows do not fit 64
     (dict(P=8), B.PA_ERR_UNSUPPORTED),
+    (dict(msp=(1 << 24) + 1, pts=1 << 25, dpts=1 << 25), B.PA_ERR_UNSUPPORTED),   # positions past 2^30
 ])
 def test_evict_refusals(lib, over, status):
     assert _caller(lib.pa_evict, EVICT)(**over) == status
