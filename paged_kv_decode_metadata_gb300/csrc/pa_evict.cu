@@ -10,11 +10,14 @@
 // the threads (larger keys, equal keys) give every kept position its place.  Bound by the
 // latency of a block's passes; the keys are read once and kept in shared memory.
 //
-// Move.  To other pages (compact_kernel): every row is independent.  In place (compact_in_place_kernel): kept[i] >= i, so moving in
-// ascending batches never overwrites a row that is still to be read, as long as a batch is
-// read whole before it is stored; a block owns one (request, kv head) and a slice of the
-// channels of K or of V (slices do not touch one another's bytes, so they need no order).
-// Bound by memory: the kept rows read and written once.
+// Move.  To other pages (compact_kernel): every row is independent.  In place
+// (compact_in_place_kernel): kept[i] >= i, so moving in ascending batches never overwrites a
+// row that is still to be read, as long as a batch is read whole before it is stored; a block
+// owns one (request, kv head) and a slice of the channels of K or of V (slices do not touch
+// one another's bytes, so they need no order).
+// Bound by memory: the kept rows read and written once.  32 requests of 8K tokens to 2K rows
+// (bf16, other pages) take 107 us for both, the move at 6.5 TB/s; one request 14.2 us, ten of
+// them the selection.
 #include <math_constants.h>
 
 #include "pa_common.cuh"
