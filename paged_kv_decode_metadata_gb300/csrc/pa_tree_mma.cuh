@@ -393,20 +393,6 @@ __global__ void __launch_bounds__(Roles<kQuant>::kThreads, 1)
     // (after a wait that gave up, the pieces that are left only meet the barriers of the
     // softmax warps, so that none of them waits there for good)
     bool ok = true;
-    // What the warp's rows see of a chunk that reaches the drafted positions: four words of 32
-    // positions a row, in shared memory (one loop, kept rolled).
-    uint32_t* seen_s = reinterpret_cast<uint32_t*>(smem + Sh::kStage + warp * Sh::kStageBytes);
-    auto look = [&](const volatile Piece& vp, bool two, int c) {
-      const int row = (vp.pair * 2 + (two ? s : 0)) * kTile + r;
-      const int q_len = vp.q_len, n = vp.n;
-      const bool live = row < q_len * G;
-      const uint32_t* mask =
-          prm.tree_mask + (static_cast<int64_t>(vp.q_begin) + (live ? row >> gs : 0)) * words;
-#pragma unroll 1
-      for (int i = 0; i < 4; ++i)
-        seen_s[4 * lane + i] = live ? visible(c * kTile + 32 * i, n - q_len, n, mask, words) : 0u;
-      __syncwarp();
-    };
     // A thread's registers hold a row of scores, so the walk and the piece stay in shared
     // memory: `volatile` has them read again where they are needed.
     const volatile Piece& vp = ctl.piece[warp];
@@ -429,25 +415,14 @@ __global__ void __launch_bounds__(Roles<kQuant>::kThreads, 1)
       const int committed = max(0, vp.n - vp.q_len) / kTile - vp.c0;  // chunks of those alone
       const int plain = two ? committed : (committed - s + 1) >> 1;
       float m_ref = -CUDART_INF_F, l = 0.f;  // the row's reference and sum of weights
-      float mq[4], lq[4];                    // int8: those of the thread's four rows
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        mq[q] = -CUDART_INF_F;
-        lq[q] = 0.f;
-      }
       for (int k = 0; k < mine && ok; ++k) {
         if constexpr (kQuant) {
           // Half a chunk at a time, each half with its own scores in tensor memory: while one
-          // half's weights are made, the tensor cores work on the other's.  A thread holds
-          // columns of four rows (8 q + t / 4), so that a scale read from shared memory
-          // serves four rows: with a row per thread every scale went to every warp by itself,
-          // 2048 shared-memory cycles a chunk.
-          const float2* scales = reinterpret_cast<const float2*>(smem + Sh::kScales) +
-                                 (chunk0 + (two ? k : 2 * k + s)) % kScaleSlots * kTile + (lane & 3);
+          // half's weights are made, the tensor cores work on the other's.
+          const float4* scales = reinterpret_cast<const float4*>(smem + Sh::kScales) +
+                                 (chunk0 + (two ? k : 2 * k + s)) % kScaleSlots * (2 * kTile / 4);
           // (the chunk's K scales times the softmax scale, then its V scales; written before the
           // scores' K tile was handed on, so before these scores)
-          constexpr uint32_t kLower = 16u << 16;  // the warp's lanes 16-31
-          const bool tail = k >= plain;           // drafted or missing positions
 #pragma unroll 1
           for (int half = 0; half < 2; ++half) {
             ok = mbar_wait_bounded(&ctl.s_full[2 * s + half], step & 1u);
@@ -455,144 +430,96 @@ __global__ void __launch_bounds__(Roles<kQuant>::kThreads, 1)
             if (!ok) break;
             umma::fence_after();
             const uint32_t at = sc + 64 * half;
-            const float2* f_of = scales + 32 * half;
-            uint32_t v[2][2][16];  // [32 columns][16 rows]
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              umma::ld_frag16(at + 32 * i, v[i][0]);
-              umma::ld_frag16(at + 32 * i + kLower, v[i][1]);
-            }
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              umma::wait_ld(v[i][0]);
-              umma::wait_ld(v[i][1]);
-            }
-            // columns 32 i + 8 c + 2 (t % 4), + 1 of row q
-            auto pair_of = [&](int i, int c, int q) -> uint64_t {
-              const uint32_t(&r)[16] = v[i][q >> 1];
-              const int e = 4 * c + 2 * (q & 1);
-              return umma::pair(__uint_as_float(r[e]), __uint_as_float(r[e + 1]));
-            };
-            auto set_pair = [&](int i, int c, int q, float lo, float hi) {
-              uint32_t(&r)[16] = v[i][q >> 1];
-              const int e = 4 * c + 2 * (q & 1);
-              r[e] = __float_as_uint(lo);
-              r[e + 1] = __float_as_uint(hi);
-            };
+            const float4* f_of = scales + 16 * half;
+            float x[64];
 #pragma unroll
             for (int i = 0; i < 2; ++i)
+              umma::ld32(at + 32 * i, *reinterpret_cast<uint32_t(*)[32]>(&x[32 * i]));
 #pragma unroll
-              for (int c = 0; c < 4; ++c) {
-                const float2 f = f_of[16 * i + 4 * c];
+            for (int i = 0; i < 2; ++i) umma::wait_ld(*reinterpret_cast<uint32_t(*)[32]>(&x[32 * i]));
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                  float lo, hi;
-                  umma::unpair(umma::mul2(pair_of(i, c, q), umma::pair(f.x, f.y)), lo, hi);
-                  set_pair(i, c, q, lo, hi);
-                }
-              }
-            if (tail) {
-              if (half == 0) look(vp, two, vp.c0 + (two ? k : 2 * k + s));
+            for (int j = 0; j < 64; j += 4) {
+              const float4 f = f_of[j / 4];
+              umma::unpair(umma::mul2(umma::pair(x[j], x[j + 1]), umma::pair(f.x, f.y)), x[j], x[j + 1]);
+              umma::unpair(umma::mul2(umma::pair(x[j + 2], x[j + 3]), umma::pair(f.z, f.w)), x[j + 2],
+                           x[j + 3]);
+            }
+            if (k >= plain) {  // drafted or missing positions
+              const int row = (vp.pair * 2 + (two ? s : 0)) * kTile + r;
+              const int q_len = vp.q_len, n = vp.n;
+              const bool live = row < q_len * G;
+              const uint32_t* mask =
+                  prm.tree_mask + (static_cast<int64_t>(vp.q_begin) + (live ? row >> gs : 0)) * words;
+              const int p0 = (vp.c0 + (two ? k : 2 * k + s)) * kTile + 64 * half;
 #pragma unroll
-              for (int q = 0; q < 4; ++q) {
-                const uint2 seen = reinterpret_cast<const uint2*>(seen_s)[2 * (8 * q + (lane >> 2)) + half];
+              for (int i = 0; i < 2; ++i) {
+                const uint32_t bits = live ? visible(p0 + 32 * i, n - q_len, n, mask, words) : 0u;
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                  const uint32_t bits = (i == 0 ? seen.x : seen.y) >> (2 * (lane & 3));
-#pragma unroll
-                  for (int c = 0; c < 4; ++c) {
-                    float lo, hi;
-                    umma::unpair(pair_of(i, c, q), lo, hi);
-                    set_pair(i, c, q, (bits >> (8 * c)) & 1u ? lo : -CUDART_INF_F,
-                             (bits >> (8 * c + 1)) & 1u ? hi : -CUDART_INF_F);
-                  }
-                }
+                for (int j = 0; j < 32; ++j)
+                  x[32 * i + j] = (bits >> j) & 1u ? x[32 * i + j] : -CUDART_INF_F;
               }
               __syncwarp();
             }
-            float alpha[4];
-            bool moved = false;
+            float mx[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              float top[2] = {-CUDART_INF_F, -CUDART_INF_F};
+            for (int j = 4; j < 60; j += 8)
 #pragma unroll
-              for (int i = 0; i < 2; ++i)
+              for (int u = 0; u < 4; ++u) mx[u] = umma::max3(mx[u], x[j + u], x[j + 4 + u]);
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                  float lo, hi;
-                  umma::unpair(pair_of(i, c, q), lo, hi);
-                  top[i] = umma::max3(top[i], lo, hi);
-                }
-              float m_new = fmaxf(top[0], top[1]);
-              m_new = fmaxf(m_new, __shfl_xor_sync(0xffffffffu, m_new, 1));
-              m_new = fmaxf(m_new, __shfl_xor_sync(0xffffffffu, m_new, 2));
-              alpha[q] = 1.f;
-              if (m_new > mq[q] + mma::kMaxSlack) {
-                alpha[q] = mq[q] == -CUDART_INF_F ? 0.f : mma::fast_exp2(mq[q] - m_new);
-                mq[q] = m_new;
-                lq[q] *= alpha[q];
-                moved = true;
-              }
+            for (int u = 0; u < 4; ++u) mx[u] = fmaxf(mx[u], x[60 + u]);
+            const float m_new = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+            float alpha = 1.f;
+            if (m_new > m_ref + mma::kMaxSlack) {
+              alpha = m_ref == -CUDART_INF_F ? 0.f : mma::fast_exp2(m_ref - m_new);
+              m_ref = m_new;
+              l *= alpha;
             }
             __syncwarp();
             // The accumulator follows a moved reference, once the last product is over (before
             // the piece's first there is none).
-            if (k + half > 0 && __any_sync(0xffffffffu, moved)) {
+            if (k + half > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
               ok = mbar_wait_bounded(&ctl.pv_done[s], (2 * step + half - 1) & 1u);
               ok = __all_sync(0xffffffffu, ok);
               if (!ok) break;
               umma::fence_after();
 #pragma unroll 1
-              for (int i = 0; i < 8; ++i) {
-                uint32_t o[16];
-                const uint32_t col = oc + 32 * (i & 3) + (i >> 2 ? kLower : 0u);
-                umma::ld_frag16(col, o);
+              for (int i = 0; i < 4; ++i) {
+                uint32_t o[32];
+                umma::ld32(oc + 32 * i, o);
                 umma::wait_ld(o);
 #pragma unroll
-                for (int u = 0; u < 16; ++u)
-                  o[u] = __float_as_uint(__uint_as_float(o[u]) *
-                                         ((u >> 1) & 1 ? (i >> 2 ? alpha[3] : alpha[1])
-                                                       : (i >> 2 ? alpha[2] : alpha[0])));
-                umma::st_frag16(col, o);
+                for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * alpha);
+                umma::st32(oc + 32 * i, o);
               }
             }
-            uint64_t ref2[4], sum[4] = {0, 0, 0, 0};  // pairs of +0
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              const float ref = mq[q] == -CUDART_INF_F ? 0.f : mq[q];
-              ref2[q] = umma::pair(-ref, -ref);
-            }
+            const float ref = m_ref == -CUDART_INF_F ? 0.f : m_ref;
+            const uint64_t ref2 = umma::pair(-ref, -ref);
+            uint64_t sum[4] = {0, 0, 0, 0};  // pairs of +0
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-              uint32_t w[2][8];
+              uint32_t w[16];
 #pragma unroll
-              for (int c = 0; c < 4; ++c) {
-                const float2 g = f_of[kTile / 2 + 16 * i + 4 * c];
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                  float lo, hi;
-                  umma::unpair(umma::add2(pair_of(i, c, q), ref2[q]), lo, hi);
-                  lo = mma::fast_exp2(lo);
-                  hi = mma::fast_exp2(hi);
-                  sum[q] = umma::add2(sum[q], umma::pair(lo, hi));
-                  // the V scale goes with the weight
-                  umma::unpair(umma::mul2(umma::pair(lo, hi), umma::pair(g.x, g.y)), lo, hi);
-                  w[q >> 1][2 * c + (q & 1)] = mma::pack_bf16(lo, hi);
-                }
+              for (int j = 0; j < 16; ++j) {
+                const float4 g4 = f_of[kTile / 4 + 8 * i + j / 2];
+                const float2 g = j & 1 ? make_float2(g4.z, g4.w) : make_float2(g4.x, g4.y);
+                float lo, hi;
+                umma::unpair(umma::add2(umma::pair(x[32 * i + 2 * j], x[32 * i + 2 * j + 1]), ref2), lo, hi);
+                lo = mma::fast_exp2(lo);
+                hi = mma::fast_exp2(hi);
+                sum[j & 3] = umma::add2(sum[j & 3], umma::pair(lo, hi));
+                // the V scale goes with the weight
+                umma::unpair(umma::mul2(umma::pair(lo, hi), umma::pair(g.x, g.y)), lo, hi);
+                w[j] = mma::pack_bf16(lo, hi);
               }
-              umma::st_pairs8(at + 16 * i, w[0]);
-              umma::st_pairs8(at + 16 * i + kLower, w[1]);
+              umma::st16(at + 16 * i, w);
             }
             umma::wait_st();
             umma::fence_before();
             __syncwarp();
             if (lane == 0) mma::mbar_arrive(&ctl.p_ready[2 * s + half]);
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              float lo, hi;
-              umma::unpair(sum[q], lo, hi);
-              lq[q] += lo + hi;
-            }
+            float lo, hi;
+            umma::unpair(umma::add2(umma::add2(sum[0], sum[1]), umma::add2(sum[2], sum[3])), lo, hi);
+            l += lo + hi;
           }
           if (!ok) break;
           ++step;
@@ -681,19 +608,6 @@ __global__ void __launch_bounds__(Roles<kQuant>::kThreads, 1)
           umma::unpair(umma::add2(umma::add2(sum[0], sum[1]), umma::add2(sum[2], sum[3])), lo, hi);
           l += lo + hi;
         }
-      }
-      if constexpr (kQuant) {  // the four rows' numbers to the threads that own the rows below
-        float2* box = reinterpret_cast<float2*>(smem + Sh::kStage + warp * Sh::kStageBytes);
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          lq[q] += __shfl_xor_sync(0xffffffffu, lq[q], 1);
-          lq[q] += __shfl_xor_sync(0xffffffffu, lq[q], 2);
-          if ((lane & 3) == 0) box[8 * q + (lane >> 2)] = make_float2(mq[q], lq[q]);
-        }
-        __syncwarp();
-        m_ref = box[lane].x;
-        l = box[lane].y;
-        __syncwarp();
       }
       chunk0 += vp.c1 - vp.c0;
       // ----- the rows' results -------------------------------------------------------------
