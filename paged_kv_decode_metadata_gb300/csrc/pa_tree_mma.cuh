@@ -738,6 +738,12 @@ __global__ void __launch_bounds__(Roles<kQuant>::kThreads, 1)
     // ======================= int8: codes to bf16 ============================================
     Piece p;
     const int t = tid - kConvertWarp * 32;  // 0..127
+    // A warp turns 8 rows x 4 pieces of 16 codes at a time: every row's swizzle puts its piece
+    // in another bank group, for the loads and for both stores.  Offsets of the warp's first
+    // rows; the other four pieces of a row and the piece's second half are a bit away.
+    const int first_row = ((warp - kConvertWarp) * 32 + (lane & 7)) * 128;
+    const int from = first_row + (((lane >> 3) ^ (lane & 7)) << 4);
+    const int to = first_row + (((2 * (lane >> 3)) ^ (lane & 7)) << 4);
     int it = 0;
     uint32_t chunk = 0;
     bool ok = true;
@@ -759,30 +765,23 @@ __global__ void __launch_bounds__(Roles<kQuant>::kThreads, 1)
             out[t] = in[t] * prm.q_scale;
             out[kTile + t] = c * kTile + t < p.n ? in[kTile + t] : 0.f;
           }
-          // a warp turns 8 rows x 4 pieces of 16 codes at a time: every row's swizzle puts its
-          // piece in another bank group, for the loads and for both stores
+          // four pieces are loaded before the first store: the compiler cannot know that the two
+          // tiles do not overlap
 #pragma unroll 1
-          for (int u0 = 0; u0 < 8; u0 += 4) {
-            // (four pieces are loaded before the first store: the compiler cannot know that the
-            // two tiles do not overlap)
+          for (int rows = 0; rows < 32 * 128; rows += 16 * 128) {
             uint4 w[4];
-            auto row_of = [&](int u) { return ((warp - kConvertWarp) * 4 + (u >> 1)) * 8 + (lane & 7); };
-            auto piece_of = [&](int u) { return (u & 1) * 4 + (lane >> 3); };
 #pragma unroll
             for (int u = 0; u < 4; ++u)
-              w[u] = *reinterpret_cast<const uint4*>(src + mma::swz(row_of(u0 + u), piece_of(u)));
+              w[u] = *reinterpret_cast<const uint4*>(src + rows + (u >> 1) * 1024 + (u & 1 ? from ^ 64 : from));
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
-              const int row = row_of(u0 + u), j = piece_of(u);
-              const uint4 lo =
+              unsigned char* half = dst + rows + (u >> 1) * 1024 + (u & 1) * kHalfBytes;
+              *reinterpret_cast<uint4*>(half + to) =
                   make_uint4(codes_to_bf16x2(w[u].x, 0x4140), codes_to_bf16x2(w[u].x, 0x4342),
                              codes_to_bf16x2(w[u].y, 0x4140), codes_to_bf16x2(w[u].y, 0x4342));
-              const uint4 hi =
+              *reinterpret_cast<uint4*>(half + (to ^ 16)) =
                   make_uint4(codes_to_bf16x2(w[u].z, 0x4140), codes_to_bf16x2(w[u].z, 0x4342),
                              codes_to_bf16x2(w[u].w, 0x4140), codes_to_bf16x2(w[u].w, 0x4342));
-              unsigned char* half = dst + (j >> 2) * kHalfBytes;
-              *reinterpret_cast<uint4*>(half + mma::swz(row, (2 * j) & 7)) = lo;
-              *reinterpret_cast<uint4*>(half + mma::swz(row, (2 * j + 1) & 7)) = hi;
             }
           }
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
