@@ -255,8 +255,8 @@ struct Walk {
 // the products of the chunk before); the raw tiles behind it are what is in flight.
 template <int kTiles, bool kQuant>
 struct Shared {
-  static constexpr int kSlots = kQuant ? 3 : 6 - kTiles;
-  static constexpr int kRawSlots = kTiles == 2 ? 2 : 4;
+  static constexpr int kSlots = kQuant ? 5 - kTiles : 6 - kTiles;
+  static constexpr int kRawSlots = 2;
   static constexpr int kLinePieces = kQuant ? 4 : 8;  // 16-byte pieces of a row on the way out
   static constexpr int kStageBytes = 32 * 16 * kLinePieces;  // per softmax warp
   static constexpr int kQ = 0;
