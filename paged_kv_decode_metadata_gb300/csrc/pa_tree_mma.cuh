@@ -16,32 +16,31 @@
 // = all 512): with two tiles a stream is a tile; with one, the streams take alternate chunks
 // and are joined at the end.  So the tensor cores work on one stream while the other's
 // softmax runs.
-//   warps 0-3, 4-7   softmax of stream 0, 1: bf16: a thread owns a row, so maxima and sums need
-//                    no exchange; int8: columns of four rows, so that a scale serves four.
-//                    Scores come from and weights go back to tensor memory (P takes the place
-//                    of S, as the A operand of P V)
+//   warps 0-3, 4-7   softmax of stream 0, 1: a thread owns a row, so maxima and sums need no
+//                    exchange; scores come from and weights go back to tensor memory (P
+//                    takes the place of S, as the A operand of P V)
 //   warp 8           TMA: a ring of four or five 32 KiB tiles, K and V in turn, running ahead
 //                    into the next unit; a lane issues one box (up to 64 tokens of one page,
 //                    64 channels), so small pages cost no more time than large ones
 //   warp 9           issues every MMA: P V of chunk c, then Q K^T of the stream's next chunk,
 //                    whose scores are ready when the other stream's are used up
 //   warp 10          zeroes V rows past a request's last token (0 * NaN is NaN)
-//   warps 12-15      int8 pools: codes to bf16 (exact), from a ring of raw tiles into the ring;
+//   warps 12-19      int8 pools: codes to bf16 (exact), from a ring of raw tiles into the ring;
 //                    the K scale multiplies the fp32 score, the V scale the weight before
 //                    it is rounded
 // Masks cost nothing before the last chunks: only chunks that reach the drafted positions
 // look at the ancestor bits.
 //
 // Bound by, bf16: memory up to about 256 rows per kv head (64 KiB of K/V per 128 tokens against
-// 1024 tensor cycles per tile), the tensor cores above.  int8: a chunk takes 2.5 us with one
-// tile and 2.7 with two, 1.6 and 2.3 without the widening (bf16: 1.5 and 1.7): the three
-// integer steps and the subtraction of each pair of codes share the schedulers with the
-// softmax.  Eight widening warps instead of four, four for K and four for V, a third raw tile,
-// and shares weighted by the tiles of a chunk were all measured and were no faster.
+// 1024 tensor cycles per tile), the tensor cores above.  int8: a chunk takes 1.9 us with one
+// tile and 2.5 with two (bf16: 1.5 and 1.7).  Widening is four steps a pair of codes on the
+// softmax's schedulers, and the widened tiles, the scales and scores in halves (Q read twice)
+// keep shared memory about three quarters busy.  Shares weighted by the tiles of a chunk were
+// measured and were slower (689 and 731 us against 633 at the time).
 // Measured, both launches where a row is cut (heads / kv heads): one request of 1K tokens with 8
 // drafted (32 / 8) 11.3 us; 32 requests of 8K with 32 drafted (32 / 8) 167.5 us (6.5 TB/s); 16
-// of 16K with 64 drafted (64 / 8) 369-417 us (1.3-1.5 PFLOP/s, under the power cap); 64 ragged
-// to 16K, int8, with 32 drafted (64 / 8) 610 us.
+// of 16K with 64 drafted (64 / 8) 369-434 us (1.3-1.5 PFLOP/s, under the power cap); 64 ragged
+// to 16K, int8, with 32 drafted (64 / 8) 548 us.
 #pragma once
 
 #include "pa_splitk_mma.cuh"
@@ -52,14 +51,17 @@ namespace tree {
 
 constexpr int kTile = 128;            // rows of a tile, tokens of a chunk
 constexpr int kSoftmaxThreads = 256;  // two groups of four warps
-constexpr int kTmaWarp = 8, kMmaWarp = 9, kCleanWarp = 10, kConvertWarp = 12;
-// Threads of a block.  bf16: the softmax warps (a row's 128 scores in registers) and the others
-// split the registers that the block was launched with; int8: everyone keeps 128.
+constexpr int kTmaWarp = 8, kMmaWarp = 9, kCleanWarp = 10, kConvertWarp = 12, kConvertWarps = 8;
+// Threads of a block.  The softmax warps (a row's 128 scores in registers, int8: 64 at a time)
+// and the others split the registers that the block was launched with.  int8: eight widening
+// warps, not four: 1.88 against 2.19 us a chunk with one tile, as fast with two.
 template <bool kQuant>
 struct Roles {
-  static constexpr int kThreads = kQuant ? 512 : 384;
-  static constexpr int kSoftmaxRegs = 216, kOtherRegs = 72;
-  static_assert(256 * kSoftmaxRegs + 128 * kOtherRegs <= 384 * 168, "register split");
+  static constexpr int kThreads = kQuant ? 640 : 384;
+  static constexpr int kLaunchRegs = kQuant ? 96 : 168;  // what fits the threads into 65,536
+  static constexpr int kSoftmaxRegs = kQuant ? 128 : 216, kOtherRegs = 72;
+  static_assert(256 * kSoftmaxRegs + (kThreads - 256) * kOtherRegs <= kThreads * kLaunchRegs,
+                "register split");
 };
 constexpr int kHalfBytes = kTile * 128;       // 64 channels of 128 rows
 constexpr int kTileBytes = 2 * kHalfBytes;
@@ -251,12 +253,13 @@ struct Walk {
 // Shared memory of a block: the Q tiles, the ring, the softmax warps' way out, the control
 // words.  kTiles: Q tiles of the batch's units; with one, the other's room is a ring tile
 // more (memory bound there: two V tiles are held by the streams, the rest is in flight).
-// int8: the ring holds three widened tiles (so that widening V of a chunk does not wait for
-// the products of the chunk before); the raw tiles behind it are what is in flight.
+// int8: the ring holds the widened tiles, three (so that widening V of a chunk does not wait for
+// the products of the chunk before) or, with one Q tile, four (nor K of the chunk after next
+// for this one's); the raw tiles behind it are what is in flight.
 template <int kTiles, bool kQuant>
 struct Shared {
   static constexpr int kSlots = kQuant ? 5 - kTiles : 6 - kTiles;
-  static constexpr int kRawSlots = 2;
+  static constexpr int kRawSlots = 2;  // (a third: no faster)
   static constexpr int kLinePieces = kQuant ? 4 : 8;  // 16-byte pieces of a row on the way out
   static constexpr int kStageBytes = 32 * 16 * kLinePieces;  // per softmax warp
   static constexpr int kQ = 0;
@@ -316,12 +319,12 @@ __global__ void __launch_bounds__(Roles<kQuant>::kThreads, 1)
 
   if (tid == 0) {
     for (int i = 0; i < kSlots; ++i) {
-      mbar_init(&ctl.full[i], kQuant ? 4 : 1);  // int8: the widening warps
+      mbar_init(&ctl.full[i], kQuant ? kConvertWarps : 1);  // int8: the widening warps
       mbar_init(&ctl.empty[i], 1);
     }
     for (int i = 0; i < kRawSlots; ++i) {
       mbar_init(&ctl.raw_full[i], 1);
-      mbar_init(&ctl.raw_empty[i], 4);
+      mbar_init(&ctl.raw_empty[i], kConvertWarps);
     }
     mbar_init(&ctl.q_full, 1);
     mbar_init(&ctl.q_empty, 1);
@@ -382,7 +385,7 @@ __global__ void __launch_bounds__(Roles<kQuant>::kThreads, 1)
 
   if (warp < kTmaWarp) {
     // ======================= softmax ===================================================
-    if constexpr (!kQuant) umma::registers_up<Ro::kSoftmaxRegs>();
+    umma::registers_up<Ro::kSoftmaxRegs>();
     const int s = warp >> 2, r = tid & (kTile - 1);
     const uint32_t lane_base = static_cast<uint32_t>(warp & 3) << 21;  // lane 32 (warp % 4)
     const uint32_t sc = s_col(s) + lane_base, oc = o_col(s) + lane_base;
@@ -736,12 +739,13 @@ __global__ void __launch_bounds__(Roles<kQuant>::kThreads, 1)
     }
   } else if (kQuant && warp >= kConvertWarp) {
     // ======================= int8: codes to bf16 ============================================
+    umma::registers_down<Ro::kOtherRegs>();
     Piece p;
-    const int t = tid - kConvertWarp * 32;  // 0..127
+    const int t = tid - kConvertWarp * 32;  // 0..255
     // A warp turns 8 rows x 4 pieces of 16 codes at a time: every row's swizzle puts its piece
     // in another bank group, for the loads and for both stores.  Offsets of the warp's first
     // rows; the other four pieces of a row and the piece's second half are a bit away.
-    const int first_row = ((warp - kConvertWarp) * 32 + (lane & 7)) * 128;
+    const int first_row = ((warp - kConvertWarp) * 16 + (lane & 7)) * 128;
     const int from = first_row + (((lane >> 3) ^ (lane & 7)) << 4);
     const int to = first_row + (((2 * (lane >> 3)) ^ (lane & 7)) << 4);
     int it = 0;
@@ -762,20 +766,18 @@ __global__ void __launch_bounds__(Roles<kQuant>::kThreads, 1)
             // V scales of positions past the end may hold anything, and 0 * NaN is NaN
             const float* in = reinterpret_cast<const float*>(src + kRawCodes);
             float* out = reinterpret_cast<float*>(smem + Sh::kScales) + chunk % kScaleSlots * 2 * kTile;
-            out[t] = in[t] * prm.q_scale;
-            out[kTile + t] = c * kTile + t < p.n ? in[kTile + t] : 0.f;
+            out[t] = t < kTile ? in[t] * prm.q_scale : (c - 1) * kTile + t < p.n ? in[t] : 0.f;
           }
           // four pieces are loaded before the first store: the compiler cannot know that the two
           // tiles do not overlap
-#pragma unroll 1
-          for (int rows = 0; rows < 32 * 128; rows += 16 * 128) {
+          {
             uint4 w[4];
 #pragma unroll
             for (int u = 0; u < 4; ++u)
-              w[u] = *reinterpret_cast<const uint4*>(src + rows + (u >> 1) * 1024 + (u & 1 ? from ^ 64 : from));
+              w[u] = *reinterpret_cast<const uint4*>(src + (u >> 1) * 1024 + (u & 1 ? from ^ 64 : from));
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
-              unsigned char* half = dst + rows + (u >> 1) * 1024 + (u & 1) * kHalfBytes;
+              unsigned char* half = dst + (u >> 1) * 1024 + (u & 1) * kHalfBytes;
               *reinterpret_cast<uint4*>(half + to) =
                   make_uint4(codes_to_bf16x2(w[u].x, 0x4140), codes_to_bf16x2(w[u].x, 0x4342),
                              codes_to_bf16x2(w[u].y, 0x4140), codes_to_bf16x2(w[u].y, 0x4342));
@@ -795,7 +797,7 @@ __global__ void __launch_bounds__(Roles<kQuant>::kThreads, 1)
     }
     if (!ok && lane == 0) give_up();
   } else {
-    if constexpr (!kQuant) umma::registers_down<Ro::kOtherRegs>();
+    umma::registers_down<Ro::kOtherRegs>();
     Piece p;
     if (warp == kTmaWarp) {
       // ======================= TMA ======================================================
