@@ -681,7 +681,7 @@ PA_API pa_status pa_compact_cache(
  * cache_seqlens).  The rows then move as by pa_compact_cache with begin 0 (weights always
  * move too); every head keeps its own positions, so position i of the shrunk cache is a
  * different token from head to head.  1 <= budget, num_first + num_recent <= budget;
- * max_seq_pages * page_size <= 2^30.
+ * max_seq_pages * page_size <= 2^30; weights 16-byte aligned.
  */
 PA_API pa_status pa_evict(const int32_t* page_table, int64_t page_table_stride,
                           const int32_t* cache_seqlens, int32_t max_seq_pages, float* weights,

@@ -478,7 +478,8 @@ pa_status pa_evict(const int32_t* page_table, int64_t page_table_stride,
                                 dst_page_table, dst_page_table_stride, dst_max_pages, bs,
                                 num_kv_heads, head_dim, page_size, num_pages, &p, &in_place);
   if (st != PA_OK) return st;
-  if (!weights || !new_seqlens || new_seqlens == cache_seqlens) return PA_ERR_INVALID;
+  if (!weights || !aligned(weights, 16) || !new_seqlens || new_seqlens == cache_seqlens)
+    return PA_ERR_INVALID;
   if (budget < 1 || num_first < 0 || num_recent < 0 ||
       static_cast<int64_t>(num_first) + num_recent > budget)
     return PA_ERR_INVALID;

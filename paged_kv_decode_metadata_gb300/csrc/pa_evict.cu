@@ -16,7 +16,7 @@
 // owns one (request, kv head) and a slice of the channels of K or of V (slices do not touch
 // one another's bytes, so they need no order).
 // Bound by memory: the kept rows read and written once.  32 requests of 8K tokens to 2K rows
-// (bf16, other pages) take 107 us for both, the move at 6.5 TB/s; one request 14.2 us, ten of
+// (bf16, other pages) take 97 us for both, the move at 6.5 TB/s; one request 12.9 us, nine of
 // them the selection.
 #include <math_constants.h>
 
@@ -28,9 +28,10 @@ namespace {
 
 // ---- selection ------------------------------------------------------------------------------
 
-constexpr int kSelectThreads = 1024;
+constexpr int kSelectThreads = 1024;  // two blocks an SM: 97 against 101 us for 32 requests of 8K
 constexpr int kSelectWarps = kSelectThreads / 32;
 constexpr int kBins = 2048;
+constexpr int kOwnBins = kBins / kSelectThreads;  // of a thread
 // positions of a row whose keys stay in shared memory; longer rows read them again (from L2)
 constexpr int kCachedKeys = 40 * 1024;
 
@@ -41,7 +42,7 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-__global__ void __launch_bounds__(kSelectThreads) select_kernel(const SelectParams p, int cached) {
+__global__ void __launch_bounds__(kSelectThreads, 2) select_kernel(const SelectParams p, int cached) {
   extern __shared__ __align__(16) uint32_t keys_s[];  // the keys, of rows of up to `cached`
   // the first digit has two histograms, for even and odd lanes: weights cluster in few
   // exponents, and a warp's counts of one bin queue up
@@ -74,28 +75,34 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const SelectPara
   }
 
   const int32_t* pt = p.page_table + static_cast<int64_t>(b) * p.page_table_stride;
-  auto key_of = [&](int pg, int j) -> uint32_t {
+  // Keys of positions j .. j + 3 (j a multiple of 4: one page, one 16-byte read; past n they are
+  // whatever the page holds): from memory, or from shared memory for rows that fit it.
+  auto keys_of = [&](int pg, int j) -> uint4 {
     if (pg < 0 || pg >= p.num_pages) {
       record_error(p.err, kErrPageOutOfRange);
-      return 0u;
+      return make_uint4(0u, 0u, 0u, 0u);
     }
-    return weight_key(
-        p.weights[((static_cast<int64_t>(pg) * p.num_kv_heads + h) << ps) + (j & (p.page_size - 1))]);
+    const float4 w = *reinterpret_cast<const float4*>(
+        p.weights + ((static_cast<int64_t>(pg) * p.num_kv_heads + h) << ps) + (j & (p.page_size - 1)));
+    return make_uint4(weight_key(w.x), weight_key(w.y), weight_key(w.z), weight_key(w.w));
   };
-  // Keys of positions j, j + step, ..: from shared memory or, of rows too long for it, again
-  // from memory; all on their way before the first is used.
-  constexpr int kAhead = 8;
+  constexpr int kAhead = 2;  // such reads on their way before the first is used
   const bool in_smem = n <= cached;
-  auto keys_at = [&](uint32_t (&k)[kAhead], int j, int step, int limit) {
-    if (in_smem) {
+  auto read_keys = [&](uint4 (&k)[kAhead], int j, int step, bool memory) {
+    int pg[kAhead];
 #pragma unroll
-      for (int u = 0; u < kAhead; ++u) k[u] = j + u * step < limit ? keys_s[j + u * step] : 0u;
-    } else {
-      int pg[kAhead];
+    for (int u = 0; u < kAhead; ++u) {
+      k[u] = make_uint4(0u, 0u, 0u, 0u);
+      pg[u] = 0;
+      if (j + u * step < n) {
+        if (memory) pg[u] = pt[(j + u * step) >> ps];
+        else k[u] = *reinterpret_cast<const uint4*>(keys_s + j + u * step);
+      }
+    }
+    if (memory) {
 #pragma unroll
-      for (int u = 0; u < kAhead; ++u) pg[u] = j + u * step < limit ? pt[(j + u * step) >> ps] : -2;
-#pragma unroll
-      for (int u = 0; u < kAhead; ++u) k[u] = pg[u] == -2 ? 0u : key_of(pg[u], j + u * step);
+      for (int u = 0; u < kAhead; ++u)
+        if (j + u * step < n) k[u] = keys_of(pg[u], j + u * step);
     }
   };
 
@@ -110,40 +117,33 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const SelectPara
     const int bits = digit < 2 ? 11 : 10, shift = digit == 0 ? 21 : digit == 1 ? 10 : 0;
     if (none) break;
     int* bins = hist[digit == 0 ? lane & 1 : digit + 1];
-    for (int j0 = tid; j0 < n; j0 += kAhead * kSelectThreads) {
-      uint32_t k[kAhead];
-      if (digit == 0) {  // the keys come with the first digit's pass: a page and a weight each
-        int pg[kAhead];
-#pragma unroll
-        for (int u = 0; u < kAhead; ++u) {
-          const int j = j0 + u * kSelectThreads;
-          pg[u] = j < n ? pt[j >> ps] : -2;
-        }
-#pragma unroll
-        for (int u = 0; u < kAhead; ++u) k[u] = pg[u] == -2 ? 0u : key_of(pg[u], j0 + u * kSelectThreads);
-        if (in_smem) {
-#pragma unroll
-          for (int u = 0; u < kAhead; ++u)
-            if (j0 + u * kSelectThreads < n) keys_s[j0 + u * kSelectThreads] = k[u];
-        }
-      } else {
-        keys_at(k, j0, kSelectThreads, n);
-      }
+    // (the keys come into shared memory with the first digit's pass)
+    for (int j0 = 4 * tid; j0 < n; j0 += 4 * kAhead * kSelectThreads) {
+      uint4 k[kAhead];
+      read_keys(k, j0, 4 * kSelectThreads, digit == 0 || !in_smem);
 #pragma unroll
       for (int u = 0; u < kAhead; ++u) {
-        const int j = j0 + u * kSelectThreads;
-        if (j >= lo && j < hi && (digit == 0 || (k[u] >> (shift + bits)) == prefix))
-          atomicAdd(&bins[(k[u] >> shift) & ((1u << bits) - 1u)], 1);
+        const int j = j0 + u * 4 * kSelectThreads;
+        if (digit == 0 && in_smem && j < n) *reinterpret_cast<uint4*>(keys_s + j) = k[u];
+        const uint32_t key[4] = {k[u].x, k[u].y, k[u].z, k[u].w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (j + e >= lo && j + e < hi && (digit == 0 || (key[e] >> (shift + bits)) == prefix))
+            atomicAdd(&bins[(key[e] >> shift) & ((1u << bits) - 1u)], 1);
       }
     }
     __syncthreads();
-    // bins from the largest down, 64 a warp, two a lane: the one in which the count from
-    // above reaches `need`
-    const int top = kBins - 1 - 2 * tid;
+    // bins from the largest down, kOwnBins a lane: the one in which the count from above
+    // reaches `need`
+    const int top = kBins - 1 - kOwnBins * tid;
     const int* sums = hist[digit == 0 ? 0 : digit + 1];
-    const int c0 = sums[top] + (digit == 0 ? hist[1][top] : 0);
-    const int c1 = sums[top - 1] + (digit == 0 ? hist[1][top - 1] : 0);
-    int incl = c0 + c1;
+    int own[kOwnBins], total = 0;
+#pragma unroll
+    for (int i = 0; i < kOwnBins; ++i) {
+      own[i] = sums[top - i] + (digit == 0 ? hist[1][top - i] : 0);
+      total += own[i];
+    }
+    int incl = total;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
       const int up = __shfl_up_sync(0xffffffffu, incl, d);
@@ -155,11 +155,17 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const SelectPara
 #pragma unroll
     for (int d = 16; d >= 1; d >>= 1) before += __shfl_xor_sync(0xffffffffu, before, d);
     incl += before;
-    const int above = incl - c0 - c1;
+    int above = incl - total;
     if (above < need && incl >= need) {
-      const bool first = above + c0 >= need;
-      found_s[digit][0] = first ? top : top - 1;
-      found_s[digit][1] = first ? above : above + c0;
+      int i = 0;
+#pragma unroll
+      for (int u = 0; u < kOwnBins - 1; ++u)
+        if (i == u && above + own[u] < need) {
+          above += own[u];
+          i = u + 1;
+        }
+      found_s[digit][0] = top - i;
+      found_s[digit][1] = above;
     }
     __syncthreads();
     prefix = (prefix << bits) | found_s[digit][0];
@@ -168,20 +174,17 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const SelectPara
   // `prefix` is the smallest kept key; `need` of the keys equal to it stay (the lowest
   // positions)
 
-  // Each thread places the kept positions of its run, eight at a time (a lane's eight keys
-  // are two 16-byte reads); prefix sums over the threads say where it starts.
-  const int run = ((n + kSelectThreads - 1) / kSelectThreads + kAhead - 1) / kAhead * kAhead;
+  // Each thread places the kept positions of its run, eight at a time; prefix sums over the
+  // threads say where it starts.
+  constexpr int kEight = 8;
+  const int run = ((n + kSelectThreads - 1) / kSelectThreads + kEight - 1) / kEight * kEight;
   const int r0 = min(tid * run, n), r1 = min(n, r0 + run);
-  auto load_run = [&](uint32_t (&k)[kAhead], int j) {
+  auto load_run = [&](uint32_t (&k)[kEight], int j) {
     if (none) return;
-    if (in_smem) {  // (keys past n are there, unused: the room is a multiple of 16 positions)
-      const uint4 a = *reinterpret_cast<const uint4*>(keys_s + j);
-      const uint4 c = *reinterpret_cast<const uint4*>(keys_s + j + 4);
-      k[0] = a.x; k[1] = a.y; k[2] = a.z; k[3] = a.w;
-      k[4] = c.x; k[5] = c.y; k[6] = c.z; k[7] = c.w;
-    } else {
-      keys_at(k, j, 1, r1);
-    }
+    uint4 x[kAhead];
+    read_keys(x, j, 4, !in_smem);
+    k[0] = x[0].x; k[1] = x[0].y; k[2] = x[0].z; k[3] = x[0].w;
+    k[4] = x[1].x; k[5] = x[1].y; k[6] = x[1].z; k[7] = x[1].w;
   };
   auto judge = [&](int j, uint32_t k, bool& keep, bool& tie) {
     const bool in = j < r1;
@@ -190,11 +193,11 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const SelectPara
     tie = in && !always && !none && k == prefix;
   };
   int sure = 0, equal = 0;  // this thread's
-  for (int j = r0; j < r1; j += kAhead) {
-    uint32_t k[kAhead];
+  for (int j = r0; j < r1; j += kEight) {
+    uint32_t k[kEight];
     load_run(k, j);
 #pragma unroll
-    for (int u = 0; u < kAhead; ++u) {
+    for (int u = 0; u < kEight; ++u) {
       bool keep, tie;
       judge(j + u, k[u], keep, tie);
       sure += keep;
@@ -212,8 +215,8 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const SelectPara
   }
   if (lane == 31) placed_s[warp] = make_int2(sure_at, equal_at);
   __syncthreads();
-  int2 other = placed_s[lane];
-  if (lane >= warp) other = make_int2(0, 0);
+  int2 other = make_int2(0, 0);
+  if (lane < warp) other = placed_s[lane];
 #pragma unroll
   for (int d = 16; d >= 1; d >>= 1) {
     other.x += __shfl_xor_sync(0xffffffffu, other.x, d);
@@ -221,11 +224,11 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const SelectPara
   }
   sure_at += other.x - sure;
   equal_at += other.y - equal;
-  for (int j = r0; j < r1; j += kAhead) {
-    uint32_t k[kAhead];
+  for (int j = r0; j < r1; j += kEight) {
+    uint32_t k[kEight];
     load_run(k, j);
 #pragma unroll
-    for (int u = 0; u < kAhead; ++u) {
+    for (int u = 0; u < kEight; ++u) {
       bool keep, tie;
       judge(j + u, k[u], keep, tie);
       if (keep || (tie && equal_at < need)) kept[sure_at + min(equal_at, need)] = j + u;

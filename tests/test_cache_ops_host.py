@@ -163,6 +163,7 @@ EVICT = dict(pt=FAKE, pts=16, cl=FAKE, msp=16, w=FAKE, k=FAKE, v=FAKE, ksc=None,
 @pytest.mark.parametrize("over,status", [
     (dict(bs=0), B.PA_OK), (dict(w=None), B.PA_ERR_INVALID), (dict(new=None), B.PA_ERR_INVALID),
     (dict(new=FAKE), B.PA_ERR_INVALID), (dict(budget=0), B.PA_ERR_INVALID),
+    (dict(w=FAKE + 4), B.PA_ERR_INVALID),
     (dict(first=-1), B.PA_ERR_INVALID), (dict(recent=97), B.PA_ERR_INVALID),
     (dict(first=2**31 - 1, recent=2**31 - 1, budget=2**31 - 1), B.PA_ERR_INVALID),
     (dict(dpt=FAKE + 256, dmp=1), B.PA_ERR_INVALID),     # 100 rows do not fit 64
