@@ -12,7 +12,7 @@
 // MMA registers; nothing is staged.  A warp owns 16 tokens at a time.
 //
 // Bound by memory: K, and the weights read and written: 64 requests of up to 16K tokens (int8)
-// take 104 us (5.7 TB/s), one of 8K (bf16) 3.1 us, most of it launch and first loads.
+// take 104 us (5.7 TB/s), one of 8K (bf16) 3.1 us, which is what an eager launch costs the host.
 #include <math_constants.h>
 
 #include "pa_splitk_mma.cuh"
