@@ -474,6 +474,24 @@ def test_tree_random_shapes(seed):
     t.check(*t.run(r.randint(0, 5)))
 
 
+@pytest.mark.parametrize("kv", ["bf16", "int8"])
+@pytest.mark.parametrize("splits", [0, 1, 2])
+@pytest.mark.parametrize("equal", [False, True])
+def test_tree_many_requests(kv, splits, equal):
+    """More requests than a warp has lanes: ragged ones, some with nothing drafted or cached, and
+    equal ones in as many units as the device has SMs, which stay whole."""
+    r = random.Random(7)
+    if equal:
+        seqlens, q_lens, hkv, group = [300] * 38, [9] * 38, 4, 4
+    else:
+        seqlens = [r.choice([0, 1, 128, r.randint(1, 700)]) for _ in range(100)]
+        q_lens = [min(n, r.choice([0, 1, 5, r.randint(1, 50)])) for n in seqlens]
+        q_lens[31] = q_lens[32] = q_lens[99] = 2         # (of an empty cache, too)
+        hkv, group = 2, 8
+    t = Tree(Cache(seqlens, hkv, 32, kv, 3), q_lens, hkv * group, 4)
+    t.check(*t.run(splits))
+
+
 # ---- accumulated weights -----------------------------------------------------------------------
 
 WEIGHT_CASES = [  # seqlens, hq, hkv, page, kv
@@ -758,3 +776,60 @@ def test_speculative_loop(kv):
         position = [p + 1 for p in position]
         check_evict(c, 60, 2, 20, True)
         n = [min(x, 60) for x in n]
+
+
+@pytest.mark.parametrize("kv", ["bf16", "int8"])
+def test_pages_past_four_gigabytes_give_the_same_bits(kv):
+    """Append, tree, weights and both moves on pages whose byte offsets pass 32 bits, against the
+    same pages at the start of a small pool."""
+    hq, hkv, page, m = 16, 8, 64, 12
+    g = torch.Generator().manual_seed(91)
+    size = 2 if kv == "bf16" else 1
+    far = 2 ** 32 // (hkv * page * 128 * size) + 1
+    dtype = torch.bfloat16 if kv == "bf16" else torch.int8
+    shape = (m, hkv, page, 128)
+    first = [torch.randn(shape, generator=g).to(dtype) if kv == "bf16" else
+             torch.randint(-127, 128, shape, generator=g, dtype=dtype) for _ in "kv"]
+    first += [torch.rand(shape[:3], generator=g) * 0.045 + 0.005 for _ in range(3)]  # scales, weights
+    x = torch.randn((20, hq + 2 * hkv, 128), generator=g).to(torch.bfloat16).cuda()
+    q, k, v = x.split([hq, hkv, hkv], dim=1)
+    masks = R.mask_tensor([m for p in ([-1, 0, 0, 1, 2, -1, 5, 6, 7, 8], [-1] * 10) for m in R.ancestor_rows(p)], 1)
+    cu = torch.tensor([0, 10, 20], dtype=torch.int32).cuda()
+    n = torch.tensor([370, 129], dtype=torch.int32).cuda()
+    freq = B.pa_rope_frequencies(128).cuda()
+    results = []
+    for off in (0, far):
+        pools = [torch.empty((off + m, *t.shape[1:]), dtype=t.dtype, device="cuda") for t in first]
+        for big, small in zip(pools, first):
+            big[off:] = small.cuda()
+        pk, pv, ks, vs, w = pools
+        ks, vs = (ks, vs) if kv == "int8" else (None, None)
+        table = torch.tensor([[3, 7, 1, 0, 9, 11], [2, 10, 4, 5, 6, 8]], dtype=torch.int32) + off
+        at = [(0, 360 + i) for i in range(10)] + [(1, 119 + i) for i in range(10)]
+        slots = torch.tensor([int(table[b, j // page]) * page + j % page for b, j in at]).cuda()
+        table = table.cuda()
+        rows = dict(page_table=table, max_seq_pages=6)
+        cache = dict(k_cache=pk, v_cache=pv, k_scale=ks, v_scale=vs)
+        q_out = torch.empty((20, hq, 128), dtype=torch.bfloat16, device="cuda")
+        B.pa_rope_append(q=q, k=k, v=v, positions=torch.arange(20).cuda(), slots=slots, inv_freq=freq,
+                         q_out=q_out, **cache)
+        out, lse = torch.empty_like(q_out), torch.empty((20, hq), device="cuda")
+        ws = torch.empty(max(16, B.pa_tree_workspace_bytes(2, 20, 10, hq, hkv, 128, page, 6)),
+                         dtype=torch.uint8, device="cuda")
+        B.pa_tree_attention(q=q_out, cache_seqlens=n, cu_seqlens_q=cu, tree_mask=masks.cuda(), max_q_len=10,
+                            num_splits=0, sm_scale=SCALE, workspace=ws, out=out, lse=lse, **rows, **cache)
+        B.pa_accumulate_weights(q=q_out[9::10].contiguous(), lse=lse[9::10].contiguous(), k_cache=pk,
+                                k_scale=ks, cache_seqlens=n, weights=w, sm_scale=SCALE, **rows)
+        kept = torch.empty((2, hkv, 100), dtype=torch.int32, device="cuda")
+        new = torch.empty(2, dtype=torch.int32, device="cuda")
+        evict = dict(weights=w, budget=100, num_first=3, num_recent=20, kept=kept, new_seqlens=new, **rows, **cache)
+        # the first request to the second's last pages, then both in place
+        B.pa_evict(cache_seqlens=torch.tensor([370, 0], dtype=torch.int32).cuda(),
+                   dst_page_table=(torch.tensor([[6, 8], [6, 8]], dtype=torch.int32) + off).cuda(), **evict)
+        B.pa_evict(cache_seqlens=n, dst_page_table=table, **evict)
+        torch.cuda.synchronize()
+        results.append([t.cpu() for t in (q_out, out, lse, kept, new)] +
+                       [t[off:].cpu() for t in (pk, pv, w) + ((ks, vs) if kv == "int8" else ())])
+        del pools, pk, pv, ks, vs, w, cache, evict
+    for near, there in zip(*results):
+        assert same_bits(near, there)
