@@ -270,7 +270,10 @@ struct Shared {
   static constexpr int kEnd = kStage + kSoftmaxThreads / 32 * kStageBytes;
   struct Control {
     uint64_t full[kSlots], empty[kSlots], raw_full[kRawSlots], raw_empty[kRawSlots];
-    uint64_t q_full, q_empty, o_full[2], v_last, drained;
+    uint64_t q_full, q_empty, o_full[2], drained;
+    // by ring tile: a request's last V tile on its way to the cleaning warp.  (One for all would
+    // not do: the next short request's tile may be issued before this one has landed.)
+    uint64_t v_last[kSlots];
     // bf16: a stream's scores, the first half of its weights, all of them; int8: [stream][half
     // of the chunk], and each product's end
     uint64_t s_full[4], p_half[2], p_ready[4], pv_done[2];
@@ -278,7 +281,8 @@ struct Shared {
     Piece piece[kSoftmaxThreads / 32];
     float join[2][kTile];  // one number a row, from stream to stream
     uint32_t tmem;
-    int abort, issued, issued_v, issued_q;
+    int abort, issued, issued_q;
+    int issued_v[kSlots];
   };
   static constexpr int kBytes = kEnd + static_cast<int>(sizeof(Control)) + 1024;  // + alignment
   static_assert(kBytes <= 227 * 1024, "one block's shared memory");
@@ -321,6 +325,8 @@ __global__ void __launch_bounds__(Roles<kQuant>::kThreads, 1)
     for (int i = 0; i < kSlots; ++i) {
       mbar_init(&ctl.full[i], kQuant ? kConvertWarps : 1);  // int8: the widening warps
       mbar_init(&ctl.empty[i], 1);
+      mbar_init(&ctl.v_last[i], 1);
+      ctl.issued_v[i] = 0;
     }
     for (int i = 0; i < kRawSlots; ++i) {
       mbar_init(&ctl.raw_full[i], 1);
@@ -337,11 +343,9 @@ __global__ void __launch_bounds__(Roles<kQuant>::kThreads, 1)
       mbar_init(&ctl.o_full[s], 1);
       mbar_init(&ctl.pv_done[s], 1);
     }
-    mbar_init(&ctl.v_last, 1);
     mbar_init(&ctl.drained, 1);
     ctl.abort = 0;
     ctl.issued = 0;
-    ctl.issued_v = 0;
     ctl.issued_q = 0;
     fence_barrier_init();
   }
@@ -878,10 +882,11 @@ __global__ void __launch_bounds__(Roles<kQuant>::kThreads, 1)
             if (!ok) break;
             // (a last V tile that the request's end cuts goes to the cleaning warp first, which
             // then completes the slot's barrier)
-            uint64_t* bar = kv && (c + 1) * kTile > p.n ? &ctl.v_last : &ctl.full[slot];
+            const bool last = kv && (c + 1) * kTile > p.n;
+            uint64_t* bar = last ? &ctl.v_last[slot] : &ctl.full[slot];
             if (lane == 0) {
-              if (bar == &ctl.v_last) {
-                ctl.issued_v += 1;
+              if (last) {
+                ctl.issued_v[slot] += 1;
               } else {
                 ctl.issued = it + 1;
               }
@@ -1017,24 +1022,25 @@ __global__ void __launch_bounds__(Roles<kQuant>::kThreads, 1)
     } else if (!kQuant && warp == kCleanWarp) {
       // ======================= V rows past the last token ===================================
       int it = 0;
-      uint32_t cleaned = 0;
+      uint32_t cleaned = 0;  // bit per ring tile: parity of its uses
       while (walk.next(prm, P, p)) {
         it += 2 * (p.c1 - p.c0);
         const int valid = p.n - (p.c1 - 1) * kTile;  // tokens of the last chunk
         if (valid >= kTile) continue;
-        if (!mbar_wait_bounded(&ctl.v_last, cleaned & 1u)) {
+        const int slot = (it - 1) % kSlots;
+        if (!mbar_wait_bounded(&ctl.v_last[slot], (cleaned >> slot) & 1u)) {
           if (lane == 0) give_up();
           break;
         }
-        ++cleaned;
-        unsigned char* rows = smem + Sh::kRing + ((it - 1) % kSlots) * kTileBytes;
+        cleaned ^= 1u << slot;
+        unsigned char* rows = smem + Sh::kRing + slot * kTileBytes;
         for (int u = valid * 8 + lane; u < kTile * 8; u += 32) {
           *reinterpret_cast<uint4*>(rows + u * 16) = make_uint4(0u, 0u, 0u, 0u);
           *reinterpret_cast<uint4*>(rows + kHalfBytes + u * 16) = make_uint4(0u, 0u, 0u, 0u);
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
-        if (lane == 0) mma::mbar_arrive(&ctl.full[(it - 1) % kSlots]);
+        if (lane == 0) mma::mbar_arrive(&ctl.full[slot]);
       }
       __syncwarp();
     }
@@ -1049,8 +1055,10 @@ __global__ void __launch_bounds__(Roles<kQuant>::kThreads, 1)
     uint64_t* landed = kQuant ? ctl.raw_full : ctl.full;
     for (int i = max(0, issued - kInFlight); i < issued; ++i)
       mbar_wait_bounded(&landed[i % kInFlight], static_cast<uint32_t>(i / kInFlight) & 1u);
-    const int issued_v = *static_cast<volatile int*>(&ctl.issued_v);
-    if (issued_v > 0) mbar_wait_bounded(&ctl.v_last, static_cast<uint32_t>(issued_v - 1) & 1u);
+    for (int i = 0; i < kSlots; ++i) {
+      const int uses = *static_cast<volatile int*>(&ctl.issued_v[i]);
+      if (uses > 0) mbar_wait_bounded(&ctl.v_last[i], static_cast<uint32_t>(uses - 1) & 1u);
+    }
     const int issued_q = *static_cast<volatile int*>(&ctl.issued_q);
     if (issued_q > 0) mbar_wait_bounded(&ctl.q_full, static_cast<uint32_t>(issued_q - 1) & 1u);
   }

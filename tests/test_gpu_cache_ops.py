@@ -492,6 +492,37 @@ def test_tree_many_requests(kv, splits, equal):
     t.check(*t.run(splits))
 
 
+@pytest.mark.parametrize("kv", ["bf16", "int8"])
+def test_tree_short_requests_while_memory_is_busy(kv):
+    """Requests of a chunk or two, several to a block, so that the last V tiles of two of them are
+    on their way at once; copies on another stream make that take longer.  Every call gives
+    the first one's bits."""
+    r = random.Random(11)
+    seqlens = [r.randint(1, 171) for _ in range(30)]
+    q_lens = [min(n, r.randint(1, 58)) for n in seqlens]
+    t = Tree(Cache(seqlens, 16, 64, kv, 12), q_lens, 64, 13)
+    out, lse = t.run(0)
+    t.check(out, lse)
+    c, rows = t.c, t.total
+    size = B.pa_tree_workspace_bytes(30, rows, t.max_q, 64, 16, 128, 64, c.msp)
+    again = torch.empty_like(out), torch.empty_like(lse)
+    call = B.prepare_tree_attention(
+        q=t.q.cuda(), k_cache=c.d_k, v_cache=c.d_v, k_scale=c.d_ks, v_scale=c.d_vs, page_table=c.d_table,
+        cache_seqlens=c.d_n, cu_seqlens_q=t.cu.cuda(), tree_mask=R.mask_tensor(t.masks, t.words).cuda(),
+        max_q_len=t.max_q, max_seq_pages=c.msp, num_splits=0, sm_scale=SCALE,
+        workspace=torch.empty(max(16, size), dtype=torch.uint8, device="cuda"), out=again[0], lse=again[1])
+    side = torch.cuda.Stream()
+    a, b = (torch.zeros(1 << 30, dtype=torch.uint8, device="cuda") for _ in "ab")
+    torch.cuda.synchronize()
+    for _ in range(20):
+        with torch.cuda.stream(side):
+            for _ in range(4):
+                b.copy_(a)
+        for _ in range(50):                              # (beside the copies)
+            call()
+        assert same_bits(out, again[0]) and same_bits(lse, again[1])
+
+
 # ---- accumulated weights -----------------------------------------------------------------------
 
 WEIGHT_CASES = [  # seqlens, hq, hkv, page, kv
