@@ -542,6 +542,20 @@ PA_API pa_status pa_rope_append(const void* q, int64_t q_stride, const void* k, 
                                 int32_t use_pdl);
 
 /*
+ * pa_rope_append_weights -- the same, and the accumulated weights (pa_accumulate_weights) of
+ * the rows it writes set to 0: weights [num_pages, num_kv_heads, page_size] fp32, or NULL.
+ * The rows that a request grows into hold what an evicted, rejected or finished token left
+ * there, so a loop that accumulates weights appends with this form.
+ */
+PA_API pa_status pa_rope_append_weights(
+    const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+    int64_t v_stride, const int64_t* positions, const int64_t* slots, const double* inv_freq,
+    int32_t rotary_dim, int32_t interleaved, float amplitude, int32_t num_tokens,
+    int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim, void* q_out, int64_t q_out_stride,
+    void* k_cache, void* v_cache, float* k_scale, float* v_scale, float* weights, int32_t kv_dtype,
+    int32_t page_size, int64_t num_pages, void* stream, int32_t use_pdl);
+
+/*
  * pa_build_tree_mask -- ancestor masks of drafted trees, from parent indices.
  *   parents    [total_q] int32: of node i of request b (row cu_seqlens_q[b] + i) the node
  *              index of its parent within the request (< i), or -1 for a root
@@ -633,7 +647,8 @@ PA_API size_t pa_tree_workspace_bytes(int32_t bs, int32_t total_q, int32_t max_q
  * lse = -inf adds nothing).  weights [num_pages, num_kv_heads, page_size] fp32, kept with
  * the pools; pools, tables and limits as for pa_decode_splitk (k_scale: int8 only), and
  * max_seq_pages * page_size <= 2^30.  Rows of
- * other positions are not touched.  A page that several requests share gets all of their
+ * other positions are not touched.  A row's weight has to be 0 when its token enters the
+ * cache (pa_rope_append_weights, or the caller, sees to that).  A page that several requests share gets all of their
  * weights, in an order that is not fixed; otherwise the result is the same every time.
  */
 PA_API pa_status pa_accumulate_weights(
@@ -655,7 +670,8 @@ PA_API pa_status pa_accumulate_weights(
  *          kept[b, h, i] >= begin[b] + i; or another table whose pages of the moved
  *          positions hold no position that this call reads (fresh pages: needed where
  *          requests share pages).  [bs, dst_page_table_stride], dst_max_pages columns used.
- * Rows of the destination that no kept position moves to are left as they are.  A kept
+ * Rows of the destination that no kept position moves to are left as they are, weights
+ * included (tokens appended there later: pa_rope_append_weights).  A kept
  * position outside [0, cache_seqlens[b]), a target past dst_max_pages * page_size or, in
  * place, a kept position before its target is not moved and sets
  * PA_DEVERR_KEPT_OUT_OF_RANGE.  max_kept: the largest count; larger counts are cut to it.

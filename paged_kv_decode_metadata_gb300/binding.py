@@ -133,6 +133,8 @@ def _declare(lib):
     lib.pa_rope_frequencies.argtypes = [vp, i32, f64, i32, f64, i64, f64, f64]
     lib.pa_rope_append.argtypes = [vp, i64, vp, i64, vp, i64, vp, vp, vp, i32, i32, f32, i32, i32,
                                    i32, i32, vp, i64, vp, vp, vp, vp, i32, i32, i64, vp, i32]
+    lib.pa_rope_append_weights.argtypes = [*lib.pa_rope_append.argtypes[:22], vp,
+                                           *lib.pa_rope_append.argtypes[22:]]
     lib.pa_build_tree_mask.argtypes = [vp, vp, i32, i32, i32, vp, i32, vp, i32]
     lib.pa_tree_attention.argtypes = [vp, vp, vp, vp, vp, i32, vp, i64, vp, vp, vp, i32, i32, i32,
                                       i32, i32, i32, i32, i32, i64, i32, i32, f32, vp, sz, vp, vp,
@@ -167,6 +169,7 @@ def _declare(lib):
                  "pa_decode_step", "pa_decode_step_host", "pa_decode_step_host_packed",
                  "pa_decode_step_multi",
                  "pa_decode_step_window", "pa_rope_frequencies", "pa_rope_append",
+                 "pa_rope_append_weights",
                  "pa_build_tree_mask", "pa_tree_attention", "pa_decode_step_tree",
                  "pa_accumulate_weights", "pa_compact_cache", "pa_evict",
                  "pa_read_error_flags"):
@@ -717,10 +720,11 @@ def _token_rows(t: torch.Tensor, tokens: int, name: str):
 
 
 def _rope_append_args(*, q, k, v, positions, slots, inv_freq, q_out, k_cache, v_cache,
-                      k_scale=None, v_scale=None, interleaved: bool = False,
+                      k_scale=None, v_scale=None, weights=None, interleaved: bool = False,
                       amplitude: float = 1.0, stream=None, use_pdl: bool = True):
     _on_device(q=q, k=k, v=v, positions=positions, slots=slots, inv_freq=inv_freq, q_out=q_out,
-               k_cache=k_cache, v_cache=v_cache, k_scale=k_scale, v_scale=v_scale)
+               k_cache=k_cache, v_cache=v_cache, k_scale=k_scale, v_scale=v_scale,
+               weights=weights)
     kv_dtype, ks, vs, (num_pages, hkv, page_size, d) = _pools(k_cache, v_cache, k_scale, v_scale)
     tokens = q.shape[0]
     qp, q_stride, hq = _token_rows(q, tokens, "q")
@@ -734,23 +738,27 @@ def _rope_append_args(*, q, k, v, positions, slots, inv_freq, q_out, k_cache, v_
     _shape(slots, (tokens,), "slots")
     if inv_freq.dim() != 1:
         raise ValueError("inv_freq must be [rotary_dim / 2]")
+    if weights is not None:
+        _shape(weights, (num_pages, hkv, page_size), "weights")
     return (qp, q_stride, kp, k_stride, vp, v_stride, _ptr(positions, torch.int64, "positions"),
             _ptr(slots, torch.int64, "slots"), _ptr(inv_freq, torch.float64, "inv_freq"),
             2 * inv_freq.numel(), int(bool(interleaved)), float(amplitude), tokens, hq, hkv, d, op,
             o_stride, _ptr(k_cache, None, "k_cache"), _ptr(v_cache, None, "v_cache"), ks, vs,
-            kv_dtype, page_size, num_pages, _stream(stream), int(bool(use_pdl)))
+            _ptr(weights, torch.float32, "weights"), kv_dtype, page_size, num_pages, _stream(stream),
+            int(bool(use_pdl)))
 
 
 def pa_rope_append(**kw):
     """Rotary positions on q (into q_out) and k, and the new k and v rows written to their
-    slots of the pools; see include/pa.h.  Keyword arguments: those of
-    ``_rope_append_args``."""
-    _check("pa_rope_append", load().pa_rope_append(*_rope_append_args(**kw)))
+    slots of the pools, the written rows' accumulated ``weights`` (if given) set to 0; see
+    include/pa.h.  Keyword arguments: those of ``_rope_append_args``."""
+    _check("pa_rope_append", load().pa_rope_append_weights(*_rope_append_args(**kw)))
 
 
 def prepare_rope_append(*, lib=None, **kw) -> PreparedCall:
     """``pa_rope_append`` with the given keyword arguments, marshalled once."""
-    return PreparedCall("pa_rope_append", _rope_append_args(**kw), lib, keep=tuple(kw.values()))
+    return PreparedCall("pa_rope_append_weights", _rope_append_args(**kw), lib,
+                        keep=tuple(kw.values()))
 
 
 def pa_build_tree_mask(parents, cu_seqlens_q, tree_mask, *, max_q_len: int, stream=None,

@@ -79,14 +79,14 @@ pa_status pa_rope_frequencies(double* inv_freq, int32_t rotary_dim, double base,
   return PA_OK;
 }
 
-pa_status pa_rope_append(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
-                         const void* v, int64_t v_stride, const int64_t* positions,
-                         const int64_t* slots, const double* inv_freq, int32_t rotary_dim,
-                         int32_t interleaved, float amplitude, int32_t num_tokens,
-                         int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim, void* q_out,
-                         int64_t q_out_stride, void* k_cache, void* v_cache, float* k_scale,
-                         float* v_scale, int32_t kv_dtype, int32_t page_size, int64_t num_pages,
-                         void* stream, int32_t use_pdl) {
+pa_status pa_rope_append_weights(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                                 const void* v, int64_t v_stride, const int64_t* positions,
+                                 const int64_t* slots, const double* inv_freq, int32_t rotary_dim,
+                                 int32_t interleaved, float amplitude, int32_t num_tokens,
+                                 int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim, void* q_out,
+                                 int64_t q_out_stride, void* k_cache, void* v_cache, float* k_scale,
+                                 float* v_scale, float* weights, int32_t kv_dtype, int32_t page_size,
+                                 int64_t num_pages, void* stream, int32_t use_pdl) {
   if (num_tokens < 0) return PA_ERR_INVALID;
   if (num_tokens == 0) return PA_OK;
   pa_status st = check_pools(k_cache, v_cache, k_scale, v_scale, kv_dtype, num_kv_heads, head_dim,
@@ -104,6 +104,7 @@ pa_status pa_rope_append(const void* q, int64_t q_stride, const void* k, int64_t
   }
   if (q_out == q && q_out_stride != q_stride) return PA_ERR_INVALID;
   if (!std::isfinite(amplitude)) return PA_ERR_INVALID;
+  if (weights != nullptr && !aligned(weights, 4)) return PA_ERR_INVALID;
   if (rotary_dim < 16 || rotary_dim > 128 || rotary_dim % 16 != 0) return PA_ERR_UNSUPPORTED;
   pa::RopeParams p = {};
   p.q = q;
@@ -126,6 +127,7 @@ pa_status pa_rope_append(const void* q, int64_t q_stride, const void* k, int64_t
   p.v_cache = v_cache;
   p.k_scale = k_scale;
   p.v_scale = v_scale;
+  p.weights = weights;
   p.page_size = page_size;
   p.num_pages = num_pages;
   cudaError_t e = pa::error_word(&p.err);
@@ -133,6 +135,21 @@ pa_status pa_rope_append(const void* q, int64_t q_stride, const void* k, int64_t
   return finish(pa::launch_rope(p, kv_dtype == PA_KV_INT8, interleaved != 0,
                                 static_cast<cudaStream_t>(stream), use_pdl != 0),
                 "rotary append launch");
+}
+
+pa_status pa_rope_append(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                         const void* v, int64_t v_stride, const int64_t* positions,
+                         const int64_t* slots, const double* inv_freq, int32_t rotary_dim,
+                         int32_t interleaved, float amplitude, int32_t num_tokens,
+                         int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim, void* q_out,
+                         int64_t q_out_stride, void* k_cache, void* v_cache, float* k_scale,
+                         float* v_scale, int32_t kv_dtype, int32_t page_size, int64_t num_pages,
+                         void* stream, int32_t use_pdl) {
+  return pa_rope_append_weights(q, q_stride, k, k_stride, v, v_stride, positions, slots, inv_freq,
+                                rotary_dim, interleaved, amplitude, num_tokens, num_q_heads,
+                                num_kv_heads, head_dim, q_out, q_out_stride, k_cache, v_cache,
+                                k_scale, v_scale, nullptr, kv_dtype, page_size, num_pages, stream,
+                                use_pdl);
 }
 
 pa_status pa_build_tree_mask(const int32_t* parents, const int32_t* cu_seqlens_q, int32_t bs,

@@ -106,6 +106,7 @@ struct RopeParams {
   int64_t q_out_stride;
   void *k_cache, *v_cache;
   float *k_scale, *v_scale;  // int8 pools only
+  float* weights;            // nullptr, or accumulated weights: 0 for the rows written
   int32_t page_size;
   int64_t num_pages;
   unsigned int* err;

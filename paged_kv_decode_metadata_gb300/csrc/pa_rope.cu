@@ -108,6 +108,9 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeParams p, int 
     if (to >= 0 && !cached && lane == 0 && part == 0) record_error(p.err, kErrSlotOutOfRange);
     const int64_t page = cached ? to / p.page_size : 0;
     const int row_in_page = cached ? static_cast<int>(to - page * p.page_size) : 0;
+    // (here, once a token: with its K rows below it cost the append 2 % even where it is off)
+    if (p.weights != nullptr && cached && part == 0)
+      for (int h = lane; h < hkv; h += 32) p.weights[(page * hkv + h) * p.page_size + row_in_page] = 0.f;
     float c[8], s[8];  // of pairs 8 l ..
     {
       float mine_c[2], mine_s[2];

@@ -249,3 +249,18 @@ def test_binding_refuses_host_tensors_and_wrong_shapes():
     with pytest.raises(ValueError, match="bf16"):
         B._token_rows(x.float(), 2, "q")
     assert B._token_rows(x[:, 2:4], 2, "k")[1:] == (1024, 2)   # a view of wider rows
+
+
+# the same, with the rows' accumulated weights before the KV type
+ROPE_WEIGHTS = {**{k: v for k, v in list(ROPE.items())[:22]}, "w": FAKE,
+                **{k: v for k, v in list(ROPE.items())[22:]}}
+
+
+@pytest.mark.parametrize("over,status", [
+    (dict(tokens=0), B.PA_OK), (dict(tokens=-1), B.PA_ERR_INVALID), (dict(q=None), B.PA_ERR_INVALID),
+    (dict(w=FAKE + 2), B.PA_ERR_INVALID),          # misaligned
+    (dict(kv=1), B.PA_ERR_INVALID), (dict(P=48), B.PA_ERR_UNSUPPORTED), (dict(rot=8), B.PA_ERR_UNSUPPORTED),
+])
+def test_rope_with_weights_refusals(lib, over, status):
+    assert list(ROPE_WEIGHTS)[21:24] == ["vsc", "w", "kv"]
+    assert _caller(lib.pa_rope_append_weights, ROPE_WEIGHTS)(**over) == status

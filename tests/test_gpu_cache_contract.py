@@ -1,0 +1,140 @@
+"""What the header promises of the cache operators at the edges of a serving loop, beside the
+plain cases of test_gpu_cache_ops.py."""
+
+import random
+
+import pytest
+import torch
+
+import cache_reference as R
+from paged_kv_decode_metadata_gb300 import binding as B
+from paged_kv_decode_metadata_gb300 import build
+from test_gpu_cache_ops import SCALE, Cache, Tree, evict, random_parents, same_bits
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def lib():
+    build.build()
+    B.load()
+    B.pa_read_error_flags(reset=True)
+    yield
+    assert B.pa_read_error_flags(reset=True) == 0
+
+
+# ---- accumulated weights of reused rows -----------------------------------------------------
+
+
+@pytest.mark.parametrize("kv", ["bf16", "int8"])
+@pytest.mark.parametrize("hkv,page", [(1, 16), (3, 64)])
+def test_append_clears_the_weights_of_the_rows_it_writes(kv, hkv, page):
+    """Those rows' weights become 0 in every head; padded tokens' rows, and all others, keep theirs."""
+    tokens = 70
+    c = Cache([tokens], hkv, page, kv, 5, poison=False)
+    x = torch.randn((tokens, 4 * hkv, 128), generator=c.g).to(torch.bfloat16).cuda()
+    q, k, v = x.split([2 * hkv, hkv, hkv], dim=1)
+    at = torch.randperm(tokens, generator=c.g)
+    slots = c.table[0].long()[at // page] * page + at % page
+    slots[3], slots[69] = -1, -5
+    kw = dict(q=q, k=k, v=v, positions=at.cuda(), slots=slots.cuda(), inv_freq=B.pa_rope_frequencies(128).cuda(),
+              q_out=torch.empty((tokens, 2 * hkv, 128), dtype=torch.bfloat16, device="cuda"), k_cache=c.d_k,
+              v_cache=c.d_v, k_scale=c.d_ks, v_scale=c.d_vs)
+    B.pa_rope_append(**kw)                               # without the weights: none change
+    assert same_bits(c.d_w, c.weights)
+    plain = [t.clone() for t in (kw["q_out"], c.d_k, c.d_v)]
+    B.prepare_rope_append(weights=c.d_w, **kw)()
+    want = c.weights.clone()
+    for s in slots.tolist():
+        if s >= 0:
+            want[s // page, :, s % page] = 0
+    assert same_bits(c.d_w, want)
+    for a, b in zip(plain, (kw["q_out"], c.d_k, c.d_v)):
+        assert same_bits(a, b)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "int8"])
+def test_loop_adds_up_weights_by_token(kv):
+    """Append, verify, keep the path, append, decode, accumulate, evict in place, three times.  The
+    host keeps every token's total itself (0 when it is appended); the pool's weight of each
+    live row stays that token's, whatever stood in the row before."""
+    hq, hkv, page, msp = 8, 2, 16, 24
+    n = [200, 37]
+    g = torch.Generator().manual_seed(81)
+    r = random.Random(82)
+    c = Cache([msp * page] * 2, hkv, page, kv, 83, poison=False)
+    # rows past the prompt hold what other requests left
+    total = c.weights.double()
+    for b in range(2):
+        j = torch.arange(n[b])
+        total[c.table[b].long()[j // page], :, j % page] = 0
+    c.d_w.copy_(total.float())
+    slack = torch.zeros_like(total)
+    freq = B.pa_rope_frequencies(64)
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32).cuda()
+
+    def append(count):
+        t = sum(count)
+        x = torch.randn((t, hq + 2 * hkv, 128), generator=g).to(torch.bfloat16).cuda()
+        q, k, v = x.split([hq, hkv, hkv], dim=1)
+        where = [(b, n[b] + i) for b in range(2) for i in range(count[b])]
+        slots = torch.tensor([int(c.table[b, j // page]) * page + j % page for b, j in where])
+        q_out = torch.empty((t, hq, 128), dtype=torch.bfloat16, device="cuda")
+        B.pa_rope_append(q=q, k=k, v=v, positions=torch.tensor([j for _, j in where]).cuda(),
+                         slots=slots.cuda(), inv_freq=freq.cuda(), q_out=q_out, k_cache=c.d_k, v_cache=c.d_v,
+                         k_scale=c.d_ks, v_scale=c.d_vs, weights=c.d_w)
+        for b, j in where:                               # a new token has been attended to by none
+            at = int(c.table[b, j // page]), slice(None), j % page
+            total[at] = slack[at] = 0
+        for b in range(2):
+            n[b] += count[b]
+        c.n, c.d_n = list(n), i32(n)
+        return q_out
+
+    def attend(q, count, masks):
+        t = Tree(c, count, hq, 0, masks=masks)
+        t.q = q.cpu()
+        return t.run(0)[1]
+
+    for _ in range(3):
+        count = [7, 5]
+        parents = [random_parents(r, k) for k in count]
+        attend(append(count), count, [m for p in parents for m in R.ancestor_rows(p)])
+        begin = [a - b for a, b in zip(n, count)]
+        kept = torch.full((2, 1, 7), -1, dtype=torch.int32)
+        path = []
+        for b, p in enumerate(parents):
+            node, nodes = len(p) - 1, []
+            while node >= 0:
+                nodes.append(begin[b] + node)
+                node = p[node]
+            path.append(nodes[::-1])
+            kept[b, 0, :len(nodes)] = torch.tensor(path[b])
+        new = torch.empty(2, dtype=torch.int32, device="cuda")
+        B.pa_compact_cache(page_table=c.d_table, cache_seqlens=c.d_n, kept=kept.cuda(),
+                           counts=i32([len(p) for p in path]), begin=i32(begin), k_cache=c.d_k,
+                           v_cache=c.d_v, k_scale=c.d_ks, v_scale=c.d_vs, weights=c.d_w,
+                           max_seq_pages=msp, new_seqlens=new)
+        n[:] = new.tolist()
+        total, slack = R.move([total, slack], c.table, c.table, [[p] * hkv for p in path], begin)
+        q = append([1, 1])
+        lse = attend(q, [1, 1], [1, 1])
+        B.pa_accumulate_weights(q=q, lse=lse, k_cache=c.d_k, k_scale=c.d_ks, page_table=c.d_table,
+                                cache_seqlens=c.d_n, weights=c.d_w, max_seq_pages=msp, sm_scale=SCALE)
+        ks = c.d_ks.cpu() if kv == "int8" else None
+        total, more = R.accumulate(total, q.cpu(), lse.cpu(), c.d_k.cpu(), ks, c.table, n, SCALE)
+        slack = slack + more
+        c.weights = c.d_w.cpu()
+        lists = []
+        for b in range(2):
+            j = torch.arange(n[b])
+            at = c.table[b].long()[j // page], slice(None), j % page
+            err = (c.weights[at].double() - total[at]).abs()
+            assert bool((err <= slack[at]).all()), float((err - slack[at]).max())
+            lists.append([R.kept_positions(c.weights[at][:, h].tolist(), n[b], 60, 2, 20) for h in range(hkv)])
+        got, _, _ = evict(c, 60, 2, 20, True)
+        for b in range(2):
+            for h in range(hkv):
+                assert got[b, h].tolist()[:len(lists[b][h])] == lists[b][h]
+        total, slack = R.move([total, slack], c.table, c.table, lists, [0, 0])
+        n[:] = [min(x, 60) for x in n]
