@@ -579,7 +579,8 @@ PA_API pa_status pa_build_tree_mask(const int32_t* parents, const int32_t* cu_se
  * tree_mask row i is set (bits t >= q_len are ignored; the caller sets bit i for the
  * query's own token).  A query that attends to nothing gives out = 0, lse = -inf.
  *   out [total_q, num_q_heads, 128] bf16;  lse [total_q, num_q_heads] fp32 or NULL; rows at
- *   or past cu_seqlens_q[bs] (padding of a captured batch) are not touched.
+ *   or past cu_seqlens_q[bs] (padding of a captured batch), before cu_seqlens_q[0], and of a
+ *   request whose rows are refused (more than max_q_len, outside [0, total_q)) are not touched.
  *   tree_mask [total_q, mask_words] int64, mask_words >= ceil(max_q_len / 64)
  * K/V pools, scales, page_table and cache_seqlens as for pa_decode_splitk (page_table as the
  * metadata stage writes it).  K of positions that a query does not attend to may hold

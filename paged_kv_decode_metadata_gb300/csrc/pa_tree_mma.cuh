@@ -106,13 +106,16 @@ struct Walk {
   int base, pos, end, share;                // its start on the line; where the walk is
   bool whole;                               // units are not cut
 
-  // Lengths of request r, checked; `report` records what is wrong with them.
-  __device__ __forceinline__ void load(const TreeParams& prm, int page_size, int r, bool report) {
+  // Lengths of request r, checked; `report` records what is wrong with them.  False: its query
+  // rows are refused.
+  __device__ __forceinline__ bool load(const TreeParams& prm, int page_size, int r, bool report) {
     b = r;
     q_begin = prm.cu_seqlens_q[r];
     q_len = prm.cu_seqlens_q[r + 1] - q_begin;
     n = prm.cache_seqlens[r];
-    if (q_begin < 0 || q_len < 0 || q_len > prm.max_q_len || q_begin > prm.total_q - q_len) {
+    const bool fits =
+        q_begin >= 0 && q_len >= 0 && q_len <= prm.max_q_len && q_begin <= prm.total_q - q_len;
+    if (!fits) {
       if (report) record_error(prm.err, kErrSeqLenOutOfRange);
       q_len = 0;
     }
@@ -123,23 +126,27 @@ struct Walk {
     }
     pairs = ((q_len << prm.group_shift) + 2 * kTile - 1) / (2 * kTile);
     chunks = (n + kTile - 1) / kTile;
+    return fits;
   }
   __device__ __forceinline__ int length(const TreeParams& prm) const {
     return pairs * prm.num_kv_heads * chunks;
   }
 
-  // Whole-warp: finds the block's share.  Returns whether some request has queries but
-  // nothing cached (its rows are no work, but have a result).
-  __device__ __forceinline__ bool start(const TreeParams& prm, int page_size, int lane, bool report) {
+  // Whole-warp: finds the block's share.  Returns kEmpties where some request has queries but
+  // nothing cached (its rows are no work, but have a result), kGaps where rows before the last
+  // request's end belong to none: those before the first request's and refused ones.
+  static constexpr uint32_t kEmpties = 1, kGaps = 2;
+  __device__ __forceinline__ uint32_t start(const TreeParams& prm, int page_size, int lane, bool report) {
     int total = 0, first_sum = 0, first_w = 0;  // the first 32 requests' lengths are kept
     int longest = 0, shortest = INT_MAX;        // units, in chunks
-    bool empties = false;
+    uint32_t special = 0;
     for (int r0 = 0; r0 < prm.bs; r0 += 32) {
       int w = 0;
       if (r0 + lane < prm.bs) {
-        load(prm, page_size, r0 + lane, report);
+        const bool fits = load(prm, page_size, r0 + lane, report);
         w = length(prm);
-        empties = empties || (q_len > 0 && n == 0);
+        if (!fits || (r0 + lane == 0 && q_begin != 0)) special |= kGaps;
+        if (q_len > 0 && n == 0) special |= kEmpties;
         if (w > 0) {
           longest = max(longest, chunks);
           shortest = min(shortest, chunks);
@@ -157,7 +164,7 @@ struct Walk {
       }
       total += __shfl_sync(0xffffffffu, incl, 31);
     }
-    empties = __any_sync(0xffffffffu, empties);
+    special = __reduce_or_sync(0xffffffffu, special);
     const int grid = static_cast<int>(gridDim.x);
     longest = __reduce_max_sync(0xffffffffu, longest);
     shortest = __reduce_min_sync(0xffffffffu, shortest);
@@ -170,7 +177,7 @@ struct Walk {
     const long long at_ll = static_cast<long long>(blockIdx.x) * share;
     pos = static_cast<int>(min(at_ll, static_cast<long long>(total)));
     end = static_cast<int>(min(at_ll + share, static_cast<long long>(total)));
-    if (pos >= end) return empties;
+    if (pos >= end) return special;
     // the request that holds pos and, where units are not cut, the unit starts at or after
     // pos and end
     int at = 0, new_end = end < total ? end : total, found = -1, found_base = 0;
@@ -220,7 +227,7 @@ struct Walk {
       pos = base + (pos - base + chunks - 1) / chunks * chunks;
       end = new_end;
     }
-    return empties;
+    return special;
   }
 
   __device__ __forceinline__ bool next(const TreeParams& prm, int page_size, Piece& p) {
@@ -353,8 +360,8 @@ __global__ void __launch_bounds__(Roles<kQuant>::kThreads, 1)
   grid_dependency_wait();
 
   Walk walk;
-  const bool empties = walk.start(prm, P, lane, blockIdx.x == 0 && warp == 0);
-  if (empties) {  // requests with queries and an empty cache
+  const uint32_t special = walk.start(prm, P, lane, blockIdx.x == 0 && warp == 0);
+  if (special & Walk::kEmpties) {  // requests with queries and an empty cache
     Walk w;
     for (int r = blockIdx.x; r < prm.bs; r += gridDim.x) {
       w.load(prm, P, r, false);
@@ -366,6 +373,20 @@ __global__ void __launch_bounds__(Roles<kQuant>::kThreads, 1)
       }
       for (int i = tid; i < w.q_len * prm.num_q_heads * 16; i += kThreads)
         static_cast<uint4*>(prm.out)[first * 16 + i] = make_uint4(0u, 0u, 0u, 0u);
+    }
+  }
+  if ((special & Walk::kGaps) && S > 1) {  // the join leaves a row alone whose first sum is negative
+    const int rows = max(0, min(prm.cu_seqlens_q[prm.bs], prm.total_q));
+    for (int64_t row = static_cast<int64_t>(blockIdx.x) * kThreads + tid; row < rows;
+         row += static_cast<int64_t>(gridDim.x) * kThreads) {
+      Walk w;
+      bool covered = false;
+      for (int r = 0; r < prm.bs && !covered; ++r) {
+        w.load(prm, P, r, false);
+        covered = row >= w.q_begin && row < w.q_begin + w.q_len;
+      }
+      for (int h = 0; h < prm.num_q_heads && !covered; ++h)
+        prm.l_out[(row * prm.num_q_heads + h) * S] = -1.f;
     }
   }
 

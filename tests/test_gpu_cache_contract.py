@@ -138,3 +138,44 @@ def test_loop_adds_up_weights_by_token(kv):
                 assert got[b, h].tolist()[:len(lists[b][h])] == lists[b][h]
         total, slack = R.move([total, slack], c.table, c.table, lists, [0, 0])
         n[:] = [min(x, 60) for x in n]
+
+
+# ---- query rows that no request covers --------------------------------------------------------
+
+
+@pytest.mark.parametrize("kv", ["bf16", "int8"])
+@pytest.mark.parametrize("splits", [1, 3])
+def test_rows_before_the_first_request_are_left(kv, splits):
+    c = Cache([900, 260], 2, 64, kv, 7)
+    t = Tree(c, [4, 6], 8, 8)
+    want = t.run(splits)
+    front = 3
+    rows = t.total + front
+    q = torch.zeros((rows, 8, 128), dtype=torch.bfloat16)
+    q[front:] = t.q
+    mask = torch.full((rows, 1), -1, dtype=torch.int64)
+    mask[front:] = R.mask_tensor(t.masks, 1)
+    out, lse = t.run(splits, pad=front, q=q.cuda(), tree_mask=mask.cuda(), cu_seqlens_q=(t.cu + front).cuda())
+    assert bool((out[:front] == 7.0).all()) and bool((lse[:front] == 7.0).all())
+    assert same_bits(out[front:], want[0]) and same_bits(lse[front:], want[1])
+
+
+@pytest.mark.parametrize("kv", ["bf16", "int8"])
+@pytest.mark.parametrize("splits", [1, 3])
+@pytest.mark.parametrize("bs", [3, 40])
+def test_rows_of_a_refused_request_are_left(kv, splits, bs):
+    """A request with more rows than max_q_len is reported and not run; its rows stay as they were, and
+    the others' are right."""
+    n = [300 + 37 * i for i in range(bs)]
+    q_lens = [4] * bs
+    bad = bs - 2
+    q_lens[bad] = 5
+    c = Cache(n, 2, 64, kv, 17)
+    t = Tree(c, q_lens, 8, 18)
+    out, lse = t.run(splits, max_q_len=4)
+    assert B.pa_read_error_flags(reset=True) == B.DEVERR_SEQLEN_OUT_OF_RANGE
+    lo = sum(q_lens[:bad])
+    assert bool((out[lo:lo + 5] == 7.0).all()) and bool((lse[lo:lo + 5] == 7.0).all())
+    full = t.run(splits)
+    out[lo:lo + 5], lse[lo:lo + 5] = full[0][lo:lo + 5], full[1][lo:lo + 5]
+    t.check(out, lse)
