@@ -577,7 +577,8 @@ PA_API pa_status pa_build_tree_mask(const int32_t* parents, const int32_t* cu_se
  * tokens, already in its cache in the same order.  With n = cache_seqlens[b], query i
  * attends to every position j < n - q_len and to position n - q_len + t where bit t of
  * tree_mask row i is set (bits t >= q_len are ignored; the caller sets bit i for the
- * query's own token).  A query that attends to nothing gives out = 0, lse = -inf.
+ * query's own token).  A query that attends to nothing gives out = 0, lse = -inf; one with a
+ * NaN score among those it attends to gives NaN in both.
  *   out [total_q, num_q_heads, 128] bf16;  lse [total_q, num_q_heads] fp32 or NULL; rows at
  *   or past cu_seqlens_q[bs] (padding of a captured batch), before cu_seqlens_q[0], and of a
  *   request whose rows are refused (more than max_q_len, outside [0, total_q)) are not touched.

@@ -74,12 +74,14 @@ __global__ void __launch_bounds__(kJoinWarps * 32) tree_join_kernel(const TreePa
     const float* l = p.l_out + row * S;
     const float4* acc = reinterpret_cast<const float4*>(p.acc_out) + row * S * 32 + lane;
     float top = -CUDART_INF_F, total = 0.f;
+    bool nan = false;  // a piece had a NaN score: its sum is NaN, its maximum may be -inf
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int s0 = 0; s0 < S; s0 += 32) {
       const float ls = s0 + lane < S ? l[s0 + lane] : -1.f;
       const uint32_t ends = __ballot_sync(0xffffffffu, ls < 0.f);
       const int count = ends != 0 ? __ffs(ends) - 1 : 32;
       const float ms = lane < count ? m[s0 + lane] : -CUDART_INF_F;
+      nan = nan || __any_sync(0xffffffffu, lane < count && ls != ls);
       const float new_top = fmaxf(top, warp_max(ms));
       if (new_top != -CUDART_INF_F) {
         const float keep = top == -CUDART_INF_F ? 0.f : expf(top - new_top);
@@ -105,13 +107,14 @@ __global__ void __launch_bounds__(kJoinWarps * 32) tree_join_kernel(const TreePa
       }
       if (count < 32) break;
     }
-    const float inv = top == -CUDART_INF_F ? 0.f : 1.f / total;
+    if (nan) total = CUDART_NAN_F;
+    const float inv = top == -CUDART_INF_F && !nan ? 0.f : 1.f / total;
     const __nv_bfloat162 lo = __floats2bfloat162_rn(o.x * inv, o.y * inv);
     const __nv_bfloat162 hi = __floats2bfloat162_rn(o.z * inv, o.w * inv);
     static_cast<uint2*>(p.out)[row * 32 + lane] = make_uint2(
         *reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
     if (p.lse != nullptr && lane == 0)
-      p.lse[row] = top == -CUDART_INF_F ? top : top + logf(total);
+      p.lse[row] = top == -CUDART_INF_F && !nan ? top : top + logf(total);
   }
 }
 

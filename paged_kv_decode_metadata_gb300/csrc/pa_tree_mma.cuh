@@ -748,7 +748,9 @@ __global__ void __launch_bounds__(Roles<kQuant>::kThreads, 1)
       if (write && (two || s == 0)) {
         const float m_nat = m_ref * 0.69314718055994530942f;  // -inf stays -inf
         if (direct) {
-          if (prm.lse != nullptr) prm.lse[slot] = m_ref == -CUDART_INF_F ? m_ref : m_nat + logf(l);
+          // (l is NaN where a score was: m_ref, a maximum, does not show it)
+          if (prm.lse != nullptr)
+            prm.lse[slot] = m_ref == -CUDART_INF_F && l == l ? m_ref : m_nat + logf(l);
           if (S > 1) prm.l_out[slot * S] = -1.f;  // nothing to combine
         } else {
           prm.m_out[slot * S + p.slot] = m_nat;

@@ -1,6 +1,7 @@
 """What the header promises of the cache operators at the edges of a serving loop, beside the
 plain cases of test_gpu_cache_ops.py."""
 
+import math
 import random
 
 import pytest
@@ -179,3 +180,38 @@ def test_rows_of_a_refused_request_are_left(kv, splits, bs):
     full = t.run(splits)
     out[lo:lo + 5], lse[lo:lo + 5] = full[0][lo:lo + 5], full[1][lo:lo + 5]
     t.check(out, lse)
+
+
+# ---- NaN scores --------------------------------------------------------------------------------
+
+
+@pytest.mark.parametrize("kv", ["bf16", "int8"])
+@pytest.mark.parametrize("splits", [1, 4])
+@pytest.mark.parametrize("nodes", [6, 40])
+def test_tree_nan_query_gives_nan(kv, splits, nodes):
+    """A query with NaN gets NaN (out and lse), however its context is cut; one that sees nothing
+    still gets 0 and -inf; the others keep their bits."""
+    c = Cache([900, 20], 2, 64, kv, 31)
+    masks = [m for p in ([-1] * nodes, [-1] * nodes) for m in R.ancestor_rows(p)]
+    masks[nodes + 1] = 0
+    t = Tree(c, [nodes, min(nodes, 20)], 16, 32, masks=masks[:nodes + min(nodes, 20)])
+    clean = t.run(splits)
+    t.q[2, 5, 7] = math.nan                              # one head of one query
+    t.q[nodes + 3, 0, 0] = math.nan
+    out, lse = t.run(splits)
+    for row, head in ((2, 5), (nodes + 3, 0)):
+        assert bool(torch.isnan(out[row, head]).all()) and bool(torch.isnan(lse[row, head]))
+        out[row, head], lse[row, head] = clean[0][row, head], clean[1][row, head]
+    assert same_bits(out, clean[0]) and same_bits(lse, clean[1])
+
+
+@pytest.mark.parametrize("splits", [1, 6])
+def test_tree_nan_key_of_a_committed_position_gives_nan(splits):
+    """A NaN key far from the others' pieces reaches every query of its kv head and no other."""
+    c = Cache([1500], 2, 64, "bf16", 33)
+    t = Tree(c, [3], 4, 34)
+    clean = t.run(splits)
+    c.d_k[int(c.table[0, 0]), 1, 5] = math.nan
+    out, lse = t.run(splits)
+    assert bool(torch.isnan(out[:, 2:]).all()) and bool(torch.isnan(lse[:, 2:]).all())
+    assert same_bits(out[:, :2], clean[0][:, :2]) and same_bits(lse[:, :2], clean[1][:, :2])
