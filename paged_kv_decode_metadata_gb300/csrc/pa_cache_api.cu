@@ -291,10 +291,6 @@ pa_status pa_tree_attention(const void* q, const void* k_cache, const void* v_ca
   p.num_splits = splits;
   for (int g = num_q_heads / num_kv_heads; g > 1; g >>= 1) ++p.group_shift;
   const int64_t chunks = cdiv(static_cast<int64_t>(max_seq_pages) * page_size, 128);
-  // a unit of c chunks meets at most floor((c - 1) / share) + 2 shares (c of them if share = 1)
-  p.min_share = splits == 1 || splits >= chunks
-                    ? 1
-                    : static_cast<int32_t>(cdiv(chunks, splits - 1));
   const int64_t most = static_cast<int64_t>(bs) * num_kv_heads *
                        cdiv(static_cast<int64_t>(num_q_heads / num_kv_heads) * max_q_len, 256) * chunks;
   int64_t sms = pa::sm_count_of_current_device();

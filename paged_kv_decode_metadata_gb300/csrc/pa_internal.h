@@ -136,7 +136,6 @@ struct TreeParams {
   int64_t num_pages;
   int32_t max_seq_pages;
   int32_t num_splits;  // most pieces of a row's context (partial slots per row)
-  int32_t min_share;   // fewest chunks in a block's share (keeps the pieces within num_splits)
   int32_t blocks;
   int32_t group_shift;  // log2 of the query heads per kv head
   float q_scale;  // sm_scale * log2(e)

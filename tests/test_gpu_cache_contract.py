@@ -215,3 +215,29 @@ def test_tree_nan_key_of_a_committed_position_gives_nan(splits):
     out, lse = t.run(splits)
     assert bool(torch.isnan(out[:, 2:]).all()) and bool(torch.isnan(lse[:, 2:]).all())
     assert same_bits(out[:, :2], clean[0][:, :2]) and same_bits(lse[:, :2], clean[1][:, :2])
+
+
+# ---- page tables wider than the lengths need ----------------------------------------------------
+
+
+@pytest.mark.parametrize("kv", ["bf16", "int8"])
+@pytest.mark.parametrize("seqlens", [[900, 400, 77], [2000] * 5, [5000]])
+def test_tree_cuts_do_not_depend_on_the_tables_width(kv, seqlens):
+    """The same pieces (their sums in the workspace) and the same bits from a table of the
+    longest request's width and from one sized for contexts 64 times as long."""
+    c = Cache(seqlens, 4, 64, kv, 21)
+    t = Tree(c, [5] * len(seqlens), 16, 22)
+    wide = torch.full((len(seqlens), 64 * c.msp), -1, dtype=torch.int32)
+    wide[:, :c.msp] = c.table
+    splits, rows = 6, t.total * 16 * 6
+    start = -(-rows * 4 // 256) * 256                    # m, then l, each on 256 bytes
+    got = []
+    for table, msp in ((c.d_table, c.msp), (wide.cuda(), 64 * c.msp)):
+        ws = torch.full((B.pa_workspace_bytes(t.total, 16, 128, splits),), 255, dtype=torch.uint8, device="cuda")
+        out, lse = t.run(splits, page_table=table, max_seq_pages=msp, workspace=ws)
+        t.check(out, lse)
+        got.append((out, lse, ws[start:start + rows * 4].view(torch.int32)))
+    for a, b in zip(*got):
+        assert same_bits(a, b)
+    if len(seqlens) == 1:                                # (four units over the whole device: cut)
+        assert bool((got[1][2].view(torch.float32).view(-1, splits)[:, 0] >= 0).all())
