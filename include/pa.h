@@ -591,9 +591,9 @@ PA_API pa_status pa_build_tree_mask(const int32_t* parents, const int32_t* cu_se
  * pa_choose_tree_splits(...).  With 1 the output is written directly and `workspace` may be
  * NULL; otherwise the partials of rows that are cut go to `workspace` (16-byte aligned,
  * workspace_bytes >= pa_workspace_bytes(total_q, num_q_heads, 128, that number)) and a
- * second launch combines them.  The cuts follow from the lengths on the device (not from
- * max_seq_pages, but for what num_splits == 0 makes of it), so equal inputs give equal bits.  Calls that overlap on the GPU need
- * workspaces of their own.
+ * second launch combines them.  The cuts follow from num_splits and the lengths on the
+ * device, so equal inputs give equal bits.  Calls that overlap on the GPU need workspaces of
+ * their own.
  * sm_scale is finite and positive.
  * Supported: head_dim 128; page_size 16, 32, 64, 128; num_q_heads / num_kv_heads in {1, 2,
  * 4, 8, 16}; 1 <= max_q_len <= 256; max_seq_pages * page_size <= 2^29 and bs *

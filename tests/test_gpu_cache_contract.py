@@ -241,3 +241,64 @@ def test_tree_cuts_do_not_depend_on_the_tables_width(kv, seqlens):
         assert same_bits(a, b)
     if len(seqlens) == 1:                                # (four units over the whole device: cut)
         assert bool((got[1][2].view(torch.float32).view(-1, splits)[:, 0] >= 0).all())
+
+
+@pytest.mark.parametrize("kv,hq", [("bf16", 8), ("int8", 8), ("bf16", 32)])
+def test_weights_do_not_depend_on_the_tables_width(kv, hq):
+    """Blocks with one run of tokens and with several give the same bits: a row gets one sum."""
+    seqlens = [3000, 1, 700, 2049]
+    c = Cache(seqlens, 2, 64, kv, 23)
+    q = torch.randn((4, hq, 128), generator=c.g).to(torch.bfloat16).cuda()
+    lse = torch.full((4, hq), 6.0, device="cuda")
+    got = []
+    for width in (c.msp, 4096, 65536):
+        table = torch.full((4, width), -1, dtype=torch.int32)
+        table[:, :c.msp] = c.table
+        w = c.d_w.clone()
+        B.pa_accumulate_weights(q=q, lse=lse, k_cache=c.d_k, k_scale=c.d_ks, page_table=table.cuda(),
+                                cache_seqlens=c.d_n, weights=w, max_seq_pages=width, sm_scale=SCALE)
+        got.append(w)
+    want, bound = R.accumulate(c.weights, q.cpu(), lse.cpu(), c.k, c.ks, c.table, seqlens, SCALE)
+    assert bool(((got[0].cpu().double() - want).abs() <= bound).all())
+    assert same_bits(got[0], got[1]) and same_bits(got[0], got[2])
+
+
+def test_weights_of_long_contexts_in_several_runs():
+    """Requests that reach past the first run of every block."""
+    c = Cache([150001, 140000], 1, 128, "int8", 24)
+    q = torch.randn((2, 4, 128), generator=c.g).to(torch.bfloat16)
+    lse = torch.full((2, 4), 6.0)
+    table = torch.full((2, 16 * c.msp), -1, dtype=torch.int32)
+    table[:, :c.msp] = c.table
+    B.pa_accumulate_weights(q=q.cuda(), lse=lse.cuda(), k_cache=c.d_k, k_scale=c.d_ks, page_table=table.cuda(),
+                            cache_seqlens=c.d_n, weights=c.d_w, max_seq_pages=16 * c.msp, sm_scale=SCALE)
+    want, bound = R.accumulate(c.weights, q, lse, c.k, c.ks, c.table, c.n, SCALE)
+    assert bool(((c.d_w.cpu().double() - want).abs() <= bound).all())
+
+
+def test_weights_time_does_not_follow_the_tables_width():
+    """Short contexts under a table for a million tokens: no more than three times as long as under
+    a table of their own (1.1 times; 9 with a block for each run of the table)."""
+    bs, hkv, page, n = 32, 8, 64, 4096
+    pool = torch.zeros((n // page * 2, hkv, page, 128), dtype=torch.bfloat16, device="cuda")
+    w = torch.zeros(pool.shape[:3], device="cuda")
+    q = torch.zeros((bs, 4 * hkv, 128), dtype=torch.bfloat16, device="cuda")
+    lse = torch.zeros((bs, 4 * hkv), device="cuda")
+    lens = torch.full((bs,), n, dtype=torch.int32, device="cuda")
+    times = []
+    for width in (n // page, (1 << 20) // page):
+        table = torch.zeros((bs, width), dtype=torch.int32, device="cuda")
+        table[:, :n // page] = torch.arange(n // page, device="cuda")
+        call = B.prepare_accumulate_weights(q=q, lse=lse, k_cache=pool, page_table=table, cache_seqlens=lens,
+                                            weights=w, max_seq_pages=width, sm_scale=SCALE)
+        runs = []
+        for _ in range(5):
+            start, stop = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            start.record()
+            for _ in range(20):
+                call()
+            stop.record()
+            torch.cuda.synchronize()
+            runs.append(start.elapsed_time(stop))
+        times.append(sorted(runs)[2])
+    assert times[1] < 3 * times[0], times
