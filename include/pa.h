@@ -594,7 +594,7 @@ PA_API pa_status pa_build_tree_mask(const int32_t* parents, const int32_t* cu_se
  * second launch combines them.  The cuts follow from num_splits and the lengths on the
  * device, so equal inputs give equal bits.  Calls that overlap on the GPU need workspaces of
  * their own.
- * sm_scale is finite and positive.
+ * sm_scale is positive, sm_scale * log2(e) finite in fp32.
  * Supported: head_dim 128; page_size 16, 32, 64, 128; num_q_heads / num_kv_heads in {1, 2,
  * 4, 8, 16}; 1 <= max_q_len <= 256; max_seq_pages * page_size <= 2^29 and bs *
  * num_kv_heads * ceil(num_q_heads / num_kv_heads * max_q_len / 256) * ceil(max_seq_pages *
@@ -648,10 +648,11 @@ PA_API size_t pa_tree_workspace_bytes(int32_t bs, int32_t total_q, int32_t max_q
  * with the step's q [bs, num_q_heads, 128] bf16 and lse [bs, num_q_heads] fp32 (a head with
  * lse = -inf adds nothing).  weights [num_pages, num_kv_heads, page_size] fp32, kept with
  * the pools; pools, tables and limits as for pa_decode_splitk (k_scale: int8 only), and
- * max_seq_pages * page_size <= 2^30.  Rows of
- * other positions are not touched.  A row's weight has to be 0 when its token enters the
- * cache (pa_rope_append_weights, or the caller, sees to that).  A page that several requests share gets all of their
- * weights, in an order that is not fixed; otherwise the result is the same every time.
+ * max_seq_pages * page_size <= 2^30; sm_scale * log2(e) finite in fp32.  Rows of other
+ * positions are not touched.  A row's weight has to be 0 when its token enters the cache
+ * (pa_rope_append_weights, or the caller, sees to that).  A page that several requests share
+ * gets all of their weights, in an order that is not fixed; otherwise the result is the same
+ * every time.
  */
 PA_API pa_status pa_accumulate_weights(
     const void* q, const float* lse, const void* k_cache, const float* k_scale, int32_t kv_dtype,

@@ -229,7 +229,7 @@ pa_status check_tree(const void* q, const void* k_cache, const void* v_cache, co
   if (st != PA_OK) return st;
   if (!cu_seqlens_q || !tree_mask || !aligned(tree_mask, 8)) return PA_ERR_INVALID;
   if (!out || !aligned(out, 16)) return PA_ERR_INVALID;
-  if (!std::isfinite(sm_scale) || !(sm_scale > 0.f)) return PA_ERR_INVALID;
+  if (!std::isfinite(sm_scale * 1.4426950408889634f) || !(sm_scale > 0.f)) return PA_ERR_INVALID;
   if (*splits > 1 &&
       (!workspace || !aligned(workspace, 16) ||
        workspace_bytes < pa_workspace_bytes(total_q, num_q_heads, head_dim, *splits)))
@@ -363,6 +363,9 @@ pa_status pa_accumulate_weights(const void* q, const float* lse, const void* k_c
                                      num_kv_heads, head_dim, page_size, num_pages, max_seq_pages, 1);
   if (st != PA_OK || bs == 0) return st;
   if (!lse || !weights || !aligned(lse, 4) || !aligned(weights, 16)) return PA_ERR_INVALID;
+  const float q_scale = sm_scale * 1.4426950408889634f;  // log2(e): the kernel works in base 2
+  // (a sum that has become NaN stays it, and ranks above every other)
+  if (!std::isfinite(q_scale)) return PA_ERR_INVALID;
   if (static_cast<int64_t>(max_seq_pages) * page_size > kMaxPositions) return PA_ERR_UNSUPPORTED;
   pa::WeightsParams p = {};
   p.q = q;
@@ -378,7 +381,7 @@ pa_status pa_accumulate_weights(const void* q, const float* lse, const void* k_c
   p.num_kv_heads = num_kv_heads;
   p.num_pages = num_pages;
   p.max_seq_pages = max_seq_pages;
-  p.q_scale = sm_scale * 1.4426950408889634f;
+  p.q_scale = q_scale;
   cudaError_t e = pa::error_word(&p.err);
   if (e != cudaSuccess) return pa::from_cuda(e, "error word lookup");
   return finish(pa::launch_weights(p, kv_dtype == PA_KV_INT8, num_q_heads / num_kv_heads, page_size,

@@ -264,3 +264,13 @@ ROPE_WEIGHTS = {**{k: v for k, v in list(ROPE.items())[:22]}, "w": FAKE,
 def test_rope_with_weights_refusals(lib, over, status):
     assert list(ROPE_WEIGHTS)[21:24] == ["vsc", "w", "kv"]
     assert _caller(lib.pa_rope_append_weights, ROPE_WEIGHTS)(**over) == status
+
+
+@pytest.mark.parametrize("scale", [math.nan, math.inf, -math.inf, 3e38])
+def test_weights_refuse_a_scale_that_is_not_finite(lib, scale):
+    """(3e38: not finite in base 2.)  Scales of 0 and below are a step's like any other."""
+    assert _caller(lib.pa_accumulate_weights, WEIGHTS)(scale=scale) == B.PA_ERR_INVALID
+
+
+def test_tree_refuses_a_scale_that_is_not_finite_in_base_2(lib):
+    assert _caller(lib.pa_tree_attention, TREE)(scale=3e38) == B.PA_ERR_INVALID
