@@ -677,7 +677,8 @@ PA_API pa_status pa_accumulate_weights(
  * included (tokens appended there later: pa_rope_append_weights).  A kept
  * position outside [0, cache_seqlens[b]), a target past dst_max_pages * page_size or, in
  * place, a kept position before its target is not moved and sets
- * PA_DEVERR_KEPT_OUT_OF_RANGE.  max_kept: the largest count; larger counts are cut to it.
+ * PA_DEVERR_KEPT_OUT_OF_RANGE.  max_kept: the largest count; larger counts are cut to it.  With
+ * 0, kept may be NULL and only new_seqlens is written.
  * Supported: head_dim 128; page_size 16, 32, 64, 128; max_seq_pages * page_size and max_kept
  * <= 2^30.
  */

@@ -404,7 +404,7 @@ pa_status compact_params(const int32_t* page_table, int64_t page_table_stride,
   pa_status st = check_pools(k_cache, v_cache, k_scale, v_scale, kv_dtype, num_kv_heads, head_dim,
                              page_size, num_pages);
   if (st != PA_OK) return st;
-  if (!page_table || !cache_seqlens || !kept || !dst_page_table) return PA_ERR_INVALID;
+  if (!page_table || !cache_seqlens || !dst_page_table) return PA_ERR_INVALID;
   if (bs > 65535 || max_seq_pages < 1 || page_table_stride < max_seq_pages || dst_max_pages < 1 ||
       dst_page_table_stride < dst_max_pages)
     return PA_ERR_INVALID;
@@ -458,7 +458,8 @@ pa_status pa_compact_cache(const int32_t* page_table, int64_t page_table_stride,
                                 dst_page_table, dst_page_table_stride, dst_max_pages, bs,
                                 num_kv_heads, head_dim, page_size, num_pages, &p, &in_place);
   if (st != PA_OK) return st;
-  if (!counts || max_kept < 0 || kept_stride < max_kept) return PA_ERR_INVALID;
+  if (!counts || max_kept < 0 || kept_stride < max_kept || (!kept && max_kept > 0))
+    return PA_ERR_INVALID;
   if (kept_heads != 1 && kept_heads != num_kv_heads) return PA_ERR_INVALID;
   if (max_kept > kMaxPositions) return PA_ERR_UNSUPPORTED;
   // the blocks read these while one of them writes new_seqlens
@@ -494,7 +495,7 @@ pa_status pa_evict(const int32_t* page_table, int64_t page_table_stride,
                                 dst_page_table, dst_page_table_stride, dst_max_pages, bs,
                                 num_kv_heads, head_dim, page_size, num_pages, &p, &in_place);
   if (st != PA_OK) return st;
-  if (!weights || !aligned(weights, 16) || !new_seqlens || new_seqlens == cache_seqlens)
+  if (!kept || !weights || !aligned(weights, 16) || !new_seqlens || new_seqlens == cache_seqlens)
     return PA_ERR_INVALID;
   if (budget < 1 || num_first < 0 || num_recent < 0 ||
       static_cast<int64_t>(num_first) + num_recent > budget)

@@ -274,3 +274,8 @@ def test_weights_refuse_a_scale_that_is_not_finite(lib, scale):
 
 def test_tree_refuses_a_scale_that_is_not_finite_in_base_2(lib):
     assert _caller(lib.pa_tree_attention, TREE)(scale=3e38) == B.PA_ERR_INVALID
+
+
+def test_compact_and_evict_need_their_lists(lib):
+    assert _caller(lib.pa_compact_cache, COMPACT)(kept=None, max_kept=1, ks=1) == B.PA_ERR_INVALID
+    assert _caller(lib.pa_evict, EVICT)(kept=None) == B.PA_ERR_INVALID

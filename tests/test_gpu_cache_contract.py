@@ -302,3 +302,21 @@ def test_weights_time_does_not_follow_the_tables_width():
             runs.append(start.elapsed_time(stop))
         times.append(sorted(runs)[2])
     assert times[1] < 3 * times[0], times
+
+
+# ---- empty lists ---------------------------------------------------------------------------------
+
+
+def test_compact_of_an_empty_list_only_writes_the_lengths():
+    """Nothing accepted anywhere: a list of no columns (whose tensor has no memory)."""
+    c = Cache([100, 30], 2, 64, "bf16", 41, poison=False)
+    before = [dev.clone() for _, dev in c.pools()]
+    new = torch.full((2,), 99, dtype=torch.int32, device="cuda")
+    B.pa_compact_cache(page_table=c.d_table, cache_seqlens=c.d_n,
+                       kept=torch.empty((2, 1, 0), dtype=torch.int32, device="cuda"),
+                       counts=torch.zeros(2, dtype=torch.int32, device="cuda"),
+                       begin=torch.tensor([95, 28], dtype=torch.int32).cuda(), k_cache=c.d_k, v_cache=c.d_v,
+                       weights=c.d_w, max_seq_pages=c.msp, new_seqlens=new)
+    assert new.tolist() == [95, 28]
+    for a, (_, dev) in zip(before, c.pools()):
+        assert same_bits(a, dev)
