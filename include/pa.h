@@ -587,7 +587,7 @@ PA_API pa_status pa_build_tree_mask(const int32_t* parents, const int32_t* cu_se
  * metadata stage writes it).  K of positions that a query does not attend to may hold
  * anything; so may V at or past n, but a non-finite V row below n reaches every query of
  * its request (a weight of 0 times it is NaN).
- * num_splits: the most pieces that a row's context may be cut into, or 0 for
+ * num_splits: the most pieces (1 to 4096) that a row's context may be cut into, or 0 for
  * pa_choose_tree_splits(...).  With 1 the output is written directly and `workspace` may be
  * NULL; otherwise the partials of rows that are cut go to `workspace` (16-byte aligned,
  * workspace_bytes >= pa_workspace_bytes(total_q, num_q_heads, 128, that number)) and a
@@ -596,8 +596,11 @@ PA_API pa_status pa_build_tree_mask(const int32_t* parents, const int32_t* cu_se
  * their own.
  * sm_scale is positive, sm_scale * log2(e) finite in fp32.
  * Supported: head_dim 128; page_size 16, 32, 64, 128; num_q_heads / num_kv_heads in {1, 2,
- * 4, 8, 16}; 1 <= max_q_len <= 256; max_seq_pages * page_size <= 2^29 and bs *
- * num_kv_heads * ceil(num_q_heads / num_kv_heads * max_q_len / 256) * ceil(max_seq_pages *
+ * 4, 8, 16}; 1 <= max_q_len <= 256; max_seq_pages * page_size <= 2^29 and, where num_splits
+ * is given, <= max(1, num_splits - 1) * 2^20 (the tensor cores truncate as they add: a piece
+ * of n tokens loses up to n 2^-25 of a sum whose terms have one sign; the library's own
+ * choice keeps pieces within 2^18, in one launch's workspace of up to 1 + ceil(tokens /
+ * 2^17) pieces a row); bs * num_kv_heads * ceil(num_q_heads / num_kv_heads * max_q_len / 256) * ceil(max_seq_pages *
  * page_size / 128) < 2^30.  All device memory.  Request lengths and row offsets
  * that only the device sees are bounds-checked like those of pa_decode_splitk_multi.
  */

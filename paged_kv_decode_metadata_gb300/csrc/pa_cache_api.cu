@@ -191,6 +191,11 @@ int32_t pa_choose_tree_splits(int32_t bs, int32_t max_q_len, int32_t num_q_heads
   int64_t share = units * chunks / sm_count;
   if (share < 1) share = 1;
   int64_t want = cdiv(2 * chunks, share) + 1;
+  // long contexts: pieces of half of the longest allowed, so that shares never grow past it
+  if (chunks > pa::kTreePieceChunks) {
+    const int64_t pieces = cdiv(2 * chunks, pa::kTreePieceChunks) + 1;
+    if (want < pieces) want = pieces;
+  }
   if (want > chunks) want = chunks;  // a piece holds a chunk at least
   if (want > 4096) want = 4096;
   return static_cast<int32_t>(want);
@@ -237,6 +242,9 @@ pa_status check_tree(const void* q, const void* k_cache, const void* v_cache, co
   if (max_q_len > kMaxTreeNodes) return PA_ERR_UNSUPPORTED;
   // keeps every position the kernel forms within int32
   if (static_cast<int64_t>(max_seq_pages) * page_size > (int64_t{1} << 29)) return PA_ERR_UNSUPPORTED;
+  // keeps a piece within 2^20 tokens, whose sums are good to a bf16 rounding
+  if (static_cast<int64_t>(max_seq_pages) * page_size > (int64_t{*splits > 1 ? *splits - 1 : 1} << 20))
+    return PA_ERR_UNSUPPORTED;
   // keeps the batch's chunks (128 tokens of up to 256 rows of a kv head) within 31 bits
   const int64_t tiles = cdiv(static_cast<int64_t>(num_q_heads / num_kv_heads) * max_q_len, 256);
   const int64_t chunks = cdiv(static_cast<int64_t>(max_seq_pages) * page_size, 128);

@@ -99,12 +99,13 @@ struct Piece {
 };
 
 // The batch as one line of chunks, unit after unit, cut into equal shares: block i takes
-// [i share, (i + 1) share).  Every warp walks its block's share by itself.  (The host keeps
-// the line's length within 31 bits.)
+// [i share, (i + 1) share), or several shares in a row where one each would be longer than a
+// piece should be.  Every warp walks its block's shares by itself.  (The host keeps the
+// line's length within 31 bits.)
 struct Walk {
   int b, q_begin, q_len, n, pairs, chunks;  // the request at hand
   int base, pos, end, share;                // its start on the line; where the walk is
-  bool whole;                               // units are not cut
+  int at_share;                             // and in which share; -1: units are not cut
 
   // Lengths of request r, checked; `report` records what is wrong with them.  False: its query
   // rows are refused.
@@ -174,16 +175,21 @@ struct Walk {
     // (From the lengths, not from the page table's width: under a table for 1M tokens that left
     // most SMs without work, 8 requests of 8K taking 1550 us against 54.)
     const int S = prm.num_splits;
-    share = S == 1 || S >= longest ? even : max(even, (longest + S - 2) / (S - 1));
+    int rounds = max(1, (even + kTreePieceChunks - 1) / kTreePieceChunks);  // shares per block
+    share = (even + rounds - 1) / rounds;
+    if (S > 1 && S < longest) share = max(share, (longest + S - 2) / (S - 1));
+    if (rounds > 1) rounds = (even + share - 1) / share;
     // Units of one length that fill the blocks well enough stay whole: partials and their
     // join cost more than up to a quarter of a share left idle (256 units on 152 SMs: whole
     // 169 / 382 us, cut 179 / 407 us for one and two tiles).
-    whole = S == 1 ||
-            (longest == shortest && (total / longest + grid - 1) / grid * longest <= share + share / 4);
-    if (whole) share = even;
-    const long long at_ll = static_cast<long long>(blockIdx.x) * share;
+    const bool whole =
+        S == 1 || (longest == shortest && longest <= kTreePieceChunks &&
+                   (total / longest + grid - 1) / grid * longest <= rounds * share + rounds * share / 4);
+    const int own = whole ? even : rounds * share;  // of the line, this block's
+    const long long at_ll = static_cast<long long>(blockIdx.x) * own;
     pos = static_cast<int>(min(at_ll, static_cast<long long>(total)));
-    end = static_cast<int>(min(at_ll + share, static_cast<long long>(total)));
+    at_share = whole ? -1 : static_cast<int>(blockIdx.x) * rounds;
+    end = static_cast<int>(min(at_ll + own, static_cast<long long>(total)));
     if (pos >= end) return special;
     // the request that holds pos and, where units are not cut, the unit starts at or after
     // pos and end
@@ -254,9 +260,11 @@ struct Walk {
     p.c1 = min(chunks, end - from);
     p.slot = 0;
     p.pieces = 1;
-    if (!whole) {
-      const int first = from / share;
-      p.slot = static_cast<int>(blockIdx.x) - first;
+    if (at_share >= 0) {
+      const int first = from / share, edge = (at_share + 1) * share;
+      p.c1 = min(p.c1, edge - from);
+      p.slot = at_share - first;
+      at_share += from + p.c1 == edge;
       p.pieces = (from + chunks - 1) / share - first + 1;
     }
     pos = from + p.c1;

@@ -279,3 +279,16 @@ def test_tree_refuses_a_scale_that_is_not_finite_in_base_2(lib):
 def test_compact_and_evict_need_their_lists(lib):
     assert _caller(lib.pa_compact_cache, COMPACT)(kept=None, max_kept=1, ks=1) == B.PA_ERR_INVALID
     assert _caller(lib.pa_evict, EVICT)(kept=None) == B.PA_ERR_INVALID
+
+
+@pytest.mark.parametrize("msp,splits", [((1 << 14) + 1, 1), ((1 << 14) + 1, 2), ((1 << 15) + 1, 3), (1 << 23, 512)])
+def test_tree_refuses_pieces_past_2_to_20_tokens(lib, msp, splits):
+    assert _caller(lib.pa_tree_attention, TREE)(msp=msp, pts=msp, S=splits, wsb=1 << 40) == B.PA_ERR_UNSUPPORTED
+
+
+def test_tree_splits_of_long_contexts():
+    # at least a piece for every 2^17 tokens and one more, from 2^18 tokens on
+    for tokens in (1 << 19, 1 << 20, 1 << 24):
+        assert B.pa_choose_tree_splits(64, 8, 32, 8, 64, tokens // 64, 152) >= (tokens >> 17) + 1
+    assert B.pa_choose_tree_splits(64, 8, 32, 8, 64, 1 << 23, 152) == 4096
+    assert B.pa_choose_tree_splits(64, 8, 32, 8, 64, (1 << 18) // 64, 152) <= 3

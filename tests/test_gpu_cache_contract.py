@@ -182,6 +182,42 @@ def test_rows_of_a_refused_request_are_left(kv, splits, bs):
     t.check(out, lse)
 
 
+# ---- long contexts -------------------------------------------------------------------------------
+
+
+@pytest.mark.parametrize("kv", ["bf16", "int8"])
+@pytest.mark.parametrize("nodes", [1, 160])
+def test_tree_sums_of_long_contexts(kv, nodes):
+    """Near-equal weights and V of one sign over 2^24 - 5 tokens (every page the same), in as many
+    units as fill the device.  The tensor cores truncate each sum of 4 tokens to the accumulator's
+    2^-23: pieces of 2^18 tokens are 2^16 such steps at most, 2^-7; then the output's rounding,
+    2^-8.  (Whole, the sums read 4 % low: fp32 does not hold an addend 2^-22 of its sum.)"""
+    n, bs, hkv = 2 ** 24 - 5, 19 if nodes == 1 else 2, 8
+    pages = -(-n // 128)
+    value = 0.69921875 if kv == "bf16" else 89.0
+    pools = {x + "_cache": torch.full((1, hkv, 128, 128), y, dtype=torch.bfloat16 if kv == "bf16" else torch.int8,
+                                      device="cuda") for x, y in (("k", 1), ("v", value))}
+    if kv == "int8":
+        pools |= {x: torch.ones((1, hkv, 128), device="cuda") for x in ("k_scale", "v_scale")}
+    rows = bs * nodes
+    out = torch.full((rows, hkv, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((rows, hkv), 7.0, device="cuda")
+    words = -(-nodes // 64)
+    B.pa_tree_attention(q=torch.zeros((rows, hkv, 128), dtype=torch.bfloat16, device="cuda"),
+                        page_table=torch.zeros((bs, pages), dtype=torch.int32, device="cuda"),
+                        cache_seqlens=torch.full((bs,), n, dtype=torch.int32, device="cuda"),
+                        cu_seqlens_q=torch.arange(bs + 1, dtype=torch.int32, device="cuda") * nodes,
+                        tree_mask=torch.full((rows, words), -1, dtype=torch.int64, device="cuda"),
+                        max_q_len=nodes, max_seq_pages=pages, sm_scale=SCALE, out=out, lse=lse,
+                        workspace=torch.empty(B.pa_tree_workspace_bytes(bs, rows, nodes, hkv, hkv, 128, 128, pages),
+                                              dtype=torch.uint8, device="cuda"), **pools)
+    torch.cuda.synchronize()
+    assert B.pa_read_error_flags(reset=True) == 0
+    err = (out.cpu().double() / value - 1).abs().max()
+    assert float(err) <= 2.0 ** -7 + 2.0 ** -8, float(err)
+    assert float((lse.cpu().double() - math.log(n)).abs().max()) <= 2.0 ** -20 * math.log(n)
+
+
 # ---- NaN scores --------------------------------------------------------------------------------
 
 
