@@ -1066,7 +1066,16 @@ __global__ void __launch_bounds__(Roles<kQuant>::kThreads, 1)
         const int valid = p.n - (p.c1 - 1) * kTile;  // tokens of the last chunk
         if (valid >= kTile) continue;
         const int slot = (it - 1) % kSlots;
-        if (!mbar_wait_bounded(&ctl.v_last[slot], (cleaned >> slot) & 1u)) {
+        // (this waits for all of the work before that tile, so the limit starts anew as long as
+        // tiles are issued)
+        bool ok = false;
+        for (int before = -1; !ok;) {
+          const int now = *static_cast<volatile int*>(&ctl.issued);
+          if (now == before || *abort_flag) break;
+          before = now;
+          ok = mbar_wait_bounded(&ctl.v_last[slot], (cleaned >> slot) & 1u);
+        }
+        if (!__all_sync(0xffffffffu, ok)) {
           if (lane == 0) give_up();
           break;
         }

@@ -218,6 +218,36 @@ def test_tree_sums_of_long_contexts(kv, nodes):
     assert float((lse.cpu().double() - math.log(n)).abs().max()) <= 2.0 ** -20 * math.log(n)
 
 
+@pytest.mark.parametrize("kv", ["bf16", "int8"])
+def test_tree_blocks_that_work_for_seconds(kv):
+    """2^29 - 1 tokens (a table's most, less one; every page the same) in as many units as fill the
+    device: no wait gives up although a block's cut V tile comes seconds after its start.  All
+    scores are 0 and V is 1, -1 or 0: the sums of 2^18 tokens, and of 2^11 pieces of them, are
+    integers that fp32 holds exactly, but for the last token's of 2^29."""
+    n, bs, hkv = 2 ** 29 - 1, 19, 8
+    v = torch.tensor([1, -1, 0, 1]).repeat(32)
+    dtype = torch.bfloat16 if kv == "bf16" else torch.int8
+    pools = dict(k_cache=torch.randint(-3, 4, (1, hkv, 128, 128)).to(dtype).cuda(),
+                 v_cache=v.expand(1, hkv, 128, 128).contiguous().to(dtype).cuda())
+    if kv == "int8":
+        pools |= {x: torch.ones((1, hkv, 128), device="cuda") for x in ("k_scale", "v_scale")}
+    out = torch.full((bs, hkv, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((bs, hkv), 7.0, device="cuda")
+    pages = 2 ** 22
+    B.pa_tree_attention(q=torch.zeros((bs, hkv, 128), dtype=torch.bfloat16, device="cuda"),
+                        page_table=torch.zeros((1, pages), dtype=torch.int32, device="cuda").repeat(bs, 1),
+                        cache_seqlens=torch.full((bs,), n, dtype=torch.int32, device="cuda"),
+                        cu_seqlens_q=torch.arange(bs + 1, dtype=torch.int32, device="cuda"),
+                        tree_mask=torch.ones((bs, 1), dtype=torch.int64, device="cuda"), max_q_len=1,
+                        max_seq_pages=pages, sm_scale=SCALE, out=out, lse=lse,
+                        workspace=torch.empty(B.pa_tree_workspace_bytes(bs, bs, 1, hkv, hkv, 128, 128, pages),
+                                              dtype=torch.uint8, device="cuda"), **pools)
+    torch.cuda.synchronize()
+    assert B.pa_read_error_flags(reset=True) == 0
+    assert bool((out.cpu().double() == v).all())
+    assert float((lse.cpu().double() - math.log(n)).abs().max()) <= 2.0 ** -20 * math.log(n)
+
+
 # ---- NaN scores --------------------------------------------------------------------------------
 
 
