@@ -74,6 +74,8 @@ cudaError_t error_word(unsigned int** out) {
   return cudaSuccess;
 }
 
+int32_t test_hold_loads() { return g_hold_loads.load(); }
+
 int sm_count_of_current_device() {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return 0;

@@ -312,6 +312,7 @@ pa_status pa_tree_attention(const void* q, const void* k_cache, const void* v_ca
   }
   p.out = out;
   p.lse = lse;
+  p.hold_loads = pa::test_hold_loads();
   cudaError_t e = pa::error_word(&p.err);
   if (e != cudaSuccess) return pa::from_cuda(e, "error word lookup");
   const cudaStream_t s = static_cast<cudaStream_t>(stream);

@@ -145,6 +145,7 @@ struct TreeParams {
   int32_t blocks;
   int32_t group_shift;  // log2 of the query heads per kv head
   float q_scale;  // sm_scale * log2(e)
+  int32_t hold_loads;  // instrumented build only: three tiles, then no more (timeout test)
   // partials of several splits, or (one split) the output itself
   float *m_out, *l_out, *acc_out;
   void* out;
@@ -218,6 +219,7 @@ pa_status from_cuda(cudaError_t e, const char* where);
 // Device address of the current device's error word (looked up once per device).
 cudaError_t error_word(unsigned int** out);
 int sm_count_of_current_device();
+int32_t test_hold_loads();  // what pa_set_test_hold_loads was given (instrumented build; else 0)
 
 // Argument checks shared by the entry points: the metadata stage's, and those of every
 // attention over the pools (bs == 0 passes).

@@ -887,6 +887,11 @@ __global__ void __launch_bounds__(Roles<kQuant>::kThreads, 1)
           }
           const int boxes = min(kBoxes, (p.n - c * kTile + kBoxRows - 1) / kBoxRows);
           for (int kv = 0; kv < 2; ++kv, ++it) {
+#ifdef PA_TIMESTAMPS
+            // failure-detection test of the instrumented build: after three tiles nothing is
+            // issued, so the other warps' waits give up with products in flight
+            if (prm.hold_loads && it >= 3) break;
+#endif
             if constexpr (kQuant) {
               const int slot = it % kRawSlots;
               ok = it < kRawSlots || mbar_wait_bounded(&ctl.raw_empty[slot],
