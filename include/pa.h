@@ -578,7 +578,10 @@ PA_API pa_status pa_build_tree_mask(const int32_t* parents, const int32_t* cu_se
  * attends to every position j < n - q_len and to position n - q_len + t where bit t of
  * tree_mask row i is set (bits t >= q_len are ignored; the caller sets bit i for the
  * query's own token).  A query that attends to nothing gives out = 0, lse = -inf; one with a
- * NaN score among those it attends to gives NaN in both.
+ * NaN score among those it attends to gives NaN in both.  lse and the sums are fp32; each
+ * weight (int8: times its V scale) enters the product with V as one bf16, so out is within
+ * 2^-8 sum_j p_j |v_j| before its own rounding.  pa_decode_splitk_multi keeps weights to 2^-16
+ * or better: for short chains it is the more accurate call.
  *   out [total_q, num_q_heads, 128] bf16;  lse [total_q, num_q_heads] fp32 or NULL; rows at
  *   or past cu_seqlens_q[bs] (padding of a captured batch), before cu_seqlens_q[0], and of a
  *   request whose rows are refused (more than max_q_len, outside [0, total_q)) are not touched.

@@ -6,6 +6,10 @@
 // weights are 2^(x - r) for a reference r that moves only when a score passes it by more
 // than 2^8, so the accumulator is rescaled a few times per split, not per chunk.  Weights
 // enter P V rounded to bf16 (2^-8 of each weight's share); their sum l stays unrounded fp32.
+// That rounding is chosen for time: what it leaves of a weight as a second bf16 operand brought
+// the error against 64 bits from 0.0022-0.0024 to 0.0017, the output's own rounding, and cost
+// half as many products again: one request of 1K 12.5 against 11.7 us, 32 of 8K 183 against 169,
+// 64 ragged int8 ones 654 against 546, 16 of 16K with 64 drafted 551 against 388.
 //
 // Shape.  A unit of work is up to 256 rows (two tiles of 128) of one (request, kv head), so a
 // K/V chunk of 128 tokens is fetched once for both tiles.  The batch's units are laid end to
