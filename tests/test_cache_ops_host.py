@@ -292,3 +292,18 @@ def test_tree_splits_of_long_contexts():
         assert B.pa_choose_tree_splits(64, 8, 32, 8, 64, tokens // 64, 152) >= (tokens >> 17) + 1
     assert B.pa_choose_tree_splits(64, 8, 32, 8, 64, 1 << 23, 152) == 4096
     assert B.pa_choose_tree_splits(64, 8, 32, 8, 64, (1 << 18) // 64, 152) <= 3
+
+
+@pytest.mark.parametrize("d,base,length,factor", [(128, 10000.0, 4096, 32.0), (64, 500000.0, 8192, 8.0),
+                                                  (16, 10000.0, 2048, 4.0)])
+def test_rope_by_parts_ramp(d, base, length, factor):
+    """Every pair of the ramp, from the header's formula."""
+    pair = lambda turns: d * math.log(length / (2 * math.pi * turns)) / (2 * math.log(base))
+    lo, hi = max(0, math.floor(pair(32.0))), min(d - 1, math.ceil(pair(1.0)))
+    assert hi - lo >= 2
+    got = B.pa_rope_frequencies(d, base, B.PA_ROPE_BY_PARTS, factor=factor, original_length=length, low=1.0,
+                                high=32.0).tolist()
+    for i, y in enumerate(got):
+        f = base ** (-2 * i / d)
+        r = min(1.0, max(0.0, (i - lo) / max(hi - lo, 0.001)))
+        assert abs(y / (f * (1 - r) + f / factor * r) - 1) < 1e-12

@@ -248,6 +248,33 @@ def test_tree_blocks_that_work_for_seconds(kv):
     assert float((lse.cpu().double() - math.log(n)).abs().max()) <= 2.0 ** -20 * math.log(n)
 
 
+# ---- lse ------------------------------------------------------------------------------------------
+
+
+@pytest.mark.parametrize("kv", ["bf16", "int8"])
+@pytest.mark.parametrize("splits", [1, 3])
+def test_tree_lse_is_good_to_fp32(kv, splits):
+    """Small scores, so that little hides behind them.  A score: products of two bf16 (or a code) are
+    exact, 128 truncating adds, the scales' and the softmax scale's rounding (132 * 2^-23 of
+    sum |q k|).  A weight: the difference to the reference and 2^x, 2^-21.  l: n adds of positive
+    terms, 2^-24 each at most.  ln l, m ln 2 and their sum: 2^-22 of |lse| + 1."""
+    c = Cache([1500, 333, 129], 2, 64, kv, 35)
+    t = Tree(c, [20, 5, 1], 8, 36)
+    t.q *= 0.0625
+    _, want, _ = R.tree_attention(t.q, c.k, c.v, c.ks, c.vs, c.table, c.n, t.q_lens, t.masks, SCALE)
+    _, lse = t.run(splits)
+    at = 0
+    for b, (n, ql) in enumerate(zip(c.n, t.q_lens)):
+        for h in range(8):
+            k = R.pool_rows(c.k, c.ks, c.table[b], n, h // 4).abs()
+            size = (t.q[at:at + ql, h].double().abs() @ k.T).amax(-1) * SCALE
+            w = want[at:at + ql, h]
+            bound = 132 * 2.0 ** -23 * size + 2.0 ** -21 + n * 2.0 ** -24 + 2.0 ** -22 * (w.abs() + 1)
+            err = (lse[at:at + ql, h].cpu().double() - w).abs()
+            assert bool((err <= bound).all()), (float(err.max()), float(bound.max()))
+        at += ql
+
+
 # ---- NaN scores --------------------------------------------------------------------------------
 
 
