@@ -42,8 +42,8 @@
 // keep shared memory about three quarters busy.  Shares weighted by the tiles of a chunk were
 // measured and were slower (689 and 731 us against 633 at the time).
 // Measured, both launches where a row is cut (heads / kv heads): one request of 1K tokens with 8
-// drafted (32 / 8) 11.3 us; 32 requests of 8K with 32 drafted (32 / 8) 167.5 us (6.5 TB/s); 16
-// of 16K with 64 drafted (64 / 8) 369-434 us (1.3-1.5 PFLOP/s, under the power cap); 64 ragged
+// drafted (32 / 8) 11.4 us; 32 requests of 8K with 32 drafted (32 / 8) 168-171 us (6.4 TB/s); 16
+// of 16K with 64 drafted (64 / 8) 378-440 us (1.2-1.4 PFLOP/s, under the power cap); 64 ragged
 // to 16K, int8, with 32 drafted (64 / 8) 548 us.
 #pragma once
 
