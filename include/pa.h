@@ -599,12 +599,13 @@ PA_API pa_status pa_build_tree_mask(const int32_t* parents, const int32_t* cu_se
  * their own.
  * sm_scale is positive, sm_scale * log2(e) finite in fp32.
  * Supported: head_dim 128; page_size 16, 32, 64, 128; num_q_heads / num_kv_heads in {1, 2,
- * 4, 8, 16}; 1 <= max_q_len <= 256; max_seq_pages * page_size <= 2^29 and, where num_splits
- * is given, <= max(1, num_splits - 1) * 2^20 (the tensor cores truncate as they add: a piece
- * of n tokens loses up to n 2^-25 of a sum whose terms have one sign; the library's own
- * choice keeps pieces within 2^18, in one launch's workspace of up to 1 + ceil(tokens /
- * 2^17) pieces a row); bs * num_kv_heads * ceil(num_q_heads / num_kv_heads * max_q_len / 256) * ceil(max_seq_pages *
- * page_size / 128) < 2^30.  All device memory.  Request lengths and row offsets
+ * 4, 8, 16}; 1 <= max_q_len <= 256; max_seq_pages * page_size <= 2^29 and bs *
+ * num_kv_heads * ceil(num_q_heads / num_kv_heads * max_q_len / 256) * ceil(max_seq_pages *
+ * page_size / 128) < 2^30; a given num_splits: max_seq_pages * page_size <= max(1, num_splits
+ * - 1) * 2^20.  (The tensor cores truncate as they add: n near-equal weights of one piece and
+ * V of one sign lose about n 2^-28 of their sum, n 2^-25 at most.  The library's own choice
+ * keeps pieces within 2^18 tokens, with 1 + ceil(tokens / 2^17) of them a row for tables past
+ * 2^18.)  All device memory.  Request lengths and row offsets
  * that only the device sees are bounds-checked like those of pa_decode_splitk_multi.
  */
 PA_API pa_status pa_tree_attention(

@@ -242,7 +242,7 @@ pa_status check_tree(const void* q, const void* k_cache, const void* v_cache, co
   if (max_q_len > kMaxTreeNodes) return PA_ERR_UNSUPPORTED;
   // keeps every position the kernel forms within int32
   if (static_cast<int64_t>(max_seq_pages) * page_size > (int64_t{1} << 29)) return PA_ERR_UNSUPPORTED;
-  // keeps a piece within 2^20 tokens, whose sums are good to a bf16 rounding
+  // keeps a piece within 2^20 tokens, whose sums lose about as much as a bf16 rounding at most
   if (static_cast<int64_t>(max_seq_pages) * page_size > (int64_t{*splits > 1 ? *splits - 1 : 1} << 20))
     return PA_ERR_UNSUPPORTED;
   // keeps the batch's chunks (128 tokens of up to 256 rows of a kv head) within 31 bits

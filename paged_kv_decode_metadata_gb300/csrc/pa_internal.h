@@ -123,8 +123,8 @@ struct TreeMaskParams {
 
 // Chunks (of 128 tokens) that a piece of a tree's context has at most, where num_splits allows
 // it: the tensor cores truncate each 4 tokens' sum as they add it to the accumulator, so n near-
-// equal weights of one sign lose up to n 2^-25.  (Whole contexts of 4M tokens read 1.1 % low, of
-// 16M 3.9 %; in pieces of this length, nothing that bf16 shows.)
+// equal weights of one sign lose about n 2^-28, n 2^-25 at most.  (Whole contexts of 4M tokens
+// read 1.1 % low, of 16M 3.9 %; in pieces of this length, nothing that bf16 shows.)
 constexpr int32_t kTreePieceChunks = 2048;
 
 struct TreeParams {
