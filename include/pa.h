@@ -68,7 +68,11 @@ typedef enum {
                               than PA_STATIC_SCRATCH_BYTES */
 } pa_status;
 
-typedef enum { PA_KV_BF16 = 0, PA_KV_INT8 = 1 } pa_kv_dtype;
+typedef enum {
+  PA_KV_BF16 = 0,
+  PA_KV_INT8 = 1,
+  PA_KV_E4M3 = 2 /* block-scaled pools only (pa_block_attention and its append) */
+} pa_kv_dtype;
 
 /* Implementations of the split-K producer (pa_select_producer). */
 typedef enum {
@@ -718,6 +722,79 @@ PA_API pa_status pa_evict(const int32_t* page_table, int64_t page_table_stride,
                           int32_t dst_max_pages, int32_t* kept, int32_t* new_seqlens, int32_t bs,
                           int32_t num_kv_heads, int32_t head_dim, int32_t page_size,
                           int64_t num_pages, void* stream, int32_t use_pdl);
+
+/*
+ * Block-scaled pools: k_cache, v_cache [num_pages, num_kv_heads, page_size, 128] of e4m3 codes
+ * (PA_KV_E4M3), k_scale, v_scale [num_pages, num_kv_heads, page_size / scale_block] fp32: one
+ * scale for each block of scale_block tokens (16, 32, 64 or 128, at most page_size) and kv head,
+ * K = k_scale * code.  Half of a bf16 pool's bytes, and 8 bytes of scales a block.  Pools are
+ * 16-byte aligned, scales 4-byte.
+ */
+
+/*
+ * pa_block_attention -- attention over block-scaled pools.  Query rows of request b are
+ * q[cu_seqlens_q[b] .. cu_seqlens_q[b+1]) (row b where cu_seqlens_q is NULL; then total_q = bs and
+ * max_q_len = 1); they are its newest tokens, already in its cache, so query i attends to
+ * positions j < n - q_len + i + 1, n = cache_seqlens[b].  out and lse as for pa_tree_attention: a
+ * query that attends to nothing gives out = 0, lse = -inf; rows that no request covers, and those
+ * of a request whose rows are refused, are not touched.
+ * The codes are multiplied as they are, against bf16 q (exact but for channels below 2^-13 of the
+ * row's largest, which keep 2^-21 of it) and weights with 12 bits: out is within 2^-12 sum_j p_j
+ * |v_j| before its own rounding, where the scales of 128 consecutive tokens lie within 2^14 of one
+ * another; a weight below 2^-26 of the largest weight times scale among them counts as 0 in
+ * out (not in lse).  Non-finite codes (NaN) and scales reach the queries that attend to them, a V
+ * code every query of its request.  Codes and scales at or past n may hold anything.
+ * num_splits: the number of pieces (1 to 4096) that a context is cut into, or 0 for
+ * pa_choose_block_splits(...).  With 1 `workspace` may be NULL; otherwise it is 16-byte aligned,
+ * workspace_bytes >= pa_workspace_bytes(total_q, num_q_heads, 128, that number), and a second
+ * launch combines the pieces.  Equal inputs give equal bits.  Calls that overlap on the GPU need
+ * workspaces of their own.
+ * sm_scale * log2(e) finite in fp32.
+ * Supported: head_dim 128; page_size 16, 32, 64, 128; num_q_heads / num_kv_heads 1 to 32 (any
+ * whole number); 1 <= max_q_len <= 65535; bs and num_kv_heads <= 65535; max_seq_pages * page_size
+ * <= 2^29.  A tile has up to 32 (query, head) pairs of a kv head, and every tile reads the
+ * request's cache: the call is meant for decoding and short drafts, and right for longer chunks.
+ */
+PA_API pa_status pa_block_attention(
+    const void* q, const void* k_cache, const void* v_cache, const float* k_scale,
+    const float* v_scale, int32_t kv_dtype, int32_t scale_block, const int32_t* page_table,
+    int64_t page_table_stride, const int32_t* cache_seqlens, const int32_t* cu_seqlens_q,
+    int32_t bs, int32_t total_q, int32_t max_q_len, int32_t num_q_heads, int32_t num_kv_heads,
+    int32_t head_dim, int32_t page_size, int64_t num_pages, int32_t max_seq_pages,
+    int32_t num_splits, float sm_scale, void* workspace, size_t workspace_bytes, void* out,
+    float* lse, void* stream, int32_t use_pdl);
+
+/*
+ * pa_decode_step_block -- the decode or verify step over block-scaled pools: pa_build_metadata_full
+ * with the query side (q_mode, qlens, q_stride as for pa_decode_step_multi; cu_seqlens_q NULL with
+ * PA_Q_MODE_NONE: one query per request), then pa_block_attention over the page table it wrote.
+ * The arguments are those of the two calls; everything is checked before anything is enqueued.
+ * total_q == 0 runs the metadata stage only.
+ */
+PA_API pa_status pa_decode_step_block(
+    const int64_t* req_pool_indices, const int64_t* seq_lens, const int32_t* req_to_token,
+    int64_t req_to_token_rows, int64_t req_to_token_stride,
+    const int64_t* full_to_swa_mapping, int64_t full_to_swa_mapping_len,
+    int32_t seqlen_offset, int32_t max_seq_pages, int32_t* cache_seqlens,
+    int32_t* cu_seqlens_k, int32_t* page_table, int64_t page_table_stride,
+    int32_t* swa_page_table, int64_t swa_page_table_stride, const int64_t* qlens,
+    int32_t q_mode, int32_t q_stride, int32_t* cu_seqlens_q, const void* q, int32_t total_q,
+    int32_t max_q_len, const void* k_cache, const void* v_cache, const float* k_scale,
+    const float* v_scale, int32_t kv_dtype, int32_t scale_block, int32_t bs, int32_t num_q_heads,
+    int32_t num_kv_heads, int32_t head_dim, int32_t page_size, int64_t num_pages,
+    int32_t num_splits, float sm_scale, void* workspace, size_t workspace_bytes, void* out,
+    float* lse, void* stream, int32_t use_pdl);
+
+/*
+ * The number of pieces that pa_block_attention takes for num_splits == 0 (sm_count <= 0: the
+ * current device), and the workspace bytes it then needs (0 where it is 1).
+ */
+PA_API int32_t pa_choose_block_splits(int32_t bs, int32_t max_q_len, int32_t num_q_heads,
+                                      int32_t num_kv_heads, int32_t page_size,
+                                      int32_t max_seq_pages, int32_t sm_count);
+PA_API size_t pa_block_workspace_bytes(int32_t bs, int32_t total_q, int32_t max_q_len,
+                                       int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                                       int32_t page_size, int32_t max_seq_pages);
 
 /* Bytes of workspace pa_decode_step needs: m, l and acc partials, each 256-byte aligned. */
 PA_API size_t pa_workspace_bytes(int32_t bs, int32_t num_q_heads, int32_t head_dim,

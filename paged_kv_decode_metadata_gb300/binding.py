@@ -19,7 +19,7 @@ from . import build as _build
 
 PA_OK, PA_ERR_INVALID, PA_ERR_UNSUPPORTED, PA_ERR_CUDA, PA_ERR_SCRATCH_LIMIT = 0, 1, 2, 3, 4
 PA_STATIC_SCRATCH_BYTES = 16 * 1024 * 1024
-PA_KV_BF16, PA_KV_INT8 = 0, 1
+PA_KV_BF16, PA_KV_INT8, PA_KV_E4M3 = 0, 1, 2
 PA_Q_MODE_NONE, PA_Q_MODE_CUMSUM, PA_Q_MODE_STRIDED = 0, 1, 2
 PA_PRODUCER_AUTO, PA_PRODUCER_FMA, PA_PRODUCER_MMA = 0, 1, 2
 DEVERR_PAGE_OUT_OF_RANGE = 0x1
@@ -153,6 +153,17 @@ def _declare(lib):
                                      i32, vp, vp, i64, i32, vp, i32, i32, i32, i32, i64, vp, i32]
     lib.pa_evict.argtypes = [vp, i64, vp, i32, vp, vp, vp, vp, vp, i32, i32, i32, i32, vp, i64, i32,
                              vp, vp, i32, i32, i32, i32, i64, vp, i32]
+    lib.pa_block_attention.argtypes = [vp, vp, vp, vp, vp, i32, i32, vp, i64, vp, vp, i32, i32, i32,
+                                       i32, i32, i32, i32, i64, i32, i32, f32, vp, sz, vp, vp, vp,
+                                       i32]
+    lib.pa_decode_step_block.argtypes = [vp, vp, vp, i64, i64, vp, i64, i32, i32, vp, vp, vp, i64,
+                                         vp, i64, vp, i32, i32, vp, vp, i32, i32, vp, vp, vp, vp,
+                                         i32, i32, i32, i32, i32, i32, i32, i64, i32, f32, vp, sz,
+                                         vp, vp, vp, i32]
+    lib.pa_choose_block_splits.argtypes = [i32] * 7
+    lib.pa_choose_block_splits.restype = i32
+    lib.pa_block_workspace_bytes.argtypes = [i32] * 8
+    lib.pa_block_workspace_bytes.restype = sz
     lib.pa_workspace_bytes.argtypes = [i32, i32, i32, i32]
     lib.pa_workspace_bytes.restype = sz
     lib.pa_choose_splits.argtypes = [i32, i32, i32, i32, i32, i32]
@@ -172,6 +183,7 @@ def _declare(lib):
                  "pa_rope_append_weights",
                  "pa_build_tree_mask", "pa_tree_attention", "pa_decode_step_tree",
                  "pa_accumulate_weights", "pa_compact_cache", "pa_evict",
+                 "pa_block_attention", "pa_decode_step_block",
                  "pa_read_error_flags"):
         getattr(lib, name).restype = ctypes.c_int
     return lib
@@ -1008,3 +1020,139 @@ def pa_evict(**kw):
 def prepare_evict(*, lib=None, **kw) -> PreparedCall:
     """``pa_evict`` with the given keyword arguments, marshalled once."""
     return PreparedCall("pa_evict", _evict_args(**kw), lib, keep=tuple(kw.values()))
+
+
+# ---- block-scaled caches: e4m3 codes, a scale per block of tokens and head --------------------
+
+
+def _block_pools(k_cache, v_cache, k_scale, v_scale):
+    """(scale_block, pool shape) of e4m3 pools and their scales."""
+    if k_cache.dim() != 4:
+        raise ValueError("k_cache must be [num_pages, num_kv_heads, page_size, head_dim]")
+    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+        if t.dtype != torch.float8_e4m3fn:
+            raise ValueError(f"{name} must be {torch.float8_e4m3fn}, got {t.dtype}")
+    _shape(v_cache, tuple(k_cache.shape), "v_cache")
+    num_pages, hkv, page_size, _ = k_cache.shape
+    if k_scale.dim() != 3 or k_scale.shape[2] < 1 or page_size % k_scale.shape[2] != 0:
+        raise ValueError("k_scale must be [num_pages, num_kv_heads, page_size / scale_block]")
+    _shape(k_scale, (num_pages, hkv, k_scale.shape[2]), "k_scale")
+    _shape(v_scale, tuple(k_scale.shape), "v_scale")
+    return page_size // k_scale.shape[2], tuple(k_cache.shape)
+
+
+def pa_choose_block_splits(bs: int, max_q_len: int, num_q_heads: int, num_kv_heads: int,
+                           page_size: int, max_seq_pages: int, sm_count: int = 0) -> int:
+    """Split count of a block attention; see include/pa.h."""
+    return int(load().pa_choose_block_splits(bs, max_q_len, num_q_heads, num_kv_heads, page_size,
+                                             max_seq_pages, sm_count))
+
+
+def pa_block_workspace_bytes(bs: int, total_q: int, max_q_len: int, num_q_heads: int,
+                             num_kv_heads: int, head_dim: int, page_size: int,
+                             max_seq_pages: int) -> int:
+    """Workspace of a block attention with the library's split count; see include/pa.h."""
+    return int(load().pa_block_workspace_bytes(bs, total_q, max_q_len, num_q_heads, num_kv_heads,
+                                               head_dim, page_size, max_seq_pages))
+
+
+def _block_rows(q, cu_seqlens_q, cache_seqlens, max_q_len, out, lse, d: int):
+    """Shapes shared by the block calls; returns (total_q, num_q_heads, bs, max_q_len)."""
+    if q.dim() != 3 or q.shape[2] != d:
+        raise ValueError(f"q must be [total_q, num_q_heads, {d}]")
+    total_q, hq, _ = q.shape
+    bs = cache_seqlens.shape[0]
+    if cu_seqlens_q is not None:
+        _shape(cu_seqlens_q, (bs + 1,), "cu_seqlens_q")
+    elif total_q != bs or max_q_len != 1:
+        raise ValueError("without cu_seqlens_q there is one query per request")
+    _shape(out, tuple(q.shape), "out")
+    if lse is not None:
+        _shape(lse, (total_q, hq), "lse")
+    return total_q, hq, bs, int(max_q_len)
+
+
+def _block_attention_args(*, q, k_cache, v_cache, k_scale, v_scale, page_table, cache_seqlens,
+                          max_seq_pages: int, sm_scale: float, out, cu_seqlens_q=None,
+                          max_q_len: int = 1, lse=None, num_splits: int = 0, workspace=None,
+                          stream=None, use_pdl: bool = True):
+    _on_device(q=q, k_cache=k_cache, v_cache=v_cache, page_table=page_table,
+               cache_seqlens=cache_seqlens, cu_seqlens_q=cu_seqlens_q, out=out, lse=lse,
+               workspace=workspace, k_scale=k_scale, v_scale=v_scale)
+    block, (num_pages, hkv, page_size, d) = _block_pools(k_cache, v_cache, k_scale, v_scale)
+    total_q, hq, bs, mql = _block_rows(q, cu_seqlens_q, cache_seqlens, max_q_len, out, lse, d)
+    pt, pt_stride = _table(page_table, bs, int(max_seq_pages), "page_table")
+    ws, ws_bytes = _workspace(workspace)
+    return (_ptr(q, torch.bfloat16, "q"), _ptr(k_cache, None, "k_cache"),
+            _ptr(v_cache, None, "v_cache"), _ptr(k_scale, torch.float32, "k_scale"),
+            _ptr(v_scale, torch.float32, "v_scale"), PA_KV_E4M3, block, pt, pt_stride,
+            _ptr(cache_seqlens, torch.int32, "cache_seqlens"),
+            _ptr(cu_seqlens_q, torch.int32, "cu_seqlens_q"), bs, total_q, mql, hq, hkv, d,
+            page_size, num_pages, int(max_seq_pages), int(num_splits), float(sm_scale), ws,
+            ws_bytes, _ptr(out, torch.bfloat16, "out"), _ptr(lse, torch.float32, "lse"),
+            _stream(stream), int(bool(use_pdl)))
+
+
+def pa_block_attention(**kw):
+    """Attention over a block-scaled cache; see include/pa.h.  Keyword arguments: those of
+    ``_block_attention_args``."""
+    _check("pa_block_attention", load().pa_block_attention(*_block_attention_args(**kw)))
+
+
+def prepare_block_attention(*, lib=None, **kw) -> PreparedCall:
+    """``pa_block_attention`` with the given keyword arguments, marshalled once."""
+    return PreparedCall("pa_block_attention", _block_attention_args(**kw), lib,
+                        keep=tuple(kw.values()))
+
+
+def _decode_step_block_args(*, req_pool_indices, seq_lens, req_to_token, seqlen_offset: int,
+                            max_seq_pages: int, cache_seqlens, cu_seqlens_k, page_table, q,
+                            k_cache, v_cache, k_scale, v_scale, sm_scale: float, out,
+                            cu_seqlens_q=None, max_q_len: int = 1, lse=None, num_splits: int = 0,
+                            workspace=None, qlens=None, q_mode: int = PA_Q_MODE_NONE,
+                            q_stride: int = 0, full_to_swa_mapping=None, swa_page_table=None,
+                            stream=None, use_pdl: bool = True):
+    _on_device(req_pool_indices=req_pool_indices, seq_lens=seq_lens, req_to_token=req_to_token,
+               cache_seqlens=cache_seqlens, cu_seqlens_k=cu_seqlens_k, page_table=page_table,
+               cu_seqlens_q=cu_seqlens_q, q=q, k_cache=k_cache, v_cache=v_cache, out=out, lse=lse,
+               workspace=workspace, qlens=qlens, k_scale=k_scale, v_scale=v_scale,
+               full_to_swa_mapping=full_to_swa_mapping, swa_page_table=swa_page_table)
+    block, (num_pages, hkv, page_size, d) = _block_pools(k_cache, v_cache, k_scale, v_scale)
+    total_q, hq, bs, mql = _block_rows(q, cu_seqlens_q, cache_seqlens, max_q_len, out, lse, d)
+    _shape(req_pool_indices, (bs,), "req_pool_indices")
+    _shape(seq_lens, (bs,), "seq_lens")
+    _shape(cu_seqlens_k, (bs + 1,), "cu_seqlens_k")
+    if qlens is not None:
+        _shape(qlens, (bs,), "qlens")
+    pt, pt_stride = _table(page_table, bs, int(max_seq_pages), "page_table")
+    swa, swa_stride = (None, 0) if swa_page_table is None else \
+        _table(swa_page_table, bs, int(max_seq_pages), "swa_page_table")
+    ws, ws_bytes = _workspace(workspace)
+    return (_ptr(req_pool_indices, torch.int64, "req_pool_indices"),
+            _ptr(seq_lens, torch.int64, "seq_lens"),
+            _ptr2d(req_to_token, torch.int32, "req_to_token"), req_to_token.shape[0],
+            req_to_token.stride(0), _ptr(full_to_swa_mapping, torch.int64, "full_to_swa_mapping"),
+            full_to_swa_mapping.numel() if full_to_swa_mapping is not None else 0,
+            int(seqlen_offset), int(max_seq_pages),
+            _ptr(cache_seqlens, torch.int32, "cache_seqlens"),
+            _ptr(cu_seqlens_k, torch.int32, "cu_seqlens_k"), pt, pt_stride, swa, swa_stride,
+            _ptr(qlens, torch.int64, "qlens"), int(q_mode), int(q_stride),
+            _ptr(cu_seqlens_q, torch.int32, "cu_seqlens_q"), _ptr(q, torch.bfloat16, "q"),
+            total_q, mql, _ptr(k_cache, None, "k_cache"), _ptr(v_cache, None, "v_cache"),
+            _ptr(k_scale, torch.float32, "k_scale"), _ptr(v_scale, torch.float32, "v_scale"),
+            PA_KV_E4M3, block, bs, hq, hkv, d, page_size, num_pages, int(num_splits),
+            float(sm_scale), ws, ws_bytes, _ptr(out, torch.bfloat16, "out"),
+            _ptr(lse, torch.float32, "lse"), _stream(stream), int(bool(use_pdl)))
+
+
+def pa_decode_step_block(*, lib=None, **kw):
+    """Metadata + block attention in one call; see include/pa.h.  Keyword arguments: those
+    of ``_decode_step_block_args``."""
+    lib = lib or load()
+    _check("pa_decode_step_block", lib.pa_decode_step_block(*_decode_step_block_args(**kw)), lib)
+
+
+def prepare_decode_step_block(*, lib=None, **kw) -> PreparedCall:
+    """``pa_decode_step_block`` with the given keyword arguments, marshalled once."""
+    return PreparedCall("pa_decode_step_block", _decode_step_block_args(**kw), lib,
+                        keep=tuple(kw.values()))

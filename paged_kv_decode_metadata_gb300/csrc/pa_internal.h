@@ -153,6 +153,30 @@ struct TreeParams {
   unsigned int* err;
 };
 
+struct BlockParams {
+  const void* q;  // bf16 [total_q, Hq, 128]
+  const void *k_cache, *v_cache;
+  const float *k_scale, *v_scale;  // [num_pages, Hkv, page_size >> block_shift]
+  int32_t page_shift, block_shift;  // log2 of the page size, of a scale's tokens
+  const int32_t* page_table;
+  int64_t page_table_stride;
+  const int32_t* cache_seqlens;
+  const int32_t* cu_seqlens_q;  // nullptr: one query per request
+  int32_t bs, total_q, max_q_len;
+  int32_t num_q_heads, num_kv_heads, group;
+  int64_t num_pages;
+  int32_t max_seq_pages;
+  int32_t tile_queries;  // queries of a tile: its columns are those times the group
+  int32_t num_splits, split_chunks;
+  float q_scale;       // sm_scale * log2(e)
+  int32_t hold_loads;  // instrumented build only: three tiles, then no more (timeout test)
+  // partials of several splits, or (one split) the output itself
+  float *m_out, *l_out, *acc_out;
+  void* out;
+  float* lse;
+  unsigned int* err;
+};
+
 struct WeightsParams {
   const void* q;
   const float* lse;
@@ -266,6 +290,10 @@ cudaError_t launch_tree_mma_bf16(const TreeParams& p, int group, int page_size,
                                  cudaStream_t stream, bool use_pdl);
 cudaError_t launch_tree_mma_int8(const TreeParams& p, int group, int page_size,
                                  cudaStream_t stream, bool use_pdl);
+// columns: (query, head) pairs of a tile, 8, 16 or 32.
+cudaError_t launch_block(const BlockParams& p, int columns, cudaStream_t stream, bool use_pdl);
+// Combines the partials of launch_block (num_splits > 1).
+cudaError_t launch_block_join(const BlockParams& p, cudaStream_t stream, bool use_pdl);
 cudaError_t launch_weights(const WeightsParams& p, bool int8, int group, int page_size,
                            cudaStream_t stream, bool use_pdl);
 cudaError_t launch_select(const SelectParams& p, cudaStream_t stream, bool use_pdl);
