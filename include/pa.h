@@ -729,7 +729,36 @@ PA_API pa_status pa_evict(const int32_t* page_table, int64_t page_table_stride,
  * scale for each block of scale_block tokens (16, 32, 64 or 128, at most page_size) and kv head,
  * K = k_scale * code.  Half of a bf16 pool's bytes, and 8 bytes of scales a block.  Pools are
  * 16-byte aligned, scales 4-byte.
+ *
+ * pa_rope_append_blocks -- the append of such pools: rotary positions on the new queries and
+ * keys (as pa_rope_append), the new keys and values written as codes.  Rows of request b are
+ * cu_seqlens_q[b] .. cu_seqlens_q[b+1] of q, k, v and positions (at most max_q_len of them); they
+ * are its newest tokens, so row i goes to position cache_seqlens[b] - q_len + i of its pages.
+ * For every block that gets rows, with `top` the largest magnitude among its new rows:
+ *   need = 2^e, the smallest with top / 2^e <= 448 (e >= -126; 0 where top is 0)
+ *   scale = need where the block's first row is new, else the larger of need and its scale; where
+ *   that is a new scale, the rows before the new ones get the codes round(code * (old / scale))
+ *   codes = round(x * (1 / scale)) in fp32, to even, saturated (scale 0: 0)
+ * Powers of two, so a scale that grows costs earlier rows no bits but those that leave e4m3's
+ * range at the small end.  Rows of a block behind the new ones are left as they are; their codes
+ * have no meaning until they are written.  New rows must be finite, scales of blocks that are
+ * continued finite and not negative.  Two requests must not write one block.
+ * rotary_dim 0: keys and queries are taken as they are (inv_freq, positions and, with num_q_heads
+ * 0, q and q_out may be NULL).  Rows of q_out that no request covers, and of a request whose rows
+ * are refused (more than max_q_len, outside [0, total_q), more than its cache_seqlens), are not
+ * touched.  The call can be repeated: equal inputs leave equal bits.
+ * Supported: head_dim 128; rotary_dim 0, 16, 32, ..., 128; page_size 16, 32, 64, 128; bs and
+ * num_kv_heads <= 65535; max_seq_pages * page_size <= 2^29.
  */
+PA_API pa_status pa_rope_append_blocks(
+    const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+    int64_t v_stride, const int64_t* positions, const double* inv_freq, int32_t rotary_dim,
+    int32_t interleaved, float amplitude, const int32_t* cu_seqlens_q, const int32_t* cache_seqlens,
+    const int32_t* page_table, int64_t page_table_stride, int32_t max_seq_pages, int32_t bs,
+    int32_t total_q, int32_t max_q_len, int32_t num_q_heads, int32_t num_kv_heads,
+    int32_t head_dim, void* q_out, int64_t q_out_stride, void* k_cache, void* v_cache,
+    float* k_scale, float* v_scale, int32_t kv_dtype, int32_t scale_block, int32_t page_size,
+    int64_t num_pages, void* stream, int32_t use_pdl);
 
 /*
  * pa_block_attention -- attention over block-scaled pools.  Query rows of request b are

@@ -153,6 +153,9 @@ def _declare(lib):
                                      i32, vp, vp, i64, i32, vp, i32, i32, i32, i32, i64, vp, i32]
     lib.pa_evict.argtypes = [vp, i64, vp, i32, vp, vp, vp, vp, vp, i32, i32, i32, i32, vp, i64, i32,
                              vp, vp, i32, i32, i32, i32, i64, vp, i32]
+    lib.pa_rope_append_blocks.argtypes = [vp, i64, vp, i64, vp, i64, vp, vp, i32, i32, f32, vp, vp,
+                                          vp, i64, i32, i32, i32, i32, i32, i32, i32, vp, i64, vp,
+                                          vp, vp, vp, i32, i32, i32, i64, vp, i32]
     lib.pa_block_attention.argtypes = [vp, vp, vp, vp, vp, i32, i32, vp, i64, vp, vp, i32, i32, i32,
                                        i32, i32, i32, i32, i64, i32, i32, f32, vp, sz, vp, vp, vp,
                                        i32]
@@ -183,7 +186,7 @@ def _declare(lib):
                  "pa_rope_append_weights",
                  "pa_build_tree_mask", "pa_tree_attention", "pa_decode_step_tree",
                  "pa_accumulate_weights", "pa_compact_cache", "pa_evict",
-                 "pa_block_attention", "pa_decode_step_block",
+                 "pa_rope_append_blocks", "pa_block_attention", "pa_decode_step_block",
                  "pa_read_error_flags"):
         getattr(lib, name).restype = ctypes.c_int
     return lib
@@ -1039,6 +1042,60 @@ def _block_pools(k_cache, v_cache, k_scale, v_scale):
     _shape(k_scale, (num_pages, hkv, k_scale.shape[2]), "k_scale")
     _shape(v_scale, tuple(k_scale.shape), "v_scale")
     return page_size // k_scale.shape[2], tuple(k_cache.shape)
+
+
+def _rope_append_blocks_args(*, k, v, k_cache, v_cache, k_scale, v_scale, cu_seqlens_q,
+                             cache_seqlens, page_table, max_seq_pages: int, q=None, q_out=None,
+                             positions=None, inv_freq=None, max_q_len: Optional[int] = None,
+                             interleaved: bool = False, amplitude: float = 1.0, stream=None,
+                             use_pdl: bool = True):
+    _on_device(q=q, k=k, v=v, positions=positions, inv_freq=inv_freq, q_out=q_out, k_cache=k_cache,
+               v_cache=v_cache, k_scale=k_scale, v_scale=v_scale, cu_seqlens_q=cu_seqlens_q,
+               cache_seqlens=cache_seqlens, page_table=page_table)
+    block, (num_pages, hkv, page_size, d) = _block_pools(k_cache, v_cache, k_scale, v_scale)
+    tokens = k.shape[0]
+    kp, k_stride, k_heads = _token_rows(k, tokens, "k")
+    vp, v_stride, v_heads = _token_rows(v, tokens, "v")
+    qp, q_stride, hq, op, o_stride = None, 0, 0, None, 0
+    if q is not None:
+        qp, q_stride, hq = _token_rows(q, tokens, "q")
+        if q_out is None or q.shape[2] != d:
+            raise ValueError(f"q needs q_out, and rows of {d} channels")
+        _shape(q_out, tuple(q.shape), "q_out")
+        op, o_stride, _ = _token_rows(q_out, tokens, "q_out")
+    if k_heads != hkv or v_heads != hkv or not k.shape[2] == v.shape[2] == d:
+        raise ValueError("k and v must have the pools' heads and head_dim")
+    bs = cache_seqlens.shape[0]
+    _shape(cu_seqlens_q, (bs + 1,), "cu_seqlens_q")
+    if inv_freq is not None:
+        if inv_freq.dim() != 1 or positions is None:
+            raise ValueError("inv_freq must be [rotary_dim / 2], with positions")
+        _shape(positions, (tokens,), "positions")
+    pt, pt_stride = _table(page_table, bs, int(max_seq_pages), "page_table")
+    return (qp, q_stride, kp, k_stride, vp, v_stride, _ptr(positions, torch.int64, "positions"),
+            _ptr(inv_freq, torch.float64, "inv_freq"),
+            2 * inv_freq.numel() if inv_freq is not None else 0, int(bool(interleaved)),
+            float(amplitude), _ptr(cu_seqlens_q, torch.int32, "cu_seqlens_q"),
+            _ptr(cache_seqlens, torch.int32, "cache_seqlens"), pt, pt_stride, int(max_seq_pages),
+            bs, tokens, max(tokens, 1) if max_q_len is None else int(max_q_len), hq, hkv, d, op,
+            o_stride, _ptr(k_cache, None, "k_cache"), _ptr(v_cache, None, "v_cache"),
+            _ptr(k_scale, torch.float32, "k_scale"), _ptr(v_scale, torch.float32, "v_scale"),
+            PA_KV_E4M3, block, page_size, num_pages, _stream(stream), int(bool(use_pdl)))
+
+
+def pa_rope_append_blocks(**kw):
+    """Rotary positions on q (into q_out) and k, and each request's new k and v rows written
+    to a block-scaled cache; see include/pa.h.  Without ``inv_freq`` rows are taken as they
+    are, without ``q`` there are only k and v.  Keyword arguments: those of
+    ``_rope_append_blocks_args``."""
+    _check("pa_rope_append_blocks",
+           load().pa_rope_append_blocks(*_rope_append_blocks_args(**kw)))
+
+
+def prepare_rope_append_blocks(*, lib=None, **kw) -> PreparedCall:
+    """``pa_rope_append_blocks`` with the given keyword arguments, marshalled once."""
+    return PreparedCall("pa_rope_append_blocks", _rope_append_blocks_args(**kw), lib,
+                        keep=tuple(kw.values()))
 
 
 def pa_choose_block_splits(bs: int, max_q_len: int, num_q_heads: int, num_kv_heads: int,

@@ -1,4 +1,4 @@
-// C ABI of the block-scaled cache: attention, the step around it, split counts.  Argument
+// C ABI of the block-scaled cache: append, attention, the step around it, split counts.  Argument
 // checks and launches; see include/pa.h for the contract.
 #include <cuda_runtime.h>
 
@@ -123,6 +123,73 @@ size_t pa_block_workspace_bytes(int32_t bs, int32_t total_q, int32_t max_q_len,
   const int32_t splits =
       pa_choose_block_splits(bs, max_q_len, num_q_heads, num_kv_heads, page_size, max_seq_pages, 0);
   return splits > 1 ? pa_workspace_bytes(total_q, num_q_heads, head_dim, splits) : 0;
+}
+
+pa_status pa_rope_append_blocks(
+    const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+    int64_t v_stride, const int64_t* positions, const double* inv_freq, int32_t rotary_dim,
+    int32_t interleaved, float amplitude, const int32_t* cu_seqlens_q, const int32_t* cache_seqlens,
+    const int32_t* page_table, int64_t page_table_stride, int32_t max_seq_pages, int32_t bs,
+    int32_t total_q, int32_t max_q_len, int32_t num_q_heads, int32_t num_kv_heads,
+    int32_t head_dim, void* q_out, int64_t q_out_stride, void* k_cache, void* v_cache,
+    float* k_scale, float* v_scale, int32_t kv_dtype, int32_t scale_block, int32_t page_size,
+    int64_t num_pages, void* stream, int32_t use_pdl) {
+  if (bs < 0 || total_q < 0) return PA_ERR_INVALID;
+  if (bs == 0 || total_q == 0) return PA_OK;
+  pa_status st = check_block_pools(k_cache, v_cache, k_scale, v_scale, kv_dtype, scale_block,
+                                   page_table, page_table_stride, cache_seqlens, bs, num_kv_heads,
+                                   head_dim, page_size, num_pages, max_seq_pages);
+  if (st != PA_OK) return st;
+  if (!cu_seqlens_q || max_q_len < 1) return PA_ERR_INVALID;
+  if (!k || !v || !aligned(k, 16) || !aligned(v, 16)) return PA_ERR_INVALID;
+  if (num_q_heads < 0 || num_q_heads > (1 << 20)) return PA_ERR_INVALID;
+  if (rotary_dim != 0 && (!positions || !inv_freq || !aligned(positions, 8) || !aligned(inv_freq, 8)))
+    return PA_ERR_INVALID;
+  const int64_t strides[4] = {q_stride, k_stride, v_stride, q_out_stride};
+  for (int i = 0; i < 4; ++i) {
+    const int64_t heads = i == 0 || i == 3 ? num_q_heads : num_kv_heads;
+    if (heads > 0 && (strides[i] % 8 != 0 || strides[i] < heads * 128)) return PA_ERR_INVALID;
+  }
+  if (num_q_heads > 0) {
+    if (!q || !q_out || !aligned(q, 16) || !aligned(q_out, 16)) return PA_ERR_INVALID;
+    if (q_out == q && q_out_stride != q_stride) return PA_ERR_INVALID;
+  }
+  if (!std::isfinite(amplitude)) return PA_ERR_INVALID;
+  if (rotary_dim < 0 || rotary_dim > 128 || rotary_dim % 16 != 0) return PA_ERR_UNSUPPORTED;
+  pa::RopeBlocksParams p = {};
+  p.q = q;
+  p.k = k;
+  p.v = v;
+  p.q_stride = q_stride;
+  p.k_stride = k_stride;
+  p.v_stride = v_stride;
+  p.positions = positions;
+  p.inv_freq = inv_freq;
+  p.rotary_dim = rotary_dim;
+  p.amplitude = amplitude;
+  p.cu_seqlens_q = cu_seqlens_q;
+  p.cache_seqlens = cache_seqlens;
+  p.page_table = page_table;
+  p.page_table_stride = page_table_stride;
+  p.max_seq_pages = max_seq_pages;
+  p.bs = bs;
+  p.total_q = total_q;
+  p.max_q_len = max_q_len;
+  p.num_q_heads = num_q_heads;
+  p.num_kv_heads = num_kv_heads;
+  p.q_out = q_out;
+  p.q_out_stride = q_out_stride;
+  p.k_cache = k_cache;
+  p.v_cache = v_cache;
+  p.k_scale = k_scale;
+  p.v_scale = v_scale;
+  p.page_shift = log2_of(page_size);
+  p.block_shift = log2_of(scale_block);
+  p.num_pages = num_pages;
+  cudaError_t e = pa::error_word(&p.err);
+  if (e != cudaSuccess) return pa::from_cuda(e, "error word lookup");
+  return finish(pa::launch_rope_blocks(p, interleaved != 0, static_cast<cudaStream_t>(stream), use_pdl != 0),
+                "block append launch");
 }
 
 pa_status pa_block_attention(const void* q, const void* k_cache, const void* v_cache,

@@ -112,6 +112,29 @@ struct RopeParams {
   unsigned int* err;
 };
 
+struct RopeBlocksParams {
+  const void *q, *k, *v;  // bf16 rows, head h of token t at x + t * stride + h * 128
+  int64_t q_stride, k_stride, v_stride;
+  const int64_t* positions;
+  const double* inv_freq;
+  int32_t rotary_dim;
+  float amplitude;
+  const int32_t* cu_seqlens_q;
+  const int32_t* cache_seqlens;
+  const int32_t* page_table;
+  int64_t page_table_stride;
+  int32_t max_seq_pages;
+  int32_t bs, total_q, max_q_len;
+  int32_t num_q_heads, num_kv_heads;
+  void* q_out;
+  int64_t q_out_stride;
+  void *k_cache, *v_cache;
+  float *k_scale, *v_scale;        // [num_pages, Hkv, page_size >> block_shift]
+  int32_t page_shift, block_shift;  // log2 of the page size, of a scale's tokens
+  int64_t num_pages;
+  unsigned int* err;
+};
+
 struct TreeMaskParams {
   const int32_t* parents;
   const int32_t* cu_seqlens_q;
@@ -283,6 +306,8 @@ cudaError_t launch_reduce(const ReduceParams& p, cudaStream_t stream, bool use_p
 
 cudaError_t launch_rope(const RopeParams& p, bool int8, bool interleaved, cudaStream_t stream,
                         bool use_pdl);
+cudaError_t launch_rope_blocks(const RopeBlocksParams& p, bool interleaved, cudaStream_t stream,
+                               bool use_pdl);
 // Combines the partials that the tree attention left in `m_out`, `l_out` and `acc_out`.
 cudaError_t launch_tree_join(const TreeParams& p, cudaStream_t stream, bool use_pdl);
 cudaError_t launch_tree_mask(const TreeMaskParams& p, cudaStream_t stream, bool use_pdl);

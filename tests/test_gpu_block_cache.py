@@ -127,3 +127,98 @@ def test_attention(seqlens, q_lens, hq, hkv, page, block, splits):
     q = torch.randn((sum(lens), hq, 128), generator=c.g).to(torch.bfloat16)
     out, lse = attend(c, q.cuda(), q_lens, num_splits=splits)
     check(out, lse, R.attention(q, c.k, c.v, c.ks, c.vs, c.table, seqlens, lens, SCALE))
+
+
+# ---- append -----------------------------------------------------------------------------------
+
+APPEND_CASES = [  # seqlens, q_lens, hq, hkv, page, block, rot, interleaved, amplitude
+    ([1], [1], 4, 1, 16, 16, 128, False, 1.0),
+    ([200, 64, 65, 1], [1, 1, 1, 1], 32, 8, 64, 64, 128, False, 1.0),
+    ([300, 129], [300, 70], 8, 2, 64, 32, 64, True, 1.25),
+    ([90, 17, 40], [33, 17, 0], 6, 3, 16, 16, 16, False, 0.9),
+    ([260, 500], [131, 129], 5, 5, 128, 128, 96, True, 1.0),
+    ([1000], [999], 16, 2, 128, 16, 128, False, 1.0),
+    ([50, 70], [20, 9], 0, 4, 32, 32, 0, False, 1.0),
+]
+
+
+def append_inputs(c, q_lens, hq, rot, seed):
+    """New rows of every request; some requests' are large, some zero, some small."""
+    g = torch.Generator().manual_seed(seed)
+    rows = sum(q_lens)
+    wide = torch.randn((rows, hq + 2 * c.hkv + 1, 128), generator=g)
+    size = torch.tensor([1.0, 30.0, 2.0 ** -30, 0.0])[torch.arange(rows) // 7 % 4]
+    wide = (wide * torch.where(size > 0, size, 0.0)[:, None, None]).to(torch.bfloat16)
+    positions = torch.cat([torch.arange(n - d, n) for n, d in zip(c.n, q_lens)]) * 37 + seed
+    inv = 10000.0 ** (-2.0 * torch.arange(rot // 2, dtype=torch.float64) / max(rot, 1))
+    return wide, positions, inv
+
+
+def run_append(c, q_lens, wide, positions, inv, hq, interleaved, amplitude, **kw):
+    d_wide = wide.cuda()
+    q, k, v, _ = d_wide.split([hq, c.hkv, c.hkv, 1], dim=1)
+    q_out = torch.full((wide.shape[0], hq, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+    rot = dict(positions=positions.cuda(), inv_freq=inv.cuda()) if inv.numel() else {}
+    B.pa_rope_append_blocks(q=q if hq else None, q_out=q_out if hq else None, k=k, v=v,
+                            k_cache=c.d_k, v_cache=c.d_v, k_scale=c.d_ks, v_scale=c.d_vs,
+                            cu_seqlens_q=kw.pop("cu", rows_of(q_lens)).cuda(),
+                            cache_seqlens=c.d_n, page_table=c.d_table, max_seq_pages=c.msp,
+                            interleaved=interleaved, amplitude=amplitude, **rot, **kw)
+    torch.cuda.synchronize()
+    return q_out
+
+
+def near_codes(got, want, exact_x, scale):
+    """Codes equal but where the value lies within 2^-18 of a border between two codes (the
+    fp32 rotation: sines to 2 ulp, two products and a sum: below 6 * 2^-23 of the largest term)."""
+    off = got != want
+    if not off.any():
+        return
+    gap = (got - want).abs()[off]
+    assert (gap <= torch.maximum(want.abs()[off], got.abs()[off]) * 2.0 ** -3 + 2.0 ** -9).all()
+    middle = (got + want)[off] / 2
+    x = (exact_x / scale)[off]
+    assert ((x - middle).abs() <= 2.0 ** -18 * 448).all()
+    assert off.double().mean() < 1e-3
+
+
+@pytest.mark.parametrize("seqlens,q_lens,hq,hkv,page,block,rot,interleaved,amplitude", APPEND_CASES)
+def test_append(seqlens, q_lens, hq, hkv, page, block, rot, interleaved, amplitude):
+    c = BlockCache(seqlens, hkv, page, block, seed=rot + page)
+    for s in (c.ks, c.vs):  # as earlier appends leave them: powers of two, some too small
+        s.copy_(torch.exp2(-torch.randint(3, 12, s.shape, generator=c.g).float()))
+    c.to_device()
+    wide, positions, inv = append_inputs(c, q_lens, hq, rot, seed=page)
+    q_out = run_append(c, q_lens, wide, positions, inv, hq, interleaved, amplitude)
+    q, k, v, _ = wide.split([hq, hkv, hkv, 1], dim=1)
+    turn = (lambda x: R.rope(x, positions, inv, interleaved, amplitude)) if rot else (lambda x: x.double())
+    if hq:
+        want = turn(q)
+        pair = want.abs().amax(-1, keepdim=True)
+        assert ((q_out.double().cpu() - want).abs() <= HALF_STEP * want.abs() + 2.0 ** -20 * pair).all()
+    for x, codes, scale, d_codes, d_scale in ((turn(k), c.k, c.ks, c.d_k, c.d_ks),
+                                              (v.double(), c.v, c.vs, c.d_v, c.d_vs)):
+        want, ws = R.code_values(codes), scale.double()
+        before = want.clone()
+        at = 0
+        values = before.clone() * ws.repeat_interleave(block, -1)[..., None]
+        for b, (n, d) in enumerate(zip(seqlens, q_lens)):
+            if d:
+                R.append(x[at:at + d], want, ws, c.table[b], n)
+                for i in range(d):
+                    j = n - d + i
+                    values[int(c.table[b, j // page]), :, j % page] = x[at + i]
+            at += d
+        assert torch.equal(d_scale.cpu().double(), ws)
+        got = R.code_values(d_codes.cpu())
+        # (rows that nothing wrote hold what they held, NaN codes among them)
+        same = torch.isnan(want)
+        assert torch.equal(torch.isnan(got), same)
+        full = torch.where(ws > 0, ws, 1.0).repeat_interleave(block, -1)[..., None].expand_as(want)
+        zero = torch.zeros(())
+        near_codes(torch.where(same, zero, got), torch.where(same, zero, want),
+                   torch.where(same, zero, values), full)
+        again = d_codes.clone()
+    # the same append once more leaves the same bits
+    run_append(c, q_lens, wide, positions, inv, hq, interleaved, amplitude)
+    assert torch.equal(c.d_v.view(torch.uint8), again.view(torch.uint8))
