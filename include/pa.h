@@ -88,7 +88,9 @@ typedef enum {
 #define PA_DEVERR_WAIT_TIMEOUT 0x8u          /* a shared-memory copy wait gave up (~2 s) */
 #define PA_DEVERR_SEQLEN_OUT_OF_RANGE 0x10u  /* cache_seqlens < 0 or > max_seq_pages*page_size */
 #define PA_DEVERR_KEPT_OUT_OF_RANGE 0x20u    /* pa_compact_cache: a kept position or its target */
-#define PA_DEVERR_TREE_PARENT 0x40u          /* pa_build_tree_mask: parent not an earlier node */
+#define PA_DEVERR_TREE_PARENT 0x40u          /* pa_build_tree_mask, pa_verify_drafts: parent not an earlier node */
+#define PA_DEVERR_TOKEN_OUT_OF_RANGE 0x80u   /* pa_verify_drafts: token outside the vocabulary */
+#define PA_DEVERR_NO_PROBABILITY 0x100u      /* pa_verify_drafts: a target row of zeros */
 
 /* cu_seqlens_q modes of pa_build_metadata_full. */
 #define PA_Q_MODE_NONE 0    /* leave cu_seqlens_q untouched (decode, target-verify) */
@@ -824,6 +826,49 @@ PA_API int32_t pa_choose_block_splits(int32_t bs, int32_t max_q_len, int32_t num
 PA_API size_t pa_block_workspace_bytes(int32_t bs, int32_t total_q, int32_t max_q_len,
                                        int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
                                        int32_t page_size, int32_t max_seq_pages);
+
+/*
+ * pa_verify_drafts -- drafted tokens accepted or rejected by the target's probabilities and given
+ * random numbers, and the token that follows the accepted ones: what stands between a verify step
+ * (pa_decode_step_tree, pa_decode_step_multi, pa_decode_step_block) and pa_compact_cache.
+ * The rows of request b, cu_seqlens_q[b] .. cu_seqlens_q[b+1], are a tree: row 0 is its newest
+ * token, which stays in any case; row i > 0 is drafted token tokens[row] after row parents[row] of
+ * the request (< i; parents NULL: a chain, i - 1; -1: never reached).  p_i = target_probs[row i]
+ * is the target's distribution of the token after row i; q_i = draft_probs[row i] the one that
+ * row i's children were drawn from, independently.  From node 0, the children x of the node in
+ * order of their rows, with w = p, c = 0, S = 1 at each new node (fp32; the test in fp64):
+ *   accepted if u q(x) S < w(x), u = uniforms[row of x]: on from x
+ *   otherwise c += S, w = max(p - c q, 0), S = sum of w
+ * draft_probs NULL (children proposed for certain, e.g. the draft's likeliest tokens):
+ *   accepted if u S < w(x); otherwise S -= w(x), w(x) = 0 (in fp64)
+ * At the last node the next token is drawn from its w, or from p where nothing of w is left: with
+ * W_x = floor(2^42 min(w(x), 1)) and T their sum, the first x with W_0 + .. + W_x > floor(u T), u =
+ * final_uniforms[b], the product in fp64.  (S above is T 2^-42, rounded to fp32.)  The sums are of
+ * whole numbers, so equal inputs give equal tokens.  Probabilities are finite and not negative.
+ *   target_probs, draft_probs  fp32, row r at x + r * stride (strides in elements, >= vocab; rows
+ *                 on 16-byte boundaries with vocab % 4 == 0 are read faster); normalised
+ *   tokens        [total_q] int64 (row 0 of a request is not read as a draft)
+ *   uniforms      [total_q], final_uniforms [bs] fp32, in [0, 1)
+ *   kept          [bs, kept_stride] int32 (out): positions cache_seqlens[b] - q_len + row of the
+ *                 accepted rows in order, then -1 up to column max_q_len (cache_seqlens NULL: rows)
+ *   counts [bs], begin [bs] int32 (out; begin may be NULL): accepted rows, row 0 among them, and
+ *                 cache_seqlens[b] - q_len: kept (one list for all heads), counts and begin are
+ *                 those of pa_compact_cache in place
+ *   next_tokens   [bs] int64 (out)
+ * A request without rows, or whose rows are refused (more than max_q_len, outside [0, total_q)),
+ * gets counts 0, next token -1.  A token outside [0, vocab) is rejected and sets
+ * PA_DEVERR_TOKEN_OUT_OF_RANGE; a target row without a positive probability that is drawn from
+ * gives -1 and sets PA_DEVERR_NO_PROBABILITY.
+ * Supported: 1 <= max_q_len <= 256; 1 <= vocab <= 2^20; bs <= 65535.
+ */
+PA_API pa_status pa_verify_drafts(const float* target_probs, int64_t target_stride,
+                                  const float* draft_probs, int64_t draft_stride, int32_t vocab,
+                                  const int64_t* tokens, const int32_t* parents,
+                                  const int32_t* cu_seqlens_q, const int32_t* cache_seqlens,
+                                  const float* uniforms, const float* final_uniforms, int32_t bs,
+                                  int32_t total_q, int32_t max_q_len, int32_t* kept,
+                                  int64_t kept_stride, int32_t* counts, int32_t* begin,
+                                  int64_t* next_tokens, void* stream, int32_t use_pdl);
 
 /* Bytes of workspace pa_decode_step needs: m, l and acc partials, each 256-byte aligned. */
 PA_API size_t pa_workspace_bytes(int32_t bs, int32_t num_q_heads, int32_t head_dim,

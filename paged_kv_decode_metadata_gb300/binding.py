@@ -29,6 +29,8 @@ DEVERR_WAIT_TIMEOUT = 0x8
 DEVERR_SEQLEN_OUT_OF_RANGE = 0x10
 DEVERR_KEPT_OUT_OF_RANGE = 0x20
 DEVERR_TREE_PARENT = 0x40
+DEVERR_TOKEN_OUT_OF_RANGE = 0x80
+DEVERR_NO_PROBABILITY = 0x100
 PA_ROPE_PLAIN, PA_ROPE_LINEAR, PA_ROPE_BASE, PA_ROPE_BY_PARTS, PA_ROPE_WAVELENGTH = range(5)
 
 _lock = threading.Lock()
@@ -167,6 +169,8 @@ def _declare(lib):
     lib.pa_choose_block_splits.restype = i32
     lib.pa_block_workspace_bytes.argtypes = [i32] * 8
     lib.pa_block_workspace_bytes.restype = sz
+    lib.pa_verify_drafts.argtypes = [vp, i64, vp, i64, i32, vp, vp, vp, vp, vp, vp, i32, i32, i32,
+                                     vp, i64, vp, vp, vp, vp, i32]
     lib.pa_workspace_bytes.argtypes = [i32, i32, i32, i32]
     lib.pa_workspace_bytes.restype = sz
     lib.pa_choose_splits.argtypes = [i32, i32, i32, i32, i32, i32]
@@ -187,6 +191,7 @@ def _declare(lib):
                  "pa_build_tree_mask", "pa_tree_attention", "pa_decode_step_tree",
                  "pa_accumulate_weights", "pa_compact_cache", "pa_evict",
                  "pa_rope_append_blocks", "pa_block_attention", "pa_decode_step_block",
+                 "pa_verify_drafts",
                  "pa_read_error_flags"):
         getattr(lib, name).restype = ctypes.c_int
     return lib
@@ -1212,4 +1217,56 @@ def pa_decode_step_block(*, lib=None, **kw):
 def prepare_decode_step_block(*, lib=None, **kw) -> PreparedCall:
     """``pa_decode_step_block`` with the given keyword arguments, marshalled once."""
     return PreparedCall("pa_decode_step_block", _decode_step_block_args(**kw), lib,
+                        keep=tuple(kw.values()))
+
+
+# ---- verification of drafted tokens -------------------------------------------------------------
+
+
+def _verify_drafts_args(*, target_probs, tokens, cu_seqlens_q, uniforms, final_uniforms, kept,
+                        counts, next_tokens, max_q_len: int, draft_probs=None, parents=None,
+                        cache_seqlens=None, begin=None, stream=None, use_pdl: bool = True):
+    _on_device(target_probs=target_probs, draft_probs=draft_probs, tokens=tokens, parents=parents,
+               cu_seqlens_q=cu_seqlens_q, cache_seqlens=cache_seqlens, uniforms=uniforms,
+               final_uniforms=final_uniforms, kept=kept, counts=counts, begin=begin,
+               next_tokens=next_tokens)
+    tp = _ptr2d(target_probs, torch.float32, "target_probs")
+    total_q, vocab = target_probs.shape
+    bs = final_uniforms.shape[0]
+    dp, d_stride = None, 0
+    if draft_probs is not None:
+        dp, d_stride = _ptr2d(draft_probs, torch.float32, "draft_probs"), draft_probs.stride(0)
+        _shape(draft_probs, (total_q, vocab), "draft_probs")
+        d_stride = d_stride if total_q > 1 else max(d_stride, vocab)
+    _shape(tokens, (total_q,), "tokens")
+    _shape(uniforms, (total_q,), "uniforms")
+    _shape(cu_seqlens_q, (bs + 1,), "cu_seqlens_q")
+    for name, t in (("counts", counts), ("next_tokens", next_tokens), ("begin", begin),
+                    ("cache_seqlens", cache_seqlens)):
+        if t is not None:
+            _shape(t, (bs,), name)
+    if parents is not None:
+        _shape(parents, (total_q,), "parents")
+    kp, k_stride = _table(kept, bs, int(max_q_len), "kept")
+    stride = target_probs.stride(0)
+    return (tp, stride if total_q > 1 else max(stride, vocab), dp, d_stride, vocab,
+            _ptr(tokens, torch.int64, "tokens"), _ptr(parents, torch.int32, "parents"),
+            _ptr(cu_seqlens_q, torch.int32, "cu_seqlens_q"),
+            _ptr(cache_seqlens, torch.int32, "cache_seqlens"),
+            _ptr(uniforms, torch.float32, "uniforms"),
+            _ptr(final_uniforms, torch.float32, "final_uniforms"), bs, total_q, int(max_q_len), kp,
+            k_stride, _ptr(counts, torch.int32, "counts"), _ptr(begin, torch.int32, "begin"),
+            _ptr(next_tokens, torch.int64, "next_tokens"), _stream(stream), int(bool(use_pdl)))
+
+
+def pa_verify_drafts(**kw):
+    """Drafted tokens accepted or rejected by the target's probabilities and given random
+    numbers, and the token that follows; see include/pa.h.  Keyword arguments: those of
+    ``_verify_drafts_args``."""
+    _check("pa_verify_drafts", load().pa_verify_drafts(*_verify_drafts_args(**kw)))
+
+
+def prepare_verify_drafts(*, lib=None, **kw) -> PreparedCall:
+    """``pa_verify_drafts`` with the given keyword arguments, marshalled once."""
+    return PreparedCall("pa_verify_drafts", _verify_drafts_args(**kw), lib,
                         keep=tuple(kw.values()))

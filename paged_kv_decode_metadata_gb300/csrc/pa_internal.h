@@ -11,6 +11,8 @@ namespace pa {
 // Error-word bits of the cache operators, beside those of pa_common.cuh (include/pa.h).
 constexpr unsigned int kErrKeptOutOfRange = 1u << 5;  // kept position, or the position it moves to
 constexpr unsigned int kErrTreeParent = 1u << 6;      // parent of a drafted node, not an earlier node
+constexpr unsigned int kErrTokenOutOfRange = 1u << 7;  // drafted token outside the vocabulary
+constexpr unsigned int kErrNoProbability = 1u << 8;    // a target row without a positive probability
 
 struct MetadataParams {
   const void* req_pool_indices;  // int64 or int32 (idx64)
@@ -200,6 +202,26 @@ struct BlockParams {
   unsigned int* err;
 };
 
+struct VerifyParams {
+  const float* target_probs;
+  int64_t target_stride;
+  const float* draft_probs;  // nullptr: drafted tokens were proposed for certain
+  int64_t draft_stride;
+  int32_t vocab;
+  const int64_t* tokens;
+  const int32_t* parents;  // nullptr: chains
+  const int32_t* cu_seqlens_q;
+  const int32_t* cache_seqlens;  // nullptr: kept nodes are counted from 0
+  const float *uniforms, *final_uniforms;
+  int32_t bs, total_q, max_q_len;
+  int32_t* kept;
+  int64_t kept_stride;
+  int32_t* counts;
+  int32_t* begin;  // nullptr: not written
+  int64_t* next_tokens;
+  unsigned int* err;
+};
+
 struct WeightsParams {
   const void* q;
   const float* lse;
@@ -315,6 +337,7 @@ cudaError_t launch_tree_mma_bf16(const TreeParams& p, int group, int page_size,
                                  cudaStream_t stream, bool use_pdl);
 cudaError_t launch_tree_mma_int8(const TreeParams& p, int group, int page_size,
                                  cudaStream_t stream, bool use_pdl);
+cudaError_t launch_verify(const VerifyParams& p, cudaStream_t stream, bool use_pdl);
 // columns: (query, head) pairs of a tile, 8, 16 or 32.
 cudaError_t launch_block(const BlockParams& p, int columns, cudaStream_t stream, bool use_pdl);
 // Combines the partials of launch_block (num_splits > 1).
