@@ -91,6 +91,8 @@ typedef enum {
 #define PA_DEVERR_TREE_PARENT 0x40u          /* pa_build_tree_mask, pa_verify_drafts: parent not an earlier node */
 #define PA_DEVERR_TOKEN_OUT_OF_RANGE 0x80u   /* pa_verify_drafts: token outside the vocabulary */
 #define PA_DEVERR_NO_PROBABILITY 0x100u      /* pa_verify_drafts: a target row of zeros */
+#define PA_DEVERR_OUT_OF_PAGES 0x200u        /* pa_pages_fork, _extend: fewer free pages than needed */
+#define PA_DEVERR_PAGE_REFS 0x400u           /* pa_pages_fork, _free: a page that nobody holds */
 
 /* cu_seqlens_q modes of pa_build_metadata_full. */
 #define PA_Q_MODE_NONE 0    /* leave cu_seqlens_q untouched (decode, target-verify) */
@@ -869,6 +871,101 @@ PA_API pa_status pa_verify_drafts(const float* target_probs, int64_t target_stri
                                   int32_t total_q, int32_t max_q_len, int32_t* kept,
                                   int64_t kept_stride, int32_t* counts, int32_t* begin,
                                   int64_t* next_tokens, void* stream, int32_t use_pdl);
+
+/*
+ * The page operators -- pages of the pools copied, shared by forked requests, handed out, given
+ * back, and moved to the front.  Their state is the slot table that the metadata stage reads,
+ * req_to_token [num_rows, row_stride] int32 (a page handed out to a row fills all of the page's
+ * slots there, page * page_size + r, up to row_stride), and page_refs [num_pages] int32: the
+ * number of rows that hold a page, 0 where it is free (a caller starts with zeros and hands out
+ * every page by pa_pages_extend or pa_pages_fork).  Free pages are handed out lowest first, so
+ * equal states give equal tables.
+ * A pool is a base address and the bytes of a page in it (K, V, scales, accumulated weights, of
+ * every layer): page p is at base + p * page_bytes.  page_bytes is a multiple of 4 (bases and
+ * page_bytes that are multiples of 16 copy faster), any number of pools; the lists are host
+ * memory, read during the call.
+ * Rows are table rows (req_pool_indices), lens the tokens of each; a call's lists hold `count`
+ * entries.  max_seq_pages: the most pages of a row, (max_seq_pages - 1) * page_size < row_stride.
+ * Rows, lengths, slots that are out of range are skipped (their count or length: 0 or what was
+ * held) and set PA_DEVERR_POOL_ROW_OUT_OF_RANGE, _SEQLEN_OUT_OF_RANGE, _PAGE_OUT_OF_RANGE.
+ * Supported: any page_size >= 1; num_pages <= 2^20, num_pages * page_size < 2^31; count <= 65535;
+ * max_seq_pages * page_size <= 2^29.  workspace: 16-byte aligned, pa_pages_workspace_bytes(
+ * num_pages, count) bytes; calls that overlap on the GPU need workspaces of their own, and calls
+ * on one state must not overlap.
+ */
+typedef struct {
+  void* base;
+  int64_t page_bytes;
+} pa_page_pool;
+
+PA_API size_t pa_pages_workspace_bytes(int64_t num_pages, int32_t count);
+
+/*
+ * pa_pages_copy -- page src_pages[i] of every pool of src_pools to page dst_pages[i] of the same
+ * pool of dst_pools (NULL: src_pools), 0 <= i < count; an entry with a negative page is skipped.
+ * No destination may be a source or another destination of the call.  Either side may be pinned
+ * host memory (swapping a request out or in).  page_bytes of the two lists are equal.
+ */
+PA_API pa_status pa_pages_copy(const pa_page_pool* src_pools, const pa_page_pool* dst_pools,
+                               int32_t num_pools, int64_t num_src_pages, int64_t num_dst_pages,
+                               const int32_t* src_pages, const int32_t* dst_pages, int32_t count,
+                               void* stream, int32_t use_pdl);
+
+/*
+ * pa_pages_fork -- row children[i] becomes a request with the first lens[i] tokens of row
+ * parents[i] (at most what that row holds): full pages are shared, a partly filled last page is
+ * copied, in every pool, to a page of the child's own, so that both may append.  (Whatever
+ * rewrites full pages, as pa_evict in place does, must not be used on shared ones.)  One parent
+ * may have many children; a child is a row that holds nothing, and is listed once.
+ * child_lens[i] (out) = lens[i], or, where no page was left for the last one, its full pages'
+ * tokens, with PA_DEVERR_OUT_OF_PAGES.  A shared page that nobody holds sets PA_DEVERR_PAGE_REFS.
+ */
+PA_API pa_status pa_pages_fork(int32_t* req_to_token, int64_t num_rows, int64_t row_stride,
+                               int32_t* page_refs, int64_t num_pages, int32_t page_size,
+                               int32_t max_seq_pages, const int64_t* parents,
+                               const int64_t* children, const int32_t* lens, int32_t count,
+                               const pa_page_pool* pools, int32_t num_pools, int32_t* child_lens,
+                               void* workspace, size_t workspace_bytes, void* stream,
+                               int32_t use_pdl);
+
+/*
+ * pa_pages_extend -- pages for rows[i] to grow from lens[i] to new_lens[i] tokens (0 for a new
+ * request).  granted[i] (out) = the larger of the two, or less where pages ran out (what the
+ * pages it got hold; entries are served in order), with PA_DEVERR_OUT_OF_PAGES.  A row is listed
+ * once.
+ */
+PA_API pa_status pa_pages_extend(int32_t* req_to_token, int64_t num_rows, int64_t row_stride,
+                                 int32_t* page_refs, int64_t num_pages, int32_t page_size,
+                                 int32_t max_seq_pages, const int64_t* rows, const int32_t* lens,
+                                 const int32_t* new_lens, int32_t count, int32_t* granted,
+                                 void* workspace, size_t workspace_bytes, void* stream,
+                                 int32_t use_pdl);
+
+/*
+ * pa_pages_free -- the pages of rows[i] that hold tokens past keep_lens[i] (NULL: 0) given back:
+ * one holder less each, and the page's first slot in the row becomes -1.  Pages whose first slot
+ * is negative have been given back already (a row listed twice is given back once).  A page that
+ * nobody holds sets PA_DEVERR_PAGE_REFS.
+ */
+PA_API pa_status pa_pages_free(int32_t* req_to_token, int64_t num_rows, int64_t row_stride,
+                               int32_t* page_refs, int64_t num_pages, int32_t page_size,
+                               int32_t max_seq_pages, const int64_t* rows, const int32_t* lens,
+                               const int32_t* keep_lens, int32_t count, void* stream,
+                               int32_t use_pdl);
+
+/*
+ * pa_pages_compact -- the live pages moved to the front of every pool: with L of them (num_live
+ * [1], out), the live pages at L and past it, in order, move to the free ones below L, in order.
+ * page_refs follow, and the slots of the listed rows (every row that holds pages should be
+ * listed).  page_map [num_pages] int32 (out): the new place of every live page, -1 for free ones,
+ * for tables kept elsewhere.  count 0: no row is rewritten.
+ */
+PA_API pa_status pa_pages_compact(int32_t* req_to_token, int64_t num_rows, int64_t row_stride,
+                                  int32_t* page_refs, int64_t num_pages, int32_t page_size,
+                                  int32_t max_seq_pages, const int64_t* rows, const int32_t* lens,
+                                  int32_t count, const pa_page_pool* pools, int32_t num_pools,
+                                  int32_t* page_map, int32_t* num_live, void* workspace,
+                                  size_t workspace_bytes, void* stream, int32_t use_pdl);
 
 /* Bytes of workspace pa_decode_step needs: m, l and acc partials, each 256-byte aligned. */
 PA_API size_t pa_workspace_bytes(int32_t bs, int32_t num_q_heads, int32_t head_dim,

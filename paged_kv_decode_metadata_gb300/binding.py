@@ -31,6 +31,8 @@ DEVERR_KEPT_OUT_OF_RANGE = 0x20
 DEVERR_TREE_PARENT = 0x40
 DEVERR_TOKEN_OUT_OF_RANGE = 0x80
 DEVERR_NO_PROBABILITY = 0x100
+DEVERR_OUT_OF_PAGES = 0x200
+DEVERR_PAGE_REFS = 0x400
 PA_ROPE_PLAIN, PA_ROPE_LINEAR, PA_ROPE_BASE, PA_ROPE_BY_PARTS, PA_ROPE_WAVELENGTH = range(5)
 
 _lock = threading.Lock()
@@ -171,6 +173,14 @@ def _declare(lib):
     lib.pa_block_workspace_bytes.restype = sz
     lib.pa_verify_drafts.argtypes = [vp, i64, vp, i64, i32, vp, vp, vp, vp, vp, vp, i32, i32, i32,
                                      vp, i64, vp, vp, vp, vp, i32]
+    lib.pa_pages_workspace_bytes.argtypes = [i64, i32]
+    lib.pa_pages_workspace_bytes.restype = sz
+    lib.pa_pages_copy.argtypes = [vp, vp, i32, i64, i64, vp, vp, i32, vp, i32]
+    table = [vp, i64, i64, vp, i64, i32, i32]
+    lib.pa_pages_fork.argtypes = table + [vp, vp, vp, i32, vp, i32, vp, vp, sz, vp, i32]
+    lib.pa_pages_extend.argtypes = table + [vp, vp, vp, i32, vp, vp, sz, vp, i32]
+    lib.pa_pages_free.argtypes = table + [vp, vp, vp, i32, vp, i32]
+    lib.pa_pages_compact.argtypes = table + [vp, vp, i32, vp, i32, vp, vp, vp, sz, vp, i32]
     lib.pa_workspace_bytes.argtypes = [i32, i32, i32, i32]
     lib.pa_workspace_bytes.restype = sz
     lib.pa_choose_splits.argtypes = [i32, i32, i32, i32, i32, i32]
@@ -191,7 +201,8 @@ def _declare(lib):
                  "pa_build_tree_mask", "pa_tree_attention", "pa_decode_step_tree",
                  "pa_accumulate_weights", "pa_compact_cache", "pa_evict",
                  "pa_rope_append_blocks", "pa_block_attention", "pa_decode_step_block",
-                 "pa_verify_drafts",
+                 "pa_verify_drafts", "pa_pages_copy", "pa_pages_fork", "pa_pages_extend",
+                 "pa_pages_free", "pa_pages_compact",
                  "pa_read_error_flags"):
         getattr(lib, name).restype = ctypes.c_int
     return lib
@@ -569,7 +580,9 @@ class PreparedCall:
         self.fn = getattr(self.lib, name)
         self.args = tuple(t(a) if a is not None else None
                           for t, a in zip(self.fn.argtypes, args))
-        self._keep = tuple(k for k in keep if isinstance(k, torch.Tensor))
+        # (and to host arrays, and the tensors of a list of pools)
+        flat = [x for k in keep for x in (k if isinstance(k, (list, tuple)) else (k,))]
+        self._keep = tuple(k for k in flat if isinstance(k, (torch.Tensor, ctypes.Array)))
 
     def __call__(self):
         st = self.fn(*self.args)
@@ -1270,3 +1283,181 @@ def prepare_verify_drafts(*, lib=None, **kw) -> PreparedCall:
     """``pa_verify_drafts`` with the given keyword arguments, marshalled once."""
     return PreparedCall("pa_verify_drafts", _verify_drafts_args(**kw), lib,
                         keep=tuple(kw.values()))
+
+
+# ---- pages: copied, forked, extended, freed, compacted --------------------------------------------
+
+
+class _PagePool(ctypes.Structure):
+    _fields_ = [("base", ctypes.c_void_p), ("page_bytes", ctypes.c_int64)]
+
+
+def _page_pools(pools, num_pages: int, name: str, pinned: bool = False):
+    """Host array of the pools' base addresses and page sizes: tensors [num_pages, ...],
+    contiguous, on the current device (``pinned``: or in pinned host memory)."""
+    array = (_PagePool * max(len(pools), 1))()
+    for i, t in enumerate(pools):
+        if t.dim() < 2 or t.shape[0] != num_pages or not t.is_contiguous():
+            raise ValueError(f"{name}[{i}] must be a contiguous tensor of {num_pages} pages")
+        if pinned and not t.is_cuda:
+            if not t.is_pinned():
+                raise ValueError(f"{name}[{i}] must be a CUDA tensor or pinned host memory")
+        else:
+            _on_device(**{f"{name}[{i}]": t})
+        array[i].base = t.data_ptr()
+        array[i].page_bytes = t.numel() // max(num_pages, 1) * t.element_size()
+    return array
+
+
+def _slot_table(req_to_token, page_refs, page_size: int, max_seq_pages: int, rows, lens):
+    """The page operators' common arguments and the length of their lists."""
+    stride = _row_stride(req_to_token, "req_to_token")
+    stride = stride if req_to_token.shape[0] > 1 else max(stride, req_to_token.shape[1])
+    if page_refs.dim() != 1:
+        raise ValueError("page_refs must be [num_pages]")
+    count = rows.numel()
+    _shape(rows, (count,), "rows")
+    _shape(lens, (count,), "lens")
+    if int(max_seq_pages) * int(page_size) > req_to_token.shape[1] + int(page_size) - 1:
+        raise ValueError(f"req_to_token has room for fewer than {max_seq_pages} pages a row")
+    return (_ptr2d(req_to_token, torch.int32, "req_to_token"), req_to_token.shape[0], stride,
+            _ptr(page_refs, torch.int32, "page_refs"), page_refs.numel(), int(page_size),
+            int(max_seq_pages)), count
+
+
+def pa_pages_workspace_bytes(num_pages: int, count: int) -> int:
+    """Workspace of a fork, extension or compaction; see include/pa.h."""
+    return int(load().pa_pages_workspace_bytes(int(num_pages), int(count)))
+
+
+def _pages_copy_args(*, src_pools, src_pages, dst_pages, dst_pools=None, stream=None,
+                     use_pdl: bool = True):
+    _on_device(src_pages=src_pages, dst_pages=dst_pages)
+    count = src_pages.numel()
+    _shape(src_pages, (count,), "src_pages")
+    _shape(dst_pages, (count,), "dst_pages")
+    num_src = src_pools[0].shape[0] if src_pools else 0
+    src = _page_pools(src_pools, num_src, "src_pools", pinned=True)
+    dst, num_dst = src, num_src
+    if dst_pools is not None:
+        if len(dst_pools) != len(src_pools):
+            raise ValueError("src_pools and dst_pools must be lists of one length")
+        num_dst = dst_pools[0].shape[0] if dst_pools else 0
+        dst = _page_pools(dst_pools, num_dst, "dst_pools", pinned=True)
+    return (ctypes.addressof(src), ctypes.addressof(dst), len(src_pools), num_src, num_dst,
+            _ptr(src_pages, torch.int32, "src_pages"), _ptr(dst_pages, torch.int32, "dst_pages"),
+            count, _stream(stream), int(bool(use_pdl))), (src, dst)
+
+
+def pa_pages_copy(**kw):
+    """Pages copied within or between pools; see include/pa.h.  Keyword arguments: those of
+    ``_pages_copy_args``."""
+    args, _arrays = _pages_copy_args(**kw)
+    _check("pa_pages_copy", load().pa_pages_copy(*args))
+
+
+def prepare_pages_copy(*, lib=None, **kw) -> PreparedCall:
+    """``pa_pages_copy`` with the given keyword arguments, marshalled once."""
+    args, arrays = _pages_copy_args(**kw)
+    return PreparedCall("pa_pages_copy", args, lib, keep=(*kw.values(), *arrays))
+
+
+def _pages_fork_args(*, req_to_token, page_refs, page_size: int, max_seq_pages: int, parents,
+                     children, lens, pools, child_lens, workspace, stream=None,
+                     use_pdl: bool = True):
+    _on_device(req_to_token=req_to_token, page_refs=page_refs, parents=parents, children=children,
+               lens=lens, child_lens=child_lens, workspace=workspace)
+    table, count = _slot_table(req_to_token, page_refs, page_size, max_seq_pages, parents, lens)
+    _shape(children, (count,), "children")
+    _shape(child_lens, (count,), "child_lens")
+    array = _page_pools(pools, page_refs.numel(), "pools")
+    return (*table, _ptr(parents, torch.int64, "parents"), _ptr(children, torch.int64, "children"),
+            _ptr(lens, torch.int32, "lens"), count, ctypes.addressof(array), len(pools),
+            _ptr(child_lens, torch.int32, "child_lens"), *_workspace(workspace), _stream(stream),
+            int(bool(use_pdl))), (array,)
+
+
+def pa_pages_fork(**kw):
+    """Requests forked: full pages shared, the last one copied; see include/pa.h.  Keyword
+    arguments: those of ``_pages_fork_args``."""
+    args, _arrays = _pages_fork_args(**kw)
+    _check("pa_pages_fork", load().pa_pages_fork(*args))
+
+
+def prepare_pages_fork(*, lib=None, **kw) -> PreparedCall:
+    """``pa_pages_fork`` with the given keyword arguments, marshalled once."""
+    args, arrays = _pages_fork_args(**kw)
+    return PreparedCall("pa_pages_fork", args, lib, keep=(*kw.values(), *arrays))
+
+
+def _pages_extend_args(*, req_to_token, page_refs, page_size: int, max_seq_pages: int, rows, lens,
+                       new_lens, granted, workspace, stream=None, use_pdl: bool = True):
+    _on_device(req_to_token=req_to_token, page_refs=page_refs, rows=rows, lens=lens,
+               new_lens=new_lens, granted=granted, workspace=workspace)
+    table, count = _slot_table(req_to_token, page_refs, page_size, max_seq_pages, rows, lens)
+    _shape(new_lens, (count,), "new_lens")
+    _shape(granted, (count,), "granted")
+    return (*table, _ptr(rows, torch.int64, "rows"), _ptr(lens, torch.int32, "lens"),
+            _ptr(new_lens, torch.int32, "new_lens"), count,
+            _ptr(granted, torch.int32, "granted"), *_workspace(workspace), _stream(stream),
+            int(bool(use_pdl)))
+
+
+def pa_pages_extend(**kw):
+    """Free pages handed out to growing requests; see include/pa.h.  Keyword arguments: those
+    of ``_pages_extend_args``."""
+    _check("pa_pages_extend", load().pa_pages_extend(*_pages_extend_args(**kw)))
+
+
+def prepare_pages_extend(*, lib=None, **kw) -> PreparedCall:
+    """``pa_pages_extend`` with the given keyword arguments, marshalled once."""
+    return PreparedCall("pa_pages_extend", _pages_extend_args(**kw), lib, keep=tuple(kw.values()))
+
+
+def _pages_free_args(*, req_to_token, page_refs, page_size: int, max_seq_pages: int, rows, lens,
+                     keep_lens=None, stream=None, use_pdl: bool = True):
+    _on_device(req_to_token=req_to_token, page_refs=page_refs, rows=rows, lens=lens,
+               keep_lens=keep_lens)
+    table, count = _slot_table(req_to_token, page_refs, page_size, max_seq_pages, rows, lens)
+    if keep_lens is not None:
+        _shape(keep_lens, (count,), "keep_lens")
+    return (*table, _ptr(rows, torch.int64, "rows"), _ptr(lens, torch.int32, "lens"),
+            _ptr(keep_lens, torch.int32, "keep_lens"), count, _stream(stream), int(bool(use_pdl)))
+
+
+def pa_pages_free(**kw):
+    """Pages of requests given back; see include/pa.h.  Keyword arguments: those of
+    ``_pages_free_args``."""
+    _check("pa_pages_free", load().pa_pages_free(*_pages_free_args(**kw)))
+
+
+def prepare_pages_free(*, lib=None, **kw) -> PreparedCall:
+    """``pa_pages_free`` with the given keyword arguments, marshalled once."""
+    return PreparedCall("pa_pages_free", _pages_free_args(**kw), lib, keep=tuple(kw.values()))
+
+
+def _pages_compact_args(*, req_to_token, page_refs, page_size: int, max_seq_pages: int, rows, lens,
+                        pools, page_map, num_live, workspace, stream=None, use_pdl: bool = True):
+    _on_device(req_to_token=req_to_token, page_refs=page_refs, rows=rows, lens=lens,
+               page_map=page_map, num_live=num_live, workspace=workspace)
+    table, count = _slot_table(req_to_token, page_refs, page_size, max_seq_pages, rows, lens)
+    _shape(page_map, tuple(page_refs.shape), "page_map")
+    _shape(num_live, (1,), "num_live")
+    array = _page_pools(pools, page_refs.numel(), "pools")
+    return (*table, _ptr(rows, torch.int64, "rows"), _ptr(lens, torch.int32, "lens"), count,
+            ctypes.addressof(array), len(pools), _ptr(page_map, torch.int32, "page_map"),
+            _ptr(num_live, torch.int32, "num_live"), *_workspace(workspace), _stream(stream),
+            int(bool(use_pdl))), (array,)
+
+
+def pa_pages_compact(**kw):
+    """The live pages moved to the front of their pools; see include/pa.h.  Keyword arguments:
+    those of ``_pages_compact_args``."""
+    args, _arrays = _pages_compact_args(**kw)
+    _check("pa_pages_compact", load().pa_pages_compact(*args))
+
+
+def prepare_pages_compact(*, lib=None, **kw) -> PreparedCall:
+    """``pa_pages_compact`` with the given keyword arguments, marshalled once."""
+    args, arrays = _pages_compact_args(**kw)
+    return PreparedCall("pa_pages_compact", args, lib, keep=(*kw.values(), *arrays))

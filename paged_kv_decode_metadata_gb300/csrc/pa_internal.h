@@ -13,6 +13,8 @@ constexpr unsigned int kErrKeptOutOfRange = 1u << 5;  // kept position, or the p
 constexpr unsigned int kErrTreeParent = 1u << 6;      // parent of a drafted node, not an earlier node
 constexpr unsigned int kErrTokenOutOfRange = 1u << 7;  // drafted token outside the vocabulary
 constexpr unsigned int kErrNoProbability = 1u << 8;    // a target row without a positive probability
+constexpr unsigned int kErrOutOfPages = 1u << 9;       // fewer free pages than were asked for
+constexpr unsigned int kErrPageRefs = 1u << 10;        // a page shared or given back that nobody holds
 
 struct MetadataParams {
   const void* req_pool_indices;  // int64 or int32 (idx64)
@@ -222,6 +224,38 @@ struct VerifyParams {
   unsigned int* err;
 };
 
+// The page operators; each uses what it needs.
+struct PagesParams {
+  int32_t* req_to_token;
+  int64_t num_rows, row_stride;
+  int32_t* page_refs;
+  int64_t num_pages, num_dst_pages;
+  int32_t page_size, max_seq_pages;
+  const int64_t *rows, *children;  // table rows (forks: the parents', the children's)
+  const int32_t *lens, *new_lens;  // (free: tokens held, tokens kept, or nullptr)
+  int32_t count;
+  int32_t* granted;
+  int32_t *src_pages, *dst_pages;  // copies; extend: first of a request's pages in `list`, how many
+  int32_t* list;                   // free pages
+  int32_t* page_map;
+  int32_t* num_live;
+  int32_t* num_moves;  // compaction: copies, counted on the device; else nullptr: `count`
+  unsigned int* err;
+};
+
+// Up to kMax pools of a copy: the large ones (in tasks of part of a page) first.
+struct PagesPools {
+  static constexpr int kMax = 128;
+  struct Pool {
+    const void* src;
+    void* dst;
+    int64_t bytes;  // of a page
+  };
+  Pool pool[kMax];
+  int32_t first_task[kMax + 1];
+  int32_t num, large, tasks;
+};
+
 struct WeightsParams {
   const void* q;
   const float* lse;
@@ -336,6 +370,14 @@ cudaError_t launch_tree_mask(const TreeMaskParams& p, cudaStream_t stream, bool 
 cudaError_t launch_tree_mma_bf16(const TreeParams& p, int group, int page_size,
                                  cudaStream_t stream, bool use_pdl);
 cudaError_t launch_tree_mma_int8(const TreeParams& p, int group, int page_size,
+                                 cudaStream_t stream, bool use_pdl);
+cudaError_t launch_pages_copy(const PagesParams& p, const pa_page_pool* src, const pa_page_pool* dst,
+                              int32_t from, int32_t num, int64_t most, cudaStream_t stream, bool use_pdl);
+cudaError_t launch_pages_fork(const PagesParams& p, const pa_page_pool* pools, int32_t num,
+                              cudaStream_t stream, bool use_pdl);
+cudaError_t launch_pages_extend(const PagesParams& p, cudaStream_t stream, bool use_pdl);
+cudaError_t launch_pages_free(const PagesParams& p, cudaStream_t stream, bool use_pdl);
+cudaError_t launch_pages_compact(const PagesParams& p, const pa_page_pool* pools, int32_t num,
                                  cudaStream_t stream, bool use_pdl);
 cudaError_t launch_verify(const VerifyParams& p, cudaStream_t stream, bool use_pdl);
 // columns: (query, head) pairs of a tile, 8, 16 or 32.
