@@ -772,21 +772,23 @@ PA_API pa_status pa_rope_append_blocks(
  * query that attends to nothing gives out = 0, lse = -inf; rows that no request covers, and those
  * of a request whose rows are refused, are not touched.
  * The codes are multiplied as they are, against bf16 q (exact but for channels below 2^-13 of the
- * row's largest, which keep 2^-21 of it) and weights with 12 bits: out is within 2^-12 sum_j p_j
+ * row's largest, which keep 2^-21 of it) and weights rounded to fp16: out is within 2^-11 sum_j p_j
  * |v_j| before its own rounding, where the scales of 128 consecutive tokens lie within 2^14 of one
- * another; a weight below 2^-26 of the largest weight times scale among them counts as 0 in
- * out (not in lse).  Non-finite codes (NaN) and scales reach the queries that attend to them, a V
+ * another; a weight times scale below 2^-33 of the largest among them counts as 0 in out (not in
+ * lse).  Non-finite codes (NaN) and scales reach the queries that attend to them, a V
  * code every query of its request.  Codes and scales at or past n may hold anything.
- * num_splits: the number of pieces (1 to 4096) that a context is cut into, or 0 for
+ * num_splits: the most pieces (1 to 4096) that a row's context may be cut into, or 0 for
  * pa_choose_block_splits(...).  With 1 `workspace` may be NULL; otherwise it is 16-byte aligned,
  * workspace_bytes >= pa_workspace_bytes(total_q, num_q_heads, 128, that number), and a second
- * launch combines the pieces.  Equal inputs give equal bits.  Calls that overlap on the GPU need
+ * launch combines the pieces of rows that are cut.  The cuts follow from num_splits and the
+ * lengths on the device, so equal inputs give equal bits.  Calls that overlap on the GPU need
  * workspaces of their own.
  * sm_scale * log2(e) finite in fp32.
  * Supported: head_dim 128; page_size 16, 32, 64, 128; num_q_heads / num_kv_heads 1 to 32 (any
  * whole number); 1 <= max_q_len <= 65535; bs and num_kv_heads <= 65535; max_seq_pages * page_size
- * <= 2^29.  A tile has up to 32 (query, head) pairs of a kv head, and every tile reads the
- * request's cache: the call is meant for decoding and short drafts, and right for longer chunks.
+ * <= 2^29 and bs * num_kv_heads * tiles * ceil(max_seq_pages * page_size / 128) < 2^30.  A tile
+ * has up to 32 (query, head) pairs of a kv head, and every tile reads the request's cache: the
+ * call is meant for decoding and short drafts, and right for longer chunks.
  */
 PA_API pa_status pa_block_attention(
     const void* q, const void* k_cache, const void* v_cache, const float* k_scale,
@@ -819,7 +821,7 @@ PA_API pa_status pa_decode_step_block(
     float* lse, void* stream, int32_t use_pdl);
 
 /*
- * The number of pieces that pa_block_attention takes for num_splits == 0 (sm_count <= 0: the
+ * The number of pieces that pa_block_attention allows for num_splits == 0 (sm_count <= 0: the
  * current device), and the workspace bytes it then needs (0 where it is 1).
  */
 PA_API int32_t pa_choose_block_splits(int32_t bs, int32_t max_q_len, int32_t num_q_heads,

@@ -32,6 +32,14 @@ int32_t tile_queries(int32_t group, int32_t max_q_len) {
   return fit < max_q_len ? fit : max_q_len;
 }
 
+// Chunks (128 tokens of a tile of a kv head) of a batch of full lengths.
+int64_t line_chunks(int32_t bs, int32_t max_q_len, int32_t group, int32_t num_kv_heads,
+                    int32_t page_size, int32_t max_seq_pages) {
+  const int64_t units = static_cast<int64_t>(bs) * num_kv_heads * cdiv(max_q_len, tile_queries(group, max_q_len));
+  const int64_t chunks = cdiv(static_cast<int64_t>(max_seq_pages) * page_size, 128) + 2;  // (and what a unit costs beside them)
+  return units > INT64_MAX / chunks ? INT64_MAX : units * chunks;
+}
+
 pa_status check_block_pools(const void* k_cache, const void* v_cache, const float* k_scale,
                             const float* v_scale, int32_t kv_dtype, int32_t scale_block,
                             const int32_t* page_table, int64_t page_table_stride,
@@ -78,6 +86,10 @@ pa_status check_block(const void* q, const void* k_cache, const void* v_cache,
   if (st != PA_OK) return st;
   if (!std::isfinite(sm_scale * 1.4426950408889634f)) return PA_ERR_INVALID;
   if (num_q_heads / num_kv_heads > kMaxColumns || max_q_len > 65535) return PA_ERR_UNSUPPORTED;
+  // keeps the batch's chunks within 30 bits
+  if (line_chunks(bs, max_q_len, num_q_heads / num_kv_heads, num_kv_heads, page_size, max_seq_pages) >=
+      (int64_t{1} << 30))
+    return PA_ERR_UNSUPPORTED;
   *splits = num_splits > 0 ? num_splits
                            : pa_choose_block_splits(bs, max_q_len, num_q_heads, num_kv_heads,
                                                     page_size, max_seq_pages, 0);
@@ -105,16 +117,20 @@ int32_t pa_choose_block_splits(int32_t bs, int32_t max_q_len, int32_t num_q_head
     return 1;
   if (sm_count <= 0) sm_count = pa::sm_count_of_current_device();
   if (sm_count <= 0) sm_count = 152;
+  // The batch's chunks of 128 tokens are shared out equally over the resident blocks, so a unit (a
+  // tile of a kv head) longer than a share is cut.  Shares of a batch of equal lengths, and room
+  // for one of half the length on average (a ragged one) before shares have to grow.
   const int32_t group = num_q_heads / num_kv_heads;
-  const int64_t units = static_cast<int64_t>(bs) * num_kv_heads *
-                        cdiv(max_q_len, tile_queries(group, max_q_len));
+  const int32_t columns = tile_columns(group, max_q_len);
+  const int64_t units = static_cast<int64_t>(bs) * num_kv_heads * cdiv(max_q_len, tile_queries(group, max_q_len));
   const int64_t chunks = cdiv(static_cast<int64_t>(max_seq_pages) * page_size, 128);
-  const int64_t slots = static_cast<int64_t>(sm_count) * (tile_columns(group, max_q_len) == 8 ? 3 : 2);
-  int64_t want = cdiv(5 * slots / 2, units);
-  const int64_t most = cdiv(chunks, 2);  // a piece holds two chunks at least
-  if (want > most) want = most;
-  const int64_t per = cdiv(chunks, want);
-  return static_cast<int32_t>(cdiv(chunks, per));
+  const int64_t blocks = static_cast<int64_t>(sm_count) * (columns == 8 ? 3 : columns == 16 ? 2 : 1);
+  int64_t share = units * chunks / blocks;
+  if (share < 1) share = 1;
+  int64_t want = cdiv(2 * chunks, share) + 1;
+  if (want > chunks) want = chunks;  // a piece holds a chunk at least
+  if (want > 4096) want = 4096;
+  return static_cast<int32_t>(want);
 }
 
 size_t pa_block_workspace_bytes(int32_t bs, int32_t total_q, int32_t max_q_len,
@@ -235,8 +251,9 @@ pa_status pa_block_attention(const void* q, const void* k_cache, const void* v_c
   p.max_seq_pages = max_seq_pages;
   p.tile_queries = tile_queries(p.group, max_q_len);
   p.num_splits = splits;
-  p.split_chunks = static_cast<int32_t>(
-      cdiv(cdiv(static_cast<int64_t>(max_seq_pages) * page_size, 128), splits));
+  p.sm_count = pa::sm_count_of_current_device();
+  if (p.sm_count < 1) p.sm_count = 1;
+  p.line = line_chunks(bs, max_q_len, p.group, num_kv_heads, page_size, max_seq_pages);
   p.q_scale = sm_scale * 1.4426950408889634f;  // log2(e): the kernel works in base 2
   p.hold_loads = pa::test_hold_loads();
   if (splits > 1) {

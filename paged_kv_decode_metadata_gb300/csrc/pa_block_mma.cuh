@@ -5,8 +5,8 @@
 // a running maximum.  The codes go from memory to the tensor cores as they are, so the other
 // operand of each product is e4m3, too, in pieces: a query row, scaled by a power of two, is
 // hi + lo / 16, which holds bf16 exactly (8 significant bits are 4 and 4; what is lost of the
-// row's small channels is 2^-21 of its largest); a weight is h1 + h2 / 16 + h3 / 256, within
-// 2^-12 of itself, or within 2^-26 of the chunk's largest weight times V scale.  Each piece has
+// row's small channels is 2^-21 of its largest); a weight is rounded to fp16 (2^-11 of itself, or
+// 2^-33 of the chunk's largest weight times V scale) and is h1 + h2 / 16 + h3 / 256.  Each piece has
 // columns of its own in the product, so the pieces are added in fp32.  The K scale multiplies
 // the fp32 score; the V scale multiplies the weight before it is cut into pieces, relative to
 // the chunk's largest V scale, which multiplies the chunk's product.  Products leave tensor
@@ -16,12 +16,17 @@
 // Shape.  M is the cache side: scores are S^T = K Q^T (128 tokens x 2 C columns), outputs O^T =
 // V^T P^T (128 channels x 3 C), C = 8, 16 or 32 columns of (query, head) pairs of one kv head.
 // So few columns cost few cycles, a thread owns a token in the softmax and a channel in the
-// sums, and neither K nor V is moved or widened.  A column's maximum goes over 128 threads: a
-// warp reduction, four numbers in shared memory, one barrier a chunk.
-//   warps 0-3   softmax and sums
-//   warp 4      TMA: a ring of 16 KiB tiles, K and V in turn
-//   warp 5      issues K Q^T (two score buffers: a chunk ahead of the softmax)
-//   warp 6      issues V^T P^T
+// sums, and neither K nor V is moved or widened.  Four warps have 8 columns; a column's maximum
+// goes over their 128 threads: a warp reduction, four numbers in shared memory, one barrier a
+// chunk.
+//   warps 0 .. C/2 - 1   softmax and sums, four for each 8 columns
+//   then one each        TMA: a ring of 16 KiB tiles, K and V in turn, running ahead into the
+//                        next piece; K Q^T (two score buffers: a chunk ahead of the softmax);
+//                        V^T P^T
+// A unit of work is a tile of columns of one (request, kv head).  The batch's units are laid end
+// to end in chunks of 128 tokens and cut into equal shares, one for each of the blocks that are
+// resident at once: ragged batches leave none idle, and only units that a cut falls into need
+// partials.
 #pragma once
 
 #include <math_constants.h>
@@ -34,52 +39,243 @@ namespace block {
 
 constexpr int kTile = 128;  // tokens of a chunk, channels
 constexpr int kTileBytes = kTile * 128;
-constexpr int kThreads = 224;
-constexpr int kTmaWarp = 4, kScoreWarp = 5, kOutWarp = 6;
-constexpr float kLift = 256.f;  // of a chunk's largest weight: its first piece
+constexpr float kNothing = -3.402823466e38f;  // a maximum before any score (which, finite, is not below it)
+
+// One piece of work: chunks [c0, c1) of one unit (a tile of queries of a request, a kv head).
+struct Piece {
+  int b, q_begin, q_len, n;  // the request, its query rows, its cached tokens
+  int kvh, tile;
+  int c0, c1;
+  int slot, pieces;  // which of the unit's pieces this is, and how many it has
+};
+
+// The batch as one line, unit after unit (by request, kv head, tile), a place for each chunk and
+// kUnitCost before them for what a unit costs beside them: block i takes [i share, (i + 1) share),
+// or, where units are not cut, the units that start there.  Every warp walks its block's share by
+// itself.  (The host keeps the line's length within 31 bits.)
+// (Measured at 0 / 1 / 2 / 4: 64 ragged requests to 16K, 64 / 8 heads, 196 / 175 / 174 / 174 us; 8 ragged
+// chains to 4001 36 / 31 / 24 / 24 us.)
+constexpr int kUnitCost = 2;
+struct Walk {
+  int b, q_begin, q_len, n, tiles, chunks;  // the request at hand
+  int base, pos, end, share;                // its start on the line; where the walk is
+  int cut;                                  // whether units are cut
+
+  // Lengths of request r as they stand, then checked; `report` records what is wrong with them.
+  __device__ __forceinline__ void fetch(const BlockParams& prm, int r) {
+    b = r;
+    q_begin = r;
+    q_len = 1;
+    if (prm.cu_seqlens_q != nullptr) {
+      q_begin = prm.cu_seqlens_q[r];
+      q_len = prm.cu_seqlens_q[r + 1];
+    }
+    n = prm.cache_seqlens[r];
+  }
+  __device__ __forceinline__ void check(const BlockParams& prm, bool report) {
+    if (prm.cu_seqlens_q != nullptr) {
+      q_len -= q_begin;
+      if (q_begin < 0 || q_len < 0 || q_len > prm.max_q_len || q_begin > prm.total_q - q_len) {
+        if (report) record_error(prm.err, kErrSeqLenOutOfRange);
+        q_len = 0;
+      }
+    }
+    const int cap = prm.max_seq_pages << prm.page_shift;
+    if (n < 0 || n > cap) {
+      if (report) record_error(prm.err, kErrSeqLenOutOfRange);
+      n = n < 0 ? 0 : cap;
+    }
+    // (a division only where there can be several tiles)
+    tiles = prm.max_q_len <= prm.tile_queries ? (q_len > 0) : (q_len + prm.tile_queries - 1) / prm.tile_queries;
+    chunks = (n + kTile - 1) / kTile;
+  }
+  __device__ __forceinline__ void load(const BlockParams& prm, int r, bool report) {
+    fetch(prm, r);
+    check(prm, report);
+  }
+  __device__ __forceinline__ int length(const BlockParams& prm) const {
+    return chunks > 0 ? tiles * prm.num_kv_heads * (chunks + kUnitCost) : 0;
+  }
+
+  // Whole-warp: finds the block's share.  Returns whether some request has queries but nothing
+  // cached (its rows are no work, but have a result).  A lane has 4 requests of each 128 (one of 32
+  // in small batches), whose lengths are asked for at once.
+  __device__ __forceinline__ bool start(const BlockParams& prm, int lane) {
+    constexpr int kPer = 4;
+    const int per = prm.bs <= 32 ? 1 : kPer, round_size = 32 * per;
+    Walk r[kPer];
+    int total = 0, longest = 0, w = 0, incl = 0;
+    bool empties = false;
+    auto round = [&](int r0, bool report) {
+      w = 0;
+#pragma unroll
+      for (int k = 0; k < kPer; ++k)
+        if (k < per) r[k].fetch(prm, min(r0 + lane * per + k, prm.bs - 1));
+#pragma unroll
+      for (int k = 0; k < kPer; ++k) {
+        if (k < per) r[k].check(prm, report);
+        if (k >= per || r0 + lane * per + k >= prm.bs) r[k].n = r[k].q_len = r[k].tiles = r[k].chunks = 0;
+        w += r[k].length(prm);
+      }
+      incl = w;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int up = __shfl_up_sync(0xffffffffu, incl, d);
+        if (lane >= d) incl += up;
+      }
+    };
+    for (int r0 = 0; r0 < prm.bs; r0 += round_size) {
+      round(r0, blockIdx.x == 0);
+#pragma unroll
+      for (int k = 0; k < kPer; ++k) {
+        empties = empties || (r[k].q_len > 0 && r[k].n == 0);
+        if (r[k].tiles > 0) longest = max(longest, r[k].chunks);
+      }
+      total += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    longest = __reduce_max_sync(0xffffffffu, longest);
+    empties = __any_sync(0xffffffffu, empties);
+    // A unit of c chunks (its places in a row) meets at most floor((c - 1) / share) + 2 shares (c of them if share is
+    // 1): a share of longest / (num_splits - 1) keeps every unit's pieces within num_splits.
+    const int S = prm.num_splits, grid = static_cast<int>(gridDim.x);
+    share = (total + grid - 1) / grid;
+    cut = S > 1;
+    if (cut && S < longest) share = max(share, (longest + S - 2) / (S - 1));
+    const long long at_ll = static_cast<long long>(blockIdx.x) * share;
+    pos = static_cast<int>(min(at_ll, static_cast<long long>(total)));
+    end = static_cast<int>(min(at_ll + share, static_cast<long long>(total)));
+    if (pos >= end) return empties;
+    // the request that holds pos
+    int before = 0;
+    for (int r0 = 0; r0 < prm.bs; r0 += round_size) {
+      if (prm.bs > round_size) round(r0, false);
+      const uint32_t has = __ballot_sync(0xffffffffu, pos < before + incl);
+      if (has != 0) {
+        const int from = __ffs(has) - 1;
+        int first = before + incl - w;  // (of lane `from`, whose requests hold pos)
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) {
+          const int length_k = r[k].length(prm);
+          if (first <= pos && pos < first + length_k) {
+            b = r[k].b;
+            q_begin = r[k].q_begin;
+            q_len = r[k].q_len;
+            n = r[k].n;
+            tiles = r[k].tiles;
+            chunks = r[k].chunks;
+            base = first;
+          }
+          first += length_k;
+        }
+        b = __shfl_sync(0xffffffffu, b, from);
+        q_begin = __shfl_sync(0xffffffffu, q_begin, from);
+        q_len = __shfl_sync(0xffffffffu, q_len, from);
+        n = __shfl_sync(0xffffffffu, n, from);
+        tiles = __shfl_sync(0xffffffffu, tiles, from);
+        chunks = __shfl_sync(0xffffffffu, chunks, from);
+        base = __shfl_sync(0xffffffffu, base, from);
+        break;
+      }
+      before += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    const int unit = chunks + kUnitCost;
+    if (!cut) pos = base + (pos - base + unit - 1) / unit * unit;
+    return empties;
+  }
+
+  __device__ __forceinline__ bool next(const BlockParams& prm, Piece& p) {
+    while (pos < end) {
+      while (pos - base >= length(prm)) {  // into the next request that has work
+        base += length(prm);
+        load(prm, b + 1, false);
+      }
+      const int unit = (pos - base) / (chunks + kUnitCost);
+      const int from = base + unit * (chunks + kUnitCost) + kUnitCost;  // of the unit's first chunk
+      p.b = b;
+      p.q_begin = q_begin;
+      p.q_len = q_len;
+      p.n = n;
+      p.kvh = tiles == 1 ? unit : unit / tiles;
+      p.tile = unit - p.kvh * tiles;
+      p.c0 = max(pos - from, 0);
+      p.c1 = cut ? min(chunks, end - from) : chunks;
+      p.slot = 0;
+      p.pieces = 1;
+      if (cut) {
+        const int first = from / share;
+        p.slot = static_cast<int>(blockIdx.x) - first;
+        p.pieces = (from + chunks - 1) / share - first + 1;
+      }
+      pos = min(from + chunks, cut ? end : INT_MAX);
+      if (p.c1 > p.c0) return true;  // (a share may end before a unit's first chunk)
+    }
+    return false;
+  }
+};
 
 template <int C>
 struct Shape {
+  static constexpr int kSoftmaxWarps = C / 2;
+  static constexpr int kTmaWarp = kSoftmaxWarps, kScoreWarp = kTmaWarp + 1, kOutWarp = kTmaWarp + 2;
+  static constexpr int kThreads = 32 * (kOutWarp + 2);  // (a warpgroup of these, one idle)
+  // registers a thread: of the launch, then of the softmax warps and the others
+  static constexpr int kLaunchRegs = C == 32 ? 96 : 80;
+  static constexpr int kSoftmaxRegs = C == 8 ? 96 : C == 16 ? 88 : 104, kOtherRegs = 64;
+  static_assert(32 * (kSoftmaxWarps * kSoftmaxRegs + 4 * kOtherRegs) <= kThreads * kLaunchRegs, "register split");
   static constexpr int kScoreCols = 2 * C;
   static constexpr int kOutCols = (3 * C + 15) / 16 * 16;
-  static constexpr int kTmemCols = 2 * kScoreCols + kOutCols <= 64    ? 64
-                                   : 2 * kScoreCols + kOutCols <= 128 ? 128
-                                                                      : 256;
-  static constexpr int kSlots = C == 8 ? 4 : C == 16 ? 6 : 5;
-  static constexpr int kBlocks = C == 8 ? 3 : 2;  // resident per SM
+  static constexpr int kTmemCols = C == 8 ? 64 : C == 16 ? 128 : 256;
+  static_assert(2 * kScoreCols + kOutCols <= kTmemCols, "tensor memory");
+  static constexpr int kSlots = C == 8 ? 4 : C == 16 ? 6 : 10;
+  // A slot holds K tiles or V tiles, never both in turn: only then has whoever waits for a tile
+  // seen the slot's one before, and a barrier's parity tells which of the two has landed.
+  static_assert(kSlots % 2 == 0, "K and V slots");
+  static constexpr int kBlocks = C == 8 ? 3 : C == 16 ? 2 : 1;  // resident per SM
   static constexpr int kRing = 0;
   static constexpr int kQ = kSlots * kTileBytes;
   static constexpr int kP = kQ + kScoreCols * 128;
-  static constexpr int kEnd = kP + kOutCols * 128;
+  // The weights' tile: a row per token, its 3 C pieces next to one another ("MN-major"), rows of 32,
+  // 64 or 128 bytes with that swizzle.
+  static constexpr int kRowBytes = C == 8 ? 32 : C == 16 ? 64 : 128;
+  static constexpr int kEnd = kP + kTile * kRowBytes;
+  // High word of its descriptor: the stride offset steps 8 rows; version 1; the swizzle's code.
+  static constexpr uint32_t kWeightsHigh =
+      (8u * kRowBytes >> 4) | (1u << 14) | ((C == 8 ? 6u : C == 16 ? 4u : 2u) << 29);
+  // Byte offset of 16-byte piece `c` of row `t`.
+  static __device__ __forceinline__ uint32_t weights_at(int t, int c) {
+    return static_cast<uint32_t>(t * kRowBytes + ((c ^ (C == 8 ? t >> 2 & 1 : C == 16 ? t >> 1 & 3 : t & 7)) << 4));
+  }
   struct alignas(16) Control {
     uint64_t full[kSlots], empty[kSlots];
     uint64_t q_full, s_full[2], s_empty[2], p_full, o_full, drained[2];
-    // per warp: a column's largest score, the largest V scale; of even and of odd chunks (a warp
-    // may write the next chunk's while another still reads this one's)
-    alignas(16) float peak[2][C + 1][4];
+    // per warp of four: a column's largest score, the largest V scale; of even and of odd chunks
+    // (a warp may write the next chunk's while another still reads this one's)
+    alignas(16) float peak[2][C][4];
+    alignas(16) float v_peak[2][C / 8][4];
     alignas(16) float sum[C][4];
     float factor[C];  // of a column's scores
+    Walk walk;
     uint32_t tmem;
-    int abort, issued;
+    int abort, issued, empties;
   };
   static constexpr int kBytes = kEnd + static_cast<int>(sizeof(Control)) + 1024;  // + alignment
-  static_assert((kBytes + 1024) * kBlocks <= 228 * 1024, "resident blocks");
+  static_assert((kBytes + 1024) * kBlocks <= 228 * 1024 && kBytes <= 227 * 1024, "resident blocks");
   static_assert(kTmemCols * kBlocks <= 512, "tensor memory");
 };
 
 // Instruction descriptor: fp32 accumulator, e4m3 operands, M = 128.
-constexpr uint32_t instruction(int n, bool a_mn_major) {
-  return (1u << 4) | (a_mn_major ? 1u << 15 : 0u) | (static_cast<uint32_t>(n / 8) << 17) |
+constexpr uint32_t instruction(int n, bool mn_major) {
+  return (1u << 4) | (mn_major ? 3u << 15 : 0u) | (static_cast<uint32_t>(n / 8) << 17) |
          (static_cast<uint32_t>(kTile / 16) << 24);
 }
 
-__device__ __forceinline__ void mma(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc,
+__device__ __forceinline__ void mma(uint32_t d, uint32_t a, uint32_t b, uint32_t b_high, uint32_t idesc,
                                     bool accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\tsetp.ne.u32 p, %5, 0;\n\t"
-      "mov.b64 da, {%1, %4};\n\tmov.b64 db, {%2, %4};\n\t"
+      "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\tsetp.ne.u32 p, %6, 0;\n\t"
+      "mov.b64 da, {%1, %4};\n\tmov.b64 db, {%2, %5};\n\t"
       "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], da, db, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "r"(b), "r"(idesc), "r"(umma::kOperandHigh), "r"(accumulate ? 1u : 0u)
+      "r"(a), "r"(b), "r"(idesc), "r"(umma::kOperandHigh), "r"(b_high), "r"(accumulate ? 1u : 0u)
       : "memory");
 }
 
@@ -142,10 +338,46 @@ __device__ __forceinline__ float2 from_codes(uint32_t codes) {
   return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
 
-__device__ __forceinline__ void softmax_barrier() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+// Two fp16 values to codes; and 16 times what the codes leave of them (exact: fp16 holds it).
+__device__ __forceinline__ uint32_t half_codes(uint32_t w) {
+  uint16_t c;
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(c) : "r"(w));
+  return c;
+}
+__device__ __forceinline__ uint32_t rest_of(uint32_t w, uint32_t codes) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(codes)));
+  const __half2 d = __hmul2(__hsub2(*reinterpret_cast<const __half2*>(&w), *reinterpret_cast<const __half2*>(&h)),
+                            __float2half2_rn(16.f));
+  return *reinterpret_cast<const uint32_t*>(&d);
+}
+
+// (a predicate, not a branch around the arrival)
+__device__ __forceinline__ void arrive_if(uint64_t* bar, bool yes) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+      "@p mbarrier.arrive.shared::cta.b64 _, [%0];\n\t}" ::"r"(smem_addr(bar)),
+      "r"(yes ? 1u : 0u)
+      : "memory");
+}
+
+// The four warps of 8 columns.  (Numbers that the compiler knows: for others it sets all 16 of a
+// block's barriers aside.)
+template <int kGroups>
+__device__ __forceinline__ void group_barrier(int group) {
+  if (kGroups == 1 || group == 0) {
+    asm volatile("bar.sync 1, 128;" ::: "memory");
+  } else if (kGroups == 2 || group == 1) {
+    asm volatile("bar.sync 2, 128;" ::: "memory");
+  } else if (group == 2) {
+    asm volatile("bar.sync 3, 128;" ::: "memory");
+  } else {
+    asm volatile("bar.sync 4, 128;" ::: "memory");
+  }
+}
 
 template <int C>
-__global__ void __launch_bounds__(kThreads, Shape<C>::kBlocks)
+__global__ void __launch_bounds__(Shape<C>::kThreads, Shape<C>::kBlocks)
     block_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
                  const BlockParams prm) {
   using Sh = Shape<C>;
@@ -158,378 +390,428 @@ __global__ void __launch_bounds__(kThreads, Shape<C>::kBlocks)
 
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // (uniform for the compiler too)
-  const int b = blockIdx.z, kvh = blockIdx.y;
-  const int S = prm.num_splits;
-  const int split = static_cast<int>(blockIdx.x) % S, tile = static_cast<int>(blockIdx.x) / S;
-  const int G = prm.group;
+  const int S = prm.num_splits, G = prm.group;
+  const int page_shift = prm.page_shift, P = 1 << page_shift;
 
   if (tid == 0) {
     for (int i = 0; i < kSlots; ++i) {
       mbar_init(&ctl.full[i], 1);
       mbar_init(&ctl.empty[i], 1);
     }
-    mbar_init(&ctl.q_full, 4);
+    mbar_init(&ctl.q_full, Sh::kSoftmaxWarps);
+    mbar_init(&ctl.p_full, Sh::kSoftmaxWarps);
+    mbar_init(&ctl.o_full, 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&ctl.s_full[i], 1);
-      mbar_init(&ctl.s_empty[i], 4);
+      mbar_init(&ctl.s_empty[i], Sh::kSoftmaxWarps);
       mbar_init(&ctl.drained[i], 1);
     }
-    mbar_init(&ctl.p_full, 4);
-    mbar_init(&ctl.o_full, 1);
     ctl.abort = 0;
     ctl.issued = 0;
     fence_barrier_init();
   }
-  grid_dependency_wait();
-
-  // the request, checked; its queries of this tile and the tokens of this split
-  int q_begin = b, q_len = 1;
-  if (prm.cu_seqlens_q != nullptr) {
-    q_begin = prm.cu_seqlens_q[b];
-    q_len = prm.cu_seqlens_q[b + 1] - q_begin;
-    if (q_begin < 0 || q_len < 0 || q_len > prm.max_q_len || q_begin > prm.total_q - q_len) {
-      if (tid == 0 && blockIdx.x == 0 && kvh == 0) record_error(prm.err, kErrSeqLenOutOfRange);
-      q_len = 0;
-    }
+  if (warp == Sh::kScoreWarp) alloc<Sh::kTmemCols>(&ctl.tmem);
+  if (warp == Sh::kTmaWarp && lane == 0) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map_k)) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map_v)) : "memory");
   }
-  int n = prm.cache_seqlens[b];
-  const int page_shift = prm.page_shift, P = 1 << page_shift;
-  const int cap = prm.max_seq_pages << page_shift;
-  if (n < 0 || n > cap) {
-    if (tid == 0 && blockIdx.x == 0 && kvh == 0) record_error(prm.err, kErrSeqLenOutOfRange);
-    n = n < 0 ? 0 : cap;
-  }
-  const int q0 = tile * prm.tile_queries;
-  const int live = min(q_len - q0, prm.tile_queries);  // queries of this tile
-  if (live <= 0) return;
-  const int cols = live * G;
-  // query i sees positions below n - q_len + i + 1
-  const int end = max(0, min(n, n - q_len + q0 + live));
-  const int first = min(split * prm.split_chunks * kTile, end);
-  const int last = min(end, first + prm.split_chunks * kTile);
-  const int chunks = (last - first + kTile - 1) / kTile;
-  const int64_t row0 = (static_cast<int64_t>(q_begin) + q0) * prm.num_q_heads + kvh * G;
-  auto row_of = [&](int c) { return row0 + static_cast<int64_t>(c / G) * prm.num_q_heads + c % G; };
-  if (chunks == 0) {
-    for (int c = tid; c < cols; c += kThreads) {
-      if (S > 1) {
-        prm.m_out[row_of(c) * S + split] = -CUDART_INF_F;
-        prm.l_out[row_of(c) * S + split] = 0.f;
-      } else if (prm.lse != nullptr) {
-        prm.lse[row_of(c)] = -CUDART_INF_F;
-      }
-    }
-    if (S == 1)
-      for (int i = tid; i < cols * 16; i += kThreads)
-        static_cast<uint4*>(prm.out)[row_of(i >> 4) * 16 + (i & 15)] = make_uint4(0u, 0u, 0u, 0u);
-    return;
-  }
-
-  if (warp == kScoreWarp) alloc<Sh::kTmemCols>(&ctl.tmem);
   umma::fence_before();
   __syncthreads();  // barriers initialised, tensor memory allocated
   umma::fence_after();
   const uint32_t tmem = ctl.tmem;
   const uint32_t out_col = tmem + 2 * Sh::kScoreCols;
+  grid_dependency_wait();
+
+  // The TMA warp finds the block's share and goes on, the others take it over.
+  Walk walk;
+  if (warp == Sh::kTmaWarp) {
+    const bool empties = walk.start(prm, lane);
+    if (lane == 0) {
+      ctl.walk = walk;
+      ctl.empties = empties;
+    }
+    __syncwarp();
+    asm volatile("bar.arrive 5, %0;" ::"n"(Sh::kThreads) : "memory");
+  } else {
+    asm volatile("bar.sync 5, %0;" ::"n"(Sh::kThreads) : "memory");
+    walk = ctl.walk;
+    if (ctl.empties) {  // requests with queries and an empty cache
+      const int at = tid < Sh::kTmaWarp * 32 ? tid : tid - 32;
+      constexpr int kOthers = Sh::kThreads - 32;
+      Walk w;
+      for (int r = blockIdx.x; r < prm.bs; r += gridDim.x) {
+        w.load(prm, r, false);
+        if (w.n > 0) continue;
+        const int64_t first = static_cast<int64_t>(w.q_begin) * prm.num_q_heads;
+        for (int i = at; i < w.q_len * prm.num_q_heads; i += kOthers) {
+          if (prm.lse != nullptr) prm.lse[first + i] = -CUDART_INF_F;
+          if (S > 1) prm.l_out[(first + i) * S] = -1.f;
+        }
+        for (int i = at; i < w.q_len * prm.num_q_heads * 16; i += kOthers)
+          static_cast<uint4*>(prm.out)[first * 16 + i] = make_uint4(0u, 0u, 0u, 0u);
+      }
+    }
+  }
+  Piece p;
   auto give_up = [&]() {
     record_error(prm.err, kErrWaitTimeout);
     *abort_flag = 1;
   };
+  // what a piece covers: tokens [first, last), its tile's queries
+  auto first_of = [&](const Piece& w) { return w.c0 * kTile; };
+  auto live_of = [&](const Piece& w) { return min(w.q_len - w.tile * prm.tile_queries, prm.tile_queries); };
+  // positions that the tile's first query sees (query i: i more)
+  auto seen_of = [&](const Piece& w) { return w.n - w.q_len + w.tile * prm.tile_queries + 1; };
+  auto last_of = [&](const Piece& w) {
+    return max(first_of(w), min(min(w.n, w.c1 * kTile), seen_of(w) + live_of(w) - 1));
+  };
 
-  if (warp < 4) {
+  if (warp < Sh::kSoftmaxWarps) {
     // ======================= softmax and sums ============================================
-    const uint32_t lane_base = static_cast<uint32_t>(warp) << 21;  // lane 32 warp
-    // ----- the query rows' pieces: a warp takes every fourth column, a lane 4 channels -----
-    for (int c = warp; c < C; c += 4) {
-      uint2 w = make_uint2(0u, 0u);
-      if (c < cols)
-        w = reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(prm.q) + row_of(c) * 128)[lane];
-      const float x[4] = {bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y)};
-      const float big = warp_max(fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3]))));
-      const int e = big > 0.f ? 7 - mma::float_exponent(big) : 0;  // the largest in [128, 256)
-      const float up = mma::pow2_clamped(e);
-      uint32_t hi = 0, lo = 0;
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const float y0 = x[2 * i] * up, y1 = x[2 * i + 1] * up;
-        const uint32_t h = to_codes(y0, y1);
-        const float2 back = from_codes(h);
-        hi |= h << (16 * i);
-        lo |= to_codes(16.f * (y0 - back.x), 16.f * (y1 - back.y)) << (16 * i);
-      }
-      auto at = [&](int row) {
-        return smem + Sh::kQ + mma::swz(row, lane >> 2) + 4 * (lane & 3);
-      };
-      *reinterpret_cast<uint32_t*>(at(c)) = hi;
-      *reinterpret_cast<uint32_t*>(at(C + c)) = lo;
-      // (an infinite or NaN channel makes the row's scores NaN)
-      const bool finite = __all_sync(0xffffffffu, fabsf(x[0]) < CUDART_INF_F && fabsf(x[1]) < CUDART_INF_F &&
-                                                      fabsf(x[2]) < CUDART_INF_F && fabsf(x[3]) < CUDART_INF_F);
-      if (lane == 0) ctl.factor[c] = finite ? prm.q_scale * mma::pow2_clamped(-e) : CUDART_NAN_F;
-    }
-    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-    __syncwarp();
-    if (lane == 0) mma::mbar_arrive(&ctl.q_full);
-    softmax_barrier();
-
-    // ----- scales: a thread's token's, a chunk ahead; its page two chunks ahead -----------
-    const int32_t* pt = prm.page_table + static_cast<int64_t>(b) * prm.page_table_stride;
-    const int blocks = P >> prm.block_shift;  // of a page
-    auto page_of = [&](int i) -> int {
-      const int pos = first + i * kTile + tid;
-      return pos < last ? pt[pos >> page_shift] : 0;
-    };
-    auto scale_at = [&](int i, int page) -> int64_t {
-      const int row = (first + i * kTile + tid) & (P - 1);
-      if (page < 0 || page >= prm.num_pages) page = 0;  // (the TMA warp reports it)
-      return (static_cast<int64_t>(page) * prm.num_kv_heads + kvh) * blocks + (row >> prm.block_shift);
-    };
-    int page = page_of(0);
-    float ks = 0.f, vs = 0.f;
-    if (first + tid < last) {
-      ks = prm.k_scale[scale_at(0, page)];
-      vs = prm.v_scale[scale_at(0, page)];
-    }
-    page = page_of(1);
-
-    float m[C], l[C], acc[C];
-#pragma unroll
-    for (int c = 0; c < C; ++c) {
-      m[c] = -CUDART_INF_F;
-      l[c] = 0.f;
-      acc[c] = 0.f;
-    }
-    float v_peak = 0.f;  // of the chunk before
+    umma::registers_up<Sh::kSoftmaxRegs>();
+    const int group = warp >> 2, token = tid & 127, w4 = warp & 3;  // 8 columns, a row of the tile
+    const uint32_t lane_base = static_cast<uint32_t>(w4) << 21;     // lane 32 (warp % 4)
+    const int blocks = P >> prm.block_shift;                        // scales of a page and head
+    uint32_t step = 0;                                              // chunks of the pieces before
     bool ok = true;
-    auto add_product = [&](int i) {  // acc += the product of chunk i
-      ok = ok && mbar_wait_bounded(&ctl.o_full, i & 1u);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) return;
-      umma::fence_after();
-      const float f = v_peak * (1.f / kLift);
+    // the queries of the group's columns, a byte each (no division in the loops)
+    uint32_t queries[2] = {0, 0};
 #pragma unroll
-      for (int g = 0; g < C / 8; ++g) {
+    for (int j = 0; j < 8; ++j) queries[j >> 2] |= static_cast<uint32_t>((8 * group + j) / G) << (8 * (j & 3));
+    auto query_of = [&](int j) { return static_cast<int>((j & 4 ? queries[1] : queries[0]) >> (8 * (j & 3)) & 0xffu); };
+    while (walk.next(prm, p)) {
+      const int first = first_of(p), last = last_of(p), seen0 = seen_of(p);
+      const int chunks = (last - first + kTile - 1) / kTile;
+      const int cols = live_of(p) * G;
+      const int64_t row0 = (static_cast<int64_t>(p.q_begin) + p.tile * prm.tile_queries) * prm.num_q_heads + p.kvh * G;
+      auto row_of = [&](int j) {  // of column 8 group + j
+        return row0 + static_cast<int64_t>(query_of(j)) * (prm.num_q_heads - G) + 8 * group + j;
+      };
+      const int32_t* pt = prm.page_table + static_cast<int64_t>(p.b) * prm.page_table_stride;
+      auto page_of = [&](int i) -> int {
+        const int pos = first + i * kTile + token;
+        return pos < last ? pt[pos >> page_shift] : 0;
+      };
+      auto scale_at = [&](int i, int page) -> int64_t {
+        const int row = (first + i * kTile + token) & (P - 1);
+        if (page < 0 || page >= prm.num_pages) page = 0;  // (the TMA warp reports it)
+        return (static_cast<int64_t>(page) * prm.num_kv_heads + p.kvh) * blocks + (row >> prm.block_shift);
+      };
+      int page = page_of(0);
+      // ----- the query rows' pieces: a warp has two columns, a lane 4 channels ----------------
+      uint2 rows[2];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int c = 2 * warp + u;
+        rows[u] = c < cols && chunks > 0
+                      ? reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(prm.q) + row_of(2 * w4 + u) * 128)[lane]
+                      : make_uint2(0u, 0u);
+      }
+      float ks = 0.f, vs = 0.f;  // a thread's token's scales, a chunk ahead; its page two ahead
+      if (first + token < last) {
+        ks = prm.k_scale[scale_at(0, page)];
+        vs = prm.v_scale[scale_at(0, page)];
+      }
+      page = page_of(1);
+      if (chunks > 0) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const int c = 2 * warp + u;
+          const float x[4] = {bf16_lo(rows[u].x), bf16_hi(rows[u].x), bf16_lo(rows[u].y), bf16_hi(rows[u].y)};
+          const float mine = fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3])));
+          const float big = warp_peak(mine);
+          const int e = big > 0.f ? 7 - mma::float_exponent(big) : 0;  // the largest in [128, 256)
+          const float up = mma::pow2_clamped(e);
+          uint32_t hi = 0, lo = 0;
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const float y0 = x[2 * i] * up, y1 = x[2 * i + 1] * up;
+            const uint32_t h = to_codes(y0, y1);
+            const float2 back = from_codes(h);
+            hi |= h << (16 * i);
+            lo |= to_codes(16.f * (y0 - back.x), 16.f * (y1 - back.y)) << (16 * i);
+          }
+          auto at = [&](int row) { return smem + Sh::kQ + mma::swz(row, lane >> 2) + 4 * (lane & 3); };
+          *reinterpret_cast<uint32_t*>(at(c)) = hi;
+          *reinterpret_cast<uint32_t*>(at(C + c)) = lo;
+          // (an infinite or NaN channel makes the row's scores NaN)
+          const bool finite = __all_sync(0xffffffffu, fabsf(x[0]) < CUDART_INF_F && fabsf(x[1]) < CUDART_INF_F &&
+                                                          fabsf(x[2]) < CUDART_INF_F && fabsf(x[3]) < CUDART_INF_F);
+          if (lane == 0) ctl.factor[c] = finite ? prm.q_scale * mma::pow2_clamped(-e) : CUDART_NAN_F;
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        arrive_if(&ctl.q_full, lane == 0);
+        group_barrier<C / 8>(group);  // the group's factors
+      }
+
+      float m[8], l[8], acc[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        m[j] = kNothing;
+        l[j] = 0.f;
+        acc[j] = 0.f;
+      }
+      float v_down = 0.f;  // of the chunk before: what undoes its V scales' power of two
+      auto add_product = [&](uint32_t at) {  // acc += the product of chunk `at`
+        ok = ok && mbar_wait_bounded(&ctl.o_full, at & 1u);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) return;
+        umma::fence_after();
         float h1[8], h2[8], h3[8];
-        ld8(out_col + lane_base + 8 * g, h1);
-        ld8(out_col + lane_base + C + 8 * g, h2);
-        ld8(out_col + lane_base + 2 * C + 8 * g, h3);
+        const uint32_t oc = out_col + lane_base + 8 * group;
+        ld8(oc, h1);
+        ld8(oc + C, h2);
+        ld8(oc + 2 * C, h3);
         wait_ld(h1, h2, h3);
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-          acc[8 * g + j] = fmaf(fmaf(fmaf(h3[j], 1.f / 16.f, h2[j]), 1.f / 16.f, h1[j]), f, acc[8 * g + j]);
-      }
-      umma::fence_before();
-    };
-    for (int i = 0; i < chunks; ++i) {
-      const int pos = first + i * kTile + tid;
-      // what the next chunks need, on its way
-      float ks_next = 0.f, vs_next = 0.f;
-      if (pos + kTile < last) {
-        ks_next = prm.k_scale[scale_at(i + 1, page)];
-        vs_next = prm.v_scale[scale_at(i + 1, page)];
-      }
-      page = page_of(i + 2);
-      // (after a wait that gave up, the chunks that are left only meet the barrier, so that no
-      // warp waits there for good)
-      ok = ok && mbar_wait_bounded(&ctl.s_full[i & 1], (i >> 1) & 1u);
-      ok = __all_sync(0xffffffffu, ok);
-      umma::fence_after();
-      const uint32_t sc = tmem + (i & 1) * Sh::kScoreCols + lane_base;
-      const int seen0 = n - q_len + q0 + 1;  // positions that the tile's first query sees
-      const bool masked = first + (i + 1) * kTile > min(last, seen0);
-      // columns 8 g .. of this token; positions past the chunk's end or past the column's
-      // query's own are not seen
-      auto scores = [&](int g, float (&x)[8]) {
-        float lo[8];
-        ld8(sc + 8 * g, x);
-        ld8(sc + C + 8 * g, lo);
-        wait_ld(x, lo);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] = fmaf(lo[j], 1.f / 16.f, x[j]) * (ctl.factor[8 * g + j] * ks);
-        if (masked) {
+          acc[j] = fmaf(fmaf(fmaf(h3[j], 1.f / 16.f, h2[j]), 1.f / 16.f, h1[j]), v_down, acc[j]);
+        umma::fence_before();
+      };
+      for (int i = 0; i < chunks; ++i, ++step) {
+        const int pos = first + i * kTile + token;
+        // what the next chunks need, on its way
+        float ks_next = 0.f, vs_next = 0.f;
+        if (pos + kTile < last) {
+          ks_next = prm.k_scale[scale_at(i + 1, page)];
+          vs_next = prm.v_scale[scale_at(i + 1, page)];
+        }
+        page = page_of(i + 2);
+        const uint32_t buf = step & 1u;
+        vs = pos < last ? vs : 0.f;
+        const float v_top = warp_peak(fabsf(vs));
+        if (lane == 0) ctl.v_peak[buf][group][w4] = v_top;
+        // (after a wait that gave up, the chunks that are left only meet the barriers, so that no
+        // warp waits there for good)
+        ok = ok && mbar_wait_bounded(&ctl.s_full[buf], (step >> 1) & 1u);
+        ok = __all_sync(0xffffffffu, ok);
+        float x[8];
+        if (ok) {
+          umma::fence_after();
+          const uint32_t sc = tmem + buf * Sh::kScoreCols + lane_base + 8 * group;
+          float lo[8];
+          ld8(sc, x);
+          ld8(sc + C, lo);
+          wait_ld(x, lo);
+          umma::fence_before();
+          __syncwarp();
+          arrive_if(&ctl.s_empty[buf], lane == 0);
 #pragma unroll
           for (int j = 0; j < 8; ++j)
-            if (pos >= last || pos >= seen0 + (8 * g + j) / G) x[j] = -CUDART_INF_F;
-        }
-      };
-      auto scores_done = [&]() {
-        umma::fence_before();
-        __syncwarp();
-        if (lane == 0) mma::mbar_arrive(&ctl.s_empty[i & 1]);
-      };
-      constexpr bool kKeep = C == 8;  // (wider ones are read again: registers)
-      float x[8];
-      if (ok) {
+            x[j] = fmaf(lo[j], 1.f / 16.f, x[j]) * (ctl.factor[8 * group + j] * ks);
+          // positions past the chunk's end or past the column's query's own are not seen
+          if (first + (i + 1) * kTile > min(last, seen0)) {
 #pragma unroll
-        for (int g = 0; g < C / 8; ++g) {
-          scores(g, x);
-          if (kKeep) scores_done();
+            for (int j = 0; j < 8; ++j)
+              if (pos >= last || pos >= seen0 + query_of(j)) x[j] = -CUDART_INF_F;
+          }
+          // (all eight at once: with a store behind each they took 665 cycles, not 200)
+          float top[8];
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const float top = warp_peak(x[j]);
-            if (lane == 0) ctl.peak[i & 1][8 * g + j][warp] = top;
+          for (int j = 0; j < 8; ++j) top[j] = warp_peak(x[j]);
+          if (lane == 0) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) ctl.peak[buf][8 * group + j][w4] = top[j];
           }
         }
-        vs = pos < last ? vs : 0.f;
-        const float top = warp_peak(fabsf(vs));
-        if (lane == 0) ctl.peak[i & 1][C][warp] = top;
-      }
-      softmax_barrier();
-      if (ok && i > 0) add_product(i - 1);
-      if (ok) {
-        const float4 t = *reinterpret_cast<const float4*>(ctl.peak[i & 1][C]);
-        v_peak = fmaxf(umma::max3(t.x, t.y, t.z), t.w);
-        // the scale relative to the chunk's largest (a chunk of zeros: 0)
-        const float lift = v_peak > 0.f ? vs / v_peak * kLift : v_peak == 0.f ? 0.f : CUDART_NAN_F;
-        unsigned char* p_tile = smem + Sh::kP;
-        auto at = [&](int row) { return p_tile + mma::swz(row, tid >> 4) + (tid & 15); };
+        group_barrier<C / 8>(group);
+        // the product before, which has had the time of a softmax (behind the weights, with buffers
+        // of its own, it held more registers and was slower: 73 us against 65 for 64 chunks)
+        if (ok && i > 0) add_product(step - 1);
+        if (ok) {
+          float4 top[8];
 #pragma unroll
-        for (int g = 0; g < C / 8; ++g) {
-          if (!kKeep) scores(g, x);
-          if (!kKeep && g == C / 8 - 1) scores_done();
+          for (int j = 0; j < 8; ++j) top[j] = *reinterpret_cast<const float4*>(ctl.peak[buf][8 * group + j]);
+          const float4 tv = *reinterpret_cast<const float4*>(ctl.v_peak[buf][group]);
+          // V scales times a power of two that brings the chunk's largest to [128, 256) (infinite: NaN)
+          const float v_top = fmaxf(umma::max3(tv.x, tv.y, tv.z), tv.w);
+          const int e = 7 - mma::float_exponent(v_top);
+          const float lift = v_top < CUDART_INF_F ? vs * mma::pow2_clamped(e) : CUDART_NAN_F;
+          v_down = mma::pow2_clamped(-e);
+          bool moved = false;
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
-            const int c = 8 * g + j;
-            const float4 t = *reinterpret_cast<const float4*>(ctl.peak[i & 1][c]);
-            const float top = fmaxf(umma::max3(t.x, t.y, t.z), fmaxf(t.w, m[c]));
-            if (top != m[c]) {  // (all threads alike)
-              const float alpha = mma::fast_exp2(m[c] - top);
-              m[c] = top;
-              acc[c] *= alpha;
-              l[c] *= alpha;
+            top[j].x = fmaxf(umma::max3(top[j].x, top[j].y, top[j].z), fmaxf(top[j].w, m[j]));
+            moved = moved || top[j].x != m[j];
+          }
+          if (moved) {  // (all threads alike)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const float alpha = mma::fast_exp2(m[j] - top[j].x);
+              m[j] = top[j].x;
+              acc[j] *= alpha;
+              l[j] *= alpha;
             }
-            x[j] = mma::fast_exp2(x[j] - (top == -CUDART_INF_F ? 0.f : top));
-            l[c] += x[j];
-            x[j] *= lift;
           }
+          const uint64_t lift2 = umma::pair(lift, lift);
 #pragma unroll
           for (int j = 0; j < 8; j += 2) {
-            float y0 = x[j], y1 = x[j + 1];
+            const float p0 = mma::fast_exp2(x[j] - m[j]), p1 = mma::fast_exp2(x[j + 1] - m[j + 1]);
+            l[j] += p0;
+            l[j + 1] += p1;
+            umma::unpair(umma::mul2(umma::pair(p0, p1), lift2), x[j], x[j + 1]);
+          }
+          // rounded to fp16 (11 bits), then cut into pieces of 4 bits, exactly
+          uint32_t w[4];
 #pragma unroll
-            for (int piece = 0; piece < 3; ++piece) {
-              const int row = piece * C + 8 * g + j;
-              const uint32_t codes = to_codes(y0, y1);
-              *at(row) = static_cast<unsigned char>(codes);
-              *at(row + 1) = static_cast<unsigned char>(codes >> 8);
-              if (piece < 2) {
-                const float2 back = from_codes(codes);
-                y0 = 16.f * (y0 - back.x);
-                y1 = 16.f * (y1 - back.y);
-              }
+          for (int j = 0; j < 4; ++j) w[j] = mma::pack_f16(x[2 * j], x[2 * j + 1]);
+          unsigned char* p_tile = smem + Sh::kP;
+#pragma unroll
+          for (int piece = 0; piece < 3; ++piece) {
+            uint2 codes;
+            codes.x = half_codes(w[0]) | half_codes(w[1]) << 16;
+            codes.y = half_codes(w[2]) | half_codes(w[3]) << 16;
+            const int at = piece * C + 8 * group;
+            *reinterpret_cast<uint2*>(p_tile + Sh::weights_at(token, at >> 4) + (at & 8)) = codes;
+            if (piece < 2) {
+              w[0] = rest_of(w[0], codes.x & 0xffffu);
+              w[1] = rest_of(w[1], codes.x >> 16);
+              w[2] = rest_of(w[2], codes.y & 0xffffu);
+              w[3] = rest_of(w[3], codes.y >> 16);
+            }
+          }
+          // V rows past the last token may hold anything, and 0 times NaN is NaN
+          const int valid = last - (first + i * kTile);
+          if (valid < kTile && group == 0) {
+            const uint32_t it = 2 * step + 1, slot = it % kSlots;
+            ok = mbar_wait_bounded(&ctl.full[slot], (it / kSlots) & 1u);
+            ok = __all_sync(0xffffffffu, ok);
+            for (int u = valid * 8 + token; u < kTile * 8 && ok; u += 128)
+              *reinterpret_cast<uint4*>(smem + Sh::kRing + slot * kTileBytes + u * 16) = make_uint4(0u, 0u, 0u, 0u);
+          }
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          umma::fence_before();
+          __syncwarp();
+          arrive_if(&ctl.p_full, ok && lane == 0);
+        }
+        ks = ks_next;
+        vs = vs_next;
+      }
+      if (chunks > 0) add_product(step - 1);
+      // ----- the columns' results -----------------------------------------------------------
+      // (sums of 8 columns over 32 lanes: half of the columns change sides at each of three steps)
+      float part[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        part[j] = (lane & 16 ? l[j + 4] : l[j]) + __shfl_xor_sync(0xffffffffu, lane & 16 ? l[j] : l[j + 4], 16);
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        part[j] = (lane & 8 ? part[j + 2] : part[j]) + __shfl_xor_sync(0xffffffffu, lane & 8 ? part[j] : part[j + 2], 8);
+      part[0] = (lane & 4 ? part[1] : part[0]) + __shfl_xor_sync(0xffffffffu, lane & 4 ? part[0] : part[1], 4);
+      part[0] += __shfl_xor_sync(0xffffffffu, part[0], 2);
+      part[0] += __shfl_xor_sync(0xffffffffu, part[0], 1);
+      if ((lane & 3) == 0) ctl.sum[8 * group + (lane >> 2 & 4) + (lane >> 2 & 2) + (lane >> 2 & 1)][w4] = part[0];
+      group_barrier<C / 8>(group);
+      if (ok) {
+        const bool direct = p.pieces == 1;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int c = 8 * group + j;
+          if (c >= cols) break;
+          const float4 t = *reinterpret_cast<const float4*>(ctl.sum[c]);
+          const float total = (t.x + t.y) + (t.z + t.w);
+          const int64_t row = row_of(j);
+          const float m_nat = m[j] == kNothing ? -CUDART_INF_F : m[j] * 0.69314718055994530942f;
+          if (direct) {
+            const float inv = total > 0.f || total != total ? 1.f / total : 0.f;
+            static_cast<__nv_bfloat16*>(prm.out)[row * 128 + token] = __float2bfloat16_rn(acc[j] * inv);
+            if (token == 0) {
+              if (prm.lse != nullptr)
+                prm.lse[row] = m_nat == -CUDART_INF_F && total == total ? m_nat : m_nat + logf(total);
+              if (S > 1) prm.l_out[row * S] = -1.f;  // nothing to combine
+            }
+          } else {
+            prm.acc_out[(row * S + p.slot) * 128 + token] = acc[j];
+            if (token == 0) {
+              prm.m_out[row * S + p.slot] = m_nat;
+              prm.l_out[row * S + p.slot] = total;
+              // the sum after the last piece's ends the row's list
+              if (p.slot == 0 && p.pieces < S) prm.l_out[row * S + p.pieces] = -1.f;
             }
           }
         }
-        // V rows past the last token may hold anything, and 0 times NaN is NaN
-        const int valid = last - (first + i * kTile);
-        if (valid < kTile) {
-          const int it = 2 * i + 1, slot = it % kSlots;
-          ok = mbar_wait_bounded(&ctl.full[slot], static_cast<uint32_t>(it / kSlots) & 1u);
-          ok = __all_sync(0xffffffffu, ok);
-          for (int u = valid * 8 + tid; u < kTile * 8 && ok; u += 128)
-            *reinterpret_cast<uint4*>(smem + Sh::kRing + slot * kTileBytes + u * 16) = make_uint4(0u, 0u, 0u, 0u);
-        }
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        umma::fence_before();
-        __syncwarp();
-        if (ok && lane == 0) mma::mbar_arrive(&ctl.p_full);
       }
-      ks = ks_next;
-      vs = vs_next;
+      group_barrier<C / 8>(group);  // (before the next piece's sums, where neither has chunks)
     }
-    add_product(chunks - 1);
     if (!ok && lane == 0) give_up();
-    // ----- the columns' results -------------------------------------------------------------
-#pragma unroll
-    for (int c = 0; c < C; ++c) {
-      const float part = warp_sum(l[c]);
-      if (lane == 0) ctl.sum[c][warp] = part;
-    }
-    softmax_barrier();
-    if (ok) {
-#pragma unroll
-      for (int c = 0; c < C; ++c) {
-        if (c >= cols) break;
-        const float4 t = *reinterpret_cast<const float4*>(ctl.sum[c]);
-        const float total = (t.x + t.y) + (t.z + t.w);
-        const int64_t row = row_of(c);
-        const float m_nat = m[c] * 0.69314718055994530942f;  // -inf stays -inf
-        if (S > 1) {
-          prm.acc_out[(row * S + split) * 128 + tid] = acc[c];
-          if (tid == 0) {
-            prm.m_out[row * S + split] = m_nat;
-            prm.l_out[row * S + split] = total;
-          }
-        } else {
-          const float inv = total > 0.f || total != total ? 1.f / total : 0.f;
-          static_cast<__nv_bfloat16*>(prm.out)[row * 128 + tid] = __float2bfloat16_rn(acc[c] * inv);
-          if (prm.lse != nullptr && tid == 0)
-            prm.lse[row] = m[c] == -CUDART_INF_F && total == total ? m[c] : m_nat + logf(total);
-        }
-      }
-    }
     umma::fence_before();
-  } else if (warp == kTmaWarp) {
+  } else if (warp == Sh::kTmaWarp) {
     // ======================= TMA ==========================================================
+    umma::registers_down<Sh::kOtherRegs>();
     const int box_shift = min(page_shift, 6), box_rows = 1 << box_shift;
-    const int boxes_of_tile = kTile >> box_shift;  // of a tile: a lane issues one
-    const int32_t* pt = prm.page_table + static_cast<int64_t>(b) * prm.page_table_stride;
+    const int boxes_of_tile = kTile >> box_shift;  // a lane issues one
     const uint64_t policy = l2_evict_first_policy();
-    auto page_of = [&](int i) -> int {
-      const int pos = first + i * kTile + lane * box_rows;
-      return lane < boxes_of_tile && pos < last ? pt[pos >> page_shift] : -1;
-    };
-    int next = page_of(0);
+    uint32_t it = 0;
     bool ok = true;
-    for (int i = 0; i < chunks && ok; ++i) {
-      const int pos = first + i * kTile + lane * box_rows;
-      const bool mine = lane < boxes_of_tile && pos < last;
-      int page = next;
-      next = i + 1 < chunks ? page_of(i + 1) : -1;
-      if (mine && (page < 0 || page >= prm.num_pages)) {
-        record_error(prm.err, kErrPageOutOfRange);
-        page = 0;
-      }
-      const int boxes = min(boxes_of_tile, (last - first - i * kTile + box_rows - 1) >> box_shift);
-      for (int kv = 0; kv < 2; ++kv) {
-        const int it = 2 * i + kv, slot = it % kSlots;
-#ifdef PA_TIMESTAMPS
-        // failure-detection test of the instrumented build: after three tiles nothing is issued,
-        // so the other warps' waits give up with products in flight
-        if (prm.hold_loads && it >= 3) continue;
-#endif
-        ok = it < kSlots || mbar_wait_bounded(&ctl.empty[slot], static_cast<uint32_t>(it / kSlots - 1) & 1u);
-        ok = __all_sync(0xffffffffu, ok && !*abort_flag);
-        if (!ok) break;
-        if (lane == 0) {
-          ctl.issued = it + 1;
-          mbar_arrive_expect_tx(&ctl.full[slot], boxes * box_rows * 128);
+    while (ok && walk.next(prm, p)) {
+      const int first = first_of(p), last = last_of(p);
+      const int chunks = (last - first + kTile - 1) / kTile;
+      const int32_t* pt = prm.page_table + static_cast<int64_t>(p.b) * prm.page_table_stride;
+      auto page_of = [&](int i) -> int {
+        const int pos = first + i * kTile + lane * box_rows;
+        return lane < boxes_of_tile && pos < last ? pt[pos >> page_shift] : -1;
+      };
+      int next = page_of(0);
+      for (int i = 0; i < chunks && ok; ++i) {
+        const int pos = first + i * kTile + lane * box_rows;
+        const bool mine = lane < boxes_of_tile && pos < last;
+        int page = next;
+        next = i + 1 < chunks ? page_of(i + 1) : -1;
+        if (mine && (page < 0 || page >= prm.num_pages)) {
+          record_error(prm.err, kErrPageOutOfRange);
+          page = 0;
         }
-        __syncwarp();
-        if (mine)
-          mma::tma_load_4d(base_addr + Sh::kRing + slot * kTileBytes + lane * box_rows * 128,
-                           kv ? &map_v : &map_k, 0, pos & (P - 1), kvh, page, &ctl.full[slot], policy);
-        __syncwarp();
+        const int boxes = min(boxes_of_tile, (last - first - i * kTile + box_rows - 1) >> box_shift);
+        for (int kv = 0; kv < 2; ++kv, ++it) {
+          const uint32_t slot = it % kSlots;
+#ifdef PA_TIMESTAMPS
+          // failure-detection test of the instrumented build: after three tiles nothing is issued,
+          // so the other warps' waits give up with products in flight
+          if (prm.hold_loads && it >= 3) continue;
+#endif
+          ok = it < kSlots || mbar_wait_bounded(&ctl.empty[slot], (it / kSlots - 1) & 1u);
+          ok = __all_sync(0xffffffffu, ok && !*abort_flag);
+          if (!ok) break;
+          if (lane == 0) {
+            ctl.issued = static_cast<int>(it) + 1;
+            mbar_arrive_expect_tx(&ctl.full[slot], boxes * box_rows * 128);
+          }
+          __syncwarp();
+          if (mine)
+            mma::tma_load_4d(base_addr + Sh::kRing + slot * kTileBytes + lane * box_rows * 128,
+                             kv ? &map_v : &map_k, 0, pos & (P - 1), p.kvh, page, &ctl.full[slot], policy);
+          __syncwarp();
+        }
       }
     }
     if (!ok && lane == 0) give_up();
-  } else if (warp == kScoreWarp) {
+  } else if (warp == Sh::kScoreWarp) {
     // ======================= K Q^T ========================================================
+    umma::registers_down<Sh::kOtherRegs>();
     if (umma::elect()) {
       constexpr uint32_t kDesc = instruction(Sh::kScoreCols, false);
       const uint32_t q = umma::operand(base_addr + Sh::kQ, 16);
-      bool ok = mbar_wait_bounded(&ctl.q_full, 0);
-      for (int i = 0; i < chunks && ok; ++i) {
-        const int it = 2 * i, slot = it % kSlots;
-        ok = mbar_wait_bounded(&ctl.full[slot], static_cast<uint32_t>(it / kSlots) & 1u);
-        if (ok && i >= 2) ok = mbar_wait_bounded(&ctl.s_empty[i & 1], ((i >> 1) - 1) & 1u);
-        if (!ok) break;
-        umma::fence_after();
-        const uint32_t k = umma::operand(base_addr + Sh::kRing + slot * kTileBytes, 16);
+      uint32_t step = 0, piece = 0;
+      bool ok = true;
+      while (ok && walk.next(prm, p)) {
+        const int chunks = (last_of(p) - first_of(p) + kTile - 1) / kTile;
+        if (chunks == 0) continue;
+        ok = mbar_wait_bounded(&ctl.q_full, piece & 1u);
+        ++piece;
+        for (int i = 0; i < chunks && ok; ++i, ++step) {
+          const uint32_t it = 2 * step, slot = it % kSlots, buf = step & 1u;
+          ok = mbar_wait_bounded(&ctl.full[slot], (it / kSlots) & 1u);
+          if (ok && step >= 2) ok = mbar_wait_bounded(&ctl.s_empty[buf], ((step >> 1) - 1) & 1u);
+          if (!ok) break;
+          umma::fence_after();
+          const uint32_t k = umma::operand(base_addr + Sh::kRing + slot * kTileBytes, 16);
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          mma(tmem + (i & 1) * Sh::kScoreCols, k + 2 * j, q + 2 * j, kDesc, j > 0);
-        umma::commit(&ctl.empty[slot]);
-        umma::commit(&ctl.s_full[i & 1]);
+          for (int j = 0; j < 4; ++j) 
+            mma(tmem + buf * Sh::kScoreCols, k + 2 * j, q + 2 * j, umma::kOperandHigh, kDesc, j > 0);
+          umma::commit(&ctl.empty[slot]);
+          umma::commit(&ctl.s_full[buf]);
+        }
       }
       if (!ok) {
         give_up();
@@ -538,24 +820,30 @@ __global__ void __launch_bounds__(kThreads, Shape<C>::kBlocks)
       }
     }
     __syncwarp();
-  } else if (warp == kOutWarp) {
+  } else if (warp == Sh::kOutWarp) {
     // ======================= V^T P^T ======================================================
+    umma::registers_down<Sh::kOtherRegs>();
     if (umma::elect()) {
       constexpr uint32_t kDesc = instruction(Sh::kOutCols, true);
-      const uint32_t p = umma::operand(base_addr + Sh::kP, 16);
+      const uint32_t weights = umma::operand(base_addr + Sh::kP, 16);
+      uint32_t step = 0;
       bool ok = true;
-      for (int i = 0; i < chunks && ok; ++i) {
-        const int it = 2 * i + 1, slot = it % kSlots;
-        ok = mbar_wait_bounded(&ctl.full[slot], static_cast<uint32_t>(it / kSlots) & 1u);
-        if (ok) ok = mbar_wait_bounded(&ctl.p_full, i & 1u);
-        if (!ok) break;
-        umma::fence_after();
-        // 32 tokens a step: 4 KiB of V, 32 bytes of a row of P
-        const uint32_t v = umma::operand(base_addr + Sh::kRing + slot * kTileBytes, 16);
+      while (ok && walk.next(prm, p)) {
+        const int chunks = (last_of(p) - first_of(p) + kTile - 1) / kTile;
+        for (int i = 0; i < chunks && ok; ++i, ++step) {
+          const uint32_t it = 2 * step + 1, slot = it % kSlots;
+          ok = mbar_wait_bounded(&ctl.full[slot], (it / kSlots) & 1u);
+          if (ok) ok = mbar_wait_bounded(&ctl.p_full, step & 1u);
+          if (!ok) break;
+          umma::fence_after();
+          // 32 tokens a step: rows of V, rows of weights
+          const uint32_t v = umma::operand(base_addr + Sh::kRing + slot * kTileBytes, 16);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) mma(out_col, v + j * (4096 >> 4), p + 2 * j, kDesc, j > 0);
-        umma::commit(&ctl.empty[slot]);
-        umma::commit(&ctl.o_full);
+          for (int j = 0; j < 4; ++j)
+            mma(out_col, v + j * (4096 >> 4), weights + j * (32 * Sh::kRowBytes >> 4), Sh::kWeightsHigh, kDesc, j > 0);
+          umma::commit(&ctl.empty[slot]);
+          umma::commit(&ctl.o_full);
+        }
       }
       if (!ok) {
         give_up();
@@ -564,7 +852,10 @@ __global__ void __launch_bounds__(kThreads, Shape<C>::kBlocks)
       }
     }
     __syncwarp();
+  } else {
+    umma::registers_down<Sh::kOtherRegs>();
   }
+  // (not earlier: with the next launches' blocks waiting beside them these took 137 us, not 95)
   trigger_dependents();
   umma::fence_before();
   __syncthreads();  // every load from tensor memory is over
@@ -574,7 +865,7 @@ __global__ void __launch_bounds__(kThreads, Shape<C>::kBlocks)
     for (int i = max(0, issued - kSlots); i < issued; ++i)
       mbar_wait_bounded(&ctl.full[i % kSlots], static_cast<uint32_t>(i / kSlots) & 1u);
   }
-  if (warp == kScoreWarp) {
+  if (warp == Sh::kScoreWarp) {
     umma::fence_after();
     dealloc<Sh::kTmemCols>(tmem);
   }
@@ -583,7 +874,7 @@ __global__ void __launch_bounds__(kThreads, Shape<C>::kBlocks)
 // ---- host side ------------------------------------------------------------------------------
 
 template <int C>
-cudaError_t launch_one(const BlockParams& p, int tiles, cudaStream_t stream, bool use_pdl) {
+cudaError_t launch_one(const BlockParams& p, cudaStream_t stream, bool use_pdl) {
   CUtensorMap mk, mv;
   cudaError_t e = mma::encode_pool_map(&mk, p.k_cache, true, p.num_pages, p.num_kv_heads, 1 << p.page_shift);
   if (e != cudaSuccess) return fail_at(e, "tensor map encode (K)");
@@ -599,9 +890,10 @@ cudaError_t launch_one(const BlockParams& p, int tiles, cudaStream_t stream, boo
     if (e != cudaSuccess) return fail_at(e, "shared-memory attribute");
     configured.fetch_or(bit);
   }
-  return fail_at(launch_kernel(block_kernel<C>,
-                               dim3(static_cast<unsigned>(p.num_splits * tiles), p.num_kv_heads, p.bs),
-                               dim3(kThreads), static_cast<size_t>(Shape<C>::kBytes), stream, use_pdl, mk, mv, p),
+  const int64_t most = static_cast<int64_t>(p.sm_count) * Shape<C>::kBlocks;
+  const unsigned blocks = static_cast<unsigned>(p.line < most ? p.line : most);
+  return fail_at(launch_kernel(block_kernel<C>, dim3(blocks), dim3(Shape<C>::kThreads),
+                               static_cast<size_t>(Shape<C>::kBytes), stream, use_pdl, mk, mv, p),
                  "cudaLaunchKernelEx");
 }
 

@@ -194,7 +194,9 @@ struct BlockParams {
   int64_t num_pages;
   int32_t max_seq_pages;
   int32_t tile_queries;  // queries of a tile: its columns are those times the group
-  int32_t num_splits, split_chunks;
+  int32_t num_splits;  // most pieces of a row's context (partial slots per row)
+  int32_t sm_count;
+  int64_t line;        // chunks of the batch at most
   float q_scale;       // sm_scale * log2(e)
   int32_t hold_loads;  // instrumented build only: three tiles, then no more (timeout test)
   // partials of several splits, or (one split) the output itself

@@ -88,13 +88,13 @@ def attend(c, q, q_lens=None, **kw):
 
 
 def check(out, lse, ref, sm_scale=SCALE):
-    """Weights carry 12 bits (2^-12 sum p |v|).  Scores: the pieces' products are added in the
+    """Weights are rounded to fp16 (2^-11 sum p |v|).  Scores: the pieces' products are added in the
     tensor cores' 32 bits, 4 sums of 32, truncated: 2^-20 sum |q k| covers them, the pieces'
     2^-21 and the fp32 factors; a weight is off by twice that (numerator and sum).  Then the
     output's rounding."""
     o, ls, mass, size = ref
     got = out.double().cpu()
-    bound = HALF_STEP * o.abs() + (2.0 ** -12 + 2.0 ** -18 + 2.0 ** -18 * size[..., None]) * mass + 1e-30
+    bound = HALF_STEP * o.abs() + (2.0 ** -11 + 2.0 ** -18 + 2.0 ** -18 * size[..., None]) * mass + 1e-30
     bad = (got - o).abs() > bound
     assert not bad.any(), f"out off by {((got - o).abs() / bound).max():.3g} of its bound"
     dead = ls == -math.inf
