@@ -19,8 +19,8 @@
 namespace pa {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kRowsAtOnce = kThreads / 8;
+constexpr int kFewThreads = 128;
+
 
 __device__ __forceinline__ void unpack(const uint4& w, float* x) {
   const uint32_t v[4] = {w.x, w.y, w.z, w.w};
@@ -77,9 +77,128 @@ __device__ __forceinline__ float needed_scale(float top) {
   return __int_as_float((max(e, -126) + 127) << 23);
 }
 
+// Sine and cosine of `whole` 2^-31 half turns, to 1.4 ulp at most and half an ulp in general (a code
+// that lies next to a border feels the steps that a plain fp32 sine is off).  The nearest quarter is
+// taken off exactly; of the rest, |t| <= pi / 4, Taylor's series with the leading terms' rounding
+// errors carried along: sin t = t + (t_lo - t^3 P(t^2)), cos t = (1 - u) + (.. - u_lo + t^4 Q(t^2)),
+// u = t^2 / 2.
+__device__ __forceinline__ void turn_of(int32_t whole, float& s, float& c) {
+  const int32_t quarter = static_cast<int32_t>((static_cast<uint32_t>(whole) + (1u << 29)) >> 30);
+  const int32_t rest = static_cast<int32_t>(static_cast<uint32_t>(whole) - (static_cast<uint32_t>(quarter) << 30));
+  const float r = static_cast<float>(rest & ~0x3f), r_lo = static_cast<float>(rest & 0x3f);
+  constexpr double kPi = 3.14159265358979323846 / 2147483648.0;
+  constexpr float kHi = static_cast<float>(kPi), kLo = static_cast<float>(kPi - kHi);
+  const float t = r * kHi;
+  const float t_lo = fmaf(r_lo, kHi, fmaf(r, kLo, fmaf(r, kHi, -t)));
+  const float t2 = t * t;
+  float p = fmaf(t2, -1.f / 39916800.f, 1.f / 362880.f);
+  p = fmaf(t2, p, -1.f / 5040.f);
+  p = fmaf(t2, p, 1.f / 120.f);
+  p = fmaf(t2, p, -1.f / 6.f);
+  float sn = t + fmaf(t * t2, p, t_lo);
+  float q = fmaf(t2, 1.f / 479001600.f, -1.f / 3628800.f);
+  q = fmaf(t2, q, 1.f / 40320.f);
+  q = fmaf(t2, q, -1.f / 720.f);
+  q = fmaf(t2, q, 1.f / 24.f);
+  const float u = 0.5f * t2, w = 1.f - u;
+  const float u_lo = fmaf(t, t_lo, 0.5f * fmaf(t, t, -t2));
+  float cs = w + (((1.f - w) - u) + fmaf(t2 * t2, q, -u_lo));
+  if (quarter & 1) {
+    const float x = sn;
+    sn = cs;
+    cs = -x;
+  }
+  s = quarter & 2 ? -sn : sn;
+  c = quarter & 2 ? -cs : cs;
+}
+
+// A scale block that gets rows: the slot's request, its rows and where they go.
+struct Block {
+  int count;           // new rows
+  int held;            // rows of the block before them
+  int in_page;         // row of its page of the first new one
+  int64_t page, t0;    // (page: 0 where the table's is outside the pool); the first new token
+  bool cached;
+
+  // Whole-warp.  False: nothing to do.
+  __device__ __forceinline__ bool find(const RopeBlocksParams& p, int slot, int lane, bool report) {
+    const int B = 1 << p.block_shift;
+    int lo = 0, hi = p.bs;  // the last request whose slots start at or before this one
+    while (true) {
+      const int step = (hi - lo + 31) / 32, at = lo + lane * step;
+      const bool before = at < hi && (p.cu_seqlens_q[at] >> p.block_shift) + 2 * at <= slot;
+      const uint32_t miss = ~__ballot_sync(0xffffffffu, before);
+      const int ahead = miss == 0 ? 32 : __ffs(miss) - 1;
+      if (ahead == 0) return false;
+      lo += (ahead - 1) * step;
+      hi = min(hi, lo + step);
+      if (step == 1) break;
+    }
+    const int b = lo;
+    const int q_begin = p.cu_seqlens_q[b], q_len = p.cu_seqlens_q[b + 1] - q_begin;
+    const int n = p.cache_seqlens[b];
+    if (q_begin < 0 || q_len < 0 || q_len > p.max_q_len || q_begin > p.total_q - q_len || n < q_len ||
+        n > p.max_seq_pages << p.page_shift) {
+      if (report) record_error(p.err, kErrSeqLenOutOfRange);
+      return false;
+    }
+    const int begin = n - q_len;
+    const int block = (begin >> p.block_shift) + slot - ((q_begin >> p.block_shift) + 2 * b);
+    const int first = max(block << p.block_shift, begin);
+    count = min((block + 1) << p.block_shift, n) - first;
+    if (count <= 0) return false;
+    const int at = p.page_table[b * p.page_table_stride + (first >> p.page_shift)];
+    cached = at >= 0 && at < p.num_pages;
+    if (!cached && report) record_error(p.err, kErrPageOutOfRange);
+    page = cached ? at : 0;
+    in_page = first & ((1 << p.page_shift) - 1);
+    held = first & (B - 1);
+    t0 = static_cast<int64_t>(q_begin) + first - begin;
+    return true;
+  }
+};
+
+// A lane's two 16-byte pieces of a row, and their rotation.
+template <bool kInterleaved>
+struct Pieces {
+  bool rotates;
+  int a, b;
+  __device__ __forceinline__ Pieces(int l, int half_pieces) : rotates(l < half_pieces) {
+    a = kInterleaved || !rotates ? 2 * l : l;
+    b = kInterleaved || !rotates ? 2 * l + 1 : l + half_pieces;
+  }
+  static __device__ __forceinline__ void turn(float (&x)[16], const float (&c)[8], const float (&s)[8]) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int u = kInterleaved ? 2 * i : i, v = kInterleaved ? 2 * i + 1 : i + 8;
+      const float y0 = x[u], y1 = x[v];
+      x[u] = y0 * c[i] - y1 * s[i];
+      x[v] = y1 * c[i] + y0 * s[i];
+    }
+  }
+};
+
+__device__ __forceinline__ uint64_t turn_fraction(double inv_freq) {
+  const double turns = inv_freq * 0.15915494309189533577;  // / 2 pi
+  return __double2ull_rz((turns - floor(turns)) * 18446744073709551616.0);
+}
+
+// The sines of a token's pairs 8 l .. 8 l + 7.
+__device__ __forceinline__ void sines_of(uint64_t position, const uint64_t* fraction, int l, float amplitude,
+                                         float (&c)[8], float (&s)[8]) {
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    turn_of(static_cast<int32_t>((position * fraction[8 * l + k]) >> 32), s[k], c[k]);
+    c[k] *= amplitude;
+    s[k] *= amplitude;
+  }
+}
+
 // kPasses: rows of a block, 32 at a time.
-template <int kPasses, bool kInterleaved>
-__global__ void __launch_bounds__(kThreads) rope_blocks_kernel(const RopeBlocksParams p) {
+template <int kThreads, int kPasses, bool kInterleaved>
+__global__ void __launch_bounds__(kThreads, kPasses <= 2 ? 1024 / kThreads : 2)
+    rope_blocks_kernel(const RopeBlocksParams p) {
+  constexpr int kRowsAtOnce = kThreads / 8;
   __shared__ uint64_t fraction[64];
   __shared__ float tops[2][kThreads / 32];
   extern __shared__ float4 sines[];  // [pass][chunk of two pairs][thread]
@@ -87,41 +206,10 @@ __global__ void __launch_bounds__(kThreads) rope_blocks_kernel(const RopeBlocksP
   const int half = p.rotary_dim / 2, half_pieces = p.rotary_dim / 16;
   grid_dependency_wait();
 
-  // ----- the slot's request and block ---------------------------------------------------------
-  const int slot = blockIdx.x, B = 1 << p.block_shift;
-  int lo = 0, hi = p.bs;  // the last request whose slots start at or before this one
-  bool found = true;
-  while (found) {
-    const int step = (hi - lo + 31) / 32, at = lo + lane * step;
-    const bool before = at < hi && (p.cu_seqlens_q[at] >> p.block_shift) + 2 * at <= slot;
-    const uint32_t miss = ~__ballot_sync(0xffffffffu, before);
-    const int ahead = miss == 0 ? 32 : __ffs(miss) - 1;
-    found = ahead > 0;
-    lo += (ahead - 1) * step;
-    hi = min(hi, lo + step);
-    if (step == 1) break;
-  }
-  if (!found) return;
-  const int b = lo;
-  const int q_begin = p.cu_seqlens_q[b], q_len = p.cu_seqlens_q[b + 1] - q_begin;
-  const int n = p.cache_seqlens[b];
-  if (q_begin < 0 || q_len < 0 || q_len > p.max_q_len || q_begin > p.total_q - q_len || n < q_len ||
-      n > p.max_seq_pages << p.page_shift) {
-    if (tid == 0 && blockIdx.y == 0) record_error(p.err, kErrSeqLenOutOfRange);
-    return;
-  }
-  const int begin = n - q_len;
-  const int block = (begin >> p.block_shift) + slot - ((q_begin >> p.block_shift) + 2 * b);
-  const int first = max(block << p.block_shift, begin);
-  const int count = min((block + 1) << p.block_shift, n) - first;  // new rows of this block
-  if (count <= 0) return;
-  const int page_in = p.page_table[b * p.page_table_stride + (first >> p.page_shift)];
-  const bool cached = page_in >= 0 && page_in < p.num_pages;
-  if (!cached && tid == 0 && blockIdx.y == 0) record_error(p.err, kErrPageOutOfRange);
-  const int64_t page = cached ? page_in : 0;
-  const int in_page = first & ((1 << p.page_shift) - 1);  // of the first new row
-  const int held = first & (B - 1);                       // earlier rows of the block
-  const int64_t t0 = static_cast<int64_t>(q_begin) + first - begin;
+  Block blk;
+  if (!blk.find(p, static_cast<int>(blockIdx.x), lane, tid == 0 && blockIdx.y == 0)) return;
+  const int count = blk.count, held = blk.held, in_page = blk.in_page;
+  const int64_t page = blk.page, t0 = blk.t0;
 
   // this share's heads
   const int parts = gridDim.y, part = blockIdx.y;
@@ -130,92 +218,75 @@ __global__ void __launch_bounds__(kThreads) rope_blocks_kernel(const RopeBlocksP
   const int kv_from = static_cast<int>(static_cast<int64_t>(p.num_kv_heads) * part / parts);
   const int kv_to = static_cast<int>(static_cast<int64_t>(p.num_kv_heads) * (part + 1) / parts);
 
-  if (half > 0) {
-    if (tid < half) {
-      const double turns = p.inv_freq[tid] * 0.15915494309189533577;  // / 2 pi
-      fraction[tid] = __double2ull_rz((turns - floor(turns)) * 18446744073709551616.0);
+  const Pieces<kInterleaved> piece(l, half_pieces);
+  const bool rotates = piece.rotates;
+  const int pa = piece.a, pb = piece.b;
+  // ----- the sines of a thread's tokens, and the query rows -------------------------------------
+  // (four rows are on their way all the time: a row's place is filled again as it leaves)
+  const int passes = (count + kRowsAtOnce - 1) / kRowsAtOnce, heads = q_to - q_from;
+  constexpr int kDeep = 4;
+  uint4 wa[kDeep], wb[kDeep];
+  int ask_pass = 0, ask_head = 0;  // the row that is asked for next
+  auto ask = [&](int u) {
+    const int r = ask_pass * kRowsAtOnce + (tid >> 3);
+    if (ask_pass < passes && r < count) {
+      const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) +
+                                                        (t0 + r) * p.q_stride) + (q_from + ask_head) * 16;
+      wa[u] = src[pa];
+      wb[u] = src[pb];
     }
-    __syncthreads();
-  }
-  const bool rotates = l < half_pieces;
-  int pa, pb;  // this lane's two 16-byte pieces of a row
-  if (kInterleaved || !rotates) {
-    pa = 2 * l;
-    pb = 2 * l + 1;
-  } else {
-    pa = l;
-    pb = l + half_pieces;
-  }
-  auto turn = [&](float (&x)[16], const float (&c)[8], const float (&s)[8]) {
-    if constexpr (kInterleaved) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float a = x[2 * i], y = x[2 * i + 1];
-        x[2 * i] = a * c[i] - y * s[i];
-        x[2 * i + 1] = y * c[i] + a * s[i];
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float a = x[i], y = x[i + 8];
-        x[i] = a * c[i] - y * s[i];
-        x[i + 8] = y * c[i] + a * s[i];
-      }
+    if (++ask_head == heads) {
+      ask_head = 0;
+      ++ask_pass;
     }
   };
-
-  // ----- the sines of a thread's tokens, and the query rows -------------------------------------
-#pragma unroll 1
-  for (int pass = 0; pass < kPasses; ++pass) {
-    const int r = pass * kRowsAtOnce + (tid >> 3);
-    if (r >= count) break;  // (no barrier below)
-    const int64_t t = t0 + r;
-    float c[8], s[8];
-    if (rotates) {
-      const uint64_t at = static_cast<uint64_t>(p.positions[t]);
+  if (heads > 0) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const uint64_t phase = at * fraction[8 * l + i];
-        // (24 bits of the angle's 32 are an exact fp32; the others turn the pair a little further:
-        // a code that lies next to a border feels them)
-        const int32_t whole = static_cast<int32_t>(phase >> 32);
-        const float x = static_cast<float>(whole & ~0xff), rest = static_cast<float>(whole & 0xff) * 0x1.921fb6p-30f;
-        float s0, c0;
-        sincospif(x * 0x1p-31f, &s0, &c0);
-        c[i] = fmaf(-s0, rest, c0) * p.amplitude;
-        s[i] = fmaf(c0, rest, s0) * p.amplitude;
+    for (int u = 0; u < kDeep; ++u) ask(u);
+  }
+  if (half > 0) {
+    if (tid < half) fraction[tid] = turn_fraction(p.inv_freq[tid]);
+    __syncthreads();
+  }
+  float c[8], s[8];
+  int pass = -1, head = heads;  // (the next row starts a pass)
+  const int total = heads > 0 ? passes * heads : passes;
+  for (int i = 0; i < total; i += kDeep) {
+#pragma unroll
+    for (int u = 0; u < kDeep; ++u) {
+      if (i + u >= total) break;
+      if (heads == 0 || head == heads) {
+        head = 0;
+        ++pass;
+        const int r = pass * kRowsAtOnce + (tid >> 3);
+        if (rotates && r < count) {
+          sines_of(static_cast<uint64_t>(p.positions[t0 + r]), fraction, l, p.amplitude, c, s);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            sines[(pass * 4 + k) * kThreads + tid] = make_float4(c[2 * k], s[2 * k], c[2 * k + 1], s[2 * k + 1]);
+        }
       }
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        sines[(pass * 4 + i) * kThreads + tid] = make_float4(c[2 * i], s[2 * i], c[2 * i + 1], s[2 * i + 1]);
-    }
-    const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) + t * p.q_stride);
-    uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.q_out) + t * p.q_out_stride);
-    for (int h0 = q_from; h0 < q_to; h0 += 4) {
-      uint4 wa[4], wb[4];
-#pragma unroll
-      for (int u = 0; u < 4; ++u)
-        if (h0 + u < q_to) {
-          wa[u] = src[(h0 + u) * 16 + pa];
-          wb[u] = src[(h0 + u) * 16 + pb];
+      if (heads == 0) continue;
+      const int r = pass * kRowsAtOnce + (tid >> 3);
+      if (r < count) {
+        uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.q_out) + (t0 + r) * p.q_out_stride) +
+                     (q_from + head) * 16;
+        if (rotates) {
+          float x[16];
+          unpack(wa[u], x);
+          unpack(wb[u], x + 8);
+          piece.turn(x, c, s);
+          wa[u] = pack(x);
+          wb[u] = pack(x + 8);
         }
-#pragma unroll
-      for (int u = 0; u < 4; ++u)
-        if (h0 + u < q_to) {
-          if (rotates) {
-            float x[16];
-            unpack(wa[u], x);
-            unpack(wb[u], x + 8);
-            turn(x, c, s);
-            wa[u] = pack(x);
-            wb[u] = pack(x + 8);
-          }
-          dst[(h0 + u) * 16 + pa] = wa[u];
-          dst[(h0 + u) * 16 + pb] = wb[u];
-        }
+        dst[pa] = wa[u];
+        dst[pb] = wb[u];
+      }
+      ++head;
+      ask(u);
     }
   }
-  if (!cached) return;
+  if (!blk.cached) return;
 
   // ----- keys and values: a (head, K or V) at a time, the next one's rows on their way ----------
   const int blocks = 1 << (p.page_shift - p.block_shift);
@@ -268,7 +339,7 @@ __global__ void __launch_bounds__(kThreads) rope_blocks_kernel(const RopeBlocksP
             c[2 * i + 1] = w.z;
             s[2 * i + 1] = w.w;
           }
-          turn(x[pass], c, s);
+          piece.turn(x[pass], c, s);
         }
 #pragma unroll
         for (int i = 0; i < 16; ++i) top = fmaxf(top, fabsf(x[pass][i]));
@@ -309,23 +380,155 @@ __global__ void __launch_bounds__(kThreads) rope_blocks_kernel(const RopeBlocksP
   }
 }
 
-}  // namespace
+// Few new rows a block (decoding, short drafts): a warp has the block and a share of its heads,
+// kRows rows (one or four) of 4 / kRows heads at once, 8 lanes a row, kPasses times.  A block's
+// largest value is a reduction over 8 kRows lanes.  Blocks with more rows than that take several
+// rounds, and read keys and values twice.
+template <int kRows, int kPasses, bool kInterleaved>
+__global__ void __launch_bounds__(kFewThreads) rope_few_kernel(const RopeBlocksParams p, int slots, int parts) {
+  constexpr int kUnits = 4 / kRows, kLanes = 8 * kRows;
+  __shared__ uint64_t fraction[64];
+  const int tid = threadIdx.x, lane = tid & 31, l = lane & 7;
+  const int row = (lane >> 3) % kRows, unit = (lane >> 3) / kRows;
+  const int half = p.rotary_dim / 2;
+  grid_dependency_wait();
+  if (tid < half) fraction[tid] = turn_fraction(p.inv_freq[tid]);
+  __syncthreads();
+  const int64_t task = static_cast<int64_t>(blockIdx.x) * (kFewThreads / 32) + (tid >> 5);
+  const int slot = static_cast<int>(task / parts), part = static_cast<int>(task - static_cast<int64_t>(slot) * parts);
+  if (slot >= slots) return;
+  Block blk;
+  if (!blk.find(p, slot, lane, lane == 0 && part == 0)) return;
+  const int q_from = static_cast<int>(static_cast<int64_t>(p.num_q_heads) * part / parts);
+  const int q_to = static_cast<int>(static_cast<int64_t>(p.num_q_heads) * (part + 1) / parts);
+  const int kv_from = static_cast<int>(static_cast<int64_t>(p.num_kv_heads) * part / parts);
+  const int kv_to = static_cast<int>(static_cast<int64_t>(p.num_kv_heads) * (part + 1) / parts);
+  const Pieces<kInterleaved> piece(l, p.rotary_dim / 16);
+  const int rounds = (blk.count + kRows * kPasses - 1) / (kRows * kPasses);
+  float c[kPasses][8], s[kPasses][8];
+  auto sines = [&](int round) {
+#pragma unroll
+    for (int pass = 0; pass < kPasses; ++pass) {
+      const int r = (round * kPasses + pass) * kRows + row;
+      if (piece.rotates && r < blk.count)
+        sines_of(static_cast<uint64_t>(p.positions[blk.t0 + r]), fraction, l, p.amplitude, c[pass], s[pass]);
+    }
+  };
+  for (int round = 0; round < rounds; ++round) {
+    sines(round);
+#pragma unroll
+    for (int pass = 0; pass < kPasses; ++pass) {
+      const int r = (round * kPasses + pass) * kRows + row;
+      if (r >= blk.count) continue;
+      const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) + (blk.t0 + r) * p.q_stride);
+      uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.q_out) + (blk.t0 + r) * p.q_out_stride);
+      for (int h = q_from + unit; h < q_to; h += kUnits) {
+        uint4 wa = src[h * 16 + piece.a], wb = src[h * 16 + piece.b];
+        if (piece.rotates) {
+          float x[16];
+          unpack(wa, x);
+          unpack(wb, x + 8);
+          piece.turn(x, c[pass], s[pass]);
+          wa = pack(x);
+          wb = pack(x + 8);
+        }
+        dst[h * 16 + piece.a] = wa;
+        dst[h * 16 + piece.b] = wb;
+      }
+    }
+  }
+  if (!blk.cached) return;
+  const int blocks = 1 << (p.page_shift - p.block_shift);
+  const int units = 2 * (kv_to - kv_from);  // (head, K or V)
+  for (int u0 = 0; u0 < units; u0 += kUnits) {
+    const int u = u0 + unit;
+    const bool live = u < units, is_v = u & 1;
+    const int h = kv_from + (u >> 1);
+    const int64_t head = blk.page * p.num_kv_heads + h;
+    float* scale_at = (is_v ? p.v_scale : p.k_scale) + head * blocks + (blk.in_page >> p.block_shift);
+    unsigned char* codes =
+        static_cast<unsigned char*>(is_v ? p.v_cache : p.k_cache) + ((head << p.page_shift) + blk.in_page) * 128;
+    const float old = live && blk.held > 0 ? *scale_at : 0.f;
+    float x[kPasses][16];
+    auto values = [&](int round) {  // the unit's rows of a round, turned
+      if (rounds > 1) sines(round);
+#pragma unroll
+      for (int pass = 0; pass < kPasses; ++pass) {
+        const int r = (round * kPasses + pass) * kRows + row;
+        uint4 wa = make_uint4(0u, 0u, 0u, 0u), wb = wa;
+        if (live && r < blk.count) {
+          const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(is_v ? p.v : p.k) +
+                                                            (blk.t0 + r) * (is_v ? p.v_stride : p.k_stride) + h * 128);
+          wa = src[piece.a];
+          wb = src[piece.b];
+        }
+        unpack(wa, x[pass]);
+        unpack(wb, x[pass] + 8);
+        if (piece.rotates && !is_v && r < blk.count) piece.turn(x[pass], c[pass], s[pass]);
+      }
+    };
+    float top = 0.f;
+    for (int round = 0; round < rounds; ++round) {
+      values(round);
+#pragma unroll
+      for (int pass = 0; pass < kPasses; ++pass)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) top = fmaxf(top, fabsf(x[pass][i]));
+    }
+#pragma unroll
+    for (int d = kLanes / 2; d >= 1; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+    const float need = needed_scale(top);
+    const float scale = blk.held > 0 ? fmaxf(old, need) : need;
+    // blocks whose scale grows: the rows they held, by the whole warp
+    const bool grows = live && blk.held > 0 && scale != old;
+    uint32_t todo = __ballot_sync(0xffffffffu, grows && lane % kLanes == 0);
+    while (todo != 0) {
+      const int from = __ffs(todo) - 1;
+      todo &= todo - 1;
+      const float ratio = __shfl_sync(0xffffffffu, old / scale, from);
+      uint4* rows = reinterpret_cast<uint4*>(
+          __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(codes), from) -
+          static_cast<unsigned long long>(blk.held) * 128);
+      for (int i0 = lane; i0 < blk.held * 8; i0 += 4 * 32) {
+        uint4 w[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (i0 + 32 * k < blk.held * 8) w[k] = rows[i0 + 32 * k];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (i0 + 32 * k < blk.held * 8)
+            rows[i0 + 32 * k] = make_uint4(rescale(w[k].x, ratio), rescale(w[k].y, ratio), rescale(w[k].z, ratio),
+                                           rescale(w[k].w, ratio));
+      }
+    }
+    const float inv = scale > 0.f ? 1.f / scale : 0.f;
+    for (int round = 0; round < rounds; ++round) {
+      if (rounds > 1) values(round);
+#pragma unroll
+      for (int pass = 0; pass < kPasses; ++pass) {
+        const int r = (round * kPasses + pass) * kRows + row;
+        if (live && r < blk.count) {
+          uint2* dst = reinterpret_cast<uint2*>(codes + r * 128);
+          dst[piece.a] = codes8(x[pass], inv);
+          dst[piece.b] = codes8(x[pass] + 8, inv);
+        }
+      }
+    }
+    __syncwarp();  // (every lane has the old scale)
+    if (live && lane % kLanes == 0 && !(blk.held > 0 && scale == old)) *scale_at = scale;
+  }
+}
 
-cudaError_t launch_rope_blocks(const RopeBlocksParams& p, bool interleaved, cudaStream_t stream, bool use_pdl) {
-  const int block = 1 << p.block_shift;
-  const int64_t slots = (static_cast<int64_t>(p.total_q) >> p.block_shift) + 2 * static_cast<int64_t>(p.bs);
+template <int kThreads, int kPasses>
+cudaError_t launch_many(const RopeBlocksParams& p, bool interleaved, int64_t slots, cudaStream_t stream, bool use_pdl) {
   // Few blocks of tokens: the heads over several thread blocks, down to one kv head each.
   const int most = p.num_kv_heads > p.num_q_heads / 4 ? p.num_kv_heads : p.num_q_heads / 4;
   int parts = 1;
   while (parts < most && slots * parts < 152 * 8) parts *= 2;
   if (parts > most) parts = most < 1 ? 1 : most;
-#define PA_BLOCKS_CASE(PASSES) \
-  (interleaved ? rope_blocks_kernel<PASSES, true> : rope_blocks_kernel<PASSES, false>)
-  void (*kernel)(const RopeBlocksParams) = block <= 32   ? PA_BLOCKS_CASE(1)
-                                           : block == 64 ? PA_BLOCKS_CASE(2)
-                                                         : PA_BLOCKS_CASE(4);
-#undef PA_BLOCKS_CASE
-  const size_t smem = p.rotary_dim > 0 ? static_cast<size_t>(block <= 32 ? 1 : block / 32) * 4 * kThreads * 16 : 0;
+  void (*kernel)(const RopeBlocksParams) =
+      interleaved ? rope_blocks_kernel<kThreads, kPasses, true> : rope_blocks_kernel<kThreads, kPasses, false>;
+  const size_t smem = p.rotary_dim > 0 ? static_cast<size_t>(kPasses) * 4 * kThreads * 16 : 0;
   if (smem > 48 * 1024) {
     const cudaError_t e =
         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
@@ -334,6 +537,37 @@ cudaError_t launch_rope_blocks(const RopeBlocksParams& p, bool interleaved, cuda
   return fail_at(launch_kernel(kernel, dim3(static_cast<unsigned>(slots), static_cast<unsigned>(parts)),
                                dim3(kThreads), smem, stream, use_pdl, p),
                  "cudaLaunchKernelEx");
+}
+
+template <int kRows, int kPasses>
+cudaError_t launch_few(const RopeBlocksParams& p, bool interleaved, int64_t slots, cudaStream_t stream, bool use_pdl) {
+  // a warp down to four q rows and a kv head, while there are not two warps a scheduler
+  const int most = p.num_kv_heads > p.num_q_heads / 4 ? p.num_kv_heads : p.num_q_heads / 4;
+  int parts = 1;
+  while (parts < most && slots * parts < 152 * 16) parts *= 2;
+  if (parts > most) parts = most < 1 ? 1 : most;
+  void (*kernel)(const RopeBlocksParams, int, int) =
+      interleaved ? rope_few_kernel<kRows, kPasses, true> : rope_few_kernel<kRows, kPasses, false>;
+  const int64_t blocks = (slots * parts + kFewThreads / 32 - 1) / (kFewThreads / 32);
+  return fail_at(launch_kernel(kernel, dim3(static_cast<unsigned>(blocks)), dim3(kFewThreads), 0, stream, use_pdl, p,
+                               static_cast<int>(slots), parts),
+                 "cudaLaunchKernelEx (few)");
+}
+
+}  // namespace
+
+cudaError_t launch_rope_blocks(const RopeBlocksParams& p, bool interleaved, cudaStream_t stream, bool use_pdl) {
+  const int block = 1 << p.block_shift;
+  const int64_t slots = (static_cast<int64_t>(p.total_q) >> p.block_shift) + 2 * static_cast<int64_t>(p.bs);
+  // Up to 8 new rows a request on average: a warp for each block.
+  const int64_t few = p.bs;
+  if (p.total_q <= few) return launch_few<1, 1>(p, interleaved, slots, stream, use_pdl);
+  if (p.total_q <= 4 * few) return launch_few<4, 1>(p, interleaved, slots, stream, use_pdl);
+  if (p.total_q <= 8 * few) return launch_few<4, 2>(p, interleaved, slots, stream, use_pdl);
+  return block == 16   ? launch_many<128, 1>(p, interleaved, slots, stream, use_pdl)
+         : block == 32 ? launch_many<256, 1>(p, interleaved, slots, stream, use_pdl)
+         : block == 64 ? launch_many<256, 2>(p, interleaved, slots, stream, use_pdl)
+                       : launch_many<256, 4>(p, interleaved, slots, stream, use_pdl);
 }
 
 }  // namespace pa

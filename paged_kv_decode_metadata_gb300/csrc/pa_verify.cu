@@ -12,34 +12,38 @@
 // 21-bit integers by two additions that round down.
 //
 // Shape.  A cluster of eight thread blocks has a request.  The children's p(x) and q(x) are
-// gathered at once, so the walk down the tree is arithmetic in shared memory, done by one thread
-// of each block alike.  Only a residual's sum needs a whole row (and the draft's): every block
-// sums an eighth, a warp a contiguous piece of it; the block sums are exchanged through
-// distributed shared memory, the piece that holds the drawn number is read once more.
-// A chain needs one such row, the last node's.
+// gathered at once, so the walk down the tree is arithmetic, done by one warp of each block alike,
+// which finds a node's next child by ballots.  Only a residual's sum needs a whole row (and the
+// draft's): every block sums an eighth, a warp a contiguous piece of it, 512 tokens at a time; the
+// block sums are exchanged through distributed shared memory, and the 512 tokens that hold the
+// drawn number are read once more.  A chain needs one such row, the last node's.
 #include "pa_common.cuh"
 #include "pa_internal.h"
 
 namespace pa {
 namespace {
 
-constexpr int kThreads = 512, kWarps = kThreads / 32;
+// (256 threads: blocks of 512 and 1024 start more slowly than they save in rounds of loads, 32 chains
+// at a vocabulary of 128000 11.7 and 12.6 us against 11.1; clusters of four as much)
+constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kCluster = 8;
 constexpr int kMaxNodes = 256;
 constexpr float kUnits = 0x1p42f;  // a weight of 1
+constexpr int kDeep = 4;           // loads of a row on their way: a batch of 4 x 128 tokens a warp
+constexpr int kBatches = (1 << 20) / (kCluster * kWarps * kDeep * 128);  // of a warp's piece, at most
 
 struct Shared {
   float p[kMaxNodes], q[kMaxNodes], u[kMaxNodes];
   long long token[kMaxNodes];
   int parent[kMaxNodes];
   int path[kMaxNodes];
-  long long gone[kMaxNodes];  // without draft probabilities: tokens taken out of the row
-  unsigned long long warp_sum[kWarps], block_sum[2][kCluster];
-  // the walk
-  int next, node, length, num_gone;
-  float c, sum;        // w = max(p - c q, 0); its sum, the first row's being 1
-  double left;         // without draft probabilities: the row's sum less what is gone
-  int todo;            // 0: sum w for the next sibling, 1: draw the token
+  long long gone[kMaxNodes];  // without draft probabilities: tokens taken out of the row,
+  float gone_p[kMaxNodes];    // and their probabilities
+  unsigned long long batch_sum[kWarps][kBatches], warp_sum[kWarps], block_sum[2][kCluster];
+  // what the walk has come to
+  int node, length, num_gone;
+  float c;   // w = max(p - c q, 0)
+  int todo;  // 0: sum w for the next sibling, 1: draw the token
 };
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -139,16 +143,6 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
     sh.q[tid] = q;
     sh.u[tid] = tid > 0 ? prm.uniforms[q_begin + tid] : 0.f;
   }
-  if (tid == 0) {
-    sh.next = 1;
-    sh.node = 0;
-    sh.length = 1;
-    sh.path[0] = 0;
-    sh.c = 0.f;
-    sh.sum = 1.f;
-    sh.left = 1.0;
-    sh.num_gone = 0;
-  }
   __syncthreads();
 
   // a warp's piece of the row, and the eighth's
@@ -163,35 +157,46 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
 #pragma unroll
     for (int j = 0; j < 4; ++j) to_units(q_row != nullptr ? fmaf(-c, q[j], p[j]) : p[j], hi[j], lo[j]);
   };
-  // the sum of w over the row; warp and block sums stay in shared memory
+  // a batch's loads, all on their way at once
+  auto load_batch = [&](int x0, float (&p)[kDeep][4], float (&q)[kDeep][4]) {
+#pragma unroll
+    for (int d = 0; d < kDeep; ++d) {
+      const int x = x0 + d * 128 + lane * 4;
+      load4<kVec>(p_row, x, to, p[d]);
+      if (q_row != nullptr) load4<kVec>(q_row, x, to, q[d]);
+    }
+  };
+  auto warp_total = [](unsigned long long v) {
+#pragma unroll
+    for (int d = 16; d >= 1; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+    return v;
+  };
+  // the sum of w over the row; batch, warp and block sums stay in shared memory
   auto row_sum = [&](int buffer) -> unsigned long long {
     unsigned long long total = 0;
-    constexpr int kDeep = 4;
-    for (int x0 = from; x0 < to; x0 += kDeep * 128) {
+    const int num_gone = sh.num_gone;
+    for (int x0 = from, batch = 0; x0 < to; x0 += kDeep * 128, ++batch) {
       float p[kDeep][4], q[kDeep][4];
-#pragma unroll
-      for (int d = 0; d < kDeep; ++d) {
-        const int x = x0 + d * 128 + lane * 4;
-        load4<kVec>(p_row, x, to, p[d]);
-        if (q_row != nullptr) load4<kVec>(q_row, x, to, q[d]);
-      }
+      load_batch(x0, p, q);  // (the next one's ahead of this one's sums: no faster)
+      unsigned long long sum = 0;
 #pragma unroll
       for (int d = 0; d < kDeep; ++d) {
         uint32_t hi[4], lo[4];
         weights(p[d], q[d], hi, lo);
-        total += (static_cast<unsigned long long>(hi[0] + hi[1] + hi[2] + hi[3]) << 21) +
-                 (lo[0] + lo[1] + lo[2] + lo[3]);
+        sum += (static_cast<unsigned long long>(hi[0] + hi[1] + hi[2] + hi[3]) << 21) +
+               (lo[0] + lo[1] + lo[2] + lo[3]);
       }
-    }
-#pragma unroll
-    for (int d = 16; d >= 1; d >>= 1) total += __shfl_xor_sync(0xffffffffu, total, d);
-    for (int i = 0; i < sh.num_gone; ++i) {
-      const long long x = sh.gone[i];
-      if (x >= from && x < to) {
-        uint32_t hi, lo;
-        to_units(p_row[x], hi, lo);
-        total -= (static_cast<unsigned long long>(hi) << 21) + lo;
+      for (int i = lane; i < num_gone; i += 32) {
+        const long long x = sh.gone[i];
+        if (x >= x0 && x < min(x0 + kDeep * 128, to)) {
+          uint32_t hi, lo;
+          to_units(sh.gone_p[i], hi, lo);
+          sum -= (static_cast<unsigned long long>(hi) << 21) + lo;  // (of the whole warp's sum)
+        }
       }
+      sum = warp_total(sum);
+      if (lane == 0) sh.batch_sum[warp][batch] = sum;
+      total += sum;
     }
     if (lane == 0) sh.warp_sum[warp] = total;
     __syncthreads();
@@ -209,46 +214,74 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
   // ----- the walk: up to a residual that has to be summed, or to the end -----------------------
   int buffer = 0;
   unsigned long long all = 0;
+  // (warp 0's, every lane alike)
+  int next = 1, node = 0, length = 1, num_gone = 0;
+  float walk_c = 0.f, sum = 1.f;  // w = max(p - c q, 0) and its sum, -1 where it is not known
+  double left = 1.0;              // without draft probabilities: the row's sum less what is gone
+  if (tid == 0) sh.path[0] = 0;
   while (true) {
-    if (tid == 0) {
+    if (warp == 0) {
       const bool drafted = prm.draft_probs != nullptr;
-      sh.todo = 1;
-      int i = sh.next, node = sh.node;
-      for (; i < q_len; ++i) {
-        if (sh.parent[i] != node) continue;
-        bool ok;
-        if (drafted) {
-          if (sh.c > 0.f && sh.sum < 0.f) {  // not known yet
-            sh.todo = 0;
-            break;
+      int todo = 1;
+      for (int base = next & ~31; base < q_len && todo == 1; base += 32) {
+        const int mine = base + lane;
+        const int up = mine < q_len ? sh.parent[mine] : -1;
+        const float my_p = mine < q_len ? sh.p[mine] : 0.f, my_q = mine < q_len ? sh.q[mine] : 0.f;
+        const float my_u = mine < q_len ? sh.u[mine] : 0.f;
+        const long long my_x = mine < q_len ? sh.token[mine] : -1;
+        while (true) {  // the node's next child among these 32
+          const uint32_t children = __ballot_sync(0xffffffffu, up == node && mine >= next);
+          if (children == 0) break;
+          const int at = __ffs(children) - 1;
+          const float p = __shfl_sync(0xffffffffu, my_p, at), u = __shfl_sync(0xffffffffu, my_u, at);
+          bool ok;
+          if (drafted) {
+            if (sum < 0.f) {  // (siblings before it were rejected)
+              todo = 0;
+              break;
+            }
+            const float q = __shfl_sync(0xffffffffu, my_q, at);
+            const float w = walk_c > 0.f ? fmaxf(fmaf(-walk_c, q, p), 0.f) : p;
+            ok = static_cast<double>(u) * static_cast<double>(q) * static_cast<double>(sum) < static_cast<double>(w);
+            if (!ok) {
+              walk_c += sum;
+              sum = -1.f;
+            }
+          } else {
+            const long long x = __shfl_sync(0xffffffffu, my_x, at);
+            bool taken = false;
+            for (int g = lane; g < num_gone; g += 32) taken = taken || sh.gone[g] == x;
+            const float w = __any_sync(0xffffffffu, taken) ? 0.f : p;
+            ok = static_cast<double>(u) * left < static_cast<double>(w);
+            if (!ok && w > 0.f) {
+              if (lane == 0) {
+                sh.gone[num_gone] = x;
+                sh.gone_p[num_gone] = p;
+              }
+              __syncwarp();
+              ++num_gone;
+              left -= static_cast<double>(w);
+            }
           }
-          const float w = sh.c > 0.f ? fmaxf(fmaf(-sh.c, sh.q[i], sh.p[i]), 0.f) : sh.p[i];
-          ok = static_cast<double>(sh.u[i]) * static_cast<double>(sh.q[i]) * static_cast<double>(sh.sum) <
-               static_cast<double>(w);
-          if (!ok) {
-            sh.c += sh.sum;
-            sh.sum = -1.f;
+          next = base + at + 1;
+          if (ok) {
+            node = base + at;
+            if (lane == 0) sh.path[length] = node;
+            ++length;
+            walk_c = 0.f;
+            sum = 1.f;
+            left = 1.0;
+            num_gone = 0;
           }
-        } else {
-          float w = sh.p[i];
-          for (int g = 0; g < sh.num_gone; ++g) w = sh.gone[g] == sh.token[i] ? 0.f : w;
-          ok = static_cast<double>(sh.u[i]) * sh.left < static_cast<double>(w);
-          if (!ok && w > 0.f) {
-            sh.gone[sh.num_gone++] = sh.token[i];
-            sh.left -= static_cast<double>(w);
-          }
-        }
-        if (ok) {
-          node = i;
-          sh.path[sh.length++] = i;
-          sh.c = 0.f;
-          sh.sum = 1.f;
-          sh.left = 1.0;
-          sh.num_gone = 0;
         }
       }
-      sh.next = i;
-      sh.node = node;
+      if (lane == 0) {
+        sh.node = node;
+        sh.length = length;
+        sh.num_gone = num_gone;
+        sh.c = walk_c;
+        sh.todo = todo;
+      }
     }
     __syncthreads();
     const int todo = sh.todo;
@@ -258,7 +291,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
     all = row_sum(buffer);
     if (todo == 1) break;
     buffer ^= 1;
-    if (tid == 0) sh.sum = static_cast<float>(all) * (1.f / kUnits);
+    sum = static_cast<float>(all) * (1.f / kUnits);
     __syncthreads();
   }
   if (all == 0 && (c > 0.f || sh.num_gone > 0)) {
@@ -300,31 +333,47 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
     t -= sh.warp_sum[w];
   }
   if (t >= sh.warp_sum[warp]) return;
-  for (int x0 = from; x0 < to; x0 += 128) {
-    const int x = x0 + lane * 4;
-    float p[4], q[4];
+  int x0 = from, batch = 0;
+  while (t >= sh.batch_sum[warp][batch]) {
+    t -= sh.batch_sum[warp][batch++];
+    x0 += kDeep * 128;
+  }
+  float p[kDeep][4], q[kDeep][4];
+  load_batch(x0, p, q);
+  for (int i = 0; i < sh.num_gone; ++i) {
+    const long long at = sh.gone[i] - x0;
+    if (at < 0 || at >= kDeep * 128) continue;  // (the whole warp)
+#pragma unroll
+    for (int d = 0; d < kDeep; ++d)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) p[d][j] = at == d * 128 + lane * 4 + j ? 0.f : p[d][j];
+  }
+#pragma unroll
+  for (int d = 0; d < kDeep; ++d) {
+    const int x = x0 + d * 128 + lane * 4;
     uint32_t hi[4], lo[4];
-    load4<kVec>(p_row, x, to, p);
-    if (q_row != nullptr) load4<kVec>(q_row, x, to, q);
-    weights(p, q, hi, lo);
+    weights(p[d], q[d], hi, lo);
     unsigned long long v[4];
-    for (int j = 0; j < 4; ++j) {
-      v[j] = (static_cast<unsigned long long>(hi[j]) << 21) + lo[j];
-      for (int i = 0; i < sh.num_gone; ++i) v[j] = sh.gone[i] == x + j ? 0ull : v[j];
-    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = (static_cast<unsigned long long>(hi[j]) << 21) + lo[j];
     const unsigned long long mine = v[0] + v[1] + v[2] + v[3];
     unsigned long long upto = mine;
 #pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const unsigned long long before = __shfl_up_sync(0xffffffffu, upto, d);
-      if (lane >= d) upto += before;
+    for (int k = 1; k < 32; k <<= 1) {
+      const unsigned long long before = __shfl_up_sync(0xffffffffu, upto, k);
+      if (lane >= k) upto += before;
     }
     const uint32_t past = __ballot_sync(0xffffffffu, t < upto);
     if (past != 0) {
       if (lane == __ffs(past) - 1) {
         t -= upto - mine;
         int j = 0;
-        while (j < 3 && t >= v[j]) t -= v[j++];
+#pragma unroll
+        for (int k = 0; k < 3; ++k)
+          if (j == k && t >= v[k]) {
+            t -= v[k];
+            ++j;
+          }
         prm.next_tokens[b] = x + j;
       }
       return;

@@ -139,6 +139,11 @@ APPEND_CASES = [  # seqlens, q_lens, hq, hkv, page, block, rot, interleaved, amp
     ([260, 500], [131, 129], 5, 5, 128, 128, 96, True, 1.0),
     ([1000], [999], 16, 2, 128, 16, 128, False, 1.0),
     ([50, 70], [20, 9], 0, 4, 32, 32, 0, False, 1.0),
+    # few rows a request on average, up to 1, 4 and 8, some requests with more
+    ([30, 100, 64, 17, 128, 5, 61, 33], [1, 0, 0, 3, 0, 0, 2, 1], 8, 4, 32, 32, 128, False, 1.0),
+    ([70, 9, 300, 65, 2, 128], [5, 3, 4, 1, 2, 6], 40, 8, 64, 64, 64, True, 1.0),
+    ([70, 9, 300, 65, 8, 128], [8, 8, 7, 6, 8, 11], 6, 2, 128, 16, 96, False, 1.1),
+    ([500] * 3, [1, 1, 1], 5, 5, 128, 128, 128, True, 1.0),
 ]
 
 
