@@ -18,35 +18,44 @@
 namespace pa {
 namespace {
 
-constexpr int kPlanThreads = 1024;
 constexpr int kThreads = 256;
 constexpr int kTaskBytes = kThreads * 16 * 4;
 
-// Inclusive scan over the block of one number a thread; `total` is the sum.
-__device__ __forceinline__ int block_scan(int v, int* warp_sums, int& total) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+// Inclusive scans over the block of one number a thread.  (Two sets of warp sums in turn: one
+// barrier a scan.)
+template <int kThreads>
+struct Scan {
+  int sums[2][32];
+  __device__ __forceinline__ int operator()(int v, int& turn, int& total) {
+    constexpr int kWarps = kThreads / 32;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const int up = __shfl_up_sync(0xffffffffu, v, d);
-    if (lane >= d) v += up;
+    for (int d = 1; d < 32; d <<= 1) {
+      const int up = __shfl_up_sync(0xffffffffu, v, d);
+      if (lane >= d) v += up;
+    }
+    int* mine = sums[turn];
+    turn ^= 1;
+    if (lane == 31) mine[warp] = v;
+    __syncthreads();
+    int w = lane < kWarps ? mine[lane] : 0;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int up = __shfl_up_sync(0xffffffffu, w, d);
+      if (lane >= d) w += up;
+    }
+    total = __shfl_sync(0xffffffffu, w, 31);
+    const int before = __shfl_sync(0xffffffffu, w, max(warp - 1, 0));
+    return v + (warp > 0 ? before : 0);
   }
-  if (lane == 31) warp_sums[warp] = v;
-  __syncthreads();
-  int before = 0;
-  total = 0;
-  for (int w = 0; w < kPlanThreads / 32; ++w) {
-    const int s = warp_sums[w];
-    before += w < warp ? s : 0;
-    total += s;
-  }
-  __syncthreads();
-  return v + before;
-}
+};
 
 // The lowest `want` free pages, in order, to `list`; returns how many there are (all threads).
-__device__ int find_free(const int32_t* refs, int64_t num_pages, int want, int32_t* list, int* warp_sums) {
+template <int kThreads>
+__device__ int find_free(const int32_t* refs, int64_t num_pages, int want, int32_t* list, Scan<kThreads>& scan,
+                         int& turn) {
   int found = 0;
-  for (int64_t base = 0; base < num_pages && found < want; base += kPlanThreads * 4) {
+  for (int64_t base = 0; base < num_pages && found < want; base += kThreads * 4) {
     const int64_t at = base + threadIdx.x * 4;
     int r[4], free = 0;
 #pragma unroll
@@ -55,7 +64,7 @@ __device__ int find_free(const int32_t* refs, int64_t num_pages, int want, int32
       free += r[j] == 0;
     }
     int total;
-    int rank = found + block_scan(free, warp_sums, total) - free;
+    int rank = found + scan(free, turn, total) - free;
 #pragma unroll
     for (int j = 0; j < 4; ++j)
       if (r[j] == 0) {
@@ -83,15 +92,22 @@ __device__ __forceinline__ int checked_length(const PagesParams& p, const int32_
   return -1;
 }
 
+// Threads of a plan: 256 start sooner, 1024 read more pages and entries at a time.
+#define PA_PLAN(kernel, p) ((p).num_pages <= 4096 && (p).count <= 1024 ? kernel<256> : kernel<1024>)
+#define PA_PLAN_THREADS(p) dim3((p).num_pages <= 4096 && (p).count <= 1024 ? 256 : 1024)
+
 // ---- plans --------------------------------------------------------------------------------------
 
 // Forks: a free page for every child whose last page is partly filled.
-__global__ void __launch_bounds__(kPlanThreads) plan_fork_kernel(const PagesParams p) {
-  __shared__ int warp_sums[kPlanThreads / 32];
+template <int kPlan>
+__global__ void __launch_bounds__(kPlan) plan_fork_kernel(const PagesParams p) {
+  __shared__ Scan<kPlan> scan;
+  int turn = 0;
+  trigger_dependents();  // (what applies the plan waits for its end)
   grid_dependency_wait();
   const int tid = threadIdx.x;
   int want = 0;
-  for (int base = 0; base < p.count; base += kPlanThreads) {
+  for (int base = 0; base < p.count; base += kPlan) {
     const int i = base + tid;
     int needs = 0;
     if (i < p.count) {
@@ -111,14 +127,14 @@ __global__ void __launch_bounds__(kPlanThreads) plan_fork_kernel(const PagesPara
       p.granted[i] = parent >= 0 && child >= 0 && n >= 0 ? n : 0;
     }
     int total;
-    const int rank = want + block_scan(needs, warp_sums, total) - needs;
+    const int rank = want + scan(needs, turn, total) - needs;
     if (i < p.count) p.dst_pages[i] = needs ? rank : -1;
     want += total;
   }
   __syncthreads();
-  const int found = find_free(p.page_refs, p.num_pages, want, p.list, warp_sums);
+  const int found = find_free(p.page_refs, p.num_pages, want, p.list, scan, turn);
   __syncthreads();
-  for (int i = tid; i < p.count; i += kPlanThreads) {
+  for (int i = tid; i < p.count; i += kPlan) {
     const int rank = p.dst_pages[i];
     if (rank < 0) {
       // a last page that could not be read: the child has what is before it
@@ -137,12 +153,15 @@ __global__ void __launch_bounds__(kPlanThreads) plan_fork_kernel(const PagesPara
 }
 
 // Growth: free pages for the pages of every request between its old and its new length.
-__global__ void __launch_bounds__(kPlanThreads) plan_extend_kernel(const PagesParams p) {
-  __shared__ int warp_sums[kPlanThreads / 32];
+template <int kPlan>
+__global__ void __launch_bounds__(kPlan) plan_extend_kernel(const PagesParams p) {
+  __shared__ Scan<kPlan> scan;
+  int turn = 0;
+  trigger_dependents();  // (what applies the plan waits for its end)
   grid_dependency_wait();
   const int tid = threadIdx.x;
   int want = 0;
-  for (int base = 0; base < p.count; base += kPlanThreads) {
+  for (int base = 0; base < p.count; base += kPlan) {
     const int i = base + tid;
     int needs = 0;
     if (i < p.count) {
@@ -154,15 +173,15 @@ __global__ void __launch_bounds__(kPlanThreads) plan_extend_kernel(const PagesPa
     // (more than there are pages is more than enough: the sums stay within 31 bits)
     needs = static_cast<int>(min(static_cast<int64_t>(needs), p.num_pages));
     int total;
-    const int rank = want + block_scan(needs, warp_sums, total) - needs;
+    const int rank = want + scan(needs, turn, total) - needs;
     if (i < p.count) p.src_pages[i] = rank;
     want = static_cast<int>(min(static_cast<int64_t>(want) + total, p.num_pages));
   }
   __syncthreads();
-  const int found = find_free(p.page_refs, p.num_pages, want, p.list, warp_sums);
+  const int found = find_free(p.page_refs, p.num_pages, want, p.list, scan, turn);
   __syncthreads();
-  for (int r = tid; r < found; r += kPlanThreads) p.page_refs[p.list[r]] = 1;
-  for (int i = tid; i < p.count; i += kPlanThreads) {
+  for (int r = tid; r < found; r += kPlan) p.page_refs[p.list[r]] = 1;
+  for (int i = tid; i < p.count; i += kPlan) {
     const int64_t row = checked_row(p, p.rows, i, false);
     const int old_n = checked_length(p, p.lens, i, false), new_n = checked_length(p, p.new_lens, i, false);
     if (row < 0 || old_n < 0 || new_n < 0) {
@@ -179,24 +198,27 @@ __global__ void __launch_bounds__(kPlanThreads) plan_extend_kernel(const PagesPa
 }
 
 // Compaction: live pages at or past the number of live pages move to the free ones before it.
-__global__ void __launch_bounds__(kPlanThreads) plan_compact_kernel(const PagesParams p) {
-  __shared__ int warp_sums[kPlanThreads / 32];
+template <int kPlan>
+__global__ void __launch_bounds__(kPlan) plan_compact_kernel(const PagesParams p) {
+  __shared__ Scan<kPlan> scan;
+  int turn = 0;
+  trigger_dependents();  // (what applies the plan waits for its end)
   grid_dependency_wait();
   const int tid = threadIdx.x;
   int live = 0;
-  for (int64_t i = tid; i < p.num_pages; i += kPlanThreads) live += p.page_refs[i] > 0;
+  for (int64_t i = tid; i < p.num_pages; i += kPlan) live += p.page_refs[i] > 0;
   int total;
-  block_scan(live, warp_sums, total);
+  scan(live, turn, total);
   const int count = total;
   int moves = 0, holes = 0;
-  for (int64_t base = 0; base < p.num_pages; base += kPlanThreads) {
+  for (int64_t base = 0; base < p.num_pages; base += kPlan) {
     const int64_t i = base + tid;
     const bool used = i < p.num_pages && p.page_refs[i] > 0;
     const int moved = used && i >= count, hole = i < p.num_pages && !used && i < count;
     if (i < p.num_pages) p.page_map[i] = used ? static_cast<int32_t>(i) : -1;
     // (below `count` there are holes, from there on moves: one scan ranks both)
-    const int rank = block_scan(moved + hole, warp_sums, total) - (moved + hole);
-    const int mine_holes = base + kPlanThreads <= count ? total : -1;
+    const int rank = scan(moved + hole, turn, total) - (moved + hole);
+    const int mine_holes = base + kPlan <= count ? total : -1;
     if (mine_holes >= 0) {
       if (hole) p.dst_pages[holes + rank] = static_cast<int32_t>(i);
       holes += total;
@@ -205,7 +227,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_compact_kernel(const PagesP
       moves += total;
     } else {  // the stretch that holds the border
       int of_holes;
-      const int at = block_scan(hole, warp_sums, of_holes) - hole;
+      const int at = scan(hole, turn, of_holes) - hole;
       if (hole) p.dst_pages[holes + at] = static_cast<int32_t>(i);
       if (moved) p.src_pages[moves + rank - of_holes] = static_cast<int32_t>(i);
       holes += of_holes;
@@ -213,7 +235,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_compact_kernel(const PagesP
     }
   }
   __syncthreads();
-  for (int r = tid; r < moves; r += kPlanThreads) {  // (as many holes as moves)
+  for (int r = tid; r < moves; r += kPlan) {  // (as many holes as moves)
     const int src = p.src_pages[r], dst = p.dst_pages[r];
     p.page_map[src] = dst;
     p.page_refs[dst] = p.page_refs[src];
@@ -443,7 +465,7 @@ cudaError_t launch_pages_copy(const PagesParams& p, const pa_page_pool* src, con
 
 cudaError_t launch_pages_fork(const PagesParams& p, const pa_page_pool* pools, int32_t num,
                               cudaStream_t stream, bool use_pdl) {
-  cudaError_t e = launch_kernel(plan_fork_kernel, dim3(1), dim3(kPlanThreads), 0, stream, use_pdl, p);
+  cudaError_t e = launch_kernel(PA_PLAN(plan_fork_kernel, p), dim3(1), PA_PLAN_THREADS(p), 0, stream, use_pdl, p);
   if (e != cudaSuccess) return fail_at(e, "cudaLaunchKernelEx (plan)");
   const PagesPools first = pack(pools, pools, 0, num);
   const int64_t tables = static_cast<int64_t>(p.count) * ((p.max_seq_pages + kTablePages - 1) / kTablePages);
@@ -454,7 +476,7 @@ cudaError_t launch_pages_fork(const PagesParams& p, const pa_page_pool* pools, i
 }
 
 cudaError_t launch_pages_extend(const PagesParams& p, cudaStream_t stream, bool use_pdl) {
-  cudaError_t e = launch_kernel(plan_extend_kernel, dim3(1), dim3(kPlanThreads), 0, stream, use_pdl, p);
+  cudaError_t e = launch_kernel(PA_PLAN(plan_extend_kernel, p), dim3(1), PA_PLAN_THREADS(p), 0, stream, use_pdl, p);
   if (e != cudaSuccess) return fail_at(e, "cudaLaunchKernelEx (plan)");
   const int64_t tables = static_cast<int64_t>(p.count) * ((p.max_seq_pages + kTablePages - 1) / kTablePages);
   return fail_at(launch_kernel(apply_extend_kernel, dim3(blocks_for(tables)), dim3(kThreads), 0, stream, use_pdl, p),
@@ -470,7 +492,7 @@ cudaError_t launch_pages_free(const PagesParams& p, cudaStream_t stream, bool us
 
 cudaError_t launch_pages_compact(const PagesParams& p, const pa_page_pool* pools, int32_t num,
                                  cudaStream_t stream, bool use_pdl) {
-  cudaError_t e = launch_kernel(plan_compact_kernel, dim3(1), dim3(kPlanThreads), 0, stream, use_pdl, p);
+  cudaError_t e = launch_kernel(PA_PLAN(plan_compact_kernel, p), dim3(1), PA_PLAN_THREADS(p), 0, stream, use_pdl, p);
   if (e != cudaSuccess) return fail_at(e, "cudaLaunchKernelEx (plan)");
   const PagesPools first = pack(pools, pools, 0, num);
   const int64_t tables = static_cast<int64_t>(p.count) * ((p.max_seq_pages + kTablePages - 1) / kTablePages);
