@@ -26,12 +26,12 @@ pa_status check_pools(const pa_page_pool* pools, int32_t num_pools) {
   return PA_OK;
 }
 
-// What the operators on the slot table have in common (count >= 1).
+// What the operators on the slot table have in common.
 pa_status table_params(int32_t* req_to_token, int64_t num_rows, int64_t row_stride,
                        int32_t* page_refs, int64_t num_pages, int32_t page_size,
                        int32_t max_seq_pages, const int64_t* rows, const int32_t* lens,
                        int32_t count, pa::PagesParams* p) {
-  if (!req_to_token || !page_refs || !rows || !lens) return PA_ERR_INVALID;
+  if (!req_to_token || !page_refs || (count > 0 && (!rows || !lens))) return PA_ERR_INVALID;
   if (!aligned(req_to_token, 4) || !aligned(page_refs, 4) || !aligned(rows, 8) || !aligned(lens, 4))
     return PA_ERR_INVALID;
   if (num_rows < 1 || num_pages < 1 || page_size < 1 || max_seq_pages < 1) return PA_ERR_INVALID;
@@ -50,8 +50,7 @@ pa_status table_params(int32_t* req_to_token, int64_t num_rows, int64_t row_stri
   p->rows = rows;
   p->lens = lens;
   p->count = count;
-  const cudaError_t e = pa::error_word(&p->err);
-  return e == cudaSuccess ? PA_OK : pa::from_cuda(e, "error word lookup");
+  return PA_OK;
 }
 
 // The workspace: a number, the copies' two lists, the free pages.
@@ -125,6 +124,8 @@ pa_status pa_pages_fork(int32_t* req_to_token, int64_t num_rows, int64_t row_str
   if (!children || !aligned(children, 8) || !child_lens || child_lens == lens) return PA_ERR_INVALID;
   p.children = children;
   p.granted = child_lens;
+  const cudaError_t e = pa::error_word(&p.err);
+  if (e != cudaSuccess) return pa::from_cuda(e, "error word lookup");
   return finish(pa::launch_pages_fork(p, pools, num_pools, static_cast<cudaStream_t>(stream), use_pdl != 0),
                 "page fork launch");
 }
@@ -145,6 +146,8 @@ pa_status pa_pages_extend(int32_t* req_to_token, int64_t num_rows, int64_t row_s
   if (!new_lens || !granted || granted == lens || granted == new_lens) return PA_ERR_INVALID;
   p.new_lens = new_lens;
   p.granted = granted;
+  const cudaError_t e = pa::error_word(&p.err);
+  if (e != cudaSuccess) return pa::from_cuda(e, "error word lookup");
   return finish(pa::launch_pages_extend(p, static_cast<cudaStream_t>(stream), use_pdl != 0),
                 "page extend launch");
 }
@@ -160,6 +163,8 @@ pa_status pa_pages_free(int32_t* req_to_token, int64_t num_rows, int64_t row_str
                                     page_size, max_seq_pages, rows, lens, count, &p);
   if (st != PA_OK) return st;
   p.new_lens = keep_lens;
+  const cudaError_t e = pa::error_word(&p.err);
+  if (e != cudaSuccess) return pa::from_cuda(e, "error word lookup");
   return finish(pa::launch_pages_free(p, static_cast<cudaStream_t>(stream), use_pdl != 0),
                 "page free launch");
 }
@@ -181,6 +186,8 @@ pa_status pa_pages_compact(int32_t* req_to_token, int64_t num_rows, int64_t row_
   if (!page_map || !num_live) return PA_ERR_INVALID;
   p.page_map = page_map;
   p.num_live = num_live;
+  const cudaError_t e = pa::error_word(&p.err);
+  if (e != cudaSuccess) return pa::from_cuda(e, "error word lookup");
   return finish(pa::launch_pages_compact(p, pools, num_pools, static_cast<cudaStream_t>(stream), use_pdl != 0),
                 "page compaction launch");
 }

@@ -101,6 +101,10 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
     q_len = 0;
   }
   const int n = prm.cache_seqlens != nullptr ? prm.cache_seqlens[b] : q_len;
+  if (n < q_len) {
+    if (rank == 0 && tid == 0) record_error(prm.err, kErrSeqLenOutOfRange);
+    q_len = 0;
+  }
   const int begin = n - q_len;
   int32_t* kept = prm.kept + static_cast<int64_t>(b) * prm.kept_stride;
   if (q_len == 0) {  // (the whole cluster)
