@@ -227,3 +227,247 @@ def test_append(seqlens, q_lens, hq, hkv, page, block, rot, interleaved, amplitu
     # the same append once more leaves the same bits
     run_append(c, q_lens, wide, positions, inv, hq, interleaved, amplitude)
     assert torch.equal(c.d_v.view(torch.uint8), again.view(torch.uint8))
+
+
+# ---- the contract around the numbers --------------------------------------------------------------
+
+
+def raw_call(c, q, out, lse, cu, mql, **kw):
+    splits = kw.pop("num_splits", 0)
+    ws = torch.full((B.pa_workspace_bytes(q.shape[0], q.shape[1], 128, max(splits, 70)),), 0xff, dtype=torch.uint8,
+                    device="cuda")
+    return B.prepare_block_attention(
+        q=q, k_cache=c.d_k, v_cache=c.d_v, k_scale=c.d_ks, v_scale=c.d_vs, page_table=kw.pop("table", c.d_table),
+        cache_seqlens=kw.pop("n", c.d_n), cu_seqlens_q=cu, max_q_len=mql, max_seq_pages=kw.pop("msp", c.msp),
+        sm_scale=SCALE, out=out, lse=lse, workspace=ws, num_splits=splits, **kw)
+
+
+def blank(rows, hq):
+    return (torch.full((rows, hq, 128), 7.0, dtype=torch.bfloat16, device="cuda"),
+            torch.full((rows, hq), 7.0, device="cuda"))
+
+
+def same(a, b):
+    return torch.equal(a.view(torch.int16 if a.element_size() == 2 else torch.int32),
+                       b.view(torch.int16 if b.element_size() == 2 else torch.int32))
+
+
+@pytest.mark.parametrize("hq,hkv,splits", [(8, 2, 1), (8, 2, 3), (32, 2, 0), (32, 1, 2)])
+def test_rows_that_no_request_covers_stay(hq, hkv, splits):
+    """Padding rows, rows before the first request and those of refused requests."""
+    c = BlockCache([300, 40, 20, 700], hkv, 64, 32, 71)
+    q = torch.randn((14, hq, 128), generator=c.g).to(torch.bfloat16)
+    out, lse = blank(14, hq)
+    cu = torch.tensor([2, 4, 9, 9, 11], dtype=torch.int32).cuda()    # the second has 5 > max_q_len
+    raw_call(c, q.cuda(), out, lse, cu, 4, num_splits=splits)()
+    torch.cuda.synchronize()
+    assert B.pa_read_error_flags(reset=True) == B.DEVERR_SEQLEN_OUT_OF_RANGE
+    ref = R.attention(torch.cat((q[2:4], q[9:11])), c.k, c.v, c.ks, c.vs, c.table[[0, 3]], [300, 700], [2, 2], SCALE)
+    pick = [2, 3, 9, 10]
+    check(out[pick], lse[pick], ref)
+    rest = [i for i in range(14) if i not in pick]
+    assert bool((out[rest] == 7.0).all()) and bool((lse[rest] == 7.0).all())
+
+
+@pytest.mark.parametrize("splits", [1, 3])
+def test_a_query_that_sees_nothing(splits):
+    """Queries before the context's start, and an empty context."""
+    c = BlockCache([3, 0, 200], 2, 16, 16, 72)
+    q = torch.randn((7 + 2 + 5, 6, 128), generator=c.g).to(torch.bfloat16)
+    out, lse = attend(c, q.cuda(), [7, 2, 5], num_splits=splits)
+    check(out, lse, R.attention(q, c.k, c.v, c.ks, c.vs, c.table, c.n, [7, 2, 5], SCALE))
+    assert not out[:4].any() and bool((lse[:4] == -math.inf).all())
+    assert not out[7:9].any() and bool((lse[7:9] == -math.inf).all())
+
+
+def test_non_finite_values_stay_where_they_are_seen():
+    c = BlockCache([150, 150], 2, 64, 64, 73)
+    q = torch.randn((6, 8, 128), generator=c.g).to(torch.bfloat16)
+    q[4, 3, 77] = math.nan
+    q[5, 6, 0] = math.inf
+    page, row = int(c.table[0, 149 // 64]), 149 % 64     # the first request's newest token
+    c.k.view(torch.uint8)[page, 1, row, 5] = NAN_CODE     # seen by its last query alone, heads 4 .. 7
+    c.to_device()
+    out, lse = attend(c, q.cuda(), [3, 3], num_splits=2)
+    bad = torch.isnan(out.float()).all(-1).cpu()
+    want = torch.zeros(6, 8, dtype=torch.bool)
+    want[2, 4:] = want[4, 3] = want[5, 6] = True
+    assert torch.equal(bad, want) and torch.equal(torch.isnan(lse).cpu(), want)
+    assert torch.equal(torch.isnan(out.float()).any(-1).cpu(), want)
+
+
+def test_blocks_of_zeros_and_of_very_different_scales():
+    """Zero scales (rows of zeros as the append leaves them); scales 2^12 apart in one chunk."""
+    c = BlockCache([256, 130], 1, 64, 16, 74)
+    for s in (c.ks, c.vs):
+        s.copy_(torch.exp2(torch.randint(-12, 1, s.shape, generator=c.g).float()))
+    for b, n in enumerate(c.n):
+        for j in range(16 * b, n, 48):
+            p, i = int(c.table[b, j // 64]), j % 64 // 16
+            c.ks[p, 0, i] = c.vs[p, 0, i] = 0.0
+    c.to_device()
+    q = (torch.randn((2, 4, 128), generator=c.g) * 0.02).to(torch.bfloat16)
+    out, lse = attend(c, q.cuda(), num_splits=1)
+    check(out, lse, R.attention(q, c.k, c.v, c.ks, c.vs, c.table, c.n, [1, 1], SCALE))
+    c.vs.zero_()
+    c.to_device()
+    out, again = attend(c, q.cuda(), num_splits=3)
+    assert not out.any() and torch.allclose(lse, again, rtol=0, atol=1e-4)
+
+
+@pytest.mark.parametrize("factor", [1e30, 1e-30, 65536.0])
+def test_queries_of_any_size(factor):
+    c = BlockCache([200], 2, 64, 64, 75)
+    q = (torch.randn((1, 8, 128), generator=c.g) * factor).to(torch.bfloat16)
+    scale = SCALE / factor
+    out, lse = attend(c, q.cuda(), num_splits=1, sm_scale=scale)
+    check(out, lse, R.attention(q, c.k, c.v, c.ks, c.vs, c.table, c.n, [1], scale), scale)
+
+
+def test_what_the_device_alone_sees_is_reported():
+    c = BlockCache([100, 90], 2, 16, 16, 76)
+    q = torch.randn((2, 4, 128), generator=c.g).to(torch.bfloat16).cuda()
+    out, lse = blank(2, 4)
+    table = c.d_table.clone()
+    table[0, 2] = c.num_pages
+    table[1, 1] = -3
+    raw_call(c, q, out, lse, None, 1, table=table)()
+    torch.cuda.synchronize()
+    assert B.pa_read_error_flags(reset=True) == B.DEVERR_PAGE_OUT_OF_RANGE
+    n = torch.tensor([c.msp * 16 + 1, -5], dtype=torch.int32).cuda()
+    raw_call(c, q, out, lse, None, 1, n=n)()
+    torch.cuda.synchronize()
+    assert B.pa_read_error_flags(reset=True) & B.DEVERR_SEQLEN_OUT_OF_RANGE
+    assert not out[1].any() and bool((lse[1] == -math.inf).all())
+
+
+def test_equal_inputs_give_equal_bits_whatever_the_pages_and_the_launch():
+    c = BlockCache([1000, 13, 400], 4, 32, 16, 77)
+    q = torch.randn((9, 16, 128), generator=c.g).to(torch.bfloat16).cuda()
+    first = attend(c, q, [4, 3, 2])
+    for pdl in (True, False):
+        again = attend(c, q, [4, 3, 2], use_pdl=pdl)
+        assert same(first[0], again[0]) and same(first[1], again[1])
+    # a wider table, pages in another order
+    perm = torch.randperm(c.num_pages, generator=c.g)
+    for x, d in ((c.k, "d_k"), (c.v, "d_v"), (c.ks, "d_ks"), (c.vs, "d_vs")):
+        moved = torch.empty_like(x)
+        moved.view(torch.uint8)[perm] = x.view(torch.uint8)
+        setattr(c, d, moved.cuda())
+    c.d_table = perm.to(torch.int32)[c.table.long()].cuda()
+    again = attend(c, q, [4, 3, 2])
+    assert same(first[0], again[0]) and same(first[1], again[1])
+
+
+def test_two_captured_graphs_with_their_own_workspaces():
+    """Captured on a side stream, replayed in turn with other queries and lengths."""
+    c = BlockCache([500, 900], 2, 64, 64, 78)
+    side = torch.cuda.Stream()
+    cases = []
+    for k in range(2):
+        q = torch.randn((2, 8, 128), generator=c.g).to(torch.bfloat16).cuda()
+        out, lse = blank(2, 8)
+        n = c.d_n.clone()
+        with torch.cuda.stream(side):
+            call = raw_call(c, q, out, lse, None, 1, num_splits=4 + k, n=n)
+            side.synchronize()
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph, stream=side):
+                raw = raw_call(c, q, out, lse, None, 1, num_splits=4 + k, n=n)
+                raw()
+        cases.append((graph, q, out, lse, n, call, raw))
+    for step in range(3):
+        for k, (graph, q, out, lse, n, *_) in enumerate(cases):
+            q.copy_(torch.randn((2, 8, 128), generator=c.g).to(torch.bfloat16))
+            n.copy_(torch.tensor([500 - 130 * step, 900 - 77 * k - 1 * step], dtype=torch.int32))
+        torch.cuda.synchronize()
+        for graph, *_ in cases:
+            graph.replay()
+        torch.cuda.synchronize()
+        for graph, q, out, lse, n, *_ in cases:
+            lens = n.tolist()
+            check(out, lse, R.attention(q.cpu(), c.k, c.v, c.ks, c.vs, c.table, lens, [1, 1], SCALE))
+
+
+def test_pages_past_four_gigabytes():
+    """Page and scale offsets past 2^32 bytes, in attention and append."""
+    page, hkv = 128, 8
+    pages = (5 << 30) // (hkv * page * 128) + 3
+    pool = torch.empty((2, pages, hkv, page, 128), dtype=torch.uint8, device="cuda")
+    c = BlockCache([300], hkv, page, 128, 79)
+    c.table[0, :3] = torch.tensor([pages - 1, 5, pages - 2])
+    big = []
+    for i, (x, s) in enumerate(((c.k, c.ks), (c.v, c.vs))):
+        used = (torch.randn((3, hkv, page, 128), generator=c.g) * 90).clamp(-448, 448).to(torch.float8_e4m3fn)
+        scale = torch.full((pages, hkv, 1), math.nan)
+        for j in range(3):
+            pool[i, c.table[0, j].item()] = used[j].view(torch.uint8).cuda()
+            scale[c.table[0, j].item()] = torch.rand((hkv, 1), generator=c.g) * 0.01 + 0.01
+        big.append((used, scale))
+    c.d_k, c.d_v = (pool[i].view(torch.float8_e4m3fn) for i in range(2))
+    c.d_ks, c.d_vs = (s.cuda() for _, s in big)
+    c.d_table, c.num_pages, c.msp = c.table.cuda(), pages, 3
+    q = torch.randn((1, 32, 128), generator=c.g).to(torch.bfloat16)
+    out, lse = attend(c, q.cuda())
+    small = torch.tensor([[0, 1, 2]], dtype=torch.int32)
+    order = c.table[0].long()
+    check(out, lse, R.attention(q, big[0][0], big[1][0], big[0][1][order], big[1][1][order], small, [300], [1], SCALE))
+    new = torch.ones((1, hkv, 128), dtype=torch.bfloat16, device="cuda")
+    n = torch.tensor([301], dtype=torch.int32).cuda()
+    B.pa_rope_append_blocks(k=new, v=new * 2, k_cache=c.d_k, v_cache=c.d_v, k_scale=c.d_ks, v_scale=c.d_vs,
+                            cu_seqlens_q=torch.tensor([0, 1], dtype=torch.int32).cuda(), cache_seqlens=n,
+                            page_table=c.d_table, max_seq_pages=3)
+    torch.cuda.synchronize()
+    got = pool[1, pages - 2, :, 300 - 256].view(torch.float8_e4m3fn).float() * c.d_vs[pages - 2]
+    assert bool(((got - 2.0).abs() <= 2.0 * 2.0 ** -4).all())
+
+
+def test_append_leaves_rows_of_refused_requests():
+    c = BlockCache([100, 60, 30], 2, 16, 16, 80)
+    wide, positions, inv = append_inputs(c, [4, 3, 2], 4, 128, 80)
+    before = [x.clone() for x in (c.d_k, c.d_v, c.d_ks, c.d_vs)]
+    table = c.d_table.clone()
+    c.d_table[0, 6] = c.num_pages + 9                       # the page of positions 96 ..
+    c.d_n = torch.tensor([100, 2, 30], dtype=torch.int32).cuda()   # fewer than its three new rows
+    q_out = run_append(c, [4, 3, 2], wide, positions, inv, 4, False, 1.0)
+    assert B.pa_read_error_flags(reset=True) == B.DEVERR_PAGE_OUT_OF_RANGE | B.DEVERR_SEQLEN_OUT_OF_RANGE
+    assert bool((q_out[4:7] == 7.0).all()) and not bool((q_out[7:] == 7.0).any())
+    pages = [int(table[2, 28 // 16])]
+    for x, y in zip(before, (c.d_k, c.d_v, c.d_ks, c.d_vs)):
+        x, y = (z.view(torch.uint8) if z.element_size() == 1 else z.view(torch.int32) for z in (x, y))
+        changed = (x != y).flatten(1).any(1).nonzero().flatten().tolist()
+        assert set(changed) <= set(pages)
+
+
+def test_append_in_place_on_a_projection_and_grown_scales():
+    """q turned in place in the projection it lies in; a block filled token by token, larger and
+    larger, holds what one append of all tokens would, to the halvings' rounding."""
+    hkv, n = 2, 16
+    c = BlockCache([n], hkv, 16, 16, 81)
+    d = BlockCache([n], hkv, 16, 16, 81)
+    wide = torch.randn((n, 4 + 2 * hkv, 128), generator=c.g)
+    wide = (wide * torch.exp2(torch.arange(n).float() / 2)[:, None, None]).to(torch.bfloat16)
+    inv = 10000.0 ** (-2.0 * torch.arange(64, dtype=torch.float64) / 128)
+    whole, by_one = wide.cuda(), wide.cuda()
+    def append(c, rows, lo, hi):
+        q, k, v = rows[lo:hi].split([4, hkv, hkv], dim=1)
+        B.pa_rope_append_blocks(q=q, q_out=q, k=k, v=v, positions=torch.arange(lo, hi).cuda(), inv_freq=inv.cuda(),
+                                k_cache=c.d_k, v_cache=c.d_v, k_scale=c.d_ks, v_scale=c.d_vs,
+                                cu_seqlens_q=torch.tensor([0, hi - lo], dtype=torch.int32).cuda(),
+                                cache_seqlens=torch.tensor([hi], dtype=torch.int32).cuda(), page_table=c.d_table,
+                                max_seq_pages=c.msp)
+    append(c, whole, 0, n)
+    for i in range(n):
+        append(d, by_one, i, i + 1)
+    torch.cuda.synchronize()
+    assert torch.equal(whole[:, :4].view(torch.int16), by_one[:, :4].view(torch.int16))
+    want = R.rope(wide[:, :4], torch.arange(n), inv, False, 1.0)
+    big = want.abs().amax(-1, keepdim=True)
+    assert ((whole[:, :4].double().cpu() - want).abs() <= HALF_STEP * want.abs() + 2.0 ** -20 * big).all()
+    p = int(c.table[0, 0])
+    assert torch.equal(c.d_ks[p], d.d_ks[p]) and torch.equal(c.d_vs[p], d.d_vs[p])
+    for x, y, s in ((c.d_k, d.d_k, c.d_ks), (c.d_v, d.d_v, c.d_vs)):
+        a, b = x[p].float(), y[p].float()
+        # a code is exact through a halving until it leaves the normal range: then each of up to 9
+        # halvings rounds to the smallest step, 2^-9, by half of it at most, halved by the later ones
+        assert bool(((a - b).abs() <= torch.where(a.abs() < 2.0 ** -6, 2.0 ** -9, 0.0)).all())

@@ -122,3 +122,112 @@ def test_verify(q_lens, vocab, width, drafted, pad):
     d.check(got)
     again = d.run()
     assert all(torch.equal(a, b) for a, b in zip(got, again))
+
+
+def test_accepted_tokens_follow_the_target():
+    """20000 requests of one drafted token over 12 tokens: whatever the draft, the first token that
+    comes out is the target's to 5 standard deviations of its count."""
+    n, vocab = 20000, 12
+    g = torch.Generator().manual_seed(5)
+    p = torch.softmax(torch.randn(vocab, generator=g) * 1.5, -1)
+    q = torch.softmax(torch.randn(vocab, generator=g) * 1.5, -1)
+    for drafted in (True, False):
+        d = Drafts([2] * n, vocab, 0, drafted, seed=6)
+        d.target = p.expand(2 * n, vocab).contiguous()
+        d.draft = q.expand(2 * n, vocab).contiguous() if drafted else None
+        x = torch.multinomial(q, n, replacement=True, generator=g)
+        d.tokens = torch.stack((torch.zeros(n, dtype=torch.int64), x), 1).flatten()
+        kept, counts, begin, tokens = d.run()
+        first = torch.where(counts == 2, x, tokens)
+        seen = torch.bincount(first, minlength=vocab).double()
+        want = p.double() * n
+        assert ((seen - want).abs() <= 5 * (want * (1 - p.double())).sqrt() + 1).all()
+
+
+def test_trees_with_siblings_follow_the_target():
+    """Three siblings drawn from the draft, and the three likeliest tokens: the token that follows
+    the root is the target's."""
+    n, vocab = 20000, 9
+    g = torch.Generator().manual_seed(7)
+    p = torch.softmax(torch.randn(vocab, generator=g), -1)
+    q = torch.softmax(torch.randn(vocab, generator=g), -1)
+    for drafted in (True, False):
+        d = Drafts([4] * n, vocab, 3, drafted, seed=8)
+        d.parents = [-1, 0, 0, 0] * n
+        d.target = p.expand(4 * n, vocab).contiguous()
+        d.draft = q.expand(4 * n, vocab).contiguous() if drafted else None
+        x = torch.multinomial(q, 3 * n, replacement=True, generator=g).view(n, 3) if drafted else \
+            torch.topk(q, 3).indices.expand(n, 3)
+        d.tokens = torch.cat((torch.zeros(n, 1, dtype=torch.int64), x), 1).flatten().contiguous()
+        kept, counts, begin, tokens = d.run()
+        node = (kept[:, 1] - begin).clamp(min=0).long()
+        first = torch.where(counts == 2, d.tokens.view(n, 4).gather(1, node[:, None])[:, 0], tokens)
+        seen = torch.bincount(first, minlength=vocab).double()
+        want = p.double() * n
+        assert ((seen - want).abs() <= 5 * (want * (1 - p.double())).sqrt() + 1).all()
+
+
+def test_nothing_left_of_the_row():
+    """A draft equal to the target is accepted for any number below 1; where a number of 1 rejects it
+    all the same, the token comes from the row itself.  A row of zeros gives -1 and is reported."""
+    d = Drafts([3, 2], 40, 0, True, seed=9)
+    d.draft = d.target.clone()
+    d.check(d.run())
+    d.uniforms.fill_(1.0)
+    d.check(d.run())
+    d.target[3].zero_()
+    d.target[4].zero_()
+    d.check(d.run())
+    assert B.pa_read_error_flags(reset=True) == B.DEVERR_NO_PROBABILITY
+
+
+def test_what_is_refused_is_reported():
+    d = Drafts([4, 3, 5], 50, 3, False, seed=10)
+    d.tokens[2], d.tokens[5] = 50, -1                        # outside the vocabulary: never accepted
+    d.check(d.run())
+    assert B.pa_read_error_flags(reset=True) == B.DEVERR_TOKEN_OUT_OF_RANGE
+    d = Drafts([4, 3, 5], 50, 3, True, seed=11)
+    got = d.run(parents=torch.tensor([-1, 1, 0, 9, -1, 0, -2, -1, 0, 1, 2, 3], dtype=torch.int32).cuda())
+    assert B.pa_read_error_flags(reset=True) == B.DEVERR_TREE_PARENT
+    d.parents = [-1, -1, 0, -1, -1, 0, -1, -1, 0, 1, 2, 3]
+    d.check(got)
+    d.n[1] = 2                                               # fewer than its rows
+    kept, counts, begin, tokens = d.run(max_q_len=4, kept=torch.full((3, 6), 77, dtype=torch.int32, device="cuda"))
+    assert B.pa_read_error_flags(reset=True) & B.DEVERR_SEQLEN_OUT_OF_RANGE
+    assert counts[1:].tolist() == [0, 0] and tokens[1:].tolist() == [-1, -1]
+    assert kept[1:].tolist() == [[-1] * 4 + [77, 77]] * 2 and int(counts[0]) > 0
+
+
+def test_without_lengths_kept_are_rows():
+    d = Drafts([6, 6], 100, 0, True, seed=12)
+    with_lengths = d.run()
+    d.n = torch.tensor([6, 6], dtype=torch.int32)
+    kept, counts, begin, tokens = d.run(cache_seqlens=None, begin=None)
+    assert begin is None and torch.equal(counts, with_lengths[1]) and torch.equal(tokens, with_lengths[3])
+    for b in range(2):
+        assert kept[b, :int(counts[b])].tolist() == list(range(int(counts[b])))
+
+
+def test_verified_path_compacts_the_cache():
+    """kept, counts and begin go to pa_compact_cache as they are."""
+    d = Drafts([12, 9], 30, 4, False, seed=13)
+    kept, counts, begin, tokens = d.run()
+    d.check((kept, counts, begin, tokens))
+    page, hkv = 16, 2
+    per = [-(-int(n) // page) for n in d.n]
+    table = torch.zeros((2, max(per)), dtype=torch.int32)
+    table[0, :per[0]] = torch.arange(per[0])
+    table[1, :per[1]] = torch.arange(per[0], sum(per))
+    k, v = (torch.randn((sum(per), hkv, page, 128)).to(torch.bfloat16).cuda() for _ in "kv")
+    before = k.clone()
+    new = torch.zeros(2, dtype=torch.int32, device="cuda")
+    B.pa_compact_cache(page_table=table.cuda(), cache_seqlens=d.n.cuda(), kept=kept[:, None, :12].contiguous().cuda(),
+                       counts=counts.cuda(), begin=begin.cuda(), k_cache=k, v_cache=v, max_seq_pages=max(per),
+                       new_seqlens=new)
+    torch.cuda.synchronize()
+    assert torch.equal(new.cpu(), begin + counts)
+    for b in range(2):
+        for i in range(int(counts[b])):
+            src, dst = int(kept[b, i]), int(begin[b]) + i
+            assert torch.equal(k[table[b, dst // page].item(), :, dst % page],
+                               before[table[b, src // page].item(), :, src % page])
