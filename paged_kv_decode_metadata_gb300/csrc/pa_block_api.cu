@@ -124,7 +124,7 @@ int32_t pa_choose_block_splits(int32_t bs, int32_t max_q_len, int32_t num_q_head
   const int32_t columns = tile_columns(group, max_q_len);
   const int64_t units = static_cast<int64_t>(bs) * num_kv_heads * cdiv(max_q_len, tile_queries(group, max_q_len));
   const int64_t chunks = cdiv(static_cast<int64_t>(max_seq_pages) * page_size, 128);
-  const int64_t blocks = static_cast<int64_t>(sm_count) * (columns == 8 ? 3 : columns == 16 ? 2 : 1);
+  const int64_t blocks = static_cast<int64_t>(sm_count) * (columns <= 16 ? 2 : 1);
   int64_t share = units * chunks / blocks;
   if (share < 1) share = 1;
   int64_t want = cdiv(2 * chunks, share) + 1;

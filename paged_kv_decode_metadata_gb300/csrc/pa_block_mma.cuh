@@ -58,7 +58,8 @@ struct Piece {
 constexpr int kUnitCost = 2;
 struct Walk {
   int b, q_begin, q_len, n, tiles, chunks;  // the request at hand
-  int base, pos, end, share;                // its start on the line; where the walk is
+  int from, kvh, tile;                      // the unit at hand: its first chunk on the line
+  int pos, end, share;                      // where the walk is
   int cut;                                  // whether units are cut
 
   // Lengths of request r as they stand, then checked; `report` records what is wrong with them.
@@ -104,7 +105,7 @@ struct Walk {
     constexpr int kPer = 4;
     const int per = prm.bs <= 32 ? 1 : kPer, round_size = 32 * per;
     Walk r[kPer];
-    int total = 0, longest = 0, w = 0, incl = 0;
+    int total = 0, longest = 0, shortest = INT_MAX, w = 0, incl = 0;
     bool empties = false;
     auto round = [&](int r0, bool report) {
       w = 0;
@@ -129,17 +130,25 @@ struct Walk {
 #pragma unroll
       for (int k = 0; k < kPer; ++k) {
         empties = empties || (r[k].q_len > 0 && r[k].n == 0);
-        if (r[k].tiles > 0) longest = max(longest, r[k].chunks);
+        if (r[k].tiles > 0 && r[k].chunks > 0) {
+          longest = max(longest, r[k].chunks);
+          shortest = min(shortest, r[k].chunks);
+        }
       }
       total += __shfl_sync(0xffffffffu, incl, 31);
     }
     longest = __reduce_max_sync(0xffffffffu, longest);
+    shortest = __reduce_min_sync(0xffffffffu, shortest);
     empties = __any_sync(0xffffffffu, empties);
     // A unit of c chunks (its places in a row) meets at most floor((c - 1) / share) + 2 shares (c of them if share is
     // 1): a share of longest / (num_splits - 1) keeps every unit's pieces within num_splits.
     const int S = prm.num_splits, grid = static_cast<int>(gridDim.x);
     share = (total + grid - 1) / grid;
-    cut = S > 1;
+    // Units of one length that fill the blocks well enough stay whole: partials and their join cost
+    // more than up to a fifth of a share left idle (256 units of 64 chunks on 304 blocks 82 us whole,
+    // 85.5 cut; 512 of them 163 and 161).
+    const int unit_places = longest + kUnitCost;
+    cut = S > 1 && !(longest == shortest && (total / unit_places + grid - 1) / grid * unit_places <= share + share / 5);
     if (cut && S < longest) share = max(share, (longest + S - 2) / (S - 1));
     const long long at_ll = static_cast<long long>(blockIdx.x) * share;
     pos = static_cast<int>(min(at_ll, static_cast<long long>(total)));
@@ -151,8 +160,8 @@ struct Walk {
       if (prm.bs > round_size) round(r0, false);
       const uint32_t has = __ballot_sync(0xffffffffu, pos < before + incl);
       if (has != 0) {
-        const int from = __ffs(has) - 1;
-        int first = before + incl - w;  // (of lane `from`, whose requests hold pos)
+        const int lane_of = __ffs(has) - 1;
+        int first = before + incl - w;  // (of that lane, whose requests hold pos)
 #pragma unroll
         for (int k = 0; k < kPer; ++k) {
           const int length_k = r[k].length(prm);
@@ -163,50 +172,67 @@ struct Walk {
             n = r[k].n;
             tiles = r[k].tiles;
             chunks = r[k].chunks;
-            base = first;
+            from = first;
           }
           first += length_k;
         }
-        b = __shfl_sync(0xffffffffu, b, from);
-        q_begin = __shfl_sync(0xffffffffu, q_begin, from);
-        q_len = __shfl_sync(0xffffffffu, q_len, from);
-        n = __shfl_sync(0xffffffffu, n, from);
-        tiles = __shfl_sync(0xffffffffu, tiles, from);
-        chunks = __shfl_sync(0xffffffffu, chunks, from);
-        base = __shfl_sync(0xffffffffu, base, from);
+        b = __shfl_sync(0xffffffffu, b, lane_of);
+        q_begin = __shfl_sync(0xffffffffu, q_begin, lane_of);
+        q_len = __shfl_sync(0xffffffffu, q_len, lane_of);
+        n = __shfl_sync(0xffffffffu, n, lane_of);
+        tiles = __shfl_sync(0xffffffffu, tiles, lane_of);
+        chunks = __shfl_sync(0xffffffffu, chunks, lane_of);
+        from = __shfl_sync(0xffffffffu, from, lane_of);
         break;
       }
       before += __shfl_sync(0xffffffffu, incl, 31);
     }
-    const int unit = chunks + kUnitCost;
-    if (!cut) pos = base + (pos - base + unit - 1) / unit * unit;
+    const int places = chunks + kUnitCost;
+    int unit = (pos - from) / places;
+    if (!cut && unit * places < pos - from) ++unit;  // units that start here
+    from += unit * places;
+    if (!cut) pos = from;
+    from += kUnitCost;
+    kvh = tiles == 1 ? unit : unit / tiles;  // (one past the last: the next request)
+    tile = unit - kvh * tiles;
     return empties;
   }
 
+  // (No division but for units that a cut falls into: between pieces the block waits for it.)
   __device__ __forceinline__ bool next(const BlockParams& prm, Piece& p) {
     while (pos < end) {
-      while (pos - base >= length(prm)) {  // into the next request that has work
-        base += length(prm);
-        load(prm, b + 1, false);
+      if (pos >= from + chunks) {  // on to the next unit
+        from += chunks + kUnitCost;
+        if (++tile == tiles) {
+          tile = 0;
+          ++kvh;
+        }
       }
-      const int unit = (pos - base) / (chunks + kUnitCost);
-      const int from = base + unit * (chunks + kUnitCost) + kUnitCost;  // of the unit's first chunk
+      if (kvh == prm.num_kv_heads) {  // of the next request that has work
+        const int at = from - kUnitCost;
+        do {
+          load(prm, b + 1, false);
+        } while (length(prm) == 0);
+        from = at + kUnitCost;
+        kvh = tile = 0;
+      }
       p.b = b;
       p.q_begin = q_begin;
       p.q_len = q_len;
       p.n = n;
-      p.kvh = tiles == 1 ? unit : unit / tiles;
-      p.tile = unit - p.kvh * tiles;
+      p.kvh = kvh;
+      p.tile = tile;
       p.c0 = max(pos - from, 0);
       p.c1 = cut ? min(chunks, end - from) : chunks;
       p.slot = 0;
       p.pieces = 1;
-      if (cut) {
+      if (cut && (p.c0 > 0 || p.c1 < chunks)) {
         const int first = from / share;
         p.slot = static_cast<int>(blockIdx.x) - first;
         p.pieces = (from + chunks - 1) / share - first + 1;
       }
-      pos = min(from + chunks, cut ? end : INT_MAX);
+      pos = from + p.c1;
+      if (cut && p.c1 < chunks) pos = end;
       if (p.c1 > p.c0) return true;  // (a share may end before a unit's first chunk)
     }
     return false;
@@ -219,25 +245,28 @@ struct Shape {
   static constexpr int kTmaWarp = kSoftmaxWarps, kScoreWarp = kTmaWarp + 1, kOutWarp = kTmaWarp + 2;
   static constexpr int kThreads = 32 * (kOutWarp + 2);  // (a warpgroup of these, one idle)
   // registers a thread: of the launch, then of the softmax warps and the others
-  static constexpr int kLaunchRegs = C == 32 ? 96 : 80;
-  static constexpr int kSoftmaxRegs = C == 8 ? 96 : C == 16 ? 88 : 104, kOtherRegs = 64;
+  static constexpr int kLaunchRegs = C == 8 ? 128 : C == 16 ? 80 : 96;
+  static constexpr int kSoftmaxRegs = C == 8 ? 168 : C == 16 ? 96 : 104, kOtherRegs = C == 8 ? 80 : C == 16 ? 48 : 64;
   static_assert(32 * (kSoftmaxWarps * kSoftmaxRegs + 4 * kOtherRegs) <= kThreads * kLaunchRegs, "register split");
   static constexpr int kScoreCols = 2 * C;
   static constexpr int kOutCols = (3 * C + 15) / 16 * 16;
   static constexpr int kTmemCols = C == 8 ? 64 : C == 16 ? 128 : 256;
   static_assert(2 * kScoreCols + kOutCols <= kTmemCols, "tensor memory");
-  static constexpr int kSlots = C == 8 ? 4 : C == 16 ? 6 : 10;
+  // Tiles in flight: 8 an SM stream best (12 and 6: 64 requests of 16K 329 and 317-321 us against 314-316),
+  // and two blocks of them with four rather than three with two.
+  static constexpr int kSlots = C <= 16 ? 4 : 10;
   // A slot holds K tiles or V tiles, never both in turn: only then has whoever waits for a tile
   // seen the slot's one before, and a barrier's parity tells which of the two has landed.
   static_assert(kSlots % 2 == 0, "K and V slots");
-  static constexpr int kBlocks = C == 8 ? 3 : C == 16 ? 2 : 1;  // resident per SM
+  static constexpr int kBlocks = C <= 16 ? 2 : 1;  // resident per SM
   static constexpr int kRing = 0;
   static constexpr int kQ = kSlots * kTileBytes;
   static constexpr int kP = kQ + kScoreCols * 128;
   // The weights' tile: a row per token, its 3 C pieces next to one another ("MN-major"), rows of 32,
   // 64 or 128 bytes with that swizzle.
   static constexpr int kRowBytes = C == 8 ? 32 : C == 16 ? 64 : 128;
-  static constexpr int kEnd = kP + kTile * kRowBytes;
+  static constexpr int kStage = kP + kTile * kRowBytes;  // the columns' sums on their way out
+  static constexpr int kEnd = kStage + C * 128 * 4;
   // High word of its descriptor: the stride offset steps 8 rows; version 1; the swizzle's code.
   static constexpr uint32_t kWeightsHigh =
       (8u * kRowBytes >> 4) | (1u << 14) | ((C == 8 ? 6u : C == 16 ? 4u : 2u) << 29);
@@ -253,6 +282,7 @@ struct Shape {
     alignas(16) float peak[2][C][4];
     alignas(16) float v_peak[2][C / 8][4];
     alignas(16) float sum[C][4];
+    float inverse[C];
     float factor[C];  // of a column's scores
     Walk walk;
     uint32_t tmem;
@@ -359,6 +389,13 @@ __device__ __forceinline__ void arrive_if(uint64_t* bar, bool yes) {
       "@p mbarrier.arrive.shared::cta.b64 _, [%0];\n\t}" ::"r"(smem_addr(bar)),
       "r"(yes ? 1u : 0u)
       : "memory");
+}
+
+__device__ __forceinline__ float pick(const float (&x)[8], int i) {
+  float y = x[0];
+#pragma unroll
+  for (int j = 1; j < 8; ++j) y = i == j ? x[j] : y;
+  return y;
 }
 
 // The four warps of 8 columns.  (Numbers that the compiler knows: for others it sets all 16 of a
@@ -514,10 +551,11 @@ __global__ void __launch_bounds__(Shape<C>::kThreads, Shape<C>::kBlocks)
       }
       page = page_of(1);
       if (chunks > 0) {
-#pragma unroll
+#pragma unroll 1
         for (int u = 0; u < 2; ++u) {
           const int c = 2 * warp + u;
-          const float x[4] = {bf16_lo(rows[u].x), bf16_hi(rows[u].x), bf16_lo(rows[u].y), bf16_hi(rows[u].y)};
+          const uint2 row = u == 0 ? rows[0] : rows[1];
+          const float x[4] = {bf16_lo(row.x), bf16_hi(row.x), bf16_lo(row.y), bf16_hi(row.y)};
           const float mine = fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3])));
           const float big = warp_peak(mine);
           const int e = big > 0.f ? 7 - mma::float_exponent(big) : 0;  // the largest in [128, 256)
@@ -569,56 +607,58 @@ __global__ void __launch_bounds__(Shape<C>::kThreads, Shape<C>::kBlocks)
           acc[j] = fmaf(fmaf(fmaf(h3[j], 1.f / 16.f, h2[j]), 1.f / 16.f, h1[j]), v_down, acc[j]);
         umma::fence_before();
       };
-      for (int i = 0; i < chunks; ++i, ++step) {
-        const int pos = first + i * kTile + token;
-        // what the next chunks need, on its way
-        float ks_next = 0.f, vs_next = 0.f;
-        if (pos + kTile < last) {
-          ks_next = prm.k_scale[scale_at(i + 1, page)];
-          vs_next = prm.v_scale[scale_at(i + 1, page)];
-        }
-        page = page_of(i + 2);
+      for (int i = 0;; ++i, ++step) {
         const uint32_t buf = step & 1u;
-        vs = pos < last ? vs : 0.f;
-        const float v_top = warp_peak(fabsf(vs));
-        if (lane == 0) ctl.v_peak[buf][group][w4] = v_top;
-        // (after a wait that gave up, the chunks that are left only meet the barriers, so that no
-        // warp waits there for good)
-        ok = ok && mbar_wait_bounded(&ctl.s_full[buf], (step >> 1) & 1u);
-        ok = __all_sync(0xffffffffu, ok);
-        float x[8];
-        if (ok) {
-          umma::fence_after();
-          const uint32_t sc = tmem + buf * Sh::kScoreCols + lane_base + 8 * group;
-          float lo[8];
-          ld8(sc, x);
-          ld8(sc + C, lo);
-          wait_ld(x, lo);
-          umma::fence_before();
-          __syncwarp();
-          arrive_if(&ctl.s_empty[buf], lane == 0);
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-            x[j] = fmaf(lo[j], 1.f / 16.f, x[j]) * (ctl.factor[8 * group + j] * ks);
-          // positions past the chunk's end or past the column's query's own are not seen
-          if (first + (i + 1) * kTile > min(last, seen0)) {
+        float ks_next = 0.f, vs_next = 0.f, x[8];
+        if (i < chunks) {
+          const int pos = first + i * kTile + token;
+          // what the next chunks need, on its way
+          if (pos + kTile < last) {
+            ks_next = prm.k_scale[scale_at(i + 1, page)];
+            vs_next = prm.v_scale[scale_at(i + 1, page)];
+          }
+          page = page_of(i + 2);
+          vs = pos < last ? vs : 0.f;
+          const float v_top = warp_peak(fabsf(vs));
+          if (lane == 0) ctl.v_peak[buf][group][w4] = v_top;
+          // (after a wait that gave up, the chunks that are left only meet the barriers, so that no
+          // warp waits there for good)
+          ok = ok && mbar_wait_bounded(&ctl.s_full[buf], (step >> 1) & 1u);
+          ok = __all_sync(0xffffffffu, ok);
+          if (ok) {
+            umma::fence_after();
+            const uint32_t sc = tmem + buf * Sh::kScoreCols + lane_base + 8 * group;
+            float lo[8];
+            ld8(sc, x);
+            ld8(sc + C, lo);
+            wait_ld(x, lo);
+            umma::fence_before();
+            __syncwarp();
+            arrive_if(&ctl.s_empty[buf], lane == 0);
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-              if (pos >= last || pos >= seen0 + query_of(j)) x[j] = -CUDART_INF_F;
-          }
-          // (all eight at once: with a store behind each they took 665 cycles, not 200)
-          float top[8];
+              x[j] = fmaf(lo[j], 1.f / 16.f, x[j]) * (ctl.factor[8 * group + j] * ks);
+            // positions past the chunk's end or past the column's query's own are not seen
+            if (first + (i + 1) * kTile > min(last, seen0)) {
 #pragma unroll
-          for (int j = 0; j < 8; ++j) top[j] = warp_peak(x[j]);
-          if (lane == 0) {
+              for (int j = 0; j < 8; ++j)
+                if (pos >= last || pos >= seen0 + query_of(j)) x[j] = -CUDART_INF_F;
+            }
+            // (all eight at once: with a store behind each they took 665 cycles, not 200)
+            float top[8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) ctl.peak[buf][8 * group + j][w4] = top[j];
+            for (int j = 0; j < 8; ++j) top[j] = warp_peak(x[j]);
+            if (lane == 0) {
+#pragma unroll
+              for (int j = 0; j < 8; ++j) ctl.peak[buf][8 * group + j][w4] = top[j];
+            }
           }
+          group_barrier<C / 8>(group);
         }
-        group_barrier<C / 8>(group);
         // the product before, which has had the time of a softmax (behind the weights, with buffers
         // of its own, it held more registers and was slower: 73 us against 65 for 64 chunks)
-        if (ok && i > 0) add_product(step - 1);
+        if (i > 0) add_product(step - 1);
+        if (i == chunks) break;
         if (ok) {
           float4 top[8];
 #pragma unroll
@@ -688,7 +728,6 @@ __global__ void __launch_bounds__(Shape<C>::kThreads, Shape<C>::kBlocks)
         ks = ks_next;
         vs = vs_next;
       }
-      if (chunks > 0) add_product(step - 1);
       // ----- the columns' results -----------------------------------------------------------
       // (sums of 8 columns over 32 lanes: half of the columns change sides at each of three steps)
       float part[4];
@@ -702,34 +741,42 @@ __global__ void __launch_bounds__(Shape<C>::kThreads, Shape<C>::kBlocks)
       part[0] += __shfl_xor_sync(0xffffffffu, part[0], 2);
       part[0] += __shfl_xor_sync(0xffffffffu, part[0], 1);
       if ((lane & 3) == 0) ctl.sum[8 * group + (lane >> 2 & 4) + (lane >> 2 & 2) + (lane >> 2 & 1)][w4] = part[0];
-      group_barrier<C / 8>(group);
-      if (ok) {
-        const bool direct = p.pieces == 1;
+      // Little code from here on: it runs once a piece, and the loop has pushed it out of the
+      // instruction caches (unrolled over the columns it took 5000 cycles, 1700 of them to fetch).
+      float* stage = reinterpret_cast<float*>(smem + Sh::kStage) + group * 8 * 128;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const int c = 8 * group + j;
-          if (c >= cols) break;
-          const float4 t = *reinterpret_cast<const float4*>(ctl.sum[c]);
-          const float total = (t.x + t.y) + (t.z + t.w);
-          const int64_t row = row_of(j);
-          const float m_nat = m[j] == kNothing ? -CUDART_INF_F : m[j] * 0.69314718055994530942f;
-          if (direct) {
-            const float inv = total > 0.f || total != total ? 1.f / total : 0.f;
-            static_cast<__nv_bfloat16*>(prm.out)[row * 128 + token] = __float2bfloat16_rn(acc[j] * inv);
-            if (token == 0) {
-              if (prm.lse != nullptr)
-                prm.lse[row] = m_nat == -CUDART_INF_F && total == total ? m_nat : m_nat + logf(total);
-              if (S > 1) prm.l_out[row * S] = -1.f;  // nothing to combine
-            }
-          } else {
-            prm.acc_out[(row * S + p.slot) * 128 + token] = acc[j];
-            if (token == 0) {
-              prm.m_out[row * S + p.slot] = m_nat;
-              prm.l_out[row * S + p.slot] = total;
-              // the sum after the last piece's ends the row's list
-              if (p.slot == 0 && p.pieces < S) prm.l_out[row * S + p.pieces] = -1.f;
-            }
-          }
+      for (int j = 0; j < 8; ++j) stage[j * 128 + token] = acc[j];
+      const bool direct = p.pieces == 1;
+      const int live_cols = min(8, cols - 8 * group);
+      group_barrier<C / 8>(group);
+      if (ok && token < live_cols) {  // a thread a column
+        const float4 t = *reinterpret_cast<const float4*>(ctl.sum[8 * group + token]);
+        const float total = (t.x + t.y) + (t.z + t.w), top = pick(m, token);  // (0, or 1 at least; or NaN)
+        const float m_nat = top == kNothing ? -CUDART_INF_F : top * 0.69314718055994530942f;
+        const int64_t row = row_of(token);
+        ctl.inverse[8 * group + token] = total == 0.f ? 0.f : 1.f / total;
+        if (direct) {
+          if (prm.lse != nullptr)
+            prm.lse[row] = m_nat == -CUDART_INF_F && total == total ? m_nat : m_nat + logf(total);
+          if (S > 1) prm.l_out[row * S] = -1.f;  // nothing to combine
+        } else {
+          prm.m_out[row * S + p.slot] = m_nat;
+          prm.l_out[row * S + p.slot] = total;
+          // the sum after the last piece's ends the row's list
+          if (p.slot == 0 && p.pieces < S) prm.l_out[row * S + p.pieces] = -1.f;
+        }
+      }
+      if (direct) group_barrier<C / 8>(group);  // the inverses
+#pragma unroll 1
+      for (int j = w4; j < live_cols && ok; j += 4) {  // a warp a column, a lane 4 channels
+        const float4 y = *reinterpret_cast<const float4*>(stage + j * 128 + 4 * lane);
+        const int64_t row = row_of(j);
+        if (direct) {
+          const float f = ctl.inverse[8 * group + j];
+          static_cast<uint2*>(prm.out)[row * 32 + lane] =
+              make_uint2(mma::pack_bf16(y.x * f, y.y * f), mma::pack_bf16(y.z * f, y.w * f));
+        } else {
+          reinterpret_cast<float4*>(prm.acc_out)[(row * S + p.slot) * 32 + lane] = y;
         }
       }
       group_barrier<C / 8>(group);  // (before the next piece's sums, where neither has chunks)
