@@ -11,6 +11,9 @@
  * are the producer's other forms.  Around the step: pa_rope_append writes a layer's new
  * keys and values into the pools, pa_tree_attention / pa_decode_step_tree verify drafted
  * trees, pa_accumulate_weights, pa_evict and pa_compact_cache shrink a cache.
+ * pa_rope_append_blocks and pa_block_attention / pa_decode_step_block are the append and the step
+ * of a block-scaled e4m3 cache, pa_verify_drafts keeps or rejects drafted tokens and draws the
+ * next one, and the pa_pages_* operators hand out, share, copy, free and compact pages.
  * Every entry point takes plain device pointers
  * and sizes, enqueues work on `stream` (a cudaStream_t passed as void*, NULL = the
  * legacy default stream) and returns without synchronising.  The step's own inputs
@@ -746,7 +749,9 @@ PA_API pa_status pa_evict(const int32_t* page_table, int64_t page_table_stride,
  * Powers of two, so a scale that grows costs earlier rows no bits but those that leave e4m3's
  * range at the small end.  Rows of a block behind the new ones are left as they are; their codes
  * have no meaning until they are written.  New rows must be finite, scales of blocks that are
- * continued finite and not negative.  Two requests must not write one block.
+ * continued finite and 0 or at least 2^-126.  Two requests must not write one block.
+ * max_q_len picks the kernel, too: up to 8 rows of a block go to a warp, so drafts are faster with
+ * their own length here than with a larger number.
  * rotary_dim 0: keys and queries are taken as they are (inv_freq, positions and, with num_q_heads
  * 0, q and q_out may be NULL).  Rows of q_out that no request covers, and of a request whose rows
  * are refused (more than max_q_len, outside [0, total_q), more than its cache_seqlens), are not

@@ -12,7 +12,13 @@
 // which leaves room for the blocks that its rows can touch, and a warp finds b by 32 probes a
 // round.  8 lanes take a row, each with two 16-byte pieces that hold whole pairs, 32 rows at
 // once; a thread keeps its token over all heads, so it computes its 8 sines once, keeps them in
-// registers for the query heads and in its own places of shared memory for the keys.
+// registers for the query heads and in its own places of shared memory for the keys.  Where requests
+// have few new rows a warp has a block and a share of its heads.
+//
+// Bound by latency when decoding (32 requests, 32 / 8 heads: 4.3 us of dependent loads, a find, the
+// sines and one round of rows) and by memory for prompts (8192 tokens: 39.6 us, 4.7 TB/s, 70 % of
+// the copy rate: a block's chain of load, reduction, barrier and store for each head and 32 warps an
+// SM leave gaps).
 #include "pa_common.cuh"
 #include "pa_internal.h"
 
@@ -20,7 +26,6 @@ namespace pa {
 namespace {
 
 constexpr int kFewThreads = 128;
-
 
 __device__ __forceinline__ void unpack(const uint4& w, float* x) {
   const uint32_t v[4] = {w.x, w.y, w.z, w.w};
@@ -559,11 +564,15 @@ cudaError_t launch_few(const RopeBlocksParams& p, bool interleaved, int64_t slot
 cudaError_t launch_rope_blocks(const RopeBlocksParams& p, bool interleaved, cudaStream_t stream, bool use_pdl) {
   const int block = 1 << p.block_shift;
   const int64_t slots = (static_cast<int64_t>(p.total_q) >> p.block_shift) + 2 * static_cast<int64_t>(p.bs);
-  // Up to 8 new rows a request on average: a warp for each block.
-  const int64_t few = p.bs;
-  if (p.total_q <= few) return launch_few<1, 1>(p, interleaved, slots, stream, use_pdl);
-  if (p.total_q <= 4 * few) return launch_few<4, 1>(p, interleaved, slots, stream, use_pdl);
-  if (p.total_q <= 8 * few) return launch_few<4, 2>(p, interleaved, slots, stream, use_pdl);
+  // The most new rows that a request can have, as far as the host knows: up to 8 a warp has a block
+  // (64 requests, 32 / 8 heads, scale blocks of 64: 4 rows each 6.4 us and 8 rows 8.5, by thread
+  // blocks 10.1 and 10.5).  Where it does not know, one a request on average is taken for decoding;
+  // more may be a prompt among decoding requests, whose blocks are long for a warp (31 with a row
+  // and one with 200: 11.2 us by thread blocks, 57 by warps).
+  const int most = p.max_q_len < p.total_q ? p.max_q_len : p.total_q;
+  if (most == 1 || p.total_q <= p.bs) return launch_few<1, 1>(p, interleaved, slots, stream, use_pdl);
+  if (most <= 4) return launch_few<4, 1>(p, interleaved, slots, stream, use_pdl);
+  if (most <= 8) return launch_few<4, 2>(p, interleaved, slots, stream, use_pdl);
   return block == 16   ? launch_many<128, 1>(p, interleaved, slots, stream, use_pdl)
          : block == 32 ? launch_many<256, 1>(p, interleaved, slots, stream, use_pdl)
          : block == 64 ? launch_many<256, 2>(p, interleaved, slots, stream, use_pdl)

@@ -471,3 +471,40 @@ def test_append_in_place_on_a_projection_and_grown_scales():
         # a code is exact through a halving until it leaves the normal range: then each of up to 9
         # halvings rounds to the smallest step, 2^-9, by half of it at most, halved by the later ones
         assert bool(((a - b).abs() <= torch.where(a.abs() < 2.0 ** -6, 2.0 ** -9, 0.0)).all())
+
+
+@pytest.mark.parametrize("q_lens,mql", [([1, 1, 1], 1), ([4, 1, 3], 4), ([1, 8, 5], 8), ([2, 7, 8], 8)])
+@pytest.mark.parametrize("page,block", [(16, 16), (64, 32), (128, 128)])
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_append_by_warps_and_by_thread_blocks_writes_the_same_bits(q_lens, mql, page, block, interleaved):
+    """max_q_len picks the kernel: with the drafts' own length warps have the blocks, with a
+    larger one thread blocks do."""
+    seqlens = [page + 5, 2 * page + 3, max(page // 2, 8)]
+    results = []
+    for most in (mql, 60):
+        c = BlockCache(seqlens, 2, page, block, 82)
+        for s in (c.ks, c.vs):
+            s.copy_(torch.exp2(-torch.randint(3, 12, s.shape, generator=c.g).float()))
+        c.to_device()
+        wide, positions, inv = append_inputs(c, q_lens, 6, 96, 82)
+        wide, positions = (torch.cat([x, x.new_zeros((60 - len(x),) + x.shape[1:])]) for x in (wide, positions))
+        q_out = run_append(c, q_lens, wide, positions, inv, 6, interleaved, 1.0, max_q_len=most)
+        results.append([x.view(torch.uint8).clone() for x in (q_out, c.d_k, c.d_v, c.d_ks, c.d_vs)])
+    for a, b in zip(*results):
+        assert torch.equal(a, b)
+
+
+def test_append_of_a_prompt_among_decoding_requests():
+    """Twenty requests with a row each and one with 130: every request's rows as by a call of its own."""
+    seqlens, q_lens = [40 + i for i in range(20)] + [150], [1] * 20 + [130]
+    c, d = (BlockCache(seqlens, 2, 64, 64, 83) for _ in range(2))
+    wide, positions, inv = append_inputs(c, q_lens, 4, 128, 83)
+    q_out = run_append(c, q_lens, wide, positions, inv, 4, False, 1.0)
+    at, table, n = 0, d.d_table, d.d_n
+    for b, rows in enumerate(q_lens):
+        d.d_table, d.d_n = table[b:b + 1], n[b:b + 1]
+        alone = run_append(d, [rows], wide[at:at + rows], positions[at:at + rows], inv, 4, False, 1.0)
+        assert torch.equal(q_out[at:at + rows].view(torch.int16), alone.view(torch.int16))
+        at += rows
+    for a, b in zip((c.d_k, c.d_v, c.d_ks, c.d_vs), (d.d_k, d.d_v, d.d_ks, d.d_vs)):
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
