@@ -27,6 +27,12 @@
 // to end in chunks of 128 tokens and cut into equal shares, one for each of the blocks that are
 // resident at once: ragged batches leave none idle, and only units that a cut falls into need
 // partials.
+//
+// Bound by memory with 8 columns: 32 requests of 8192 tokens, 32 / 8 heads, 83 us and 6.4 TB/s; 64
+// ragged ones up to 16K, 64 / 8 heads, 161 us and 6.7 TB/s.  With 16 and 32 columns by the softmax, whose
+// warps issue in 7 of 10 cycles: 1.7 us a chunk of 32 columns on an SM (16 requests of 8192 tokens,
+// 25 columns: 92 us, where memory would take 40), as long as two of 16 on its two blocks.  One
+// request of 1024 tokens: 8.5 us, launches and dependent latencies.
 #pragma once
 
 #include <math_constants.h>
@@ -283,7 +289,7 @@ struct Shape {
     alignas(16) float v_peak[2][C / 8][4];
     alignas(16) float sum[C][4];
     float inverse[C];
-    float factor[C];  // of a column's scores
+    alignas(16) float factor[C];  // of a column's scores
     Walk walk;
     uint32_t tmem;
     int abort, issued, empties;
@@ -583,13 +589,31 @@ __global__ void __launch_bounds__(Shape<C>::kThreads, Shape<C>::kBlocks)
         group_barrier<C / 8>(group);  // the group's factors
       }
 
-      float m[8], l[8], acc[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        m[j] = kNothing;
-        l[j] = 0.f;
-        acc[j] = 0.f;
+      // Columns that the tile leaves empty (short drafts among longer ones, groups that do not fill
+      // it): their four warps only keep the barriers' count, a chunk at a time, and leave the issue
+      // slots to the others.  What their columns of the products hold is of no use.
+      if (C > 8 && 8 * group >= cols) {
+        for (int i = 0; i < chunks; ++i, ++step) {
+          const uint32_t buf = step & 1u;
+          ok = ok && mbar_wait_bounded(&ctl.s_full[buf], (step >> 1) & 1u);
+          ok = __all_sync(0xffffffffu, ok);
+          arrive_if(&ctl.s_empty[buf], ok && lane == 0);
+          arrive_if(&ctl.p_full, ok && lane == 0);
+          ok = ok && mbar_wait_bounded(&ctl.o_full, step & 1u);
+          ok = __all_sync(0xffffffffu, ok);
+        }
+        continue;
       }
+
+      // (two columns an instruction wherever there is one: the schedulers are what bounds 16 and 32
+      // columns)
+      float m[8], m_mine = kNothing;  // (lane j of eight has column j's once more)
+      uint64_t l2[4], acc2[4];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) m[j] = kNothing;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) l2[k] = acc2[k] = umma::pair(0.f, 0.f);
+      const uint64_t sixteenth = umma::pair(1.f / 16.f, 1.f / 16.f);
       float v_down = 0.f;  // of the chunk before: what undoes its V scales' power of two
       auto add_product = [&](uint32_t at) {  // acc += the product of chunk `at`
         ok = ok && mbar_wait_bounded(&ctl.o_full, at & 1u);
@@ -602,9 +626,13 @@ __global__ void __launch_bounds__(Shape<C>::kThreads, Shape<C>::kBlocks)
         ld8(oc + C, h2);
         ld8(oc + 2 * C, h3);
         wait_ld(h1, h2, h3);
+        const uint64_t down = umma::pair(v_down, v_down);
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          acc[j] = fmaf(fmaf(fmaf(h3[j], 1.f / 16.f, h2[j]), 1.f / 16.f, h1[j]), v_down, acc[j]);
+        for (int k = 0; k < 4; ++k) {
+          const int j = 2 * k;
+          const uint64_t tail = umma::fma2(umma::pair(h3[j], h3[j + 1]), sixteenth, umma::pair(h2[j], h2[j + 1]));
+          acc2[k] = umma::fma2(umma::fma2(tail, sixteenth, umma::pair(h1[j], h1[j + 1])), down, acc2[k]);
+        }
         umma::fence_before();
       };
       for (int i = 0;; ++i, ++step) {
@@ -635,9 +663,16 @@ __global__ void __launch_bounds__(Shape<C>::kThreads, Shape<C>::kBlocks)
             umma::fence_before();
             __syncwarp();
             arrive_if(&ctl.s_empty[buf], lane == 0);
+            const uint64_t ks2 = umma::pair(ks, ks);
+            const ulonglong2* factors = reinterpret_cast<const ulonglong2*>(ctl.factor + 8 * group);
+            const ulonglong2 f01 = factors[0], f23 = factors[1];
+            const uint64_t f[4] = {f01.x, f01.y, f23.x, f23.y};
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-              x[j] = fmaf(lo[j], 1.f / 16.f, x[j]) * (ctl.factor[8 * group + j] * ks);
+            for (int k = 0; k < 4; ++k) {
+              const int j = 2 * k;
+              const uint64_t y = umma::fma2(umma::pair(lo[j], lo[j + 1]), sixteenth, umma::pair(x[j], x[j + 1]));
+              umma::unpair(umma::mul2(y, umma::mul2(f[k], ks2)), x[j], x[j + 1]);
+            }
             // positions past the chunk's end or past the column's query's own are not seen
             if (first + (i + 1) * kTile > min(last, seen0)) {
 #pragma unroll
@@ -660,37 +695,36 @@ __global__ void __launch_bounds__(Shape<C>::kThreads, Shape<C>::kBlocks)
         if (i > 0) add_product(step - 1);
         if (i == chunks) break;
         if (ok) {
-          float4 top[8];
-#pragma unroll
-          for (int j = 0; j < 8; ++j) top[j] = *reinterpret_cast<const float4*>(ctl.peak[buf][8 * group + j]);
+          // (lane j of eight looks after column j)
+          const float4 tm = *reinterpret_cast<const float4*>(ctl.peak[buf][8 * group + (lane & 7)]);
+          const float top = fmaxf(umma::max3(tm.x, tm.y, tm.z), fmaxf(tm.w, m_mine));
           const float4 tv = *reinterpret_cast<const float4*>(ctl.v_peak[buf][group]);
           // V scales times a power of two that brings the chunk's largest to [128, 256) (infinite: NaN)
           const float v_top = fmaxf(umma::max3(tv.x, tv.y, tv.z), tv.w);
           const int e = 7 - mma::float_exponent(v_top);
           const float lift = v_top < CUDART_INF_F ? vs * mma::pow2_clamped(e) : CUDART_NAN_F;
           v_down = mma::pow2_clamped(-e);
-          bool moved = false;
+          if (__any_sync(0xffffffffu, top != m_mine)) {  // (all threads of the group alike)
+            m_mine = top;
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            top[j].x = fmaxf(umma::max3(top[j].x, top[j].y, top[j].z), fmaxf(top[j].w, m[j]));
-            moved = moved || top[j].x != m[j];
-          }
-          if (moved) {  // (all threads alike)
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              const float alpha = mma::fast_exp2(m[j] - top[j].x);
-              m[j] = top[j].x;
-              acc[j] *= alpha;
-              l[j] *= alpha;
+            for (int k = 0; k < 4; ++k) {
+              const float m0 = __shfl_sync(0xffffffffu, top, 2 * k), m1 = __shfl_sync(0xffffffffu, top, 2 * k + 1);
+              const uint64_t alpha = umma::pair(mma::fast_exp2(m[2 * k] - m0), mma::fast_exp2(m[2 * k + 1] - m1));
+              m[2 * k] = m0;
+              m[2 * k + 1] = m1;
+              acc2[k] = umma::mul2(acc2[k], alpha);
+              l2[k] = umma::mul2(l2[k], alpha);
             }
           }
-          const uint64_t lift2 = umma::pair(lift, lift);
+          const uint64_t lift2 = umma::pair(lift, lift), minus = umma::pair(-1.f, -1.f);
 #pragma unroll
-          for (int j = 0; j < 8; j += 2) {
-            const float p0 = mma::fast_exp2(x[j] - m[j]), p1 = mma::fast_exp2(x[j + 1] - m[j + 1]);
-            l[j] += p0;
-            l[j + 1] += p1;
-            umma::unpair(umma::mul2(umma::pair(p0, p1), lift2), x[j], x[j + 1]);
+          for (int k = 0; k < 4; ++k) {
+            const int j = 2 * k;
+            float d0, d1;  // x - m
+            umma::unpair(umma::fma2(umma::pair(m[j], m[j + 1]), minus, umma::pair(x[j], x[j + 1])), d0, d1);
+            const uint64_t e2 = umma::pair(mma::fast_exp2(d0), mma::fast_exp2(d1));
+            l2[k] = umma::add2(l2[k], e2);
+            umma::unpair(umma::mul2(e2, lift2), x[j], x[j + 1]);
           }
           // rounded to fp16 (11 bits), then cut into pieces of 4 bits, exactly
           uint32_t w[4];
@@ -729,6 +763,12 @@ __global__ void __launch_bounds__(Shape<C>::kThreads, Shape<C>::kBlocks)
         vs = vs_next;
       }
       // ----- the columns' results -----------------------------------------------------------
+      float l[8], acc[8];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        umma::unpair(l2[k], l[2 * k], l[2 * k + 1]);
+        umma::unpair(acc2[k], acc[2 * k], acc[2 * k + 1]);
+      }
       // (sums of 8 columns over 32 lanes: half of the columns change sides at each of three steps)
       float part[4];
 #pragma unroll
