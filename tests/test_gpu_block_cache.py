@@ -508,3 +508,16 @@ def test_append_of_a_prompt_among_decoding_requests():
         at += rows
     for a, b in zip((c.d_k, c.d_v, c.d_ks, c.d_vs), (d.d_k, d.d_v, d.d_ks, d.d_vs)):
         assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+
+
+@pytest.mark.parametrize("splits", [0, 1, 4])
+@pytest.mark.parametrize("q_lens,hq,hkv", [([5, 1, 1, 2, 4, 5], 10, 2), ([1, 8, 2, 10, 7, 1], 5, 1),
+                                           ([2, 1, 0, 1, 2, 1], 16, 1), ([3, 1, 2, 1, 1, 3], 20, 2)])
+def test_tiles_with_empty_columns_between_full_ones(q_lens, hq, hkv, splits):
+    """Short drafts among longer ones and tiles of a remainder: columns 8, 16 or 24 to 31 of a
+    tile are empty for some pieces of a block's share and not for the next."""
+    seqlens = [300, 900, 2, 700, 129, 2000]
+    c = BlockCache(seqlens, hkv, 64, 32, 84)
+    q = torch.randn((sum(q_lens), hq, 128), generator=c.g).to(torch.bfloat16)
+    out, lse = attend(c, q.cuda(), q_lens, num_splits=splits)
+    check(out, lse, R.attention(q, c.k, c.v, c.ks, c.vs, c.table, seqlens, q_lens, SCALE))
