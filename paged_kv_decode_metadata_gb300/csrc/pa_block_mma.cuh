@@ -22,17 +22,19 @@
 //   warps 0 .. C/2 - 1   softmax and sums, four for each 8 columns
 //   then one each        TMA: a ring of 16 KiB tiles, K and V in turn, running ahead into the
 //                        next piece; K Q^T (two score buffers: a chunk ahead of the softmax);
-//                        V^T P^T
+//                        V^T P^T; the scales, which arrive together with a chunk's scores (so
+//                        that the softmax warps neither find them nor wait for them)
 // A unit of work is a tile of columns of one (request, kv head).  The batch's units are laid end
 // to end in chunks of 128 tokens and cut into equal shares, one for each of the blocks that are
 // resident at once: ragged batches leave none idle, and only units that a cut falls into need
 // partials.
 //
 // Bound by memory with 8 columns: 32 requests of 8192 tokens, 32 / 8 heads, 83 us and 6.4 TB/s; 64
-// ragged ones up to 16K, 64 / 8 heads, 161 us and 6.7 TB/s.  With 16 and 32 columns by the softmax, whose
-// warps issue in 7 of 10 cycles: 1.7 us a chunk of 32 columns on an SM (16 requests of 8192 tokens,
-// 25 columns: 92 us, where memory would take 40), as long as two of 16 on its two blocks.  One
-// request of 1024 tokens: 8.5 us, launches and dependent latencies.
+// ragged ones up to 16K, 64 / 8 heads, 161 us and 6.7 TB/s.  With 16 and 32 columns by the softmax
+// warps' instructions: 1.5 us a chunk of 32 columns on an SM (16 requests of 8192 tokens, 25 columns: 83
+// us, where memory would take 40; with the scales found by the softmax warps 93), nearly as long as two
+// of 16 on its two blocks.  One request of 1024 tokens: 8.3 us, launches and dependent latencies;
+// short contexts by the same latencies once a unit (256 requests of 128 tokens: 30 us, memory 10).
 #pragma once
 
 #include <math_constants.h>
@@ -249,7 +251,8 @@ template <int C>
 struct Shape {
   static constexpr int kSoftmaxWarps = C / 2;
   static constexpr int kTmaWarp = kSoftmaxWarps, kScoreWarp = kTmaWarp + 1, kOutWarp = kTmaWarp + 2;
-  static constexpr int kThreads = 32 * (kOutWarp + 2);  // (a warpgroup of these, one idle)
+  static constexpr int kScaleWarp = kTmaWarp + 3;
+  static constexpr int kThreads = 32 * (kScaleWarp + 1);  // (a warpgroup of these)
   // registers a thread: of the launch, then of the softmax warps and the others
   static constexpr int kLaunchRegs = C == 8 ? 128 : C == 16 ? 80 : 96;
   static constexpr int kSoftmaxRegs = C == 8 ? 168 : C == 16 ? 96 : 104, kOtherRegs = C == 8 ? 80 : C == 16 ? 48 : 64;
@@ -283,10 +286,13 @@ struct Shape {
   struct alignas(16) Control {
     uint64_t full[kSlots], empty[kSlots];
     uint64_t q_full, s_full[2], s_empty[2], p_full, o_full, drained[2];
-    // per warp of four: a column's largest score, the largest V scale; of even and of odd chunks
-    // (a warp may write the next chunk's while another still reads this one's)
+    // per warp of four: a column's largest score; of even and of odd chunks (a warp may write the next
+    // chunk's while another still reads this one's)
     alignas(16) float peak[2][C][4];
-    alignas(16) float v_peak[2][C / 8][4];
+    // a chunk's scales, block by block; the power of two that brings its largest V scale to [128, 256)
+    // (NaN: an infinite one), and what undoes it
+    float k_scales[2][kTile / 16], v_scales[2][kTile / 16];
+    float v_up[2], v_down[2];
     alignas(16) float sum[C][4];
     float inverse[C];
     alignas(16) float factor[C];  // of a column's scores
@@ -445,7 +451,7 @@ __global__ void __launch_bounds__(Shape<C>::kThreads, Shape<C>::kBlocks)
     mbar_init(&ctl.p_full, Sh::kSoftmaxWarps);
     mbar_init(&ctl.o_full, 1);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&ctl.s_full[i], 1);
+      mbar_init(&ctl.s_full[i], 2);  // the scores and the scales
       mbar_init(&ctl.s_empty[i], Sh::kSoftmaxWarps);
       mbar_init(&ctl.drained[i], 1);
     }
@@ -514,8 +520,7 @@ __global__ void __launch_bounds__(Shape<C>::kThreads, Shape<C>::kBlocks)
     umma::registers_up<Sh::kSoftmaxRegs>();
     const int group = warp >> 2, token = tid & 127, w4 = warp & 3;  // 8 columns, a row of the tile
     const uint32_t lane_base = static_cast<uint32_t>(w4) << 21;     // lane 32 (warp % 4)
-    const int blocks = P >> prm.block_shift;                        // scales of a page and head
-    uint32_t step = 0;                                              // chunks of the pieces before
+    uint32_t step = 0;  // chunks of the pieces before
     bool ok = true;
     // the queries of the group's columns, a byte each (no division in the loops)
     uint32_t queries[2] = {0, 0};
@@ -530,17 +535,6 @@ __global__ void __launch_bounds__(Shape<C>::kThreads, Shape<C>::kBlocks)
       auto row_of = [&](int j) {  // of column 8 group + j
         return row0 + static_cast<int64_t>(query_of(j)) * (prm.num_q_heads - G) + 8 * group + j;
       };
-      const int32_t* pt = prm.page_table + static_cast<int64_t>(p.b) * prm.page_table_stride;
-      auto page_of = [&](int i) -> int {
-        const int pos = first + i * kTile + token;
-        return pos < last ? pt[pos >> page_shift] : 0;
-      };
-      auto scale_at = [&](int i, int page) -> int64_t {
-        const int row = (first + i * kTile + token) & (P - 1);
-        if (page < 0 || page >= prm.num_pages) page = 0;  // (the TMA warp reports it)
-        return (static_cast<int64_t>(page) * prm.num_kv_heads + p.kvh) * blocks + (row >> prm.block_shift);
-      };
-      int page = page_of(0);
       // ----- the query rows' pieces: a warp has two columns, a lane 4 channels ----------------
       uint2 rows[2];
 #pragma unroll
@@ -550,12 +544,6 @@ __global__ void __launch_bounds__(Shape<C>::kThreads, Shape<C>::kBlocks)
                       ? reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(prm.q) + row_of(2 * w4 + u) * 128)[lane]
                       : make_uint2(0u, 0u);
       }
-      float ks = 0.f, vs = 0.f;  // a thread's token's scales, a chunk ahead; its page two ahead
-      if (first + token < last) {
-        ks = prm.k_scale[scale_at(0, page)];
-        vs = prm.v_scale[scale_at(0, page)];
-      }
-      page = page_of(1);
       if (chunks > 0) {
 #pragma unroll 1
         for (int u = 0; u < 2; ++u) {
@@ -637,18 +625,9 @@ __global__ void __launch_bounds__(Shape<C>::kThreads, Shape<C>::kBlocks)
       };
       for (int i = 0;; ++i, ++step) {
         const uint32_t buf = step & 1u;
-        float ks_next = 0.f, vs_next = 0.f, x[8];
+        float x[8], vs = 0.f, up = 0.f, down = 0.f;
         if (i < chunks) {
           const int pos = first + i * kTile + token;
-          // what the next chunks need, on its way
-          if (pos + kTile < last) {
-            ks_next = prm.k_scale[scale_at(i + 1, page)];
-            vs_next = prm.v_scale[scale_at(i + 1, page)];
-          }
-          page = page_of(i + 2);
-          vs = pos < last ? vs : 0.f;
-          const float v_top = warp_peak(fabsf(vs));
-          if (lane == 0) ctl.v_peak[buf][group][w4] = v_top;
           // (after a wait that gave up, the chunks that are left only meet the barriers, so that no
           // warp waits there for good)
           ok = ok && mbar_wait_bounded(&ctl.s_full[buf], (step >> 1) & 1u);
@@ -659,6 +638,10 @@ __global__ void __launch_bounds__(Shape<C>::kThreads, Shape<C>::kBlocks)
             float lo[8];
             ld8(sc, x);
             ld8(sc + C, lo);
+            const float ks = ctl.k_scales[buf][token >> prm.block_shift];
+            vs = pos < last ? ctl.v_scales[buf][token >> prm.block_shift] : 0.f;
+            up = ctl.v_up[buf];
+            down = ctl.v_down[buf];
             wait_ld(x, lo);
             umma::fence_before();
             __syncwarp();
@@ -698,12 +681,8 @@ __global__ void __launch_bounds__(Shape<C>::kThreads, Shape<C>::kBlocks)
           // (lane j of eight looks after column j)
           const float4 tm = *reinterpret_cast<const float4*>(ctl.peak[buf][8 * group + (lane & 7)]);
           const float top = fmaxf(umma::max3(tm.x, tm.y, tm.z), fmaxf(tm.w, m_mine));
-          const float4 tv = *reinterpret_cast<const float4*>(ctl.v_peak[buf][group]);
-          // V scales times a power of two that brings the chunk's largest to [128, 256) (infinite: NaN)
-          const float v_top = fmaxf(umma::max3(tv.x, tv.y, tv.z), tv.w);
-          const int e = 7 - mma::float_exponent(v_top);
-          const float lift = v_top < CUDART_INF_F ? vs * mma::pow2_clamped(e) : CUDART_NAN_F;
-          v_down = mma::pow2_clamped(-e);
+          const float lift = vs * up;
+          v_down = down;
           if (__any_sync(0xffffffffu, top != m_mine)) {  // (all threads of the group alike)
             m_mine = top;
 #pragma unroll
@@ -759,8 +738,6 @@ __global__ void __launch_bounds__(Shape<C>::kThreads, Shape<C>::kBlocks)
           __syncwarp();
           arrive_if(&ctl.p_full, ok && lane == 0);
         }
-        ks = ks_next;
-        vs = vs_next;
       }
       // ----- the columns' results -----------------------------------------------------------
       float l[8], acc[8];
@@ -940,7 +917,49 @@ __global__ void __launch_bounds__(Shape<C>::kThreads, Shape<C>::kBlocks)
     }
     __syncwarp();
   } else {
+    // ======================= the scales ===================================================
     umma::registers_down<Sh::kOtherRegs>();
+    // lanes 0 .. 15 have the K scales of up to eight blocks of a chunk, the others V's; a lane's page is asked
+    // for two chunks ahead, its scale one
+    const int blocks = P >> prm.block_shift, block = lane & 15;
+    const bool is_v = lane >= 16, mine = block < kTile >> prm.block_shift;
+    const float* scales = is_v ? prm.v_scale : prm.k_scale;
+    uint32_t step = 0;
+    bool ok = true;
+    while (ok && walk.next(prm, p)) {
+      const int first = first_of(p), last = last_of(p);
+      const int chunks = (last - first + kTile - 1) / kTile;
+      const int32_t* pt = prm.page_table + static_cast<int64_t>(p.b) * prm.page_table_stride;
+      auto pos_of = [&](int i) { return first + i * kTile + (block << prm.block_shift); };
+      auto page_of = [&](int i) -> int { return mine && pos_of(i) < last ? pt[pos_of(i) >> page_shift] : 0; };
+      auto scale_of = [&](int i, int page) -> float {
+        if (!mine || pos_of(i) >= last) return 0.f;
+        if (page < 0 || page >= prm.num_pages) page = 0;  // (the TMA warp reports it)
+        return scales[(static_cast<int64_t>(page) * prm.num_kv_heads + p.kvh) * blocks +
+                      ((pos_of(i) & (P - 1)) >> prm.block_shift)];
+      };
+      float next = scale_of(0, page_of(0));
+      int page = page_of(1);
+      for (int i = 0; i < chunks && ok; ++i, ++step) {
+        const uint32_t buf = step & 1u;
+        const float scale = next;
+        next = scale_of(i + 1, page);
+        page = page_of(i + 2);
+        if (step >= 2) ok = mbar_wait_bounded(&ctl.s_empty[buf], ((step >> 1) - 1) & 1u);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        const float v_top = warp_peak(is_v ? fabsf(scale) : 0.f);
+        const int e = 7 - mma::float_exponent(v_top);
+        if (mine) (is_v ? ctl.v_scales : ctl.k_scales)[buf][block] = scale;
+        if (lane == 0) {
+          ctl.v_up[buf] = v_top < CUDART_INF_F ? mma::pow2_clamped(e) : CUDART_NAN_F;
+          ctl.v_down[buf] = mma::pow2_clamped(-e);
+        }
+        __syncwarp();
+        arrive_if(&ctl.s_full[buf], lane == 0);
+      }
+    }
+    if (!ok && lane == 0) give_up();
   }
   // (not earlier: with the next launches' blocks waiting beside them these took 137 us, not 95)
   trigger_dependents();
