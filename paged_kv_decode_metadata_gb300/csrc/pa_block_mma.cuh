@@ -289,10 +289,10 @@ struct Shape {
     // per warp of four: a column's largest score; of even and of odd chunks (a warp may write the next
     // chunk's while another still reads this one's)
     alignas(16) float peak[2][C][4];
-    // a chunk's scales, block by block; the power of two that brings its largest V scale to [128, 256)
-    // (NaN: an infinite one), and what undoes it
+    // a chunk's scales, block by block, V's times the power of two that brings the largest of them to
+    // [128, 256) (all NaN where it is infinite); and what undoes that
     float k_scales[2][kTile / 16], v_scales[2][kTile / 16];
-    float v_up[2], v_down[2];
+    float v_down[2];
     alignas(16) float sum[C][4];
     float inverse[C];
     alignas(16) float factor[C];  // of a column's scores
@@ -625,7 +625,7 @@ __global__ void __launch_bounds__(Shape<C>::kThreads, Shape<C>::kBlocks)
       };
       for (int i = 0;; ++i, ++step) {
         const uint32_t buf = step & 1u;
-        float x[8], vs = 0.f, up = 0.f, down = 0.f;
+        float x[8], lift = 0.f, down = 0.f;
         if (i < chunks) {
           const int pos = first + i * kTile + token;
           // (after a wait that gave up, the chunks that are left only meet the barriers, so that no
@@ -639,8 +639,7 @@ __global__ void __launch_bounds__(Shape<C>::kThreads, Shape<C>::kBlocks)
             ld8(sc, x);
             ld8(sc + C, lo);
             const float ks = ctl.k_scales[buf][token >> prm.block_shift];
-            vs = pos < last ? ctl.v_scales[buf][token >> prm.block_shift] : 0.f;
-            up = ctl.v_up[buf];
+            lift = pos < last ? ctl.v_scales[buf][token >> prm.block_shift] : 0.f;
             down = ctl.v_down[buf];
             wait_ld(x, lo);
             umma::fence_before();
@@ -681,7 +680,6 @@ __global__ void __launch_bounds__(Shape<C>::kThreads, Shape<C>::kBlocks)
           // (lane j of eight looks after column j)
           const float4 tm = *reinterpret_cast<const float4*>(ctl.peak[buf][8 * group + (lane & 7)]);
           const float top = fmaxf(umma::max3(tm.x, tm.y, tm.z), fmaxf(tm.w, m_mine));
-          const float lift = vs * up;
           v_down = down;
           if (__any_sync(0xffffffffu, top != m_mine)) {  // (all threads of the group alike)
             m_mine = top;
@@ -950,11 +948,9 @@ __global__ void __launch_bounds__(Shape<C>::kThreads, Shape<C>::kBlocks)
         if (!ok) break;
         const float v_top = warp_peak(is_v ? fabsf(scale) : 0.f);
         const int e = 7 - mma::float_exponent(v_top);
-        if (mine) (is_v ? ctl.v_scales : ctl.k_scales)[buf][block] = scale;
-        if (lane == 0) {
-          ctl.v_up[buf] = v_top < CUDART_INF_F ? mma::pow2_clamped(e) : CUDART_NAN_F;
-          ctl.v_down[buf] = mma::pow2_clamped(-e);
-        }
+        const float up = v_top < CUDART_INF_F ? mma::pow2_clamped(e) : CUDART_NAN_F;
+        if (mine) (is_v ? ctl.v_scales : ctl.k_scales)[buf][block] = is_v ? scale * up : scale;
+        if (lane == 0) ctl.v_down[buf] = mma::pow2_clamped(-e);
         __syncwarp();
         arrive_if(&ctl.s_full[buf], lane == 0);
       }
