@@ -31,8 +31,8 @@
 //
 // Bound by memory with 8 columns: 32 requests of 8192 tokens, 32 / 8 heads, 83 us and 6.4 TB/s; 64
 // ragged ones up to 16K, 64 / 8 heads, 161 us and 6.7 TB/s.  With 16 and 32 columns by the softmax
-// warps' instructions: 1.5 us a chunk of 32 columns on an SM (16 requests of 8192 tokens, 25 columns: 83
-// us, where memory would take 40; with the scales found by the softmax warps 93), nearly as long as two
+// warps' instructions: 1.5 us a chunk of 32 columns on an SM (16 requests of 8192 tokens, 25 columns: 82
+// us, where memory would take 40; with the scales found by the softmax warps 92), nearly as long as two
 // of 16 on its two blocks.  One request of 1024 tokens: 8.3 us, launches and dependent latencies;
 // short contexts by the same latencies once a unit (256 requests of 128 tokens: 30 us, memory 10).
 #pragma once
