@@ -24,6 +24,8 @@
 //                        next piece; K Q^T (two score buffers: a chunk ahead of the softmax);
 //                        V^T P^T; the scales, which arrive together with a chunk's scores (so
 //                        that the softmax warps neither find them nor wait for them)
+// One warp, TMA's, walks the block's share and hands its pieces to the others: code that runs once a
+// piece comes from beyond the instruction caches, so there is little of it.
 // A unit of work is a tile of columns of one (request, kv head).  The batch's units are laid end
 // to end in chunks of 128 tokens and cut into equal shares, one for each of the blocks that are
 // resident at once: ragged batches leave none idle, and only units that a cut falls into need
@@ -31,10 +33,10 @@
 //
 // Bound by memory with 8 columns: 32 requests of 8192 tokens, 32 / 8 heads, 83 us and 6.4 TB/s; 64
 // ragged ones up to 16K, 64 / 8 heads, 161 us and 6.7 TB/s.  With 16 and 32 columns by the softmax
-// warps' instructions: 1.5 us a chunk of 32 columns on an SM (16 requests of 8192 tokens, 25 columns: 82
-// us, where memory would take 40; with the scales found by the softmax warps 92), nearly as long as two
-// of 16 on its two blocks.  One request of 1024 tokens: 8.3 us, launches and dependent latencies;
-// short contexts by the same latencies once a unit (256 requests of 128 tokens: 30 us, memory 10).
+// warps' instructions: 1.3 us a chunk of 32 columns on an SM (16 requests of 8192 tokens, 25 columns: 73
+// us, where memory would take 40; with the scales found by the softmax warps 92, with every warp
+// walking for itself 82).  One request of 1024 tokens: 8.4 us, launches and dependent latencies; short
+// contexts by the same latencies once a unit (256 requests of 128 tokens: 28 us, memory 10).
 #pragma once
 
 #include <math_constants.h>
@@ -57,10 +59,18 @@ struct Piece {
   int slot, pieces;  // which of the unit's pieces this is, and how many it has
 };
 
+// A piece as the walking warp hands it to the others: tokens [first, last) of request b, of which the
+// tile's first query sees those below `seen` (query i: i more).
+struct alignas(16) Job {
+  int first, last, seen, cols;  // (0 columns: there are no more pieces)
+  int b, kvh, slot, pieces;
+  long long row0;  // the first column's row of q and of the results
+};
+
 // The batch as one line, unit after unit (by request, kv head, tile), a place for each chunk and
 // kUnitCost before them for what a unit costs beside them: block i takes [i share, (i + 1) share),
-// or, where units are not cut, the units that start there.  Every warp walks its block's share by
-// itself.  (The host keeps the line's length within 31 bits.)
+// or, where units are not cut, the units that start there.  (The host keeps the line's length within
+// 31 bits.)
 // (Measured at 0 / 1 / 2 / 4: 64 ragged requests to 16K, 64 / 8 heads, 196 / 175 / 174 / 174 us; 8 ragged
 // chains to 4001 36 / 31 / 24 / 24 us.)
 constexpr int kUnitCost = 2;
@@ -261,6 +271,7 @@ struct Shape {
   static constexpr int kOutCols = (3 * C + 15) / 16 * 16;
   static constexpr int kTmemCols = C == 8 ? 64 : C == 16 ? 128 : 256;
   static_assert(2 * kScoreCols + kOutCols <= kTmemCols, "tensor memory");
+  static constexpr int kJobs = 4;  // pieces handed over and not yet taken by every warp
   // Tiles in flight: 8 an SM stream best (12 and 6: 64 requests of 16K 329 and 317-321 us against 314-316),
   // and two blocks of them with four rather than three with two.
   static constexpr int kSlots = C <= 16 ? 4 : 10;
@@ -288,7 +299,7 @@ struct Shape {
     uint64_t q_full, s_full[2], s_empty[2], p_full, o_full, drained[2];
     // per warp of four: a column's largest score; of even and of odd chunks (a warp may write the next
     // chunk's while another still reads this one's)
-    alignas(16) float peak[2][C][4];
+    alignas(16) float peak[2][C / 8][4][8];
     // a chunk's scales, block by block, V's times the power of two that brings the largest of them to
     // [128, 256) (all NaN where it is infinite); and what undoes that
     float k_scales[2][kTile / 16], v_scales[2][kTile / 16];
@@ -296,7 +307,8 @@ struct Shape {
     alignas(16) float sum[C][4];
     float inverse[C];
     alignas(16) float factor[C];  // of a column's scores
-    Walk walk;
+    Job jobs[kJobs];
+    uint64_t job_full[kJobs], job_empty[kJobs];
     uint32_t tmem;
     int abort, issued, empties;
   };
@@ -425,6 +437,25 @@ __device__ __forceinline__ void group_barrier(int group) {
   }
 }
 
+// Whether `yes` holds in all of their threads.
+template <int kBarrier>
+__device__ __forceinline__ bool barrier_all(bool yes) {
+  uint32_t all = yes;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %0, 0;\n\t"
+      "bar.red.and.pred q, %1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "+r"(all)
+      : "n"(kBarrier)
+      : "memory");
+  return all != 0;
+}
+template <int kGroups>
+__device__ __forceinline__ bool group_all(int group, bool yes) {
+  if (kGroups == 1 || group == 0) return barrier_all<1>(yes);
+  if (kGroups == 2 || group == 1) return barrier_all<2>(yes);
+  return group == 2 ? barrier_all<3>(yes) : barrier_all<4>(yes);
+}
+
 template <int C>
 __global__ void __launch_bounds__(Shape<C>::kThreads, Shape<C>::kBlocks)
     block_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
@@ -455,6 +486,10 @@ __global__ void __launch_bounds__(Shape<C>::kThreads, Shape<C>::kBlocks)
       mbar_init(&ctl.s_empty[i], Sh::kSoftmaxWarps);
       mbar_init(&ctl.drained[i], 1);
     }
+    for (int i = 0; i < Sh::kJobs; ++i) {
+      mbar_init(&ctl.job_full[i], 1);
+      mbar_init(&ctl.job_empty[i], Sh::kSoftmaxWarps + 3);
+    }
     ctl.abort = 0;
     ctl.issued = 0;
     fence_barrier_init();
@@ -471,19 +506,15 @@ __global__ void __launch_bounds__(Shape<C>::kThreads, Shape<C>::kBlocks)
   const uint32_t out_col = tmem + 2 * Sh::kScoreCols;
   grid_dependency_wait();
 
-  // The TMA warp finds the block's share and goes on, the others take it over.
+  // The TMA warp finds the block's share and goes on.
   Walk walk;
   if (warp == Sh::kTmaWarp) {
     const bool empties = walk.start(prm, lane);
-    if (lane == 0) {
-      ctl.walk = walk;
-      ctl.empties = empties;
-    }
+    if (lane == 0) ctl.empties = empties;
     __syncwarp();
     asm volatile("bar.arrive 5, %0;" ::"n"(Sh::kThreads) : "memory");
   } else {
     asm volatile("bar.sync 5, %0;" ::"n"(Sh::kThreads) : "memory");
-    walk = ctl.walk;
     if (ctl.empties) {  // requests with queries and an empty cache
       const int at = tid < Sh::kTmaWarp * 32 ? tid : tid - 32;
       constexpr int kOthers = Sh::kThreads - 32;
@@ -501,18 +532,24 @@ __global__ void __launch_bounds__(Shape<C>::kThreads, Shape<C>::kBlocks)
       }
     }
   }
-  Piece p;
   auto give_up = [&]() {
     record_error(prm.err, kErrWaitTimeout);
     *abort_flag = 1;
   };
-  // what a piece covers: tokens [first, last), its tile's queries
-  auto first_of = [&](const Piece& w) { return w.c0 * kTile; };
-  auto live_of = [&](const Piece& w) { return min(w.q_len - w.tile * prm.tile_queries, prm.tile_queries); };
-  // positions that the tile's first query sees (query i: i more)
-  auto seen_of = [&](const Piece& w) { return w.n - w.q_len + w.tile * prm.tile_queries + 1; };
-  auto last_of = [&](const Piece& w) {
-    return max(first_of(w), min(min(w.n, w.c1 * kTile), seen_of(w) + live_of(w) - 1));
+  auto chunks_of = [&](const Job& w) { return (w.last - w.first + kTile - 1) / kTile; };
+  // The next piece, for a warp that is not TMA's (`lone`: for one of its threads).  False where the wait for
+  // it gave up.
+  uint32_t taken = 0;
+  auto take = [&](Job& w, bool lone) {
+    const uint32_t s = taken % Sh::kJobs;
+    bool got = mbar_wait_bounded(&ctl.job_full[s], (taken / Sh::kJobs) & 1u);
+    if (!lone) got = __all_sync(0xffffffffu, got);
+    if (!got) return false;
+    w = ctl.jobs[s];
+    if (!lone) __syncwarp();
+    arrive_if(&ctl.job_empty[s], lone || lane == 0);
+    ++taken;
+    return true;
   };
 
   if (warp < Sh::kSoftmaxWarps) {
@@ -527,13 +564,18 @@ __global__ void __launch_bounds__(Shape<C>::kThreads, Shape<C>::kBlocks)
 #pragma unroll
     for (int j = 0; j < 8; ++j) queries[j >> 2] |= static_cast<uint32_t>((8 * group + j) / G) << (8 * (j & 3));
     auto query_of = [&](int j) { return static_cast<int>((j & 4 ? queries[1] : queries[0]) >> (8 * (j & 3)) & 0xffu); };
-    while (walk.next(prm, p)) {
-      const int first = first_of(p), last = last_of(p), seen0 = seen_of(p);
-      const int chunks = (last - first + kTile - 1) / kTile;
-      const int cols = live_of(p) * G;
-      const int64_t row0 = (static_cast<int64_t>(p.q_begin) + p.tile * prm.tile_queries) * prm.num_q_heads + p.kvh * G;
+    Job p;
+    while (true) {
+      // (all warps of a group go on or none does: none may wait for another that has gone; and the sums of the
+      // piece before have been read)
+      const bool got = group_all<C / 8>(group, take(p, false));
+      ok = ok && got;
+      if (!got || p.cols == 0) break;
+      const int first = p.first, last = p.last, seen0 = p.seen;
+      const int chunks = chunks_of(p);
+      const int cols = p.cols;
       auto row_of = [&](int j) {  // of column 8 group + j
-        return row0 + static_cast<int64_t>(query_of(j)) * (prm.num_q_heads - G) + 8 * group + j;
+        return p.row0 + static_cast<int64_t>(query_of(j)) * (prm.num_q_heads - G) + 8 * group + j;
       };
       // ----- the query rows' pieces: a warp has two columns, a lane 4 channels ----------------
       uint2 rows[2];
@@ -666,8 +708,9 @@ __global__ void __launch_bounds__(Shape<C>::kThreads, Shape<C>::kBlocks)
 #pragma unroll
             for (int j = 0; j < 8; ++j) top[j] = warp_peak(x[j]);
             if (lane == 0) {
-#pragma unroll
-              for (int j = 0; j < 8; ++j) ctl.peak[buf][8 * group + j][w4] = top[j];
+              float4* at = reinterpret_cast<float4*>(ctl.peak[buf][group][w4]);
+              at[0] = make_float4(top[0], top[1], top[2], top[3]);
+              at[1] = make_float4(top[4], top[5], top[6], top[7]);
             }
           }
           group_barrier<C / 8>(group);
@@ -678,8 +721,8 @@ __global__ void __launch_bounds__(Shape<C>::kThreads, Shape<C>::kBlocks)
         if (i == chunks) break;
         if (ok) {
           // (lane j of eight looks after column j)
-          const float4 tm = *reinterpret_cast<const float4*>(ctl.peak[buf][8 * group + (lane & 7)]);
-          const float top = fmaxf(umma::max3(tm.x, tm.y, tm.z), fmaxf(tm.w, m_mine));
+          const float* tm = &ctl.peak[buf][group][0][lane & 7];
+          const float top = fmaxf(umma::max3(tm[0], tm[8], tm[16]), fmaxf(tm[24], m_mine));
           v_down = down;
           if (__any_sync(0xffffffffu, top != m_mine)) {  // (all threads of the group alike)
             m_mine = top;
@@ -794,7 +837,6 @@ __global__ void __launch_bounds__(Shape<C>::kThreads, Shape<C>::kBlocks)
           reinterpret_cast<float4*>(prm.acc_out)[(row * S + p.slot) * 32 + lane] = y;
         }
       }
-      group_barrier<C / 8>(group);  // (before the next piece's sums, where neither has chunks)
     }
     if (!ok && lane == 0) give_up();
     umma::fence_before();
@@ -804,11 +846,36 @@ __global__ void __launch_bounds__(Shape<C>::kThreads, Shape<C>::kBlocks)
     const int box_shift = min(page_shift, 6), box_rows = 1 << box_shift;
     const int boxes_of_tile = kTile >> box_shift;  // a lane issues one
     const uint64_t policy = l2_evict_first_policy();
-    uint32_t it = 0;
+    uint32_t it = 0, handed = 0;
     bool ok = true;
+    auto hand_over = [&](const Job& w) {
+      const uint32_t s = handed % Sh::kJobs;
+      bool free = handed < Sh::kJobs || mbar_wait_bounded(&ctl.job_empty[s], (handed / Sh::kJobs - 1) & 1u);
+      free = __all_sync(0xffffffffu, free);
+      if (!free) return false;
+      if (lane == 0) ctl.jobs[s] = w;
+      arrive_if(&ctl.job_full[s], lane == 0);
+      __syncwarp();
+      ++handed;
+      return true;
+    };
+    Piece p;
+    Job job;
     while (ok && walk.next(prm, p)) {
-      const int first = first_of(p), last = last_of(p);
-      const int chunks = (last - first + kTile - 1) / kTile;
+      const int live = min(p.q_len - p.tile * prm.tile_queries, prm.tile_queries);
+      const int first = p.c0 * kTile, seen = p.n - p.q_len + p.tile * prm.tile_queries + 1;
+      const int last = max(first, min(min(p.n, p.c1 * kTile), seen + live - 1));
+      job.first = first;
+      job.last = last;
+      job.seen = seen;
+      job.cols = live * G;
+      job.b = p.b;
+      job.kvh = p.kvh;
+      job.slot = p.slot;
+      job.pieces = p.pieces;
+      job.row0 = (static_cast<int64_t>(p.q_begin) + p.tile * prm.tile_queries) * prm.num_q_heads + p.kvh * G;
+      ok = hand_over(job);
+      const int chunks = chunks_of(job);
       const int32_t* pt = prm.page_table + static_cast<int64_t>(p.b) * prm.page_table_stride;
       auto page_of = [&](int i) -> int {
         const int pos = first + i * kTile + lane * box_rows;
@@ -847,6 +914,8 @@ __global__ void __launch_bounds__(Shape<C>::kThreads, Shape<C>::kBlocks)
         }
       }
     }
+    job.cols = 0;
+    ok = hand_over(job) && ok;
     if (!ok && lane == 0) give_up();
   } else if (warp == Sh::kScoreWarp) {
     // ======================= K Q^T ========================================================
@@ -856,8 +925,9 @@ __global__ void __launch_bounds__(Shape<C>::kThreads, Shape<C>::kBlocks)
       const uint32_t q = umma::operand(base_addr + Sh::kQ, 16);
       uint32_t step = 0, piece = 0;
       bool ok = true;
-      while (ok && walk.next(prm, p)) {
-        const int chunks = (last_of(p) - first_of(p) + kTile - 1) / kTile;
+      Job p;
+      while (ok && (ok = take(p, true)) && p.cols > 0) {
+        const int chunks = chunks_of(p);
         if (chunks == 0) continue;
         ok = mbar_wait_bounded(&ctl.q_full, piece & 1u);
         ++piece;
@@ -890,8 +960,9 @@ __global__ void __launch_bounds__(Shape<C>::kThreads, Shape<C>::kBlocks)
       const uint32_t weights = umma::operand(base_addr + Sh::kP, 16);
       uint32_t step = 0;
       bool ok = true;
-      while (ok && walk.next(prm, p)) {
-        const int chunks = (last_of(p) - first_of(p) + kTile - 1) / kTile;
+      Job p;
+      while (ok && (ok = take(p, true)) && p.cols > 0) {
+        const int chunks = chunks_of(p);
         for (int i = 0; i < chunks && ok; ++i, ++step) {
           const uint32_t it = 2 * step + 1, slot = it % kSlots;
           ok = mbar_wait_bounded(&ctl.full[slot], (it / kSlots) & 1u);
@@ -924,9 +995,10 @@ __global__ void __launch_bounds__(Shape<C>::kThreads, Shape<C>::kBlocks)
     const float* scales = is_v ? prm.v_scale : prm.k_scale;
     uint32_t step = 0;
     bool ok = true;
-    while (ok && walk.next(prm, p)) {
-      const int first = first_of(p), last = last_of(p);
-      const int chunks = (last - first + kTile - 1) / kTile;
+    Job p;
+    while (ok && (ok = take(p, false)) && p.cols > 0) {
+      const int first = p.first, last = p.last;
+      const int chunks = chunks_of(p);
       const int32_t* pt = prm.page_table + static_cast<int64_t>(p.b) * prm.page_table_stride;
       auto pos_of = [&](int i) { return first + i * kTile + (block << prm.block_shift); };
       auto page_of = [&](int i) -> int { return mine && pos_of(i) < last ? pt[pos_of(i) >> page_shift] : 0; };
