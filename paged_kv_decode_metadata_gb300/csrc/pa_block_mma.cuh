@@ -300,9 +300,9 @@ struct Shape {
     // per warp of four: a column's largest score; of even and of odd chunks (a warp may write the next
     // chunk's while another still reads this one's)
     alignas(16) float peak[2][C / 8][4][8];
-    // a chunk's scales, block by block, V's times the power of two that brings the largest of them to
-    // [128, 256) (all NaN where it is infinite); and what undoes that
-    float k_scales[2][kTile / 16], v_scales[2][kTile / 16];
+    // a chunk's scales, K's and V's, block by block, V's times the power of two that brings the largest of
+    // them to [128, 256) (all NaN where it is infinite); and what undoes that
+    alignas(16) float2 scales[2][kTile / 16];
     float v_down[2];
     alignas(16) float sum[C][4];
     float inverse[C];
@@ -559,6 +559,13 @@ __global__ void __launch_bounds__(Shape<C>::kThreads, Shape<C>::kBlocks)
     const uint32_t lane_base = static_cast<uint32_t>(w4) << 21;     // lane 32 (warp % 4)
     uint32_t step = 0;  // chunks of the pieces before
     bool ok = true;
+    uint32_t weights_at[3];  // of the thread's token in the weights' tile
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+      const int at = i * C + 8 * group;
+      weights_at[i] = Sh::kP + Sh::weights_at(token, at >> 4) + (at & 8);
+    }
+    const int block = token >> prm.block_shift;  // the token's scale of a chunk
     // the queries of the group's columns, a byte each (no division in the loops)
     uint32_t queries[2] = {0, 0};
 #pragma unroll
@@ -680,8 +687,9 @@ __global__ void __launch_bounds__(Shape<C>::kThreads, Shape<C>::kBlocks)
             float lo[8];
             ld8(sc, x);
             ld8(sc + C, lo);
-            const float ks = ctl.k_scales[buf][token >> prm.block_shift];
-            lift = pos < last ? ctl.v_scales[buf][token >> prm.block_shift] : 0.f;
+            const float2 kv = ctl.scales[buf][block];
+            const float ks = kv.x;
+            lift = pos < last ? kv.y : 0.f;
             down = ctl.v_down[buf];
             wait_ld(x, lo);
             umma::fence_before();
@@ -715,8 +723,8 @@ __global__ void __launch_bounds__(Shape<C>::kThreads, Shape<C>::kBlocks)
           }
           group_barrier<C / 8>(group);
         }
-        // the product before, which has had the time of a softmax (behind the weights, with buffers
-        // of its own, it held more registers and was slower: 73 us against 65 for 64 chunks)
+        // the product before, which has had the time of a softmax (behind the weights, with two
+        // buffers of both, it was slower: 78 us against 73 for 25 columns, 96 against 88 for 10)
         if (i > 0) add_product(step - 1);
         if (i == chunks) break;
         if (ok) {
@@ -750,14 +758,12 @@ __global__ void __launch_bounds__(Shape<C>::kThreads, Shape<C>::kBlocks)
           uint32_t w[4];
 #pragma unroll
           for (int j = 0; j < 4; ++j) w[j] = mma::pack_f16(x[2 * j], x[2 * j + 1]);
-          unsigned char* p_tile = smem + Sh::kP;
 #pragma unroll
           for (int piece = 0; piece < 3; ++piece) {
             uint2 codes;
             codes.x = half_codes(w[0]) | half_codes(w[1]) << 16;
             codes.y = half_codes(w[2]) | half_codes(w[3]) << 16;
-            const int at = piece * C + 8 * group;
-            *reinterpret_cast<uint2*>(p_tile + Sh::weights_at(token, at >> 4) + (at & 8)) = codes;
+            *reinterpret_cast<uint2*>(smem + weights_at[piece]) = codes;
             if (piece < 2) {
               w[0] = rest_of(w[0], codes.x & 0xffffu);
               w[1] = rest_of(w[1], codes.x >> 16);
@@ -1021,7 +1027,7 @@ __global__ void __launch_bounds__(Shape<C>::kThreads, Shape<C>::kBlocks)
         const float v_top = warp_peak(is_v ? fabsf(scale) : 0.f);
         const int e = 7 - mma::float_exponent(v_top);
         const float up = v_top < CUDART_INF_F ? mma::pow2_clamped(e) : CUDART_NAN_F;
-        if (mine) (is_v ? ctl.v_scales : ctl.k_scales)[buf][block] = is_v ? scale * up : scale;
+        if (mine) reinterpret_cast<float*>(&ctl.scales[buf][block])[is_v] = is_v ? scale * up : scale;
         if (lane == 0) ctl.v_down[buf] = mma::pow2_clamped(-e);
         __syncwarp();
         arrive_if(&ctl.s_full[buf], lane == 0);
