@@ -898,7 +898,8 @@ PA_API pa_status pa_verify_drafts(const float* target_probs, int64_t target_stri
  * Supported: any page_size >= 1; num_pages <= 2^20, num_pages * page_size < 2^31; count <= 65535;
  * max_seq_pages * page_size <= 2^29.  workspace: 16-byte aligned, pa_pages_workspace_bytes(
  * num_pages, count) bytes; calls that overlap on the GPU need workspaces of their own, and calls
- * on one state must not overlap.
+ * on one state must not overlap.  With use_pdl no call triggers its dependents before its last
+ * write, so the metadata stage, which reads its inputs early, may follow any of them.
  */
 typedef struct {
   void* base;

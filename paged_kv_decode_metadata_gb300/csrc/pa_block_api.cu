@@ -49,7 +49,8 @@ pa_status check_block_pools(const void* k_cache, const void* v_cache, const floa
   if (kv_dtype != PA_KV_E4M3) return PA_ERR_INVALID;
   if (!k_cache || !v_cache || !k_scale || !v_scale || !page_table || !cache_seqlens)
     return PA_ERR_INVALID;
-  if (!aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(k_scale, 4) || !aligned(v_scale, 4))
+  if (!aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(k_scale, 4) || !aligned(v_scale, 4) ||
+      !aligned(page_table, 4) || !aligned(cache_seqlens, 4))
     return PA_ERR_INVALID;
   if (num_kv_heads < 1 || num_kv_heads > 65535 || bs > 65535) return PA_ERR_INVALID;
   if (num_pages < 1 || max_seq_pages < 1 || page_table_stride < max_seq_pages)
@@ -75,7 +76,8 @@ pa_status check_block(const void* q, const void* k_cache, const void* v_cache,
                       float sm_scale, const void* workspace, size_t workspace_bytes,
                       const void* out, const float* lse, int32_t* splits) {
   if (num_splits < 0 || num_splits > 4096 || max_q_len < 1) return PA_ERR_INVALID;
-  if (!q || !aligned(q, 16) || !out || !aligned(out, 16) || !aligned(lse, 4)) return PA_ERR_INVALID;
+  if (!q || !aligned(q, 16) || !out || !aligned(out, 16) || !aligned(lse, 4) || !aligned(cu_seqlens_q, 4))
+    return PA_ERR_INVALID;
   if (num_q_heads < 1 || num_kv_heads < 1 || num_q_heads % num_kv_heads != 0)
     return PA_ERR_INVALID;
   if (cu_seqlens_q == nullptr && (total_q != bs || max_q_len != 1)) return PA_ERR_INVALID;
@@ -156,7 +158,7 @@ pa_status pa_rope_append_blocks(
                                    page_table, page_table_stride, cache_seqlens, bs, num_kv_heads,
                                    head_dim, page_size, num_pages, max_seq_pages);
   if (st != PA_OK) return st;
-  if (!cu_seqlens_q || max_q_len < 1) return PA_ERR_INVALID;
+  if (!cu_seqlens_q || !aligned(cu_seqlens_q, 4) || max_q_len < 1) return PA_ERR_INVALID;
   if (!k || !v || !aligned(k, 16) || !aligned(v, 16)) return PA_ERR_INVALID;
   if (num_q_heads < 0 || num_q_heads > (1 << 20)) return PA_ERR_INVALID;
   if (rotary_dim != 0 && (!positions || !inv_freq || !aligned(positions, 8) || !aligned(inv_freq, 8)))

@@ -121,7 +121,8 @@ pa_status pa_pages_fork(int32_t* req_to_token, int64_t num_rows, int64_t row_str
   if (st != PA_OK) return st;
   int32_t* number = nullptr;
   if ((st = carve(workspace, workspace_bytes, num_pages, count, &p, &number)) != PA_OK) return st;
-  if (!children || !aligned(children, 8) || !child_lens || child_lens == lens) return PA_ERR_INVALID;
+  if (!children || !aligned(children, 8) || !child_lens || !aligned(child_lens, 4) || child_lens == lens)
+    return PA_ERR_INVALID;
   p.children = children;
   p.granted = child_lens;
   const cudaError_t e = pa::error_word(&p.err);
@@ -143,7 +144,9 @@ pa_status pa_pages_extend(int32_t* req_to_token, int64_t num_rows, int64_t row_s
   if (st != PA_OK) return st;
   int32_t* number = nullptr;
   if ((st = carve(workspace, workspace_bytes, num_pages, count, &p, &number)) != PA_OK) return st;
-  if (!new_lens || !granted || granted == lens || granted == new_lens) return PA_ERR_INVALID;
+  if (!new_lens || !granted || !aligned(new_lens, 4) || !aligned(granted, 4) || granted == lens ||
+      granted == new_lens)
+    return PA_ERR_INVALID;
   p.new_lens = new_lens;
   p.granted = granted;
   const cudaError_t e = pa::error_word(&p.err);
@@ -162,6 +165,7 @@ pa_status pa_pages_free(int32_t* req_to_token, int64_t num_rows, int64_t row_str
   const pa_status st = table_params(req_to_token, num_rows, row_stride, page_refs, num_pages,
                                     page_size, max_seq_pages, rows, lens, count, &p);
   if (st != PA_OK) return st;
+  if (!aligned(keep_lens, 4)) return PA_ERR_INVALID;
   p.new_lens = keep_lens;
   const cudaError_t e = pa::error_word(&p.err);
   if (e != cudaSuccess) return pa::from_cuda(e, "error word lookup");
@@ -183,7 +187,7 @@ pa_status pa_pages_compact(int32_t* req_to_token, int64_t num_rows, int64_t row_
                     max_seq_pages, rows, lens, count, &p);
   if (st != PA_OK) return st;
   if ((st = carve(workspace, workspace_bytes, num_pages, count, &p, &p.num_moves)) != PA_OK) return st;
-  if (!page_map || !num_live) return PA_ERR_INVALID;
+  if (!page_map || !num_live || !aligned(page_map, 4) || !aligned(num_live, 4)) return PA_ERR_INVALID;
   p.page_map = page_map;
   p.num_live = num_live;
   const cudaError_t e = pa::error_word(&p.err);
@@ -207,6 +211,11 @@ pa_status pa_verify_drafts(const float* target_probs, int64_t target_stride,
     return PA_ERR_INVALID;
   if (!aligned(target_probs, 4) || !aligned(draft_probs, 4) || !aligned(tokens, 8) || !aligned(next_tokens, 8))
     return PA_ERR_INVALID;
+  for (const void* x : {static_cast<const void*>(parents), static_cast<const void*>(cu_seqlens_q),
+                        static_cast<const void*>(cache_seqlens), static_cast<const void*>(uniforms),
+                        static_cast<const void*>(final_uniforms), static_cast<const void*>(kept),
+                        static_cast<const void*>(counts), static_cast<const void*>(begin)})
+    if (!aligned(x, 4)) return PA_ERR_INVALID;
   if (vocab < 1 || target_stride < vocab || (draft_probs && draft_stride < vocab)) return PA_ERR_INVALID;
   if (max_q_len < 1 || kept_stride < max_q_len || bs > 65535) return PA_ERR_INVALID;
   // the blocks read these while one of them writes the outputs

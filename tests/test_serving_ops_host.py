@@ -242,3 +242,17 @@ def test_prepared_calls_keep_their_pools_alive():
     x, y = torch.zeros(1), torch.zeros(2)
     call = B.PreparedCall("pa_choose_splits", (1, 1, 1, 16, 0, 152), keep=(x, [y], array, None, 3))
     assert any(k is array for k in call._keep) and any(k is y for k in call._keep) and len(call._keep) == 3
+
+
+@pytest.mark.parametrize("name,defaults,pointers", [
+    ("pa_rope_append_blocks", APPEND, ("cu", "cl", "pt")),
+    ("pa_block_attention", ATTEND, ("cu", "cl", "pt")),
+    ("pa_verify_drafts", VERIFY, ("par", "cu", "cl", "u", "fu", "kept", "counts", "begin")),
+    ("pa_pages_fork", TABLE | LISTS["pa_pages_fork"], ("lens", "refs", "out")),
+    ("pa_pages_extend", TABLE | LISTS["pa_pages_extend"], ("lens", "new", "out")),
+    ("pa_pages_free", TABLE | LISTS["pa_pages_free"], ("lens", "keep")),
+    ("pa_pages_compact", TABLE | LISTS["pa_pages_compact"], ("lens", "map", "live")),
+])
+def test_index_arrays_off_their_alignment_are_refused(lib, name, defaults, pointers):
+    for pointer in pointers:
+        assert _caller(getattr(lib, name), defaults)(**{pointer: FAKE + 256 + 2}) == B.PA_ERR_INVALID, pointer
