@@ -777,11 +777,12 @@ PA_API pa_status pa_rope_append_blocks(
  * query that attends to nothing gives out = 0, lse = -inf; rows that no request covers, and those
  * of a request whose rows are refused, are not touched.
  * The codes are multiplied as they are, against bf16 q (exact but for channels below 2^-13 of the
- * row's largest, which keep 2^-21 of it) and weights rounded to fp16: out is within 2^-11 sum_j p_j
- * |v_j| before its own rounding, where the scales of 128 consecutive tokens lie within 2^14 of one
- * another; a weight times scale below 2^-33 of the largest among them counts as 0 in out (not in
- * lse).  Non-finite codes (NaN) and scales reach the queries that attend to them, a V
- * code every query of its request.  Codes and scales at or past n may hold anything.
+ * row's largest, which keep 2^-21 of it) and weights rounded to fp16: before its own rounding out is
+ * within 2^-11 sum_j p_j |v_j| + 2^-36 p_max sum_j t_j |c_j|, with p_max the row's largest weight, c_j
+ * the V codes and t_j the largest |V scale| (at least 2^-112) among the 128 tokens of j (from a multiple of
+ * 128 on): a weight counts in out to about 2^-36 of the largest, and in lse always.  NaN codes of K and
+ * scales of K that are not finite reach the queries that attend to them; NaN codes of V and scales of V that are not
+ * finite may reach every query of their request.  Codes and scales at or past n may hold anything.
  * num_splits: the most pieces (1 to 4096) that a row's context may be cut into, or 0 for
  * pa_choose_block_splits(...).  With 1 `workspace` may be NULL; otherwise it is 16-byte aligned,
  * workspace_bytes >= pa_workspace_bytes(total_q, num_q_heads, 128, that number), and a second

@@ -3,18 +3,21 @@
 //
 // Mathematics.  x_j = s q . K_j, out = sum_j e^(x_j - m) V_j / sum_j e^(x_j - m), one pass with
 // a running maximum.  The codes go from memory to the tensor cores as they are, so the other
-// operand of each product is e4m3, too, in pieces: a query row, scaled by a power of two, is
-// hi + lo / 16, which holds bf16 exactly (8 significant bits are 4 and 4; what is lost of the
-// row's small channels is 2^-21 of its largest); a weight is rounded to fp16 (2^-11 of itself, or
-// 2^-33 of the chunk's largest weight times V scale) and is h1 + h2 / 16 + h3 / 256.  Each piece has
-// columns of its own in the product, so the pieces are added in fp32.  The K scale multiplies
-// the fp32 score; the V scale multiplies the weight before it is cut into pieces, relative to
-// the chunk's largest V scale, which multiplies the chunk's product.  Products leave tensor
+// operand of each product has 8 bits, too, in pieces.  A query row, scaled by a power of two, is
+// hi + lo / 16 in e4m3, which holds bf16 exactly (8 significant bits are 4 and 4; what is lost of the
+// row's small channels is 2^-21 of its largest).  A weight, e^(x - m) times the V scale, the chunk's
+// largest V scale lifted to [2^14, 2^15), is rounded to fp16 (2^-11 of itself) and is
+// h1 + h2 + (h3 + h4) / 128 in e5m2, which is the upper byte of an fp16: 3 bits a piece, 12 in all.
+// e5m2 for its range, since weights are as small as scores lie apart: they are exact from 2^-13 up, and
+// what is lost of smaller ones is 2^-23 + 2^-25, 2^-36 of the largest scale's weight of 1 (three pieces
+// in e4m3 end 2^-25 below it: beside a token 18 above the others, those were gone).  Pieces of one scale
+// are added up by the product, the others in fp32 registers.  The K scale multiplies the
+// fp32 score; what lifts the V scales is undone on the chunk's product.  Products leave tensor
 // memory chunk by chunk and are summed in fp32 registers: no accumulator is rescaled in place,
 // and long contexts do not add up the tensor cores' truncation.
 //
 // Shape.  M is the cache side: scores are S^T = K Q^T (128 tokens x 2 C columns), outputs O^T =
-// V^T P^T (128 channels x 3 C), C = 8, 16 or 32 columns of (query, head) pairs of one kv head.
+// V^T P^T (128 channels x 2 C, two passes; C = 8: 4 C), C = 8, 16 or 32 columns of (query, head) pairs of one kv head.
 // So few columns cost few cycles, a thread owns a token in the softmax and a channel in the
 // sums, and neither K nor V is moved or widened.  Four warps have 8 columns; a column's maximum
 // goes over their 128 threads: a warp reduction, four numbers in shared memory, one barrier a
@@ -33,9 +36,10 @@
 //
 // Bound by memory with 8 columns: 32 requests of 8192 tokens, 32 / 8 heads, 83 us and 6.4 TB/s; 64
 // ragged ones up to 16K, 64 / 8 heads, 161 us and 6.7 TB/s.  With 16 and 32 columns by the softmax
-// warps' instructions: 1.3 us a chunk of 32 columns on an SM (16 requests of 8192 tokens, 25 columns: 73
-// us, where memory would take 40; with the scales found by the softmax warps 92, with every warp
-// walking for itself 82).  One request of 1024 tokens: 8.4 us, launches and dependent latencies; short
+// warps' instructions: 1.35 us a chunk of 32 columns on an SM (16 requests of 8192 tokens, 25 columns: 77
+// us, where memory would take 40; 73 with weights of three e4m3 pieces, which lost small ones; of those with
+// the scales found by the softmax warps 92, with every warp walking for itself 82).  A column for each
+// of the four pieces took 79.5, and 153 in place of 148 us for 32 requests and 32 columns.  One request of 1024 tokens: 8.4 us, launches and dependent latencies; short
 // contexts by the same latencies once a unit (256 requests of 128 tokens: 28 us, memory 10).
 #pragma once
 
@@ -268,7 +272,11 @@ struct Shape {
   static constexpr int kSoftmaxRegs = C == 8 ? 168 : C == 16 ? 96 : 104, kOtherRegs = C == 8 ? 80 : C == 16 ? 48 : 64;
   static_assert(32 * (kSoftmaxWarps * kSoftmaxRegs + 4 * kOtherRegs) <= kThreads * kLaunchRegs, "register split");
   static constexpr int kScoreCols = 2 * C;
-  static constexpr int kOutCols = (3 * C + 15) / 16 * 16;
+  // The weights' pieces h1 and h3 of a group of 8 columns lie next to one another, and h2 and h4.  h1 and h2
+  // have one scale, and h3 and h4: one product adds them up in two passes over V, each with a tile of its
+  // own.  (Rows of 16 bytes, which 8 columns would have, are another layout: they take one pass.)
+  static constexpr int kPasses = C == 8 ? 1 : 2;
+  static constexpr int kOutCols = 4 * C / kPasses;
   static constexpr int kTmemCols = C == 8 ? 64 : C == 16 ? 128 : 256;
   static_assert(2 * kScoreCols + kOutCols <= kTmemCols, "tensor memory");
   static constexpr int kJobs = 4;  // pieces handed over and not yet taken by every warp
@@ -282,17 +290,17 @@ struct Shape {
   static constexpr int kRing = 0;
   static constexpr int kQ = kSlots * kTileBytes;
   static constexpr int kP = kQ + kScoreCols * 128;
-  // The weights' tile: a row per token, its 3 C pieces next to one another ("MN-major"), rows of 32,
-  // 64 or 128 bytes with that swizzle.
-  static constexpr int kRowBytes = C == 8 ? 32 : C == 16 ? 64 : 128;
-  static constexpr int kStage = kP + kTile * kRowBytes;  // the columns' sums on their way out
+  // The weights' tiles, one a pass: a row per token ("MN-major"), rows of 32 or 64 bytes with that swizzle.
+  static constexpr int kRowBytes = kOutCols, kWeightsTile = kTile * kRowBytes;
+  static constexpr int kStage = kP + kPasses * kWeightsTile;  // the columns' sums on their way out
   static constexpr int kEnd = kStage + C * 128 * 4;
-  // High word of its descriptor: the stride offset steps 8 rows; version 1; the swizzle's code.
-  static constexpr uint32_t kWeightsHigh =
-      (8u * kRowBytes >> 4) | (1u << 14) | ((C == 8 ? 6u : C == 16 ? 4u : 2u) << 29);
-  // Byte offset of 16-byte piece `c` of row `t`.
-  static __device__ __forceinline__ uint32_t weights_at(int t, int c) {
-    return static_cast<uint32_t>(t * kRowBytes + ((c ^ (C == 8 ? t >> 2 & 1 : C == 16 ? t >> 1 & 3 : t & 7)) << 4));
+  // High word of their descriptors: the stride offset steps 8 rows; version 1; the swizzle's code.
+  static constexpr uint32_t kWeightsHigh = (8u * kRowBytes >> 4) | (1u << 14) | ((kRowBytes == 32 ? 6u : 4u) << 29);
+  // Byte offset from kP of a group's pieces in row `t`: h1 and h3 (half 0), h2 and h4 (half 1).
+  static __device__ __forceinline__ uint32_t weights_at(int t, int half, int group) {
+    const int tile = kPasses == 1 ? 0 : half, c = kPasses == 1 ? half : group;
+    return static_cast<uint32_t>(tile * kWeightsTile + t * kRowBytes +
+                                 ((c ^ (kRowBytes == 32 ? t >> 2 & 1 : t >> 1 & 3)) << 4));
   }
   struct alignas(16) Control {
     uint64_t full[kSlots], empty[kSlots];
@@ -301,7 +309,7 @@ struct Shape {
     // chunk's while another still reads this one's)
     alignas(16) float peak[2][C / 8][4][8];
     // a chunk's scales, K's and V's, block by block, V's times the power of two that brings the largest of
-    // them to [128, 256) (all NaN where it is infinite); and what undoes that
+    // them to [2^14, 2^15) (all NaN where it is infinite); and what undoes that
     alignas(16) float2 scales[2][kTile / 16];
     float v_down[2];
     alignas(16) float sum[C][4];
@@ -317,9 +325,10 @@ struct Shape {
   static_assert(kTmemCols * kBlocks <= 512, "tensor memory");
 };
 
-// Instruction descriptor: fp32 accumulator, e4m3 operands, M = 128.
-constexpr uint32_t instruction(int n, bool mn_major) {
-  return (1u << 4) | (mn_major ? 3u << 15 : 0u) | (static_cast<uint32_t>(n / 8) << 17) |
+// Instruction descriptors: fp32 accumulator, M = 128; scores e4m3 by e4m3, products e4m3 by e5m2 with both
+// operands "MN-major".
+constexpr uint32_t instruction(int n, bool product) {
+  return (1u << 4) | (product ? 1u << 10 | 3u << 15 : 0u) | (static_cast<uint32_t>(n / 8) << 17) |
          (static_cast<uint32_t>(kTile / 16) << 24);
 }
 
@@ -354,12 +363,12 @@ __device__ __forceinline__ void ld8(uint32_t addr, float (&r)[8]) {
                  "=f"(r[7])
                : "r"(addr));
 }
-__device__ __forceinline__ void wait_ld(float (&a)[8], float (&b)[8], float (&c)[8]) {
+__device__ __forceinline__ void wait_ld(float (&a)[8], float (&b)[8], float (&c)[8], float (&d)[8]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+f"(a[0]), "+f"(a[1]), "+f"(a[2]), "+f"(a[3]), "+f"(a[4]), "+f"(a[5]), "+f"(a[6]),
-                 "+f"(a[7]), "+f"(b[0]), "+f"(b[1]), "+f"(b[2]), "+f"(b[3]), "+f"(b[4]), "+f"(b[5]),
-                 "+f"(b[6]), "+f"(b[7]), "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3]), "+f"(c[4]),
-                 "+f"(c[5]), "+f"(c[6]), "+f"(c[7])
+               : "+f"(a[0]), "+f"(a[1]), "+f"(a[2]), "+f"(a[3]), "+f"(a[4]), "+f"(a[5]), "+f"(a[6]), "+f"(a[7]),
+                 "+f"(b[0]), "+f"(b[1]), "+f"(b[2]), "+f"(b[3]), "+f"(b[4]), "+f"(b[5]), "+f"(b[6]), "+f"(b[7]),
+                 "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3]), "+f"(c[4]), "+f"(c[5]), "+f"(c[6]), "+f"(c[7]),
+                 "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3]), "+f"(d[4]), "+f"(d[5]), "+f"(d[6]), "+f"(d[7])
                :
                : "memory");
 }
@@ -392,17 +401,15 @@ __device__ __forceinline__ float2 from_codes(uint32_t codes) {
   return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
 
-// Two fp16 values to codes; and 16 times what the codes leave of them (exact: fp16 holds it).
-__device__ __forceinline__ uint32_t half_codes(uint32_t w) {
-  uint16_t c;
-  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(c) : "r"(w));
-  return c;
+// Upper bytes of four fp16 values, e5m2 codes; and what they leave of two of them (exact).
+__device__ __forceinline__ uint32_t upper_bytes(uint32_t w01, uint32_t w23) { return __byte_perm(w01, w23, 0x7531); }
+__device__ __forceinline__ uint32_t rest_of(uint32_t w) {
+  const uint32_t upper = w & 0xff00ff00u;
+  const __half2 d = __hsub2(*reinterpret_cast<const __half2*>(&w), *reinterpret_cast<const __half2*>(&upper));
+  return *reinterpret_cast<const uint32_t*>(&d);
 }
-__device__ __forceinline__ uint32_t rest_of(uint32_t w, uint32_t codes) {
-  uint32_t h;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(codes)));
-  const __half2 d = __hmul2(__hsub2(*reinterpret_cast<const __half2*>(&w), *reinterpret_cast<const __half2*>(&h)),
-                            __float2half2_rn(16.f));
+__device__ __forceinline__ uint32_t times_128(uint32_t w) {
+  const __half2 d = __hmul2(*reinterpret_cast<const __half2*>(&w), __float2half2_rn(128.f));
   return *reinterpret_cast<const uint32_t*>(&d);
 }
 
@@ -559,12 +566,8 @@ __global__ void __launch_bounds__(Shape<C>::kThreads, Shape<C>::kBlocks)
     const uint32_t lane_base = static_cast<uint32_t>(w4) << 21;     // lane 32 (warp % 4)
     uint32_t step = 0;  // chunks of the pieces before
     bool ok = true;
-    uint32_t weights_at[3];  // of the thread's token in the weights' tile
-#pragma unroll
-    for (int i = 0; i < 3; ++i) {
-      const int at = i * C + 8 * group;
-      weights_at[i] = Sh::kP + Sh::weights_at(token, at >> 4) + (at & 8);
-    }
+    // of the thread's token in the weights' tiles
+    const uint32_t weights_at[2] = {Sh::kP + Sh::weights_at(token, 0, group), Sh::kP + Sh::weights_at(token, 1, group)};
     const int block = token >> prm.block_shift;  // the token's scale of a chunk
     // the queries of the group's columns, a byte each (no division in the loops)
     uint32_t queries[2] = {0, 0};
@@ -650,25 +653,36 @@ __global__ void __launch_bounds__(Shape<C>::kThreads, Shape<C>::kBlocks)
       for (int j = 0; j < 8; ++j) m[j] = kNothing;
 #pragma unroll
       for (int k = 0; k < 4; ++k) l2[k] = acc2[k] = umma::pair(0.f, 0.f);
-      const uint64_t sixteenth = umma::pair(1.f / 16.f, 1.f / 16.f);
+      const uint64_t sixteenth = umma::pair(1.f / 16.f, 1.f / 16.f), small = umma::pair(1.f / 128.f, 1.f / 128.f);
       float v_down = 0.f;  // of the chunk before: what undoes its V scales' power of two
       auto add_product = [&](uint32_t at) {  // acc += the product of chunk `at`
         ok = ok && mbar_wait_bounded(&ctl.o_full, at & 1u);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) return;
         umma::fence_after();
-        float h1[8], h2[8], h3[8];
-        const uint32_t oc = out_col + lane_base + 8 * group;
+        float h1[8], h3[8];  // of h1 + h2, of h3 + h4
+        const uint32_t oc = out_col + lane_base + 16 * group;
         ld8(oc, h1);
-        ld8(oc + C, h2);
-        ld8(oc + 2 * C, h3);
-        wait_ld(h1, h2, h3);
+        ld8(oc + 8, h3);
+        if constexpr (Sh::kPasses == 1) {
+          float h2[8], h4[8];
+          ld8(oc + 16, h2);
+          ld8(oc + 24, h4);
+          wait_ld(h1, h2, h3, h4);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            h1[j] += h2[j];
+            h3[j] += h4[j];
+          }
+        } else {
+          wait_ld(h1, h3);
+        }
         const uint64_t down = umma::pair(v_down, v_down);
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           const int j = 2 * k;
-          const uint64_t tail = umma::fma2(umma::pair(h3[j], h3[j + 1]), sixteenth, umma::pair(h2[j], h2[j + 1]));
-          acc2[k] = umma::fma2(umma::fma2(tail, sixteenth, umma::pair(h1[j], h1[j + 1])), down, acc2[k]);
+          const uint64_t sum = umma::fma2(umma::pair(h3[j], h3[j + 1]), small, umma::pair(h1[j], h1[j + 1]));
+          acc2[k] = umma::fma2(sum, down, acc2[k]);
         }
         umma::fence_before();
       };
@@ -724,7 +738,8 @@ __global__ void __launch_bounds__(Shape<C>::kThreads, Shape<C>::kBlocks)
           group_barrier<C / 8>(group);
         }
         // the product before, which has had the time of a softmax (behind the weights, with two
-        // buffers of both, it was slower: 78 us against 73 for 25 columns, 96 against 88 for 10)
+        // buffers of both, it was slower: 78 us against 73 for 25 columns, 96 against 88 for 10, with the
+        // weights cut into three pieces)
         if (i > 0) add_product(step - 1);
         if (i == chunks) break;
         if (ok) {
@@ -754,23 +769,24 @@ __global__ void __launch_bounds__(Shape<C>::kThreads, Shape<C>::kBlocks)
             l2[k] = umma::add2(l2[k], e2);
             umma::unpair(umma::mul2(e2, lift2), x[j], x[j + 1]);
           }
-          // rounded to fp16 (11 bits), then cut into pieces of 4 bits, exactly
+          // rounded to fp16 (11 bits), then cut into pieces of 3 bits, the last one rounded
           uint32_t w[4];
 #pragma unroll
           for (int j = 0; j < 4; ++j) w[j] = mma::pack_f16(x[2 * j], x[2 * j + 1]);
+          uint32_t h[4][2];
 #pragma unroll
-          for (int piece = 0; piece < 3; ++piece) {
-            uint2 codes;
-            codes.x = half_codes(w[0]) | half_codes(w[1]) << 16;
-            codes.y = half_codes(w[2]) | half_codes(w[3]) << 16;
-            *reinterpret_cast<uint2*>(smem + weights_at[piece]) = codes;
-            if (piece < 2) {
-              w[0] = rest_of(w[0], codes.x & 0xffffu);
-              w[1] = rest_of(w[1], codes.x >> 16);
-              w[2] = rest_of(w[2], codes.y & 0xffffu);
-              w[3] = rest_of(w[3], codes.y >> 16);
+          for (int piece = 0; piece < 4; ++piece) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              if (piece > 0) w[j] = rest_of(w[j]);
+              if (piece == 2) w[j] = times_128(w[j]);  // (below 2^9 before)
+              if (piece == 3) w[j] += 0x00800080u;     // (half a step; NaN is in the other pieces)
             }
+            h[piece][0] = upper_bytes(w[0], w[1]);
+            h[piece][1] = upper_bytes(w[2], w[3]);
           }
+          *reinterpret_cast<uint4*>(smem + weights_at[0]) = make_uint4(h[0][0], h[0][1], h[2][0], h[2][1]);
+          *reinterpret_cast<uint4*>(smem + weights_at[1]) = make_uint4(h[1][0], h[1][1], h[3][0], h[3][1]);
           // V rows past the last token may hold anything, and 0 times NaN is NaN
           const int valid = last - (first + i * kTile);
           if (valid < kTile && group == 0) {
@@ -978,8 +994,11 @@ __global__ void __launch_bounds__(Shape<C>::kThreads, Shape<C>::kBlocks)
           // 32 tokens a step: rows of V, rows of weights
           const uint32_t v = umma::operand(base_addr + Sh::kRing + slot * kTileBytes, 16);
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            mma(out_col, v + j * (4096 >> 4), weights + j * (32 * Sh::kRowBytes >> 4), Sh::kWeightsHigh, kDesc, j > 0);
+          for (int j = 0; j < 4 * Sh::kPasses; ++j) {
+            const int pass = j / 4, k = j % 4;
+            mma(out_col, v + k * (4096 >> 4), weights + ((pass * Sh::kWeightsTile + k * 32 * Sh::kRowBytes) >> 4),
+                Sh::kWeightsHigh, kDesc, j > 0);
+          }
           umma::commit(&ctl.empty[slot]);
           umma::commit(&ctl.o_full);
         }
@@ -1025,10 +1044,11 @@ __global__ void __launch_bounds__(Shape<C>::kThreads, Shape<C>::kBlocks)
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         const float v_top = warp_peak(is_v ? fabsf(scale) : 0.f);
-        const int e = 7 - mma::float_exponent(v_top);
-        const float up = v_top < CUDART_INF_F ? mma::pow2_clamped(e) : CUDART_NAN_F;
+        // (a power of two and what undoes it, both normal)
+        const int e = max(-126, min(126, 14 - mma::float_exponent(v_top)));
+        const float up = v_top < CUDART_INF_F ? __int_as_float((e + 127) << 23) : CUDART_NAN_F;
         if (mine) reinterpret_cast<float*>(&ctl.scales[buf][block])[is_v] = is_v ? scale * up : scale;
-        if (lane == 0) ctl.v_down[buf] = mma::pow2_clamped(-e);
+        if (lane == 0) ctl.v_down[buf] = __int_as_float((127 - e) << 23);
         __syncwarp();
         arrive_if(&ctl.s_full[buf], lane == 0);
       }
