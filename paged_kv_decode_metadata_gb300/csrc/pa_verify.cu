@@ -55,10 +55,10 @@ __device__ __forceinline__ uint32_t cluster_rank() {
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
   return r;
 }
-__device__ __forceinline__ void cluster_barrier() {
-  asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
-}
-// Stores to the same variable of block `rank` of the cluster.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.aligned;" ::: "memory"); }
+// Stores to the same variable of block `rank` of the cluster (which has started: that is waited for before
+// the first of them).
 __device__ __forceinline__ void store_remote(unsigned long long* at, uint32_t rank, unsigned long long v) {
   uint32_t remote;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(smem_addr(at)), "r"(rank));
@@ -96,6 +96,8 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rank = static_cast<int>(cluster_rank());
   const int b = blockIdx.y;
+  // A block's memory may be stored to only once it runs: all arrive here, and wait before the walk.
+  cluster_arrive();
   grid_dependency_wait();
 
   const int q_begin = prm.cu_seqlens_q[b];
@@ -112,6 +114,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
   const int begin = n - q_len;
   int32_t* kept = prm.kept + static_cast<int64_t>(b) * prm.kept_stride;
   if (q_len == 0) {  // (the whole cluster)
+    cluster_wait();
     if (rank == 0) {
       for (int i = tid; i < prm.max_q_len; i += kThreads) kept[i] = -1;
       if (tid == 0) {
@@ -213,7 +216,8 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
       for (int w = 0; w < kWarps; ++w) mine += sh.warp_sum[w];
       store_remote(&sh.block_sum[buffer][rank], static_cast<uint32_t>(tid), mine);
     }
-    cluster_barrier();
+    cluster_arrive();
+    cluster_wait();
     unsigned long long all = 0;
     for (int r = 0; r < kCluster; ++r) all += sh.block_sum[buffer][r];
     return all;
@@ -227,6 +231,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
   float walk_c = 0.f, sum = 1.f;  // w = max(p - c q, 0) and its sum, -1 where it is not known
   double left = 1.0;              // without draft probabilities: the row's sum less what is gone
   if (tid == 0) sh.path[0] = 0;
+  cluster_wait();  // (every block of the cluster has started; the loads above took longer)
   while (true) {
     if (warp == 0) {
       const bool drafted = prm.draft_probs != nullptr;
