@@ -1311,14 +1311,18 @@ def _page_pools(pools, num_pages: int, name: str, pinned: bool = False):
 
 def _slot_table(req_to_token, page_refs, page_size: int, max_seq_pages: int, rows, lens):
     """The page operators' common arguments and the length of their lists."""
+    num_rows, width = req_to_token.shape if req_to_token.dim() == 2 else (0, 0)
     stride = _row_stride(req_to_token, "req_to_token")
-    stride = stride if req_to_token.shape[0] > 1 else max(stride, req_to_token.shape[1])
+    stride = stride if num_rows > 1 else width
     if page_refs.dim() != 1:
         raise ValueError("page_refs must be [num_pages]")
     count = rows.numel()
     _shape(rows, (count,), "rows")
     _shape(lens, (count,), "lens")
-    if int(max_seq_pages) * int(page_size) > req_to_token.shape[1] + int(page_size) - 1:
+    # a row's last page may end past the row only where the row is all that its stride covers: its
+    # slots are written up to the stride
+    room = width if stride > width else width + int(page_size) - 1
+    if int(max_seq_pages) * int(page_size) > room:
         raise ValueError(f"req_to_token has room for fewer than {max_seq_pages} pages a row")
     return (_ptr2d(req_to_token, torch.int32, "req_to_token"), req_to_token.shape[0], stride,
             _ptr(page_refs, torch.int32, "page_refs"), page_refs.numel(), int(page_size),

@@ -255,3 +255,34 @@ def test_what_the_device_alone_sees_is_refused_and_reported():
     assert B.pa_read_error_flags(reset=True) == B.DEVERR_PAGE_REFS | B.DEVERR_PAGE_OUT_OF_RANGE
     s.table[3, 0] = s.table[3, 16] = -1
     s.check()
+
+
+def test_columns_beside_a_table_stay():
+    """A table that is a range of columns of a wider one, and one row of it: what lies beside stays."""
+    big = torch.full((5, 100), 77, dtype=torch.int32, device="cuda")
+    ints = lambda *x: torch.tensor(x, dtype=torch.int32).cuda()
+    rows = lambda *x: torch.tensor(x).cuda()
+    refs = torch.zeros(12, dtype=torch.int32, device="cuda")
+    pages = [torch.arange(12 * 8, dtype=torch.float32, device="cuda").view(12, 8)]
+    out, one = ints(0, 0), ints(0)
+    ws = torch.empty(B.pa_pages_workspace_bytes(12, 2), dtype=torch.uint8, device="cuda")
+    kw = dict(req_to_token=big[:, 20:68], page_refs=refs, page_size=16, max_seq_pages=3)
+    B.pa_pages_extend(rows=rows(0, 4), lens=ints(0, 0), new_lens=ints(40, 48), granted=out, workspace=ws, **kw)
+    B.pa_pages_fork(parents=rows(0, 4), children=rows(1, 3), lens=ints(40, 48), pools=pages, child_lens=out,
+                    workspace=ws, **kw)
+    # one row, whose last page ends past its columns
+    B.pa_pages_extend(rows=rows(0), lens=ints(0), new_lens=ints(30), granted=one, workspace=ws,
+                      **kw | dict(req_to_token=big[2:3, 70:100], max_seq_pages=2))
+    live = torch.full((1,), -1, dtype=torch.int32, device="cuda")
+    B.pa_pages_free(rows=rows(0, 4), lens=ints(40, 48), **kw)
+    B.pa_pages_compact(rows=rows(1, 3), lens=ints(40, 48), pools=pages, page_map=torch.empty_like(refs),
+                       num_live=live, workspace=ws, **kw)
+    torch.cuda.synchronize()
+    assert out.tolist() == [40, 48] and one.tolist() == [30] and int(live) == 8
+    mine = torch.zeros((5, 100), dtype=torch.bool)
+    mine[[0, 1, 3, 4], 20:68] = True
+    mine[2, 70:100] = True
+    assert bool((big.cpu()[~mine] == 77).all())
+    assert big[2, 70:100].tolist() == list(range(7 * 16, 8 * 16)) + list(range(8 * 16, 8 * 16 + 14))
+    with pytest.raises(ValueError, match="room for fewer"):
+        B.pa_pages_free(rows=rows(0), lens=ints(0), **kw | dict(req_to_token=big[:, 20:70], max_seq_pages=4))

@@ -256,3 +256,19 @@ def test_prepared_calls_keep_their_pools_alive():
 def test_index_arrays_off_their_alignment_are_refused(lib, name, defaults, pointers):
     for pointer in pointers:
         assert _caller(getattr(lib, name), defaults)(**{pointer: FAKE + 256 + 2}) == B.PA_ERR_INVALID, pointer
+
+
+def test_tables_that_are_columns_of_wider_ones():
+    """Slots are written up to the row's stride, so a last page must not reach past the columns of
+    a view.  (A host tensor is refused, too, but after the table's shape.)"""
+    big = torch.zeros((4, 256), dtype=torch.int32)
+    refs, one = torch.zeros(9, dtype=torch.int32), torch.zeros(1, dtype=torch.int64)
+    lens = torch.zeros(1, dtype=torch.int32)
+    for table, pages in ((big[:, 200:256], 1), (big[:, :200], 4), (big[:, 64:129], 2), (big[3:, 250:], 2),
+                         (big, 5)):
+        with pytest.raises(ValueError, match="room for fewer"):
+            B._slot_table(table, refs, 64, pages, one, lens)
+    for table, pages in ((big[:, 64:192], 2), (big[:, :200], 3), (big, 4), (big[:, :200].contiguous(), 4),
+                         (big[3:, 200:256], 1)):
+        with pytest.raises(ValueError, match="must be a CUDA tensor"):
+            B._slot_table(table, refs, 64, pages, one, lens)
