@@ -927,7 +927,9 @@ PA_API pa_status pa_pages_copy(const pa_page_pool* src_pools, const pa_page_pool
  * rewrites full pages, as pa_evict in place does, must not be used on shared ones.)  One parent
  * may have many children; a child is a row that holds nothing, and is listed once.
  * child_lens[i] (out) = lens[i], or, where no page was left for the last one, its full pages'
- * tokens, with PA_DEVERR_OUT_OF_PAGES.  A shared page that nobody holds sets PA_DEVERR_PAGE_REFS.
+ * tokens, with PA_DEVERR_OUT_OF_PAGES.  A page that nobody holds is not shared or copied and sets
+ * PA_DEVERR_PAGE_REFS: its slots in the child's row become -1, and a last one takes the child's length back to
+ * its full pages.
  */
 PA_API pa_status pa_pages_fork(int32_t* req_to_token, int64_t num_rows, int64_t row_stride,
                                int32_t* page_refs, int64_t num_pages, int32_t page_size,

@@ -51,19 +51,26 @@ struct Scan {
   }
 };
 
+// Holders of a thread's four pages from `base` on.
+__device__ __forceinline__ int4 holders(const int32_t* refs, int64_t num_pages, int64_t base) {
+  const int64_t at = base + threadIdx.x * 4;
+  return make_int4(at < num_pages ? refs[at] : 1, at + 1 < num_pages ? refs[at + 1] : 1,
+                   at + 2 < num_pages ? refs[at + 2] : 1, at + 3 < num_pages ? refs[at + 3] : 1);
+}
+
 // The lowest `want` free pages, in order, to `list`; returns how many there are (all threads).
+// `first`: holders(.., 0), which the plans ask for before they read their entries.
 template <int kThreads>
 __device__ int find_free(const int32_t* refs, int64_t num_pages, int want, int32_t* list, Scan<kThreads>& scan,
-                         int& turn) {
+                         int& turn, int4 first) {
   int found = 0;
   for (int64_t base = 0; base < num_pages && found < want; base += kThreads * 4) {
     const int64_t at = base + threadIdx.x * 4;
-    int r[4], free = 0;
+    if (base > 0) first = holders(refs, num_pages, base);
+    const int r[4] = {first.x, first.y, first.z, first.w};
+    int free = 0;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      r[j] = at + j < num_pages ? refs[at + j] : 1;
-      free += r[j] == 0;
-    }
+    for (int j = 0; j < 4; ++j) free += r[j] == 0;
     int total;
     int rank = found + scan(free, turn, total) - free;
 #pragma unroll
@@ -110,6 +117,7 @@ __global__ void __launch_bounds__(kPlan) plan_fork_kernel(const PagesParams p) {
   trigger_dependents();  // (what applies the plan waits for its end)
   grid_dependency_wait();
   const int tid = threadIdx.x;
+  const int4 first = holders(p.page_refs, p.num_pages, 0);
   int want = 0;
   for (int base = 0; base < p.count; base += kPlan) {
     const int i = base + tid;
@@ -120,10 +128,12 @@ __global__ void __launch_bounds__(kPlan) plan_fork_kernel(const PagesParams p) {
       int32_t src = -1;
       if (parent >= 0 && child >= 0 && n >= 0 && n % p.page_size != 0) {
         const int32_t slot = p.req_to_token[parent * p.row_stride + n / p.page_size * p.page_size];
-        if (slot >= 0 && slot / p.page_size < p.num_pages) {
-          src = slot / p.page_size;
-        } else {
+        if (slot < 0 || slot / p.page_size >= p.num_pages) {
           record_error(p.err, kErrPageOutOfRange);
+        } else if (p.page_refs[slot / p.page_size] <= 0) {
+          record_error(p.err, kErrPageRefs);
+        } else {
+          src = slot / p.page_size;
         }
       }
       needs = src >= 0;
@@ -136,12 +146,12 @@ __global__ void __launch_bounds__(kPlan) plan_fork_kernel(const PagesParams p) {
     want += total;
   }
   __syncthreads();
-  const int found = find_free(p.page_refs, p.num_pages, want, p.list, scan, turn);
+  const int found = find_free(p.page_refs, p.num_pages, want, p.list, scan, turn, first);
   __syncthreads();
   for (int i = tid; i < p.count; i += kPlan) {
     const int rank = p.dst_pages[i];
     if (rank < 0) {
-      // a last page that could not be read: the child has what is before it
+      // a last page that could not be read, or that nobody holds: the child has what is before it
       if (p.granted[i] % p.page_size != 0) p.granted[i] -= p.granted[i] % p.page_size;
       continue;
     }
@@ -164,6 +174,7 @@ __global__ void __launch_bounds__(kPlan) plan_extend_kernel(const PagesParams p)
   trigger_dependents();  // (what applies the plan waits for its end)
   grid_dependency_wait();
   const int tid = threadIdx.x;
+  const int4 first = holders(p.page_refs, p.num_pages, 0);
   int want = 0;
   for (int base = 0; base < p.count; base += kPlan) {
     const int i = base + tid;
@@ -182,7 +193,7 @@ __global__ void __launch_bounds__(kPlan) plan_extend_kernel(const PagesParams p)
     want = static_cast<int>(min(static_cast<int64_t>(want) + total, p.num_pages));
   }
   __syncthreads();
-  const int found = find_free(p.page_refs, p.num_pages, want, p.list, scan, turn);
+  const int found = find_free(p.page_refs, p.num_pages, want, p.list, scan, turn, first);
   __syncthreads();
   for (int r = tid; r < found; r += kPlan) p.page_refs[p.list[r]] = 1;
   for (int i = tid; i < p.count; i += kPlan) {
@@ -325,8 +336,16 @@ __device__ __forceinline__ void write_slots(const PagesParams& p, int64_t row, i
 // Tables of 32 pages of a row are a task, a warp taking every eighth.
 constexpr int kTablePages = 32;
 
+// One holder more of a page that somebody holds.  (Looked at first: counts only rise in this launch, so a
+// page that nobody held when it began is refused to every child alike.)
+__device__ __forceinline__ bool hold(int32_t* refs) {
+  if (*static_cast<volatile int32_t*>(refs) <= 0) return false;
+  atomicAdd(refs, 1);
+  return true;
+}
+
 // Forks: the child's row up to its last full page is the parent's, each of those pages has one
-// holder more; then the copied page's slots.
+// holder more (a page that cannot be shared leaves -1); then the copied page's slots.
 __global__ void __launch_bounds__(kThreads) apply_fork_kernel(const PagesParams p, const __grid_constant__ PagesPools pools) {
   grid_dependency_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -349,15 +368,14 @@ __global__ void __launch_bounds__(kThreads) apply_fork_kernel(const PagesParams 
       int32_t* to = p.req_to_token + child * p.row_stride + pos;
       const int32_t slot = from[0];
       const bool known = slot >= 0 && slot / p.page_size < p.num_pages;
-      if (lane == 0) {
-        if (!known) {
-          record_error(p.err, kErrPageOutOfRange);
-        } else if (atomicAdd(&p.page_refs[slot / p.page_size], 1) <= 0) {
-          atomicSub(&p.page_refs[slot / p.page_size], 1);
-          record_error(p.err, kErrPageRefs);
-        }
-      }
       for (int r = lane; r < p.page_size && pos + r < p.row_stride; r += 32) to[r] = from[r];
+      bool shared = true;
+      if (lane == 0) {
+        shared = known && hold(&p.page_refs[slot / p.page_size]);
+        if (!shared) record_error(p.err, known ? kErrPageRefs : kErrPageOutOfRange);
+      }
+      if (__any_sync(0xffffffffu, !shared))  // (the row first: nothing waits for the count where all is well)
+        for (int r = lane; r < p.page_size && pos + r < p.row_stride; r += 32) to[r] = -1;
     }
   }
   copy_pages(p, pools, p.count, task - tables);

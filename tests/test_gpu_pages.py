@@ -286,3 +286,29 @@ def test_columns_beside_a_table_stay():
     assert big[2, 70:100].tolist() == list(range(7 * 16, 8 * 16)) + list(range(8 * 16, 8 * 16 + 14))
     with pytest.raises(ValueError, match="room for fewer"):
         B.pa_pages_free(rows=rows(0), lens=ints(0), **kw | dict(req_to_token=big[:, 20:70], max_seq_pages=4))
+
+
+@pytest.mark.parametrize("children", [2, 3, 500])
+def test_pages_that_nobody_holds_are_not_forked(children):
+    """Many children of a row with a full page, and a last one, that nobody holds: refused for all of
+    them alike, whatever their order."""
+    for last in (48, 40):                       # whole pages; a partly filled last one
+        s = Pages(children + 2, children + 8, 16, 3, BF16)
+        s.extend([0, 1], [last, 48])
+        dead = [s.page_at(0, 1)] + ([s.page_at(0, 2)] if last == 40 else [])
+        s.d_refs[dead] = 0
+        kw, d_parents = s.common([0] * children, [last] * children)
+        lens = torch.full((children,), -9, dtype=torch.int32, device="cuda")
+        B.pa_pages_fork(parents=d_parents, children=torch.arange(2, children + 2).cuda(), pools=s.d_pools,
+                        child_lens=lens, workspace=s.workspace(children), **kw)
+        torch.cuda.synchronize()
+        assert B.pa_read_error_flags(reset=True) == B.DEVERR_PAGE_REFS
+        assert lens.tolist() == [48 if last == 48 else 32] * children
+        s.refs[dead] = 0
+        s.refs[s.page_at(0, 0)] += children
+        s.table[2:, :16] = s.table[0, :16]
+        s.table[2:, 16:32] = -1
+        if last == 48:
+            s.refs[s.page_at(0, 2)] += children
+            s.table[2:, 32:] = s.table[0, 32:]
+        s.check()
