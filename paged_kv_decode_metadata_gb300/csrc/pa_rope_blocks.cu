@@ -568,11 +568,16 @@ cudaError_t launch_rope_blocks(const RopeBlocksParams& p, bool interleaved, cuda
   // (64 requests, 32 / 8 heads, scale blocks of 64: 4 rows each 6.4 us and 8 rows 8.5, by thread
   // blocks 10.1 and 10.5).  Where it does not know, one a request on average is taken for decoding;
   // more may be a prompt among decoding requests, whose blocks are long for a warp (31 with a row
-  // and one with 200: 11.2 us by thread blocks, 57 by warps).
+  // and one with 200: 11.2 us by thread blocks, 57 by warps).  Where it knows more than 8, requests
+  // without rows may stand beside a prompt (256 of which one has 200 rows and two have one: 16 us by
+  // thread blocks, 56 and 115 by warps that take 8 rows or one at a time), or all may be decoding all the
+  // same (25, 10 and 7.4 us): up to 16 rows, 8 at a time cost least at their worst (19 us, where thread
+  // blocks take 25 and one at a time 31).
   const int most = p.max_q_len < p.total_q ? p.max_q_len : p.total_q;
-  if (most == 1 || p.total_q <= p.bs) return launch_few<1, 1>(p, interleaved, slots, stream, use_pdl);
+  const bool known = p.max_q_len < p.total_q, sparse = p.total_q <= p.bs;
+  if (most == 1 || (sparse && !known)) return launch_few<1, 1>(p, interleaved, slots, stream, use_pdl);
   if (most <= 4) return launch_few<4, 1>(p, interleaved, slots, stream, use_pdl);
-  if (most <= 8) return launch_few<4, 2>(p, interleaved, slots, stream, use_pdl);
+  if (most <= 8 || (sparse && most <= 16)) return launch_few<4, 2>(p, interleaved, slots, stream, use_pdl);
   return block == 16   ? launch_many<128, 1>(p, interleaved, slots, stream, use_pdl)
          : block == 32 ? launch_many<256, 1>(p, interleaved, slots, stream, use_pdl)
          : block == 64 ? launch_many<256, 2>(p, interleaved, slots, stream, use_pdl)

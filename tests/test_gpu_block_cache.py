@@ -521,3 +521,61 @@ def test_tiles_with_empty_columns_between_full_ones(q_lens, hq, hkv, splits):
     q = torch.randn((sum(q_lens), hq, 128), generator=c.g).to(torch.bfloat16)
     out, lse = attend(c, q.cuda(), q_lens, num_splits=splits)
     check(out, lse, R.attention(q, c.k, c.v, c.ks, c.vs, c.table, seqlens, q_lens, SCALE))
+
+
+def append_time(c, q_lens, max_q_len):
+    """Microseconds of an append (32 / 8 heads), best of five replays of a graph of ten."""
+    rows = sum(q_lens)
+    wide, positions, inv = append_inputs(c, q_lens, 32, 128, 1)
+    q, k, v, _ = wide.cuda().split([32, c.hkv, c.hkv, 1], dim=1)
+    kw = dict(q=q, q_out=torch.empty((rows, 32, 128), dtype=torch.bfloat16, device="cuda"), k=k, v=v, k_cache=c.d_k,
+              v_cache=c.d_v, k_scale=c.d_ks, v_scale=c.d_vs, cu_seqlens_q=rows_of(q_lens).cuda(),
+              cache_seqlens=c.d_n, page_table=c.d_table, max_seq_pages=c.msp, positions=positions.cuda(),
+              inv_freq=inv.cuda(), max_q_len=max_q_len)
+    side = torch.cuda.Stream()
+    best = math.inf
+    with torch.cuda.stream(side):
+        B.pa_rope_append_blocks(**kw)
+        side.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            call = B.prepare_rope_append_blocks(**kw)
+            for _ in range(10):
+                call()
+        graph.replay()
+        for _ in range(5):
+            a, b = (torch.cuda.Event(enable_timing=True) for _ in "ab")
+            a.record()
+            graph.replay()
+            b.record()
+            side.synchronize()
+            best = min(best, a.elapsed_time(b) * 100)
+    return best
+
+
+def test_a_prompt_in_a_padded_batch_is_not_appended_row_by_row():
+    """200 rows of one request in a batch of 256 where all but two others have none, and max_q_len
+    says so: within four times what the three take by themselves (a row at a time by single warps
+    it is ten times)."""
+    alone = append_time(BlockCache([300, 40, 41], 8, 64, 64, 85), [200, 1, 1], 200)
+    padded = append_time(BlockCache([300, 40, 41] + [10] * 253, 8, 64, 64, 85), [200, 1, 1] + [0] * 253, 200)
+    assert padded <= 4 * alone, (padded, alone)
+
+
+@pytest.mark.parametrize("q_lens,mql", [([1] * 20, 4), ([1] * 20, 8), ([1] * 20, 15), ([13, 1] + [0] * 14 + [2], 13),
+                                        ([18, 0, 1] + [0] * 22, 18), ([0, 30] + [1] * 6 + [0] * 30, 30)])
+@pytest.mark.parametrize("page,block", [(16, 16), (128, 64)])
+def test_append_of_sparse_batches_writes_the_same_bits(q_lens, mql, page, block):
+    """Fewer rows than requests: whatever max_q_len makes of it, equal bits."""
+    seqlens = [n + 3 * i for i, n in enumerate(q_lens)]
+    results = []
+    for most in (mql, 200):                                  # (200: the host knows nothing)
+        c = BlockCache(seqlens, 2, page, block, 86)
+        for s in (c.ks, c.vs):
+            s.copy_(torch.exp2(-torch.randint(3, 12, s.shape, generator=c.g).float()))
+        c.to_device()
+        wide, positions, inv = append_inputs(c, q_lens, 6, 96, 86)
+        q_out = run_append(c, q_lens, wide, positions, inv, 6, False, 1.0, max_q_len=most)
+        results.append([x.view(torch.uint8).clone() for x in (q_out, c.d_k, c.d_v, c.d_ks, c.d_vs)])
+    for a, b in zip(*results):
+        assert torch.equal(a, b)
