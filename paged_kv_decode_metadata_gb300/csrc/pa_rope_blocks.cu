@@ -131,7 +131,9 @@ struct Block {
     int lo = 0, hi = p.bs;  // the last request whose slots start at or before this one
     while (true) {
       const int step = (hi - lo + 31) / 32, at = lo + lane * step;
-      const bool before = at < hi && (p.cu_seqlens_q[at] >> p.block_shift) + 2 * at <= slot;
+      // (a start outside [0, total_q] has a slot all the same, so that the request is refused there)
+      const bool before =
+          at < hi && (min(max(p.cu_seqlens_q[at], 0), p.total_q) >> p.block_shift) + 2 * at <= slot;
       const uint32_t miss = ~__ballot_sync(0xffffffffu, before);
       const int ahead = miss == 0 ? 32 : __ffs(miss) - 1;
       if (ahead == 0) return false;

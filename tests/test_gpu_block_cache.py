@@ -579,3 +579,20 @@ def test_append_of_sparse_batches_writes_the_same_bits(q_lens, mql, page, block)
         results.append([x.view(torch.uint8).clone() for x in (q_out, c.d_k, c.d_v, c.d_ks, c.d_vs)])
     for a, b in zip(*results):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("cu", [[0, 3, 100000, 100002], [0, 3, -900, -898], [500, 501, 502, 503], [0, 3, 3, 2000000000]])
+@pytest.mark.parametrize("mql", [2, 3, 2000000000])
+def test_append_reports_rows_far_outside(cu, mql):
+    """Requests whose rows lie beyond every slot of the launch are refused and reported, too."""
+    c = BlockCache([40, 41, 42], 2, 16, 16, 87)
+    before = [x.clone() for x in (c.d_k, c.d_v, c.d_ks, c.d_vs)]
+    wide, positions, inv = append_inputs(c, [3, 2, 2], 4, 128, 87)
+    q_out = run_append(c, [3, 2, 2], wide, positions, inv, 4, False, 1.0, cu=torch.tensor(cu, dtype=torch.int32),
+                       max_q_len=mql)
+    assert B.pa_read_error_flags(reset=True) == B.DEVERR_SEQLEN_OUT_OF_RANGE
+    covered = 3 if cu[0] == 0 and mql >= 3 else 0
+    assert bool((q_out[covered:] == 7.0).all())
+    if not covered:
+        for x, y in zip(before, (c.d_k, c.d_v, c.d_ks, c.d_vs)):
+            assert torch.equal(x.view(torch.uint8), y.view(torch.uint8))
