@@ -530,11 +530,12 @@ __global__ void __launch_bounds__(Shape<C>::kThreads, Shape<C>::kBlocks)
         w.load(prm, r, false);
         if (w.n > 0) continue;
         const int64_t first = static_cast<int64_t>(w.q_begin) * prm.num_q_heads;
-        for (int i = at; i < w.q_len * prm.num_q_heads; i += kOthers) {
+        const int64_t rows = static_cast<int64_t>(w.q_len) * prm.num_q_heads;
+        for (int64_t i = at; i < rows; i += kOthers) {
           if (prm.lse != nullptr) prm.lse[first + i] = -CUDART_INF_F;
           if (S > 1) prm.l_out[(first + i) * S] = -1.f;
         }
-        for (int i = at; i < w.q_len * prm.num_q_heads * 16; i += kOthers)
+        for (int64_t i = at; i < rows * 16; i += kOthers)
           static_cast<uint4*>(prm.out)[first * 16 + i] = make_uint4(0u, 0u, 0u, 0u);
       }
     }

@@ -596,3 +596,17 @@ def test_append_reports_rows_far_outside(cu, mql):
     if not covered:
         for x, y in zip(before, (c.d_k, c.d_v, c.d_ks, c.d_vs)):
             assert torch.equal(x.view(torch.uint8), y.view(torch.uint8))
+
+
+def test_an_empty_request_with_more_than_32_gigabytes_of_rows():
+    """Nothing cached and 65535 x 2080 rows of 256 bytes (q is not read, so out stands in for it)."""
+    c = BlockCache([0], 65, 16, 16, 88)
+    out = torch.full((65535, 65 * 32, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((65535, 65 * 32), 7.0, device="cuda")
+    B.pa_block_attention(q=out, k_cache=c.d_k, v_cache=c.d_v, k_scale=c.d_ks, v_scale=c.d_vs, page_table=c.d_table,
+                         cache_seqlens=c.d_n, cu_seqlens_q=rows_of([65535]).cuda(), max_q_len=65535,
+                         max_seq_pages=c.msp, sm_scale=SCALE, out=out, lse=lse, num_splits=1)
+    torch.cuda.synchronize()
+    assert bool((lse == -math.inf).all())
+    for part in out.split(4096):
+        assert not bool(part.view(torch.int16).any())
