@@ -866,7 +866,8 @@ PA_API size_t pa_block_workspace_bytes(int32_t bs, int32_t total_q, int32_t max_
  *                 those of pa_compact_cache in place
  *   next_tokens   [bs] int64 (out)
  * A request without rows, or whose rows are refused (more than max_q_len, outside [0, total_q),
- * more than its cache_seqlens), gets counts 0, next token -1.  A token outside [0, vocab) is rejected and sets
+ * more than its cache_seqlens), gets counts 0, next token -1 (total_q 0: all of them; target_probs, tokens and
+ * uniforms may be NULL).  A token outside [0, vocab) is rejected and sets
  * PA_DEVERR_TOKEN_OUT_OF_RANGE; a target row without a positive probability that is drawn from
  * gives -1 and sets PA_DEVERR_NO_PROBABILITY.
  * Supported: 1 <= max_q_len <= 256; 1 <= vocab <= 2^20; bs <= 65535.

@@ -206,9 +206,9 @@ pa_status pa_verify_drafts(const float* target_probs, int64_t target_stride,
                            int32_t use_pdl) {
   if (bs < 0 || total_q < 0) return PA_ERR_INVALID;
   if (bs == 0) return PA_OK;
-  if (!target_probs || !tokens || !cu_seqlens_q || !uniforms || !final_uniforms || !kept || !counts ||
-      !next_tokens)
-    return PA_ERR_INVALID;
+  // (no rows at all: the requests' results are still written)
+  if (total_q > 0 && (!target_probs || !tokens || !uniforms)) return PA_ERR_INVALID;
+  if (!cu_seqlens_q || !final_uniforms || !kept || !counts || !next_tokens) return PA_ERR_INVALID;
   if (!aligned(target_probs, 4) || !aligned(draft_probs, 4) || !aligned(tokens, 8) || !aligned(next_tokens, 8))
     return PA_ERR_INVALID;
   for (const void* x : {static_cast<const void*>(parents), static_cast<const void*>(cu_seqlens_q),

@@ -243,3 +243,13 @@ def test_blocks_that_start_late(vocab, new):
     d.check(first)
     for _ in range(20):
         assert all(torch.equal(a, b) for a, b in zip(first, d.run()))
+
+
+@pytest.mark.parametrize("drafted", [True, False])
+def test_a_batch_without_rows(drafted):
+    """Every request of a padded batch without rows: the tensors of rows are empty."""
+    d = Drafts([0, 0, 0], 50, 0, drafted, seed=22)
+    d.check(d.run())
+    kept, counts, begin, tokens = d.run(max_q_len=4, kept=torch.full((3, 6), 77, dtype=torch.int32, device="cuda"))
+    assert kept.tolist() == [[-1] * 4 + [77, 77]] * 3
+    assert counts.tolist() == [0] * 3 and tokens.tolist() == [-1] * 3 and torch.equal(begin, d.n)
