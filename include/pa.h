@@ -792,7 +792,7 @@ PA_API pa_status pa_rope_append_blocks(
  * sm_scale * log2(e) finite in fp32.
  * Supported: head_dim 128; page_size 16, 32, 64, 128; num_q_heads / num_kv_heads 1 to 32 (any
  * whole number); 1 <= max_q_len <= 65535; bs and num_kv_heads <= 65535; max_seq_pages * page_size
- * <= 2^29 and bs * num_kv_heads * tiles * ceil(max_seq_pages * page_size / 128) < 2^30.  A tile
+ * <= 2^29 and bs * num_kv_heads * tiles * (ceil(max_seq_pages * page_size / 128) + 2) < 2^30.  A tile
  * has up to 32 (query, head) pairs of a kv head, and every tile reads the request's cache: the
  * call is meant for decoding and short drafts, and right for longer chunks.
  */

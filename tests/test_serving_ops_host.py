@@ -272,3 +272,12 @@ def test_tables_that_are_columns_of_wider_ones():
                          (big[3:, 200:256], 1)):
         with pytest.raises(ValueError, match="must be a CUDA tensor"):
             B._slot_table(table, refs, 64, pages, one, lens)
+
+
+@pytest.mark.parametrize("msp,P,status", [(1021, 128, B.PA_ERR_INVALID), (1022, 128, B.PA_ERR_UNSUPPORTED),
+                                          (2 * 1021, 64, B.PA_ERR_INVALID), (2 * 1021 + 1, 64, B.PA_ERR_UNSUPPORTED)])
+def test_the_largest_batch_of_chunks(lib, msp, P, status):
+    """2^20 tiles (1024 requests, 1024 kv heads) of 1021 chunks of 128 tokens, and two more a tile for what
+    it costs beside them, are the most.  (Invalid: past that check, but without a workspace.)"""
+    assert _caller(lib.pa_block_attention, ATTEND)(bs=1024, total=1024, mql=1, hq=1024, hkv=1024, P=P, msp=msp,
+                                                   pts=1 << 12, ws=None) == status
