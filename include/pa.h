@@ -924,8 +924,9 @@ PA_API pa_status pa_pages_copy(const pa_page_pool* src_pools, const pa_page_pool
 /*
  * pa_pages_fork -- row children[i] becomes a request with the first lens[i] tokens of row
  * parents[i] (at most what that row holds): full pages are shared, a partly filled last page is
- * copied, in every pool, to a page of the child's own, so that both may append.  (Whatever
- * rewrites full pages, as pa_evict in place does, must not be used on shared ones.)  One parent
+ * copied, in every pool, to a page of the child's own, so that both may append.  Shared pages are
+ * guarded by nobody: what rewrites full pages, as pa_evict in place does, must not be used on them, and neither
+ * must an append to a row that was cut short inside one (see pa_pages_free).  One parent
  * may have many children; a child is a row that holds nothing, and is listed once.
  * child_lens[i] (out) = lens[i], or, where no page was left for the last one, its full pages'
  * tokens, with PA_DEVERR_OUT_OF_PAGES.  A page that nobody holds is not shared or copied and sets
@@ -958,6 +959,9 @@ PA_API pa_status pa_pages_extend(int32_t* req_to_token, int64_t num_rows, int64_
  * one holder less each, and the page's first slot in the row becomes -1.  Pages whose first slot
  * is negative have been given back already (a row listed twice is given back once).  A page that
  * nobody holds sets PA_DEVERR_PAGE_REFS.
+ * Where keep_lens[i] ends inside a page that other rows hold too, the row goes on holding it, and what is
+ * appended next would be written into it for all of them (no call reports that): fork the row at
+ * keep_lens[i] tokens, which copies that page, and free the row itself instead.
  */
 PA_API pa_status pa_pages_free(int32_t* req_to_token, int64_t num_rows, int64_t row_stride,
                                int32_t* page_refs, int64_t num_pages, int32_t page_size,

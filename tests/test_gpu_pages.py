@@ -312,3 +312,21 @@ def test_pages_that_nobody_holds_are_not_forked(children):
             s.refs[s.page_at(0, 2)] += children
             s.table[2:, 32:] = s.table[0, 32:]
         s.check()
+
+
+def test_a_row_cut_short_inside_a_shared_page():
+    """Cut by a fork at its new length, a row has a page of its own to append to; cut by a free alone it
+    goes on sharing the page, as the header says."""
+    s = Pages(4, 12, 16, 4, BF16)
+    s.extend([0], [60])
+    s.fork([0], [1], [48])                      # three full pages shared
+    s.fork([1], [2], [40])                      # row 1 cut to 40: its last page copied
+    s.free([1])
+    s.extend([2], [55])
+    assert s.page_at(2, 2) != s.page_at(0, 2) and int(s.refs[s.page_at(2, 2)]) == 1
+    assert int(s.refs[s.page_at(0, 2)]) == 1
+    s.fork([0], [3], [48])
+    s.free([3], [40])
+    assert s.page_at(3, 2) == s.page_at(0, 2) and int(s.refs[s.page_at(0, 2)]) == 2
+    s.free([0, 2, 3])
+    assert int(s.refs.sum()) == 0
