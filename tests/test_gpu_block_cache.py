@@ -610,3 +610,18 @@ def test_an_empty_request_with_more_than_32_gigabytes_of_rows():
     assert bool((lse == -math.inf).all())
     for part in out.split(4096):
         assert not bool(part.view(torch.int16).any())
+
+
+@pytest.mark.parametrize("seqlens,q_lens,hq,hkv,page,block,rot,interleaved,amplitude", APPEND_CASES)
+def test_an_append_repeated_leaves_the_same_bits(seqlens, q_lens, hq, hkv, page, block, rot, interleaved, amplitude):
+    """Keys, values, both scales and the turned queries, blocks with rows before the new ones among them."""
+    c = BlockCache(seqlens, hkv, page, block, seed=rot + page)
+    for s in (c.ks, c.vs):
+        s.copy_(torch.exp2(-torch.randint(3, 12, s.shape, generator=c.g).float()))
+    c.to_device()
+    wide, positions, inv = append_inputs(c, q_lens, hq, rot, seed=page)
+    first = run_append(c, q_lens, wide, positions, inv, hq, interleaved, amplitude)
+    once = [x.clone() for x in (first, c.d_k, c.d_v, c.d_ks, c.d_vs)]
+    again = run_append(c, q_lens, wide, positions, inv, hq, interleaved, amplitude)
+    for a, b in zip(once, (again, c.d_k, c.d_v, c.d_ks, c.d_vs)):
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
