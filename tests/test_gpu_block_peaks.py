@@ -112,3 +112,23 @@ def test_v_scales_of_any_size(e):
     assert torch.equal(lse, again)
     assert torch.equal(out.double(), small.double() * 2.0 ** e)
     assert math.isfinite(float(out.float().abs().max()))
+
+
+@pytest.mark.parametrize("bad", [math.nan, math.inf])
+@pytest.mark.parametrize("splits", [1, 2])
+def test_scales_that_are_not_finite(bad, splits):
+    """A K scale reaches the queries that see its block, a V scale no other request and no other head."""
+    c = BlockCache([300, 300, 300], 2, 64, 16, 31)
+    q = torch.randn((9, 8, 128), generator=c.g).to(torch.bfloat16)
+    plain, _ = attend(c, q.cuda(), [3, 3, 3], num_splits=splits)
+    page = int(c.table[0, 299 // 64])
+    c.ks[page, 0, 299 % 64 // 16] = bad            # positions 288 .. 299: every query sees some
+    c.vs[int(c.table[1, 1]), 1, 2] = bad
+    c.to_device()
+    out, lse = attend(c, q.cuda(), [3, 3, 3], num_splits=splits)
+    gone = torch.zeros((9, 8), dtype=torch.bool)
+    gone[:3, :4] = gone[3:6, 4:] = True
+    assert torch.equal(~torch.isfinite(out.float()).all(-1).cpu(), gone)
+    assert torch.equal(out.cpu()[~gone].view(torch.int16), plain.cpu()[~gone].view(torch.int16))
+    # (V leaves the sums alone)
+    assert bool(torch.isfinite(lse[3:]).all())
