@@ -843,7 +843,7 @@ PA_API size_t pa_block_workspace_bytes(int32_t bs, int32_t total_q, int32_t max_
  * (pa_decode_step_tree, pa_decode_step_multi, pa_decode_step_block) and pa_compact_cache.
  * The rows of request b, cu_seqlens_q[b] .. cu_seqlens_q[b+1], are a tree: row 0 is its newest
  * token, which stays in any case; row i > 0 is drafted token tokens[row] after row parents[row] of
- * the request (< i; parents NULL: a chain, i - 1; -1: never reached).  p_i = target_probs[row i]
+ * the request (< i; parents NULL: a chain, i - 1; -1: never reached; of row 0: -1).  p_i = target_probs[row i]
  * is the target's distribution of the token after row i; q_i = draft_probs[row i] the one that
  * row i's children were drawn from, independently.  From node 0, the children x of the node in
  * order of their rows, with w = p, c = 0, S = 1 at each new node (fp32; the test in fp64):

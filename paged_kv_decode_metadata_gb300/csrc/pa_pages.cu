@@ -7,7 +7,7 @@
 //
 // Shape.  One thread block plans: it ranks the free pages by a scan of page_refs (reading stops
 // when enough are found) and leaves (source, destination) pairs.  A grid applies the plan: table
-// rows, and the pages of every pool in tasks of 16 KiB.  A list of up to kMaxPools pools travels
+// rows, and the pages of every pool in tasks of 16 KiB.  A list of up to PagesPools::kMax pools travels
 // in the kernel's arguments, so a fork or a compaction over all layers is two launches.
 //
 // Bound by memory for copies, every byte read and written once (2.1 GB of a compaction 335 us, 6.4
@@ -453,7 +453,7 @@ unsigned blocks_for(int64_t tasks) {
   return static_cast<unsigned>(tasks < 1 ? 1 : tasks < most ? tasks : most);
 }
 
-// Pools [from, from + kMaxPools) as kernel arguments, the large ones first.
+// Pools [from, from + PagesPools::kMax) as kernel arguments, the large ones first.
 PagesPools pack(const pa_page_pool* src, const pa_page_pool* dst, int32_t from, int32_t num) {
   PagesPools out = {};
   for (int pass = 0; pass < 2; ++pass) {
