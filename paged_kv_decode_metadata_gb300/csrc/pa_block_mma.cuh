@@ -162,8 +162,7 @@ struct Walk {
     longest = __reduce_max_sync(0xffffffffu, longest);
     shortest = __reduce_min_sync(0xffffffffu, shortest);
     empties = __any_sync(0xffffffffu, empties);
-    // A unit of c chunks (its places in a row) meets at most floor((c - 1) / share) + 2 shares (c of them if share is
-    // 1): a share of longest / (num_splits - 1) keeps every unit's pieces within num_splits.
+    // A unit of c > 1 chunks (its places in a row) meets at most floor((c - 2) / share) + 2 shares: a share of longest / (num_splits - 1) keeps every unit's pieces within num_splits.
     const int S = prm.num_splits, grid = static_cast<int>(gridDim.x);
     share = (total + grid - 1) / grid;
     // Units of one length that fill the blocks well enough stay whole: partials and their join cost
