@@ -17,8 +17,8 @@
 // and long contexts do not add up the tensor cores' truncation.
 //
 // Shape.  M is the cache side: scores are S^T = K Q^T (128 tokens x 2 C columns), outputs O^T =
-// V^T P^T (128 channels x 2 C, two passes; C = 8: 4 C), C = 8, 16 or 32 columns of (query, head) pairs of one kv head.
-// So few columns cost few cycles, a thread owns a token in the softmax and a channel in the
+// V^T P^T (128 channels x 2 C, two passes; C = 8: 4 C), C = 8, 16 or 32 columns of (query, head)
+// pairs of one kv head.  So few columns cost few cycles, a thread owns a token in the softmax and a channel in the
 // sums, and neither K nor V is moved or widened.  Four warps have 8 columns; a column's maximum
 // goes over their 128 threads: a warp reduction, four numbers in shared memory, one barrier a
 // chunk.
@@ -39,8 +39,8 @@
 // warps' instructions: 1.35 us a chunk of 32 columns on an SM (16 requests of 8192 tokens, 25 columns: 77
 // us, where memory would take 40; 73 with weights of three e4m3 pieces, which lost small ones; of those with
 // the scales found by the softmax warps 92, with every warp walking for itself 82).  A column for each
-// of the four pieces took 79.5, and 153 in place of 148 us for 32 requests and 32 columns.  One request of 1024 tokens: 8.4 us, launches and dependent latencies; short
-// contexts by the same latencies once a unit (256 requests of 128 tokens: 28 us, memory 10).
+// of the four pieces took 79.5, and 153 in place of 148 us for 32 requests and 32 columns.  One request
+// of 1024 tokens: 8.4 us, launches and dependent latencies; short contexts by the same latencies once a unit (256 requests of 128 tokens: 28 us, memory 10).
 #pragma once
 
 #include <math_constants.h>
@@ -162,7 +162,8 @@ struct Walk {
     longest = __reduce_max_sync(0xffffffffu, longest);
     shortest = __reduce_min_sync(0xffffffffu, shortest);
     empties = __any_sync(0xffffffffu, empties);
-    // A unit of c > 1 chunks (its places in a row) meets at most floor((c - 2) / share) + 2 shares: a share of longest / (num_splits - 1) keeps every unit's pieces within num_splits.
+    // A unit of c > 1 chunks (its places in a row) meets at most floor((c - 2) / share) + 2 shares: a
+    // share of (longest - 1) / (num_splits - 1), rounded up, keeps every unit's pieces within num_splits.
     const int S = prm.num_splits, grid = static_cast<int>(gridDim.x);
     share = (total + grid - 1) / grid;
     // Units of one length that fill the blocks well enough stay whole: partials and their join cost
